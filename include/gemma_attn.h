@@ -69,7 +69,7 @@ typedef enum {
 
 /* Bits OR-ed into the optional device error word. */
 #define GEMMA_DEVERR_SEQ_LEN 1u    /* seq_lens[b] outside [n_tok, min(kv_capacity, max_seq_len)] */
-#define GEMMA_DEVERR_WRITE_POS 2u  /* write_pos[b] < 0 or write_pos[b] + n_new > kv_capacity */
+#define GEMMA_DEVERR_WRITE_POS 2u  /* write_pos[b] (read_pos[b]) < 0 or + n_new > kv_capacity */
 #define GEMMA_DEVERR_TIMEOUT 4u    /* an internal pipeline wait gave up */
 #define GEMMA_DEVERR_N_REAL 8u     /* n_real[b] outside [0, n_new] (padded-bucket entry points) */
 #define GEMMA_DEVERR_PAGE 16u      /* a block-table entry outside [0, n_pages) (paged entry points) */
@@ -313,6 +313,72 @@ int gemma_attn_paged(void* out, const void* q, void* const* k_pool, void* const*
  * invalid arguments, including GEMMA_SLIDING_RING). */
 size_t gemma_attn_workspace_size_paged(int batch, gemma_layer_kind kind, int window, int n_q,
                                        int n_kv, int head_dim, int max_seq_len, int n_new);
+
+/*
+ * 4-bit KV cache -- the pages hold the cache in bf16 and keep it on the device for the whole
+ * conversation (first page, section 5.1), so its bytes bound both the context and the decode
+ * step. These entry points hold an owner layer's cache in 4 bits instead (4.25 per element with
+ * the scales), 3.76 times smaller, for every kind of layer: plain and ring caches, and paged
+ * pools.
+ *   codes       DEVICE [batch][n_kv][kv_capacity][head_dim / 2] bytes per owner layer,
+ *   scales      DEVICE [batch][n_kv][kv_capacity][head_dim / 64] bf16
+ *               (pools: [n_pages][n_kv][page_size][...]), caller-owned, 16-byte aligned.
+ *   Each 64 consecutive elements x of a row share a scale s: the smallest number of at most five
+ *   significant bits, at least 2^-126 and at most 1.125 * 2^125 (7 s is finite), with
+ *   7 s >= max |x|; 0 if all are zero; NaN if any is NaN or infinite (the group then reads as
+ *   NaN). An element's code is x / s rounded to the nearest
+ *   integer, halves to even (in [-7, 7]), and stands for code * s, which bf16 holds exactly.
+ *   Codes are sign-magnitude, eight to a 32-bit little-endian word: element 2j of the eight has
+ *   its magnitude in bits 4j..4j+2 and its sign in bit (15 + 4j) % 32, element 2j + 1 in bits
+ *   16+4j..16+4j+2 and bit (31 + 4j) % 32.
+ *   kv_capacity is a multiple of 32 (of 128 for GEMMA_SLIDING_RING) and page_size of 128, else
+ *   GEMMA_ERR_UNSUPPORTED; kv_capacity is ignored with a block table. block_table (NULL: a plain
+ *   or ring cache), max_pages, page_size and n_pages are those of the paged entry points; a
+ *   block table with GEMMA_SLIDING_RING gives GEMMA_ERR_INVALID_ARG.
+ */
+
+/* gemma_kv_append_q4 -- quantise this step's new rows [batch][n_new][n_kv][head_dim] (dtype bf16
+ * or fp32) into an owner layer's 4-bit cache at write_pos[b] + t (slot modulo kv_capacity on a
+ * ring). Owner map, k_eq_v, errors and no-ops as for gemma_kv_append / _ring / _paged. */
+int gemma_kv_append_q4(void* const* k_codes, void* const* k_scales, void* const* v_codes,
+                       void* const* v_scales, const int32_t* owner_map, int n_layers, int layer,
+                       const void* k_new, const void* v_new, const int32_t* write_pos,
+                       const int32_t* block_table, int max_pages, int page_size, int n_pages,
+                       int batch, int n_new, gemma_layer_kind kind, int n_kv, int head_dim,
+                       int kv_capacity, int k_eq_v, gemma_dtype dtype, uint32_t* device_error,
+                       void* stream);
+
+/* gemma_kv_read_q4 -- the values of rows read_pos[b] + t, t < n_rows, of the cache that the layer
+ * reads (its owner's): k_out, v_out [batch][n_rows][n_kv][head_dim] of dtype (bf16 or fp32, both
+ * exact; v_out is ignored with k_eq_v). A read_pos out of range gives zeros and
+ * GEMMA_DEVERR_WRITE_POS, a bad page zeros and GEMMA_DEVERR_PAGE. */
+int gemma_kv_read_q4(const void* const* k_codes, const void* const* k_scales,
+                     const void* const* v_codes, const void* const* v_scales,
+                     const int32_t* owner_map, int n_layers, int layer, void* k_out, void* v_out,
+                     const int32_t* read_pos, const int32_t* block_table, int max_pages,
+                     int page_size, int n_pages, int batch, int n_rows, gemma_layer_kind kind,
+                     int n_kv, int head_dim, int kv_capacity, int k_eq_v, gemma_dtype dtype,
+                     uint32_t* device_error, void* stream);
+
+/* gemma_attn_q4 -- attention of n_new query tokens per sequence (1: a decode step) over a 4-bit
+ * cache whose rows were appended first: gemma_attn_decode / gemma_attn_prefill / _paged with K
+ * and V the values that the cache stands for, and an optional soft-cap of the scaled scores as in
+ * gemma_attn_softcap (0: none). q and out are bf16 (GEMMA_FP32 gives GEMMA_ERR_UNSUPPORTED).
+ * Scratch: gemma_attn_workspace_size_q4(...) bytes; calls that may overlap must not share it. */
+int gemma_attn_q4(void* out, const void* q, const void* const* k_codes,
+                  const void* const* k_scales, const void* const* v_codes,
+                  const void* const* v_scales, const int32_t* owner_map, int n_layers, int layer,
+                  const int32_t* seq_lens, const int32_t* block_table, int max_pages,
+                  int page_size, int n_pages, int max_seq_len, int n_new, int batch,
+                  gemma_layer_kind kind, int window, int n_q, int n_kv, int head_dim, int k_eq_v,
+                  int kv_capacity, float scale, float softcap, gemma_dtype dtype, void* workspace,
+                  size_t workspace_bytes, uint32_t* device_error, void* stream);
+
+/* Scratch bytes of gemma_attn_q4 for these arguments on the current device ((size_t)-1 for
+ * invalid ones). */
+size_t gemma_attn_workspace_size_q4(int batch, gemma_layer_kind kind, int window, int n_q,
+                                    int n_kv, int head_dim, int max_seq_len, int n_new,
+                                    int k_eq_v);
 
 /*
  * gemma_logit_softcap_argmax -- final-logit soft-cap and greedy argmax of each row.

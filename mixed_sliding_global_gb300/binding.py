@@ -69,6 +69,14 @@ _SIGNATURES = {
                                   _c_size_t, _c_void_p, _c_void_p]),
     "gemma_attn_workspace_size_paged": (_c_size_t, [_c_int, _c_int, _c_int, _c_int, _c_int,
                                                     _c_int, _c_int, _c_int]),
+    "gemma_kv_append_q4": (_c_int, [_PVOID] * 4 + [_PI32, _c_int, _c_int] + [_c_void_p] * 4 +
+                           [_c_int] * 10 + [_c_int, _c_void_p, _c_void_p]),
+    "gemma_kv_read_q4": (_c_int, [_PVOID] * 4 + [_PI32, _c_int, _c_int] + [_c_void_p] * 4 +
+                         [_c_int] * 10 + [_c_int, _c_void_p, _c_void_p]),
+    "gemma_attn_q4": (_c_int, [_c_void_p, _c_void_p] + [_PVOID] * 4 + [_PI32, _c_int, _c_int] +
+                      [_c_void_p] * 2 + [_c_int] * 13 + [_c_float, _c_float, _c_int, _c_void_p,
+                                                         _c_size_t, _c_void_p, _c_void_p]),
+    "gemma_attn_workspace_size_q4": (_c_size_t, [_c_int] * 9),
     "gemma_logit_softcap_argmax": (_c_int, [_c_void_p, _c_int, _c_int, _c_int, _c_float,
                                             _c_void_p, _c_void_p, _c_void_p, _c_size_t,
                                             _c_void_p]),
@@ -334,6 +342,131 @@ def gemma_attn_workspace_size_paged(batch: int, kind: int, window: int, n_q: int
                                                   max_seq_len, n_new)
     if n == ctypes.c_size_t(-1).value:
         raise ValueError("invalid arguments for gemma_attn_workspace_size_paged")
+    return int(n)
+
+
+def _q4_caches(codes, scales, v_codes, v_scales, owner_map):
+    """Pointer arrays of a 4-bit cache; the owner layers' codes must be uint8, scales bf16."""
+    n = len(owner_map)
+    arrays = [list(codes), list(scales),
+              list(v_codes) if v_codes is not None else [None] * n,
+              list(v_scales) if v_scales is not None else [None] * n]
+    for xs, dt in zip(arrays, (torch.uint8, torch.bfloat16) * 2):
+        if len(xs) != n:
+            raise ValueError("one cache entry per layer")
+        for x in xs:
+            if x is not None and x.dtype != dt:
+                raise TypeError(f"4-bit caches hold uint8 codes and bf16 scales, not {x.dtype}")
+    return arrays
+
+
+def _q4_geometry(arrays, owner_map, layer, k_eq_v, d, n_kv, block_table):
+    """Check the owner layer's shapes; (capacity, max_pages, page_size, n_pages) of its cache."""
+    o = int(owner_map[layer])
+    kc = arrays[0][o]
+    if kc is None or arrays[1][o] is None:
+        raise ValueError("the owner layer has no cache")
+    if kc.dim() != 4 or kc.shape[1] != n_kv or kc.shape[3] * 2 != d:
+        raise ValueError("codes must be [batch][n_kv][capacity][head_dim / 2]")
+    want = (tuple(kc.shape), tuple(kc.shape[:3]) + (d // 64,))
+    for i, x in enumerate(a[o] for a in (arrays[:2] if k_eq_v else arrays)):
+        if x is None or tuple(x.shape) != want[i % 2]:
+            raise ValueError("codes and scales of K and V must have matching shapes")
+    if block_table is None:
+        return kc.shape[2], 0, 0, 0
+    if block_table.dtype != torch.int32:
+        raise TypeError("block_table must be int32")
+    return 0, int(block_table.shape[1]), int(kc.shape[2]), int(kc.shape[0])
+
+
+def _q4_rows(fn, k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_rows, v_rows, pos, *,
+             k_eq_v, kind, block_table, device_error, stream):
+    B, n, n_kv, d = k_rows.shape
+    if pos.dtype != torch.int32:
+        raise TypeError("positions must be int32")
+    if not k_eq_v and (v_rows is None or v_rows.shape != k_rows.shape or
+                       v_rows.dtype != k_rows.dtype):
+        raise ValueError("K and V rows must have one shape and type")
+    arrays = _q4_caches(k_codes, k_scales, v_codes, v_scales, owner_map)
+    if pos.numel() != B:
+        raise ValueError("one position per sequence")
+    cap, max_pages, page_size, n_pages = _q4_geometry(arrays, owner_map, layer, k_eq_v, d, n_kv,
+                                                      block_table)
+    cache_batch = arrays[0][int(owner_map[layer])].shape[0]
+    if (block_table.shape[0] if block_table is not None else cache_batch) != B:
+        raise ValueError("the cache (or block table) must have one entry per sequence")
+    st = getattr(library(), fn)(
+        *[_ptr_array(a) for a in arrays], _i32_array(owner_map), len(owner_map), layer,
+        _dev_ptr(k_rows), None if k_eq_v else _dev_ptr(v_rows), _dev_ptr(pos),
+        _dev_ptr(block_table), max_pages, page_size, n_pages, B, n, int(kind), n_kv, d, int(cap),
+        int(bool(k_eq_v)), _dtype(k_rows), _dev_ptr(device_error), _stream(stream))
+    _check(fn, st)
+
+
+def gemma_kv_append_q4(k_codes, k_scales, v_codes, v_scales, owner_map, layer: int,
+                       k_new: torch.Tensor, v_new: Optional[torch.Tensor],
+                       write_pos: torch.Tensor, *, k_eq_v: bool, kind: int = GEMMA_GLOBAL,
+                       block_table: Optional[torch.Tensor] = None,
+                       device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Quantise rows [B][n_new][n_kv][d] (bf16 or fp32) into a 4-bit cache. Per owner layer: codes
+    uint8 [B][n_kv][cap][d / 2] and scales bf16 [B][n_kv][cap][d / 64] (pools
+    [n_pages][n_kv][page_size][...] with a block_table int32 [B][max_pages]); write_pos int32 [B];
+    kind GEMMA_SLIDING_RING wraps the slot, the other kinds write alike."""
+    if int(owner_map[layer]) != layer:
+        return  # a shared layer writes no cache
+    _q4_rows("gemma_kv_append_q4", k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_new,
+             v_new, write_pos, k_eq_v=k_eq_v, kind=kind, block_table=block_table,
+             device_error=device_error, stream=stream)
+
+
+def gemma_kv_read_q4(k_codes, k_scales, v_codes, v_scales, owner_map, layer: int,
+                     k_out: torch.Tensor, v_out: Optional[torch.Tensor], read_pos: torch.Tensor,
+                     *, k_eq_v: bool, kind: int = GEMMA_GLOBAL,
+                     block_table: Optional[torch.Tensor] = None,
+                     device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The values of rows read_pos[b] + t of a 4-bit cache: k_out, v_out [B][n_rows][n_kv][d],
+    bf16 or fp32. Caches as for gemma_kv_append_q4."""
+    _q4_rows("gemma_kv_read_q4", k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_out,
+             v_out, read_pos, k_eq_v=k_eq_v, kind=kind, block_table=block_table,
+             device_error=device_error, stream=stream)
+
+
+def gemma_attn_q4(out: torch.Tensor, q: torch.Tensor, k_codes, k_scales, v_codes, v_scales,
+                  owner_map, layer: int, seq_lens: torch.Tensor, max_seq_len: int, *, kind: int,
+                  window: int, n_kv: int, k_eq_v: bool, scale: float, softcap: float = 0.0,
+                  block_table: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None,
+                  device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Attention over a 4-bit cache (as for gemma_kv_append_q4): q, out bf16 [B][n_new][n_q][d],
+    seq_lens int32 [B] counting the new tokens. n_new = 1 is a decode step."""
+    if q.dim() != 4 or out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("q and out must be [batch][n_new][n_q][head_dim] of one type")
+    if seq_lens.dtype != torch.int32 or seq_lens.numel() != q.shape[0]:
+        raise ValueError("seq_lens must be int32 [batch]")
+    B, n_new, n_q, d = q.shape
+    arrays = _q4_caches(k_codes, k_scales, v_codes, v_scales, owner_map)
+    cap, max_pages, page_size, n_pages = _q4_geometry(arrays, owner_map, layer, k_eq_v, d, n_kv,
+                                                      block_table)
+    cache_batch = arrays[0][int(owner_map[layer])].shape[0]
+    if (block_table.shape[0] if block_table is not None else cache_batch) != B:
+        raise ValueError("the cache (or block table) must have one entry per sequence")
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = library().gemma_attn_q4(
+        _dev_ptr(out), _dev_ptr(q), *[_ptr_array(a) for a in arrays], _i32_array(owner_map),
+        len(owner_map), layer, _dev_ptr(seq_lens), _dev_ptr(block_table), max_pages, page_size,
+        n_pages, int(max_seq_len), n_new, B, int(kind), int(window), n_q, int(n_kv), d,
+        int(bool(k_eq_v)), int(cap), float(scale), float(softcap), _dtype(q),
+        _dev_ptr(workspace), ws_bytes, _dev_ptr(device_error), _stream(stream))
+    _check("gemma_attn_q4", st)
+
+
+def gemma_attn_workspace_size_q4(batch: int, kind: int, window: int, n_q: int, n_kv: int,
+                                 head_dim: int, max_seq_len: int, n_new: int = 1, *,
+                                 k_eq_v: bool) -> int:
+    n = library().gemma_attn_workspace_size_q4(batch, kind, window, n_q, n_kv, head_dim,
+                                               max_seq_len, n_new, int(bool(k_eq_v)))
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("invalid arguments for gemma_attn_workspace_size_q4")
     return int(n)
 
 

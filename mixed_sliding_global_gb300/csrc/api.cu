@@ -8,6 +8,7 @@
 #include "../../include/gemma_attn.h"
 #include "attn_internal.h"
 #include "logits.h"
+#include "q4.h"
 
 using gemma::RowsParams;
 
@@ -571,6 +572,213 @@ size_t gemma_logit_workspace_size(int batch, int vocab) {
     const int n_sm = sm_count();
     if (n_sm < 0) return (size_t)-1;
     return gemma::logit_plan(batch, vocab, n_sm).ws_bytes;
+}
+
+// ---------------------------------------------------------------------------------------------
+// 4-bit KV cache
+// ---------------------------------------------------------------------------------------------
+namespace {
+
+// Kind, layout and sizes of a 4-bit cache; fills everything of *c but the pointers.
+int q4_layout(int kind, int n_kv, int head_dim, int kv_capacity, const int32_t* block_table,
+              int max_pages, int page_size, int n_pages, gemma::Q4Cache* c) {
+    if (kind != GEMMA_SLIDING && kind != GEMMA_GLOBAL && kind != GEMMA_SLIDING_RING)
+        return GEMMA_ERR_INVALID_ARG;
+    if (n_kv < 1) return GEMMA_ERR_INVALID_ARG;
+    if (!head_dim_ok(head_dim)) return GEMMA_ERR_UNSUPPORTED;
+    *c = gemma::Q4Cache{};
+    c->n_kv = n_kv;
+    if (block_table) {
+        if (kind == GEMMA_SLIDING_RING) return GEMMA_ERR_INVALID_ARG;
+        const int st = check_paged(max_pages, page_size, n_pages);
+        if (st != GEMMA_OK) return st;
+        if ((long long)n_pages * n_kv > (1ll << 31) - 1) return GEMMA_ERR_UNSUPPORTED;
+        c->pg = gemma::PagedLayout{block_table, max_pages, page_size, n_pages};
+        c->cap = max_pages * page_size;
+        return GEMMA_OK;
+    }
+    if (kv_capacity < 1) return GEMMA_ERR_INVALID_ARG;
+    // key tiles start at multiples of 32 slots, a ring's at multiples of 128
+    const int unit = kind == GEMMA_SLIDING_RING ? 128 : 32;
+    if (kv_capacity % unit != 0 || kv_capacity > (1 << 30)) return GEMMA_ERR_UNSUPPORTED;
+    c->cap = kv_capacity;
+    c->ring = kind == GEMMA_SLIDING_RING ? kv_capacity : 0;
+    return GEMMA_OK;
+}
+
+// The owner layer's pointers.
+int q4_pointers(void* const* k_codes, void* const* k_scales, void* const* v_codes,
+                void* const* v_scales, int owner, int k_eq_v, gemma::Q4Cache* c) {
+    if (!k_codes || !k_scales || !k_codes[owner] || !k_scales[owner]) return GEMMA_ERR_INVALID_ARG;
+    c->k_codes = static_cast<uint8_t*>(k_codes[owner]);
+    c->k_scales = static_cast<__nv_bfloat16*>(k_scales[owner]);
+    if (!aligned16(c->k_codes) || !aligned16(c->k_scales)) return GEMMA_ERR_INVALID_ARG;
+    if (k_eq_v) return GEMMA_OK;
+    if (!v_codes || !v_scales || !v_codes[owner] || !v_scales[owner]) return GEMMA_ERR_INVALID_ARG;
+    c->v_codes = static_cast<uint8_t*>(v_codes[owner]);
+    c->v_scales = static_cast<__nv_bfloat16*>(v_scales[owner]);
+    if (!aligned16(c->v_codes) || !aligned16(c->v_scales)) return GEMMA_ERR_INVALID_ARG;
+    return GEMMA_OK;
+}
+
+// One index unit is eight elements of one row; a sequence's units are counted in 32 bits.
+bool q4_units_ok(long long rows, int n_kv, int head_dim) {
+    return rows * n_kv <= (1ll << 30) / (head_dim / 8);
+}
+
+// Append (write_rows) or read-back of n rows per sequence.
+int q4_rows(bool append, void* const* k_codes, void* const* k_scales, void* const* v_codes,
+            void* const* v_scales, const int32_t* owner_map, int n_layers, int layer, void* k_rows,
+            void* v_rows, const int32_t* pos, const int32_t* block_table, int max_pages,
+            int page_size, int n_pages, int batch, int n, int kind, int n_kv, int head_dim,
+            int kv_capacity, int k_eq_v, int dtype, uint32_t* device_error, void* stream) {
+    if (batch < 0 || n < 0) return GEMMA_ERR_INVALID_ARG;
+    if (dtype != GEMMA_BF16 && dtype != GEMMA_FP32) return GEMMA_ERR_INVALID_ARG;
+    gemma::Q4Cache c;
+    int st = q4_layout(kind, n_kv, head_dim, kv_capacity, block_table, max_pages, page_size,
+                       n_pages, &c);
+    if (st != GEMMA_OK) return st;
+    int o = 0;
+    st = resolve_owner(owner_map, n_layers, layer, &o);
+    if (st != GEMMA_OK) return st;
+    if (append && o != layer) return GEMMA_OK;  // a shared layer writes no cache
+    if (n > c.cap) return GEMMA_ERR_CAPACITY;
+    if (batch > 65535 || !q4_units_ok(n, n_kv, head_dim)) return GEMMA_ERR_UNSUPPORTED;
+    if (batch == 0 || n == 0) return GEMMA_OK;
+    st = q4_pointers(k_codes, k_scales, v_codes, v_scales, o, k_eq_v, &c);
+    if (st != GEMMA_OK) return st;
+    if (!k_rows || !pos || !aligned16(k_rows)) return GEMMA_ERR_INVALID_ARG;
+    if (!k_eq_v && (!v_rows || !aligned16(v_rows))) return GEMMA_ERR_INVALID_ARG;
+    const int n_sm = sm_count();
+    if (n_sm < 0) return GEMMA_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int f32 = dtype == GEMMA_FP32;
+    const cudaError_t e =
+        append ? gemma::launch_q4_append(c, k_rows, v_rows, pos, batch, n, head_dim, f32,
+                                         device_error, n_sm, s)
+               : gemma::launch_q4_read(c, k_rows, v_rows, pos, batch, n, head_dim, f32,
+                                       device_error, n_sm, s);
+    return e == cudaSuccess ? GEMMA_OK : GEMMA_ERR_CUDA;
+}
+
+// Scratch of the attention over a dequantised copy: lengths, K rows, V rows, split partials.
+struct Q4Expand {
+    int slots;
+    size_t k_off, v_off, plan_off, bytes;
+};
+Q4Expand q4_expand_plan(int batch, int kind, int window, int n_q, int n_kv, int head_dim,
+                        int max_seq_len, int n_new, int k_eq_v, int n_sm) {
+    Q4Expand e{};
+    const long long reach = kind == GEMMA_GLOBAL ? max_seq_len : (long long)window + n_new - 1;
+    e.slots = (int)(reach < max_seq_len ? reach : max_seq_len);
+    const size_t rows = (size_t)batch * n_kv * e.slots * head_dim * 2;
+    e.k_off = (size_t)round_up(4ll * batch, 256);
+    e.v_off = e.k_off + (size_t)round_up((long long)rows, 256);
+    e.plan_off = e.v_off + (k_eq_v ? 0 : (size_t)round_up((long long)rows, 256));
+    e.bytes = e.plan_off + make_plan(batch, kind == GEMMA_GLOBAL ? GEMMA_GLOBAL : GEMMA_SLIDING,
+                                     window, n_q, n_kv, head_dim, e.slots, n_new, n_sm)
+                               .ws_bytes;
+    return e;
+}
+
+}  // namespace
+
+int gemma_kv_append_q4(void* const* k_codes, void* const* k_scales, void* const* v_codes,
+                       void* const* v_scales, const int32_t* owner_map, int n_layers, int layer,
+                       const void* k_new, const void* v_new, const int32_t* write_pos,
+                       const int32_t* block_table, int max_pages, int page_size, int n_pages,
+                       int batch, int n_new, gemma_layer_kind kind, int n_kv, int head_dim,
+                       int kv_capacity, int k_eq_v, gemma_dtype dtype, uint32_t* device_error,
+                       void* stream) {
+    return q4_rows(true, k_codes, k_scales, v_codes, v_scales, owner_map, n_layers, layer,
+                   const_cast<void*>(k_new), const_cast<void*>(v_new), write_pos, block_table,
+                   max_pages, page_size, n_pages, batch, n_new, kind, n_kv, head_dim, kv_capacity,
+                   k_eq_v, dtype, device_error, stream);
+}
+
+int gemma_kv_read_q4(const void* const* k_codes, const void* const* k_scales,
+                     const void* const* v_codes, const void* const* v_scales,
+                     const int32_t* owner_map, int n_layers, int layer, void* k_out, void* v_out,
+                     const int32_t* read_pos, const int32_t* block_table, int max_pages,
+                     int page_size, int n_pages, int batch, int n_rows, gemma_layer_kind kind,
+                     int n_kv, int head_dim, int kv_capacity, int k_eq_v, gemma_dtype dtype,
+                     uint32_t* device_error, void* stream) {
+    return q4_rows(false, const_cast<void* const*>(k_codes), const_cast<void* const*>(k_scales),
+                   const_cast<void* const*>(v_codes), const_cast<void* const*>(v_scales),
+                   owner_map, n_layers, layer, k_out, v_out, read_pos, block_table, max_pages,
+                   page_size, n_pages, batch, n_rows, kind, n_kv, head_dim, kv_capacity, k_eq_v,
+                   dtype, device_error, stream);
+}
+
+size_t gemma_attn_workspace_size_q4(int batch, gemma_layer_kind kind, int window, int n_q,
+                                    int n_kv, int head_dim, int max_seq_len, int n_new,
+                                    int k_eq_v) {
+    if (batch < 0 || n_new < 1 || max_seq_len < n_new) return (size_t)-1;
+    if (check_shape(kind, window, n_q, n_kv, head_dim, GEMMA_BF16) != GEMMA_OK) return (size_t)-1;
+    if (batch == 0) return 0;
+    const int n_sm = sm_count();
+    if (n_sm < 0) return (size_t)-1;
+    return q4_expand_plan(batch, kind, window, n_q, n_kv, head_dim, max_seq_len, n_new, k_eq_v,
+                          n_sm)
+        .bytes;
+}
+
+int gemma_attn_q4(void* out, const void* q, const void* const* k_codes,
+                  const void* const* k_scales, const void* const* v_codes,
+                  const void* const* v_scales, const int32_t* owner_map, int n_layers, int layer,
+                  const int32_t* seq_lens, const int32_t* block_table, int max_pages,
+                  int page_size, int n_pages, int max_seq_len, int n_new, int batch,
+                  gemma_layer_kind kind, int window, int n_q, int n_kv, int head_dim, int k_eq_v,
+                  int kv_capacity, float scale, float softcap, gemma_dtype dtype, void* workspace,
+                  size_t workspace_bytes, uint32_t* device_error, void* stream) {
+    if (n_new == 0 && batch >= 0) return GEMMA_OK;
+    if (batch < 0 || n_new < 1) return GEMMA_ERR_INVALID_ARG;
+    if (!std::isfinite(softcap) || softcap < 0.f) return GEMMA_ERR_INVALID_ARG;
+    int st = check_shape(kind, window, n_q, n_kv, head_dim, dtype);
+    if (st != GEMMA_OK) return st;
+    if (dtype != GEMMA_BF16) return GEMMA_ERR_UNSUPPORTED;
+    gemma::Q4Cache c;
+    st = q4_layout(kind, n_kv, head_dim, kv_capacity, block_table, max_pages, page_size, n_pages,
+                   &c);
+    if (st != GEMMA_OK) return st;
+    int o = 0;
+    st = resolve_owner(owner_map, n_layers, layer, &o);
+    if (st != GEMMA_OK) return st;
+    if (max_seq_len < n_new || !std::isfinite(scale) || !(scale > 0.f))
+        return GEMMA_ERR_INVALID_ARG;
+    if (c.ring) {
+        if ((long long)c.cap < (long long)window + n_new - 1) return GEMMA_ERR_CAPACITY;
+    } else if (max_seq_len > c.cap) {
+        return GEMMA_ERR_CAPACITY;
+    }
+    if (batch > 65535) return GEMMA_ERR_UNSUPPORTED;
+    if (batch == 0) return GEMMA_OK;
+    st = q4_pointers(const_cast<void* const*>(k_codes), const_cast<void* const*>(k_scales),
+                     const_cast<void* const*>(v_codes), const_cast<void* const*>(v_scales), o,
+                     k_eq_v, &c);
+    if (st != GEMMA_OK) return st;
+    if (!out || !q || !seq_lens || !aligned16(out) || !aligned16(q)) return GEMMA_ERR_INVALID_ARG;
+    const int n_sm = sm_count();
+    if (n_sm < 0) return GEMMA_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const Q4Expand e = q4_expand_plan(batch, kind, window, n_q, n_kv, head_dim, max_seq_len,
+                                      n_new, k_eq_v, n_sm);
+    if (!q4_units_ok(e.slots, n_kv, head_dim)) return GEMMA_ERR_UNSUPPORTED;
+    if (!workspace || workspace_bytes < e.bytes || !aligned16(workspace))
+        return GEMMA_ERR_WORKSPACE;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    int32_t* lens = reinterpret_cast<int32_t*>(ws);
+    if (gemma::launch_q4_expand(c, ws + e.k_off, k_eq_v ? nullptr : ws + e.v_off, lens, seq_lens,
+                                batch, n_new, max_seq_len, kind == GEMMA_GLOBAL ? 0 : window,
+                                e.slots, head_dim, device_error, n_sm, s) != cudaSuccess)
+        return GEMMA_ERR_CUDA;
+    const void* kx = ws + e.k_off;
+    const void* vx = ws + e.v_off;
+    const int32_t self = 0;
+    return attention(out, q, &kx, &vx, &self, 1, 0, lens, e.slots, n_new, batch,
+                     kind == GEMMA_GLOBAL ? GEMMA_GLOBAL : GEMMA_SLIDING, window, n_q, n_kv,
+                     head_dim, k_eq_v, e.slots, scale, softcap, GEMMA_BF16, ws + e.plan_off,
+                     workspace_bytes - e.plan_off, device_error, stream);
 }
 
 }  // extern "C"
