@@ -661,6 +661,40 @@ int q4_rows(bool append, void* const* k_codes, void* const* k_scales, void* cons
     return e == cudaSuccess ? GEMMA_OK : GEMMA_ERR_CUDA;
 }
 
+// A step of at most this many rows (token, query head) per KV head attends straight over the
+// 4-bit cache; a longer one over a dequantised copy, on the bf16 kernels.
+constexpr long long kQ4DirectRows = 64;
+
+// Key chunks of a step straight over the cache: one per SM for small problems (at least a tile),
+// else about four per SM; none when the (sequence, KV head, row tile) units fill the GPU over
+// short ranges.
+Plan q4_plan(int batch, int kind, int window, int n_q, int n_kv, int head_dim, int max_seq_len,
+             int n_tok, int n_sm) {
+    Plan pl{1, 1 << 30, 0, 0, 0};
+    const long long T = gemma::kQ4KeyTile;
+    const long long rows = (long long)n_tok * (n_q / n_kv);
+    const int tile = gemma::q4_row_tile((int)rows);
+    const long long units = (long long)batch * n_kv * ((rows + tile - 1) / tile);
+    long long reach = kind == GEMMA_GLOBAL ? max_seq_len : (long long)window + n_tok - 1;
+    if (reach > max_seq_len) reach = max_seq_len;
+    reach += T - 1;  // the first tile may start up to a tile before the range
+    if (units >= 2 * n_sm && reach <= 4096) return pl;
+    const long long one = round_up((units * reach + n_sm - 1) / n_sm, T);
+    const long long four = round_up((units * reach + 4 * n_sm - 1) / (4 * n_sm), T);
+    long long chunk = one < 512 ? one : 512;
+    if (four > chunk) chunk = four;
+    const long long least = round_up((reach + gemma::kQ4MaxSplit - 1) / gemma::kQ4MaxSplit, T);
+    if (chunk < least) chunk = least;
+    const long long n_split = (reach + chunk - 1) / chunk;
+    if (n_split <= 1) return pl;
+    pl.n_split = (int)n_split;
+    pl.chunk = (int)chunk;
+    const size_t parts = (size_t)batch * n_q * n_tok * n_split;
+    pl.o_bytes = (size_t)round_up((long long)(parts * head_dim * sizeof(float)), 256);
+    pl.ws_bytes = pl.o_bytes + (size_t)round_up((long long)(parts * 2 * sizeof(float)), 256);
+    return pl;
+}
+
 // Scratch of the attention over a dequantised copy: lengths, K rows, V rows, split partials.
 struct Q4Expand {
     int slots;
@@ -718,6 +752,8 @@ size_t gemma_attn_workspace_size_q4(int batch, gemma_layer_kind kind, int window
     if (batch == 0) return 0;
     const int n_sm = sm_count();
     if (n_sm < 0) return (size_t)-1;
+    if ((long long)n_new * (n_q / n_kv) <= kQ4DirectRows)
+        return q4_plan(batch, kind, window, n_q, n_kv, head_dim, max_seq_len, n_new, n_sm).ws_bytes;
     return q4_expand_plan(batch, kind, window, n_q, n_kv, head_dim, max_seq_len, n_new, k_eq_v,
                           n_sm)
         .bytes;
@@ -761,6 +797,46 @@ int gemma_attn_q4(void* out, const void* q, const void* const* k_codes,
     const int n_sm = sm_count();
     if (n_sm < 0) return GEMMA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if ((long long)n_new * (n_q / n_kv) <= kQ4DirectRows) {
+        const Plan pl =
+            q4_plan(batch, kind, window, n_q, n_kv, head_dim, max_seq_len, n_new, n_sm);
+        if (pl.ws_bytes > 0 &&
+            (!workspace || workspace_bytes < pl.ws_bytes || !aligned16(workspace)))
+            return GEMMA_ERR_WORKSPACE;
+        RowsParams p{};
+        p.q = q;
+        p.k = c.k_codes;
+        p.v = k_eq_v ? c.k_codes : c.v_codes;
+        p.seq_lens = seq_lens;
+        p.out = out;
+        p.o_part = static_cast<float*>(workspace);
+        p.ml_part = pl.ws_bytes ? reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) +
+                                                           pl.o_bytes)
+                                : nullptr;
+        p.err = device_error;
+        p.n_tok = n_new;
+        p.n_q = n_q;
+        p.n_kv = n_kv;
+        p.G = n_q / n_kv;
+        p.cap = c.cap;
+        p.window = window;
+        p.is_sliding = kind != GEMMA_GLOBAL;
+        p.ring = c.ring;
+        p.block_table = c.pg.block_table;
+        p.page_size = c.pg.block_table ? c.pg.page_size : 0;
+        p.max_pages = c.pg.max_pages;
+        p.n_pages = c.pg.n_pages;
+        p.k_eq_v = k_eq_v ? 1 : 0;
+        p.max_seq_len = max_seq_len;
+        p.n_split = pl.n_split;
+        p.chunk = pl.chunk;
+        p.scale_log2 = scale * 1.4426950408889634f;
+        p.softcap = softcap;
+        p.cap_inner = softcap > 0.f ? scale / softcap : 0.f;
+        p.cap_log2 = softcap * 1.4426950408889634f;
+        return gemma::launch_q4_attn(p, c, head_dim, batch, s) == cudaSuccess ? GEMMA_OK
+                                                                               : GEMMA_ERR_CUDA;
+    }
     const Q4Expand e = q4_expand_plan(batch, kind, window, n_q, n_kv, head_dim, max_seq_len,
                                       n_new, k_eq_v, n_sm);
     if (!q4_units_ok(e.slots, n_kv, head_dim)) return GEMMA_ERR_UNSUPPORTED;

@@ -34,6 +34,16 @@ struct Q4Cache {
     PagedLayout pg;
 };
 
+// Attention of a few query rows straight over the cache (q4_attn.cu). Chunks are multiples of
+// kQ4KeyTile keys; p.n_split > 1 merges partials through p.o_part / p.ml_part, laid out
+// [batch][n_kv][n_tok * G][n_split][head_dim] and [...][2].
+constexpr int kQ4KeyTile = 128;
+constexpr int kQ4MaxSplit = 128;
+// rows (token, query head) per CTA
+inline int q4_row_tile(int rows) { return rows > 8 ? 16 : 8; }
+cudaError_t launch_q4_attn(const RowsParams& p, const Q4Cache& c, int head_dim, int batch,
+                           cudaStream_t st);
+
 cudaError_t launch_q4_append(const Q4Cache& c, const void* k_new, const void* v_new,
                              const int32_t* write_pos, int batch, int n_new, int head_dim,
                              int fp32, uint32_t* err, int n_sm, cudaStream_t st);
