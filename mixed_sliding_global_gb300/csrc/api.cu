@@ -665,33 +665,34 @@ int q4_rows(bool append, void* const* k_codes, void* const* k_scales, void* cons
 // 4-bit cache; a longer one over a dequantised copy, on the bf16 kernels.
 constexpr long long kQ4DirectRows = 64;
 
-// Key chunks of a step straight over the cache: one per SM for small problems (at least a tile),
-// else about four per SM; none when the (sequence, KV head, row tile) units fill the GPU over
-// short ranges.
-Plan q4_plan(int batch, int kind, int window, int n_q, int n_kv, int head_dim, int max_seq_len,
-             int n_tok, int n_sm) {
-    Plan pl{1, 1 << 30, 0, 0, 0};
+// CTAs of a step straight over the cache: as many as the GPU holds at once, each with an equal
+// share of the key tiles (fewer when there are fewer tiles); a CTA per unit (sequence, KV head,
+// row tile) when there are many short units per CTA that the GPU holds.
+struct Q4Plan {
+    int ctas, balanced;
+    size_t o_bytes, info_off, ws_bytes;
+};
+Q4Plan q4_plan(int batch, int kind, int window, int n_q, int n_kv, int head_dim, int max_seq_len,
+               int n_tok, int n_sm) {
     const long long T = gemma::kQ4KeyTile;
     const long long rows = (long long)n_tok * (n_q / n_kv);
     const int tile = gemma::q4_row_tile((int)rows);
     const long long units = (long long)batch * n_kv * ((rows + tile - 1) / tile);
     long long reach = kind == GEMMA_GLOBAL ? max_seq_len : (long long)window + n_tok - 1;
     if (reach > max_seq_len) reach = max_seq_len;
-    reach += T - 1;  // the first tile may start up to a tile before the range
-    if (units >= 2 * n_sm && reach <= 4096) return pl;
-    const long long one = round_up((units * reach + n_sm - 1) / n_sm, T);
-    const long long four = round_up((units * reach + 4 * n_sm - 1) / (4 * n_sm), T);
-    long long chunk = one < 512 ? one : 512;
-    if (four > chunk) chunk = four;
-    const long long least = round_up((reach + gemma::kQ4MaxSplit - 1) / gemma::kQ4MaxSplit, T);
-    if (chunk < least) chunk = least;
-    const long long n_split = (reach + chunk - 1) / chunk;
-    if (n_split <= 1) return pl;
-    pl.n_split = (int)n_split;
-    pl.chunk = (int)chunk;
-    const size_t parts = (size_t)batch * n_q * n_tok * n_split;
-    pl.o_bytes = (size_t)round_up((long long)(parts * head_dim * sizeof(float)), 256);
-    pl.ws_bytes = pl.o_bytes + (size_t)round_up((long long)(parts * 2 * sizeof(float)), 256);
+    const long long tiles = (reach + 2 * T - 2) / T;  // the first may start before the range
+    const long long slots = (long long)n_sm * gemma::kQ4CtasPerSm;
+    Q4Plan pl{(int)units, 0, 0, 0, 0};
+    // (the balanced launch counts its tiles in 32 bits per KV head and row tile)
+    if (tiles <= 1 || units >= 16 * slots || batch > 4096 || batch * tiles > (1ll << 30)) return pl;
+    pl.balanced = 1;
+    long long c = units * tiles < slots ? units * tiles : slots;
+    if (c > gemma::kQ4MaxShares) c = gemma::kQ4MaxShares;
+    pl.ctas = (int)c;
+    const size_t parts = (size_t)c * 2 * tile;
+    pl.o_bytes = parts * head_dim * sizeof(float);
+    pl.info_off = pl.o_bytes + (size_t)round_up((long long)(parts * 2 * sizeof(float)), 256);
+    pl.ws_bytes = pl.info_off + (size_t)units * 8;
     return pl;
 }
 
@@ -782,6 +783,7 @@ int gemma_attn_q4(void* out, const void* q, const void* const* k_codes,
     if (st != GEMMA_OK) return st;
     if (max_seq_len < n_new || !std::isfinite(scale) || !(scale > 0.f))
         return GEMMA_ERR_INVALID_ARG;
+    if (max_seq_len > (1 << 30)) return GEMMA_ERR_UNSUPPORTED;  // positions in 32 bits
     if (c.ring) {
         if ((long long)c.cap < (long long)window + n_new - 1) return GEMMA_ERR_CAPACITY;
     } else if (max_seq_len > c.cap) {
@@ -798,7 +800,7 @@ int gemma_attn_q4(void* out, const void* q, const void* const* k_codes,
     if (n_sm < 0) return GEMMA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if ((long long)n_new * (n_q / n_kv) <= kQ4DirectRows) {
-        const Plan pl =
+        const Q4Plan pl =
             q4_plan(batch, kind, window, n_q, n_kv, head_dim, max_seq_len, n_new, n_sm);
         if (pl.ws_bytes > 0 &&
             (!workspace || workspace_bytes < pl.ws_bytes || !aligned16(workspace)))
@@ -828,14 +830,15 @@ int gemma_attn_q4(void* out, const void* q, const void* const* k_codes,
         p.n_pages = c.pg.n_pages;
         p.k_eq_v = k_eq_v ? 1 : 0;
         p.max_seq_len = max_seq_len;
-        p.n_split = pl.n_split;
-        p.chunk = pl.chunk;
         p.scale_log2 = scale * 1.4426950408889634f;
         p.softcap = softcap;
         p.cap_inner = softcap > 0.f ? scale / softcap : 0.f;
         p.cap_log2 = softcap * 1.4426950408889634f;
-        return gemma::launch_q4_attn(p, c, head_dim, batch, s) == cudaSuccess ? GEMMA_OK
-                                                                               : GEMMA_ERR_CUDA;
+        return gemma::launch_q4_attn(p, c, head_dim, batch, pl.ctas, pl.balanced,
+                                     static_cast<uint8_t*>(workspace) + pl.info_off, s) ==
+                       cudaSuccess
+                   ? GEMMA_OK
+                   : GEMMA_ERR_CUDA;
     }
     const Q4Expand e = q4_expand_plan(batch, kind, window, n_q, n_kv, head_dim, max_seq_len,
                                       n_new, k_eq_v, n_sm);

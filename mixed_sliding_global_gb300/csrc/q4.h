@@ -34,15 +34,18 @@ struct Q4Cache {
     PagedLayout pg;
 };
 
-// Attention of a few query rows straight over the cache (q4_attn.cu). Chunks are multiples of
-// kQ4KeyTile keys; p.n_split > 1 merges partials through p.o_part / p.ml_part, laid out
-// [batch][n_kv][n_tok * G][n_split][head_dim] and [...][2].
+// Attention of a few query rows straight over the cache (q4_attn.cu) by C CTAs: with `balanced`
+// each takes an equal share of the launch's key tiles (parts of units meet in p.o_part
+// [C][2][row tile][head_dim] and p.ml_part [C][2][row tile][2], with two ints per unit in info, and
+// are merged by a second launch), else
+// C is the number of units (sequence, KV head, row tile) and each CTA takes one.
 constexpr int kQ4KeyTile = 128;
-constexpr int kQ4MaxSplit = 128;
+constexpr int kQ4CtasPerSm = 2;
+constexpr int kQ4MaxShares = 512;  // C of a balanced launch
 // rows (token, query head) per CTA
 inline int q4_row_tile(int rows) { return rows > 8 ? 16 : 8; }
-cudaError_t launch_q4_attn(const RowsParams& p, const Q4Cache& c, int head_dim, int batch,
-                           cudaStream_t st);
+cudaError_t launch_q4_attn(const RowsParams& p, const Q4Cache& c, int head_dim, int batch, int C,
+                           int balanced, void* info, cudaStream_t st);
 
 cudaError_t launch_q4_append(const Q4Cache& c, const void* k_new, const void* v_new,
                              const int32_t* write_pos, int batch, int n_new, int head_dim,

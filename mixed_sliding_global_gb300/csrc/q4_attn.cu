@@ -36,16 +36,20 @@ namespace gemma {
 namespace {
 
 constexpr int kT = kQ4KeyTile;      // keys per tile
-constexpr int kWarps = 8;           // warps per CTA
-constexpr int kThreads = kWarps * 32;
+constexpr int kWarps = 8;           // consumer warps per CTA, and a producer
+constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kMaxStages = 8;
 constexpr float kLazyLog2 = 8.f;
+constexpr float kNoMax = -3.0e38f;  // reference before any key (finite: x - kNoMax is no NaN)
 constexpr uint32_t kPairMask = 0x80078007u;
 
 struct Q4AttnParams {
     RowsParams r;  // shapes, masks, q / out / partials (k, v: the code arrays)
     const __nv_bfloat16* k_scales;
     const __nv_bfloat16* v_scales;
+    int batch;
+    int balanced;     // equal shares of the launch's key tiles per CTA (else a CTA per unit)
+    int2* info;       // [units]: {first part row tile, last CTA} of a shared unit, or {-1, -1}
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -55,6 +59,14 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_zero(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
     uint32_t r;
@@ -66,11 +78,23 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+// Slot j of a word: its pair of codes as two fp16 numbers code * 2^-24.
 __device__ __forceinline__ uint32_t code_pair(uint32_t word, int j) {
     return __funnelshift_r(word, word, 4 * j) & kPairMask;
 }
-// Barrier of the CTA that also ORs a flag over its threads.
-__device__ __forceinline__ bool cta_vote(bool flag) { return __syncthreads_or(flag) != 0; }
+
+// Barriers of the consumer warps; the vote also ORs a flag over their threads.
+__device__ __forceinline__ void consumer_sync() { named_bar_sync(1, kWarps * 32); }
+__device__ __forceinline__ bool consumer_vote(bool flag) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "bar.red.or.pred p, 1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)flag), "n"(kWarps * 32)
+        : "memory");
+    return r != 0;
+}
 
 template <int D>
 struct Q4Layout {
@@ -80,7 +104,6 @@ struct Q4Layout {
     static constexpr int CODES = kT * ROWB;                     // one tile of codes
     static constexpr int SCALES = kT * NG * 2;                  // and of scales
     static constexpr int OP = CODES + (SCALES + 1023) / 1024 * 1024;  // one operand of a stage
-    static constexpr int O_STRIDE = D + 4;                      // fp32 words per output row
 };
 
 // Byte of a code tile at (key, byte x of its row); 128-byte swizzle where rows fill it.
@@ -98,23 +121,98 @@ __device__ __forceinline__ int key_of_row(int g) {
     return Q4Layout<D>::BOXB < 128 ? g : (g & 3) * 2 + (g >> 2);
 }
 
-struct Range {
-    int lo, hi;  // keys [lo, hi) of one row
-};
-__device__ __forceinline__ Range row_range(const RowsParams& p, int len, int R) {
-    const int pos = len - p.n_tok + R / p.G;
-    return Range{p.is_sliding ? max(0, pos - p.window + 1) : 0, pos + 1};
-}
-// First key of a row tile's chunks: its first row's first key, rounded down to where a tile may
-// start (32 keeps scale rows 16-byte aligned; a tile must not wrap round a ring or leave a page).
-__device__ __forceinline__ int tile_base(const RowsParams& p, int lo) {
+// Rounded-down first position of a step's keys (from the first query's window): 32 keeps scale
+// rows 16-byte aligned; a tile must not wrap round a ring or leave a page.
+__device__ __forceinline__ int first_key(const RowsParams& p, int len) {
+    const int lo = p.is_sliding ? max(0, len - p.n_tok - p.window + 1) : 0;
     return lo & ~((p.ring || p.page_size ? kT : 32) - 1);
 }
 __device__ __forceinline__ bool bad_length(const RowsParams& p, int len) {
     return len < p.n_tok || (!p.ring && len > p.cap) || len > p.max_seq_len;
 }
+// Key tiles of a unit (KV head, row tile) of a sequence; an invalid sequence has one, whose CTA
+// writes the zeros.
+__device__ __forceinline__ int unit_tiles(const RowsParams& p, int len) {
+    return bad_length(p, len) ? 1 : (len - first_key(p, len) + kT - 1) / kT;
+}
 
-template <int D, int NQ, int MINB>
+// The work of a launch is one line of key tiles: sequences in order, a sequence's units in order, a
+// unit's tiles in order. CTA c of C takes tiles [c total / C, (c + 1) total / C), so every CTA
+// streams the same number of keys whatever the lengths; it meets whole units and at most two
+// parts of units, which the merge launch puts together. CTAs beyond the number of tiles have no
+// share. Where a tile x lies:
+__device__ __forceinline__ int shares(long long total, int ctas) {
+    return total < ctas ? (int)total : ctas;
+}
+__device__ __forceinline__ long long share_start(long long total, int C, int c) {
+    return total * c / C;
+}
+__device__ __forceinline__ int share_of(long long total, int C, long long x) {
+    return (int)(((x + 1) * C + total - 1) / total) - 1;
+}
+
+// Sum over the CTA's threads of their values before this one, and the total.
+__device__ __forceinline__ int cta_scan(int v, int* s_warp, int& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) s_warp[warp] = x;
+    __syncthreads();
+    int before = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += s_warp[w];
+        total += s_warp[w];
+    }
+    __syncthreads();
+    return before + x - v;
+}
+
+// One part of a unit: sequence b, KV head kvh, row tile rt, key tiles [t0, t1) of n.
+struct Part {
+    int b, kvh, rt, t0, t1, n, len;
+};
+struct Walk {
+    int b, u, t, n, len;  // next tile: t of unit u (of the sequence's upb) of sequence b
+    __device__ void enter(const RowsParams& p, int seq) {
+        b = seq;
+        len = p.seq_lens[seq];
+        n = unit_tiles(p, len);
+    }
+    // Take up to `left` tiles of the current unit and step on.
+    __device__ Part take(const RowsParams& p, int n_rt, int upb, int batch, int left) {
+        Part s{b, u / n_rt, u % n_rt, t, n, n, len};
+        if (s.t1 - t > left) s.t1 = t + left;
+        t = s.t1;
+        if (t == n) {
+            t = 0;
+            if (++u == upb) {
+                u = 0;
+                if (b + 1 < batch) enter(p, b + 1);
+            }
+        }
+        return s;
+    }
+};
+
+// What the consumer warps need of the current part (in shared memory: it would take a dozen
+// registers of every thread through the tile loop).
+struct Job {
+    Part part;
+    int row0, n_rows, key_first, whole, slot;
+    int lo_all, ke;      // keys of any row
+    int lo_max, hi_min;  // keys that every row of the tile may see
+};
+
+// PAIR: at most four rows (NQ = 1). P V then takes the pair of codes of a word's slot as two
+// operand elements of one key, weighted (P, 0) in columns 0..3 and (0, P) in columns 4..7: the
+// even and the odd output columns come out side by side and no codes are re-paired across keys.
+template <int D, int NQ, bool PAIR, int MINB>
 __global__ void __launch_bounds__(kThreads, MINB)
     q4_attn_kernel(const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const Q4AttnParams pp) {
@@ -122,480 +220,712 @@ __global__ void __launch_bounds__(kThreads, MINB)
     using L = Q4Layout<D>;
     constexpr int RT = 8 * NQ;
     constexpr int NG = L::NG;
-    constexpr int KSP = kWarps / NG;   // warps that share a column group
-    constexpr int KW = kT / KSP;       // keys per warp of a tile in P V
+    constexpr int KSP = kWarps / NG;        // warps that share a column group
+    constexpr int KW = kT / KSP;            // keys per warp of a tile in P V
+    constexpr bool QREG = NQ * D <= 256;    // query fragments in registers (else shared memory)
+    constexpr int PW = PAIR ? 16 : 8 * NQ;  // halves of P per key
     const RowsParams& p = pp.r;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ __align__(8) uint64_t full[kMaxStages];
-    __shared__ __align__(16) __half sP[2][NQ][kT][8];
-    __shared__ __align__(16) __half sV[kWarps][KW];
-    __shared__ float sMax[kWarps][RT], sSum[kWarps][RT];
+    __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages];
+    __shared__ __align__(16) __half sP[2][kT * PW];
+    __shared__ __align__(16) __half sV[kWarps][PAIR ? 2 * KW : KW];
+    __shared__ __align__(16) uint32_t sQ[D / 16][32][2 * NQ];
+    __shared__ float sMax[kWarps][RT], sSum[kWarps][RT], sFac[RT];
+    __shared__ int sScan[kThreads / 32], sAt[3];
+    __shared__ Job sJob;
+    __shared__ Walk sWalk;
+    __shared__ long long sAll[3];  // tiles of the launch, CTAs with a share, first tile of this one
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int split = blockIdx.x % p.n_split, rt = blockIdx.x / p.n_split;
-    const int kvh = blockIdx.y, b = blockIdx.z;
-    const int rows_total = p.n_tok * p.G, row0 = rt * RT;
-    const int n_rows = min(RT, rows_total - row0);
-    const bool direct = p.n_split == 1;
-
-    pdl_wait();
-    const int len = p.seq_lens[b];
-    if (bad_length(p, len)) {
-        if (split == 0) {
-            if (threadIdx.x == 0) report(p.err, GEMMA_DEVERR_SEQ_LEN);
-            if (direct)
-                for (int i = threadIdx.x; i < n_rows * (D / 8); i += kThreads) {
-                    const int R = row0 + i / (D / 8), tok = R / p.G;
-                    reinterpret_cast<uint4*>(p.out)[(((size_t)b * p.n_tok + tok) * p.n_q +
-                                                     kvh * p.G + (R - tok * p.G)) * (D / 8) +
-                                                    i % (D / 8)] = make_uint4(0u, 0u, 0u, 0u);
-                }
-        }
-        return;
-    }
-    const Range first = row_range(p, len, row0), last = row_range(p, len, row0 + n_rows - 1);
-    const int kb = tile_base(p, first.lo) + split * p.chunk;
-    const int ke = min(last.hi, kb + p.chunk);
-    if (kb >= ke) return;  // the combine pass skips it
-    const int n_tiles = (ke - kb + kT - 1) / kT;
+    const int g = lane >> 2, tq = lane & 3;
     const int nops = p.k_eq_v ? 1 : 2;
     const int stage_bytes = nops * L::OP;
     const int S = p.n_stages;
+    float* sO = reinterpret_cast<float*>(smem + S * stage_bytes);  // [KSP - 1][RT][D]
+    const int rows_total = p.n_tok * p.G;
+    const int n_rt = (rows_total + RT - 1) / RT, upb = n_rt * p.n_kv;
+    const int batch = pp.batch;
 
-    // Loads of tile t into its stage (one thread). No empty barriers: when the warps have voted on
-    // tile t, every one of them has finished with tile t - 1, whose stage is then refilled.
-    auto load_tile = [&](int t) {
-        const int slots = kv_row_slots(p);
-        uint64_t* bar = &full[t % S];
-        uint8_t* st = smem + (t % S) * stage_bytes;
-        int row = 0, slot = 0;
-        const bool ok = kv_place(p, b, kvh, kb + t * kT, row, slot);
-        // scale rows that exist (a tile may reach behind the last slot; capacities and tile starts
-        // are multiples of 32, so the copies stay multiples of 16 bytes)
-        const uint32_t sbytes = ok ? (uint32_t)(min(kT, slots - slot) * NG * 2) : 0u;
-        if (!ok) {  // a bad page reads as zeros
-            report(p.err, GEMMA_DEVERR_PAGE);
-            row = p.n_pages * p.n_kv;
-            for (int o = 0; o < nops; ++o)
-                for (int i = 0; i < L::SCALES / 16; ++i)
-                    reinterpret_cast<uint4*>(st + o * L::OP + L::CODES)[i] =
-                        make_uint4(0u, 0u, 0u, 0u);
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], kWarps);
         }
-        mbar_arrive_expect_tx(bar, (uint32_t)nops * (L::CODES + sbytes));
-        for (int o = 0; o < nops; ++o) {
-            uint8_t* dst = st + o * L::OP;
+        fence_barrier_init();
+    }
+    pdl_wait();
+    // where this CTA's share starts
+    Walk walk;
+    int left;  // tiles of this CTA
+    if (pp.balanced) {
+        const int per = (batch + kThreads - 1) / kThreads, b0 = min((int)threadIdx.x * per, batch);
+        const int b1 = min(b0 + per, batch);
+        int mine = 0, total;
+        for (int b = b0; b < b1; ++b) mine += unit_tiles(p, p.seq_lens[b]);
+        const int before = cta_scan(mine, sScan, total);
+        const long long all = (long long)total * upb;
+        const int C = shares(all, gridDim.x);
+        if ((int)blockIdx.x >= C) return;
+        const long long x0 = share_start(all, C, blockIdx.x);
+        if (threadIdx.x == 0) {
+            sAll[0] = all;
+            sAll[1] = C;
+            sAll[2] = x0;
+        }
+        left = (int)(share_start(all, C, blockIdx.x + 1) - x0);
+        if (x0 >= (long long)before * upb && x0 < (long long)(before + mine) * upb) {
+            long long x = x0 - (long long)before * upb;
+            int b = b0, n = unit_tiles(p, p.seq_lens[b]);
+            while (x >= (long long)n * upb) {
+                x -= (long long)n * upb;
+                n = unit_tiles(p, p.seq_lens[++b]);
+            }
+            sAt[0] = b;
+            sAt[1] = (int)(x / n);
+            sAt[2] = (int)(x % n);
+        }
+        __syncthreads();
+        walk.enter(p, sAt[0]);
+        walk.u = sAt[1];
+        walk.t = sAt[2];
+    } else {  // one CTA per unit
+        walk.enter(p, blockIdx.x / upb);
+        walk.u = blockIdx.x % upb;
+        walk.t = 0;
+        left = walk.n;
+        __syncthreads();
+    }
+
+    if (warp == kWarps) {
+        // producer: the share's tiles in order, one thread
+        if (lane == 0) {
+            const int slots = kv_row_slots(p);
+            int s = 0, round = 0;  // stage, and how often the ring went round
+            while (left > 0) {
+                const Part part = walk.take(p, n_rt, upb, batch, left);
+                left -= part.t1 - part.t0;
+                const bool bad = bad_length(p, part.len);
+                const int key_first = first_key(p, part.len);
+                for (int t = part.t0; t < part.t1; ++t) {
+                    uint64_t* bar = &full[s];
+                    uint8_t* st = smem + s * stage_bytes;
+                    if (round > 0 && !mbar_wait(&empty[s], (round - 1) & 1, p.err)) return;
+                    if (++s == S) {
+                        s = 0;
+                        ++round;
+                    }
+                    if (bad) {  // no keys: the consumers only count the stage
+                        mbar_arrive(bar);
+                        continue;
+                    }
+                    int row = 0, slot = 0;
+                    const bool ok = kv_place(p, part.b, part.kvh, key_first + t * kT, row, slot);
+                    // scale rows that exist (a tile may reach behind the last slot; capacities
+                    // and tile starts are multiples of 32, so the copies stay multiples of 16 B)
+                    const uint32_t sbytes = ok ? (uint32_t)(min(kT, slots - slot) * NG * 2) : 0u;
+                    if (!ok) {  // a bad page reads as zeros
+                        report(p.err, GEMMA_DEVERR_PAGE);
+                        row = p.n_pages * p.n_kv;
+                        for (int o = 0; o < nops; ++o)
+                            for (int k = 0; k < L::SCALES / 16; ++k)
+                                reinterpret_cast<uint4*>(st + o * L::OP + L::CODES)[k] =
+                                    make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    mbar_arrive_expect_tx(bar, (uint32_t)nops * (L::CODES + sbytes));
+                    for (int o = 0; o < nops; ++o) {
+                        uint8_t* dst = st + o * L::OP;
 #pragma unroll
-            for (int c = 0; c < L::ROWB / L::BOXB; ++c)
-                tma_load_3d(dst + c * kT * 128, o ? &vmap : &kmap, c * 128, slot, row, bar);
-            if (sbytes)
-                bulk_g2s(dst + L::CODES,
-                         (o ? pp.v_scales : pp.k_scales) + ((size_t)row * slots + slot) * NG,
-                         sbytes, bar);
+                        for (int c = 0; c < L::ROWB / L::BOXB; ++c)
+                            tma_load_3d(dst + c * kT * 128, o ? &vmap : &kmap, c * 128, slot, row,
+                                        bar);
+                        if (sbytes)
+                            bulk_g2s(dst + L::CODES,
+                                     (o ? pp.v_scales : pp.k_scales) +
+                                         ((size_t)row * slots + slot) * NG,
+                                     sbytes, bar);
+                    }
+                }
+            }
+        }
+        return;
+    }
+
+    const int wg = warp % NG, ksp = warp / NG;
+    const int krow = warp * 16 + key_of_row<D>(g);  // this lane's keys of S: krow, krow + 8
+    // byte offsets in a tile of the words this lane reads: for S, key krow (krow + 8 lies 8 rows
+    // on), group i at sOff[i % 4] in box i / 4; for P V, an even and an odd key of its group's words
+    constexpr int XO = L::BOXB < 128 ? 1 : (NG < 4 ? NG : 4);
+    int sOff[XO], vOff[2];
+#pragma unroll
+    for (int i = 0; i < XO; ++i) sOff[i] = code_off<D>(krow, i * 32 + tq * 8);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+        vOff[i] = code_off<D>(ksp * KW + 2 * tq + i, wg * 32 + g * 4);
+    const int vsOff = L::CODES + ((ksp * KW + lane) * NG + wg) * 2;  // V's scale of key lane
+    auto s_off = [&](int i) {
+        return L::BOXB < 128 ? sOff[0] + i * 32 : sOff[i % XO] + (i / 4) * (kT * 128);
+    };
+    int done = 0, s = 0;    // tiles taken, the next one's stage
+    uint32_t phase = 0;     // and the parity of its barrier
+    auto next_stage = [&]() {
+        ++done;
+        if (++s == S) {
+            s = 0;
+            phase ^= 1;
         }
     };
+    bool ok = true;
     if (threadIdx.x == 0) {
-        for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
-        fence_barrier_init();
-        for (int t = 0; t < min(S, n_tiles); ++t) load_tile(t);
+        sWalk = walk;
+        sJob.slot = 0;
     }
-    __syncwarp();
-
-    const int g = lane >> 2, tq = lane & 3;
-    // Query fragments: lane (g, tq) holds, of row g of each 8-row tile, elements 16 tq .. 16 tq + 15
-    // of every group, the ones whose codes it reads. A row is scaled by a power of two that brings
-    // its largest element into [2^13, 2^14) (exact unless an element is 2^-37 of that).
-    uint32_t qf[NG * 4][NQ][2];
-    float qscale[NQ];  // 2^-e of row g: score = sum * 2^24 / qscale * scale
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-        const int R = row0 + n * 8 + g;
-        uint4 raw[NG][2];
-        uint32_t mx = 0;
-        if (n * 8 + g < n_rows) {
-            const int tok = R / p.G;
-            const uint4* src = reinterpret_cast<const uint4*>(p.q) +
-                               (((size_t)b * p.n_tok + tok) * p.n_q + kvh * p.G +
-                                (R - tok * p.G)) * (D / 8) + 2 * tq;
-#pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                raw[i][0] = src[i * 8];
-                raw[i][1] = src[i * 8 + 1];
+    while (done < left) {
+        if (threadIdx.x == 0) {
+            Job j;
+            j.part = sWalk.take(p, n_rt, upb, batch, left - done);
+            const Part& part = j.part;
+            j.row0 = part.rt * RT;
+            j.n_rows = min(RT, rows_total - j.row0);
+            j.whole = part.t0 == 0 && part.t1 == part.n;
+            j.slot = 2 * (int)blockIdx.x + (done > 0);
+            j.key_first = first_key(p, part.len);
+            j.lo_all = p.is_sliding ? max(0, part.len - p.n_tok - p.window + 1) : 0;
+            j.ke = min(part.len, j.key_first + part.t1 * kT);
+            const int pos0 = part.len - p.n_tok + j.row0 / p.G;
+            const int pos1 = part.len - p.n_tok + (j.row0 + j.n_rows - 1) / p.G;
+            j.lo_max = p.is_sliding ? max(0, pos1 - p.window + 1) : 0;
+            j.hi_min = min(pos0 + 1, j.ke);
+            if (pp.balanced && part.t0 == 0) {
+                // this CTA has the unit's first tile: tell the merge launch who shares it
+                const int c1 = share_of(sAll[0], (int)sAll[1], sAll[2] + done + part.n - 1);
+                pp.info[(part.b * p.n_kv + part.kvh) * n_rt + part.rt] =
+                    j.whole ? make_int2(-1, -1) : make_int2(j.slot, c1);
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < NG; ++i) raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
+            sJob = j;
         }
+        consumer_sync();
+        // row r of the tile: token (row0 + r) / G, head kvh * G + (row0 + r) % G
+        auto row_at = [&](int r) {
+            const int R = sJob.row0 + r, tok = R / p.G;
+            return (((size_t)sJob.part.b * p.n_tok + tok) * p.n_q + sJob.part.kvh * p.G +
+                    (R - tok * p.G)) * (size_t)D;
+        };
+        if (bad_length(p, sJob.part.len)) {
+            if (threadIdx.x == 0) report(p.err, GEMMA_DEVERR_SEQ_LEN);
+            for (int i = threadIdx.x; i < sJob.n_rows * (D / 8); i += kWarps * 32)
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) +
+                                          row_at(i / (D / 8)) + i % (D / 8) * 8) =
+                    make_uint4(0u, 0u, 0u, 0u);
+            if (lane == 0) mbar_arrive(&empty[s]);
+            next_stage();
+            consumer_sync();  // sJob is rewritten
+            continue;
+        }
+
+        // Query rows as fp16 fragments: lane (g, tq) holds, of row g of each 8-row tile, elements
+        // 16 tq .. 16 tq + 15 of every group, the ones whose codes it reads. A row is scaled by
+        // a power of two that brings its largest element into [2^13, 2^14) (exact unless an
+        // element is below 2^-37 of that).
+        for (int r = warp; r < RT; r += kWarps) {
+            constexpr int CH = (D / 8 + 31) / 32;
+            uint4 raw[CH];
+            uint32_t mx = 0;
+            const __nv_bfloat16* src =
+                static_cast<const __nv_bfloat16*>(p.q) + row_at(min(r, sJob.n_rows - 1));
 #pragma unroll
-        for (int i = 0; i < NG; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const uint32_t w[4] = {raw[i][h].x, raw[i][h].y, raw[i][h].z, raw[i][h].w};
+            for (int c = 0; c < CH; ++c) {
+                const int ch = c * 32 + lane;
+                raw[c] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < sJob.n_rows && ch < D / 8) raw[c] = reinterpret_cast<const uint4*>(src)[ch];
+                const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     mx = max(mx, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
             }
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // biased exponent of the largest element -> factor 2^(13 - (exponent - 127))
-        const int ex = min(max((int)(mx >> 7), 13), 254);
-        qscale[n] = __uint_as_float((uint32_t)(267 - ex) << 23);
+            mx = __reduce_max_sync(0xffffffffu, mx);
+            // biased exponent of the largest element -> factor 2^(13 - (exponent - 127))
+            const float f = __uint_as_float(
+                (uint32_t)(267 - min(max((int)(mx >> 7), 13), 254)) << 23);
+            if (lane == 0) sFac[r] = f;
 #pragma unroll
-        for (int i = 0; i < NG; ++i)
+            for (int c = 0; c < CH; ++c) {
+                const int ch = c * 32 + lane;  // elements 8 ch .. 8 ch + 7
+                if (ch >= D / 8) continue;
+                const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+                uint32_t h[4];
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-                const uint4 v = raw[i][ks >> 1];
-                const uint32_t w0 = ks & 1 ? v.z : v.x, w1 = ks & 1 ? v.w : v.y;
-                qf[i * 4 + ks][n][0] = pack_f16(__uint_as_float(w0 << 16) * qscale[n],
-                                                __uint_as_float(w0 & 0xffff0000u) * qscale[n]);
-                qf[i * 4 + ks][n][1] = pack_f16(__uint_as_float(w1 << 16) * qscale[n],
-                                                __uint_as_float(w1 & 0xffff0000u) * qscale[n]);
+                for (int k = 0; k < 4; ++k)
+                    h[k] = pack_f16(__uint_as_float(w[k] << 16) * f,
+                                    __uint_as_float(w[k] & 0xffff0000u) * f);
+                const int ks = (ch >> 3) * 4 + 2 * (ch & 1), ln = (r & 7) * 4 + ((ch >> 1) & 3);
+                *reinterpret_cast<uint2*>(&sQ[ks][ln][(r >> 3) * 2]) = make_uint2(h[0], h[1]);
+                *reinterpret_cast<uint2*>(&sQ[ks + 1][ln][(r >> 3) * 2]) = make_uint2(h[2], h[3]);
             }
-    }
-    // the rows whose scores this lane holds: 8 n + 2 tq + c
-    float inv[NQ][2], m_run[NQ][2], l_run[NQ][2];
-    int r_lo[NQ][2], r_hi[NQ][2];
-    const float fac = p.softcap > 0.f ? p.cap_inner : p.scale_log2;
-#pragma unroll
-    for (int n = 0; n < NQ; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            inv[n][c] = fac / __shfl_sync(0xffffffffu, qscale[n], (2 * tq + c) * 4);
-            m_run[n][c] = -INFINITY;
-            l_run[n][c] = 0.f;
-            const int r = n * 8 + 2 * tq + c;
-            const Range rr = row_range(p, len, row0 + min(r, n_rows - 1));
-            r_lo[n][c] = r < n_rows ? rr.lo : INT_MAX;
-            r_hi[n][c] = min(rr.hi, ke);
         }
-    float o[4][NQ][4];
+        consumer_sync();
+        uint32_t qf[QREG ? D / 16 : 1][NQ][2];
+        if (QREG) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
-    int v_exp = 6;  // biased exponent that V's scales are relative to
-    const int wg = warp % NG, ksp = warp / NG;
-    const int krow = warp * 16 + key_of_row<D>(g);  // this lane's keys of S: krow, krow + 8
-
-    __syncthreads();
-    bool ok = true;
-    for (int t = 0; t < n_tiles; ++t) {
-        const int s = t % S;
-        if (ok) ok = mbar_wait(&full[s], (t / S) & 1, p.err);
-        const uint8_t* tK = smem + s * stage_bytes;
-        const uint8_t* tV = tK + (nops - 1) * L::OP;
-        const int key0 = kb + t * kT;
-
-        // (1) S of 16 keys
-        float sv[NQ][4];
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) sv[n][0] = sv[n][1] = sv[n][2] = sv[n][3] = 0.f;
-        {
-            const __nv_bfloat16* sk = reinterpret_cast<const __nv_bfloat16*>(tK + L::CODES);
-#pragma unroll
-            for (int i = 0; i < NG; ++i) {
-                const uint2 wa =
-                    *reinterpret_cast<const uint2*>(tK + code_off<D>(krow, i * 32 + tq * 8));
-                const uint2 wb =
-                    *reinterpret_cast<const uint2*>(tK + code_off<D>(krow + 8, i * 32 + tq * 8));
-                float acc[NQ][4];
-#pragma unroll
-                for (int n = 0; n < NQ; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-#pragma unroll
-                for (int ks = 0; ks < 4; ++ks) {
-                    const uint32_t xa = ks < 2 ? wa.x : wa.y, xb = ks < 2 ? wb.x : wb.y;
-                    const int j = 2 * (ks & 1);
-                    const uint32_t a0 = code_pair(xa, j), a1 = code_pair(xb, j);
-                    const uint32_t a2 = code_pair(xa, j + 1), a3 = code_pair(xb, j + 1);
-#pragma unroll
-                    for (int n = 0; n < NQ; ++n)
-                        mma_f16(acc[n], a0, a1, a2, a3, qf[i * 4 + ks][n][0], qf[i * 4 + ks][n][1]);
-                }
-                const float ska = __bfloat162float(sk[krow * NG + i]);
-                const float skb = __bfloat162float(sk[(krow + 8) * NG + i]);
+            for (int k = 0; k < D / 16; ++k)
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
-                    sv[n][0] = fmaf(acc[n][0], ska, sv[n][0]);
-                    sv[n][1] = fmaf(acc[n][1], ska, sv[n][1]);
-                    sv[n][2] = fmaf(acc[n][2], skb, sv[n][2]);
-                    sv[n][3] = fmaf(acc[n][3], skb, sv[n][3]);
+                    qf[QREG ? k : 0][n][0] = sQ[k][lane][2 * n];
+                    qf[QREG ? k : 0][n][1] = sQ[k][lane][2 * n + 1];
                 }
-            }
         }
-        // scores in log2 units, masked keys -inf
-        bool grow = false;
+        // the rows whose scores this lane holds: 8 n + 2 tq + c
+        float inv[NQ][2], m_run[NQ][2], l_run[NQ][2];
+        const float fac = p.softcap > 0.f ? p.cap_inner : p.scale_log2;
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int c = k & 1, key = key0 + krow + 8 * (k >> 1);
-                float x = sv[n][k] * 16777216.f * inv[n][c];
-                if (p.softcap > 0.f) x = p.cap_log2 * tanhf(x);
-                x = key >= r_lo[n][c] && key < r_hi[n][c] ? x : -INFINITY;
-                sv[n][k] = x;
-                grow = grow || x > m_run[n][c] + kLazyLog2;
+            for (int c = 0; c < 2; ++c) {
+                const int r = n * 8 + 2 * tq + c;
+                inv[n][c] = fac / sFac[r];
+                m_run[n][c] = kNoMax;
+                l_run[n][c] = 0.f;
             }
-        __half(*P)[kT][8] = sP[t & 1];
-        float pr[NQ][4];
-        auto exponentiate = [&]() {
+        float o[4][NQ][4];
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) {
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float m = m_run[n][k & 1];
-                    pr[n][k] = fast_exp2(sv[n][k] - (m == -INFINITY ? 0.f : m));
+            for (int n = 0; n < NQ; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
+        int v_exp = 6;  // biased exponent that V's scales are relative to
+
+        for (int t = sJob.part.t0, t1 = sJob.part.t1; t < t1; ++t) {
+            if (ok) ok = mbar_wait(&full[s], phase, p.err);
+            const uint8_t* tK = smem + s * stage_bytes;
+            const uint8_t* tV = tK + (nops - 1) * L::OP;
+            const int key0 = sJob.key_first + t * kT;
+
+            // (1) S of 16 keys
+            float sv[NQ][4];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) sv[n][0] = sv[n][1] = sv[n][2] = sv[n][3] = 0.f;
+            {
+                const uint8_t* sk = tK + L::CODES;
+                uint32_t ska[(NG + 1) / 2], skb[(NG + 1) / 2];  // scales of the two keys, bf16 pairs
+                if (NG == 8) {
+                    *reinterpret_cast<uint4*>(ska) = reinterpret_cast<const uint4*>(sk)[krow];
+                    *reinterpret_cast<uint4*>(skb) = reinterpret_cast<const uint4*>(sk)[krow + 8];
+                } else if (NG == 4) {
+                    *reinterpret_cast<uint2*>(ska) = reinterpret_cast<const uint2*>(sk)[krow];
+                    *reinterpret_cast<uint2*>(skb) = reinterpret_cast<const uint2*>(sk)[krow + 8];
+                } else if (NG == 2) {
+                    ska[0] = reinterpret_cast<const uint32_t*>(sk)[krow];
+                    skb[0] = reinterpret_cast<const uint32_t*>(sk)[krow + 8];
+                } else {
+                    ska[0] = reinterpret_cast<const uint16_t*>(sk)[krow];
+                    skb[0] = reinterpret_cast<const uint16_t*>(sk)[krow + 8];
                 }
-                *reinterpret_cast<uint32_t*>(&P[n][krow][2 * tq]) = pack_f16(pr[n][0], pr[n][1]);
-                *reinterpret_cast<uint32_t*>(&P[n][krow + 8][2 * tq]) = pack_f16(pr[n][2], pr[n][3]);
+#pragma unroll
+                for (int i = 0; i < NG; ++i) {
+                    const uint2 wa =
+                        *reinterpret_cast<const uint2*>(tK + s_off(i));
+                    const uint2 wb =
+                        *reinterpret_cast<const uint2*>(tK + s_off(i) + 8 * L::BOXB);
+                    float acc[NQ][4];
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const uint32_t xa = ks < 2 ? wa.x : wa.y, xb = ks < 2 ? wb.x : wb.y;
+                        const int j = 2 * (ks & 1);
+                        const uint32_t a0 = code_pair(xa, j), a1 = code_pair(xb, j);
+                        const uint32_t a2 = code_pair(xa, j + 1), a3 = code_pair(xb, j + 1);
+                        uint32_t bq[2 * NQ];
+                        if (QREG) {
+#pragma unroll
+                            for (int n = 0; n < NQ; ++n) {
+                                bq[2 * n] = qf[QREG ? i * 4 + ks : 0][n][0];
+                                bq[2 * n + 1] = qf[QREG ? i * 4 + ks : 0][n][1];
+                            }
+                        } else if (NQ == 2) {
+                            *reinterpret_cast<uint4*>(bq) =
+                                *reinterpret_cast<const uint4*>(sQ[i * 4 + ks][lane]);
+                        } else {
+                            *reinterpret_cast<uint2*>(bq) =
+                                *reinterpret_cast<const uint2*>(sQ[i * 4 + ks][lane]);
+                        }
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n) {
+                            if (ks == 0) mma_f16_zero(acc[n], a0, a1, a2, a3, bq[2 * n], bq[2 * n + 1]);
+                            else mma_f16(acc[n], a0, a1, a2, a3, bq[2 * n], bq[2 * n + 1]);
+                        }
+                    }
+                    const float fa = __uint_as_float(i & 1 ? ska[i / 2] & 0xffff0000u : ska[i / 2] << 16);
+                    const float fb = __uint_as_float(i & 1 ? skb[i / 2] & 0xffff0000u : skb[i / 2] << 16);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        sv[n][0] = fmaf(acc[n][0], fa, sv[n][0]);
+                        sv[n][1] = fmaf(acc[n][1], fa, sv[n][1]);
+                        sv[n][2] = fmaf(acc[n][2], fb, sv[n][2]);
+                        sv[n][3] = fmaf(acc[n][3], fb, sv[n][3]);
+                    }
+                }
             }
-        };
-        exponentiate();
-        // V's scales of this warp's keys and group, as fp16 relative to 2^v_exp
-        {
-            const __nv_bfloat16* vs = reinterpret_cast<const __nv_bfloat16*>(tV + L::CODES);
-            uint32_t sb[(KW + 31) / 32], mx = 0;
+            // scores in log2 units; masked keys -inf (a tile inside every row's range has none)
+            const bool edge = key0 < sJob.lo_max || key0 + kT > sJob.hi_min;
+            if (p.softcap > 0.f) {
 #pragma unroll
-            for (int i = 0; i < (KW + 31) / 32; ++i) {
-                const int k = i * 32 + lane, key = key0 + ksp * KW + k;
-                sb[i] = 0;
-                if (k < KW && key >= first.lo && key < ke)
-                    sb[i] = __bfloat16_as_ushort(vs[(ksp * KW + k) * NG + wg]);
-                if (sb[i] < 0x7f80u) mx = max(mx, sb[i]);
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        sv[n][k] = p.cap_log2 * tanhf(sv[n][k] * 16777216.f * inv[n][k & 1]);
+            } else {
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) sv[n][k] = sv[n][k] * 16777216.f * inv[n][k & 1];
             }
-            mx = __reduce_max_sync(0xffffffffu, mx) >> 7;
-            if ((int)mx > v_exp) {
-                const float a = v_exp - (int)mx < -126
-                                    ? 0.f
-                                    : __uint_as_float((uint32_t)(127 + v_exp - (int)mx) << 23);
-                v_exp = (int)mx;
+            if (edge) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                    for (int n = 0; n < NQ; ++n)
+                    for (int c = 0; c < 2; ++c) {
+                        const int r = min(n * 8 + 2 * tq + c, sJob.n_rows - 1);
+                        const int pos = sJob.part.len - p.n_tok + (sJob.row0 + r) / p.G;
+                        const int lo = p.is_sliding ? pos - p.window + 1 : 0;
+                        const int hi = min(pos + 1, sJob.ke);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) o[i][n][k] *= a;
+                        for (int h = 0; h < 2; ++h) {
+                            const int key = key0 + krow + 8 * h;
+                            if (key < lo || key >= hi) sv[n][2 * h + c] = -INFINITY;
+                        }
+                    }
             }
-            const float f = __uint_as_float((uint32_t)(259 - v_exp) << 23);  // 2^(5 - (v_exp - 127))
-#pragma unroll
-            for (int i = 0; i < (KW + 31) / 32; ++i)
-                if (i * 32 + lane < KW)
-                    sV[warp][i * 32 + lane] = __float2half_rn(__uint_as_float(sb[i] << 16) * f);
-        }
-        const bool moved = cta_vote(grow);
-        if (threadIdx.x == 0 && t > 0 && t - 1 + S < n_tiles) load_tile(t - 1 + S);
-        __syncwarp();
-        if (moved) {
-            // the reference moves: the rows' maxima over the CTA's warps, P anew
+            bool grow = false;
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float mx = fmaxf(sv[n][c], sv[n][c + 2]);
+                for (int c = 0; c < 2; ++c)
+                    grow = grow || fmaxf(sv[n][c], sv[n][c + 2]) > m_run[n][c] + kLazyLog2;
+            __half* P = sP[done & 1];
+            float pr[NQ][4];
+            auto exponentiate = [&]() {
 #pragma unroll
-                    for (int x = 4; x < 32; x <<= 1)
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-                    if (g == 0) sMax[warp][n * 8 + 2 * tq + c] = mx;
+                for (int n = 0; n < NQ; ++n) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) pr[n][k] = fast_exp2(sv[n][k] - m_run[n][k & 1]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int key = krow + 8 * h;
+                        if (PAIR) {  // [key][8] words: columns q (P, 0), 4 + q (0, P)
+                            if (tq < 2) {
+                                uint32_t* d = reinterpret_cast<uint32_t*>(P) + key * 8 + 2 * tq;
+                                const uint32_t e = pack_f16(pr[n][2 * h], 0.f);
+                                const uint32_t f = pack_f16(pr[n][2 * h + 1], 0.f);
+                                *reinterpret_cast<uint2*>(d) = make_uint2(e, f);
+                                *reinterpret_cast<uint2*>(d + 4) = make_uint2(e << 16, f << 16);
+                            }
+                        } else {     // planes of 8 rows
+                            *reinterpret_cast<uint32_t*>(P + (n * kT + key) * 8 + 2 * tq) =
+                                pack_f16(pr[n][2 * h], pr[n][2 * h + 1]);
+                        }
+                    }
                 }
-            __syncthreads();
+            };
+            exponentiate();
+            // V's scales of this warp's keys and group, as fp16 relative to 2^v_exp
+            {
+                const uint16_t* vs = reinterpret_cast<const uint16_t*>(tV + vsOff);
+                uint32_t sb[(KW + 31) / 32], mx = 0;
 #pragma unroll
-            for (int n = 0; n < NQ; ++n)
+                for (int i = 0; i < (KW + 31) / 32; ++i) {
+                    const int k = i * 32 + lane, key = key0 + ksp * KW + k;
+                    sb[i] = k < KW ? vs[i * 32 * NG] : 0;
+                    if (edge && (key < sJob.lo_all || key >= sJob.ke)) sb[i] = 0;  // may hold anything
+                    mx = max(mx, sb[i]);
+                }
+                // (a NaN scale, exponent 255, leaves NaN in its column group either way)
+                mx = min(__reduce_max_sync(0xffffffffu, mx) >> 7, 254u);
+                if ((int)mx > v_exp) {
+                    const float a = v_exp - (int)mx < -126
+                                        ? 0.f
+                                        : __uint_as_float((uint32_t)(127 + v_exp - (int)mx) << 23);
+                    v_exp = (int)mx;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float mx = m_run[n][c];
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, sMax[w][n * 8 + 2 * tq + c]);
-                    if (mx > m_run[n][c]) {
-                        const float a = fast_exp2(m_run[n][c] - mx);  // 0 from -inf
-                        m_run[n][c] = mx;
-                        l_run[n][c] *= a;
+                        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) o[i][n][k] *= a;
+                }
+                const float f = __uint_as_float((uint32_t)(259 - v_exp) << 23);  // 2^(5-(v_exp-127))
+#pragma unroll
+                for (int i = 0; i < (KW + 31) / 32; ++i)
+                    if (i * 32 + lane < KW) {
+                        const float x = __uint_as_float(sb[i] << 16) * f;
+                        if (PAIR)
+                            reinterpret_cast<uint32_t*>(sV[warp])[i * 32 + lane] = pack_f16(x, x);
+                        else
+                            sV[warp][i * 32 + lane] = __float2half_rn(x);
+                    }
+            }
+            if (consumer_vote(grow)) {
+                // the reference moves: the rows' maxima over the CTA's warps, P anew
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float mx = fmaxf(sv[n][c], sv[n][c + 2]);
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1)
+                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+                        if (g == 0) sMax[warp][n * 8 + 2 * tq + c] = mx;
+                    }
+                consumer_sync();
+#pragma unroll
+                for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float mx = m_run[n][c];
+#pragma unroll
+                        for (int w = 0; w < kWarps; ++w)
+                            mx = fmaxf(mx, sMax[w][n * 8 + 2 * tq + c]);
+                        float a = 1.f;
+                        if (mx > m_run[n][c]) {
+                            a = fast_exp2(m_run[n][c] - mx);  // 0 from kNoMax
+                            m_run[n][c] = mx;
+                            l_run[n][c] *= a;
+                        }
+                        if (PAIR) a = __shfl_sync(0xffffffffu, a, (lane & ~3) | (tq & 1));
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             o[i][n][c] *= a;
                             o[i][n][c + 2] *= a;
                         }
                     }
+                exponentiate();
+                consumer_sync();
+            }
+#pragma unroll
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) l_run[n][c] += pr[n][c] + pr[n][c + 2];
+
+            // (2) O of 64 columns over this warp's keys
+            if constexpr (PAIR) {
+                // 8 keys per step: operand elements 2 tq, 2 tq + 1 are the codes of key 2 tq's
+                // slot pair, 2 tq + 8, 2 tq + 9 those of key 2 tq + 1; MMA rows g, g + 8 of tile i
+                // are columns (8 g + 4 i, + 1) and (8 g + 4 i + 2, + 3) of the group
+#pragma unroll
+                for (int kk = 0; kk < KW; kk += 8) {
+                    const int kt = ksp * KW + kk + 2 * tq;
+                    const uint32_t* P32 = reinterpret_cast<const uint32_t*>(P);
+                    const uint2 sc = *reinterpret_cast<const uint2*>(
+                        reinterpret_cast<const uint32_t*>(sV[warp]) + kk + 2 * tq);
+                    const uint32_t b0 = mul_f16x2(P32[kt * 8 + g], sc.x);
+                    const uint32_t b1 = mul_f16x2(P32[(kt + 1) * 8 + g], sc.y);
+                    const uint32_t w0 =
+                        *reinterpret_cast<const uint32_t*>(tV + vOff[0] + kk * L::BOXB);
+                    const uint32_t w1 =
+                        *reinterpret_cast<const uint32_t*>(tV + vOff[1] + kk * L::BOXB);
+                    mma_f16(o[0][0], code_pair(w0, 0), code_pair(w0, 1),
+                            code_pair(w1, 0), code_pair(w1, 1), b0, b1);
+                    mma_f16(o[1][0], code_pair(w0, 2), code_pair(w0, 3),
+                            code_pair(w1, 2), code_pair(w1, 3), b0, b1);
                 }
-            exponentiate();
-            __syncthreads();
+            } else {
+#pragma unroll
+                for (int kk = 0; kk < KW; kk += 16) {
+                    const int kt = ksp * KW + kk;
+                    uint32_t bf[NQ][2];
+                    if (NQ == 2) {
+                        const uint32_t a = smem_u32(P + ((lane >> 4) * kT + kt + (lane & 15)) * 8);
+                        ldsm_x4_t(a, bf[0][0], bf[0][1], bf[NQ - 1][0], bf[NQ - 1][1]);
+                    } else {
+                        const uint32_t a = smem_u32(P + (kt + (lane & 15)) * 8);
+                        asm volatile(
+                            "ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
+                            : "=r"(bf[0][0]), "=r"(bf[0][1])
+                            : "r"(a));
+                    }
+                    const uint32_t s0 = *reinterpret_cast<const uint32_t*>(&sV[warp][kk + 2 * tq]);
+                    const uint32_t s1 =
+                        *reinterpret_cast<const uint32_t*>(&sV[warp][kk + 2 * tq + 8]);
+#pragma unroll
+                    for (int n = 0; n < NQ; ++n) {
+                        bf[n][0] = mul_f16x2(bf[n][0], s0);
+                        bf[n][1] = mul_f16x2(bf[n][1], s1);
+                    }
+                    uint32_t w[4];  // words of keys 2 tq, + 1, + 8, + 9: columns 8 g .. 8 g + 7
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        w[k] = *reinterpret_cast<const uint32_t*>(
+                            tV + vOff[k & 1] + (kk + 8 * (k >> 1)) * L::BOXB);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {  // MMA rows g, g + 8: columns 8 g + 2 i, + 1
+                        uint32_t r[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) r[k] = code_pair(w[k], i);
+                        const uint32_t a0 = __byte_perm(r[0], r[1], 0x5410);
+                        const uint32_t a1 = __byte_perm(r[0], r[1], 0x7632);
+                        const uint32_t a2 = __byte_perm(r[2], r[3], 0x5410);
+                        const uint32_t a3 = __byte_perm(r[2], r[3], 0x7632);
+#pragma unroll
+                        for (int n = 0; n < NQ; ++n)
+                            mma_f16(o[i][n], a0, a1, a2, a3, bf[n][0], bf[n][1]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[s]);
+            next_stage();
         }
+
+        // ---------------------------------- the part's rows ----------------------------------
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) l_run[n][c] += pr[n][c] + pr[n][c + 2];
-
-        // (2) O of 64 columns over this warp's keys
-#pragma unroll 2
-        for (int kk = 0; kk < KW; kk += 16) {
-            const int kt = ksp * KW + kk;
-            uint32_t bf[NQ][2];
-            if (NQ == 2) {
-                const uint32_t a = smem_u32(&P[lane >> 4][kt + (lane & 15)][0]);
-                ldsm_x4_t(a, bf[0][0], bf[0][1], bf[NQ - 1][0], bf[NQ - 1][1]);
-            } else {
-                const uint32_t a = smem_u32(&P[0][kt + (lane & 15)][0]);
-                asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
-                             : "=r"(bf[0][0]), "=r"(bf[0][1])
-                             : "r"(a));
+            for (int c = 0; c < 2; ++c) {
+                float l = l_run[n][c];
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+                if (g == 0) sSum[warp][n * 8 + 2 * tq + c] = l;
             }
-            const uint32_t s0 = *reinterpret_cast<const uint32_t*>(&sV[warp][kk + 2 * tq]);
-            const uint32_t s1 = *reinterpret_cast<const uint32_t*>(&sV[warp][kk + 2 * tq + 8]);
+        // this lane's columns of rows q(n, c): x = wg * 64 + 8 g .. + 7
+        const float f2 = __uint_as_float((uint32_t)(v_exp - 5) << 23);  // 2^(v_exp - 127 - 5)
+        float v[NQ][2][8];
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) {
-                bf[n][0] = mul_f16x2(bf[n][0], s0);
-                bf[n][1] = mul_f16x2(bf[n][1], s1);
-            }
-            uint32_t w[4];  // words of keys 2 tq, 2 tq + 1, 2 tq + 8, 2 tq + 9: columns 8 g .. 8 g + 7
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                w[k] = *reinterpret_cast<const uint32_t*>(
-                    tV + code_off<D>(kt + 2 * tq + (k & 1) + 8 * (k >> 1), wg * 32 + g * 4));
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {  // MMA rows g, g + 8: columns 8 g + 2 i, 8 g + 2 i + 1
-                const uint32_t r0 = code_pair(w[0], i), r1 = code_pair(w[1], i);
-                const uint32_t r2 = code_pair(w[2], i), r3 = code_pair(w[3], i);
-                const uint32_t a0 = __byte_perm(r0, r1, 0x5410), a1 = __byte_perm(r0, r1, 0x7632);
-                const uint32_t a2 = __byte_perm(r2, r3, 0x5410), a3 = __byte_perm(r2, r3, 0x7632);
+                for (int i = 0; i < 4; ++i) {
+                    if (PAIR) {
+                        // lanes tq < 2 hold the even columns of rows 2 tq + c, tq >= 2 the odd ones
+                        // of rows 2 (tq - 2) + c; o[i / 2]: columns 8 g + 4 (i / 2) + 2 (i & 1)
+                        const float mine = o[i / 2][0][c + 2 * (i & 1)] * 16777216.f * f2;
+                        const float other = __shfl_xor_sync(0xffffffffu, mine, 2);
+                        v[n][c][2 * i] = tq < 2 ? mine : other;
+                        v[n][c][2 * i + 1] = tq < 2 ? other : mine;
+                    } else {
+                        v[n][c][2 * i] = o[i][n][c] * 16777216.f * f2;
+                        v[n][c][2 * i + 1] = o[i][n][c + 2] * 16777216.f * f2;
+                    }
+                }
+        if (KSP > 1 && ksp > 0 && (!PAIR || tq < 2)) {
 #pragma unroll
-                for (int n = 0; n < NQ; ++n) mma_f16(o[i][n], a0, a1, a2, a3, bf[n][0], bf[n][1]);
-            }
+            for (int n = 0; n < NQ; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float4* d = reinterpret_cast<float4*>(
+                        sO + ((size_t)(ksp - 1) * RT + n * 8 + 2 * tq + c) * D + wg * 64 + g * 8);
+                    d[0] = make_float4(v[n][c][0], v[n][c][1], v[n][c][2], v[n][c][3]);
+                    d[1] = make_float4(v[n][c][4], v[n][c][5], v[n][c][6], v[n][c][7]);
+                }
         }
-        __syncwarp();
-    }
-
-    // ------------------------------------ epilogue -------------------------------------------
+        consumer_sync();
+        if (ksp == 0 && (!PAIR || tq < 2)) {
 #pragma unroll
-    for (int n = 0; n < NQ; ++n)
+            for (int n = 0; n < NQ; ++n)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            float l = l_run[n][c];
+                for (int c = 0; c < 2; ++c) {
+                    const int r = n * 8 + 2 * tq + c, x = wg * 64 + g * 8;
+                    if (r >= sJob.n_rows) continue;
 #pragma unroll
-            for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-            if (g == 0) {
-                sSum[warp][n * 8 + 2 * tq + c] = l;
-                if (warp == 0) sMax[0][n * 8 + 2 * tq + c] = m_run[n][c];
-            }
+                    for (int h = 1; h < KSP; ++h)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            v[n][c][k] += sO[((size_t)(h - 1) * RT + r) * D + x + k];
+                    float l = 0.f;
+#pragma unroll
+                    for (int w = 0; w < kWarps; ++w) l += sSum[w][r];
+                    const float* y = v[n][c];
+                    if (sJob.whole) {
+                        const float il = 1.f / l;
+                        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row_at(r) + x) =
+                            make_uint4(pack_bf16(y[0] * il, y[1] * il), pack_bf16(y[2] * il, y[3] * il),
+                                       pack_bf16(y[4] * il, y[5] * il), pack_bf16(y[6] * il, y[7] * il));
+                    } else {
+                        const size_t pr = (size_t)sJob.slot * RT + r;
+                        float4* d = reinterpret_cast<float4*>(p.o_part + pr * D + x);
+                        d[0] = make_float4(y[0], y[1], y[2], y[3]);
+                        d[1] = make_float4(y[4], y[5], y[6], y[7]);
+                        if (wg == 0 && g == 0)
+                            reinterpret_cast<float2*>(p.ml_part)[pr] = make_float2(m_run[n][c], l);
+                    }
+                }
         }
-    __syncthreads();  // every tile consumed: the stages are free
-    float* sO = reinterpret_cast<float*>(smem);  // [KSP][RT][O_STRIDE]
-    const float f2 = __uint_as_float((uint32_t)(v_exp - 5) << 23);  // 2^(v_exp - 127 - 5)
-#pragma unroll
-    for (int n = 0; n < NQ; ++n)
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            float* dst = sO + ((size_t)ksp * RT + n * 8 + 2 * tq + c) * L::O_STRIDE + wg * 64 + g * 8;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<float2*>(dst + 2 * i) =
-                    make_float2(o[i][n][c] * 16777216.f * f2, o[i][n][c + 2] * 16777216.f * f2);
-        }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n_rows * (D / 8); i += kThreads) {
-        const int r = i / (D / 8), x = (i - r * (D / 8)) * 8;
-        float v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = 0.f;
-#pragma unroll
-        for (int h = 0; h < KSP; ++h)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] += sO[((size_t)h * RT + r) * L::O_STRIDE + x + k];
-        float l = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) l += sSum[w][r];
-        const int R = row0 + r;
-        if (direct) {
-            const int tok = R / p.G;
-            const float il = 1.f / l;
-            reinterpret_cast<uint4*>(p.out)[((((size_t)b * p.n_tok + tok) * p.n_q + kvh * p.G +
-                                              (R - tok * p.G)) * D + x) / 8] =
-                make_uint4(pack_bf16(v[0] * il, v[1] * il), pack_bf16(v[2] * il, v[3] * il),
-                           pack_bf16(v[4] * il, v[5] * il), pack_bf16(v[6] * il, v[7] * il));
-        } else {
-            const size_t pr = (((size_t)b * p.n_kv + kvh) * rows_total + R) * p.n_split + split;
-            float4* dst = reinterpret_cast<float4*>(p.o_part + pr * D + x);
-            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-            if (x == 0) {
-                p.ml_part[2 * pr] = sMax[0][r];
-                p.ml_part[2 * pr + 1] = l;
-            }
-        }
+        consumer_sync();  // sJob, sSum, sO and sQ are rewritten for the next part
     }
 }
 
-// Merge of a row's chunks: M = max m_c, out = sum 2^(m_c - M) O_c / sum 2^(m_c - M) l_c. One CTA
-// per row; thread groups share out the chunks and meet in shared memory, in a fixed order.
+// Merge of the rows of units that several CTAs shared: M = max m_c,
+// out = sum 2^(m_c - M) O_c / sum 2^(m_c - M) l_c. A CTA takes `cols` columns of one row: all of
+// them, or 64 when there are few rows (a long cache of one sequence leaves a part per SM, and many
+// short loads at once hide their latency). cols / 4 threads read a part; the groups of threads
+// that share out the parts meet in shared memory, in a fixed order.
 constexpr int kMergeThreads = 256;
 
-template <int D>
-__global__ void __launch_bounds__(kMergeThreads) q4_merge_kernel(const RowsParams p, int row_tile) {
+__global__ void __launch_bounds__(kMergeThreads) q4_merge_kernel(const Q4AttnParams pp, int D,
+                                                                 int cols, int row_tile) {
     pdl_launch_dependents();
     pdl_wait();
-    constexpr int TPG = D / 4, NGRP = kMergeThreads / TPG;
-    __shared__ float s_w[kQ4MaxSplit];
+    const RowsParams& p = pp.r;
     __shared__ float4 s_red[kMergeThreads];
-    __shared__ float s_inv;
-    const int rows_total = p.n_tok * p.G;
-    const int R = blockIdx.x, kvh = blockIdx.y, b = blockIdx.z;
-    const int tok = R / p.G, head = kvh * p.G + R - tok * p.G, tid = threadIdx.x;
-    __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(p.out) +
-                         (((size_t)b * p.n_tok + tok) * p.n_q + head) * D;
-    const int len = p.seq_lens[b];
-    if (bad_length(p, len)) {
-        for (int c = tid; c < D; c += kMergeThreads) dst[c] = __float2bfloat16_rn(0.f);
-        return;
-    }
-    const int row0 = R / row_tile * row_tile;
-    const Range first = row_range(p, len, row0);
-    const Range last = row_range(p, len, min(row0 + row_tile, rows_total) - 1);
-    const int nc = min(p.n_split, (last.hi - tile_base(p, first.lo) + p.chunk - 1) / p.chunk);
-    const size_t base = (((size_t)b * p.n_kv + kvh) * rows_total + R) * p.n_split;
-    if (tid < 32) {
-        float m[kQ4MaxSplit / 32], l[kQ4MaxSplit / 32], M = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < kQ4MaxSplit / 32; ++i) {
-            const int c = tid + 32 * i;
-            m[i] = c < nc ? p.ml_part[(base + c) * 2] : -INFINITY;
-            l[i] = c < nc ? p.ml_part[(base + c) * 2 + 1] : 0.f;
-            M = fmaxf(M, m[i]);
-        }
-        M = warp_max(M);
-#pragma unroll
-        for (int i = 0; i < kQ4MaxSplit / 32; ++i) {
-            // a chunk without keys of this row has m = -inf and no weight
-            const float w = m[i] == -INFINITY ? 0.f : exp2f(m[i] - M);
-            s_w[tid + 32 * i] = w;
-            sum = fmaf(w, l[i], sum);
-        }
-        sum = warp_sum(sum);
-        if (tid == 0) s_inv = 1.f / sum;
-    }
+    __shared__ float s_w[kQ4MaxShares], s_max[kMergeThreads / 32], s_sum[kMergeThreads / 32];
+    const int rows_total = p.n_tok * p.G, tid = threadIdx.x;
+    const int n_rt = (rows_total + row_tile - 1) / row_tile;
+    const int slices = D / cols, slice = blockIdx.x % slices, R = blockIdx.x / slices;
+    const int kvh = blockIdx.y, b = blockIdx.z, rt = R / row_tile;
+    const int2 info = pp.info[(b * p.n_kv + kvh) * n_rt + rt];
+    if (info.x < 0) return;  // one CTA took the whole unit and wrote its rows
+    // parts: the second one of CTA info.x / 2 if info.x is odd, then the first ones up to CTA info.y
+    const int c0 = info.x >> 1, nc = info.y - c0 + 1;
+    auto part_row = [&](int c) {
+        return ((size_t)(c ? 2 * (c0 + c) : info.x)) * row_tile + (R - rt * row_tile);
+    };
+    const float2* ml = reinterpret_cast<const float2*>(p.ml_part);
+    float M = -INFINITY;
+    for (int c = tid; c < nc; c += kMergeThreads) M = fmaxf(M, ml[part_row(c)].x);
+    M = warp_max(M);
+    if ((tid & 31) == 0) s_max[tid >> 5] = M;
     __syncthreads();
-    const int grp = tid / TPG, c4 = tid - grp * TPG;
+#pragma unroll
+    for (int w = 0; w < kMergeThreads / 32; ++w) M = fmaxf(M, s_max[w]);
+    float l = 0.f;
+    for (int c = tid; c < nc; c += kMergeThreads) {
+        const float2 x = ml[part_row(c)];
+        const float w = exp2f(x.x - M);  // 0 for a part without keys of this row (kNoMax)
+        s_w[c] = w;
+        l = fmaf(w, x.y, l);
+    }
+    l = warp_sum(l);
+    if ((tid & 31) == 0) s_sum[tid >> 5] = l;
+    __syncthreads();
+    const int tpg = cols / 4, n_grp = kMergeThreads / tpg, grp = tid / tpg, c4 = tid - grp * tpg;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int c = grp; c < nc; c += NGRP) {
+    for (int c = grp; c < nc; c += n_grp) {
         const float w = s_w[c];
-        const float4 v = *reinterpret_cast<const float4*>(p.o_part + (base + c) * D + c4 * 4);
-        acc.x = fmaf(w, v.x, acc.x);
-        acc.y = fmaf(w, v.y, acc.y);
-        acc.z = fmaf(w, v.z, acc.z);
-        acc.w = fmaf(w, v.w, acc.w);
+        const float4 x =
+            *reinterpret_cast<const float4*>(p.o_part + part_row(c) * D + slice * cols + c4 * 4);
+        acc.x = fmaf(w, x.x, acc.x);
+        acc.y = fmaf(w, x.y, acc.y);
+        acc.z = fmaf(w, x.z, acc.z);
+        acc.w = fmaf(w, x.w, acc.w);
     }
     s_red[tid] = acc;
     __syncthreads();
     if (grp == 0) {
-#pragma unroll
-        for (int h = 1; h < NGRP; ++h) {
-            const float4 u = s_red[h * TPG + c4];
+        for (int h = 1; h < n_grp; ++h) {
+            const float4 u = s_red[h * tpg + c4];
             acc.x += u.x;
             acc.y += u.y;
             acc.z += u.z;
             acc.w += u.w;
         }
-        const float inv = s_inv;
-        *reinterpret_cast<uint2*>(dst + c4 * 4) =
-            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+        l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kMergeThreads / 32; ++w) l += s_sum[w];
+        const float il = 1.f / l;
+        const int tok = R / p.G;
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) +
+                                  (((size_t)b * p.n_tok + tok) * p.n_q + kvh * p.G + R - tok * p.G) * D +
+                                  slice * cols + c4 * 4) =
+            make_uint2(pack_bf16(acc.x * il, acc.y * il), pack_bf16(acc.z * il, acc.w * il));
     }
 }
 
@@ -614,56 +944,64 @@ bool encode_codes(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64
            CUDA_SUCCESS;
 }
 
-template <int D, int NQ, int MINB>
-cudaError_t launch(const Q4AttnParams& pp, int batch, cudaStream_t st) {
+template <int D, int NQ, bool PAIR>
+cudaError_t launch(const Q4AttnParams& pp, int C, cudaStream_t st) {
     using L = Q4Layout<D>;
     Q4AttnParams p = pp;
-    auto kernel = q4_attn_kernel<D, NQ, MINB>;
+    auto kernel = q4_attn_kernel<D, NQ, PAIR, kQ4CtasPerSm>;
     static std::atomic<bool> configured[64];  // per device; the same value every time
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
     if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_relaxed)) {
         const cudaError_t e = cudaFuncSetAttribute(
-            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_relaxed);
     }
-    constexpr int kOut = (kWarps / L::NG) * 8 * NQ * L::O_STRIDE * 4;  // epilogue's fp32 rows
+    // stages of the ring: as many as leave room for the other CTA of the SM, at least two
+    constexpr int kFixed = 1024 + (kWarps / L::NG - 1) * 8 * NQ * D * 4;
+    constexpr int kStatic = 2 * kT * (PAIR ? 16 : 8 * NQ) * 2 + kWarps * kT * 4 / (kWarps / L::NG) +
+                            D / 16 * 32 * 2 * NQ * 4 + 2048;
     const int stage = (p.r.k_eq_v ? 1 : 2) * L::OP;
-    int s = ((MINB >= 2 ? 100 : 200) * 1024 - 1024) / stage;
+    int s = (112 * 1024 - kFixed - kStatic) / stage;
     s = s < 2 ? 2 : (s > kMaxStages ? kMaxStages : s);
-    // no more stages than the chunk has tiles
-    const int tiles = (p.r.max_seq_len < p.r.chunk ? p.r.max_seq_len : p.r.chunk) / kT + 2;
-    if (s > tiles) s = tiles < 2 ? 2 : tiles;
     p.r.n_stages = s;
-    const size_t smem = 1024 + (s * stage > kOut ? (size_t)s * stage : (size_t)kOut);
+    const size_t smem = (size_t)kFixed + (size_t)s * stage;
     const uint64_t slots = p.r.page_size ? p.r.page_size : p.r.cap;
-    const uint64_t rows = (uint64_t)(p.r.page_size ? p.r.n_pages : batch) * p.r.n_kv;
+    const uint64_t rows = (uint64_t)(p.r.page_size ? p.r.n_pages : p.batch) * p.r.n_kv;
     CUtensorMap km, vm;
     if (!encode_codes(&km, p.r.k, L::ROWB, slots, rows) ||
         !encode_codes(&vm, p.r.v, L::ROWB, slots, rows))
         return cudaErrorInvalidValue;
-    const int rt = 8 * NQ, total = p.r.n_tok * p.r.G;
-    const dim3 grid((unsigned)((total + rt - 1) / rt * p.r.n_split), p.r.n_kv, batch);
-    cudaError_t e = launch_pdl(kernel, grid, dim3(kThreads), smem, st, km, vm, p);
-    if (e == cudaSuccess && p.r.n_split > 1)
-        e = launch_pdl(q4_merge_kernel<D>, dim3((unsigned)total, p.r.n_kv, batch),
-                       dim3(kMergeThreads), 0, st, p.r, rt);
+    cudaError_t e = launch_pdl(kernel, dim3((unsigned)C), dim3(kThreads), smem, st, km, vm, p);
+    if (e == cudaSuccess && p.balanced) {
+        const int rows = p.r.n_tok * p.r.G;
+        const int cols = (long long)rows * p.r.n_kv * p.batch >= 512 ? D : 64;
+        e = launch_pdl(q4_merge_kernel, dim3((unsigned)(rows * (D / cols)), p.r.n_kv, p.batch),
+                       dim3(kMergeThreads), 0, st, p, D, cols, 8 * NQ);
+    }
     return e;
+}
+
+template <int D>
+cudaError_t launch_d(const Q4AttnParams& p, int C, cudaStream_t st) {
+    const int rows = p.r.n_tok * p.r.G;
+    if (rows > 8) return launch<D, 2, false>(p, C, st);
+    if (rows > 4) return launch<D, 1, false>(p, C, st);
+    return launch<D, 1, true>(p, C, st);
 }
 
 }  // namespace
 
-cudaError_t launch_q4_attn(const RowsParams& r, const Q4Cache& c, int head_dim, int batch,
-                           cudaStream_t st) {
-    const Q4AttnParams p{r, c.k_scales, c.v_codes ? c.v_scales : c.k_scales};
-    const bool wide = q4_row_tile(r.n_tok * r.G) == 16;
-    // two CTAs per SM where the query fragments leave registers for them
+cudaError_t launch_q4_attn(const RowsParams& r, const Q4Cache& c, int head_dim, int batch, int C,
+                           int balanced, void* info, cudaStream_t st) {
+    const Q4AttnParams p{r, c.k_scales, c.v_codes ? c.v_scales : c.k_scales, batch, balanced,
+                         static_cast<int2*>(info)};
     switch (head_dim) {
-        case 64: return wide ? launch<64, 2, 2>(p, batch, st) : launch<64, 1, 2>(p, batch, st);
-        case 128: return wide ? launch<128, 2, 2>(p, batch, st) : launch<128, 1, 2>(p, batch, st);
-        case 256: return wide ? launch<256, 2, 1>(p, batch, st) : launch<256, 1, 2>(p, batch, st);
-        case 512: return wide ? launch<512, 2, 1>(p, batch, st) : launch<512, 1, 1>(p, batch, st);
+        case 64: return launch_d<64>(p, C, st);
+        case 128: return launch_d<128>(p, C, st);
+        case 256: return launch_d<256>(p, C, st);
+        case 512: return launch_d<512>(p, C, st);
     }
     return cudaErrorInvalidValue;
 }
