@@ -686,7 +686,7 @@ Q4Plan q4_plan(int batch, int kind, int window, int n_q, int n_kv, int head_dim,
     // (the balanced launch counts its tiles in 32 bits per KV head and row tile)
     if (tiles <= 1 || units >= 16 * slots || batch > 4096 || batch * tiles > (1ll << 30)) return pl;
     pl.balanced = 1;
-    long long c = units * tiles < slots ? units * tiles : slots;
+    long long c = units * (tiles + 1) < slots ? units * (tiles + 1) : slots;
     if (c > gemma::kQ4MaxShares) c = gemma::kQ4MaxShares;
     pl.ctas = (int)c;
     const size_t parts = (size_t)c * 2 * tile;

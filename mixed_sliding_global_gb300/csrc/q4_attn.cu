@@ -36,8 +36,8 @@ namespace gemma {
 namespace {
 
 constexpr int kT = kQ4KeyTile;      // keys per tile
-constexpr int kWarps = 8;           // consumer warps per CTA, and a producer
-constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kWarps = 8;           // consumer warps per CTA
+constexpr int kThreads = (kWarps + 2) * 32;  // and two that load and prepare for them
 constexpr int kMaxStages = 8;
 constexpr float kLazyLog2 = 8.f;
 constexpr float kNoMax = -3.0e38f;  // reference before any key (finite: x - kNoMax is no NaN)
@@ -136,14 +136,12 @@ __device__ __forceinline__ int unit_tiles(const RowsParams& p, int len) {
     return bad_length(p, len) ? 1 : (len - first_key(p, len) + kT - 1) / kT;
 }
 
-// The work of a launch is one line of key tiles: sequences in order, a sequence's units in order, a
-// unit's tiles in order. CTA c of C takes tiles [c total / C, (c + 1) total / C), so every CTA
-// streams the same number of keys whatever the lengths; it meets whole units and at most two
-// parts of units, which the merge launch puts together. CTAs beyond the number of tiles have no
-// share. Where a tile x lies:
-__device__ __forceinline__ int shares(long long total, int ctas) {
-    return total < ctas ? (int)total : ctas;
-}
+// The work of a launch is one line of places: sequences in order, a sequence's units in order, a
+// unit's tiles in order behind kHead empty places (a part's set-up and its rows cost about that
+// many tiles). CTA c of C takes places [c total / C, (c + 1) total / C), so every CTA has about
+// the same work whatever the lengths; it meets whole units and at most two parts of units, which
+// the merge launch puts together. Where a place x lies:
+constexpr int kHead = 1;
 __device__ __forceinline__ long long share_start(long long total, int C, int c) {
     return total * c / C;
 }
@@ -178,19 +176,21 @@ struct Part {
     int b, kvh, rt, t0, t1, n, len;
 };
 struct Walk {
-    int b, u, t, n, len;  // next tile: t of unit u (of the sequence's upb) of sequence b
+    int b, u, t, n, len;  // next place: tile t (before 0: the head) of unit u of sequence b
     __device__ void enter(const RowsParams& p, int seq) {
         b = seq;
         len = p.seq_lens[seq];
         n = unit_tiles(p, len);
     }
-    // Take up to `left` tiles of the current unit and step on.
-    __device__ Part take(const RowsParams& p, int n_rt, int upb, int batch, int left) {
-        Part s{b, u / n_rt, u % n_rt, t, n, n, len};
-        if (s.t1 - t > left) s.t1 = t + left;
-        t = s.t1;
+    // The part of the current unit within the next `left` places (possibly without tiles), and
+    // step on; left becomes what is left behind it.
+    __device__ Part take(const RowsParams& p, int n_rt, int upb, int batch, int& left) {
+        const int to = n - t < left ? n : t + left;
+        left -= to - t;
+        const Part s{b, u / n_rt, u % n_rt, max(t, 0), to, n, len};
+        t = to;
         if (t == n) {
-            t = 0;
+            t = -kHead;
             if (++u == upb) {
                 u = 0;
                 if (b + 1 < batch) enter(p, b + 1);
@@ -204,6 +204,7 @@ struct Walk {
 // registers of every thread through the tile loop).
 struct Job {
     Part part;
+    int last;  // no part: the share ends
     int row0, n_rows, key_first, whole, slot;
     int lo_all, ke;      // keys of any row
     int lo_max, hi_min;  // keys that every row of the tile may see
@@ -224,6 +225,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
     constexpr int KW = kT / KSP;            // keys per warp of a tile in P V
     constexpr bool QREG = NQ * D <= 256;    // query fragments in registers (else shared memory)
     constexpr int PW = PAIR ? 16 : 8 * NQ;  // halves of P per key
+    constexpr bool QPRE = NQ == 1;          // the producer prepares the next part's query rows
     const RowsParams& p = pp.r;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -231,12 +233,13 @@ __global__ void __launch_bounds__(kThreads, MINB)
     __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages];
     __shared__ __align__(16) __half sP[2][kT * PW];
     __shared__ __align__(16) __half sV[kWarps][PAIR ? 2 * KW : KW];
-    __shared__ __align__(16) uint32_t sQ[D / 16][32][2 * NQ];
-    __shared__ float sMax[kWarps][RT], sSum[kWarps][RT], sFac[RT];
+    __shared__ __align__(16) uint32_t sQ[QPRE ? 2 : 1][D / 16][32][2 * NQ];
+    __shared__ float sMax[kWarps][RT], sSum[kWarps][RT];
+    __shared__ __align__(8) float sInv[2][RT];
     __shared__ int sScan[kThreads / 32], sAt[3];
-    __shared__ Job sJob;
-    __shared__ Walk sWalk;
-    __shared__ long long sAll[3];  // tiles of the launch, CTAs with a share, first tile of this one
+    // the part being worked on and the one that the producer prepares
+    __shared__ Job sJob[2];
+    __shared__ __align__(8) uint64_t job_full[2], job_empty[2];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, tq = lane & 3;
@@ -253,38 +256,39 @@ __global__ void __launch_bounds__(kThreads, MINB)
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], kWarps);
         }
+        for (int j = 0; j < 2; ++j) {
+            mbar_init(&job_full[j], 1);
+            mbar_init(&job_empty[j], kWarps);
+        }
         fence_barrier_init();
     }
     pdl_wait();
     // where this CTA's share starts
     Walk walk;
-    int left;  // tiles of this CTA
+    int left;                   // places of this CTA
+    long long all = 0, x0 = 0;  // places of the launch, first one of this CTA
+    int C = 0;                  // CTAs with a share (no more than places)
     if (pp.balanced) {
         const int per = (batch + kThreads - 1) / kThreads, b0 = min((int)threadIdx.x * per, batch);
         const int b1 = min(b0 + per, batch);
         int mine = 0, total;
-        for (int b = b0; b < b1; ++b) mine += unit_tiles(p, p.seq_lens[b]);
+        for (int b = b0; b < b1; ++b) mine += unit_tiles(p, p.seq_lens[b]) + kHead;
         const int before = cta_scan(mine, sScan, total);
-        const long long all = (long long)total * upb;
-        const int C = shares(all, gridDim.x);
+        all = (long long)total * upb;
+        C = all < gridDim.x ? (int)all : (int)gridDim.x;
         if ((int)blockIdx.x >= C) return;
-        const long long x0 = share_start(all, C, blockIdx.x);
-        if (threadIdx.x == 0) {
-            sAll[0] = all;
-            sAll[1] = C;
-            sAll[2] = x0;
-        }
+        x0 = share_start(all, C, blockIdx.x);
         left = (int)(share_start(all, C, blockIdx.x + 1) - x0);
         if (x0 >= (long long)before * upb && x0 < (long long)(before + mine) * upb) {
             long long x = x0 - (long long)before * upb;
-            int b = b0, n = unit_tiles(p, p.seq_lens[b]);
+            int b = b0, n = unit_tiles(p, p.seq_lens[b]) + kHead;
             while (x >= (long long)n * upb) {
                 x -= (long long)n * upb;
-                n = unit_tiles(p, p.seq_lens[++b]);
+                n = unit_tiles(p, p.seq_lens[++b]) + kHead;
             }
             sAt[0] = b;
             sAt[1] = (int)(x / n);
-            sAt[2] = (int)(x % n);
+            sAt[2] = (int)(x % n) - kHead;
         }
         __syncthreads();
         walk.enter(p, sAt[0]);
@@ -293,19 +297,67 @@ __global__ void __launch_bounds__(kThreads, MINB)
     } else {  // one CTA per unit
         walk.enter(p, blockIdx.x / upb);
         walk.u = blockIdx.x % upb;
-        walk.t = 0;
-        left = walk.n;
+        walk.t = -kHead;
+        left = walk.n + kHead;
         __syncthreads();
     }
 
+    // Element offset in q and out of row r of a part's tile: token (row0 + r) / G, head
+    // kvh * G + (row0 + r) % G.
+    auto row_at = [&](const Job& j, int r) {
+        const int R = j.row0 + r, tok = R / p.G;
+        return (((size_t)j.part.b * p.n_tok + tok) * p.n_q + j.part.kvh * p.G + (R - tok * p.G)) *
+               (size_t)D;
+    };
+    // One warp turns query row r of a part into fp16 fragments: lane (g, tq) will hold, of row g of
+    // each 8-row tile, elements 16 tq .. 16 tq + 15 of every group, the ones whose codes it reads.
+    // The row is scaled by a power of two that brings its largest element into [2^13, 2^14)
+    // (exact unless an element is below 2^-37 of that).
+    auto prepare_row = [&](const Job& j, int slot, int r) {
+        constexpr int CH = (D / 8 + 31) / 32;
+        uint4 raw[CH];
+        uint32_t mx = 0;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int ch = c * 32 + lane;
+            raw[c] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < j.n_rows && ch < D / 8)
+                raw[c] = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
+                                                        row_at(j, r))[ch];
+            const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx = max(mx, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
+        }
+        mx = __reduce_max_sync(0xffffffffu, mx);
+        // biased exponent of the largest element -> factor 2^(13 - (exponent - 127))
+        const float f =
+            __uint_as_float((uint32_t)(267 - min(max((int)(mx >> 7), 13), 254)) << 23);
+        // a score is the sum of products times 2^24 (the codes') times this
+        if (lane == 0) sInv[slot][r] = (p.softcap > 0.f ? p.cap_inner : p.scale_log2) / f;
+#pragma unroll
+        for (int c = 0; c < CH; ++c) {
+            const int ch = c * 32 + lane;  // elements 8 ch .. 8 ch + 7
+            if (ch >= D / 8) continue;
+            const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
+            uint32_t h[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                h[k] = pack_f16(__uint_as_float(w[k] << 16) * f,
+                                __uint_as_float(w[k] & 0xffff0000u) * f);
+            const int ks = (ch >> 3) * 4 + 2 * (ch & 1), ln = (r & 7) * 4 + ((ch >> 1) & 3);
+            auto& q = sQ[QPRE ? slot : 0];
+            *reinterpret_cast<uint2*>(&q[ks][ln][(r >> 3) * 2]) = make_uint2(h[0], h[1]);
+            *reinterpret_cast<uint2*>(&q[ks + 1][ln][(r >> 3) * 2]) = make_uint2(h[2], h[3]);
+        }
+    };
+
     if (warp == kWarps) {
-        // producer: the share's tiles in order, one thread
+        // the share's tiles in order, one thread issuing the copies
         if (lane == 0) {
             const int slots = kv_row_slots(p);
             int s = 0, round = 0;  // stage, and how often the ring went round
             while (left > 0) {
                 const Part part = walk.take(p, n_rt, upb, batch, left);
-                left -= part.t1 - part.t0;
                 const bool bad = bad_length(p, part.len);
                 const int key_first = first_key(p, part.len);
                 for (int t = part.t0; t < part.t1; ++t) {
@@ -316,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
                         s = 0;
                         ++round;
                     }
-                    if (bad) {  // no keys: the consumers only count the stage
+                    if (bad) {  // no keys: the consumers skip the stage
                         mbar_arrive(bar);
                         continue;
                     }
@@ -351,6 +403,57 @@ __global__ void __launch_bounds__(kThreads, MINB)
         }
         return;
     }
+    if (warp == kWarps + 1) {
+        // The share's parts: their descriptions and, for up to eight rows, their query fragments,
+        // one part ahead of the consumers.
+        int n_job = 0;
+        for (long long x = x0; left > 0;) {
+            const int js = n_job & 1, before = left;
+            Job j;
+            j.part = walk.take(p, n_rt, upb, batch, left);
+            const Part& part = j.part;
+            const long long first = x + (before - left) - part.t1;  // place of the unit's tile 0
+            x += before - left;
+            if (part.t1 <= part.t0) continue;  // a head only
+            j.last = 0;
+            j.row0 = part.rt * RT;
+            j.n_rows = min(RT, rows_total - j.row0);
+            j.whole = part.t0 == 0 && part.t1 == part.n;
+            j.slot = 2 * (int)blockIdx.x + (n_job > 0);
+            j.key_first = first_key(p, part.len);
+            j.lo_all = p.is_sliding ? max(0, part.len - p.n_tok - p.window + 1) : 0;
+            j.ke = min(part.len, j.key_first + part.t1 * kT);
+            const int pos0 = part.len - p.n_tok + j.row0 / p.G;
+            const int pos1 = part.len - p.n_tok + (j.row0 + j.n_rows - 1) / p.G;
+            j.lo_max = p.is_sliding ? max(0, pos1 - p.window + 1) : 0;
+            j.hi_min = min(pos0 + 1, j.ke);
+            if (n_job >= 2 && !mbar_wait(&job_empty[js], (n_job / 2 - 1) & 1, p.err)) return;
+            if (lane == 0) {
+                sJob[js] = j;
+                if (pp.balanced && part.t0 == 0)  // who shares the unit, for the merge
+                    pp.info[(part.b * p.n_kv + part.kvh) * n_rt + part.rt] =
+                        j.whole ? make_int2(-1, -1)
+                                : make_int2(j.slot, share_of(all, C, first + part.n - 1));
+            }
+            // (the consumers prepare the first part's rows themselves, one warp each)
+            if (QPRE && n_job > 0 && !bad_length(p, part.len)) {
+#pragma unroll (PAIR ? 4 : 2)
+                for (int r = 0; r < RT; ++r)
+                    if (r < j.n_rows || n_job == 1) prepare_row(j, js, r);  // (the rest stay zero)
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&job_full[js]);
+            ++n_job;
+        }
+        // the end of the share
+        const int js = n_job & 1;
+        if (n_job >= 2 && !mbar_wait(&job_empty[js], (n_job / 2 - 1) & 1, p.err)) return;
+        if (lane == 0) {
+            sJob[js].last = 1;
+            mbar_arrive(&job_full[js]);
+        }
+        return;
+    }
 
     const int wg = warp % NG, ksp = warp / NG;
     const int krow = warp * 16 + key_of_row<D>(g);  // this lane's keys of S: krow, krow + 8
@@ -377,113 +480,46 @@ __global__ void __launch_bounds__(kThreads, MINB)
         }
     };
     bool ok = true;
-    if (threadIdx.x == 0) {
-        sWalk = walk;
-        sJob.slot = 0;
-    }
-    while (done < left) {
-        if (threadIdx.x == 0) {
-            Job j;
-            j.part = sWalk.take(p, n_rt, upb, batch, left - done);
-            const Part& part = j.part;
-            j.row0 = part.rt * RT;
-            j.n_rows = min(RT, rows_total - j.row0);
-            j.whole = part.t0 == 0 && part.t1 == part.n;
-            j.slot = 2 * (int)blockIdx.x + (done > 0);
-            j.key_first = first_key(p, part.len);
-            j.lo_all = p.is_sliding ? max(0, part.len - p.n_tok - p.window + 1) : 0;
-            j.ke = min(part.len, j.key_first + part.t1 * kT);
-            const int pos0 = part.len - p.n_tok + j.row0 / p.G;
-            const int pos1 = part.len - p.n_tok + (j.row0 + j.n_rows - 1) / p.G;
-            j.lo_max = p.is_sliding ? max(0, pos1 - p.window + 1) : 0;
-            j.hi_min = min(pos0 + 1, j.ke);
-            if (pp.balanced && part.t0 == 0) {
-                // this CTA has the unit's first tile: tell the merge launch who shares it
-                const int c1 = share_of(sAll[0], (int)sAll[1], sAll[2] + done + part.n - 1);
-                pp.info[(part.b * p.n_kv + part.kvh) * n_rt + part.rt] =
-                    j.whole ? make_int2(-1, -1) : make_int2(j.slot, c1);
-            }
-            sJob = j;
-        }
-        consumer_sync();
-        // row r of the tile: token (row0 + r) / G, head kvh * G + (row0 + r) % G
-        auto row_at = [&](int r) {
-            const int R = sJob.row0 + r, tok = R / p.G;
-            return (((size_t)sJob.part.b * p.n_tok + tok) * p.n_q + sJob.part.kvh * p.G +
-                    (R - tok * p.G)) * (size_t)D;
-        };
-        if (bad_length(p, sJob.part.len)) {
+    for (int n_job = 0;; ++n_job) {
+        const int js = n_job & 1;
+        // (the vote lets every warp leave together if one gave up waiting)
+        if (consumer_vote(!mbar_wait(&job_full[js], (n_job >> 1) & 1, p.err))) return;
+        const Job& job = sJob[js];
+        if (job.last) return;
+        if (bad_length(p, job.part.len)) {
             if (threadIdx.x == 0) report(p.err, GEMMA_DEVERR_SEQ_LEN);
-            for (int i = threadIdx.x; i < sJob.n_rows * (D / 8); i += kWarps * 32)
+            for (int i = threadIdx.x; i < job.n_rows * (D / 8); i += kWarps * 32)
                 *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) +
-                                          row_at(i / (D / 8)) + i % (D / 8) * 8) =
+                                          row_at(job, i / (D / 8)) + i % (D / 8) * 8) =
                     make_uint4(0u, 0u, 0u, 0u);
-            if (lane == 0) mbar_arrive(&empty[s]);
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&empty[s]);
+                mbar_arrive(&job_empty[js]);
+            }
             next_stage();
-            consumer_sync();  // sJob is rewritten
             continue;
         }
-
-        // Query rows as fp16 fragments: lane (g, tq) holds, of row g of each 8-row tile, elements
-        // 16 tq .. 16 tq + 15 of every group, the ones whose codes it reads. A row is scaled by
-        // a power of two that brings its largest element into [2^13, 2^14) (exact unless an
-        // element is below 2^-37 of that).
-        for (int r = warp; r < RT; r += kWarps) {
-            constexpr int CH = (D / 8 + 31) / 32;
-            uint4 raw[CH];
-            uint32_t mx = 0;
-            const __nv_bfloat16* src =
-                static_cast<const __nv_bfloat16*>(p.q) + row_at(min(r, sJob.n_rows - 1));
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const int ch = c * 32 + lane;
-                raw[c] = make_uint4(0u, 0u, 0u, 0u);
-                if (r < sJob.n_rows && ch < D / 8) raw[c] = reinterpret_cast<const uint4*>(src)[ch];
-                const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mx = max(mx, max(w[k] & 0x7fffu, (w[k] >> 16) & 0x7fffu));
-            }
-            mx = __reduce_max_sync(0xffffffffu, mx);
-            // biased exponent of the largest element -> factor 2^(13 - (exponent - 127))
-            const float f = __uint_as_float(
-                (uint32_t)(267 - min(max((int)(mx >> 7), 13), 254)) << 23);
-            if (lane == 0) sFac[r] = f;
-#pragma unroll
-            for (int c = 0; c < CH; ++c) {
-                const int ch = c * 32 + lane;  // elements 8 ch .. 8 ch + 7
-                if (ch >= D / 8) continue;
-                const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
-                uint32_t h[4];
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    h[k] = pack_f16(__uint_as_float(w[k] << 16) * f,
-                                    __uint_as_float(w[k] & 0xffff0000u) * f);
-                const int ks = (ch >> 3) * 4 + 2 * (ch & 1), ln = (r & 7) * 4 + ((ch >> 1) & 3);
-                *reinterpret_cast<uint2*>(&sQ[ks][ln][(r >> 3) * 2]) = make_uint2(h[0], h[1]);
-                *reinterpret_cast<uint2*>(&sQ[ks + 1][ln][(r >> 3) * 2]) = make_uint2(h[2], h[3]);
-            }
+        if (!QPRE || n_job == 0) {
+            for (int r = warp; r < RT; r += kWarps) prepare_row(job, js, r);
+            consumer_sync();
         }
-        consumer_sync();
         uint32_t qf[QREG ? D / 16 : 1][NQ][2];
         if (QREG) {
 #pragma unroll
             for (int k = 0; k < D / 16; ++k)
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
-                    qf[QREG ? k : 0][n][0] = sQ[k][lane][2 * n];
-                    qf[QREG ? k : 0][n][1] = sQ[k][lane][2 * n + 1];
+                    qf[QREG ? k : 0][n][0] = sQ[QPRE ? js : 0][k][lane][2 * n];
+                    qf[QREG ? k : 0][n][1] = sQ[QPRE ? js : 0][k][lane][2 * n + 1];
                 }
         }
         // the rows whose scores this lane holds: 8 n + 2 tq + c
-        float inv[NQ][2], m_run[NQ][2], l_run[NQ][2];
-        const float fac = p.softcap > 0.f ? p.cap_inner : p.scale_log2;
+        float m_run[NQ][2], l_run[NQ][2];
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const int r = n * 8 + 2 * tq + c;
-                inv[n][c] = fac / sFac[r];
                 m_run[n][c] = kNoMax;
                 l_run[n][c] = 0.f;
             }
@@ -494,11 +530,11 @@ __global__ void __launch_bounds__(kThreads, MINB)
             for (int n = 0; n < NQ; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
         int v_exp = 6;  // biased exponent that V's scales are relative to
 
-        for (int t = sJob.part.t0, t1 = sJob.part.t1; t < t1; ++t) {
+        for (int t = job.part.t0, t1 = job.part.t1; t < t1; ++t) {
             if (ok) ok = mbar_wait(&full[s], phase, p.err);
             const uint8_t* tK = smem + s * stage_bytes;
             const uint8_t* tV = tK + (nops - 1) * L::OP;
-            const int key0 = sJob.key_first + t * kT;
+            const int key0 = job.key_first + t * kT;
 
             // (1) S of 16 keys
             float sv[NQ][4];
@@ -542,10 +578,10 @@ __global__ void __launch_bounds__(kThreads, MINB)
                             }
                         } else if (NQ == 2) {
                             *reinterpret_cast<uint4*>(bq) =
-                                *reinterpret_cast<const uint4*>(sQ[i * 4 + ks][lane]);
+                                *reinterpret_cast<const uint4*>(sQ[QPRE ? js : 0][i * 4 + ks][lane]);
                         } else {
                             *reinterpret_cast<uint2*>(bq) =
-                                *reinterpret_cast<const uint2*>(sQ[i * 4 + ks][lane]);
+                                *reinterpret_cast<const uint2*>(sQ[QPRE ? js : 0][i * 4 + ks][lane]);
                         }
 #pragma unroll
                         for (int n = 0; n < NQ; ++n) {
@@ -565,28 +601,29 @@ __global__ void __launch_bounds__(kThreads, MINB)
                 }
             }
             // scores in log2 units; masked keys -inf (a tile inside every row's range has none)
-            const bool edge = key0 < sJob.lo_max || key0 + kT > sJob.hi_min;
+            const bool edge = key0 < job.lo_max || key0 + kT > job.hi_min;
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) {
+                const float2 inv = *reinterpret_cast<const float2*>(&sInv[js][n * 8 + 2 * tq]);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    sv[n][k] = sv[n][k] * 16777216.f * (k & 1 ? inv.y : inv.x);
+            }
             if (p.softcap > 0.f) {
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        sv[n][k] = p.cap_log2 * tanhf(sv[n][k] * 16777216.f * inv[n][k & 1]);
-            } else {
-#pragma unroll
-                for (int n = 0; n < NQ; ++n)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) sv[n][k] = sv[n][k] * 16777216.f * inv[n][k & 1];
+                    for (int k = 0; k < 4; ++k) sv[n][k] = p.cap_log2 * tanhf(sv[n][k]);
             }
             if (edge) {
 #pragma unroll
                 for (int n = 0; n < NQ; ++n)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const int r = min(n * 8 + 2 * tq + c, sJob.n_rows - 1);
-                        const int pos = sJob.part.len - p.n_tok + (sJob.row0 + r) / p.G;
+                        const int r = min(n * 8 + 2 * tq + c, job.n_rows - 1);
+                        const int pos = job.part.len - p.n_tok + (job.row0 + r) / p.G;
                         const int lo = p.is_sliding ? pos - p.window + 1 : 0;
-                        const int hi = min(pos + 1, sJob.ke);
+                        const int hi = min(pos + 1, job.ke);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const int key = key0 + krow + 8 * h;
@@ -601,26 +638,29 @@ __global__ void __launch_bounds__(kThreads, MINB)
                 for (int c = 0; c < 2; ++c)
                     grow = grow || fmaxf(sv[n][c], sv[n][c + 2]) > m_run[n][c] + kLazyLog2;
             __half* P = sP[done & 1];
-            float pr[NQ][4];
+            float l_tile[NQ][2];
             auto exponentiate = [&]() {
 #pragma unroll
                 for (int n = 0; n < NQ; ++n) {
+                    float pr[4];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) pr[n][k] = fast_exp2(sv[n][k] - m_run[n][k & 1]);
+                    for (int k = 0; k < 4; ++k) pr[k] = fast_exp2(sv[n][k] - m_run[n][k & 1]);
+                    l_tile[n][0] = pr[0] + pr[2];
+                    l_tile[n][1] = pr[1] + pr[3];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int key = krow + 8 * h;
                         if (PAIR) {  // [key][8] words: columns q (P, 0), 4 + q (0, P)
                             if (tq < 2) {
                                 uint32_t* d = reinterpret_cast<uint32_t*>(P) + key * 8 + 2 * tq;
-                                const uint32_t e = pack_f16(pr[n][2 * h], 0.f);
-                                const uint32_t f = pack_f16(pr[n][2 * h + 1], 0.f);
+                                const uint32_t e = pack_f16(pr[2 * h], 0.f);
+                                const uint32_t f = pack_f16(pr[2 * h + 1], 0.f);
                                 *reinterpret_cast<uint2*>(d) = make_uint2(e, f);
                                 *reinterpret_cast<uint2*>(d + 4) = make_uint2(e << 16, f << 16);
                             }
                         } else {     // planes of 8 rows
                             *reinterpret_cast<uint32_t*>(P + (n * kT + key) * 8 + 2 * tq) =
-                                pack_f16(pr[n][2 * h], pr[n][2 * h + 1]);
+                                pack_f16(pr[2 * h], pr[2 * h + 1]);
                         }
                     }
                 }
@@ -634,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
                 for (int i = 0; i < (KW + 31) / 32; ++i) {
                     const int k = i * 32 + lane, key = key0 + ksp * KW + k;
                     sb[i] = k < KW ? vs[i * 32 * NG] : 0;
-                    if (edge && (key < sJob.lo_all || key >= sJob.ke)) sb[i] = 0;  // may hold anything
+                    if (edge && (key < job.lo_all || key >= job.ke)) sb[i] = 0;  // may hold anything
                     mx = max(mx, sb[i]);
                 }
                 // (a NaN scale, exponent 255, leaves NaN in its column group either way)
@@ -702,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
 #pragma unroll
             for (int n = 0; n < NQ; ++n)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) l_run[n][c] += pr[n][c] + pr[n][c + 2];
+                for (int c = 0; c < 2; ++c) l_run[n][c] += l_tile[n][c];
 
             // (2) O of 64 columns over this warp's keys
             if constexpr (PAIR) {
@@ -823,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int r = n * 8 + 2 * tq + c, x = wg * 64 + g * 8;
-                    if (r >= sJob.n_rows) continue;
+                    if (r >= job.n_rows) continue;
 #pragma unroll
                     for (int h = 1; h < KSP; ++h)
 #pragma unroll
@@ -833,13 +873,13 @@ __global__ void __launch_bounds__(kThreads, MINB)
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) l += sSum[w][r];
                     const float* y = v[n][c];
-                    if (sJob.whole) {
+                    if (job.whole) {
                         const float il = 1.f / l;
-                        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row_at(r) + x) =
+                        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row_at(job, r) + x) =
                             make_uint4(pack_bf16(y[0] * il, y[1] * il), pack_bf16(y[2] * il, y[3] * il),
                                        pack_bf16(y[4] * il, y[5] * il), pack_bf16(y[6] * il, y[7] * il));
                     } else {
-                        const size_t pr = (size_t)sJob.slot * RT + r;
+                        const size_t pr = (size_t)job.slot * RT + r;
                         float4* d = reinterpret_cast<float4*>(p.o_part + pr * D + x);
                         d[0] = make_float4(y[0], y[1], y[2], y[3]);
                         d[1] = make_float4(y[4], y[5], y[6], y[7]);
@@ -848,7 +888,9 @@ __global__ void __launch_bounds__(kThreads, MINB)
                     }
                 }
         }
-        consumer_sync();  // sJob, sSum, sO and sQ are rewritten for the next part
+        // sSum and sO are rewritten only behind another part's votes; the job's slot is free
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&job_empty[js]);
     }
 }
 
