@@ -78,6 +78,41 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+// Loads from shared memory at 32-bit addresses (generic pointers would cost the tile loop a pair of
+// registers each, and this kernel has none to spare).
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t v, uint32_t w) {
+    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(a), "r"(v), "r"(w) : "memory");
+}
+__device__ __forceinline__ void sts16(uint32_t a, uint32_t v) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"((uint16_t)v) : "memory");
+}
+
 // Slot j of a word: its pair of codes as two fp16 numbers code * 2^-24.
 __device__ __forceinline__ uint32_t code_pair(uint32_t word, int j) {
     return __funnelshift_r(word, word, 4 * j) & kPairMask;
@@ -223,7 +258,8 @@ __global__ void __launch_bounds__(kThreads, MINB)
     constexpr int NG = L::NG;
     constexpr int KSP = kWarps / NG;        // warps that share a column group
     constexpr int KW = kT / KSP;            // keys per warp of a tile in P V
-    constexpr bool QREG = NQ * D <= 256;    // query fragments in registers (else shared memory)
+    // query fragments in registers where they leave room for the rest (else in shared memory)
+    constexpr bool QREG = NQ == 1 ? D <= 256 : D <= 64;
     constexpr int PW = PAIR ? 16 : 8 * NQ;  // halves of P per key
     constexpr bool QPRE = NQ == 1;          // the producer prepares the next part's query rows
     const RowsParams& p = pp.r;
@@ -456,6 +492,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
     }
 
     const int wg = warp % NG, ksp = warp / NG;
+    const uint32_t smem0 = smem_u32(smem), aV = smem_u32(sV[warp]);
     const int krow = warp * 16 + key_of_row<D>(g);  // this lane's keys of S: krow, krow + 8
     // byte offsets in a tile of the words this lane reads: for S, key krow (krow + 8 lies 8 rows
     // on), group i at sOff[i % 4] in box i / 4; for P V, an even and an odd key of its group's words
@@ -530,10 +567,11 @@ __global__ void __launch_bounds__(kThreads, MINB)
             for (int n = 0; n < NQ; ++n) o[i][n][0] = o[i][n][1] = o[i][n][2] = o[i][n][3] = 0.f;
         int v_exp = 6;  // biased exponent that V's scales are relative to
 
+        const uint32_t tQ = smem_u32(sQ[QPRE ? js : 0][0][lane]);
         for (int t = job.part.t0, t1 = job.part.t1; t < t1; ++t) {
             if (ok) ok = mbar_wait(&full[s], phase, p.err);
-            const uint8_t* tK = smem + s * stage_bytes;
-            const uint8_t* tV = tK + (nops - 1) * L::OP;
+            const uint32_t tK = smem0 + s * stage_bytes;
+            const uint32_t tV = tK + (nops - 1) * L::OP;
             const int key0 = job.key_first + t * kT;
 
             // (1) S of 16 keys
@@ -541,27 +579,26 @@ __global__ void __launch_bounds__(kThreads, MINB)
 #pragma unroll
             for (int n = 0; n < NQ; ++n) sv[n][0] = sv[n][1] = sv[n][2] = sv[n][3] = 0.f;
             {
-                const uint8_t* sk = tK + L::CODES;
-                uint32_t ska[(NG + 1) / 2], skb[(NG + 1) / 2];  // scales of the two keys, bf16 pairs
+                alignas(16) uint32_t ska[(NG + 1) / 2], skb[(NG + 1) / 2];  // scales of the two keys, bf16 pairs
+                const uint32_t sk = tK + L::CODES + krow * (NG * 2);
                 if (NG == 8) {
-                    *reinterpret_cast<uint4*>(ska) = reinterpret_cast<const uint4*>(sk)[krow];
-                    *reinterpret_cast<uint4*>(skb) = reinterpret_cast<const uint4*>(sk)[krow + 8];
+                    const uint4 a = lds128(sk), b = lds128(sk + 8 * NG * 2);
+                    *reinterpret_cast<uint4*>(ska) = a;
+                    *reinterpret_cast<uint4*>(skb) = b;
                 } else if (NG == 4) {
-                    *reinterpret_cast<uint2*>(ska) = reinterpret_cast<const uint2*>(sk)[krow];
-                    *reinterpret_cast<uint2*>(skb) = reinterpret_cast<const uint2*>(sk)[krow + 8];
+                    const uint2 a = lds64(sk), b = lds64(sk + 8 * NG * 2);
+                    *reinterpret_cast<uint2*>(ska) = a;
+                    *reinterpret_cast<uint2*>(skb) = b;
                 } else if (NG == 2) {
-                    ska[0] = reinterpret_cast<const uint32_t*>(sk)[krow];
-                    skb[0] = reinterpret_cast<const uint32_t*>(sk)[krow + 8];
+                    ska[0] = lds32(sk);
+                    skb[0] = lds32(sk + 8 * NG * 2);
                 } else {
-                    ska[0] = reinterpret_cast<const uint16_t*>(sk)[krow];
-                    skb[0] = reinterpret_cast<const uint16_t*>(sk)[krow + 8];
+                    ska[0] = lds16(sk);
+                    skb[0] = lds16(sk + 8 * NG * 2);
                 }
 #pragma unroll
                 for (int i = 0; i < NG; ++i) {
-                    const uint2 wa =
-                        *reinterpret_cast<const uint2*>(tK + s_off(i));
-                    const uint2 wb =
-                        *reinterpret_cast<const uint2*>(tK + s_off(i) + 8 * L::BOXB);
+                    const uint2 wa = lds64(tK + s_off(i)), wb = lds64(tK + s_off(i) + 8 * L::BOXB);
                     float acc[NQ][4];
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks) {
@@ -569,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
                         const int j = 2 * (ks & 1);
                         const uint32_t a0 = code_pair(xa, j), a1 = code_pair(xb, j);
                         const uint32_t a2 = code_pair(xa, j + 1), a3 = code_pair(xb, j + 1);
-                        uint32_t bq[2 * NQ];
+                        alignas(16) uint32_t bq[2 * NQ];
                         if (QREG) {
 #pragma unroll
                             for (int n = 0; n < NQ; ++n) {
@@ -577,11 +614,11 @@ __global__ void __launch_bounds__(kThreads, MINB)
                                 bq[2 * n + 1] = qf[QREG ? i * 4 + ks : 0][n][1];
                             }
                         } else if (NQ == 2) {
-                            *reinterpret_cast<uint4*>(bq) =
-                                *reinterpret_cast<const uint4*>(sQ[QPRE ? js : 0][i * 4 + ks][lane]);
+                            const uint4 v = lds128(tQ + (i * 4 + ks) * (32 * 8 * NQ));
+                            *reinterpret_cast<uint4*>(bq) = v;
                         } else {
-                            *reinterpret_cast<uint2*>(bq) =
-                                *reinterpret_cast<const uint2*>(sQ[QPRE ? js : 0][i * 4 + ks][lane]);
+                            const uint2 v = lds64(tQ + (i * 4 + ks) * (32 * 8 * NQ));
+                            *reinterpret_cast<uint2*>(bq) = v;
                         }
 #pragma unroll
                         for (int n = 0; n < NQ; ++n) {
@@ -637,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
                     grow = grow || fmaxf(sv[n][c], sv[n][c + 2]) > m_run[n][c] + kLazyLog2;
-            __half* P = sP[done & 1];
+            const uint32_t P = smem_u32(sP[done & 1]);
             float l_tile[NQ][2];
             auto exponentiate = [&]() {
 #pragma unroll
@@ -652,15 +689,15 @@ __global__ void __launch_bounds__(kThreads, MINB)
                         const int key = krow + 8 * h;
                         if (PAIR) {  // [key][8] words: columns q (P, 0), 4 + q (0, P)
                             if (tq < 2) {
-                                uint32_t* d = reinterpret_cast<uint32_t*>(P) + key * 8 + 2 * tq;
+                                const uint32_t d = P + key * 32 + 8 * tq;
                                 const uint32_t e = pack_f16(pr[2 * h], 0.f);
                                 const uint32_t f = pack_f16(pr[2 * h + 1], 0.f);
-                                *reinterpret_cast<uint2*>(d) = make_uint2(e, f);
-                                *reinterpret_cast<uint2*>(d + 4) = make_uint2(e << 16, f << 16);
+                                sts64(d, e, f);
+                                sts64(d + 16, e << 16, f << 16);
                             }
                         } else {     // planes of 8 rows
-                            *reinterpret_cast<uint32_t*>(P + (n * kT + key) * 8 + 2 * tq) =
-                                pack_f16(pr[2 * h], pr[2 * h + 1]);
+                            sts32(P + (n * kT + key) * 16 + 4 * tq,
+                                  pack_f16(pr[2 * h], pr[2 * h + 1]));
                         }
                     }
                 }
@@ -668,12 +705,11 @@ __global__ void __launch_bounds__(kThreads, MINB)
             exponentiate();
             // V's scales of this warp's keys and group, as fp16 relative to 2^v_exp
             {
-                const uint16_t* vs = reinterpret_cast<const uint16_t*>(tV + vsOff);
                 uint32_t sb[(KW + 31) / 32], mx = 0;
 #pragma unroll
                 for (int i = 0; i < (KW + 31) / 32; ++i) {
                     const int k = i * 32 + lane, key = key0 + ksp * KW + k;
-                    sb[i] = k < KW ? vs[i * 32 * NG] : 0;
+                    sb[i] = k < KW ? lds16(tV + vsOff + i * 64 * NG) : 0;
                     if (edge && (key < job.lo_all || key >= job.ke)) sb[i] = 0;  // may hold anything
                     mx = max(mx, sb[i]);
                 }
@@ -697,9 +733,9 @@ __global__ void __launch_bounds__(kThreads, MINB)
                     if (i * 32 + lane < KW) {
                         const float x = __uint_as_float(sb[i] << 16) * f;
                         if (PAIR)
-                            reinterpret_cast<uint32_t*>(sV[warp])[i * 32 + lane] = pack_f16(x, x);
+                            sts32(aV + (i * 32 + lane) * 4, pack_f16(x, x));
                         else
-                            sV[warp][i * 32 + lane] = __float2half_rn(x);
+                            sts16(aV + (i * 32 + lane) * 2, pack_f16(x, 0.f));
                     }
             }
             if (consumer_vote(grow)) {
@@ -752,15 +788,11 @@ __global__ void __launch_bounds__(kThreads, MINB)
 #pragma unroll
                 for (int kk = 0; kk < KW; kk += 8) {
                     const int kt = ksp * KW + kk + 2 * tq;
-                    const uint32_t* P32 = reinterpret_cast<const uint32_t*>(P);
-                    const uint2 sc = *reinterpret_cast<const uint2*>(
-                        reinterpret_cast<const uint32_t*>(sV[warp]) + kk + 2 * tq);
-                    const uint32_t b0 = mul_f16x2(P32[kt * 8 + g], sc.x);
-                    const uint32_t b1 = mul_f16x2(P32[(kt + 1) * 8 + g], sc.y);
-                    const uint32_t w0 =
-                        *reinterpret_cast<const uint32_t*>(tV + vOff[0] + kk * L::BOXB);
-                    const uint32_t w1 =
-                        *reinterpret_cast<const uint32_t*>(tV + vOff[1] + kk * L::BOXB);
+                    const uint2 sc = lds64(aV + (kk + 2 * tq) * 4);
+                    const uint32_t b0 = mul_f16x2(lds32(P + kt * 32 + g * 4), sc.x);
+                    const uint32_t b1 = mul_f16x2(lds32(P + kt * 32 + 32 + g * 4), sc.y);
+                    const uint32_t w0 = lds32(tV + vOff[0] + kk * L::BOXB);
+                    const uint32_t w1 = lds32(tV + vOff[1] + kk * L::BOXB);
                     mma_f16(o[0][0], code_pair(w0, 0), code_pair(w0, 1),
                             code_pair(w1, 0), code_pair(w1, 1), b0, b1);
                     mma_f16(o[1][0], code_pair(w0, 2), code_pair(w0, 3),
@@ -772,18 +804,17 @@ __global__ void __launch_bounds__(kThreads, MINB)
                     const int kt = ksp * KW + kk;
                     uint32_t bf[NQ][2];
                     if (NQ == 2) {
-                        const uint32_t a = smem_u32(P + ((lane >> 4) * kT + kt + (lane & 15)) * 8);
+                        const uint32_t a = P + ((lane >> 4) * kT + kt + (lane & 15)) * 16;
                         ldsm_x4_t(a, bf[0][0], bf[0][1], bf[NQ - 1][0], bf[NQ - 1][1]);
                     } else {
-                        const uint32_t a = smem_u32(P + (kt + (lane & 15)) * 8);
+                        const uint32_t a = P + (kt + (lane & 15)) * 16;
                         asm volatile(
                             "ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
                             : "=r"(bf[0][0]), "=r"(bf[0][1])
                             : "r"(a));
                     }
-                    const uint32_t s0 = *reinterpret_cast<const uint32_t*>(&sV[warp][kk + 2 * tq]);
-                    const uint32_t s1 =
-                        *reinterpret_cast<const uint32_t*>(&sV[warp][kk + 2 * tq + 8]);
+                    const uint32_t s0 = lds32(aV + (kk + 2 * tq) * 2);
+                    const uint32_t s1 = lds32(aV + (kk + 2 * tq + 8) * 2);
 #pragma unroll
                     for (int n = 0; n < NQ; ++n) {
                         bf[n][0] = mul_f16x2(bf[n][0], s0);
@@ -792,8 +823,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
                     uint32_t w[4];  // words of keys 2 tq, + 1, + 8, + 9: columns 8 g .. 8 g + 7
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        w[k] = *reinterpret_cast<const uint32_t*>(
-                            tV + vOff[k & 1] + (kk + 8 * (k >> 1)) * L::BOXB);
+                        w[k] = lds32(tV + vOff[k & 1] + (kk + 8 * (k >> 1)) * L::BOXB);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {  // MMA rows g, g + 8: columns 8 g + 2 i, + 1
                         uint32_t r[4];
