@@ -74,6 +74,8 @@ typedef enum {
 #define GEMMA_DEVERR_N_REAL 8u     /* n_real[b] outside [0, n_new] (padded-bucket entry points) */
 #define GEMMA_DEVERR_PAGE 16u      /* a block-table entry outside [0, n_pages) (paged entry points) */
 
+#define GEMMA_DEVERR_SAMPLE 32u    /* gemma_logit_sample: bad parameters, or a row without candidates */
+
 /*
  * gemma_kv_append -- write this step's new K (and V) rows of an owner layer into its cache.
  *   cache[b][h][write_pos[b] + t][:] = new[b][t][h][:]   for t < n_new, h < n_kv.
@@ -413,6 +415,49 @@ int gemma_logit_softcap_argmax(const void* logits, int batch, int vocab, gemma_d
  * in the same launch); otherwise the rows' pieces meet in the scratch and a second launch
  * reduces them. */
 size_t gemma_logit_workspace_size(int batch, int vocab);
+
+/*
+ * gemma_logit_sample -- draw each row's token from its logits with temperature, top-k, top-p and
+ * min-p and a given uniform number: what a serving step does in place of the greedy index. Source:
+ * "Porting Gemma-4 (2B / 4B / 12B) to AWS Inferentia2", section 4.2 (the host applies the cap and
+ * samples); the pages give no filters, so all of them are the caller's arguments.
+ * Per row b, with z = softcap * tanh(x / softcap) (z = x when softcap == 0), over the candidates,
+ * i.e. the logits x that are neither NaN nor -infinity, in the order of falling x, equal ones by
+ * index:
+ *   1. keep the first top_k[b] (all when top_k[b] <= 0);
+ *   2. w = exp((z - z_max) / temperature[b]);
+ *   3. keep the shortest prefix whose weights sum to at least top_p[b] of the kept ones' sum (all
+ *      when top_p[b] >= 1, the first alone when top_p[b] <= 0);
+ *   4. keep those with w >= min_p[b] (the largest logit's in any case);
+ *   5. token[b] = the first one whose running sum of weights exceeds uniform[b] times the sum of
+ *      what is kept.
+ * temperature 0 draws the first of the order. Logits of +infinity leave only themselves (without a
+ * cap), with equal weights. Weights and their sums are accurate to about 2^-40, and the result does
+ * not depend on scheduling: the same call gives the same tokens.
+ *   logits      DEVICE [batch][vocab] of dtype, row-major, 16-byte aligned.
+ *   temperature, top_k, top_p, min_p
+ *               DEVICE float / int32 / float / float [batch], each optional: NULL stands for 1, 0,
+ *               1 and 0.
+ *   uniform     DEVICE float [batch], in [0, 1).
+ *   token_out   DEVICE int32 [batch]. A row without candidates, or with a temperature that is
+ *               negative, infinite or NaN, a NaN top_p or min_p, or uniform outside [0, 1), gets -1
+ *               and GEMMA_DEVERR_SAMPLE in device_error.
+ *   workspace   DEVICE scratch of gemma_logit_sample_workspace_size(batch, vocab, dtype) bytes,
+ *               16-byte aligned (NULL when that is 0); contents on entry are ignored; calls that
+ *               may overlap must not share it.
+ * Returns GEMMA_ERR_INVALID_ARG (NULL or misaligned pointer, batch < 0, vocab < 1, bad softcap or
+ * dtype), GEMMA_ERR_UNSUPPORTED (batch > 65535 or vocab > 1,048,560) or GEMMA_ERR_WORKSPACE before
+ * any launch; batch == 0 is a no-op. Asynchronous on `stream`; allocates nothing; graph-capturable.
+ */
+int gemma_logit_sample(const void* logits, int batch, int vocab, gemma_dtype dtype, float softcap,
+                       const float* temperature, const int32_t* top_k, const float* top_p,
+                       const float* min_p, const float* uniform, int32_t* token_out,
+                       void* workspace, size_t workspace_bytes, uint32_t* device_error,
+                       void* stream);
+
+/* Bytes of scratch gemma_logit_sample needs ((size_t)-1 for invalid arguments): none for bf16
+ * logits, 512 KiB per row for fp32 ones. */
+size_t gemma_logit_sample_workspace_size(int batch, int vocab, gemma_dtype dtype);
 
 /* A static, human-readable name of a gemma_status value. */
 const char* gemma_status_string(int status);

@@ -16,6 +16,7 @@ GEMMA_OK = 0
 GEMMA_DEVERR_SEQ_LEN, GEMMA_DEVERR_WRITE_POS, GEMMA_DEVERR_TIMEOUT = 1, 2, 4
 GEMMA_DEVERR_N_REAL = 8
 GEMMA_DEVERR_PAGE = 16
+GEMMA_DEVERR_SAMPLE = 32
 
 _c_int, _c_void_p, _c_size_t, _c_float = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
 _PVOID = ctypes.POINTER(ctypes.c_void_p)
@@ -80,6 +81,9 @@ _SIGNATURES = {
     "gemma_logit_softcap_argmax": (_c_int, [_c_void_p, _c_int, _c_int, _c_int, _c_float,
                                             _c_void_p, _c_void_p, _c_void_p, _c_size_t,
                                             _c_void_p]),
+    "gemma_logit_sample": (_c_int, [_c_void_p, _c_int, _c_int, _c_int, _c_float] +
+                           [_c_void_p] * 7 + [_c_size_t, _c_void_p, _c_void_p]),
+    "gemma_logit_sample_workspace_size": (_c_size_t, [_c_int, _c_int, _c_int]),
     "gemma_logit_workspace_size": (_c_size_t, [_c_int, _c_int]),
     "gemma_status_string": (ctypes.c_char_p, [_c_int]),
     "gemma_abi_version": (_c_int, []),
@@ -494,6 +498,40 @@ def gemma_logit_softcap_argmax(logits: torch.Tensor, softcap: float, argmax_out:
                                               _dev_ptr(argmax_out), ws_ptr, ws_bytes,
                                               _stream(stream))
     _check("gemma_logit_softcap_argmax", st)
+
+
+def gemma_logit_sample_workspace_size(batch: int, vocab: int, dtype: torch.dtype) -> int:
+    """dtype: the logits' type, torch.bfloat16 or torch.float32."""
+    code = {torch.bfloat16: GEMMA_BF16, torch.float32: GEMMA_FP32}.get(dtype, -1)
+    n = library().gemma_logit_sample_workspace_size(int(batch), int(vocab), code)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("invalid arguments for gemma_logit_sample_workspace_size")
+    return int(n)
+
+
+def gemma_logit_sample(logits: torch.Tensor, token_out: torch.Tensor, uniform: torch.Tensor, *,
+                       temperature: Optional[torch.Tensor] = None,
+                       top_k: Optional[torch.Tensor] = None,
+                       top_p: Optional[torch.Tensor] = None,
+                       min_p: Optional[torch.Tensor] = None, softcap: float = 0.0,
+                       workspace: Optional[torch.Tensor] = None,
+                       device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """logits [B][V] bf16 or fp32; token_out int32 [B]; uniform, temperature, top_p, min_p fp32
+    [B] and top_k int32 [B] on the device (each filter may be None: 1, 1, 0 and 0)."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be [B][V]")
+    B, V = logits.shape
+    for name, t, dt in (("token_out", token_out, torch.int32), ("uniform", uniform, torch.float32),
+                        ("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
+                        ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
+        if t is not None and (t.dtype != dt or t.numel() != B):
+            raise TypeError(f"{name} must be {dt} [batch]")
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = library().gemma_logit_sample(
+        _dev_ptr(logits), B, V, _dtype(logits), float(softcap), _dev_ptr(temperature),
+        _dev_ptr(top_k), _dev_ptr(top_p), _dev_ptr(min_p), _dev_ptr(uniform), _dev_ptr(token_out),
+        _dev_ptr(workspace), ws_bytes, _dev_ptr(device_error), _stream(stream))
+    _check("gemma_logit_sample", st)
 
 
 def _attn(fn_name, out, q, k_cache, v_cache, owner_map, layer, seq_lens, max_seq_len, n_tok, *,

@@ -9,6 +9,7 @@
 #include "attn_internal.h"
 #include "logits.h"
 #include "q4.h"
+#include "sample.h"
 
 using gemma::RowsParams;
 
@@ -858,6 +859,37 @@ int gemma_attn_q4(void* out, const void* q, const void* const* k_codes,
                      kind == GEMMA_GLOBAL ? GEMMA_GLOBAL : GEMMA_SLIDING, window, n_q, n_kv,
                      head_dim, k_eq_v, e.slots, scale, softcap, GEMMA_BF16, ws + e.plan_off,
                      workspace_bytes - e.plan_off, device_error, stream);
+}
+
+int gemma_logit_sample(const void* logits, int batch, int vocab, gemma_dtype dtype, float softcap,
+                       const float* temperature, const int32_t* top_k, const float* top_p,
+                       const float* min_p, const float* uniform, int32_t* token_out,
+                       void* workspace, size_t workspace_bytes, uint32_t* device_error,
+                       void* stream) {
+    if (batch < 0 || vocab < 1 || (dtype != GEMMA_BF16 && dtype != GEMMA_FP32))
+        return GEMMA_ERR_INVALID_ARG;
+    if (!std::isfinite(softcap) || softcap < 0.f) return GEMMA_ERR_INVALID_ARG;
+    if (batch > 65535 || vocab > gemma::kSampleMaxVocab) return GEMMA_ERR_UNSUPPORTED;
+    if (batch == 0) return GEMMA_OK;
+    if (!logits || !uniform || !token_out || !aligned16(logits)) return GEMMA_ERR_INVALID_ARG;
+    const size_t need = gemma::sample_workspace(batch, vocab, dtype == GEMMA_FP32);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+        return GEMMA_ERR_WORKSPACE;
+    const int n_sm = sm_count();
+    if (n_sm < 0) return GEMMA_ERR_CUDA;
+    const gemma::SampleParams p{logits, temperature, top_k, top_p, min_p, uniform, token_out,
+                                static_cast<unsigned long long*>(workspace), device_error, batch,
+                                vocab, softcap};
+    const cudaError_t e =
+        gemma::launch_sample(p, dtype == GEMMA_FP32, n_sm, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? GEMMA_OK : GEMMA_ERR_CUDA;
+}
+
+size_t gemma_logit_sample_workspace_size(int batch, int vocab, gemma_dtype dtype) {
+    if (batch < 0 || vocab < 1 || vocab > gemma::kSampleMaxVocab ||
+        (dtype != GEMMA_BF16 && dtype != GEMMA_FP32))
+        return (size_t)-1;
+    return gemma::sample_workspace(batch, vocab, dtype == GEMMA_FP32);
 }
 
 }  // extern "C"

@@ -1,0 +1,858 @@
+// sample.cu -- one token per row of logits by temperature, top-k, top-p and min-p.
+//
+// Per row, with z = softcap * tanh(x / softcap) (x without a cap) and the candidates (neither NaN
+// nor -inf) in the order of falling x, equal ones by index:
+//   keep the first top_k;  w = exp((z - z_max) / T);  keep the shortest prefix whose weights sum to
+//   at least top_p of the kept ones' sum;  keep those with w >= min_p;  draw the first whose
+//   running sum exceeds u times the sum of what is kept.
+//
+// No sort: the order of a row is a count per distinct value. bf16 has 65,536 of them, so one pass
+// over the logits fills a histogram in shared memory (16-bit counters, 128 KB; the row's slices
+// go to the CTAs of a cluster, at most 65,535 logits each, whose counts meet through distributed
+// shared memory), and everything else works on counts and on at most a few thousand weights, each
+// evaluated once in 64 bits: cuts and draws fall between the same tokens as in a 64-bit
+// evaluation of the definition. Ties inside a value are a division, and one look at the slice that
+// holds the wanted occurrence finds its index. fp32 logits take the same histogram over their
+// upper 16 bits, whose bins' weights are summed into global memory as integers (40 bits below the
+// bin's own largest weight, so the order of the additions does not matter), and repeat it over
+// the lower 16 bits for the bins that a cut or the draw falls into.
+//
+// The first pass is bound by shared-memory atomics; runs of eight equal logits count as one, so
+// that a row masked with one finite value does not queue on one counter.
+#include <atomic>
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "sample.h"
+
+namespace gemma {
+
+namespace {
+
+constexpr int kThreads = 1024;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 65536, kGroups = 2048;  // 32 bins per group
+constexpr int kMaxCtas = 16;
+
+// Order-preserving key of a number (-0 as +0), its inverse, and the candidates' range of keys:
+// above -inf, not above +inf.
+template <bool F32>
+struct Key;
+template <>
+struct Key<false> {
+    static constexpr uint32_t kLow = 0x0080u, kInf = 0xff80u;
+    __device__ static uint32_t of(uint32_t u) {
+        if ((u & 0x7fffu) == 0) u = 0;
+        return u & 0x8000u ? ~u & 0xffffu : u | 0x8000u;
+    }
+    __device__ static float value(uint32_t key) {
+        const uint32_t u = key & 0x8000u ? key & 0x7fffu : ~key & 0xffffu;
+        return __uint_as_float(u << 16);
+    }
+};
+template <>
+struct Key<true> {
+    static constexpr uint32_t kLow = 0x00800000u, kInf = 0xff800000u;
+    __device__ static uint32_t of(uint32_t u) {
+        if ((u & 0x7fffffffu) == 0) u = 0;
+        return u & 0x80000000u ? ~u : u | 0x80000000u;
+    }
+    __device__ static float value(uint32_t key) {
+        return __uint_as_float(key & 0x80000000u ? key & 0x7fffffffu : ~key);
+    }
+};
+
+__device__ __forceinline__ uint32_t peer_addr(const void* local, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(r)
+                 : "r"(smem_u32(local)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ uint32_t ld_peer(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_peer(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_peer(uint32_t addr, unsigned long long v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
+}
+// Barrier of the cluster (of the CTA alone when it has one); also orders global memory.
+__device__ __forceinline__ void cluster_barrier() {
+    __threadfence();
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// Unevaluated sums h + l of two fp32 numbers, |l| at most half a unit of h (Dekker's and Knuth's
+// error-free sums and products). Every operation is an intrinsic: contracted or reordered they
+// would lose their error terms.
+struct F2 {
+    float h, l;
+};
+__device__ __forceinline__ F2 fast_sum(float a, float b) {  // |a| >= |b|
+    const float s = __fadd_rn(a, b);
+    return F2{s, __fadd_rn(b, -__fadd_rn(s, -a))};
+}
+__device__ __forceinline__ F2 two_sum(float a, float b) {
+    const float s = __fadd_rn(a, b), t = __fadd_rn(s, -a);
+    return F2{s, __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -t)), __fadd_rn(b, -t))};
+}
+__device__ __forceinline__ F2 operator+(F2 a, F2 b) {
+    const F2 s = two_sum(a.h, b.h), e = two_sum(a.l, b.l);
+    const F2 t = fast_sum(s.h, __fadd_rn(s.l, e.h));
+    return fast_sum(t.h, __fadd_rn(t.l, e.l));
+}
+__device__ __forceinline__ F2 operator*(F2 a, F2 b) {
+    const float m = __fmul_rn(a.h, b.h);
+    float e = __fmaf_rn(a.h, b.h, -m);
+    e = __fmaf_rn(a.h, b.l, e);
+    return fast_sum(m, __fmaf_rn(a.l, b.h, e));
+}
+__device__ __forceinline__ F2 operator/(F2 a, F2 b) {
+    const float q = __fdiv_rn(a.h, b.h);
+    const F2 r = a + F2{-q, 0.f} * b;
+    const float q2 = __fdiv_rn(r.h, b.h);
+    const F2 r2 = r + F2{-q2, 0.f} * b;
+    const F2 t = fast_sum(q, q2);
+    return fast_sum(t.h, __fadd_rn(t.l, __fdiv_rn(r2.h, b.h)));
+}
+
+// 2^(i / 64) as such sums.
+__constant__ float2 c_exp2[64] = {
+    {0x1.0000000000000p+0f, 0x0.0p+0f}, {0x1.02c9a40000000p+0f, -0x1.887fa00000000p-28f},
+    {0x1.059b0e0000000p+0f, -0x1.9d4f520000000p-25f}, {0x1.0874520000000p+0f, -0x1.e2990e0000000p-26f},
+    {0x1.0b55860000000p+0f, 0x1.9f31220000000p-25f}, {0x1.0e3ec40000000p+0f, -0x1.a585cc0000000p-25f},
+    {0x1.11301e0000000p+0f, -0x1.fdb4960000000p-25f}, {0x1.1429aa0000000p+0f, 0x1.d525bc0000000p-25f},
+    {0x1.172b840000000p+0f, -0x1.c157420000000p-27f}, {0x1.1a35be0000000p+0f, 0x1.6df96e0000000p-25f},
+    {0x1.1d48740000000p+0f, -0x1.d2e8ca0000000p-25f}, {0x1.2063b80000000p+0f, 0x1.0c519a0000000p-25f},
+    {0x1.2387a60000000p+0f, 0x1.ceac480000000p-25f}, {0x1.26b4560000000p+0f, 0x1.789f380000000p-26f},
+    {0x1.29e9e00000000p+0f, -0x1.5c04240000000p-25f}, {0x1.2d285a0000000p+0f, 0x1.b900c20000000p-26f},
+    {0x1.306fe00000000p+0f, 0x1.4636e20000000p-25f}, {0x1.33c08c0000000p+0f, -0x1.b37d200000000p-25f},
+    {0x1.371a740000000p+0f, -0x1.18aac60000000p-25f}, {0x1.3a7db40000000p+0f, -0x1.634c020000000p-25f},
+    {0x1.3dea640000000p+0f, 0x1.8246840000000p-25f}, {0x1.4160a20000000p+0f, 0x1.f72e2a0000000p-28f},
+    {0x1.44e0860000000p+0f, 0x1.8624b40000000p-30f}, {0x1.486a2c0000000p+0f, -0x1.47d8660000000p-25f},
+    {0x1.4bfdae0000000p+0f, -0x1.593abc0000000p-25f}, {0x1.4f9b280000000p+0f, -0x1.2c5a6c0000000p-25f},
+    {0x1.5342b60000000p+0f, -0x1.2c56100000000p-25f}, {0x1.56f4740000000p+0f, -0x1.295b040000000p-25f},
+    {0x1.5ab07e0000000p+0f, -0x1.5bd5ec0000000p-27f}, {0x1.5e76f20000000p+0f, -0x1.4a5bd60000000p-25f},
+    {0x1.6247ec0000000p+0f, -0x1.f8b5500000000p-25f}, {0x1.6623880000000p+0f, 0x1.2a91120000000p-27f},
+    {0x1.6a09e60000000p+0f, 0x1.9fcef40000000p-26f}, {0x1.6dfb240000000p+0f, -0x1.cd72e80000000p-27f},
+    {0x1.71f75e0000000p+0f, 0x1.1d8bee0000000p-25f}, {0x1.75feb60000000p+0f, -0x1.37b3060000000p-25f},
+    {0x1.7a11480000000p+0f, -0x1.829fd00000000p-25f}, {0x1.7e2f340000000p+0f, -0x1.2616340000000p-25f},
+    {0x1.82589a0000000p+0f, -0x1.accc7c0000000p-26f}, {0x1.868d9a0000000p+0f, -0x1.2edb440000000p-26f},
+    {0x1.8ace540000000p+0f, 0x1.15506e0000000p-27f}, {0x1.8f1aea0000000p+0f, -0x1.baa2320000000p-26f},
+    {0x1.93737c0000000p+0f, -0x1.e647440000000p-25f}, {0x1.97d82a0000000p+0f, -0x1.0d8d840000000p-31f},
+    {0x1.9c49180000000p+0f, 0x1.51f8480000000p-27f}, {0x1.a0c6680000000p+0f, -0x1.2886a60000000p-26f},
+    {0x1.a5503c0000000p+0f, -0x1.b83b540000000p-25f}, {0x1.a9e6b60000000p+0f, -0x1.50c0480000000p-25f},
+    {0x1.ae89fa0000000p+0f, -0x1.a94b140000000p-26f}, {0x1.b33a2c0000000p+0f, -0x1.ec3a820000000p-26f},
+    {0x1.b7f7700000000p+0f, -0x1.a094380000000p-25f}, {0x1.bcc1ea0000000p+0f, -0x1.f687c60000000p-25f},
+    {0x1.c199be0000000p+0f, -0x1.3d56b20000000p-27f}, {0x1.c67f120000000p+0f, 0x1.cafa2a0000000p-25f},
+    {0x1.cb720e0000000p+0f, -0x1.8837cc0000000p-27f}, {0x1.d072d40000000p+0f, 0x1.40f1300000000p-25f},
+    {0x1.d5818e0000000p+0f, -0x1.822dbc0000000p-27f}, {0x1.da9e600000000p+0f, 0x1.ed99420000000p-27f},
+    {0x1.dfc9740000000p+0f, -0x1.908c940000000p-25f}, {0x1.e502ee0000000p+0f, 0x1.e2cffe0000000p-26f},
+    {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}, {0x1.efa1be0000000p+0f, 0x1.cc2b440000000p-25f},
+    {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f}, {0x1.fa7c180000000p+0f, 0x1.9e90d80000000p-28f}};
+
+// e^x for x <= 0: x = (64 k + i) ln 2 / 64 + r with |r| < 0.0055, e^x = 2^k 2^(i/64) e^r, and e^r by
+// its series, whose first terms keep their error terms (the fifth is below 2^-46). Below -60: 0.
+__device__ __forceinline__ F2 exp_f2(F2 x, const float2* exp2) {
+    if (!(x.h > -60.f)) return F2{0.f, 0.f};
+    const float n = rintf(x.h * 92.332482616893656f);  // 64 / ln 2
+    // ln 2 / 64 in four parts of 11 bits and a rest (n has at most 13: the products are exact)
+    const F2 nb = two_sum(__fmul_rn(n, -0x1.2140000000000p-18f), __fmul_rn(n, -0x1.fbc0000000000p-29f));
+    const F2 r = (x + F2{__fmul_rn(n, -0x1.62c0000000000p-7f), 0.f}) + fast_sum(nb.h, __fadd_rn(nb.l, __fmul_rn(n, -0x1.473de60000000p-40f)));
+    const F2 r2 = r * r;
+    const float c = r.h * r2.h * (0.16666667f + r.h * (0.041666668f + r.h * 0.0083333333f));
+    const F2 e = F2{1.f, 0.f} + (r + (F2{0.5f * r2.h, 0.5f * r2.l} + F2{c, 0.f}));
+    const int k = (int)n;
+    const float2 t = exp2[k & 63];
+    F2 w = e * F2{t.x, t.y};
+    const float sc = __uint_as_float((uint32_t)(127 + (k >> 6)) << 23);
+    return F2{w.h * sc, w.l * sc};
+}
+
+// A place in a row's order: the tokens above key `key`, and of key itself the first `ties`.
+struct Cut {
+    uint32_t key;
+    uint32_t ties;
+};
+
+typedef unsigned long long u64;
+
+struct Shared {
+    uint32_t count[kGroups];  // candidates per group of 32 bins
+    // weights per group, and then their running sums from the highest group down (place d: group
+    // kGroups - 1 - d), inclusive; fp32: the same over the lower halves of one upper half
+    u64 before[kGroups], before2[kGroups];
+    float2 exp2[64];
+    u64 part[kWarps];
+    uint32_t upart[kWarps];
+    int top[kWarps];
+    uint32_t found, key, n;
+    u64 m, start;
+};
+
+template <bool F32>
+struct Row {
+    const SampleParams& p;
+    Shared& s;
+    uint32_t* hist;   // [kBins / 2] pairs of 16-bit counters
+    uint32_t* merged; // [groups of this CTA][32] counts of the whole row (more than one CTA)
+    int C, rank, row;
+    long long i0, i1; // this CTA's slice
+    F2 inv_t, zmax;
+    uint32_t key_max; // key of the largest candidate
+    int tid, warp, lane;
+
+    using K = Key<F32>;
+
+    // z of a logit: c tanh(x / c) = +-c (1 - e) / (1 + e), e = exp(-2 |x| / c)
+    __device__ F2 capped(float x) const {
+        if (!(p.softcap > 0.f)) return F2{x, 0.f};
+        const F2 c{p.softcap, 0.f};
+        const float a = fabsf(x);
+        const F2 e = exp_f2(F2{-2.f * a, 0.f} / c, s.exp2);
+        F2 t = (F2{1.f, 0.f} + F2{-e.h, -e.l}) / (F2{1.f, 0.f} + e);
+        if (isinf(x)) t = F2{1.f, 0.f};
+        t = t * c;
+        return x < 0.f ? F2{-t.h, -t.l} : t;
+    }
+    // exp((z - top) / T) of a logit z <= top
+    __device__ F2 relative(F2 z, F2 top) const {
+        const F2 d = z + F2{-top.h, -top.l};
+        if (isinf(top.h)) return F2{isinf(z.h) && z.h > 0.f ? 1.f : 0.f, 0.f};
+        if (d.h == 0.f) return F2{1.f, 0.f};
+        if (!(d.h > -1e30f)) return F2{0.f, 0.f};
+        return exp_f2(d * inv_t, s.exp2);
+    }
+    __device__ F2 weight(uint32_t key) const {
+        return key == key_max ? F2{1.f, 0.f} : relative(capped(K::value(key)), zmax);
+    }
+    // n weights in units of 2^-43, rounded
+    __device__ u64 units(F2 w, uint32_t n) const {
+        if (!(w.h > 0.f)) return 0;
+        const F2 m = w * F2{(float)n, 0.f};  // n < 2^24: exact
+        return (u64)(__float2ll_rn(m.h * 0x1p43f) + __float2ll_rn(m.l * 0x1p43f));
+    }
+
+    // Histogram of this CTA's slice. bf16: of the keys; fp32: of the keys' upper halves (level 0)
+    // or of the lower halves of those with upper half `upper`.
+    __device__ void count_slice(int level, uint32_t upper) {
+        for (int i = tid; i < kBins / 8; i += kThreads)
+            reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+        __syncthreads();
+        auto add = [&](uint32_t u, uint32_t n) {
+            const uint32_t key = K::of(u);
+            if (key < K::kLow || key > K::kInf) return;
+            uint32_t bin = key;
+            if (F32) {
+                if (level == 0) {
+                    bin = key >> 16;
+                } else {
+                    if (key >> 16 != upper) return;
+                    bin = key & 0xffffu;
+                }
+            }
+            atomicAdd(&hist[bin >> 1], n << (16 * (bin & 1)));
+        };
+        for_slice([&](uint4 v) {
+            if (F32) {
+                if (v.x == v.y && v.x == v.z && v.x == v.w) {
+                    add(v.x, 4);
+                } else {
+                    add(v.x, 1);
+                    add(v.y, 1);
+                    add(v.z, 1);
+                    add(v.w, 1);
+                }
+            } else {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                if (v.x == v.y && v.x == v.z && v.x == v.w && (v.x & 0xffffu) == v.x >> 16) {
+                    add(v.x & 0xffffu, 8);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        add(w[k] & 0xffffu, 1);
+                        add(w[k] >> 16, 1);
+                    }
+                }
+            }
+        }, [&](uint32_t u) { add(u, 1); });
+        __syncthreads();
+    }
+    // Calls vec for every aligned 16 bytes of the slice and one for the elements around them.
+    template <class V, class O>
+    __device__ void for_slice(V vec, O one) {
+        constexpr int E = F32 ? 4 : 8;
+        const long long base = (long long)row * p.vocab;
+        const long long b0 = base + i0, b1 = base + i1;
+        const long long a0 = min((b0 + E - 1) / E * E, b1), a1 = max(b1 / E * E, a0);
+        auto load1 = [&](long long i) -> uint32_t {
+            return F32 ? static_cast<const uint32_t*>(p.logits)[i]
+                       : static_cast<const uint16_t*>(p.logits)[i];
+        };
+        for (long long i = b0 + tid; i < a0; i += kThreads) one(load1(i));
+        const uint4* v = reinterpret_cast<const uint4*>(p.logits) + a0 / E;
+        const int n = (int)((a1 - a0) / E);
+        int i = tid;
+        for (; i + 3 * kThreads < n; i += 4 * kThreads) {
+            uint4 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = v[i + k * kThreads];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) vec(x[k]);
+        }
+        for (; i < n; i += kThreads) vec(v[i]);
+        for (long long j = a1 + tid; j < b1; j += kThreads) one(load1(j));
+    }
+
+    // The row's counts: group sums into every CTA's s.count, bins into their owner's `merged`
+    // (group g belongs to CTA g % C). Needs every CTA's histogram, leaves them readable.
+    __device__ void merge_counts() {
+        cluster_barrier();
+        for (int k = warp; rank + k * C < kGroups; k += kWarps) {
+            const int g = rank + k * C, w = g * 16 + (lane & 15);
+            uint32_t lo = 0, hi = 0;
+            for (int r = lane >> 4; r < C; r += 2) {
+                const uint32_t v = ld_peer(peer_addr(hist + w, r));
+                lo += v & 0xffffu;
+                hi += v >> 16;
+            }
+            lo += __shfl_xor_sync(0xffffffffu, lo, 16);
+            hi += __shfl_xor_sync(0xffffffffu, hi, 16);
+            if (C > 1 && lane < 16)
+                *reinterpret_cast<uint2*>(merged + k * 32 + 2 * lane) = make_uint2(lo, hi);
+            const uint32_t sum = __reduce_add_sync(0xffffffffu, lane < 16 ? lo + hi : 0u);
+            if (lane < C) st_peer(peer_addr(&s.count[g], lane), sum);
+        }
+        cluster_barrier();
+    }
+    // count of bin 32 g + i (any CTA's)
+    __device__ uint32_t bin_count(int g, int i) const {
+        if (C == 1) return hist[g * 16 + (i >> 1)] >> (16 * (i & 1)) & 0xffffu;
+        return ld_peer(peer_addr(merged + (g / C) * 32 + i, g % C));
+    }
+
+    // Inclusive sums over the warp's lanes.
+    template <class T>
+    __device__ T warp_sums(T x) const {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const T y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        return x;
+    }
+    // Weights per group to running sums, in place.
+    __device__ void running_sums(u64* before) {
+        const u64 a = before[kGroups - 1 - 2 * tid], b = before[kGroups - 2 - 2 * tid];
+        const u64 x = warp_sums(a + b);
+        __syncthreads();
+        if (lane == 31) s.part[warp] = x;
+        __syncthreads();
+        u64 base = x - a - b;
+        for (int w = 0; w < warp; ++w) base += s.part[w];
+        before[2 * tid] = base + a;
+        before[2 * tid + 1] = base + a + b;
+        __syncthreads();
+    }
+    // First place d (group kGroups - 1 - d) whose running sum is at least `need`, which the last is.
+    __device__ int reach(const u64* before, u64 need) {
+        const u64 prev = tid ? before[2 * tid - 1] : 0, a = before[2 * tid], b = before[2 * tid + 1];
+        if (prev < need && need <= a) s.found = 2 * tid;
+        if (a < need && need <= b) s.found = 2 * tid + 1;
+        __syncthreads();
+        const int d = (int)s.found;
+        __syncthreads();
+        return d;
+    }
+};
+
+// floor(a b / c), a b below 2^84
+__device__ __forceinline__ u64 mul_div(u64 a, u64 b, u64 c) {
+    return (u64)((unsigned __int128)a * b / c);
+}
+
+template <bool F32>
+__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams p, int C) {
+    pdl_launch_dependents();
+    extern __shared__ __align__(16) uint8_t smem[];
+    Shared& s = *reinterpret_cast<Shared*>(smem);
+    uint32_t* hist = reinterpret_cast<uint32_t*>(smem + (sizeof(Shared) + 15) / 16 * 16);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int row = blockIdx.x / C, rank = blockIdx.x - row * C;
+    using K = Key<F32>;
+    pdl_wait();
+
+    // parameters (the same in every CTA of the row)
+    const float t = p.temperature ? p.temperature[row] : 1.f;
+    const int want_k = p.top_k ? p.top_k[row] : 0;
+    const float top_p = p.top_p ? p.top_p[row] : 1.f;
+    const float min_p = p.min_p ? p.min_p[row] : 0.f;
+    const float u = p.uniform[row];
+    const bool good = t >= 0.f && isfinite(t) && top_p == top_p && min_p == min_p && u >= 0.f && u < 1.f;
+    if (!good) {
+        if (rank == 0 && tid == 0) {
+            p.token[row] = -1;
+            report(p.err, GEMMA_DEVERR_SAMPLE);
+        }
+        return;
+    }
+    Row<F32> r{p, s, hist, hist + kBins / 2, C, rank, row};
+    const long long per = (p.vocab + C - 1) / C;
+    r.i0 = min((long long)rank * per, (long long)p.vocab);
+    r.i1 = min(r.i0 + per, (long long)p.vocab);
+    r.tid = tid;
+    r.warp = warp;
+    r.lane = lane;
+    if (tid < 64) s.exp2[tid] = c_exp2[tid];
+    // fp32: this CTA's share of the row's weight sums starts at zero
+    u64* mass = F32 ? p.mass + (size_t)row * kBins : nullptr;
+    if (F32)
+        for (int i = rank * kThreads + tid; i < kBins; i += C * kThreads) mass[i] = 0ull;
+
+    r.count_slice(0, 0);
+    r.merge_counts();
+
+    // the largest candidate and the number of them
+    uint32_t total = 0;
+    int top = -1;
+    {
+        const uint32_t a = s.count[2 * tid], b = s.count[2 * tid + 1];
+        const uint32_t sum = __reduce_add_sync(0xffffffffu, a + b);
+        const int hi = __reduce_max_sync(0xffffffffu, b ? 2 * tid + 1 : a ? 2 * tid : -1);
+        if (lane == 0) {
+            s.upart[warp] = sum;
+            s.top[warp] = hi;
+        }
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) {
+            total += s.upart[w];
+            top = max(top, s.top[w]);
+        }
+        __syncthreads();
+    }
+    if (total == 0) {
+        if (rank == 0 && tid == 0) {
+            p.token[row] = -1;
+            report(p.err, GEMMA_DEVERR_SAMPLE);
+        }
+        cluster_barrier();  // no CTA leaves while another reads its counts
+        return;
+    }
+    auto top_bin = [&](int g) {  // highest bin with a candidate of group g
+        const unsigned any = __ballot_sync(0xffffffffu, r.bin_count(g, lane) != 0);
+        return (uint32_t)(g * 32 + 31 - __clz(any));
+    };
+    const uint32_t bin_max = top_bin(top);
+
+    // fp32: bins over the lower halves of the numbers with upper half `upper` (s.count and
+    // `merged` then hold these)
+    uint32_t at = 0xffffffffu;  // that upper half
+    auto refine = [&](uint32_t upper) {
+        if (at == upper) return;
+        cluster_barrier();  // (peers may still read the counts)
+        r.count_slice(1, upper);
+        r.merge_counts();
+        at = upper;
+    };
+    uint32_t key_max = bin_max;
+    const bool greedy = t == 0.f || want_k == 1;
+    const uint32_t k = want_k > 0 && (uint32_t)want_k < total ? (uint32_t)want_k : total;
+
+    // the n-th candidate from the highest down, by counts
+    auto kth = [&](uint32_t n, uint32_t& bin, uint32_t& ties) {
+        const uint32_t a = s.count[kGroups - 1 - 2 * tid], b = s.count[kGroups - 2 - 2 * tid];
+        const uint32_t x = r.warp_sums(a + b);
+        if (lane == 31) s.upart[warp] = x;
+        __syncthreads();
+        uint32_t ex = x - a - b;
+        for (int w = 0; w < warp; ++w) ex += s.upart[w];
+        if (ex < n && ex + a >= n) {
+            s.key = kGroups - 1 - 2 * tid;
+            s.n = n - ex;
+        } else if (ex + a < n && ex + a + b >= n) {
+            s.key = kGroups - 2 - 2 * tid;
+            s.n = n - ex - a;
+        }
+        __syncthreads();
+        const int g = (int)s.key;
+        const uint32_t left = s.n;
+        __syncthreads();
+        const uint32_t c = r.bin_count(g, 31 - lane), y = r.warp_sums(c);
+        const int l = __ffs(__ballot_sync(0xffffffffu, y >= left)) - 1;
+        bin = (uint32_t)(g * 32 + 31 - l);
+        ties = left - __shfl_sync(0xffffffffu, y - c, l);
+    };
+
+    Cut cut{0u, 0u};       // kept so far: this and above
+    bool cut_all = true;   // or every candidate
+    if (F32) {
+        refine(bin_max);
+        int g2 = -1;
+        const uint32_t a = s.count[2 * tid], b = s.count[2 * tid + 1];
+        const int hi = __reduce_max_sync(0xffffffffu, b ? 2 * tid + 1 : a ? 2 * tid : -1);
+        if (lane == 0) s.top[warp] = hi;
+        __syncthreads();
+        for (int w = 0; w < kWarps; ++w) g2 = max(g2, s.top[w]);
+        __syncthreads();
+        key_max = bin_max << 16 | top_bin(g2);
+    }
+    r.key_max = key_max;
+    r.zmax = r.capped(K::value(key_max));
+    r.inv_t = t > 0.f ? F2{1.f, 0.f} / F2{t, 0.f} : F2{0.f, 0.f};
+
+    uint32_t draw_key = key_max, draw_tie = 0;
+    if (!greedy) {
+        uint32_t cut_bin = 0;
+        if (k < total) {
+            if (F32) {
+                // (the counts at hand are of the largest's lower halves: count the upper ones anew)
+                cluster_barrier();
+                r.count_slice(0, 0);
+                r.merge_counts();
+                at = 0xffffffffu;
+            }
+            kth(k, cut_bin, cut.ties);
+            cut.key = cut_bin;
+            cut_all = false;
+            if (F32) {
+                const uint32_t n = cut.ties;
+                uint32_t low;
+                refine(cut_bin);
+                kth(n, low, cut.ties);
+                cut.key = cut_bin << 16 | low;
+            }
+        }
+        // tokens of a key that are kept so far, of the c there are
+        auto kept_of = [&](uint32_t key, uint32_t c) {
+            return cut_all || key > cut.key ? c : key == cut.key ? min(c, cut.ties) : 0u;
+        };
+        // fp32: weights over the lower halves of `at`, of what is kept so far
+        uint32_t lower_of = 0xffffffffu;
+        auto lower_masses = [&](uint32_t upper) {
+            refine(upper);
+            if (lower_of == upper) return;
+            for (int q = warp; rank + q * C < kGroups; q += kWarps) {
+                const int g = rank + q * C;
+                u64 m = 0;
+                if (s.count[g]) {
+                    const uint32_t key = upper << 16 | (uint32_t)(g * 32 + lane);
+                    const uint32_t n = kept_of(key, r.bin_count(g, lane));
+                    if (n) m = r.units(r.weight(key), n);
+                    m = __shfl_sync(0xffffffffu, r.warp_sums(m), 31);
+                }
+                if (lane < C) st_peer(peer_addr(&s.before2[g], lane), m);
+            }
+            cluster_barrier();
+            r.running_sums(s.before2);
+            lower_of = upper;
+        };
+        u64 cut_mass = 0;  // fp32: kept weight of the cut's own bin
+        if (F32 && !cut_all) {
+            lower_masses(cut_bin);
+            cut_mass = s.before2[kGroups - 1];
+        }
+        if (F32) {
+            // weights of every number above the cut's bin, relative to its bin's largest
+            auto add = [&](uint32_t bits) {
+                const uint32_t key = K::of(bits);
+                if (key < K::kLow || key > K::kInf) return;
+                const uint32_t bin = key >> 16;
+                if (!cut_all && bin <= cut_bin) return;
+                const uint32_t anchor = min(bin << 16 | 0xffffu, key_max);
+                const F2 w = key == anchor ? F2{1.f, 0.f}
+                                           : r.relative(r.capped(K::value(key)),
+                                                        r.capped(K::value(anchor)));
+                const u64 v = (u64)(__float2ll_rn(w.h * 0x1p40f) + __float2ll_rn(w.l * 0x1p40f));
+                if (v) atomicAdd(mass + bin, v);
+            };
+            r.for_slice([&](uint4 v) { add(v.x); add(v.y); add(v.z); add(v.w); },
+                        [&](uint32_t bits) { add(bits); });
+            cluster_barrier();
+        }
+        // kept weight of a bin
+        auto bin_mass = [&](int g, int i) -> u64 {
+            const uint32_t bin = (uint32_t)(g * 32 + i);
+            if (bin > bin_max) return 0;
+            if (F32) {
+                if (!cut_all && bin <= cut_bin) return bin == cut_bin ? cut_mass : 0;
+                const u64 v = *reinterpret_cast<volatile u64*>(mass + bin);
+                if (!v) return 0;
+                const F2 w = r.weight(min(bin << 16 | 0xffffu, key_max));
+                // v < 2^60 as a sum of three numbers of 24 bits
+                const float a = (float)(v >> 40), b = (float)(v >> 20 & 0xfffffu),
+                            c = (float)(v & 0xfffffu);
+                return r.units(w * F2{a, 0.f}, 1u) +
+                       r.units(w * fast_sum(b * 0x1p-20f, c * 0x1p-40f), 1u);
+            }
+            const uint32_t n = kept_of(bin, r.bin_count(g, i));
+            return n ? r.units(r.weight(bin), n) : 0;
+        };
+        for (int q = warp; rank + q * C < kGroups; q += kWarps) {
+            const int g = rank + q * C;
+            u64 m = 0;
+            if (g * 32u <= bin_max && (F32 || s.count[g])) {
+                m = bin_mass(g, lane);
+                if (__any_sync(0xffffffffu, m != 0))
+                    m = __shfl_sync(0xffffffffu, r.warp_sums(m), 31);
+            }
+            if (lane < C) st_peer(peer_addr(&s.before[g], lane), m);
+        }
+        cluster_barrier();
+        r.running_sums(s.before);
+        const u64 all = s.before[kGroups - 1];
+
+        // The place in the order where the running weight first is at least `need` (1..all); and
+        // the running weight there. One warp looks into a group, the others wait for it.
+        auto place = [&](u64 need, Cut& c, u64& sum) {
+            const int d = r.reach(s.before, need);
+            if (warp == 0) {
+                const int g = kGroups - 1 - d;
+                const u64 m = bin_mass(g, 31 - lane), x = r.warp_sums(m);
+                const u64 base = d ? s.before[d - 1] : 0;
+                const int l = __ffs(__ballot_sync(0xffffffffu, base + x >= need)) - 1;
+                const uint32_t bin = (uint32_t)(g * 32 + 31 - l);
+                if (lane == l) {
+                    s.key = bin;
+                    s.start = base + x - m;
+                    s.m = m;
+                    if (!F32) s.n = kept_of(bin, r.bin_count(g, 31 - l));
+                }
+            }
+            __syncthreads();
+            if (F32) {
+                const uint32_t upper = s.key;
+                const u64 start = s.start, m_bin = s.m;
+                __syncthreads();
+                lower_masses(upper);
+                // (the bin's weight was summed token by token, here value by value: the last units
+                // may differ)
+                const u64 have = s.before2[kGroups - 1];
+                if (have == 0) {  // weights too small for a unit each: the bin's first token
+                    uint32_t low, tie;
+                    kth(1, low, tie);
+                    c = Cut{upper << 16 | low, 1u};
+                    sum = start + m_bin;
+                    return;
+                }
+                const u64 rest = min(max(m_bin ? need - start : 1, (u64)1), have);
+                const int d2 = r.reach(s.before2, rest);
+                if (warp == 0) {
+                    const int g2 = kGroups - 1 - d2;
+                    const uint32_t key = upper << 16 | (uint32_t)(g2 * 32 + 31 - lane);
+                    const uint32_t n = kept_of(key, r.bin_count(g2, 31 - lane));
+                    const u64 m = n ? r.units(r.weight(key), n) : 0, x = r.warp_sums(m);
+                    const u64 base = d2 ? s.before2[d2 - 1] : 0;
+                    const int l = __ffs(__ballot_sync(0xffffffffu, base + x >= rest)) - 1;
+                    if (lane == l) {
+                        s.key = key;
+                        s.start = start + base + x - m;
+                        s.m = m;
+                        s.n = n;
+                        need = start + rest;
+                    }
+                    need = __shfl_sync(0xffffffffu, need, l);
+                }
+            }
+            if (tid < 32) __syncwarp();
+            if (tid == 0) {
+                // the first tie i of n with start + (i + 1) m / n at least need
+                const u64 m = s.m, n = s.n;
+                const u64 gap = need > s.start ? need - s.start : 1;
+                u64 i = m ? mul_div(gap, n, m) : 0;  // (i m >= gap n, or one short of it)
+                if (i > 0 && (unsigned __int128)i * m >= (unsigned __int128)gap * n) --i;
+                if (i > n - 1) i = n - 1;
+                s.n = (uint32_t)(i + 1);
+                s.start += mul_div(i + 1, m, n);
+            }
+            __syncthreads();
+            c.key = s.key;
+            c.ties = s.n;
+            sum = s.start;
+            __syncthreads();
+        };
+
+        Cut end = cut;  // what is kept in the end, and its weight
+        bool end_all = cut_all;
+        u64 kept = all;
+        if (top_p <= 0.f) {
+            end = Cut{key_max, 1u};
+            end_all = false;
+            kept = r.units(F2{1.f, 0.f}, 1u);
+        } else if (top_p < 1.f) {
+            const double x = (double)top_p * (double)all;
+            u64 need = (u64)ceil(x);
+            place(min(max(need, (u64)1), all), end, kept);
+            end_all = false;
+        }
+        if (min_p > 0.f) {
+            // the smallest key whose weight is at least min_p (the largest candidate's at any rate)
+            if (warp == 0) {
+                uint32_t lo = K::kLow, hi = key_max;
+                while (lo < hi) {
+                    const uint32_t step = max((hi - lo) / 32u, 1u);
+                    const uint32_t off = (uint32_t)(lane + 1) * step;
+                    bool ok = off <= hi - lo;
+                    if (ok) {
+                        const F2 w = r.weight(hi - off);
+                        ok = w.h > min_p || (w.h == min_p && w.l >= 0.f);
+                    }
+                    const unsigned bad = ~__ballot_sync(0xffffffffu, ok);
+                    const uint32_t n = bad ? (uint32_t)__ffs(bad) - 1 : 32u;
+                    const uint32_t past = (n + 1) * step;  // not ok there, or out of range
+                    if (n < 32 && past <= hi - lo) lo = hi - past + 1;
+                    hi -= n * step;
+                    if (step == 1 && n < 32) break;
+                }
+                if (lane == 0) s.key = hi;
+            }
+            __syncthreads();
+            const uint32_t floor_key = s.key;
+            __syncthreads();
+            if (end_all || floor_key > end.key) {
+                // everything from the floor up (its own tokens too, if there are any)
+                const uint32_t bin = F32 ? floor_key >> 16 : floor_key;
+                if (F32) lower_masses(bin);
+                if (warp == 0) {
+                    const int g = (int)(bin / 32), d = kGroups - 1 - g;
+                    const bool above = (uint32_t)(g * 32 + lane) > bin ||
+                                       (!F32 && (uint32_t)(g * 32 + lane) == bin);
+                    u64 m = r.warp_sums(above ? bin_mass(g, lane) : (u64)0);
+                    m = __shfl_sync(0xffffffffu, m, 31) + (d ? s.before[d - 1] : 0);
+                    if (F32) {
+                        const uint32_t low = floor_key & 0xffffu;
+                        const int g2 = (int)(low / 32), d2 = kGroups - 1 - g2;
+                        const uint32_t key = bin << 16 | (uint32_t)(g2 * 32 + lane);
+                        const uint32_t c = key >= floor_key ? r.bin_count(g2, lane) : 0u;
+                        const u64 x = r.warp_sums(c ? r.units(r.weight(key), c) : (u64)0);
+                        m += __shfl_sync(0xffffffffu, x, 31) + (d2 ? s.before2[d2 - 1] : 0);
+                    }
+                    if (lane == 0) s.m = m;
+                }
+                __syncthreads();
+                kept = min(s.m, all);
+                __syncthreads();
+                end_all = false;
+            }
+        }
+        Cut c;
+        u64 sum;
+        const u64 need = (u64)((double)u * (double)kept) + 1;  // the running weight passes u kept
+        place(min(need, kept), c, sum);
+        draw_key = c.key;
+        draw_tie = c.ties - 1;
+    }
+    if (F32) refine(draw_key >> 16);
+
+    // Which CTA's slice holds occurrence draw_tie of draw_key: every CTA reads the slices' counts.
+    const uint32_t bin = F32 ? draw_key & 0xffffu : draw_key;
+    uint32_t mine = 0, before = 0;
+    for (int q = 0; q < C; ++q) {
+        const uint32_t c = ld_peer(peer_addr(hist + (bin >> 1), q)) >> (16 * (bin & 1)) & 0xffffu;
+        if (q < rank) before += c;
+        if (q == rank) mine = c;
+    }
+    cluster_barrier();  // no CTA leaves while another reads its shared memory
+    if (draw_tie < before || draw_tie >= before + mine) return;
+    const uint32_t nth = draw_tie - before;
+    // that occurrence within the slice: contiguous pieces per thread, counted, then searched
+    const int n = (int)(r.i1 - r.i0), piece = (n + kThreads - 1) / kThreads;
+    const int a = min(tid * piece, n), b = min(a + piece, n);
+    const long long base = (long long)row * p.vocab + r.i0;
+    auto key_at = [&](int i) {
+        return K::of(F32 ? static_cast<const uint32_t*>(p.logits)[base + i]
+                         : static_cast<const uint16_t*>(p.logits)[base + i]);
+    };
+    uint32_t c = 0;
+    for (int i = a; i < b; ++i) c += key_at(i) == draw_key;
+    uint32_t x = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) s.upart[warp] = x;
+    __syncthreads();
+    uint32_t ex = x - c;
+    for (int w = 0; w < warp; ++w) ex += s.upart[w];
+    if (nth >= ex && nth < ex + c) {
+        uint32_t left = nth - ex;
+        for (int i = a; i < b; ++i)
+            if (key_at(i) == draw_key && left-- == 0) {
+                p.token[row] = (int32_t)(r.i0 + i);
+                break;
+            }
+    }
+}
+
+// CTAs per row: one for short rows; else 5 to 16 (so that the merged counts fit beside the
+// histogram and no slice exceeds a 16-bit counter), as many as give the batch the fewest rounds
+// of clusters weighed with the slice that a CTA counts.
+int row_ctas(int batch, int vocab, int n_sm) {
+    if (vocab <= 4096) return 1;
+    const int gpc = n_sm / 8 > 16 ? n_sm / 8 : 16;  // SMs that a cluster can share
+    int best = 0;
+    double best_cost = 0.0;
+    for (int c = 5; c <= kMaxCtas; ++c) {
+        if ((vocab + c - 1) / c > 65535) continue;
+        const int at_once = (gpc / c > 0 ? gpc / c : 1) * 8;
+        const double rounds = (batch + at_once - 1) / at_once;
+        const double cost = rounds * (8192.0 + (double)vocab / c);
+        if (!best || cost < best_cost) {
+            best = c;
+            best_cost = cost;
+        }
+    }
+    return best ? best : kMaxCtas;
+}
+
+template <bool F32>
+cudaError_t launch(const SampleParams& p, int C, cudaStream_t st) {
+    auto kernel = sample_kernel<F32>;
+    const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + kBins * 2 +
+                        (C > 1 ? (size_t)(kGroups + C - 1) / C * 32 * 4 : 0);
+    static std::atomic<bool> configured[64];  // per device; the same values every time
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+    if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_relaxed)) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             227 * 1024);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)p.batch * C);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see pdl_wait
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p, C);
+}
+
+}  // namespace
+
+size_t sample_workspace(int batch, int vocab, int fp32) {
+    (void)vocab;
+    return fp32 ? (size_t)batch * kBins * 8 : 0;
+}
+
+cudaError_t launch_sample(const SampleParams& p, int fp32, int n_sm, cudaStream_t st) {
+    const int C = row_ctas(p.batch, p.vocab, n_sm);
+    return fp32 ? launch<true>(p, C, st) : launch<false>(p, C, st);
+}
+
+}  // namespace gemma
