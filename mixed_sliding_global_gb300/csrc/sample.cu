@@ -81,9 +81,8 @@ __device__ __forceinline__ void st_peer(uint32_t addr, uint32_t v) {
 __device__ __forceinline__ void st_peer(uint32_t addr, unsigned long long v) {
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
-// Barrier of the cluster (of the CTA alone when it has one); also orders global memory.
+// Barrier of the row's CTAs, ordering their shared memory.
 __device__ __forceinline__ void cluster_barrier() {
-    __threadfence();
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
@@ -188,6 +187,8 @@ struct Shared {
     // kGroups - 1 - d), inclusive; fp32: the same over the lower halves of one upper half
     u64 before[kGroups], before2[kGroups];
     float2 exp2[64];
+    uint32_t mine[kGroups / 32], any[kGroups / 32];  // groups with counts: this CTA's, the row's
+    uint32_t live[kGroups / 32];                     // the row's, of whole numbers or upper halves
     u64 part[kWarps];
     uint32_t upart[kWarps];
     int top[kWarps];
@@ -310,16 +311,45 @@ struct Row {
     }
 
     // The row's counts: group sums into every CTA's s.count, bins into their owner's `merged`
-    // (group g belongs to CTA g % C). Needs every CTA's histogram, leaves them readable.
+    // (group g belongs to CTA g % C). Needs every CTA's histogram, leaves them readable. A row's
+    // values lie in a few hundred of the 2,048 groups, and a peer's shared memory gives only some
+    // 16 bytes a clock: the CTAs first exchange which groups they have, and read no others.
     __device__ void merge_counts() {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int g = h * kThreads + tid;
+            uint32_t has = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 v = reinterpret_cast<const uint4*>(hist)[g * 4 + i];
+                has |= v.x | v.y | v.z | v.w;
+            }
+            const unsigned word = __ballot_sync(0xffffffffu, has != 0);
+            if (lane == 0) s.mine[h * kWarps + warp] = word;
+            s.count[g] = 0;
+        }
+        if (tid < kGroups / 32) s.any[tid] = 0;
         cluster_barrier();
+        for (int i = tid; i < kGroups / 32 * C; i += kThreads) {
+            const uint32_t v = ld_peer(peer_addr(&s.mine[i & 63], i >> 6));
+            if (v) atomicOr(&s.any[i & 63], v);
+        }
+        __syncthreads();
         for (int k = warp; rank + k * C < kGroups; k += kWarps) {
             const int g = rank + k * C, w = g * 16 + (lane & 15);
+            if (!(s.any[g / 32] >> (g & 31) & 1u)) continue;
             uint32_t lo = 0, hi = 0;
-            for (int r = lane >> 4; r < C; r += 2) {
-                const uint32_t v = ld_peer(peer_addr(hist + w, r));
-                lo += v & 0xffffu;
-                hi += v >> 16;
+            // (all loads in flight at once: a peer's memory is a few hundred ns away)
+            uint32_t v[kMaxCtas / 2];
+#pragma unroll
+            for (int i = 0; i < kMaxCtas / 2; ++i) {
+                const int r = 2 * i + (lane >> 4);
+                v[i] = r < C ? ld_peer(peer_addr(hist + w, r)) : 0u;
+            }
+#pragma unroll
+            for (int i = 0; i < kMaxCtas / 2; ++i) {
+                lo += v[i] & 0xffffu;
+                hi += v[i] >> 16;
             }
             lo += __shfl_xor_sync(0xffffffffu, lo, 16);
             hi += __shfl_xor_sync(0xffffffffu, hi, 16);
@@ -332,6 +362,7 @@ struct Row {
     }
     // count of bin 32 g + i (any CTA's)
     __device__ uint32_t bin_count(int g, int i) const {
+        if (s.count[g] == 0) return 0;
         if (C == 1) return hist[g * 16 + (i >> 1)] >> (16 * (i & 1)) & 0xffffu;
         return ld_peer(peer_addr(merged + (g / C) * 32 + i, g % C));
     }
@@ -346,15 +377,21 @@ struct Row {
         }
         return x;
     }
+    // Sum of the values of the CTA's threads before this one.
+    template <class T>
+    __device__ T sum_before(T v) {
+        const T x = warp_sums(v);
+        __syncthreads();  // (s.part may still be read)
+        if (lane == 31) s.part[warp] = x;
+        __syncthreads();
+        const T all = warp_sums((T)s.part[lane]);
+        const T base = __shfl_sync(0xffffffffu, all, (warp + 31) & 31);
+        return (warp ? base : (T)0) + x - v;
+    }
     // Weights per group to running sums, in place.
     __device__ void running_sums(u64* before) {
         const u64 a = before[kGroups - 1 - 2 * tid], b = before[kGroups - 2 - 2 * tid];
-        const u64 x = warp_sums(a + b);
-        __syncthreads();
-        if (lane == 31) s.part[warp] = x;
-        __syncthreads();
-        u64 base = x - a - b;
-        for (int w = 0; w < warp; ++w) base += s.part[w];
+        const u64 base = sum_before(a + b);
         before[2 * tid] = base + a;
         before[2 * tid + 1] = base + a + b;
         __syncthreads();
@@ -393,14 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
     const float top_p = p.top_p ? p.top_p[row] : 1.f;
     const float min_p = p.min_p ? p.min_p[row] : 0.f;
     const float u = p.uniform[row];
-    const bool good = t >= 0.f && isfinite(t) && top_p == top_p && min_p == min_p && u >= 0.f && u < 1.f;
-    if (!good) {
-        if (rank == 0 && tid == 0) {
-            p.token[row] = -1;
-            report(p.err, GEMMA_DEVERR_SAMPLE);
-        }
-        return;
-    }
+
     Row<F32> r{p, s, hist, hist + kBins / 2, C, rank, row};
     const long long per = (p.vocab + C - 1) / C;
     r.i0 = min((long long)rank * per, (long long)p.vocab);
@@ -409,13 +439,24 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
     r.warp = warp;
     r.lane = lane;
     if (tid < 64) s.exp2[tid] = c_exp2[tid];
+    s.before[tid] = s.before[tid + kThreads] = 0;
     // fp32: this CTA's share of the row's weight sums starts at zero
     u64* mass = F32 ? p.mass + (size_t)row * kBins : nullptr;
     if (F32)
         for (int i = rank * kThreads + tid; i < kBins; i += C * kThreads) mass[i] = 0ull;
+    if (F32) __threadfence();
 
     r.count_slice(0, 0);
     r.merge_counts();
+    const bool good = t >= 0.f && isfinite(t) && top_p == top_p && min_p == min_p && u >= 0.f && u < 1.f;
+    if (!good) {
+        if (rank == 0 && tid == 0) {
+            p.token[row] = -1;
+            report(p.err, GEMMA_DEVERR_SAMPLE);
+        }
+        cluster_barrier();  // no CTA leaves while another reads its counts
+        return;
+    }
 
     // the largest candidate and the number of them
     uint32_t total = 0;
@@ -423,16 +464,15 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
     {
         const uint32_t a = s.count[2 * tid], b = s.count[2 * tid + 1];
         const uint32_t sum = __reduce_add_sync(0xffffffffu, a + b);
+        if (tid < kGroups / 32) s.live[tid] = s.any[tid];
         const int hi = __reduce_max_sync(0xffffffffu, b ? 2 * tid + 1 : a ? 2 * tid : -1);
         if (lane == 0) {
             s.upart[warp] = sum;
             s.top[warp] = hi;
         }
         __syncthreads();
-        for (int w = 0; w < kWarps; ++w) {
-            total += s.upart[w];
-            top = max(top, s.top[w]);
-        }
+        total = __reduce_add_sync(0xffffffffu, s.upart[lane]);
+        top = __reduce_max_sync(0xffffffffu, s.top[lane]);
         __syncthreads();
     }
     if (total == 0) {
@@ -455,6 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
     auto refine = [&](uint32_t upper) {
         if (at == upper) return;
         cluster_barrier();  // (peers may still read the counts)
+        s.before2[tid] = s.before2[tid + kThreads] = 0;
         r.count_slice(1, upper);
         r.merge_counts();
         at = upper;
@@ -466,11 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
     // the n-th candidate from the highest down, by counts
     auto kth = [&](uint32_t n, uint32_t& bin, uint32_t& ties) {
         const uint32_t a = s.count[kGroups - 1 - 2 * tid], b = s.count[kGroups - 2 - 2 * tid];
-        const uint32_t x = r.warp_sums(a + b);
-        if (lane == 31) s.upart[warp] = x;
-        __syncthreads();
-        uint32_t ex = x - a - b;
-        for (int w = 0; w < warp; ++w) ex += s.upart[w];
+        const uint32_t ex = r.sum_before(a + b);
         if (ex < n && ex + a >= n) {
             s.key = kGroups - 1 - 2 * tid;
             s.n = n - ex;
@@ -497,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
         const int hi = __reduce_max_sync(0xffffffffu, b ? 2 * tid + 1 : a ? 2 * tid : -1);
         if (lane == 0) s.top[warp] = hi;
         __syncthreads();
-        for (int w = 0; w < kWarps; ++w) g2 = max(g2, s.top[w]);
+        g2 = __reduce_max_sync(0xffffffffu, s.top[lane]);
         __syncthreads();
         key_max = bin_max << 16 | top_bin(g2);
     }
@@ -538,13 +575,11 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
             if (lower_of == upper) return;
             for (int q = warp; rank + q * C < kGroups; q += kWarps) {
                 const int g = rank + q * C;
-                u64 m = 0;
-                if (s.count[g]) {
-                    const uint32_t key = upper << 16 | (uint32_t)(g * 32 + lane);
-                    const uint32_t n = kept_of(key, r.bin_count(g, lane));
-                    if (n) m = r.units(r.weight(key), n);
-                    m = __shfl_sync(0xffffffffu, r.warp_sums(m), 31);
-                }
+                if (s.count[g] == 0) continue;
+                const uint32_t key = upper << 16 | (uint32_t)(g * 32 + lane);
+                const uint32_t n = kept_of(key, r.bin_count(g, lane));
+                u64 m = n ? r.units(r.weight(key), n) : 0;
+                m = __shfl_sync(0xffffffffu, r.warp_sums(m), 31);
                 if (lane < C) st_peer(peer_addr(&s.before2[g], lane), m);
             }
             cluster_barrier();
@@ -572,6 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
             };
             r.for_slice([&](uint4 v) { add(v.x); add(v.y); add(v.z); add(v.w); },
                         [&](uint32_t bits) { add(bits); });
+            __threadfence();  // (the sums lie in global memory)
             cluster_barrier();
         }
         // kept weight of a bin
@@ -594,12 +630,10 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
         };
         for (int q = warp; rank + q * C < kGroups; q += kWarps) {
             const int g = rank + q * C;
-            u64 m = 0;
-            if (g * 32u <= bin_max && (F32 || s.count[g])) {
-                m = bin_mass(g, lane);
-                if (__any_sync(0xffffffffu, m != 0))
-                    m = __shfl_sync(0xffffffffu, r.warp_sums(m), 31);
-            }
+            if (!(s.live[g / 32] >> (g & 31) & 1u)) continue;
+            u64 m = bin_mass(g, lane);
+            if (!__any_sync(0xffffffffu, m != 0)) continue;
+            m = __shfl_sync(0xffffffffu, r.warp_sums(m), 31);
             if (lane < C) st_peer(peer_addr(&s.before[g], lane), m);
         }
         cluster_barrier();
@@ -663,11 +697,14 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
                 // the first tie i of n with start + (i + 1) m / n at least need
                 const u64 m = s.m, n = s.n;
                 const u64 gap = need > s.start ? need - s.start : 1;
-                u64 i = m ? mul_div(gap, n, m) : 0;  // (i m >= gap n, or one short of it)
-                if (i > 0 && (unsigned __int128)i * m >= (unsigned __int128)gap * n) --i;
-                if (i > n - 1) i = n - 1;
+                u64 i = 0;
+                if (n > 1 && m) {
+                    i = mul_div(gap, n, m);
+                    if (i > 0 && (unsigned __int128)i * m >= (unsigned __int128)gap * n) --i;
+                    if (i > n - 1) i = n - 1;
+                }
                 s.n = (uint32_t)(i + 1);
-                s.start += mul_div(i + 1, m, n);
+                s.start += i + 1 == n ? m : mul_div(i + 1, m, n);
             }
             __syncthreads();
             c.key = s.key;
@@ -768,17 +805,9 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
                          : static_cast<const uint16_t*>(p.logits)[base + i]);
     };
     uint32_t c = 0;
+#pragma unroll 8
     for (int i = a; i < b; ++i) c += key_at(i) == draw_key;
-    uint32_t x = c;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
-    }
-    if (lane == 31) s.upart[warp] = x;
-    __syncthreads();
-    uint32_t ex = x - c;
-    for (int w = 0; w < warp; ++w) ex += s.upart[w];
+    const uint32_t ex = r.sum_before(c);
     if (nth >= ex && nth < ex + c) {
         uint32_t left = nth - ex;
         for (int i = a; i < b; ++i)
