@@ -34,6 +34,9 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 65536, kGroups = 2048;  // 32 bins per group
 constexpr int kMaxCtas = 16;
+// The short list: rows with a top_k up to kListK (and fp32 rows without one) are drawn from their
+// kListK (top_k) largest logits alone; a CTA lists at most kListCap of its slice.
+constexpr uint32_t kListK = 256, kListCap = 1024;
 
 // Order-preserving key of a number (-0 as +0), its inverse, and the candidates' range of keys:
 // above -inf, not above +inf.
@@ -194,6 +197,11 @@ struct Shared {
     int top[kWarps];
     uint32_t found, key, n;
     u64 m, start;
+    // short list: digits of a selection; a CTA's entries, whether they are all it has, its largest
+    // key and its sum of weights; rank 0's verdict
+    uint32_t digit[256];
+    uint32_t n_list, whole, largest, fits;
+    u64 sum;
 };
 
 template <bool F32>
@@ -287,6 +295,11 @@ struct Row {
     // Calls vec for every aligned 16 bytes of the slice and one for the elements around them.
     template <class V, class O>
     __device__ void for_slice(V vec, O one) {
+        for_slice_at([&](uint4 v, long long) { vec(v); }, [&](uint32_t u, long long) { one(u); });
+    }
+    // The same, with the (first) element's index in the row.
+    template <class V, class O>
+    __device__ void for_slice_at(V vec, O one) {
         constexpr int E = F32 ? 4 : 8;
         const long long base = (long long)row * p.vocab;
         const long long b0 = base + i0, b1 = base + i1;
@@ -295,7 +308,7 @@ struct Row {
             return F32 ? static_cast<const uint32_t*>(p.logits)[i]
                        : static_cast<const uint16_t*>(p.logits)[i];
         };
-        for (long long i = b0 + tid; i < a0; i += kThreads) one(load1(i));
+        for (long long i = b0 + tid; i < a0; i += kThreads) one(load1(i), i - base);
         const uint4* v = reinterpret_cast<const uint4*>(p.logits) + a0 / E;
         const int n = (int)((a1 - a0) / E);
         int i = tid;
@@ -304,10 +317,280 @@ struct Row {
 #pragma unroll
             for (int k = 0; k < 4; ++k) x[k] = v[i + k * kThreads];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) vec(x[k]);
+            for (int k = 0; k < 4; ++k)
+                vec(x[k], a0 - base + (long long)(i + k * kThreads) * E);
         }
-        for (; i < n; i += kThreads) vec(v[i]);
-        for (long long j = a1 + tid; j < b1; j += kThreads) one(load1(j));
+        for (; i < n; i += kThreads) vec(v[i], a0 - base + (long long)i * E);
+        for (long long j = a1 + tid; j < b1; j += kThreads) one(load1(j), j - base);
+    }
+
+    // The largest key of this thread's part of the slice (0 if it has no candidate).
+    __device__ uint32_t thread_max() {
+        uint32_t best = 0;
+        for_slice([&](uint4 v) {
+            uint32_t m;
+            if (F32) {
+                m = __float_as_uint(fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
+                                          fmaxf(__uint_as_float(v.z), __uint_as_float(v.w))));
+            } else {
+                m = vec_max(v);
+            }
+            m = K::of(m);
+            if (m <= K::kInf) best = max(best, m);
+        }, [&](uint32_t u) {
+            const uint32_t key = K::of(u);
+            if (key <= K::kInf) best = max(best, key);
+        });
+        return best >= K::kLow ? best : 0;
+    }
+    // Largest of eight bf16 (NaN only if all are), as bits.
+    __device__ static uint32_t vec_max(const uint4& v) {
+        uint32_t m;
+        asm("{\n\t.reg .b32 a, b;\n\tmax.bf16x2 a, %1, %2;\n\tmax.bf16x2 b, %3, %4;\n\t"
+            "max.bf16x2 %0, a, b;\n\t}"
+            : "=r"(m)
+            : "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
+        const float f = fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+        return __float_as_uint(f) >> 16;
+    }
+    // The n-th largest of the keys that each(f) hands to f (0 ones do not count), 0 if there are
+    // fewer: eight bits at a time by counting.
+    template <class Each>
+    __device__ uint32_t select(uint32_t n, Each each) {
+        uint32_t prefix = 0, mask = 0;
+#pragma unroll 1
+        for (int shift = F32 ? 24 : 8; shift >= 0; shift -= 8) {
+            if (tid < 256) s.digit[tid] = 0;
+            __syncthreads();
+            each([&](uint32_t key) {
+                if (key && (key & mask) == prefix) atomicAdd(&s.digit[key >> shift & 255u], 1u);
+            });
+            __syncthreads();
+            // lane i: digits 255 - 8 i down
+            uint32_t c[8], sum = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) sum += c[j] = s.digit[255 - 8 * lane - j];
+            const uint32_t upto = warp_sums(sum);
+            const unsigned hit = __ballot_sync(0xffffffffu, upto >= n);
+            if (!hit) return 0;  // (only at the first digit)
+            const int l = __ffs(hit) - 1;
+            uint32_t left = n - (upto - sum), d = 0;
+            bool open = true;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (open && left <= c[j]) {
+                    d = 255 - 8 * lane - j;
+                    open = false;
+                } else if (open) {
+                    left -= c[j];
+                }
+            }
+            prefix |= __shfl_sync(0xffffffffu, d, l) << shift;
+            n = __shfl_sync(0xffffffffu, left, l);
+            mask |= 255u << shift;
+            __syncthreads();
+        }
+        return prefix;
+    }
+
+    // Draw from the row's n largest logits: true if that decided the row (token written). Every CTA
+    // lists what of its slice can be among them, the first one orders the lists' n largest and
+    // walks down their running weights. Without a top_k the sum of all weights is needed too (one
+    // evaluation per logit), and the draw may lie beyond the list, as may its entries beyond
+    // kListCap: then the row goes the long way.
+    __device__ bool draw_from_list(uint32_t n, bool filter_k, float top_p, float min_p, float u) {
+        u64* list = reinterpret_cast<u64*>(merged);
+        const uint32_t best = thread_max();
+        const uint32_t pivot = select(n, [&](auto f) { f(best); });
+        if (tid == 0) s.n_list = 0;
+        const uint32_t mx = __reduce_max_sync(0xffffffffu, best);
+        if (lane == 0) s.upart[warp] = mx;
+        __syncthreads();
+        const uint32_t floor_key = max(pivot, K::kLow);
+        auto take = [&](uint32_t bits, long long at) {
+            const uint32_t key = K::of(bits);
+            if (key < floor_key || key > K::kInf) return;
+            const uint32_t i = atomicAdd(&s.n_list, 1u);
+            // falling keys, then rising indices
+            if (i < kListCap) list[i] = (u64)key << 32 | (0xffffffffu - (uint32_t)at);
+        };
+        for_slice_at([&](uint4 v, long long at) {
+            if (F32) {
+                take(v.x, at);
+                take(v.y, at + 1);
+                take(v.z, at + 2);
+                take(v.w, at + 3);
+            } else {
+                const uint32_t m = K::of(vec_max(v));
+                if (m < floor_key || m > K::kInf) return;
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    take(w[k] & 0xffffu, at + 2 * k);
+                    take(w[k] >> 16, at + 2 * k + 1);
+                }
+            }
+        }, take);
+        if (warp == 0) {
+            const uint32_t m = __reduce_max_sync(0xffffffffu, s.upart[lane]);
+            if (lane == 0) {
+                s.largest = m;
+                s.whole = pivot == 0;
+            }
+        }
+        __syncthreads();
+        cluster_barrier();
+        uint32_t counts = 0, lg = 0, all_whole = 1;
+        if (lane < C) {
+            counts = ld_peer(peer_addr(&s.n_list, lane));
+            lg = ld_peer(peer_addr(&s.largest, lane));
+            all_whole = ld_peer(peer_addr(&s.whole, lane));
+        }
+        const bool over = __any_sync(0xffffffffu, counts > kListCap);
+        const bool whole = __all_sync(0xffffffffu, all_whole);
+        key_max = __reduce_max_sync(0xffffffffu, lg);
+        const uint32_t ends = warp_sums(counts);  // of lane's list among all
+        const uint32_t total = __shfl_sync(0xffffffffu, ends, 31);
+        if (over) return false;  // (the same in every CTA)
+        if (total == 0) {
+            if (rank == 0 && tid == 0) {
+                p.token[row] = -1;
+                report(p.err, GEMMA_DEVERR_SAMPLE);
+            }
+            cluster_barrier();  // no CTA leaves while another reads its shared memory
+            return true;
+        }
+        zmax = capped(K::value(key_max));
+        u64 all = 0;
+        const bool need_sum = !filter_k && !(whole && total <= n);
+        if (need_sum) {
+            u64 mine = 0;
+            auto add = [&](uint32_t bits) {
+                const uint32_t key = K::of(bits);
+                if (key >= K::kLow && key <= K::kInf) mine += units(weight(key), 1u);
+            };
+            for_slice([&](uint4 v) {
+                if (F32) {
+                    add(v.x);
+                    add(v.y);
+                    add(v.z);
+                    add(v.w);
+                }
+            }, add);
+            const u64 b = sum_before(mine);
+            if (tid == kThreads - 1) s.sum = b + mine;
+            __syncthreads();
+            cluster_barrier();
+            if (rank == 0)
+                for (int q = 0; q < C; ++q) {
+                    const uint32_t a = peer_addr(&s.sum, q);
+                    all += ld_peer(a) | (u64)ld_peer(a + 4) << 32;
+                }
+        }
+        if (rank == 0) {
+            u64* pool = reinterpret_cast<u64*>(hist);
+            for (int q = 0; q < C; ++q) {
+                const uint32_t e = __shfl_sync(0xffffffffu, ends, q);
+                const uint32_t c = __shfl_sync(0xffffffffu, counts, q);
+                const uint32_t a = peer_addr(list, q);
+                for (uint32_t i = tid; i < c; i += kThreads)
+                    pool[e - c + i] = ld_peer(a + 8 * i) | (u64)ld_peer(a + 8 * i + 4) << 32;
+            }
+            if (tid == 0) s.n_list = 0;
+            __syncthreads();
+            const uint32_t kth = select(min(n, total), [&](auto f) {
+                for (uint32_t i = tid; i < total; i += kThreads) f((uint32_t)(pool[i] >> 32));
+            });
+            u64* few = s.before;    // entries at and above the n-th key, in any order
+            u64* order = s.before2; // and the n largest in theirs
+            for (uint32_t i = tid; i < total; i += kThreads) {
+                const u64 e = pool[i];
+                if ((uint32_t)(e >> 32) >= kth) {
+                    const uint32_t at = atomicAdd(&s.n_list, 1u);
+                    if (at < kThreads) few[at] = e;
+                }
+            }
+            __syncthreads();
+            const uint32_t n_few = s.n_list, kept_n = min(n, total);
+            bool fits = n_few <= kThreads;
+            if (fits) {
+                if (tid < n_few) {
+                    const u64 e = few[tid];
+                    uint32_t before = 0;
+#pragma unroll 8
+                    for (uint32_t i = 0; i < n_few; ++i) before += few[i] > e;
+                    if (before < kept_n) order[before] = e;
+                }
+                __syncthreads();
+                const u64 e = tid < kept_n ? order[tid] : 0;
+                const uint32_t key = (uint32_t)(e >> 32);
+                const F2 w = tid < kept_n ? weight(key) : F2{0.f, 0.f};
+                const u64 m = tid < kept_n ? units(w, 1u) : 0;
+                const u64 run = sum_before(m) + m;
+                if (!need_sum) {
+                    if (tid == kThreads - 1) s.sum = run;
+                    __syncthreads();
+                    all = s.sum;
+                }
+                // how many entries are kept, and their weight; beyond: not decided by the list
+                uint32_t keep = kept_n;
+                bool open = need_sum;  // what is kept reaches beyond the list
+                u64 kept = all;
+                auto first = [&](bool yes) {  // lowest thread that says yes, or kThreads
+                    const unsigned b = __ballot_sync(0xffffffffu, yes);
+                    __syncthreads();
+                    if (lane == 0) s.upart[warp] = b ? warp * 32 + __ffs(b) - 1 : kThreads;
+                    __syncthreads();
+                    return __reduce_min_sync(0xffffffffu, s.upart[lane]);
+                };
+                auto sum_at = [&](uint32_t i) {
+                    __syncthreads();
+                    if (tid == i) s.sum = run;
+                    __syncthreads();
+                    return s.sum;
+                };
+                if (top_p <= 0.f) {
+                    keep = 1;
+                    open = false;
+                    kept = sum_at(0);
+                } else if (top_p < 1.f) {
+                    const u64 need = min(max((u64)ceil((double)top_p * (double)all), (u64)1), all);
+                    const uint32_t i = first(run >= need);
+                    if (i < kept_n) {
+                        keep = i + 1;
+                        open = false;
+                        kept = sum_at(i);
+                    } else {
+                        fits = false;
+                    }
+                }
+                if (min_p > 0.f) {
+                    const bool low = tid < kept_n && key != key_max &&
+                                     !(w.h > min_p || (w.h == min_p && w.l >= 0.f));
+                    const uint32_t i = first(low);
+                    if (i < keep) {
+                        keep = i;
+                        open = false;
+                        kept = sum_at(i - 1);
+                        fits = true;  // (whatever top_p left undecided lies below the floor)
+                    } else if (open) {
+                        fits = false;
+                    }
+                }
+                if (fits) {
+                    const u64 need = min((u64)((double)u * (double)kept) + 1, kept);
+                    const uint32_t i = first(run >= need);
+                    if (i >= kept_n) fits = false;
+                    else if (tid == i) p.token[row] = (int32_t)(0xffffffffu - (uint32_t)e);
+                }
+            }
+            if (tid == 0) s.fits = fits;
+            __syncthreads();
+        }
+        cluster_barrier();
+        const bool decided = ld_peer(peer_addr(&s.fits, 0)) != 0;
+        cluster_barrier();  // (the long way, or the end: nobody reads this CTA's list any more)
+        return decided;
     }
 
     // The row's counts: group sums into every CTA's s.count, bins into their owner's `merged`
@@ -439,6 +722,19 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
     r.warp = warp;
     r.lane = lane;
     if (tid < 64) s.exp2[tid] = c_exp2[tid];
+    const bool good = t >= 0.f && isfinite(t) && top_p == top_p && min_p == min_p && u >= 0.f && u < 1.f;
+    if (!good) {  // the same in every CTA of the row
+        if (rank == 0 && tid == 0) {
+            p.token[row] = -1;
+            report(p.err, GEMMA_DEVERR_SAMPLE);
+        }
+        return;
+    }
+    r.inv_t = t > 0.f ? F2{1.f, 0.f} / F2{t, 0.f} : F2{0.f, 0.f};
+    const uint32_t n_top = t == 0.f ? 1u : want_k > 0 ? (uint32_t)want_k : 0u;
+    if (n_top ? n_top <= kListK : F32)
+        if (r.draw_from_list(n_top ? n_top : kListK, n_top > 0, top_p, min_p, u)) return;
+
     s.before[tid] = s.before[tid + kThreads] = 0;
     // fp32: this CTA's share of the row's weight sums starts at zero
     u64* mass = F32 ? p.mass + (size_t)row * kBins : nullptr;
@@ -448,15 +744,6 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
 
     r.count_slice(0, 0);
     r.merge_counts();
-    const bool good = t >= 0.f && isfinite(t) && top_p == top_p && min_p == min_p && u >= 0.f && u < 1.f;
-    if (!good) {
-        if (rank == 0 && tid == 0) {
-            p.token[row] = -1;
-            report(p.err, GEMMA_DEVERR_SAMPLE);
-        }
-        cluster_barrier();  // no CTA leaves while another reads its counts
-        return;
-    }
 
     // the largest candidate and the number of them
     uint32_t total = 0;
@@ -540,7 +827,6 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
     }
     r.key_max = key_max;
     r.zmax = r.capped(K::value(key_max));
-    r.inv_t = t > 0.f ? F2{1.f, 0.f} / F2{t, 0.f} : F2{0.f, 0.f};
 
     uint32_t draw_key = key_max, draw_tie = 0;
     if (!greedy) {
@@ -843,7 +1129,7 @@ template <bool F32>
 cudaError_t launch(const SampleParams& p, int C, cudaStream_t st) {
     auto kernel = sample_kernel<F32>;
     const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + kBins * 2 +
-                        (C > 1 ? (size_t)(kGroups + C - 1) / C * 32 * 4 : 0);
+                        (C > 1 ? (size_t)(kGroups + C - 1) / C * 32 * 4 : kListCap * 8);
     static std::atomic<bool> configured[64];  // per device; the same values every time
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
