@@ -34,9 +34,6 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 65536, kGroups = 2048;  // 32 bins per group
 constexpr int kMaxCtas = 16;
-// The short list: rows with a top_k up to kListK (and fp32 rows without one) are drawn from their
-// kListK (top_k) largest logits alone; a CTA lists at most kListCap of its slice.
-constexpr uint32_t kListK = 256, kListCap = 1024;
 
 // Order-preserving key of a number (-0 as +0), its inverse, and the candidates' range of keys:
 // above -inf, not above +inf.
@@ -115,12 +112,15 @@ __device__ __forceinline__ F2 operator*(F2 a, F2 b) {
     return fast_sum(m, __fmaf_rn(a.l, b.h, e));
 }
 __device__ __forceinline__ F2 operator/(F2 a, F2 b) {
-    const float q = __fdiv_rn(a.h, b.h);
-    const F2 r = a + F2{-q, 0.f} * b;
-    const float q2 = __fdiv_rn(r.h, b.h);
-    const F2 r2 = r + F2{-q2, 0.f} * b;
+    // quotient digits from one approximate reciprocal, each correcting what the ones before left
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(b.h));
+    const float q = __fmul_rn(a.h, r);
+    const F2 d = a + F2{-q, 0.f} * b;
+    const float q2 = __fmul_rn(d.h, r);
+    const F2 d2 = d + F2{-q2, 0.f} * b;
     const F2 t = fast_sum(q, q2);
-    return fast_sum(t.h, __fadd_rn(t.l, __fdiv_rn(r2.h, b.h)));
+    return fast_sum(t.h, __fadd_rn(t.l, __fmul_rn(d2.h, r)));
 }
 
 // 2^(i / 64) as such sums.
@@ -197,33 +197,41 @@ struct Shared {
     int top[kWarps];
     uint32_t found, key, n;
     u64 m, start;
-    // short list: digits of a selection; a CTA's entries, whether they are all it has, its largest
-    // key and its sum of weights; rank 0's verdict
-    uint32_t digit[256];
-    uint32_t n_list, whole, largest, fits;
-    u64 sum;
 };
 
-template <bool F32>
-struct Row {
+// A CTA's slice of a row's logits, and the row's weights. T threads.
+template <bool F32, int T>
+struct Slice {
     const SampleParams& p;
-    Shared& s;
-    uint32_t* hist;   // [kBins / 2] pairs of 16-bit counters
-    uint32_t* merged; // [groups of this CTA][32] counts of the whole row (more than one CTA)
+    const float2* exp2;  // shared copy of c_exp2
+    u64* part;           // shared, one per warp
     int C, rank, row;
-    long long i0, i1; // this CTA's slice
+    long long i0, i1;
     F2 inv_t, zmax;
-    uint32_t key_max; // key of the largest candidate
+    uint32_t key_max;    // key of the row's largest candidate
     int tid, warp, lane;
 
     using K = Key<F32>;
+
+    __device__ Slice(const SampleParams& p_, float2* exp2_, u64* part_, int C_)
+        : p(p_), exp2(exp2_), part(part_), C(C_) {
+        tid = threadIdx.x;
+        warp = tid >> 5;
+        lane = tid & 31;
+        row = blockIdx.x / C;
+        rank = blockIdx.x - row * C;
+        const long long per = (p.vocab + C - 1) / C;
+        i0 = min((long long)rank * per, (long long)p.vocab);
+        i1 = min(i0 + per, (long long)p.vocab);
+        for (int i = tid; i < 64; i += T) exp2_[i] = c_exp2[i];
+    }
 
     // z of a logit: c tanh(x / c) = +-c (1 - e) / (1 + e), e = exp(-2 |x| / c)
     __device__ F2 capped(float x) const {
         if (!(p.softcap > 0.f)) return F2{x, 0.f};
         const F2 c{p.softcap, 0.f};
         const float a = fabsf(x);
-        const F2 e = exp_f2(F2{-2.f * a, 0.f} / c, s.exp2);
+        const F2 e = exp_f2(F2{-2.f * a, 0.f} / c, exp2);
         F2 t = (F2{1.f, 0.f} + F2{-e.h, -e.l}) / (F2{1.f, 0.f} + e);
         if (isinf(x)) t = F2{1.f, 0.f};
         t = t * c;
@@ -235,7 +243,7 @@ struct Row {
         if (isinf(top.h)) return F2{isinf(z.h) && z.h > 0.f ? 1.f : 0.f, 0.f};
         if (d.h == 0.f) return F2{1.f, 0.f};
         if (!(d.h > -1e30f)) return F2{0.f, 0.f};
-        return exp_f2(d * inv_t, s.exp2);
+        return exp_f2(d * inv_t, exp2);
     }
     __device__ F2 weight(uint32_t key) const {
         return key == key_max ? F2{1.f, 0.f} : relative(capped(K::value(key)), zmax);
@@ -246,6 +254,347 @@ struct Row {
         const F2 m = w * F2{(float)n, 0.f};  // n < 2^24: exact
         return (u64)(__float2ll_rn(m.h * 0x1p43f) + __float2ll_rn(m.l * 0x1p43f));
     }
+
+    // Calls vec for every aligned 16 bytes of the slice and one for the elements around them.
+    template <class V, class O>
+    __device__ void for_slice(V vec, O one) {
+        for_slice_at([&](uint4 v, long long) { vec(v); }, [&](uint32_t u, long long) { one(u); });
+    }
+    // The same, with the (first) element's index in the row.
+    template <class V, class O>
+    __device__ void for_slice_at(V vec, O one) {
+        constexpr int E = F32 ? 4 : 8;
+        const long long base = (long long)row * p.vocab;
+        const long long b0 = base + i0, b1 = base + i1;
+        const long long a0 = min((b0 + E - 1) / E * E, b1), a1 = max(b1 / E * E, a0);
+        auto load1 = [&](long long i) -> uint32_t {
+            return F32 ? static_cast<const uint32_t*>(p.logits)[i]
+                       : static_cast<const uint16_t*>(p.logits)[i];
+        };
+        for (long long i = b0 + tid; i < a0; i += T) one(load1(i), i - base);
+        const uint4* v = reinterpret_cast<const uint4*>(p.logits) + a0 / E;
+        const int n = (int)((a1 - a0) / E);
+        int i = tid;
+        for (; i + 3 * T < n; i += 4 * T) {
+            uint4 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = v[i + k * T];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                vec(x[k], a0 - base + (long long)(i + k * T) * E);
+        }
+        for (; i < n; i += T) vec(v[i], a0 - base + (long long)i * E);
+        for (long long j = a1 + tid; j < b1; j += T) one(load1(j), j - base);
+    }
+
+    // The largest key of this thread's part of the slice (0 if it has no candidate).
+    __device__ uint32_t thread_max() {
+        uint32_t best = 0;
+        for_slice([&](uint4 v) {
+            uint32_t m;
+            if (F32) {
+                m = __float_as_uint(fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
+                                          fmaxf(__uint_as_float(v.z), __uint_as_float(v.w))));
+            } else {
+                m = vec_max(v);
+            }
+            m = K::of(m);
+            if (m <= K::kInf) best = max(best, m);
+        }, [&](uint32_t u) {
+            const uint32_t key = K::of(u);
+            if (key <= K::kInf) best = max(best, key);
+        });
+        return best >= K::kLow ? best : 0;
+    }
+    // Largest of eight bf16 (NaN only if all are), as bits.
+    __device__ static uint32_t vec_max(const uint4& v) {
+        uint32_t m;
+        asm("{\n\t.reg .b32 a, b;\n\tmax.bf16x2 a, %1, %2;\n\tmax.bf16x2 b, %3, %4;\n\t"
+            "max.bf16x2 %0, a, b;\n\t}"
+            : "=r"(m)
+            : "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
+        const float f = fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+        return __float_as_uint(f) >> 16;
+    }
+    // Inclusive sums over the warp's lanes.
+    template <class N>
+    __device__ N warp_sums(N x) const {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const N y = __shfl_up_sync(0xffffffffu, x, o);
+            if (lane >= o) x += y;
+        }
+        return x;
+    }
+    // Sum of the values of the CTA's threads before this one.
+    template <class N>
+    __device__ N sum_before(N v) {
+        const N x = warp_sums(v);
+        __syncthreads();  // (`part` may still be read)
+        if (lane == 31) part[warp] = x;
+        __syncthreads();
+        const N all = warp_sums(lane < T / 32 ? (N)part[lane] : (N)0);
+        const N base = __shfl_sync(0xffffffffu, all, (warp + 31) & 31);
+        return (warp ? base : (N)0) + x - v;
+    }
+};
+
+// The parameters of a row; false if they are out of range.
+struct Filters {
+    float t, top_p, min_p, u;
+    int top_k;
+    __device__ bool load(const SampleParams& p, int row) {
+        t = p.temperature ? p.temperature[row] : 1.f;
+        top_k = p.top_k ? p.top_k[row] : 0;
+        top_p = p.top_p ? p.top_p[row] : 1.f;
+        min_p = p.min_p ? p.min_p[row] : 0.f;
+        u = p.uniform[row];
+        return t >= 0.f && isfinite(t) && top_p == top_p && min_p == min_p && u >= 0.f && u < 1.f;
+    }
+    __device__ F2 inverse_t() const {
+        return t > 0.f ? F2{1.f, 0.f} / F2{t, 0.f} : F2{0.f, 0.f};
+    }
+};
+
+// The short list. A row with a top_k up to kListK, and an fp32 row without one, is drawn from its
+// n = top_k (kListK) largest logits alone. The n-th largest of a CTA's threads' largest keys bounds
+// the row's n-th largest logit from below, and so does the smallest over the CTAs of each one's
+// (n / C)-th: every CTA sends its slice's keys down to the higher of these bounds to the first one,
+// which orders them and walks down their running weights. Without a top_k the sum of all weights is
+// needed too (one evaluation per logit), and the draw may lie beyond the list; lists may also be too
+// long (many equal logits): such rows are left to the kernel below, as are all others.
+constexpr int kListThreads = 256;
+constexpr uint32_t kListK = 256, kListMax = 1024, kListSpace = 4096;
+constexpr int32_t kUndecided = -2;  // token of a row that the list did not decide
+
+struct ListShared {
+    float2 exp2[64];
+    u64 part[kListThreads / 32];
+    uint32_t upart[kListThreads / 32];
+    uint32_t bound[2], largest, n_list;
+    // the first CTA's: entries and weight of each slice, the entries, and in order
+    uint32_t counts[kMaxCtas];
+    u64 sums[kMaxCtas];
+    u64 all, pool[kListMax], order[kListK], space[kListSpace];
+};
+
+template <bool F32>
+__global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p, int C) {
+    pdl_launch_dependents();
+    constexpr int T = kListThreads;
+    using K = Key<F32>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    ListShared& s = *reinterpret_cast<ListShared*>(smem);
+    pdl_wait();
+    Slice<F32, T> r(p, s.exp2, s.part, C);
+    const int tid = r.tid, warp = r.warp, lane = r.lane, row = r.row, rank = r.rank;
+    Filters f;
+    const bool good = f.load(p, row);
+    const uint32_t want = f.t == 0.f ? 1u : f.top_k > 0 ? (uint32_t)f.top_k : 0u;
+    // (the same in every CTA of the row)
+    if (!good || (want ? want > kListK : !F32)) {
+        if (rank == 0 && tid == 0) {
+            p.token[row] = good ? kUndecided : -1;
+            if (!good) report(p.err, GEMMA_DEVERR_SAMPLE);
+        }
+        return;
+    }
+    const uint32_t n = want ? want : kListK;
+    r.inv_t = f.inverse_t();
+    const uint32_t best = r.thread_max();
+
+    // The m-th largest of the threads' keys, 0 if fewer than m threads have one: bit by bit, with
+    // the barrier's own count.
+    auto nth_key = [&](uint32_t m) {
+        uint32_t at = 0;
+#pragma unroll 1
+        for (uint32_t bit = F32 ? 0x80000000u : 0x8000u; bit; bit >>= 1)
+            if (__syncthreads_count(best >= (at | bit)) >= (int)m) at |= bit;
+        return at >= K::kLow ? at : 0u;
+    };
+    const uint32_t own = nth_key(n), share = C > 1 ? nth_key((n + C - 1) / C) : own;
+    const uint32_t mx = __reduce_max_sync(0xffffffffu, best);
+    if (lane == 0) s.upart[warp] = mx;
+    __syncthreads();
+    if (warp == 0) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, lane < T / 32 ? s.upart[lane] : 0u);
+        if (lane == 0) {
+            s.largest = m;
+            s.bound[0] = own;
+            s.bound[1] = share;
+            s.n_list = 0;
+        }
+    }
+    cluster_barrier();
+    uint32_t lg = 0, high = 0, low = 0xffffffffu;
+    if (lane < C) {
+        high = ld_peer(peer_addr(&s.bound[0], lane));
+        low = ld_peer(peer_addr(&s.bound[1], lane));
+        lg = ld_peer(peer_addr(&s.largest, lane));
+    }
+    const uint32_t pivot = max(__reduce_max_sync(0xffffffffu, high),
+                               __reduce_min_sync(0xffffffffu, low));
+    r.key_max = __reduce_max_sync(0xffffffffu, lg);
+    const uint32_t floor_key = max(pivot, K::kLow), room = kListSpace / C;
+    const uint32_t space = peer_addr(s.space + rank * room, 0);
+    // keys down to the bound: falling keys, then rising indices, in one number
+    auto take = [&](uint32_t bits, long long at) {
+        const uint32_t key = K::of(bits);
+        if (key < floor_key || key > K::kInf) return;
+        const uint32_t i = atomicAdd(&s.n_list, 1u);
+        if (i < room) st_peer(space + 8 * i, (u64)key << 32 | (0xffffffffu - (uint32_t)at));
+    };
+    r.for_slice_at([&](uint4 v, long long at) {
+        if (F32) {
+            take(v.x, at);
+            take(v.y, at + 1);
+            take(v.z, at + 2);
+            take(v.w, at + 3);
+        } else {
+            const uint32_t m = K::of(r.vec_max(v));
+            if (m < floor_key || m > K::kInf) return;
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                take(w[k] & 0xffffu, at + 2 * k);
+                take(w[k] >> 16, at + 2 * k + 1);
+            }
+        }
+    }, take);
+    const bool need_sum = F32 && !want && r.key_max;
+    if (need_sum || rank == 0) r.zmax = r.capped(K::value(max(r.key_max, K::kLow)));
+    if (need_sum) {
+        u64 mine = 0;
+        auto add = [&](uint32_t bits) {
+            const uint32_t key = K::of(bits);
+            if (key >= K::kLow && key <= K::kInf) mine += r.units(r.weight(key), 1u);
+        };
+        r.for_slice([&](uint4 v) {
+            add(v.x);
+            add(v.y);
+            add(v.z);
+            add(v.w);
+        }, add);
+        const u64 b = r.sum_before(mine);
+        if (tid == T - 1) st_peer(peer_addr(&s.sums[rank], 0), b + mine);
+    }
+    __syncthreads();
+    if (tid == 0) st_peer(peer_addr(&s.counts[rank], 0), s.n_list);
+    cluster_barrier();
+    if (rank != 0) return;  // (its shared memory is read no more)
+
+    if (r.key_max == 0) {  // no candidate
+        if (tid == 0) {
+            p.token[row] = -1;
+            report(p.err, GEMMA_DEVERR_SAMPLE);
+        }
+        return;
+    }
+    const uint32_t count = lane < C ? s.counts[lane] : 0u;
+    const uint32_t ends = r.warp_sums(count);  // of CTA lane's entries among all
+    const uint32_t total = __shfl_sync(0xffffffffu, ends, 31);
+    if (__any_sync(0xffffffffu, count > room) || total > kListMax) {
+        if (tid == 0) p.token[row] = kUndecided;
+        return;
+    }
+    for (uint32_t i0 = warp * 32; i0 < total; i0 += T) {
+        const uint32_t i = i0 + lane;
+        uint32_t q = 0;
+        for (int c = 0; c < C; ++c) q += i >= __shfl_sync(0xffffffffu, ends, c);
+        const uint32_t first = __shfl_sync(0xffffffffu, ends - count, q & 31);
+        if (i < total) s.pool[i] = s.space[q * room + i - first];
+    }
+    __syncthreads();
+    const uint32_t kept_n = min(n, total);
+    for (uint32_t i = tid; i < total; i += T) {
+        const u64 e = s.pool[i];
+        uint32_t before = 0;
+#pragma unroll 8
+        for (uint32_t j = 0; j < total; ++j) before += s.pool[j] > e;
+        if (before < kept_n) s.order[before] = e;
+    }
+    __syncthreads();
+    const bool have = tid < (int)kept_n;
+    const u64 e = have ? s.order[tid] : 0;
+    const uint32_t key = (uint32_t)(e >> 32);
+    const F2 w = have ? r.weight(key) : F2{0.f, 0.f};
+    const u64 m = have ? r.units(w, 1u) : 0;
+    const u64 run = r.sum_before(m) + m;
+    u64 all;
+    if (need_sum) {
+        all = __shfl_sync(0xffffffffu, r.warp_sums(lane < C ? s.sums[lane] : (u64)0), 31);
+    } else {
+        if (tid == T - 1) s.all = run;
+        __syncthreads();
+        all = s.all;
+    }
+    auto first = [&](bool yes) {  // lowest thread that says yes, or T
+        const unsigned b = __ballot_sync(0xffffffffu, yes);
+        __syncthreads();
+        if (lane == 0) s.upart[warp] = b ? warp * 32 + __ffs(b) - 1 : T;
+        __syncthreads();
+        return __reduce_min_sync(0xffffffffu, s.upart[lane & (T / 32 - 1)]);
+    };
+    auto run_at = [&](uint32_t i) {
+        __syncthreads();
+        if (tid == (int)i) s.all = run;
+        __syncthreads();
+        return s.all;
+    };
+    // how many entries are kept, and their weight
+    uint32_t keep = kept_n;
+    bool open = need_sum && (pivot != 0 || total > n);  // what is kept may reach beyond the list
+    bool fits = true;
+    u64 kept = all;
+    if (f.top_p <= 0.f) {
+        keep = 1;
+        open = false;
+        kept = run_at(0);
+    } else if (f.top_p < 1.f) {
+        const u64 need = min(max((u64)ceil((double)f.top_p * (double)all), (u64)1), all);
+        const uint32_t i = first(have && run >= need);
+        if (i < kept_n) {
+            keep = i + 1;
+            open = false;
+            kept = run_at(i);
+        } else {
+            fits = false;
+        }
+    }
+    if (f.min_p > 0.f) {
+        const bool below = have && key != r.key_max &&
+                           !(w.h > f.min_p || (w.h == f.min_p && w.l >= 0.f));
+        const uint32_t i = first(below);
+        if (i < keep) {
+            keep = i;
+            kept = run_at(i - 1);
+            fits = true;  // (whatever top_p left undecided lies below the floor)
+        } else if (open) {
+            fits = false;
+        }
+    }
+    if (fits) {
+        const u64 need = min((u64)((double)f.u * (double)kept) + 1, kept);
+        const uint32_t i = first(have && run >= need);
+        if (i >= kept_n) fits = false;
+        else if (tid == (int)i) p.token[row] = (int32_t)(0xffffffffu - (uint32_t)e);
+    }
+    if (!fits && tid == 0) p.token[row] = kUndecided;
+}
+
+template <bool F32>
+struct Row : Slice<F32, kThreads> {
+    using Base = Slice<F32, kThreads>;
+    using K = Key<F32>;
+    using Base::C; using Base::lane; using Base::p; using Base::rank; using Base::row;
+    using Base::tid; using Base::warp; using Base::for_slice; using Base::warp_sums;
+    using Base::sum_before;
+    Shared& s;
+    uint32_t* hist;   // [kBins / 2] pairs of 16-bit counters
+    uint32_t* merged; // [groups of this CTA][32] counts of the whole row (more than one CTA)
+
+    __device__ Row(const SampleParams& p_, Shared& s_, uint32_t* hist_, int C_)
+        : Base(p_, s_.exp2, s_.part, C_), s(s_), hist(hist_), merged(hist_ + kBins / 2) {}
 
     // Histogram of this CTA's slice. bf16: of the keys; fp32: of the keys' upper halves (level 0)
     // or of the lower halves of those with upper half `upper`.
@@ -292,307 +641,6 @@ struct Row {
         }, [&](uint32_t u) { add(u, 1); });
         __syncthreads();
     }
-    // Calls vec for every aligned 16 bytes of the slice and one for the elements around them.
-    template <class V, class O>
-    __device__ void for_slice(V vec, O one) {
-        for_slice_at([&](uint4 v, long long) { vec(v); }, [&](uint32_t u, long long) { one(u); });
-    }
-    // The same, with the (first) element's index in the row.
-    template <class V, class O>
-    __device__ void for_slice_at(V vec, O one) {
-        constexpr int E = F32 ? 4 : 8;
-        const long long base = (long long)row * p.vocab;
-        const long long b0 = base + i0, b1 = base + i1;
-        const long long a0 = min((b0 + E - 1) / E * E, b1), a1 = max(b1 / E * E, a0);
-        auto load1 = [&](long long i) -> uint32_t {
-            return F32 ? static_cast<const uint32_t*>(p.logits)[i]
-                       : static_cast<const uint16_t*>(p.logits)[i];
-        };
-        for (long long i = b0 + tid; i < a0; i += kThreads) one(load1(i), i - base);
-        const uint4* v = reinterpret_cast<const uint4*>(p.logits) + a0 / E;
-        const int n = (int)((a1 - a0) / E);
-        int i = tid;
-        for (; i + 3 * kThreads < n; i += 4 * kThreads) {
-            uint4 x[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = v[i + k * kThreads];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-                vec(x[k], a0 - base + (long long)(i + k * kThreads) * E);
-        }
-        for (; i < n; i += kThreads) vec(v[i], a0 - base + (long long)i * E);
-        for (long long j = a1 + tid; j < b1; j += kThreads) one(load1(j), j - base);
-    }
-
-    // The largest key of this thread's part of the slice (0 if it has no candidate).
-    __device__ uint32_t thread_max() {
-        uint32_t best = 0;
-        for_slice([&](uint4 v) {
-            uint32_t m;
-            if (F32) {
-                m = __float_as_uint(fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)),
-                                          fmaxf(__uint_as_float(v.z), __uint_as_float(v.w))));
-            } else {
-                m = vec_max(v);
-            }
-            m = K::of(m);
-            if (m <= K::kInf) best = max(best, m);
-        }, [&](uint32_t u) {
-            const uint32_t key = K::of(u);
-            if (key <= K::kInf) best = max(best, key);
-        });
-        return best >= K::kLow ? best : 0;
-    }
-    // Largest of eight bf16 (NaN only if all are), as bits.
-    __device__ static uint32_t vec_max(const uint4& v) {
-        uint32_t m;
-        asm("{\n\t.reg .b32 a, b;\n\tmax.bf16x2 a, %1, %2;\n\tmax.bf16x2 b, %3, %4;\n\t"
-            "max.bf16x2 %0, a, b;\n\t}"
-            : "=r"(m)
-            : "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w));
-        const float f = fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
-        return __float_as_uint(f) >> 16;
-    }
-    // The n-th largest of the keys that each(f) hands to f (0 ones do not count), 0 if there are
-    // fewer: eight bits at a time by counting.
-    template <class Each>
-    __device__ uint32_t select(uint32_t n, Each each) {
-        uint32_t prefix = 0, mask = 0;
-#pragma unroll 1
-        for (int shift = F32 ? 24 : 8; shift >= 0; shift -= 8) {
-            if (tid < 256) s.digit[tid] = 0;
-            __syncthreads();
-            each([&](uint32_t key) {
-                if (key && (key & mask) == prefix) atomicAdd(&s.digit[key >> shift & 255u], 1u);
-            });
-            __syncthreads();
-            // lane i: digits 255 - 8 i down
-            uint32_t c[8], sum = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) sum += c[j] = s.digit[255 - 8 * lane - j];
-            const uint32_t upto = warp_sums(sum);
-            const unsigned hit = __ballot_sync(0xffffffffu, upto >= n);
-            if (!hit) return 0;  // (only at the first digit)
-            const int l = __ffs(hit) - 1;
-            uint32_t left = n - (upto - sum), d = 0;
-            bool open = true;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (open && left <= c[j]) {
-                    d = 255 - 8 * lane - j;
-                    open = false;
-                } else if (open) {
-                    left -= c[j];
-                }
-            }
-            prefix |= __shfl_sync(0xffffffffu, d, l) << shift;
-            n = __shfl_sync(0xffffffffu, left, l);
-            mask |= 255u << shift;
-            __syncthreads();
-        }
-        return prefix;
-    }
-
-    // Draw from the row's n largest logits: true if that decided the row (token written). Every CTA
-    // lists what of its slice can be among them, the first one orders the lists' n largest and
-    // walks down their running weights. Without a top_k the sum of all weights is needed too (one
-    // evaluation per logit), and the draw may lie beyond the list, as may its entries beyond
-    // kListCap: then the row goes the long way.
-    __device__ bool draw_from_list(uint32_t n, bool filter_k, float top_p, float min_p, float u) {
-        u64* list = reinterpret_cast<u64*>(merged);
-        const uint32_t best = thread_max();
-        const uint32_t pivot = select(n, [&](auto f) { f(best); });
-        if (tid == 0) s.n_list = 0;
-        const uint32_t mx = __reduce_max_sync(0xffffffffu, best);
-        if (lane == 0) s.upart[warp] = mx;
-        __syncthreads();
-        const uint32_t floor_key = max(pivot, K::kLow);
-        auto take = [&](uint32_t bits, long long at) {
-            const uint32_t key = K::of(bits);
-            if (key < floor_key || key > K::kInf) return;
-            const uint32_t i = atomicAdd(&s.n_list, 1u);
-            // falling keys, then rising indices
-            if (i < kListCap) list[i] = (u64)key << 32 | (0xffffffffu - (uint32_t)at);
-        };
-        for_slice_at([&](uint4 v, long long at) {
-            if (F32) {
-                take(v.x, at);
-                take(v.y, at + 1);
-                take(v.z, at + 2);
-                take(v.w, at + 3);
-            } else {
-                const uint32_t m = K::of(vec_max(v));
-                if (m < floor_key || m > K::kInf) return;
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    take(w[k] & 0xffffu, at + 2 * k);
-                    take(w[k] >> 16, at + 2 * k + 1);
-                }
-            }
-        }, take);
-        if (warp == 0) {
-            const uint32_t m = __reduce_max_sync(0xffffffffu, s.upart[lane]);
-            if (lane == 0) {
-                s.largest = m;
-                s.whole = pivot == 0;
-            }
-        }
-        __syncthreads();
-        cluster_barrier();
-        uint32_t counts = 0, lg = 0, all_whole = 1;
-        if (lane < C) {
-            counts = ld_peer(peer_addr(&s.n_list, lane));
-            lg = ld_peer(peer_addr(&s.largest, lane));
-            all_whole = ld_peer(peer_addr(&s.whole, lane));
-        }
-        const bool over = __any_sync(0xffffffffu, counts > kListCap);
-        const bool whole = __all_sync(0xffffffffu, all_whole);
-        key_max = __reduce_max_sync(0xffffffffu, lg);
-        const uint32_t ends = warp_sums(counts);  // of lane's list among all
-        const uint32_t total = __shfl_sync(0xffffffffu, ends, 31);
-        if (over) return false;  // (the same in every CTA)
-        if (total == 0) {
-            if (rank == 0 && tid == 0) {
-                p.token[row] = -1;
-                report(p.err, GEMMA_DEVERR_SAMPLE);
-            }
-            cluster_barrier();  // no CTA leaves while another reads its shared memory
-            return true;
-        }
-        zmax = capped(K::value(key_max));
-        u64 all = 0;
-        const bool need_sum = !filter_k && !(whole && total <= n);
-        if (need_sum) {
-            u64 mine = 0;
-            auto add = [&](uint32_t bits) {
-                const uint32_t key = K::of(bits);
-                if (key >= K::kLow && key <= K::kInf) mine += units(weight(key), 1u);
-            };
-            for_slice([&](uint4 v) {
-                if (F32) {
-                    add(v.x);
-                    add(v.y);
-                    add(v.z);
-                    add(v.w);
-                }
-            }, add);
-            const u64 b = sum_before(mine);
-            if (tid == kThreads - 1) s.sum = b + mine;
-            __syncthreads();
-            cluster_barrier();
-            if (rank == 0)
-                for (int q = 0; q < C; ++q) {
-                    const uint32_t a = peer_addr(&s.sum, q);
-                    all += ld_peer(a) | (u64)ld_peer(a + 4) << 32;
-                }
-        }
-        if (rank == 0) {
-            u64* pool = reinterpret_cast<u64*>(hist);
-            for (int q = 0; q < C; ++q) {
-                const uint32_t e = __shfl_sync(0xffffffffu, ends, q);
-                const uint32_t c = __shfl_sync(0xffffffffu, counts, q);
-                const uint32_t a = peer_addr(list, q);
-                for (uint32_t i = tid; i < c; i += kThreads)
-                    pool[e - c + i] = ld_peer(a + 8 * i) | (u64)ld_peer(a + 8 * i + 4) << 32;
-            }
-            if (tid == 0) s.n_list = 0;
-            __syncthreads();
-            const uint32_t kth = select(min(n, total), [&](auto f) {
-                for (uint32_t i = tid; i < total; i += kThreads) f((uint32_t)(pool[i] >> 32));
-            });
-            u64* few = s.before;    // entries at and above the n-th key, in any order
-            u64* order = s.before2; // and the n largest in theirs
-            for (uint32_t i = tid; i < total; i += kThreads) {
-                const u64 e = pool[i];
-                if ((uint32_t)(e >> 32) >= kth) {
-                    const uint32_t at = atomicAdd(&s.n_list, 1u);
-                    if (at < kThreads) few[at] = e;
-                }
-            }
-            __syncthreads();
-            const uint32_t n_few = s.n_list, kept_n = min(n, total);
-            bool fits = n_few <= kThreads;
-            if (fits) {
-                if (tid < n_few) {
-                    const u64 e = few[tid];
-                    uint32_t before = 0;
-#pragma unroll 8
-                    for (uint32_t i = 0; i < n_few; ++i) before += few[i] > e;
-                    if (before < kept_n) order[before] = e;
-                }
-                __syncthreads();
-                const u64 e = tid < kept_n ? order[tid] : 0;
-                const uint32_t key = (uint32_t)(e >> 32);
-                const F2 w = tid < kept_n ? weight(key) : F2{0.f, 0.f};
-                const u64 m = tid < kept_n ? units(w, 1u) : 0;
-                const u64 run = sum_before(m) + m;
-                if (!need_sum) {
-                    if (tid == kThreads - 1) s.sum = run;
-                    __syncthreads();
-                    all = s.sum;
-                }
-                // how many entries are kept, and their weight; beyond: not decided by the list
-                uint32_t keep = kept_n;
-                bool open = need_sum;  // what is kept reaches beyond the list
-                u64 kept = all;
-                auto first = [&](bool yes) {  // lowest thread that says yes, or kThreads
-                    const unsigned b = __ballot_sync(0xffffffffu, yes);
-                    __syncthreads();
-                    if (lane == 0) s.upart[warp] = b ? warp * 32 + __ffs(b) - 1 : kThreads;
-                    __syncthreads();
-                    return __reduce_min_sync(0xffffffffu, s.upart[lane]);
-                };
-                auto sum_at = [&](uint32_t i) {
-                    __syncthreads();
-                    if (tid == i) s.sum = run;
-                    __syncthreads();
-                    return s.sum;
-                };
-                if (top_p <= 0.f) {
-                    keep = 1;
-                    open = false;
-                    kept = sum_at(0);
-                } else if (top_p < 1.f) {
-                    const u64 need = min(max((u64)ceil((double)top_p * (double)all), (u64)1), all);
-                    const uint32_t i = first(run >= need);
-                    if (i < kept_n) {
-                        keep = i + 1;
-                        open = false;
-                        kept = sum_at(i);
-                    } else {
-                        fits = false;
-                    }
-                }
-                if (min_p > 0.f) {
-                    const bool low = tid < kept_n && key != key_max &&
-                                     !(w.h > min_p || (w.h == min_p && w.l >= 0.f));
-                    const uint32_t i = first(low);
-                    if (i < keep) {
-                        keep = i;
-                        open = false;
-                        kept = sum_at(i - 1);
-                        fits = true;  // (whatever top_p left undecided lies below the floor)
-                    } else if (open) {
-                        fits = false;
-                    }
-                }
-                if (fits) {
-                    const u64 need = min((u64)((double)u * (double)kept) + 1, kept);
-                    const uint32_t i = first(run >= need);
-                    if (i >= kept_n) fits = false;
-                    else if (tid == i) p.token[row] = (int32_t)(0xffffffffu - (uint32_t)e);
-                }
-            }
-            if (tid == 0) s.fits = fits;
-            __syncthreads();
-        }
-        cluster_barrier();
-        const bool decided = ld_peer(peer_addr(&s.fits, 0)) != 0;
-        cluster_barrier();  // (the long way, or the end: nobody reads this CTA's list any more)
-        return decided;
-    }
-
     // The row's counts: group sums into every CTA's s.count, bins into their owner's `merged`
     // (group g belongs to CTA g % C). Needs every CTA's histogram, leaves them readable. A row's
     // values lie in a few hundred of the 2,048 groups, and a peer's shared memory gives only some
@@ -650,27 +698,6 @@ struct Row {
         return ld_peer(peer_addr(merged + (g / C) * 32 + i, g % C));
     }
 
-    // Inclusive sums over the warp's lanes.
-    template <class T>
-    __device__ T warp_sums(T x) const {
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const T y = __shfl_up_sync(0xffffffffu, x, o);
-            if (lane >= o) x += y;
-        }
-        return x;
-    }
-    // Sum of the values of the CTA's threads before this one.
-    template <class T>
-    __device__ T sum_before(T v) {
-        const T x = warp_sums(v);
-        __syncthreads();  // (s.part may still be read)
-        if (lane == 31) s.part[warp] = x;
-        __syncthreads();
-        const T all = warp_sums((T)s.part[lane]);
-        const T base = __shfl_sync(0xffffffffu, all, (warp + 31) & 31);
-        return (warp ? base : (T)0) + x - v;
-    }
     // Weights per group to running sums, in place.
     __device__ void running_sums(u64* before) {
         const u64 a = before[kGroups - 1 - 2 * tid], b = before[kGroups - 2 - 2 * tid];
@@ -697,44 +724,28 @@ __device__ __forceinline__ u64 mul_div(u64 a, u64 b, u64 c) {
 }
 
 template <bool F32>
-__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams p, int C) {
+__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams p, int C,
+                                                             int after_list) {
     pdl_launch_dependents();
     extern __shared__ __align__(16) uint8_t smem[];
     Shared& s = *reinterpret_cast<Shared*>(smem);
     uint32_t* hist = reinterpret_cast<uint32_t*>(smem + (sizeof(Shared) + 15) / 16 * 16);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int row = blockIdx.x / C, rank = blockIdx.x - row * C;
     using K = Key<F32>;
     pdl_wait();
-
-    // parameters (the same in every CTA of the row)
-    const float t = p.temperature ? p.temperature[row] : 1.f;
-    const int want_k = p.top_k ? p.top_k[row] : 0;
-    const float top_p = p.top_p ? p.top_p[row] : 1.f;
-    const float min_p = p.min_p ? p.min_p[row] : 0.f;
-    const float u = p.uniform[row];
-
-    Row<F32> r{p, s, hist, hist + kBins / 2, C, rank, row};
-    const long long per = (p.vocab + C - 1) / C;
-    r.i0 = min((long long)rank * per, (long long)p.vocab);
-    r.i1 = min(r.i0 + per, (long long)p.vocab);
-    r.tid = tid;
-    r.warp = warp;
-    r.lane = lane;
-    if (tid < 64) s.exp2[tid] = c_exp2[tid];
-    const bool good = t >= 0.f && isfinite(t) && top_p == top_p && min_p == min_p && u >= 0.f && u < 1.f;
-    if (!good) {  // the same in every CTA of the row
+    if (after_list && p.token[blockIdx.x / C] != kUndecided) return;
+    Row<F32> r(p, s, hist, C);
+    const int tid = r.tid, warp = r.warp, lane = r.lane, row = r.row, rank = r.rank;
+    Filters f;
+    if (!f.load(p, row)) {  // the same in every CTA of the row
         if (rank == 0 && tid == 0) {
             p.token[row] = -1;
             report(p.err, GEMMA_DEVERR_SAMPLE);
         }
         return;
     }
-    r.inv_t = t > 0.f ? F2{1.f, 0.f} / F2{t, 0.f} : F2{0.f, 0.f};
-    const uint32_t n_top = t == 0.f ? 1u : want_k > 0 ? (uint32_t)want_k : 0u;
-    if (n_top ? n_top <= kListK : F32)
-        if (r.draw_from_list(n_top ? n_top : kListK, n_top > 0, top_p, min_p, u)) return;
-
+    const float t = f.t, top_p = f.top_p, min_p = f.min_p, u = f.u;
+    const int want_k = f.top_k;
+    r.inv_t = f.inverse_t();
     s.before[tid] = s.before[tid + kThreads] = 0;
     // fp32: this CTA's share of the row's weight sums starts at zero
     u64* mass = F32 ? p.mass + (size_t)row * kBins : nullptr;
@@ -1125,25 +1136,23 @@ int row_ctas(int batch, int vocab, int n_sm) {
     return best ? best : kMaxCtas;
 }
 
-template <bool F32>
-cudaError_t launch(const SampleParams& p, int C, cudaStream_t st) {
-    auto kernel = sample_kernel<F32>;
-    const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + kBins * 2 +
-                        (C > 1 ? (size_t)(kGroups + C - 1) / C * 32 * 4 : kListCap * 8);
-    static std::atomic<bool> configured[64];  // per device; the same values every time
+// One cluster of C CTAs per row; attributes set once per device (the same values every time).
+template <class... KArgs, class... Args>
+cudaError_t launch_rows(void (*kernel)(KArgs...), std::atomic<bool>* configured, int batch, int C,
+                        int threads, size_t smem, cudaStream_t st, Args... args) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
     if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_relaxed)) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             227 * 1024);
+                                             threads == kThreads ? 227 * 1024 : 64 * 1024);
         if (e == cudaSuccess)
             e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_relaxed);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)p.batch * C);
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3((unsigned)batch * C);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -1155,7 +1164,24 @@ cudaError_t launch(const SampleParams& p, int C, cudaStream_t st) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, p, C);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <bool F32>
+cudaError_t launch(const SampleParams& p, int n_sm, cudaStream_t st) {
+    static std::atomic<bool> list_set[64], row_set[64];
+    // the list can decide rows only if some may have a short top_k (or are fp32)
+    const int listed = F32 || p.top_k != nullptr;
+    if (listed) {
+        const int c = (p.vocab + 8191) / 8192, C = c > kMaxCtas ? kMaxCtas : c;
+        const cudaError_t e = launch_rows(list_kernel<F32>, list_set, p.batch, C, kListThreads,
+                                          sizeof(ListShared), st, p, C);
+        if (e != cudaSuccess) return e;
+    }
+    const int C = row_ctas(p.batch, p.vocab, n_sm);
+    const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + kBins * 2 +
+                        (C > 1 ? (size_t)(kGroups + C - 1) / C * 32 * 4 : 0);
+    return launch_rows(sample_kernel<F32>, row_set, p.batch, C, kThreads, smem, st, p, C, listed);
 }
 
 }  // namespace
@@ -1166,8 +1192,7 @@ size_t sample_workspace(int batch, int vocab, int fp32) {
 }
 
 cudaError_t launch_sample(const SampleParams& p, int fp32, int n_sm, cudaStream_t st) {
-    const int C = row_ctas(p.batch, p.vocab, n_sm);
-    return fp32 ? launch<true>(p, C, st) : launch<false>(p, C, st);
+    return fp32 ? launch<true>(p, n_sm, st) : launch<false>(p, n_sm, st);
 }
 
 }  // namespace gemma
