@@ -443,8 +443,8 @@ size_t gemma_logit_workspace_size(int batch, int vocab);
  *               negative, infinite or NaN, a NaN top_p or min_p, or uniform outside [0, 1), gets -1
  *               and GEMMA_DEVERR_SAMPLE in device_error.
  *   workspace   DEVICE scratch of gemma_logit_sample_workspace_size(batch, vocab, dtype) bytes,
- *               16-byte aligned (NULL when that is 0); contents on entry are ignored; calls that
- *               may overlap must not share it.
+ *               16-byte aligned; contents on entry are ignored; calls that may overlap must not
+ *               share it.
  * Returns GEMMA_ERR_INVALID_ARG (NULL or misaligned pointer, batch < 0, vocab < 1, bad softcap or
  * dtype), GEMMA_ERR_UNSUPPORTED (batch > 65535 or vocab > 1,048,560) or GEMMA_ERR_WORKSPACE before
  * any launch; batch == 0 is a no-op. Asynchronous on `stream`; allocates nothing; graph-capturable.
@@ -455,8 +455,8 @@ int gemma_logit_sample(const void* logits, int batch, int vocab, gemma_dtype dty
                        void* workspace, size_t workspace_bytes, uint32_t* device_error,
                        void* stream);
 
-/* Bytes of scratch gemma_logit_sample needs ((size_t)-1 for invalid arguments): none for bf16
- * logits, 512 KiB per row for fp32 ones. */
+/* Bytes of scratch gemma_logit_sample needs ((size_t)-1 for invalid arguments): 4 per row, and
+ * 512 KiB more per row of fp32 logits. */
 size_t gemma_logit_sample_workspace_size(int batch, int vocab, gemma_dtype dtype);
 
 /* A static, human-readable name of a gemma_status value. */

@@ -872,14 +872,17 @@ int gemma_logit_sample(const void* logits, int batch, int vocab, gemma_dtype dty
     if (batch > 65535 || vocab > gemma::kSampleMaxVocab) return GEMMA_ERR_UNSUPPORTED;
     if (batch == 0) return GEMMA_OK;
     if (!logits || !uniform || !token_out || !aligned16(logits)) return GEMMA_ERR_INVALID_ARG;
-    const size_t need = gemma::sample_workspace(batch, vocab, dtype == GEMMA_FP32);
+    const size_t need = gemma::sample_workspace(batch, dtype == GEMMA_FP32);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
         return GEMMA_ERR_WORKSPACE;
     const int n_sm = sm_count();
     if (n_sm < 0) return GEMMA_ERR_CUDA;
     const gemma::SampleParams p{logits, temperature, top_k, top_p, min_p, uniform, token_out,
-                                static_cast<unsigned long long*>(workspace), device_error, batch,
-                                vocab, softcap};
+                                static_cast<int32_t*>(workspace),
+                                reinterpret_cast<unsigned long long*>(
+                                    static_cast<uint8_t*>(workspace) +
+                                    gemma::sample_workspace(batch, 0)),
+                                device_error, batch, vocab, softcap};
     const cudaError_t e =
         gemma::launch_sample(p, dtype == GEMMA_FP32, n_sm, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GEMMA_OK : GEMMA_ERR_CUDA;
@@ -889,7 +892,7 @@ size_t gemma_logit_sample_workspace_size(int batch, int vocab, gemma_dtype dtype
     if (batch < 0 || vocab < 1 || vocab > gemma::kSampleMaxVocab ||
         (dtype != GEMMA_BF16 && dtype != GEMMA_FP32))
         return (size_t)-1;
-    return gemma::sample_workspace(batch, vocab, dtype == GEMMA_FP32);
+    return gemma::sample_workspace(batch, dtype == GEMMA_FP32);
 }
 
 }  // extern "C"

@@ -192,6 +192,8 @@ struct Shared {
     float2 exp2[64];
     uint32_t mine[kGroups / 32], any[kGroups / 32];  // groups with counts: this CTA's, the row's
     uint32_t live[kGroups / 32];                     // the row's, of whole numbers or upper halves
+    uint32_t open[kWarps];
+    int row;
     u64 part[kWarps];
     uint32_t upart[kWarps];
     int top[kWarps];
@@ -247,6 +249,15 @@ struct Slice {
     }
     __device__ F2 weight(uint32_t key) const {
         return key == key_max ? F2{1.f, 0.f} : relative(capped(K::value(key)), zmax);
+    }
+    // One weight in units of 2^-43, for sums over all logits: none below 2^-44, and single precision
+    // (an absolute error of 2^-46) is enough below 2^-24, where most of a row lies.
+    __device__ u64 quick_units(uint32_t key) const {
+        if (key == key_max || isinf(zmax.h) || p.softcap > 0.f) return units(weight(key), 1u);
+        const float d = (K::value(key) - zmax.h) * inv_t.h;
+        if (d < -30.6f) return 0;
+        if (d < -17.f) return (u64)__float2ll_rn(expf(d) * 0x1p43f);
+        return units(weight(key), 1u);
     }
     // n weights in units of 2^-43, rounded
     __device__ u64 units(F2 w, uint32_t n) const {
@@ -364,8 +375,7 @@ struct Filters {
 // needed too (one evaluation per logit), and the draw may lie beyond the list; lists may also be too
 // long (many equal logits): such rows are left to the kernel below, as are all others.
 constexpr int kListThreads = 256;
-constexpr uint32_t kListK = 256, kListMax = 1024, kListSpace = 4096;
-constexpr int32_t kUndecided = -2;  // token of a row that the list did not decide
+constexpr uint32_t kListK = 256, kListMax = 1024, kListSpace = 2048;
 
 struct ListShared {
     float2 exp2[64];
@@ -394,8 +404,11 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
     // (the same in every CTA of the row)
     if (!good || (want ? want > kListK : !F32)) {
         if (rank == 0 && tid == 0) {
-            p.token[row] = good ? kUndecided : -1;
-            if (!good) report(p.err, GEMMA_DEVERR_SAMPLE);
+            p.open[row] = good;
+            if (!good) {
+                p.token[row] = -1;
+                report(p.err, GEMMA_DEVERR_SAMPLE);
+            }
         }
         return;
     }
@@ -467,7 +480,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
         u64 mine = 0;
         auto add = [&](uint32_t bits) {
             const uint32_t key = K::of(bits);
-            if (key >= K::kLow && key <= K::kInf) mine += r.units(r.weight(key), 1u);
+            if (key >= K::kLow && key <= K::kInf) mine += r.quick_units(key);
         };
         r.for_slice([&](uint4 v) {
             add(v.x);
@@ -485,6 +498,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
 
     if (r.key_max == 0) {  // no candidate
         if (tid == 0) {
+            p.open[row] = 0;
             p.token[row] = -1;
             report(p.err, GEMMA_DEVERR_SAMPLE);
         }
@@ -494,7 +508,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
     const uint32_t ends = r.warp_sums(count);  // of CTA lane's entries among all
     const uint32_t total = __shfl_sync(0xffffffffu, ends, 31);
     if (__any_sync(0xffffffffu, count > room) || total > kListMax) {
-        if (tid == 0) p.token[row] = kUndecided;
+        if (tid == 0) p.open[row] = 1;
         return;
     }
     for (uint32_t i0 = warp * 32; i0 < total; i0 += T) {
@@ -579,7 +593,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
         if (i >= kept_n) fits = false;
         else if (tid == (int)i) p.token[row] = (int32_t)(0xffffffffu - (uint32_t)e);
     }
-    if (!fits && tid == 0) p.token[row] = kUndecided;
+    if (tid == 0) p.open[row] = !fits;
 }
 
 template <bool F32>
@@ -723,18 +737,13 @@ __device__ __forceinline__ u64 mul_div(u64 a, u64 b, u64 c) {
     return (u64)((unsigned __int128)a * b / c);
 }
 
+// Draw one row (every CTA of its cluster).
 template <bool F32>
-__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams p, int C,
-                                                             int after_list) {
-    pdl_launch_dependents();
-    extern __shared__ __align__(16) uint8_t smem[];
-    Shared& s = *reinterpret_cast<Shared*>(smem);
-    uint32_t* hist = reinterpret_cast<uint32_t*>(smem + (sizeof(Shared) + 15) / 16 * 16);
+__device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C, int row) {
     using K = Key<F32>;
-    pdl_wait();
-    if (after_list && p.token[blockIdx.x / C] != kUndecided) return;
     Row<F32> r(p, s, hist, C);
-    const int tid = r.tid, warp = r.warp, lane = r.lane, row = r.row, rank = r.rank;
+    r.row = row;
+    const int tid = r.tid, warp = r.warp, lane = r.lane, rank = r.rank;
     Filters f;
     if (!f.load(p, row)) {  // the same in every CTA of the row
         if (rank == 0 && tid == 0) {
@@ -1092,53 +1101,109 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
     }
     cluster_barrier();  // no CTA leaves while another reads its shared memory
     if (draw_tie < before || draw_tie >= before + mine) return;
-    const uint32_t nth = draw_tie - before;
-    // that occurrence within the slice: contiguous pieces per thread, counted, then searched
-    const int n = (int)(r.i1 - r.i0), piece = (n + kThreads - 1) / kThreads;
-    const int a = min(tid * piece, n), b = min(a + piece, n);
-    const long long base = (long long)row * p.vocab + r.i0;
-    auto key_at = [&](int i) {
-        return K::of(F32 ? static_cast<const uint32_t*>(p.logits)[base + i]
-                         : static_cast<const uint16_t*>(p.logits)[base + i]);
-    };
-    uint32_t c = 0;
-#pragma unroll 8
-    for (int i = a; i < b; ++i) c += key_at(i) == draw_key;
-    const uint32_t ex = r.sum_before(c);
-    if (nth >= ex && nth < ex + c) {
-        uint32_t left = nth - ex;
-        for (int i = a; i < b; ++i)
-            if (key_at(i) == draw_key && left-- == 0) {
-                p.token[row] = (int32_t)(r.i0 + i);
-                break;
+    // that occurrence within the slice, 16 bytes per thread at a time in the order of the indices
+    constexpr int E = F32 ? 4 : 8;
+    const long long b0 = (long long)row * p.vocab + r.i0, b1 = (long long)row * p.vocab + r.i1;
+    const long long end = (long long)p.batch * p.vocab;
+    uint32_t left = draw_tie - before;
+    for (long long v0 = b0 / E; v0 * E < b1; v0 += kThreads) {
+        const long long at = (v0 + tid) * E;
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
+        if (at + E <= end) {
+            const uint4 v = reinterpret_cast<const uint4*>(p.logits)[v0 + tid];
+            w[0] = v.x;
+            w[1] = v.y;
+            w[2] = v.z;
+            w[3] = v.w;
+        } else {  // the last elements of the array
+            for (int e = 0; e < E && at + e < end; ++e) {
+                if (F32) w[e] = static_cast<const uint32_t*>(p.logits)[at + e];
+                else w[e / 2] |= (uint32_t) static_cast<const uint16_t*>(p.logits)[at + e] << 16 * (e & 1);
             }
+        }
+        uint32_t hits = 0;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const uint32_t bits = F32 ? w[e & 3] : w[e / 2] >> 16 * (e & 1) & 0xffffu;
+            if (K::of(bits) == draw_key && at + e >= b0 && at + e < b1) hits |= 1u << e;
+        }
+        const uint32_t ex = r.sum_before((uint32_t)__popc(hits));
+        if (tid == kThreads - 1) s.n = ex + __popc(hits);
+        __syncthreads();
+        const uint32_t all = s.n;
+        if (left < all) {
+            if (left >= ex && left < ex + __popc(hits)) {
+                for (uint32_t k = left - ex; k > 0; --k) hits &= hits - 1;
+                p.token[row] = (int32_t)(at + __ffs(hits) - 1 - (long long)row * p.vocab);
+            }
+            return;
+        }
+        left -= all;
+    }
+}
+
+// Every cluster draws rows i, i + clusters, ... of those that the list launch left open (all rows
+// without one): the i-th open row is found from the row flags, which nobody changes here.
+template <bool F32>
+__global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams p, int C,
+                                                             int after_list) {
+    pdl_launch_dependents();
+    extern __shared__ __align__(16) uint8_t smem[];
+    Shared& s = *reinterpret_cast<Shared*>(smem);
+    uint32_t* hist = reinterpret_cast<uint32_t*>(smem + (sizeof(Shared) + 15) / 16 * 16);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_wait();
+    int passed = 0;  // open rows before row b0
+    int i = blockIdx.x / C;
+    for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+        const int b = b0 + tid;
+        const bool is = b < p.batch && (!after_list || p.open[b]);
+        const unsigned word = __ballot_sync(0xffffffffu, is);
+        if (lane == 0) s.open[warp] = word;
+        __syncthreads();
+        int base = 0, all = 0;
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) base += __popc(s.open[w]);
+            all += __popc(s.open[w]);
+        }
+        for (; i < passed + all; i += gridDim.x / C) {
+            if (is && passed + base + __popc(word & ((1u << lane) - 1)) == i) s.row = b;
+            __syncthreads();
+            const int row = s.row;
+            draw_row<F32>(p, s, hist, C, row);
+            cluster_barrier();  // (shared memory is used anew)
+        }
+        passed += all;
+        __syncthreads();
     }
 }
 
 // CTAs per row: one for short rows; else 5 to 16 (so that the merged counts fit beside the
 // histogram and no slice exceeds a 16-bit counter), as many as give the batch the fewest rounds
-// of clusters weighed with the slice that a CTA counts.
-int row_ctas(int batch, int vocab, int n_sm) {
-    if (vocab <= 4096) return 1;
+// of clusters, weighed with the slice that a CTA counts (a row costs about as much besides as
+// 32,768 counted logits). And the clusters that the GPU holds at once.
+int row_ctas(int batch, int vocab, int n_sm, int* clusters) {
     const int gpc = n_sm / 8 > 16 ? n_sm / 8 : 16;  // SMs that a cluster can share
-    int best = 0;
+    int best = vocab <= 4096 ? 1 : 0, at_once = n_sm;
     double best_cost = 0.0;
-    for (int c = 5; c <= kMaxCtas; ++c) {
+    for (int c = 5; c <= kMaxCtas && vocab > 4096; ++c) {
         if ((vocab + c - 1) / c > 65535) continue;
-        const int at_once = (gpc / c > 0 ? gpc / c : 1) * 8;
-        const double rounds = (batch + at_once - 1) / at_once;
-        const double cost = rounds * (8192.0 + (double)vocab / c);
+        const int fit = (gpc / c > 0 ? gpc / c : 1) * 8;
+        const double rounds = (batch + fit - 1) / fit;
+        const double cost = rounds * (32768.0 + (double)vocab / c);
         if (!best || cost < best_cost) {
             best = c;
             best_cost = cost;
+            at_once = fit;
         }
     }
-    return best ? best : kMaxCtas;
+    *clusters = batch < at_once ? batch : at_once;
+    return best;
 }
 
-// One cluster of C CTAs per row; attributes set once per device (the same values every time).
+// Clusters of C CTAs; attributes set once per device (the same values every time).
 template <class... KArgs, class... Args>
-cudaError_t launch_rows(void (*kernel)(KArgs...), std::atomic<bool>* configured, int batch, int C,
+cudaError_t launch_rows(void (*kernel)(KArgs...), std::atomic<bool>* configured, int clusters, int C,
                         int threads, size_t smem, cudaStream_t st, Args... args) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
@@ -1151,7 +1216,7 @@ cudaError_t launch_rows(void (*kernel)(KArgs...), std::atomic<bool>* configured,
         if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_relaxed);
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)batch * C);
+    cfg.gridDim = dim3((unsigned)clusters * C);
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -1178,17 +1243,17 @@ cudaError_t launch(const SampleParams& p, int n_sm, cudaStream_t st) {
                                           sizeof(ListShared), st, p, C);
         if (e != cudaSuccess) return e;
     }
-    const int C = row_ctas(p.batch, p.vocab, n_sm);
+    int clusters = 0;
+    const int C = row_ctas(p.batch, p.vocab, n_sm, &clusters);
     const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + kBins * 2 +
                         (C > 1 ? (size_t)(kGroups + C - 1) / C * 32 * 4 : 0);
-    return launch_rows(sample_kernel<F32>, row_set, p.batch, C, kThreads, smem, st, p, C, listed);
+    return launch_rows(sample_kernel<F32>, row_set, clusters, C, kThreads, smem, st, p, C, listed);
 }
 
 }  // namespace
 
-size_t sample_workspace(int batch, int vocab, int fp32) {
-    (void)vocab;
-    return fp32 ? (size_t)batch * kBins * 8 : 0;
+size_t sample_workspace(int batch, int fp32) {
+    return ((size_t)batch * 4 + 15) / 16 * 16 + (fp32 ? (size_t)batch * kBins * 8 : 0);
 }
 
 cudaError_t launch_sample(const SampleParams& p, int fp32, int n_sm, cudaStream_t st) {

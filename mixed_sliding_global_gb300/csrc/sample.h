@@ -15,6 +15,7 @@ struct SampleParams {
     const float* min_p;
     const float* uniform;
     int32_t* token;
+    int32_t* open;             // [batch] whether the short lists left the row undecided
     unsigned long long* mass;  // fp32 logits: [batch][65536] sums of weights, else unused
     uint32_t* err;
     int batch, vocab;
@@ -22,7 +23,8 @@ struct SampleParams {
 };
 
 constexpr int kSampleMaxVocab = 16 * 65535;  // 16 CTAs of a row, 16-bit counters
-size_t sample_workspace(int batch, int vocab, int fp32);
+// row flags, then the sums
+size_t sample_workspace(int batch, int fp32);
 cudaError_t launch_sample(const SampleParams& p, int fp32, int n_sm, cudaStream_t st);
 
 }  // namespace gemma

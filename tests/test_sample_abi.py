@@ -22,7 +22,7 @@ def call(x=FAKE, batch=1, vocab=8, dtype=0, cap=30.0, u=FAKE, out=FAKE, ws=None,
     (dict(cap=-1.0), INVALID), (dict(cap=float("nan")), INVALID), (dict(cap=float("inf")), INVALID),
     (dict(x=None), INVALID), (dict(x=FAKE + 8), INVALID), (dict(u=None), INVALID),
     (dict(out=None), INVALID), (dict(batch=65536), UNSUPPORTED), (dict(vocab=1048561), UNSUPPORTED),
-    (dict(dtype=1), WORKSPACE), (dict(dtype=1, ws=FAKE, ws_bytes=100), WORKSPACE),
+    (dict(), WORKSPACE), (dict(dtype=1), WORKSPACE), (dict(dtype=1, ws=FAKE, ws_bytes=100), WORKSPACE),
     (dict(dtype=1, ws=FAKE + 8, ws_bytes=1 << 20), WORKSPACE), (dict(batch=0), 0),
 ])
 def test_argument_errors(kw, status):
@@ -32,8 +32,8 @@ def test_argument_errors(kw, status):
 def test_workspace_size():
     f, bad = lib().gemma_logit_sample_workspace_size, ctypes.c_size_t(-1).value
     assert f(-1, 8, 0) == bad and f(1, 0, 0) == bad and f(1, 8, 5) == bad and f(1, 1 << 21, 0) == bad
-    assert f(4, 262144, 0) == 0 and f(0, 8, 1) == 0
-    assert f(4, 1000, 1) == 4 << 19
+    assert f(5, 262144, 0) == 32 and f(0, 8, 1) == 0
+    assert f(4, 1000, 1) == 16 + (4 << 19)
     with pytest.raises(ValueError):
         g.gemma_logit_sample_workspace_size(1, 8, torch.float16)
 
