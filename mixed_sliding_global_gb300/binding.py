@@ -349,62 +349,92 @@ def gemma_attn_workspace_size_paged(batch: int, kind: int, window: int, n_q: int
     return int(n)
 
 
-def _q4_caches(codes, scales, v_codes, v_scales, owner_map):
-    """Pointer arrays of a 4-bit cache; the owner layers' codes must be uint8, scales bf16."""
+_array_types: dict = {}   # (ctypes type, length) -> array type
+
+
+def _array(ctype, n: int):
+    t = _array_types.get((ctype, n))
+    if t is None:
+        t = _array_types[(ctype, n)] = ctype * n
+    return t
+
+
+def _raw_stream(stream, t: torch.Tensor) -> int:
+    """The raw handle of a stream (torch's current one on the tensor's device when None)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.device.index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on_current_device(t: torch.Tensor) -> None:
+    """Launches go to the current device: refuse tensors of another one (and of the CPU)."""
+    if not t.is_cuda:
+        raise ValueError("expected a CUDA tensor")
+    if t.device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"tensors on {t.device}, but the current device is another")
+
+
+def _q4_cache(k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_eq_v, d, n_kv, batch,
+              block_table):
+    """Check the owner layer's 4-bit cache. Returns the C call's arguments: four pointer arrays (only
+    the owner's entry is ever read), the owner map, n_layers, layer; and (block_table, max_pages,
+    page_size, n_pages), capacity."""
     n = len(owner_map)
-    arrays = [list(codes), list(scales),
-              list(v_codes) if v_codes is not None else [None] * n,
-              list(v_scales) if v_scales is not None else [None] * n]
-    for xs, dt in zip(arrays, (torch.uint8, torch.bfloat16) * 2):
-        if len(xs) != n:
-            raise ValueError("one cache entry per layer")
-        for x in xs:
-            if x is not None and x.dtype != dt:
-                raise TypeError(f"4-bit caches hold uint8 codes and bf16 scales, not {x.dtype}")
-    return arrays
-
-
-def _q4_geometry(arrays, owner_map, layer, k_eq_v, d, n_kv, block_table):
-    """Check the owner layer's shapes; (capacity, max_pages, page_size, n_pages) of its cache."""
     o = int(owner_map[layer])
-    kc = arrays[0][o]
-    if kc is None or arrays[1][o] is None:
+    kc, ks = k_codes[o], k_scales[o]
+    if kc is None or ks is None:
         raise ValueError("the owner layer has no cache")
-    if kc.dim() != 4 or kc.shape[1] != n_kv or kc.shape[3] * 2 != d:
+    shape = kc.shape
+    if len(shape) != 4 or shape[1] != n_kv or shape[3] * 2 != d:
         raise ValueError("codes must be [batch][n_kv][capacity][head_dim / 2]")
-    want = (tuple(kc.shape), tuple(kc.shape[:3]) + (d // 64,))
-    for i, x in enumerate(a[o] for a in (arrays[:2] if k_eq_v else arrays)):
-        if x is None or tuple(x.shape) != want[i % 2]:
-            raise ValueError("codes and scales of K and V must have matching shapes")
+    rows, _, slots, _ = shape
+    want = (rows, n_kv, slots, d // 64)
+    entries = [kc, ks]
+    if not k_eq_v:
+        if v_codes is None or v_scales is None or v_codes[o] is None or v_scales[o] is None:
+            raise ValueError("the layer needs a V cache")
+        entries += [v_codes[o], v_scales[o]]
+        if entries[2].shape != shape:
+            raise ValueError("codes of K and V must have one shape")
+    arrays = []
+    vp = _array(ctypes.c_void_p, n)
+    for i, x in enumerate(entries):
+        if x.dtype != (torch.bfloat16 if i & 1 else torch.uint8):
+            raise TypeError("4-bit caches hold uint8 codes and bf16 scales")
+        if i & 1 and x.shape != want:
+            raise ValueError("scales must be [batch][n_kv][capacity][head_dim / 64]")
+        arr = vp()
+        arr[o] = _dev_ptr(x)
+        arrays.append(arr)
+    while len(arrays) < 4:
+        arrays.append(vp())
+    head = (*arrays, _array(ctypes.c_int32, n)(*owner_map), n, layer)
     if block_table is None:
-        return kc.shape[2], 0, 0, 0
-    if block_table.dtype != torch.int32:
-        raise TypeError("block_table must be int32")
-    return 0, int(block_table.shape[1]), int(kc.shape[2]), int(kc.shape[0])
+        if rows != batch:
+            raise ValueError("the cache must have one entry per sequence")
+        return head, (None, 0, 0, 0), slots
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError("block_table must be int32 [batch][max_pages]")
+    return head, (_dev_ptr(block_table), block_table.shape[1], slots, rows), 0
 
 
 def _q4_rows(fn, k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_rows, v_rows, pos, *,
              k_eq_v, kind, block_table, device_error, stream):
     B, n, n_kv, d = k_rows.shape
-    if pos.dtype != torch.int32:
-        raise TypeError("positions must be int32")
+    if pos.dtype != torch.int32 or pos.numel() != B:
+        raise ValueError("positions must be int32 [batch]")
     if not k_eq_v and (v_rows is None or v_rows.shape != k_rows.shape or
                        v_rows.dtype != k_rows.dtype):
         raise ValueError("K and V rows must have one shape and type")
-    arrays = _q4_caches(k_codes, k_scales, v_codes, v_scales, owner_map)
-    if pos.numel() != B:
-        raise ValueError("one position per sequence")
-    cap, max_pages, page_size, n_pages = _q4_geometry(arrays, owner_map, layer, k_eq_v, d, n_kv,
-                                                      block_table)
-    cache_batch = arrays[0][int(owner_map[layer])].shape[0]
-    if (block_table.shape[0] if block_table is not None else cache_batch) != B:
-        raise ValueError("the cache (or block table) must have one entry per sequence")
+    head, pages, cap = _q4_cache(k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_eq_v, d,
+                                 n_kv, B, block_table)
+    _on_current_device(k_rows)
     st = getattr(library(), fn)(
-        *[_ptr_array(a) for a in arrays], _i32_array(owner_map), len(owner_map), layer,
-        _dev_ptr(k_rows), None if k_eq_v else _dev_ptr(v_rows), _dev_ptr(pos),
-        _dev_ptr(block_table), max_pages, page_size, n_pages, B, n, int(kind), n_kv, d, int(cap),
-        int(bool(k_eq_v)), _dtype(k_rows), _dev_ptr(device_error), _stream(stream))
-    _check(fn, st)
+        *head, _dev_ptr(k_rows), None if k_eq_v else _dev_ptr(v_rows), _dev_ptr(pos), *pages, B, n,
+        kind, n_kv, d, cap, int(k_eq_v), _dtype(k_rows), _dev_ptr(device_error),
+        _raw_stream(stream, k_rows))
+    if st:
+        _check(fn, st)
 
 
 def gemma_kv_append_q4(k_codes, k_scales, v_codes, v_scales, owner_map, layer: int,
@@ -445,23 +475,19 @@ def gemma_attn_q4(out: torch.Tensor, q: torch.Tensor, k_codes, k_scales, v_codes
     seq_lens int32 [B] counting the new tokens. n_new = 1 is a decode step."""
     if q.dim() != 4 or out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("q and out must be [batch][n_new][n_q][head_dim] of one type")
-    if seq_lens.dtype != torch.int32 or seq_lens.numel() != q.shape[0]:
-        raise ValueError("seq_lens must be int32 [batch]")
     B, n_new, n_q, d = q.shape
-    arrays = _q4_caches(k_codes, k_scales, v_codes, v_scales, owner_map)
-    cap, max_pages, page_size, n_pages = _q4_geometry(arrays, owner_map, layer, k_eq_v, d, n_kv,
-                                                      block_table)
-    cache_batch = arrays[0][int(owner_map[layer])].shape[0]
-    if (block_table.shape[0] if block_table is not None else cache_batch) != B:
-        raise ValueError("the cache (or block table) must have one entry per sequence")
+    if seq_lens.dtype != torch.int32 or seq_lens.numel() != B:
+        raise ValueError("seq_lens must be int32 [batch]")
+    head, pages, cap = _q4_cache(k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_eq_v, d,
+                                 n_kv, B, block_table)
+    _on_current_device(q)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = library().gemma_attn_q4(
-        _dev_ptr(out), _dev_ptr(q), *[_ptr_array(a) for a in arrays], _i32_array(owner_map),
-        len(owner_map), layer, _dev_ptr(seq_lens), _dev_ptr(block_table), max_pages, page_size,
-        n_pages, int(max_seq_len), n_new, B, int(kind), int(window), n_q, int(n_kv), d,
-        int(bool(k_eq_v)), int(cap), float(scale), float(softcap), _dtype(q),
-        _dev_ptr(workspace), ws_bytes, _dev_ptr(device_error), _stream(stream))
-    _check("gemma_attn_q4", st)
+        _dev_ptr(out), _dev_ptr(q), *head, _dev_ptr(seq_lens), *pages, max_seq_len, n_new, B, kind,
+        window, n_q, n_kv, d, int(k_eq_v), cap, scale, softcap, _dtype(q), _dev_ptr(workspace),
+        ws_bytes, _dev_ptr(device_error), _raw_stream(stream, q))
+    if st:
+        _check("gemma_attn_q4", st)
 
 
 def gemma_attn_workspace_size_q4(batch: int, kind: int, window: int, n_q: int, n_kv: int,
@@ -526,12 +552,14 @@ def gemma_logit_sample(logits: torch.Tensor, token_out: torch.Tensor, uniform: t
                         ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
         if t is not None and (t.dtype != dt or t.numel() != B):
             raise TypeError(f"{name} must be {dt} [batch]")
+    _on_current_device(logits)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = library().gemma_logit_sample(
-        _dev_ptr(logits), B, V, _dtype(logits), float(softcap), _dev_ptr(temperature),
-        _dev_ptr(top_k), _dev_ptr(top_p), _dev_ptr(min_p), _dev_ptr(uniform), _dev_ptr(token_out),
-        _dev_ptr(workspace), ws_bytes, _dev_ptr(device_error), _stream(stream))
-    _check("gemma_logit_sample", st)
+        _dev_ptr(logits), B, V, _dtype(logits), softcap, _dev_ptr(temperature), _dev_ptr(top_k),
+        _dev_ptr(top_p), _dev_ptr(min_p), _dev_ptr(uniform), _dev_ptr(token_out),
+        _dev_ptr(workspace), ws_bytes, _dev_ptr(device_error), _raw_stream(stream, logits))
+    if st:
+        _check("gemma_logit_sample", st)
 
 
 def _attn(fn_name, out, q, k_cache, v_cache, owner_map, layer, seq_lens, max_seq_len, n_tok, *,
