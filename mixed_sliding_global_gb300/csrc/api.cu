@@ -586,7 +586,8 @@ int q4_layout(int kind, int n_kv, int head_dim, int kv_capacity, const int32_t* 
     if (kind != GEMMA_SLIDING && kind != GEMMA_GLOBAL && kind != GEMMA_SLIDING_RING)
         return GEMMA_ERR_INVALID_ARG;
     if (n_kv < 1) return GEMMA_ERR_INVALID_ARG;
-    if (!head_dim_ok(head_dim)) return GEMMA_ERR_UNSUPPORTED;
+    // (one grid layer per KV head, of K and of V)
+    if (!head_dim_ok(head_dim) || n_kv > 32767) return GEMMA_ERR_UNSUPPORTED;
     *c = gemma::Q4Cache{};
     c->n_kv = n_kv;
     if (block_table) {
