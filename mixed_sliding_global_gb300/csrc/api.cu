@@ -876,8 +876,6 @@ int gemma_logit_sample(const void* logits, int batch, int vocab, gemma_dtype dty
     const size_t need = gemma::sample_workspace(batch, dtype == GEMMA_FP32);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
         return GEMMA_ERR_WORKSPACE;
-    const int n_sm = sm_count();
-    if (n_sm < 0) return GEMMA_ERR_CUDA;
     const gemma::SampleParams p{logits, temperature, top_k, top_p, min_p, uniform, token_out,
                                 static_cast<int32_t*>(workspace),
                                 reinterpret_cast<unsigned long long*>(
@@ -885,7 +883,7 @@ int gemma_logit_sample(const void* logits, int batch, int vocab, gemma_dtype dty
                                     gemma::sample_workspace(batch, 0)),
                                 device_error, batch, vocab, softcap};
     const cudaError_t e =
-        gemma::launch_sample(p, dtype == GEMMA_FP32, n_sm, static_cast<cudaStream_t>(stream));
+        gemma::launch_sample(p, dtype == GEMMA_FP32, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? GEMMA_OK : GEMMA_ERR_CUDA;
 }
 

@@ -10,15 +10,25 @@
 // over the logits fills a histogram in shared memory (16-bit counters, 128 KB; the row's slices
 // go to the CTAs of a cluster, at most 65,535 logits each, whose counts meet through distributed
 // shared memory), and everything else works on counts and on at most a few thousand weights, each
-// evaluated once in 64 bits: cuts and draws fall between the same tokens as in a 64-bit
-// evaluation of the definition. Ties inside a value are a division, and one look at the slice that
-// holds the wanted occurrence finds its index. fp32 logits take the same histogram over their
-// upper 16 bits, whose bins' weights are summed into global memory as integers (40 bits below the
-// bin's own largest weight, so the order of the additions does not matter), and repeat it over
-// the lower 16 bits for the bins that a cut or the draw falls into.
+// evaluated once in pairs of fp32 numbers (2^-40): cuts and draws fall between the same tokens as in
+// a 64-bit evaluation of the definition. Ties inside a value are a division, and one look at the
+// slice that holds the wanted occurrence finds its index. fp32 logits take the same histogram over
+// their upper 16 bits, whose bins' weights are summed into global memory as integers (40 bits below
+// the bin's own largest weight, so the order of the additions does not matter). The few hundred
+// logits of a bin that a cut or the draw falls into are gathered and put in order; a bin of more
+// than 1,024 takes the histogram again, over its lower 16 bits (a row of 262,144: 88 us with
+// gathered bins, 190 with histograms of them).
 //
-// The first pass is bound by shared-memory atomics; runs of eight equal logits count as one, so
-// that a row masked with one finite value does not queue on one counter.
+// Rows with a top_k of at most 256 never get there: a launch ahead (list_kernel) draws them from
+// the list of their largest logits, and leaves the others' numbers for the second launch.
+//
+// What bounds it, per row of 262,144 bf16 logits (16 us for one CTA's loads, 0.08 us at the GPU's
+// rate): latencies. One row with top_k 64: 14.0 us, of it 2.5 for reading the slices and the rest
+// barriers of the cluster, the list's order and two launches; a row by histogram: 28 us, of it 3
+// for counting (bound by shared-memory atomics; runs of eight equal logits count as one, so that
+// a row masked with one finite value does not queue on one counter), 4.5 for merging the counts,
+// 12 for cuts and draw. 64 rows by histogram: 103 us (three rounds of clusters), of which 5 us
+// would do at the memory's rate.
 #include <atomic>
 
 #include <cuda_bf16.h>
@@ -34,6 +44,9 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 65536, kGroups = 2048;  // 32 bins per group
 constexpr int kMaxCtas = 16;
+// what a row costs one CTA, or a cluster, besides counting its slice: in logits of the slice
+constexpr double kAloneCost = 140e3, kClusterCost = 95e3;
+constexpr uint32_t kGather = kThreads;  // fp32: numbers of one upper half that are put in order
 
 // Order-preserving key of a number (-0 as +0), its inverse, and the candidates' range of keys:
 // above -inf, not above +inf.
@@ -100,10 +113,11 @@ __device__ __forceinline__ F2 two_sum(float a, float b) {
     const float s = __fadd_rn(a, b), t = __fadd_rn(s, -a);
     return F2{s, __fadd_rn(__fadd_rn(a, -__fadd_rn(s, -t)), __fadd_rn(b, -t))};
 }
+// (sums and products drop the products of two error terms: an error of a few 2^-47 of the larger
+// operand, so a difference keeps the operands' absolute accuracy)
 __device__ __forceinline__ F2 operator+(F2 a, F2 b) {
-    const F2 s = two_sum(a.h, b.h), e = two_sum(a.l, b.l);
-    const F2 t = fast_sum(s.h, __fadd_rn(s.l, e.h));
-    return fast_sum(t.h, __fadd_rn(t.l, e.l));
+    const F2 s = two_sum(a.h, b.h);
+    return fast_sum(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
 }
 __device__ __forceinline__ F2 operator*(F2 a, F2 b) {
     const float m = __fmul_rn(a.h, b.h);
@@ -112,15 +126,12 @@ __device__ __forceinline__ F2 operator*(F2 a, F2 b) {
     return fast_sum(m, __fmaf_rn(a.l, b.h, e));
 }
 __device__ __forceinline__ F2 operator/(F2 a, F2 b) {
-    // quotient digits from one approximate reciprocal, each correcting what the ones before left
+    // a first quotient from an approximate reciprocal, and one correction of what it leaves
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(b.h));
     const float q = __fmul_rn(a.h, r);
-    const F2 d = a + F2{-q, 0.f} * b;
-    const float q2 = __fmul_rn(d.h, r);
-    const F2 d2 = d + F2{-q2, 0.f} * b;
-    const F2 t = fast_sum(q, q2);
-    return fast_sum(t.h, __fadd_rn(t.l, __fmul_rn(d2.h, r)));
+    const float d = __fadd_rn(__fmaf_rn(-q, b.h, a.h), __fmaf_rn(-q, b.l, a.l));
+    return fast_sum(q, __fmul_rn(d, r));
 }
 
 // 2^(i / 64) as such sums.
@@ -199,6 +210,7 @@ struct Shared {
     int top[kWarps];
     uint32_t found, key, n;
     u64 m, start;
+    uint32_t own_max, index, listed[2];  // fp32, see gather
 };
 
 // A CTA's slice of a row's logits, and the row's weights. T threads.
@@ -209,7 +221,7 @@ struct Slice {
     u64* part;           // shared, one per warp
     int C, rank, row;
     long long i0, i1;
-    F2 inv_t, zmax;
+    F2 inv_t, zmax, inner;  // 1 / T, the largest z, -2 / softcap
     uint32_t key_max;    // key of the row's largest candidate
     int tid, warp, lane;
 
@@ -225,6 +237,7 @@ struct Slice {
         const long long per = (p.vocab + C - 1) / C;
         i0 = min((long long)rank * per, (long long)p.vocab);
         i1 = min(i0 + per, (long long)p.vocab);
+        inner = p.softcap > 0.f ? F2{-2.f, 0.f} / F2{p.softcap, 0.f} : F2{0.f, 0.f};
         for (int i = tid; i < 64; i += T) exp2_[i] = c_exp2[i];
     }
 
@@ -233,7 +246,7 @@ struct Slice {
         if (!(p.softcap > 0.f)) return F2{x, 0.f};
         const F2 c{p.softcap, 0.f};
         const float a = fabsf(x);
-        const F2 e = exp_f2(F2{-2.f * a, 0.f} / c, exp2);
+        const F2 e = exp_f2(F2{a, 0.f} * inner, exp2);
         F2 t = (F2{1.f, 0.f} + F2{-e.h, -e.l}) / (F2{1.f, 0.f} + e);
         if (isinf(x)) t = F2{1.f, 0.f};
         t = t * c;
@@ -250,13 +263,19 @@ struct Slice {
     __device__ F2 weight(uint32_t key) const {
         return key == key_max ? F2{1.f, 0.f} : relative(capped(K::value(key)), zmax);
     }
-    // One weight in units of 2^-43, for sums over all logits: none below 2^-44, and single precision
-    // (an absolute error of 2^-46) is enough below 2^-24, where most of a row lies.
-    __device__ u64 quick_units(uint32_t key) const {
-        if (key == key_max || isinf(zmax.h) || p.softcap > 0.f) return units(weight(key), 1u);
-        const float d = (K::value(key) - zmax.h) * inv_t.h;
-        if (d < -30.6f) return 0;
-        if (d < -17.f) return (u64)__float2ll_rn(expf(d) * 0x1p43f);
+    // One weight in units of 2^-43, for sums over all logits (without a cap). Most of a row lies below 2^-24 of the
+    // largest: single precision is enough there (an error of 2^-46 each), and a sum of its own keeps
+    // what is less than a unit.
+    __device__ u64 quick_units(uint32_t key, float& tiny) const {
+        if (key != key_max && !isinf(zmax.h)) {
+            const F2 a = two_sum(K::value(key), -zmax.h);  // (zmax.l is zero without a cap)
+            const float d = __fmul_rn(a.h, inv_t.h);
+            if (d < -17.f) {
+                const float rest = __fmaf_rn(a.h, inv_t.h, -d) + (a.l * inv_t.h + a.h * inv_t.l);
+                if (d > -80.f) tiny += expf(d) * (1.f + rest);
+                return 0;
+            }
+        }
         return units(weight(key), 1u);
     }
     // n weights in units of 2^-43, rounded
@@ -367,8 +386,11 @@ struct Filters {
     }
 };
 
-// The short list. A row with a top_k up to kListK, and an fp32 row without one, is drawn from its
-// n = top_k (kListK) largest logits alone. The n-th largest of a CTA's threads' largest keys bounds
+// The short list. A row with a top_k up to kListK, and an fp32 row without one or a cap, is drawn
+// from its n = top_k (kListK) largest logits alone. In us, the list and the histograms: bf16, one
+// row of 262,144: top_k 20 13.3, 27.8; 256 21.7, 24.7; 64 rows: 35.2, 104.8 and 55.0, 94.8; fp32, 9
+// rows of 70,001 that top_p 0.9 ends within the list: 38.9, 54.3. (With a cap the sum of all weights
+// takes longer than the histograms do: 157, 88.) The n-th largest of a CTA's threads' largest keys bounds
 // the row's n-th largest logit from below, and so does the smallest over the CTAs of each one's
 // (n / C)-th: every CTA sends its slice's keys down to the higher of these bounds to the first one,
 // which orders them and walks down their running weights. Without a top_k the sum of all weights is
@@ -402,7 +424,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
     const bool good = f.load(p, row);
     const uint32_t want = f.t == 0.f ? 1u : f.top_k > 0 ? (uint32_t)f.top_k : 0u;
     // (the same in every CTA of the row)
-    if (!good || (want ? want > kListK : !F32)) {
+    if (!good || (want ? want > kListK : !F32 || p.softcap > 0.f)) {
         if (rank == 0 && tid == 0) {
             p.open[row] = good;
             if (!good) {
@@ -478,9 +500,10 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
     if (need_sum || rank == 0) r.zmax = r.capped(K::value(max(r.key_max, K::kLow)));
     if (need_sum) {
         u64 mine = 0;
+        float tiny = 0.f;
         auto add = [&](uint32_t bits) {
             const uint32_t key = K::of(bits);
-            if (key >= K::kLow && key <= K::kInf) mine += r.quick_units(key);
+            if (key >= K::kLow && key <= K::kInf) mine += r.quick_units(key, tiny);
         };
         r.for_slice([&](uint4 v) {
             add(v.x);
@@ -488,6 +511,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
             add(v.z);
             add(v.w);
         }, add);
+        mine += (u64)__float2ll_rn(tiny * 0x1p43f);
         const u64 b = r.sum_before(mine);
         if (tid == T - 1) st_peer(peer_addr(&s.sums[rank], 0), b + mine);
     }
@@ -606,9 +630,10 @@ struct Row : Slice<F32, kThreads> {
     Shared& s;
     uint32_t* hist;   // [kBins / 2] pairs of 16-bit counters
     uint32_t* merged; // [groups of this CTA][32] counts of the whole row (more than one CTA)
+    uint32_t best;    // fp32: this thread's largest candidate key
 
     __device__ Row(const SampleParams& p_, Shared& s_, uint32_t* hist_, int C_)
-        : Base(p_, s_.exp2, s_.part, C_), s(s_), hist(hist_), merged(hist_ + kBins / 2) {}
+        : Base(p_, s_.exp2, s_.part, C_), s(s_), hist(hist_), merged(hist_ + kBins / 2), best(0) {}
 
     // Histogram of this CTA's slice. bf16: of the keys; fp32: of the keys' upper halves (level 0)
     // or of the lower halves of those with upper half `upper`.
@@ -622,6 +647,7 @@ struct Row : Slice<F32, kThreads> {
             uint32_t bin = key;
             if (F32) {
                 if (level == 0) {
+                    best = max(best, key);
                     bin = key >> 16;
                 } else {
                     if (key >> 16 != upper) return;
@@ -763,6 +789,15 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
     if (F32) __threadfence();
 
     r.count_slice(0, 0);
+    if (F32) {
+        const uint32_t mx = __reduce_max_sync(0xffffffffu, r.best);
+        if (lane == 0) s.upart[warp] = mx;
+        __syncthreads();
+        if (warp == 0) {
+            const uint32_t m = __reduce_max_sync(0xffffffffu, s.upart[lane]);
+            if (lane == 0) s.own_max = m;
+        }
+    }
     r.merge_counts();
 
     // the largest candidate and the number of them
@@ -834,45 +869,121 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
 
     Cut cut{0u, 0u};       // kept so far: this and above
     bool cut_all = true;   // or every candidate
-    if (F32) {
-        refine(bin_max);
-        int g2 = -1;
-        const uint32_t a = s.count[2 * tid], b = s.count[2 * tid + 1];
-        const int hi = __reduce_max_sync(0xffffffffu, b ? 2 * tid + 1 : a ? 2 * tid : -1);
-        if (lane == 0) s.top[warp] = hi;
+
+    // fp32: the numbers with upper half `upper`, at most kGather, in the order, one per thread (the
+    // same in every CTA). The CTAs exchange their slices' ones as the lower half and the place in
+    // the slice; a list is written again two calls later, behind a barrier that all pass having
+    // read it.
+    struct Entry {
+        uint32_t key, tie, index;
+        bool have;
+    };
+    int buf = 0;
+    auto gather = [&](uint32_t upper) {
+        uint32_t* list = reinterpret_cast<uint32_t*>(s.before2) + buf * kGather;
+        u64* pool = s.before2 + kGather;
+        const uint32_t per = (uint32_t)((p.vocab + C - 1) / C);
+        if (tid == 0) s.listed[buf] = 0;
         __syncthreads();
-        g2 = __reduce_max_sync(0xffffffffu, s.top[lane]);
+        auto take = [&](uint32_t bits, long long at) {
+            const uint32_t key = K::of(bits);
+            if (key >> 16 != upper || key < K::kLow || key > K::kInf) return;
+            const uint32_t i = atomicAdd(&s.listed[buf], 1u);
+            if (i < kGather) list[i] = key << 16 | (0xffffu - (uint32_t)(at - r.i0));
+        };
+        r.for_slice_at([&](uint4 v, long long at) {
+            take(v.x, at);
+            take(v.y, at + 1);
+            take(v.z, at + 2);
+            take(v.w, at + 3);
+        }, take);
+        cluster_barrier();
+        const uint32_t count = lane < C ? ld_peer(peer_addr(&s.listed[buf], lane)) : 0u;
+        const uint32_t ends = r.warp_sums(count);
+        const uint32_t n = min(__shfl_sync(0xffffffffu, ends, 31), kGather);
+        Entry e{0u, 0u, 0u, (uint32_t)tid < n};
+        uint32_t q = 0;
+        for (int c = 0; c < C; ++c) q += (uint32_t)tid >= __shfl_sync(0xffffffffu, ends, c);
+        const uint32_t first = __shfl_sync(0xffffffffu, ends - count, q & 31);
+        u64 x = 0;
+        if (e.have) {
+            const uint32_t v = ld_peer(peer_addr(list + tid - first, q));
+            x = (u64)(v >> 16) << 32 | (0xffffffffu - (q * per + 0xffffu - (v & 0xffffu)));
+            pool[tid] = x;
+        }
         __syncthreads();
-        key_max = bin_max << 16 | top_bin(g2);
-    }
+        uint32_t before = 0;
+        if (e.have) {
+#pragma unroll 8
+            for (uint32_t j = 0; j < n; ++j) before += pool[j] > x;
+        }
+        __syncthreads();
+        if (e.have) pool[before] = x;
+        __syncthreads();
+        if (e.have) {
+            x = pool[tid];
+            e.key = upper << 16 | (uint32_t)(x >> 32);
+            e.index = 0xffffffffu - (uint32_t)x;
+        }
+        // equal ones before it: from the last place where the key changes
+        const bool head = e.have && (tid == 0 || (uint32_t)(pool[tid - 1] >> 32) != (uint32_t)(x >> 32));
+        const unsigned heads = __ballot_sync(0xffffffffu, head);
+        if (lane == 0) s.top[warp] = heads ? warp * 32 + 31 - __clz(heads) : -1;
+        __syncthreads();
+        const unsigned low = heads & (0xffffffffu >> (31 - lane));
+        const int past = __reduce_max_sync(0xffffffffu, lane < warp ? s.top[lane] : -1);
+        e.tie = tid - (low ? warp * 32 + 31 - __clz(low) : past);
+        buf ^= 1;
+        return e;
+    };
+    // whether the counts at hand are of upper halves and `bin` holds few enough numbers
+    auto gathers = [&](uint32_t bin) {
+        return F32 && at == 0xffffffffu && r.bin_count((int)(bin / 32), (int)(bin % 32)) <= kGather;
+    };
+    uint32_t drawn = 0xffffffffu;  // fp32: the index drawn, if a gathered list gave it
+    if (F32)
+        key_max = __reduce_max_sync(0xffffffffu,
+                                    lane < C ? ld_peer(peer_addr(&s.own_max, lane)) : 0u);
     r.key_max = key_max;
     r.zmax = r.capped(K::value(key_max));
 
     uint32_t draw_key = key_max, draw_tie = 0;
     if (!greedy) {
         uint32_t cut_bin = 0;
+        u64 cut_mass = 0;  // fp32: kept weight of the cut's own bin
         if (k < total) {
-            if (F32) {
-                // (the counts at hand are of the largest's lower halves: count the upper ones anew)
-                cluster_barrier();
-                r.count_slice(0, 0);
-                r.merge_counts();
-                at = 0xffffffffu;
-            }
             kth(k, cut_bin, cut.ties);
             cut.key = cut_bin;
             cut_all = false;
             if (F32) {
                 const uint32_t n = cut.ties;
-                uint32_t low;
-                refine(cut_bin);
-                kth(n, low, cut.ties);
-                cut.key = cut_bin << 16 | low;
+                if (gathers(cut_bin)) {
+                    const Entry e = gather(cut_bin);
+                    const u64 m = (uint32_t)tid < n ? r.units(r.weight(e.key), 1u) : 0;
+                    const u64 run = r.sum_before(m) + m;
+                    if ((uint32_t)tid == n - 1) {
+                        s.key = e.key;
+                        s.n = e.tie + 1;
+                        s.m = run;
+                    }
+                    __syncthreads();
+                    cut = Cut{s.key, s.n};
+                    cut_mass = s.m;
+                    __syncthreads();
+                } else {
+                    uint32_t low;
+                    refine(cut_bin);
+                    kth(n, low, cut.ties);
+                    cut.key = cut_bin << 16 | low;
+                }
             }
         }
         // tokens of a key that are kept so far, of the c there are
         auto kept_of = [&](uint32_t key, uint32_t c) {
             return cut_all || key > cut.key ? c : key == cut.key ? min(c, cut.ties) : 0u;
+        };
+        auto stays = [&](const Entry& e) {
+            return cut_all || e.key > cut.key || (e.key == cut.key && e.tie < cut.ties);
         };
         // fp32: weights over the lower halves of `at`, of what is kept so far
         uint32_t lower_of = 0xffffffffu;
@@ -892,8 +1003,7 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
             r.running_sums(s.before2);
             lower_of = upper;
         };
-        u64 cut_mass = 0;  // fp32: kept weight of the cut's own bin
-        if (F32 && !cut_all) {
+        if (F32 && !cut_all && at == cut_bin) {
             lower_masses(cut_bin);
             cut_mass = s.before2[kGroups - 1];
         }
@@ -968,6 +1078,28 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
                 const uint32_t upper = s.key;
                 const u64 start = s.start, m_bin = s.m;
                 __syncthreads();
+                if (gathers(upper)) {
+                    const Entry e = gather(upper);
+                    const u64 m = e.have && stays(e) ? r.units(r.weight(e.key), 1u) : 0;
+                    const u64 run = r.sum_before(m) + m;
+                    if (tid == kThreads - 1) s.m = run;
+                    __syncthreads();
+                    const u64 have = s.m;
+                    const u64 rest = have ? min(max(m_bin ? need - start : 1, (u64)1), have) : 0;
+                    if (have ? run - m < rest && rest <= run : tid == 0) {
+                        s.key = e.key;
+                        s.n = e.tie + 1;
+                        s.index = e.index;
+                        s.start = start + (have ? run : m_bin);
+                    }
+                    __syncthreads();
+                    c = Cut{s.key, s.n};
+                    sum = s.start;
+                    drawn = s.index;
+                    __syncthreads();
+                    return;
+                }
+                drawn = 0xffffffffu;
                 lower_masses(upper);
                 // (the bin's weight was summed token by token, here value by value: the last units
                 // may differ)
@@ -1059,14 +1191,29 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
             if (end_all || floor_key > end.key) {
                 // everything from the floor up (its own tokens too, if there are any)
                 const uint32_t bin = F32 ? floor_key >> 16 : floor_key;
-                if (F32) lower_masses(bin);
+                u64 from = 0;  // fp32: weight of the bin's numbers from the floor up
+                const bool few = gathers(bin);
+                if (few) {
+                    const Entry e = gather(bin);
+                    const u64 m = e.have && e.key >= floor_key && stays(e)
+                                      ? r.units(r.weight(e.key), 1u) : 0;
+                    const u64 run = r.sum_before(m) + m;
+                    if (tid == kThreads - 1) s.m = run;
+                    __syncthreads();
+                    from = s.m;
+                    __syncthreads();
+                } else if (F32) {
+                    lower_masses(bin);
+                }
                 if (warp == 0) {
                     const int g = (int)(bin / 32), d = kGroups - 1 - g;
                     const bool above = (uint32_t)(g * 32 + lane) > bin ||
                                        (!F32 && (uint32_t)(g * 32 + lane) == bin);
                     u64 m = r.warp_sums(above ? bin_mass(g, lane) : (u64)0);
                     m = __shfl_sync(0xffffffffu, m, 31) + (d ? s.before[d - 1] : 0);
-                    if (F32) {
+                    if (few) {
+                        m += from;
+                    } else if (F32) {
                         const uint32_t low = floor_key & 0xffffu;
                         const int g2 = (int)(low / 32), d2 = kGroups - 1 - g2;
                         const uint32_t key = bin << 16 | (uint32_t)(g2 * 32 + lane);
@@ -1088,6 +1235,10 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
         place(min(need, kept), c, sum);
         draw_key = c.key;
         draw_tie = c.ties - 1;
+    }
+    if (drawn != 0xffffffffu) {
+        if (rank == 0 && tid == 0) p.token[row] = (int32_t)drawn;
+        return;
     }
     if (F32) refine(draw_key >> 16);
 
@@ -1178,76 +1329,107 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams 
     }
 }
 
-// CTAs per row: one for short rows; else 5 to 16 (so that the merged counts fit beside the
-// histogram and no slice exceeds a 16-bit counter), as many as give the batch the fewest rounds
-// of clusters, weighed with the slice that a CTA counts (a row costs about as much besides as
-// 32,768 counted logits). And the clusters that the GPU holds at once.
-int row_ctas(int batch, int vocab, int n_sm, int* clusters) {
-    const int gpc = n_sm / 8 > 16 ? n_sm / 8 : 16;  // SMs that a cluster can share
-    int best = vocab <= 4096 ? 1 : 0, at_once = n_sm;
-    double best_cost = 0.0;
-    for (int c = 5; c <= kMaxCtas && vocab > 4096; ++c) {
-        if ((vocab + c - 1) / c > 65535) continue;
-        const int fit = (gpc / c > 0 ? gpc / c : 1) * 8;
-        const double rounds = (batch + fit - 1) / fit;
-        const double cost = rounds * (32768.0 + (double)vocab / c);
-        if (!best || cost < best_cost) {
-            best = c;
-            best_cost = cost;
-            at_once = fit;
-        }
+// Launches of `clusters` clusters of C CTAs.
+struct Launch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    Launch(int clusters, int C, int threads, size_t smem, bool early, cudaStream_t st) {
+        cfg.gridDim = dim3((unsigned)clusters * C);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)C;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see pdl_wait
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = early ? 2 : 1;
     }
-    *clusters = batch < at_once ? batch : at_once;
-    return best;
+};
+
+// What is asked or set once per device (the same values every time).
+struct DeviceState {
+    std::atomic<bool> configured{false};
+    std::atomic<int> at_once[kMaxCtas + 1] = {};  // clusters of C CTAs that the GPU holds, or 0
+};
+constexpr int kDevices = 64;
+
+template <class Kernel>
+cudaError_t configure(Kernel* kernel, DeviceState& d, int max_smem) {
+    if (d.configured.load(std::memory_order_relaxed)) return cudaSuccess;
+    cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, max_smem);
+    if (e == cudaSuccess)
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess) d.configured.store(true, std::memory_order_relaxed);
+    return e;
 }
 
-// Clusters of C CTAs; attributes set once per device (the same values every time).
-template <class... KArgs, class... Args>
-cudaError_t launch_rows(void (*kernel)(KArgs...), std::atomic<bool>* configured, int clusters, int C,
-                        int threads, size_t smem, cudaStream_t st, Args... args) {
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-    if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_relaxed)) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             threads == kThreads ? 227 * 1024 : 64 * 1024);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_relaxed);
+size_t row_smem(int C) {
+    return (sizeof(Shared) + 15) / 16 * 16 + kBins * 2 +
+           (C > 1 ? (size_t)(kGroups + C - 1) / C * 32 * 4 : 0);
+}
+
+// In us, bf16, 1 / 5 / 8 / 11 / 16 CTAs per row: one row of 262,144 - / 32.5 / 29.7 / 26.8 / 27.8, of
+// 32,000 41.5 / 25.1 / 24.1 / 24.4 / 25.6; 16 rows - / 40.5 / 56.9 / 55.8 / 79.6 and 45.5 / 25.3 /
+// 45.7 / 46.6 / 71.3; 64 rows - / 112 / 146 / 218 / 260 (6: 103) and 45.7 / 71.0 / 111.8 / 179.9 /
+// 231.9.
+// CTAs per row: one, or 5 to 16 (so that the merged counts fit beside the histogram), no slice above
+// what a 16-bit counter holds; as many as take the batch the least time, in rounds of the clusters
+// that the GPU holds at once.
+template <bool F32>
+cudaError_t row_ctas(const SampleParams& p, DeviceState& d, int* ctas, int* clusters) {
+    double best = 0.0;
+    *ctas = 0;
+    for (int c = 1; c <= kMaxCtas; c = c == 1 ? 5 : c + 1) {
+        const int slice = (p.vocab + c - 1) / c;
+        if (slice > 65535) continue;
+        int fit = d.at_once[c].load(std::memory_order_relaxed);
+        if (fit == 0) {
+            Launch l(1, c, kThreads, row_smem(c), true, nullptr);
+            const cudaError_t e = cudaOccupancyMaxActiveClusters(&fit, sample_kernel<F32>, &l.cfg);
+            if (e != cudaSuccess) return e;
+            if (fit < 1) fit = -1;
+            d.at_once[c].store(fit, std::memory_order_relaxed);
+        }
+        if (fit < 1) continue;
+        const double rounds = (p.batch + fit - 1) / fit;
+        const double cost = rounds * ((c == 1 ? kAloneCost : kClusterCost) + slice);
+        if (*ctas == 0 || cost < best) {
+            best = cost;
+            *ctas = c;
+            *clusters = p.batch < fit ? p.batch : fit;
+        }
     }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)clusters * C);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)C;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see pdl_wait
-    attr[1].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
+    return *ctas ? cudaSuccess : cudaErrorInvalidConfiguration;
 }
 
 template <bool F32>
-cudaError_t launch(const SampleParams& p, int n_sm, cudaStream_t st) {
-    static std::atomic<bool> list_set[64], row_set[64];
-    // the list can decide rows only if some may have a short top_k (or are fp32)
-    const int listed = F32 || p.top_k != nullptr;
+cudaError_t launch(const SampleParams& p, cudaStream_t st) {
+    static DeviceState lists[kDevices], rows[kDevices];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return cudaErrorInvalidDevice;
+    // the list can decide rows only if some may have a short top_k (or are fp32 without a cap)
+    const int listed = p.top_k != nullptr || (F32 && !(p.softcap > 0.f));
     if (listed) {
         const int c = (p.vocab + 8191) / 8192, C = c > kMaxCtas ? kMaxCtas : c;
-        const cudaError_t e = launch_rows(list_kernel<F32>, list_set, p.batch, C, kListThreads,
-                                          sizeof(ListShared), st, p, C);
+        cudaError_t e = configure(list_kernel<F32>, lists[dev], 64 * 1024);
+        if (e != cudaSuccess) return e;
+        // (not ahead of the launch before it: that one's CTAs may fill most SMs, and the lists
+        // would crowd on the others: 22.8 us for 8 rows of 262,144 logits against 16.1)
+        Launch l(p.batch, C, kListThreads, sizeof(ListShared), false, st);
+        e = cudaLaunchKernelEx(&l.cfg, list_kernel<F32>, p, C);
         if (e != cudaSuccess) return e;
     }
-    int clusters = 0;
-    const int C = row_ctas(p.batch, p.vocab, n_sm, &clusters);
-    const size_t smem = (sizeof(Shared) + 15) / 16 * 16 + kBins * 2 +
-                        (C > 1 ? (size_t)(kGroups + C - 1) / C * 32 * 4 : 0);
-    return launch_rows(sample_kernel<F32>, row_set, clusters, C, kThreads, smem, st, p, C, listed);
+    cudaError_t e = configure(sample_kernel<F32>, rows[dev], 227 * 1024);
+    if (e != cudaSuccess) return e;
+    int C = 0, clusters = 0;
+    e = row_ctas<F32>(p, rows[dev], &C, &clusters);
+    if (e != cudaSuccess) return e;
+    Launch l(clusters, C, kThreads, row_smem(C), true, st);
+    return cudaLaunchKernelEx(&l.cfg, sample_kernel<F32>, p, C, listed);
 }
 
 }  // namespace
@@ -1256,8 +1438,8 @@ size_t sample_workspace(int batch, int fp32) {
     return ((size_t)batch * 4 + 15) / 16 * 16 + (fp32 ? (size_t)batch * kBins * 8 : 0);
 }
 
-cudaError_t launch_sample(const SampleParams& p, int fp32, int n_sm, cudaStream_t st) {
-    return fp32 ? launch<true>(p, n_sm, st) : launch<false>(p, n_sm, st);
+cudaError_t launch_sample(const SampleParams& p, int fp32, cudaStream_t st) {
+    return fp32 ? launch<true>(p, st) : launch<false>(p, st);
 }
 
 }  // namespace gemma

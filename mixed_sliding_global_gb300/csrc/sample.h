@@ -25,6 +25,6 @@ struct SampleParams {
 constexpr int kSampleMaxVocab = 16 * 65535;  // 16 CTAs of a row, 16-bit counters
 // row flags, then the sums
 size_t sample_workspace(int batch, int fp32);
-cudaError_t launch_sample(const SampleParams& p, int fp32, int n_sm, cudaStream_t st);
+cudaError_t launch_sample(const SampleParams& p, int fp32, cudaStream_t st);
 
 }  // namespace gemma
