@@ -664,8 +664,17 @@ int q4_rows(bool append, void* const* k_codes, void* const* k_scales, void* cons
 }
 
 // A step of at most this many rows (token, query head) per KV head attends straight over the
-// 4-bit cache; a longer one over a dequantised copy, on the bf16 kernels.
-constexpr long long kQ4DirectRows = 64;
+// 4-bit cache, which it unpacks once per 16 rows; a longer one over a dequantised copy, on the bf16
+// kernels. Both sides in us (direct, copy), at this many rows and twice that, d = head_dim:
+//   d 64, 16 / 1 heads, 16 x 1000 keys:  15.9, 20.0 and 24.9, 19.7
+//   d 128, 8 / 2, 16 x 4096:             68.8, 76.0 and 121.6, 77.2
+//   d 256, 16 / 8, 4 x window 1024:      31.9, 32.5 and 47.8, 31.9
+//   d 512, 16 / 1, 4 x 4096:             42.1, 92.1 and 63, 77
+// (at d 512 the copy's kernels have few CTAs for so few rows: one sequence of 16,384 keys takes
+// 49 us at 256 rows against 268, 16 sequences of 8192 278 against 172).
+constexpr long long q4_direct_rows(int head_dim) {
+    return head_dim == 512 ? 192 : head_dim == 128 ? 128 : 64;
+}
 
 // CTAs of a step straight over the cache: as many as the GPU holds at once, each with an equal
 // share of the key tiles (fewer when there are fewer tiles); a CTA per unit (sequence, KV head,
@@ -683,10 +692,20 @@ Q4Plan q4_plan(int batch, int kind, int window, int n_q, int n_kv, int head_dim,
     long long reach = kind == GEMMA_GLOBAL ? max_seq_len : (long long)window + n_tok - 1;
     if (reach > max_seq_len) reach = max_seq_len;
     const long long tiles = (reach + 2 * T - 2) / T;  // the first may start before the range
+    const long long typical = (reach + T - 1) / T;
     const long long slots = (long long)n_sm * gemma::kQ4CtasPerSm;
     Q4Plan pl{(int)units, 0, 0, 0, 0};
-    // (the balanced launch counts its tiles in 32 bits per KV head and row tile)
-    if (tiles <= 1 || units >= 16 * slots || batch > 4096 || batch * tiles > (1ll << 30)) return pl;
+    // Equal shares cost a merge launch and the parts' rows (3 to 5 us; 10 to 15 with 400 units at
+    // head_dim 512), one CTA per unit the longest unit's tiles (0.6, 0.9, 1.25, 2.6 us each at
+    // head_dim 64 to 512). Both, shares first, in us: 2 units, head_dim 256: 4 tiles 9.0, 8.8, 8
+    // tiles 9.4, 13.8; 64 units: 8 tiles 14.2, 14.2, 12 tiles 16.9, 19.3; 512 units: 8 tiles 42.5,
+    // 40.9, 12 tiles 55.3, 56.3. head_dim 512: 1 unit: 2 tiles 11.9, 10.6, 4 tiles 11.9, 15.8; 64
+    // units: 6 tiles 23.6, 23.0, 12 tiles 28.4, 37.5, ragged up to 128 tiles 85, 335; 400 units: 8
+    // tiles 84.5, 68.8. And thousands of units need no shares (3200 units: 283, 283).
+    const long long few = (512 / head_dim + 2) * (units < 64 ? 1 : units <= slots ? 2 : 3);
+    if (typical <= few || units >= 16 * slots) return pl;
+    // (a balanced launch counts its tiles in 32 bits per KV head and row tile)
+    if (batch > 4096 || batch * tiles > (1ll << 30)) return pl;
     pl.balanced = 1;
     long long c = units * (tiles + 1) < slots ? units * (tiles + 1) : slots;
     if (c > gemma::kQ4MaxShares) c = gemma::kQ4MaxShares;
@@ -755,7 +774,7 @@ size_t gemma_attn_workspace_size_q4(int batch, gemma_layer_kind kind, int window
     if (batch == 0) return 0;
     const int n_sm = sm_count();
     if (n_sm < 0) return (size_t)-1;
-    if ((long long)n_new * (n_q / n_kv) <= kQ4DirectRows)
+    if ((long long)n_new * (n_q / n_kv) <= q4_direct_rows(head_dim))
         return q4_plan(batch, kind, window, n_q, n_kv, head_dim, max_seq_len, n_new, n_sm).ws_bytes;
     return q4_expand_plan(batch, kind, window, n_q, n_kv, head_dim, max_seq_len, n_new, k_eq_v,
                           n_sm)
@@ -801,7 +820,7 @@ int gemma_attn_q4(void* out, const void* q, const void* const* k_codes,
     const int n_sm = sm_count();
     if (n_sm < 0) return GEMMA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((long long)n_new * (n_q / n_kv) <= kQ4DirectRows) {
+    if ((long long)n_new * (n_q / n_kv) <= q4_direct_rows(head_dim)) {
         const Q4Plan pl =
             q4_plan(batch, kind, window, n_q, n_kv, head_dim, max_seq_len, n_new, n_sm);
         if (pl.ws_bytes > 0 &&
