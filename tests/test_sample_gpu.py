@@ -222,3 +222,34 @@ def test_captured_step(dtype):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out.cpu(), want(x.cpu(), u.cpu().numpy(), p=0.9))
+
+
+@pytest.mark.parametrize("dtype", [synth.BF16, synth.FP32])
+def test_more_rows_than_threads(dtype):
+    """1,500 rows of an odd vocabulary, each with its own filters, good and bad ones."""
+    B, V = 1500, 333
+    x = synth.logits(B, V, seed=77, dtype=dtype)
+    gen = torch.Generator().manual_seed(78)
+    pick = lambda vals: torch.tensor(vals)[torch.randint(0, len(vals), (B,), generator=gen)]  # noqa: E731
+    kw = dict(t=pick([0.0, 0.5, 1.0, -1.0]), k=pick([0, 1, 7, 300]), p=pick([1.0, 0.9, 0.3]),
+              m=pick([0.0, 0.1]))
+    u = uniforms(B, 79)
+    got, err = run(x, u, **kw)
+    assert torch.equal(got, want(x, u, **kw))
+    assert err == g.GEMMA_DEVERR_SAMPLE
+
+
+@pytest.mark.parametrize("n", [1, 31, 1023, 1024, 1025, 40000])
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+def test_crowded_upper_halves(n, softcap):
+    """fp32 logits of which n share their upper 16 bits, with equal ones among them: at, below and
+    above the number that is put in order at once."""
+    V = 50000
+    gen = torch.Generator().manual_seed(n)
+    x = torch.randn(3, V, generator=gen)
+    x[:, 2000:2000 + n] = 2.0 + torch.randint(0, 8000, (3, n), generator=gen) * 2.0 ** -20
+    x = x[:, torch.randperm(V, generator=gen)].contiguous()
+    u = uniforms(3, 6)
+    for kw in (dict(), dict(p=0.5), dict(k=300), dict(k=1000, p=0.9), dict(m=0.3), dict(t=0.2, p=0.8),
+               dict(p=0.9, m=0.999), dict(k=20000, m=0.02)):
+        check(x, u, softcap=softcap, **kw)
