@@ -392,7 +392,7 @@ struct Filters {
 // rows of 70,001 that top_p 0.9 ends within the list: 38.9, 54.3. (With a cap the sum of all weights
 // takes longer than the histograms do: 157, 88.) The n-th largest of a CTA's threads' largest keys bounds
 // the row's n-th largest logit from below, and so does the smallest over the CTAs of each one's
-// (n / C)-th: every CTA sends its slice's keys down to the higher of these bounds to the first one,
+// (n / C)-th: every CTA sends its slice's keys down to the higher of these bounds to one of them,
 // which orders them and walks down their running weights. Without a top_k the sum of all weights is
 // needed too (one evaluation per logit), and the draw may lie beyond the list; lists may also be too
 // long (many equal logits): such rows are left to the kernel below, as are all others.
@@ -404,7 +404,7 @@ struct ListShared {
     u64 part[kListThreads / 32];
     uint32_t upart[kListThreads / 32];
     uint32_t bound[2], largest, n_list;
-    // the first CTA's: entries and weight of each slice, the entries, and in order
+    // the leading CTA's: entries and weight of each slice, the entries, and in order
     uint32_t counts[kMaxCtas];
     u64 sums[kMaxCtas];
     u64 all, pool[kListMax], order[kListK], space[kListSpace];
@@ -420,12 +420,13 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
     pdl_wait();
     Slice<F32, T> r(p, s.exp2, s.part, C);
     const int tid = r.tid, warp = r.warp, lane = r.lane, row = r.row, rank = r.rank;
+    const int lead = row % C;  // (the rows' leaders on different SMs: CTAs of a rank tend to share one)
     Filters f;
     const bool good = f.load(p, row);
     const uint32_t want = f.t == 0.f ? 1u : f.top_k > 0 ? (uint32_t)f.top_k : 0u;
     // (the same in every CTA of the row)
     if (!good || (want ? want > kListK : !F32 || p.softcap > 0.f)) {
-        if (rank == 0 && tid == 0) {
+        if (rank == lead && tid == 0) {
             p.open[row] = good;
             if (!good) {
                 p.token[row] = -1;
@@ -471,7 +472,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
                                __reduce_min_sync(0xffffffffu, low));
     r.key_max = __reduce_max_sync(0xffffffffu, lg);
     const uint32_t floor_key = max(pivot, K::kLow), room = kListSpace / C;
-    const uint32_t space = peer_addr(s.space + rank * room, 0);
+    const uint32_t space = peer_addr(s.space + rank * room, lead);
     // keys down to the bound: falling keys, then rising indices, in one number
     auto take = [&](uint32_t bits, long long at) {
         const uint32_t key = K::of(bits);
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
         }
     }, take);
     const bool need_sum = F32 && !want && r.key_max;
-    if (need_sum || rank == 0) r.zmax = r.capped(K::value(max(r.key_max, K::kLow)));
+    if (need_sum || rank == lead) r.zmax = r.capped(K::value(max(r.key_max, K::kLow)));
     if (need_sum) {
         u64 mine = 0;
         float tiny = 0.f;
@@ -513,12 +514,12 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
         }, add);
         mine += (u64)__float2ll_rn(tiny * 0x1p43f);
         const u64 b = r.sum_before(mine);
-        if (tid == T - 1) st_peer(peer_addr(&s.sums[rank], 0), b + mine);
+        if (tid == T - 1) st_peer(peer_addr(&s.sums[rank], lead), b + mine);
     }
     __syncthreads();
-    if (tid == 0) st_peer(peer_addr(&s.counts[rank], 0), s.n_list);
+    if (tid == 0) st_peer(peer_addr(&s.counts[rank], lead), s.n_list);
     cluster_barrier();
-    if (rank != 0) return;  // (its shared memory is read no more)
+    if (rank != lead) return;  // (its shared memory is read no more)
 
     if (r.key_max == 0) {  // no candidate
         if (tid == 0) {
