@@ -1415,7 +1415,13 @@ cudaError_t launch(const SampleParams& p, cudaStream_t st) {
     // the list can decide rows only if some may have a short top_k (or are fp32 without a cap)
     const int listed = p.top_k != nullptr || (F32 && !(p.softcap > 0.f));
     if (listed) {
-        const int c = (p.vocab + 8191) / 8192, C = c > kMaxCtas ? kMaxCtas : c;
+        // CTAs per row, in us with 1 / 2 / 4 / 8 / 16: bf16 with top_k 200, 262,144 logits: one row
+        // - / 31.2 / 22.3 / 18.2 / 19.0, 64 - / 37.3 / 28.5 / 27.0 / 41.7 (clusters of 16 find few
+        // places), 400 - / 92.7 / 87.3 / 96.7 / 172; 32,000 logits: 64 rows 26.8 / 20.8 / 20.7 /
+        // 21.8 / 36.2, 400 39.4 / 41.9 / 47.3 / 62.9 / 139. fp32, top_k 20, 262,144 logits: one row
+        // - / 42.0 / 27.8 / 20.4 / 17.8.
+        const int slice = p.batch > 100 ? 65536 : 8192, most = F32 && p.batch <= 8 ? kMaxCtas : 8;
+        const int c = (p.vocab + slice - 1) / slice, C = c > most ? most : c;
         cudaError_t e = configure(list_kernel<F32>, lists[dev], 64 * 1024);
         if (e != cudaSuccess) return e;
         // (not ahead of the launch before it: that one's CTAs may fill most SMs, and the lists
