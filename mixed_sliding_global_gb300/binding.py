@@ -13,6 +13,7 @@ from . import _build
 GEMMA_SLIDING, GEMMA_GLOBAL, GEMMA_SLIDING_RING = 0, 1, 2
 GEMMA_BF16, GEMMA_FP32 = 0, 1
 GEMMA_OK = 0
+GEMMA_ERR_INVALID_ARG = -1
 GEMMA_DEVERR_SEQ_LEN, GEMMA_DEVERR_WRITE_POS, GEMMA_DEVERR_TIMEOUT = 1, 2, 4
 GEMMA_DEVERR_N_REAL = 8
 GEMMA_DEVERR_PAGE = 16
@@ -70,12 +71,11 @@ _SIGNATURES = {
                                   _c_size_t, _c_void_p, _c_void_p]),
     "gemma_attn_workspace_size_paged": (_c_size_t, [_c_int, _c_int, _c_int, _c_int, _c_int,
                                                     _c_int, _c_int, _c_int]),
-    "gemma_kv_append_q4": (_c_int, [_PVOID] * 4 + [_PI32, _c_int, _c_int] + [_c_void_p] * 4 +
+    "gemma_kv_append_q4": (_c_int, [_c_void_p] * 5 + [_c_int, _c_int] + [_c_void_p] * 4 +
                            [_c_int] * 10 + [_c_int, _c_void_p, _c_void_p]),
-    "gemma_kv_read_q4": (_c_int, [_PVOID] * 4 + [_PI32, _c_int, _c_int] + [_c_void_p] * 4 +
+    "gemma_kv_read_q4": (_c_int, [_c_void_p] * 5 + [_c_int, _c_int] + [_c_void_p] * 4 +
                          [_c_int] * 10 + [_c_int, _c_void_p, _c_void_p]),
-    "gemma_attn_q4": (_c_int, [_c_void_p, _c_void_p] + [_PVOID] * 4 + [_PI32, _c_int, _c_int] +
-                      [_c_void_p] * 2 + [_c_int] * 13 + [_c_float, _c_float, _c_int, _c_void_p,
+    "gemma_attn_q4": (_c_int, [_c_void_p] * 7 + [_c_int, _c_int] + [_c_void_p] * 2 + [_c_int] * 13 + [_c_float, _c_float, _c_int, _c_void_p,
                                                          _c_size_t, _c_void_p, _c_void_p]),
     "gemma_attn_workspace_size_q4": (_c_size_t, [_c_int] * 9),
     "gemma_logit_softcap_argmax": (_c_int, [_c_void_p, _c_int, _c_int, _c_int, _c_float,
@@ -349,38 +349,49 @@ def gemma_attn_workspace_size_paged(batch: int, kind: int, window: int, n_q: int
     return int(n)
 
 
-_array_types: dict = {}   # (ctypes type, length) -> array type
-
-
-def _array(ctype, n: int):
-    t = _array_types.get((ctype, n))
-    if t is None:
-        t = _array_types[(ctype, n)] = ctype * n
-    return t
-
-
-def _raw_stream(stream, t: torch.Tensor) -> int:
-    """The raw handle of a stream (torch's current one on the tensor's device when None)."""
+def _raw_stream(stream, dev: int) -> int:
+    """The raw handle of a stream (torch's current one on device dev when None)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.device.index)
+        return torch._C._cuda_getCurrentRawStream(dev)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _on_current_device(t: torch.Tensor) -> None:
-    """Launches go to the current device: refuse tensors of another one (and of the CPU)."""
-    if not t.is_cuda:
+def _current(t: torch.Tensor) -> int:
+    """Index of a tensor's device, which must be the current one: launches go there."""
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("expected a CUDA tensor")
-    if t.device.index != torch._C._cuda_getDevice():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError(f"tensors on {t.device}, but the current device is another")
+    return dev
 
 
-def _q4_cache(k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_eq_v, d, n_kv, batch,
-              block_table):
-    """Check the owner layer's 4-bit cache. Returns the C call's arguments: four pointer arrays (only
-    the owner's entry is ever read), the owner map, n_layers, layer; and (block_table, max_pages,
-    page_size, n_pages), capacity."""
+def _on(dev: int, t: Optional[torch.Tensor]) -> Optional[int]:
+    """Address of a contiguous tensor on device dev."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError("expected tensors of one CUDA device")
+    if not t.is_contiguous():
+        raise ValueError("expected a contiguous tensor")
+    return t.data_ptr()
+
+
+_Pointers = ctypes.c_void_p * 4
+_owner_zero = ctypes.c_int32(0)
+_OWNER_ZERO = ctypes.addressof(_owner_zero)
+
+
+def _q4_cache(fn, k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_eq_v, d, n_kv, batch,
+              block_table, of):
+    """Check the owner layer's 4-bit cache, on the device of tensor `of`. The C call sees a model of
+    that one layer: returns its pointers (which must outlive the call), the arguments for them
+    (four pointer arrays, owner map, n_layers, layer), (block_table, max_pages, page_size, n_pages),
+    the capacity and the device."""
     n = len(owner_map)
-    o = int(owner_map[layer])
+    o = int(owner_map[layer]) if 0 <= layer < n else -1
+    if o < 0 or o > layer or owner_map[o] != o:
+        raise GemmaError(fn, GEMMA_ERR_INVALID_ARG)
     kc, ks = k_codes[o], k_scales[o]
     if kc is None or ks is None:
         raise ValueError("the owner layer has no cache")
@@ -389,33 +400,34 @@ def _q4_cache(k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_eq_v, d,
         raise ValueError("codes must be [batch][n_kv][capacity][head_dim / 2]")
     rows, _, slots, _ = shape
     want = (rows, n_kv, slots, d // 64)
-    entries = [kc, ks]
+    vc = vs = None
     if not k_eq_v:
         if v_codes is None or v_scales is None or v_codes[o] is None or v_scales[o] is None:
             raise ValueError("the layer needs a V cache")
-        entries += [v_codes[o], v_scales[o]]
-        if entries[2].shape != shape:
+        vc, vs = v_codes[o], v_scales[o]
+        if vc.shape != shape:
             raise ValueError("codes of K and V must have one shape")
-    arrays = []
-    vp = _array(ctypes.c_void_p, n)
-    for i, x in enumerate(entries):
-        if x.dtype != (torch.bfloat16 if i & 1 else torch.uint8):
+        if vc.dtype != torch.uint8 or vs.dtype != torch.bfloat16:
             raise TypeError("4-bit caches hold uint8 codes and bf16 scales")
-        if i & 1 and x.shape != want:
+        if vs.shape != want:
             raise ValueError("scales must be [batch][n_kv][capacity][head_dim / 64]")
-        arr = vp()
-        arr[o] = _dev_ptr(x)
-        arrays.append(arr)
-    while len(arrays) < 4:
-        arrays.append(vp())
-    head = (*arrays, _array(ctypes.c_int32, n)(*owner_map), n, layer)
+    if kc.dtype != torch.uint8 or ks.dtype != torch.bfloat16:
+        raise TypeError("4-bit caches hold uint8 codes and bf16 scales")
+    if ks.shape != want:
+        raise ValueError("scales must be [batch][n_kv][capacity][head_dim / 64]")
     if block_table is None:
         if rows != batch:
             raise ValueError("the cache must have one entry per sequence")
-        return head, (None, 0, 0, 0), slots
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != batch:
+    elif (block_table.dtype != torch.int32 or block_table.dim() != 2 or
+          block_table.shape[0] != batch):
         raise ValueError("block_table must be int32 [batch][max_pages]")
-    return head, (_dev_ptr(block_table), block_table.shape[1], slots, rows), 0
+    dev = _current(of)
+    p = _Pointers(_on(dev, kc), _on(dev, ks), _on(dev, vc), _on(dev, vs))
+    a = ctypes.addressof(p)
+    head = (a, a + 8, a + 16, a + 24, _OWNER_ZERO, 1, 0)
+    if block_table is None:
+        return p, head, (None, 0, 0, 0), slots, dev
+    return p, head, (_on(dev, block_table), block_table.shape[1], slots, rows), 0, dev
 
 
 def _q4_rows(fn, k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_rows, v_rows, pos, *,
@@ -423,16 +435,15 @@ def _q4_rows(fn, k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_rows,
     B, n, n_kv, d = k_rows.shape
     if pos.dtype != torch.int32 or pos.numel() != B:
         raise ValueError("positions must be int32 [batch]")
-    if not k_eq_v and (v_rows is None or v_rows.shape != k_rows.shape or
-                       v_rows.dtype != k_rows.dtype):
+    if k_eq_v:
+        v_rows = None
+    elif v_rows is None or v_rows.shape != k_rows.shape or v_rows.dtype != k_rows.dtype:
         raise ValueError("K and V rows must have one shape and type")
-    head, pages, cap = _q4_cache(k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_eq_v, d,
-                                 n_kv, B, block_table)
-    _on_current_device(k_rows)
+    keep, head, pages, cap, dev = _q4_cache(fn, k_codes, k_scales, v_codes, v_scales, owner_map,
+                                            layer, k_eq_v, d, n_kv, B, block_table, k_rows)
     st = getattr(library(), fn)(
-        *head, _dev_ptr(k_rows), None if k_eq_v else _dev_ptr(v_rows), _dev_ptr(pos), *pages, B, n,
-        kind, n_kv, d, cap, int(k_eq_v), _dtype(k_rows), _dev_ptr(device_error),
-        _raw_stream(stream, k_rows))
+        *head, _on(dev, k_rows), _on(dev, v_rows), _on(dev, pos), *pages, B, n, kind, n_kv, d, cap,
+        1 if k_eq_v else 0, _dtype(k_rows), _on(dev, device_error), _raw_stream(stream, dev))
     if st:
         _check(fn, st)
 
@@ -478,14 +489,13 @@ def gemma_attn_q4(out: torch.Tensor, q: torch.Tensor, k_codes, k_scales, v_codes
     B, n_new, n_q, d = q.shape
     if seq_lens.dtype != torch.int32 or seq_lens.numel() != B:
         raise ValueError("seq_lens must be int32 [batch]")
-    head, pages, cap = _q4_cache(k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_eq_v, d,
-                                 n_kv, B, block_table)
-    _on_current_device(q)
+    keep, head, pages, cap, dev = _q4_cache("gemma_attn_q4", k_codes, k_scales, v_codes, v_scales,
+                                            owner_map, layer, k_eq_v, d, n_kv, B, block_table, q)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = library().gemma_attn_q4(
-        _dev_ptr(out), _dev_ptr(q), *head, _dev_ptr(seq_lens), *pages, max_seq_len, n_new, B, kind,
-        window, n_q, n_kv, d, int(k_eq_v), cap, scale, softcap, _dtype(q), _dev_ptr(workspace),
-        ws_bytes, _dev_ptr(device_error), _raw_stream(stream, q))
+        _on(dev, out), _on(dev, q), *head, _on(dev, seq_lens), *pages, max_seq_len, n_new, B, kind,
+        window, n_q, n_kv, d, 1 if k_eq_v else 0, cap, scale, softcap, _dtype(q),
+        _on(dev, workspace), ws_bytes, _on(dev, device_error), _raw_stream(stream, dev))
     if st:
         _check("gemma_attn_q4", st)
 
@@ -552,12 +562,12 @@ def gemma_logit_sample(logits: torch.Tensor, token_out: torch.Tensor, uniform: t
                         ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
         if t is not None and (t.dtype != dt or t.numel() != B):
             raise TypeError(f"{name} must be {dt} [batch]")
-    _on_current_device(logits)
+    dev = _current(logits)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = library().gemma_logit_sample(
-        _dev_ptr(logits), B, V, _dtype(logits), softcap, _dev_ptr(temperature), _dev_ptr(top_k),
-        _dev_ptr(top_p), _dev_ptr(min_p), _dev_ptr(uniform), _dev_ptr(token_out),
-        _dev_ptr(workspace), ws_bytes, _dev_ptr(device_error), _raw_stream(stream, logits))
+        _on(dev, logits), B, V, _dtype(logits), softcap, _on(dev, temperature), _on(dev, top_k),
+        _on(dev, top_p), _on(dev, min_p), _on(dev, uniform), _on(dev, token_out),
+        _on(dev, workspace), ws_bytes, _on(dev, device_error), _raw_stream(stream, dev))
     if st:
         _check("gemma_logit_sample", st)
 

@@ -104,6 +104,23 @@ def test_binding_checks_shapes_and_types():
         g.gemma_attn_q4(q, q, [codes], [scales], None, None, [0], 0, lens, 64, **kw)
 
 
+@pytest.mark.parametrize("owner,layer", [([1, 1], 0), ([0, 0, 1], 2), ([0], 1), ([0], -1), ([-1], 0)])
+def test_binding_refuses_bad_owner_maps(owner, layer):
+    """As the C entry points do, whatever the caches hold."""
+    codes, scales = torch.zeros(1, 1, 64, 32, dtype=torch.uint8), torch.zeros(1, 1, 64, 1).bfloat16()
+    q = torch.zeros(1, 1, 4, 64).bfloat16()
+    n = len(owner)
+    with pytest.raises(g.GemmaError) as e:
+        g.gemma_attn_q4(q, q, [codes] * n, [scales] * n, None, None, owner, layer,
+                        torch.ones(1, dtype=torch.int32), 64, kind=1, window=0, n_kv=1,
+                        k_eq_v=True, scale=1.0)
+    assert e.value.status == INVALID
+    with pytest.raises(g.GemmaError) as e:
+        g.gemma_kv_read_q4([codes] * n, [scales] * n, None, None, owner, layer, q[:, :, :1], None,
+                           torch.zeros(1, dtype=torch.int32), k_eq_v=True)
+    assert e.value.status == INVALID
+
+
 def test_reference_format():
     """The tests' quantiser: 7 s >= max > 7 (s minus a step), codes in range, values exact in
     bf16, and packing round-trips."""

@@ -340,3 +340,26 @@ def test_magnitudes_far_from_one(e, n):
     out, mass = R.attention(q.cpu(), kk, vv, [L], GLOBAL, 0, d ** -0.5)
     rel = 2.0 ** -10 + 2.0 ** -13
     assert ((got.double() - out).abs() <= 2.0 ** -8 * out.abs() + rel * mass).all()
+
+
+def test_tensors_of_other_devices_are_refused():
+    """Every tensor of a call has to be on the current device."""
+    cache = [*empty_cache((1, 1, 64), 64), None, None]
+    q = torch.zeros(1, 1, 4, 64, dtype=torch.bfloat16, device="cuda")
+    kw = dict(kind=GLOBAL, window=0, n_kv=1, k_eq_v=True, scale=1.0)
+
+    def call(q=q, cache=cache, lens=i32([1]), **more):
+        g.gemma_attn_q4(torch.empty_like(q), q, *[[x] for x in cache], [0], 0, lens, 64, **kw,
+                        **more)
+
+    call()
+    torch.cuda.synchronize()
+    for bad in (dict(q=q.cpu()), dict(cache=[cache[0].cpu(), *cache[1:]]), dict(lens=i32([1]).cpu()),
+                dict(workspace=torch.empty(64)), dict(device_error=torch.zeros(1).int())):
+        with pytest.raises(ValueError):
+            call(**bad)
+    x, u = torch.zeros(1, 8, device="cuda").bfloat16(), torch.zeros(1, device="cuda")
+    ws = torch.empty(16, dtype=torch.uint8, device="cuda")
+    for bad in (dict(uniform=u.cpu()), dict(top_p=u.cpu()), dict(workspace=ws.cpu())):
+        with pytest.raises(ValueError):
+            g.gemma_logit_sample(x, i32([0]), **{**dict(uniform=u, workspace=ws), **bad})
