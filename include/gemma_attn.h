@@ -366,6 +366,9 @@ int gemma_kv_read_q4(const void* const* k_codes, const void* const* k_scales,
  * cache whose rows were appended first: gemma_attn_decode / gemma_attn_prefill / _paged with K
  * and V the values that the cache stands for, and an optional soft-cap of the scaled scores as in
  * gemma_attn_softcap (0: none). q and out are bf16 (GEMMA_FP32 gives GEMMA_ERR_UNSUPPORTED).
+ * Cache rows outside every query token's keys may hold anything; a NaN group of V at a key that
+ * only some tokens of a call see may reach the others' same 64 columns. V groups whose scale is
+ * below 2^-20 of the largest of the sequence and KV head lose bits.
  * Scratch: gemma_attn_workspace_size_q4(...) bytes; calls that may overlap must not share it. */
 int gemma_attn_q4(void* out, const void* q, const void* const* k_codes,
                   const void* const* k_scales, const void* const* v_codes,
@@ -455,8 +458,8 @@ int gemma_logit_sample(const void* logits, int batch, int vocab, gemma_dtype dty
                        void* workspace, size_t workspace_bytes, uint32_t* device_error,
                        void* stream);
 
-/* Bytes of scratch gemma_logit_sample needs ((size_t)-1 for invalid arguments): 4 per row, and
- * 512 KiB more per row of fp32 logits. */
+/* Bytes of scratch gemma_logit_sample needs ((size_t)-1 for invalid arguments): 4 per row, rounded
+ * up to 16, and 512 KiB more per row of fp32 logits. */
 size_t gemma_logit_sample_workspace_size(int batch, int vocab, gemma_dtype dtype);
 
 /* A static, human-readable name of a gemma_status value. */

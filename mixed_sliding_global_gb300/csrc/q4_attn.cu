@@ -9,17 +9,32 @@
 // numbers code * 2^-24. Scales never touch the codes: K's multiply the fp32 sums of a group of
 // 64 elements, V's multiply P (a warp's output columns all lie in one group).
 //
-// A CTA takes 8 * NQ rows and one chunk of keys, 128 keys at a time: one thread streams code tiles
-// (TMA, 128-byte swizzle for rows of at least 128 bytes) and scales (bulk copies) into a ring of
-// stages; eight warps each take 16 keys of S over all of head_dim (the query fragments stay in
-// registers), exchange P through shared memory (one barrier per tile) and take a 64-column group
-// of O (at head_dim < 512 the warps of a group share out the tile's keys). There is no producer
-// warp: a ninth warp would cost the other eight a third of their registers.
+// A CTA takes 8 * NQ rows and a run of keys, 128 keys at a time. Ten warps: one thread of the first
+// extra warp streams code tiles (TMA, 128-byte swizzle for rows of at least 128 bytes) and scales
+// (bulk copies) into a ring of stages; the second extra warp describes the parts of units that the
+// CTA will meet and turns their queries into fragments, one part ahead; eight warps each take 16
+// keys of S over all of head_dim, exchange P through shared memory (one barrier per tile) and take a
+// 64-column group of O (at head_dim < 512 the warps of a group share out the tile's keys). Two CTAs
+// per SM: 96 registers a thread, which the query fragments leave free up to head_dim 256 (8 rows) or
+// 64 (16 rows); beyond they are read from shared memory for every tile.
 // The softmax reference m is common to the CTA and lazy: it moves only when a score exceeds it by
 // more than 2^8, which the tile's one barrier votes on. P and its product with V's scale are
 // rounded to fp16 (2^-11 each; the output is rounded to bf16, 2^-8); V's scales enter relative to
 // the largest one of the chunk so far, scaled into [2^5, 2^6), so that the product stays in fp16's
 // normal range down to 2^-20 of it. Everything else is fp32.
+//
+// What bounds it. Batch 64, lengths up to 16,385: the ring of 1,024 (16 / 8 heads, head_dim 256, 140
+// MB): 45.8 us, 3.1 TB/s of the 6.8 that a copy reaches; the bf16 cache's kernel takes 88.7 for four
+// times the bytes. The global layer (16 / 1, head_dim 512, K as V, 148 MB): 86 us, 1.7 TB/s, 200
+// TFLOP/s; bf16 120. With the arithmetic left out the same loads take 34 and 51 us, without Q K^T
+// 40 and 69, without P V 40 and 66: the unpacking (two integer instructions per pair of codes, and
+// in P V a permutation per register that pairs keys; the integer pipe is 51% and 57% busy), the
+// tensor pipe (20% and 39%) and their latencies with four warps per scheduler take turns rather
+// than overlap (an instruction issues in half of the cycles). A tile of one CTA alone takes 0.6,
+// 0.9, 1.25 and 2.6 us at head_dim 64 to 512 (8, 8, 8 and 16 rows), the launch 3.5 us besides.
+// Tried and slower: multiplications for the rotations (ring 83 us against 76 then), one CTA per SM
+// with deeper rings (51.6, 88.5), prefetches of later tiles into L2 (50), one box per tile at
+// head_dim 512 (no change).
 #include <cuda_fp16.h>
 
 #include <atomic>
@@ -245,7 +260,8 @@ struct Job {
     int lo_max, hi_min;  // keys that every row of the tile may see
 };
 
-// PAIR: at most four rows (NQ = 1). P V then takes the pair of codes of a word's slot as two
+// PAIR: at most four rows (NQ = 1; the ring above 46.2 us against 52.3 with eight columns of rows,
+// one unit of 4 rows 9.1 against 9.3). P V then takes the pair of codes of a word's slot as two
 // operand elements of one key, weighted (P, 0) in columns 0..3 and (0, P) in columns 4..7: the
 // even and the odd output columns come out side by side and no codes are re-paired across keys.
 template <int D, int NQ, bool PAIR, int MINB>
@@ -399,7 +415,10 @@ __global__ void __launch_bounds__(kThreads, MINB)
                 for (int t = part.t0; t < part.t1; ++t) {
                     uint64_t* bar = &full[s];
                     uint8_t* st = smem + s * stage_bytes;
-                    if (round > 0 && !mbar_wait(&empty[s], (round - 1) & 1, p.err)) return;
+                    if (round > 0 && !mbar_wait(&empty[s], (round - 1) & 1, p.err)) {
+                        left = 0;
+                        break;
+                    }
                     if (++s == S) {
                         s = 0;
                         ++round;
@@ -435,6 +454,11 @@ __global__ void __launch_bounds__(kThreads, MINB)
                                      sbytes, bar);
                     }
                 }
+            }
+            // no copy outlives the CTA, whatever the consumers waited for
+            for (int i = 0; i < S; ++i) {
+                const int uses = round + (i < s ? 1 : 0);
+                if (uses > 0) mbar_wait(&full[i], (uses - 1) & 1, p.err);
             }
         }
         return;
@@ -1060,6 +1084,7 @@ cudaError_t launch(const Q4AttnParams& pp, int C, cudaStream_t st) {
 template <int D>
 cudaError_t launch_d(const Q4AttnParams& p, int C, cudaStream_t st) {
     const int rows = p.r.n_tok * p.r.G;
+    // (8 rows of 16 x 4096 keys: 18.7, 15.8, 13.0 us at head_dim 512, 256, 64; as 16: 22.1, 18.5, 15.2)
     if (rows > 8) return launch<D, 2, false>(p, C, st);
     if (rows > 4) return launch<D, 1, false>(p, C, st);
     return launch<D, 1, true>(p, C, st);
