@@ -1,7 +1,9 @@
 """Build libgemma_attn.so in-tree with nvcc for sm_103a (GB300).
 
 Each translation unit compiles in parallel; the shared library links the CUDA runtime
-statically, so loading it needs no CUDA shared library beyond the driver.
+statically, so loading it needs no CUDA shared library beyond the driver. _bind.so, the native
+half of the Python binding, is the one part compiled against PyTorch's headers (g++), and links
+libgemma_attn.so.
 """
 from __future__ import annotations
 
@@ -10,12 +12,15 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgemma_attn.so")
+BIND_SRC = os.path.join(CSRC, "bind.cpp")
+BIND = os.path.join(PKG, "_bind.so")
 HEADER = os.path.join(ROOT, "include", "gemma_attn.h")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -36,14 +41,45 @@ def sources():
 
 def _deps():
     return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(CSRC, "*.h")) + [HEADER, os.path.abspath(__file__)]
+        glob.glob(os.path.join(CSRC, "*.h")) + [HEADER, BIND_SRC, os.path.abspath(__file__)]
 
 
 def up_to_date(lib: str = LIB) -> bool:
-    if not os.path.exists(lib):
+    if not os.path.exists(lib) or not os.path.exists(BIND):
         return False
-    t = os.path.getmtime(lib)
+    t = min(os.path.getmtime(lib), os.path.getmtime(BIND))
     return all(os.path.getmtime(d) <= t for d in _deps())
+
+
+def _run(cmd, what):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what}:\n{r.stdout}\n{r.stderr}")
+    return r.stdout + r.stderr
+
+
+def _compile_bind() -> str:
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(BUILD, "bind.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC",
+          f"-D_GLIBCXX_USE_CXX11_ABI={abi}", "-I", os.path.dirname(HEADER), "-isystem", inc,
+          "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda,
+          "-isystem", sysconfig.get_paths()["include"], "-c", BIND_SRC, "-o", obj],
+         f"g++ failed for {BIND_SRC}")
+    return obj
+
+
+def _link_bind(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BIND + f".tmp{os.getpid()}"
+    _run([shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libgemma_attn.so",
+          "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
+          "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"], "link of _bind.so failed")
+    os.replace(tmp, BIND)
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -63,13 +99,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        bind = ex.submit(_compile_bind)
         objs = list(ex.map(compile_one, sources()))
+        bind_obj = bind.result()
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [cc, "-shared", *ARCH, "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run([cc, "-shared", *ARCH, "-Xlinker", "-soname=libgemma_attn.so", "-o", tmp, *objs],
+         "link failed")
     os.replace(tmp, LIB)
+    _link_bind(bind_obj)
     return LIB
 
 

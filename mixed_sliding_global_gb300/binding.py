@@ -13,7 +13,6 @@ from . import _build
 GEMMA_SLIDING, GEMMA_GLOBAL, GEMMA_SLIDING_RING = 0, 1, 2
 GEMMA_BF16, GEMMA_FP32 = 0, 1
 GEMMA_OK = 0
-GEMMA_ERR_INVALID_ARG = -1
 GEMMA_DEVERR_SEQ_LEN, GEMMA_DEVERR_WRITE_POS, GEMMA_DEVERR_TIMEOUT = 1, 2, 4
 GEMMA_DEVERR_N_REAL = 8
 GEMMA_DEVERR_PAGE = 16
@@ -71,11 +70,12 @@ _SIGNATURES = {
                                   _c_size_t, _c_void_p, _c_void_p]),
     "gemma_attn_workspace_size_paged": (_c_size_t, [_c_int, _c_int, _c_int, _c_int, _c_int,
                                                     _c_int, _c_int, _c_int]),
-    "gemma_kv_append_q4": (_c_int, [_c_void_p] * 5 + [_c_int, _c_int] + [_c_void_p] * 4 +
+    "gemma_kv_append_q4": (_c_int, [_PVOID] * 4 + [_PI32, _c_int, _c_int] + [_c_void_p] * 4 +
                            [_c_int] * 10 + [_c_int, _c_void_p, _c_void_p]),
-    "gemma_kv_read_q4": (_c_int, [_c_void_p] * 5 + [_c_int, _c_int] + [_c_void_p] * 4 +
+    "gemma_kv_read_q4": (_c_int, [_PVOID] * 4 + [_PI32, _c_int, _c_int] + [_c_void_p] * 4 +
                          [_c_int] * 10 + [_c_int, _c_void_p, _c_void_p]),
-    "gemma_attn_q4": (_c_int, [_c_void_p] * 7 + [_c_int, _c_int] + [_c_void_p] * 2 + [_c_int] * 13 + [_c_float, _c_float, _c_int, _c_void_p,
+    "gemma_attn_q4": (_c_int, [_c_void_p, _c_void_p] + [_PVOID] * 4 + [_PI32, _c_int, _c_int] +
+                      [_c_void_p] * 2 + [_c_int] * 13 + [_c_float, _c_float, _c_int, _c_void_p,
                                                          _c_size_t, _c_void_p, _c_void_p]),
     "gemma_attn_workspace_size_q4": (_c_size_t, [_c_int] * 9),
     "gemma_logit_softcap_argmax": (_c_int, [_c_void_p, _c_int, _c_int, _c_int, _c_float,
@@ -349,103 +349,24 @@ def gemma_attn_workspace_size_paged(batch: int, kind: int, window: int, n_q: int
     return int(n)
 
 
-def _raw_stream(stream, dev: int) -> int:
-    """The raw handle of a stream (torch's current one on device dev when None)."""
+_bind = None
+
+
+def _native():
+    """The native half of the binding (built with the library, and loaded after it)."""
+    global _bind
+    if _bind is None:
+        library()
+        from . import _bind as module
+        _bind = module
+    return _bind
+
+
+def _handle(stream) -> Optional[int]:
+    """The raw handle of a stream (None: torch's current one)."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-
-
-def _current(t: torch.Tensor) -> int:
-    """Index of a tensor's device, which must be the current one: launches go there."""
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError("expected a CUDA tensor")
-    if dev != torch._C._cuda_getDevice():
-        raise ValueError(f"tensors on {t.device}, but the current device is another")
-    return dev
-
-
-def _on(dev: int, t: Optional[torch.Tensor]) -> Optional[int]:
-    """Address of a contiguous tensor on device dev."""
-    if t is None:
         return None
-    if t.get_device() != dev:
-        raise ValueError("expected tensors of one CUDA device")
-    if not t.is_contiguous():
-        raise ValueError("expected a contiguous tensor")
-    return t.data_ptr()
-
-
-_Pointers = ctypes.c_void_p * 4
-_owner_zero = ctypes.c_int32(0)
-_OWNER_ZERO = ctypes.addressof(_owner_zero)
-
-
-def _q4_cache(fn, k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_eq_v, d, n_kv, batch,
-              block_table, of):
-    """Check the owner layer's 4-bit cache, on the device of tensor `of`. The C call sees a model of
-    that one layer: returns its pointers (which must outlive the call), the arguments for them
-    (four pointer arrays, owner map, n_layers, layer), (block_table, max_pages, page_size, n_pages),
-    the capacity and the device."""
-    n = len(owner_map)
-    o = int(owner_map[layer]) if 0 <= layer < n else -1
-    if o < 0 or o > layer or owner_map[o] != o:
-        raise GemmaError(fn, GEMMA_ERR_INVALID_ARG)
-    kc, ks = k_codes[o], k_scales[o]
-    if kc is None or ks is None:
-        raise ValueError("the owner layer has no cache")
-    shape = kc.shape
-    if len(shape) != 4 or shape[1] != n_kv or shape[3] * 2 != d:
-        raise ValueError("codes must be [batch][n_kv][capacity][head_dim / 2]")
-    rows, _, slots, _ = shape
-    want = (rows, n_kv, slots, d // 64)
-    vc = vs = None
-    if not k_eq_v:
-        if v_codes is None or v_scales is None or v_codes[o] is None or v_scales[o] is None:
-            raise ValueError("the layer needs a V cache")
-        vc, vs = v_codes[o], v_scales[o]
-        if vc.shape != shape:
-            raise ValueError("codes of K and V must have one shape")
-        if vc.dtype != torch.uint8 or vs.dtype != torch.bfloat16:
-            raise TypeError("4-bit caches hold uint8 codes and bf16 scales")
-        if vs.shape != want:
-            raise ValueError("scales must be [batch][n_kv][capacity][head_dim / 64]")
-    if kc.dtype != torch.uint8 or ks.dtype != torch.bfloat16:
-        raise TypeError("4-bit caches hold uint8 codes and bf16 scales")
-    if ks.shape != want:
-        raise ValueError("scales must be [batch][n_kv][capacity][head_dim / 64]")
-    if block_table is None:
-        if rows != batch:
-            raise ValueError("the cache must have one entry per sequence")
-    elif (block_table.dtype != torch.int32 or block_table.dim() != 2 or
-          block_table.shape[0] != batch):
-        raise ValueError("block_table must be int32 [batch][max_pages]")
-    dev = _current(of)
-    p = _Pointers(_on(dev, kc), _on(dev, ks), _on(dev, vc), _on(dev, vs))
-    a = ctypes.addressof(p)
-    head = (a, a + 8, a + 16, a + 24, _OWNER_ZERO, 1, 0)
-    if block_table is None:
-        return p, head, (None, 0, 0, 0), slots, dev
-    return p, head, (_on(dev, block_table), block_table.shape[1], slots, rows), 0, dev
-
-
-def _q4_rows(fn, k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_rows, v_rows, pos, *,
-             k_eq_v, kind, block_table, device_error, stream):
-    B, n, n_kv, d = k_rows.shape
-    if pos.dtype != torch.int32 or pos.numel() != B:
-        raise ValueError("positions must be int32 [batch]")
-    if k_eq_v:
-        v_rows = None
-    elif v_rows is None or v_rows.shape != k_rows.shape or v_rows.dtype != k_rows.dtype:
-        raise ValueError("K and V rows must have one shape and type")
-    keep, head, pages, cap, dev = _q4_cache(fn, k_codes, k_scales, v_codes, v_scales, owner_map,
-                                            layer, k_eq_v, d, n_kv, B, block_table, k_rows)
-    st = getattr(library(), fn)(
-        *head, _on(dev, k_rows), _on(dev, v_rows), _on(dev, pos), *pages, B, n, kind, n_kv, d, cap,
-        1 if k_eq_v else 0, _dtype(k_rows), _on(dev, device_error), _raw_stream(stream, dev))
-    if st:
-        _check(fn, st)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def gemma_kv_append_q4(k_codes, k_scales, v_codes, v_scales, owner_map, layer: int,
@@ -459,9 +380,11 @@ def gemma_kv_append_q4(k_codes, k_scales, v_codes, v_scales, owner_map, layer: i
     kind GEMMA_SLIDING_RING wraps the slot, the other kinds write alike."""
     if int(owner_map[layer]) != layer:
         return  # a shared layer writes no cache
-    _q4_rows("gemma_kv_append_q4", k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_new,
-             v_new, write_pos, k_eq_v=k_eq_v, kind=kind, block_table=block_table,
-             device_error=device_error, stream=stream)
+    st = (_bind or _native()).kv_append_q4(
+        k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_new, v_new, write_pos, k_eq_v,
+        kind, block_table, device_error, _handle(stream))
+    if st:
+        _check("gemma_kv_append_q4", st)
 
 
 def gemma_kv_read_q4(k_codes, k_scales, v_codes, v_scales, owner_map, layer: int,
@@ -471,9 +394,11 @@ def gemma_kv_read_q4(k_codes, k_scales, v_codes, v_scales, owner_map, layer: int
                      device_error: Optional[torch.Tensor] = None, stream=None) -> None:
     """The values of rows read_pos[b] + t of a 4-bit cache: k_out, v_out [B][n_rows][n_kv][d],
     bf16 or fp32. Caches as for gemma_kv_append_q4."""
-    _q4_rows("gemma_kv_read_q4", k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_out,
-             v_out, read_pos, k_eq_v=k_eq_v, kind=kind, block_table=block_table,
-             device_error=device_error, stream=stream)
+    st = (_bind or _native()).kv_read_q4(
+        k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_out, v_out, read_pos, k_eq_v,
+        kind, block_table, device_error, _handle(stream))
+    if st:
+        _check("gemma_kv_read_q4", st)
 
 
 def gemma_attn_q4(out: torch.Tensor, q: torch.Tensor, k_codes, k_scales, v_codes, v_scales,
@@ -484,18 +409,9 @@ def gemma_attn_q4(out: torch.Tensor, q: torch.Tensor, k_codes, k_scales, v_codes
                   device_error: Optional[torch.Tensor] = None, stream=None) -> None:
     """Attention over a 4-bit cache (as for gemma_kv_append_q4): q, out bf16 [B][n_new][n_q][d],
     seq_lens int32 [B] counting the new tokens. n_new = 1 is a decode step."""
-    if q.dim() != 4 or out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("q and out must be [batch][n_new][n_q][head_dim] of one type")
-    B, n_new, n_q, d = q.shape
-    if seq_lens.dtype != torch.int32 or seq_lens.numel() != B:
-        raise ValueError("seq_lens must be int32 [batch]")
-    keep, head, pages, cap, dev = _q4_cache("gemma_attn_q4", k_codes, k_scales, v_codes, v_scales,
-                                            owner_map, layer, k_eq_v, d, n_kv, B, block_table, q)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    st = library().gemma_attn_q4(
-        _on(dev, out), _on(dev, q), *head, _on(dev, seq_lens), *pages, max_seq_len, n_new, B, kind,
-        window, n_q, n_kv, d, 1 if k_eq_v else 0, cap, scale, softcap, _dtype(q),
-        _on(dev, workspace), ws_bytes, _on(dev, device_error), _raw_stream(stream, dev))
+    st = (_bind or _native()).attn_q4(
+        k_codes, k_scales, v_codes, v_scales, owner_map, layer, out, q, seq_lens, max_seq_len, kind,
+        window, n_kv, k_eq_v, scale, softcap, block_table, workspace, device_error, _handle(stream))
     if st:
         _check("gemma_attn_q4", st)
 
@@ -554,20 +470,9 @@ def gemma_logit_sample(logits: torch.Tensor, token_out: torch.Tensor, uniform: t
                        device_error: Optional[torch.Tensor] = None, stream=None) -> None:
     """logits [B][V] bf16 or fp32; token_out int32 [B]; uniform, temperature, top_p, min_p fp32
     [B] and top_k int32 [B] on the device (each filter may be None: 1, 1, 0 and 0)."""
-    if logits.dim() != 2:
-        raise ValueError("logits must be [B][V]")
-    B, V = logits.shape
-    for name, t, dt in (("token_out", token_out, torch.int32), ("uniform", uniform, torch.float32),
-                        ("temperature", temperature, torch.float32), ("top_k", top_k, torch.int32),
-                        ("top_p", top_p, torch.float32), ("min_p", min_p, torch.float32)):
-        if t is not None and (t.dtype != dt or t.numel() != B):
-            raise TypeError(f"{name} must be {dt} [batch]")
-    dev = _current(logits)
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    st = library().gemma_logit_sample(
-        _on(dev, logits), B, V, _dtype(logits), softcap, _on(dev, temperature), _on(dev, top_k),
-        _on(dev, top_p), _on(dev, min_p), _on(dev, uniform), _on(dev, token_out),
-        _on(dev, workspace), ws_bytes, _on(dev, device_error), _raw_stream(stream, dev))
+    st = (_bind or _native()).logit_sample(
+        logits, token_out, uniform, temperature, top_k, top_p, min_p, softcap, workspace,
+        device_error, _handle(stream))
     if st:
         _check("gemma_logit_sample", st)
 
