@@ -407,8 +407,11 @@ struct ListShared {
     // the leading CTA's: entries and weight of each slice, the entries, and in order
     uint32_t counts[kMaxCtas];
     u64 sums[kMaxCtas];
-    u64 all, pool[kListMax], order[kListK], space[kListSpace];
+    u64 all;
+    alignas(16) u64 pool[kListMax];  // (also the threads' largest keys, read 16 bytes at a time)
+    u64 order[kListK], space[kListSpace];
 };
+static_assert(offsetof(ListShared, pool) % 16 == 0, "read 16 bytes at a time");
 
 template <bool F32>
 __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p, int C) {
@@ -439,25 +442,28 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
     r.inv_t = f.inverse_t();
     const uint32_t best = r.thread_max();
 
-    // The m-th largest of the threads' keys, 0 if fewer than m threads have one: bit by bit, with
-    // the barrier's own count.
-    auto nth_key = [&](uint32_t m) {
-        uint32_t at = 0;
-#pragma unroll 1
-        for (uint32_t bit = F32 ? 0x80000000u : 0x8000u; bit; bit >>= 1)
-            if (__syncthreads_count(best >= (at | bit)) >= (int)m) at |= bit;
-        return at >= K::kLow ? at : 0u;
-    };
-    const uint32_t own = nth_key(n), share = C > 1 ? nth_key((n + C - 1) / C) : own;
+    // The n-th and the (n / C)-th largest of the threads' keys (0 if fewer threads have one): every
+    // thread counts the larger ones; the thread's number makes them distinct (fp32: in place of the
+    // key's lowest bits, which makes the bound a little lower).
+    uint32_t* tops = reinterpret_cast<uint32_t*>(s.pool);
+    const uint32_t bound = F32 ? best & ~0xffu : best;
+    const uint32_t mine = (F32 ? bound : best << 8) | (T - 1 - tid);
+    tops[tid] = mine;
     const uint32_t mx = __reduce_max_sync(0xffffffffu, best);
     if (lane == 0) s.upart[warp] = mx;
     __syncthreads();
+    uint32_t above = 0;
+#pragma unroll 8
+    for (int k = 0; k < T / 4; ++k) {
+        const uint4 v = reinterpret_cast<const uint4*>(tops)[k];
+        above += (v.x > mine) + (v.y > mine) + (v.z > mine) + (v.w > mine);
+    }
+    if (above == n - 1) s.bound[0] = bound;
+    if (above == (n + C - 1) / C - 1) s.bound[1] = bound;
     if (warp == 0) {
         const uint32_t m = __reduce_max_sync(0xffffffffu, lane < T / 32 ? s.upart[lane] : 0u);
         if (lane == 0) {
             s.largest = m;
-            s.bound[0] = own;
-            s.bound[1] = share;
             s.n_list = 0;
         }
     }
