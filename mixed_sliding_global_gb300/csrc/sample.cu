@@ -211,6 +211,7 @@ struct Shared {
     uint32_t found, key, n;
     u64 m, start;
     uint32_t own_max, index, listed[2];  // fp32, see gather
+    uint16_t rank[kGather];
 };
 
 // A CTA's slice of a row's logits, and the row's weights. T threads.
@@ -263,20 +264,16 @@ struct Slice {
     __device__ F2 weight(uint32_t key) const {
         return key == key_max ? F2{1.f, 0.f} : relative(capped(K::value(key)), zmax);
     }
-    // One weight in units of 2^-43, for sums over all logits (without a cap). Most of a row lies below 2^-24 of the
-    // largest: single precision is enough there (an error of 2^-46 each), and a sum of its own keeps
-    // what is less than a unit.
-    __device__ u64 quick_units(uint32_t key, float& tiny) const {
-        if (key != key_max && !isinf(zmax.h)) {
-            const F2 a = two_sum(K::value(key), -zmax.h);  // (zmax.l is zero without a cap)
-            const float d = __fmul_rn(a.h, inv_t.h);
-            if (d < -17.f) {
-                const float rest = __fmaf_rn(a.h, inv_t.h, -d) + (a.l * inv_t.h + a.h * inv_t.l);
-                if (d > -80.f) tiny += expf(d) * (1.f + rest);
-                return 0;
-            }
-        }
-        return units(weight(key), 1u);
+    // Most of a row lies below 2^-24 of the largest weight: single precision is enough there (an
+    // error of 2^-46 each; without a cap). Adds such a weight to `tiny`, else returns false.
+    __device__ bool tiny_weight(uint32_t key, float& tiny) const {
+        if (key == key_max || isinf(zmax.h)) return false;
+        const F2 a = two_sum(K::value(key), -zmax.h);  // (zmax.l is zero without a cap)
+        const float d = __fmul_rn(a.h, inv_t.h);
+        if (!(d < -17.f)) return false;
+        const float rest = __fmaf_rn(a.h, inv_t.h, -d) + (a.l * inv_t.h + a.h * inv_t.l);
+        if (d > -80.f) tiny += expf(d) * (1.f + rest);
+        return true;
     }
     // n weights in units of 2^-43, rounded
     __device__ u64 units(F2 w, uint32_t n) const {
@@ -346,6 +343,18 @@ struct Slice {
         const float f = fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
         return __float_as_uint(f) >> 16;
     }
+    // How many of the n distinct entries are larger than entry i0 + tid / 4, which is e: four lanes
+    // share an entry.
+    __device__ uint32_t larger(const u64* entries, uint32_t n, uint32_t i0, u64& e) const {
+        const uint32_t i = i0 + tid / 4, q = (n + 3) / 4 | 1u;  // (odd: the lanes' reads in other banks)
+        e = entries[min(i, n - 1)];
+        uint32_t count = 0;
+        const uint32_t j1 = min((tid & 3) * q + q, n);
+#pragma unroll 4
+        for (uint32_t j = (tid & 3) * q; j < j1; ++j) count += entries[j] > e;
+        count += __shfl_xor_sync(0xffffffffu, count, 1);
+        return count + __shfl_xor_sync(0xffffffffu, count, 2);
+    }
     // Inclusive sums over the warp's lanes.
     template <class N>
     __device__ N warp_sums(N x) const {
@@ -403,7 +412,7 @@ struct ListShared {
     float2 exp2[64];
     u64 part[kListThreads / 32];
     uint32_t upart[kListThreads / 32];
-    uint32_t bound[2], largest, n_list;
+    uint32_t bound[2], largest, n_list, n_near;
     // the leading CTA's: entries and weight of each slice, the entries, and in order
     uint32_t counts[kMaxCtas];
     u64 sums[kMaxCtas];
@@ -464,7 +473,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
         const uint32_t m = __reduce_max_sync(0xffffffffu, lane < T / 32 ? s.upart[lane] : 0u);
         if (lane == 0) {
             s.largest = m;
-            s.n_list = 0;
+            s.n_list = s.n_near = 0;
         }
     }
     cluster_barrier();
@@ -508,9 +517,15 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
     if (need_sum) {
         u64 mine = 0;
         float tiny = 0.f;
+        // (those near the largest one, a few per thousand, are weighed together afterwards: in place
+        // one lane's would hold up its warp)
+        uint32_t* near = reinterpret_cast<uint32_t*>(s.pool);
         auto add = [&](uint32_t bits) {
             const uint32_t key = K::of(bits);
-            if (key >= K::kLow && key <= K::kInf) mine += r.quick_units(key, tiny);
+            if (key < K::kLow || key > K::kInf || r.tiny_weight(key, tiny)) return;
+            const uint32_t i = atomicAdd(&s.n_near, 1u);
+            if (i < 2 * kListMax) near[i] = key;
+            else mine += r.units(r.weight(key), 1u);
         };
         r.for_slice([&](uint4 v) {
             add(v.x);
@@ -518,6 +533,9 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
             add(v.z);
             add(v.w);
         }, add);
+        __syncthreads();
+        for (uint32_t i = tid; i < min(s.n_near, 2 * kListMax); i += T)
+            mine += r.units(r.weight(near[i]), 1u);
         mine += (u64)__float2ll_rn(tiny * 0x1p43f);
         const u64 b = r.sum_before(mine);
         if (tid == T - 1) st_peer(peer_addr(&s.sums[rank], lead), b + mine);
@@ -551,12 +569,10 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
     }
     __syncthreads();
     const uint32_t kept_n = min(n, total);
-    for (uint32_t i = tid; i < total; i += T) {
-        const u64 e = s.pool[i];
-        uint32_t before = 0;
-#pragma unroll 8
-        for (uint32_t j = 0; j < total; ++j) before += s.pool[j] > e;
-        if (before < kept_n) s.order[before] = e;
+    for (uint32_t i0 = 0; i0 < total; i0 += T / 4) {
+        u64 e;
+        const uint32_t before = r.larger(s.pool, total, i0, e);
+        if (!(tid & 3) && i0 + tid / 4 < total && before < kept_n) s.order[before] = e;
     }
     __syncthreads();
     const bool have = tid < (int)kept_n;
@@ -919,13 +935,13 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
             pool[tid] = x;
         }
         __syncthreads();
-        uint32_t before = 0;
-        if (e.have) {
-#pragma unroll 8
-            for (uint32_t j = 0; j < n; ++j) before += pool[j] > x;
+        for (uint32_t i0 = 0; i0 < n; i0 += kThreads / 4) {
+            u64 y;
+            const uint32_t before = r.larger(pool, n, i0, y);
+            if (!(tid & 3) && i0 + tid / 4 < n) s.rank[i0 + tid / 4] = (uint16_t)before;
         }
         __syncthreads();
-        if (e.have) pool[before] = x;
+        if (e.have) pool[s.rank[tid]] = x;
         __syncthreads();
         if (e.have) {
             x = pool[tid];
@@ -1374,6 +1390,8 @@ cudaError_t configure(Kernel* kernel, DeviceState& d, int max_smem) {
     return e;
 }
 
+static_assert((sizeof(Shared) + 15) / 16 * 16 + kBins * 2 + (kGroups + 4) / 5 * 128 <= 227 * 1024,
+              "a cluster of five fits");
 size_t row_smem(int C) {
     return (sizeof(Shared) + 15) / 16 * 16 + kBins * 2 +
            (C > 1 ? (size_t)(kGroups + C - 1) / C * 32 * 4 : 0);
