@@ -676,11 +676,10 @@ constexpr long long q4_direct_rows(int head_dim) {
     return head_dim == 512 ? 192 : head_dim == 128 ? 128 : 64;
 }
 
-// CTAs of a step straight over the cache: as many as the GPU holds at once, each with an equal
-// share of the key tiles (fewer when there are fewer tiles); a CTA per unit (sequence, KV head,
-// row tile) when there are many short units per CTA that the GPU holds.
+// CTAs of a step straight over the cache: one or a cluster of them per unit (sequence, KV head, row
+// tile), or as many as the GPU holds at once, each with an equal share of the key tiles.
 struct Q4Plan {
-    int ctas, balanced;
+    int ctas, balanced, cluster;
     size_t o_bytes, info_off, ws_bytes;
 };
 Q4Plan q4_plan(int batch, int kind, int window, int n_q, int n_kv, int head_dim, int max_seq_len,
@@ -694,16 +693,43 @@ Q4Plan q4_plan(int batch, int kind, int window, int n_q, int n_kv, int head_dim,
     const long long tiles = (reach + 2 * T - 2) / T;  // the first may start before the range
     const long long typical = (reach + T - 1) / T;
     const long long slots = (long long)n_sm * gemma::kQ4CtasPerSm;
-    Q4Plan pl{(int)units, 0, 0, 0, 0};
-    // Equal shares cost a merge launch and the parts' rows (3 to 5 us; 10 to 15 with 400 units at
-    // head_dim 512), one CTA per unit the longest unit's tiles (0.6, 0.9, 1.25, 2.6 us each at
-    // head_dim 64 to 512). Both, shares first, in us: 2 units, head_dim 256: 4 tiles 9.0, 8.8, 8
-    // tiles 9.4, 13.8; 64 units: 8 tiles 14.2, 14.2, 12 tiles 16.9, 19.3; 512 units: 8 tiles 42.5,
-    // 40.9, 12 tiles 55.3, 56.3. head_dim 512: 1 unit: 2 tiles 11.9, 10.6, 4 tiles 11.9, 15.8; 64
-    // units: 6 tiles 23.6, 23.0, 12 tiles 28.4, 37.5, ragged up to 128 tiles 85, 335; 400 units: 8
-    // tiles 84.5, 68.8. And thousands of units need no shares (3200 units: 283, 283).
+    Q4Plan pl{(int)units, 0, 1, 0, 0, 0};
+    // Three ways, in us (8 rows, 16 at head_dim 512): one CTA per unit / the best cluster / equal
+    // shares with a merge launch. A tile of a lone CTA takes 0.6, 0.9, 1.25, 2.6 at head_dim 64 to
+    // 512, a cluster's merge about 2, equal shares 4 and the longer the more units.
+    //   head_dim 64, 2 units:    4 tiles 6.1 / 7.0 / 8.3, 8 tiles 8.7 / 7.5 / 8.5, 32 tiles 23 / 9.6 / 8.9
+    //   head_dim 256, 2 units:   2 tiles 6.3 / 7.2 / 8.9, 4 tiles 8.9 / 7.7 / 9.0, 16 tiles 24 / 9.8 /
+    //                            9.1, 64 tiles 84 / 17.5 / 10.6
+    //   head_dim 256, 32 units:  3 tiles 7.8 / 8.7 / 11.6, 8 tiles 14.0 / 10.3 / 12.0, 32 tiles 44 /
+    //                            16.4 / 18.1
+    //   head_dim 256, 128 units: 3 tiles 10.1 / 10.9 / 13.9, 8 tiles 19.2 / 15.1 / 18.3
+    //   head_dim 256, 512 units: 8 tiles 40.9 / - / 42.5, 12 tiles 56.3 / - / 55.3
+    //   head_dim 512, 1 unit:    2 tiles 10.7 / 11.9 / 11.8, 8 tiles 26.8 / 12.1 / 11.9, 64 tiles 175 /
+    //                            30.2 / 14.0
+    //   head_dim 512, 32 units:  3 tiles 14.1 / 15.2 / 17.1, 16 tiles 48.6 / 21.8 / 23.4
+    //   head_dim 512, 64 units of 128 tiles at most: 335 / - / 85; 400 units, 8 tiles: 68.8 / - / 84.5
+    // Thousands of units need no shares (3200 units: 283, 283).
+    const long long tile_ns = head_dim == 512 ? 2600 : head_dim == 256 ? 1250 : head_dim * 7;
+    int most = 1;
+    while (most < gemma::kQ4MaxCluster && units * most * 2 <= slots) most *= 2;
+    // (a whole cache's lengths differ: half of it on average)
+    long long share = units * (typical + 1) / slots / (kind == GEMMA_GLOBAL ? 2 : 1);
+    if (share < 1) share = 1;
+    // (clusters of 8 double up on SMs where there are many of them: 16 units of 8 tiles 10.5 us
+    // against 9.2 by 4 at head_dim 256, 16.9 against 15.0 at 512)
+    if (most == 8 && units > 8 && units < 32 &&
+        (head_dim == 512 || (typical + 3) / 4 <= share + 2600 / tile_ns))
+        most = 4;
+    const long long part = (typical + most - 1) / most;  // tiles of a cluster's CTA
     const long long few = (512 / head_dim + 2) * (units < 64 ? 1 : units <= slots ? 2 : 3);
-    if (typical <= few || units >= 16 * slots) return pl;
+    const bool whole = typical <= few || units >= 16 * slots;
+    if ((typical - part) * tile_ns >= (units < 32 ? 3000 : 3600) &&
+        (whole || part <= share + 2600 / tile_ns)) {
+        while ((typical + pl.cluster - 1) / pl.cluster > part) pl.cluster *= 2;
+        pl.ctas = (int)units * pl.cluster;
+        return pl;
+    }
+    if (whole) return pl;
     // (a balanced launch counts its tiles in 32 bits per KV head and row tile)
     if (batch > 4096 || batch * tiles > (1ll << 30)) return pl;
     pl.balanced = 1;
@@ -855,7 +881,7 @@ int gemma_attn_q4(void* out, const void* q, const void* const* k_codes,
         p.softcap = softcap;
         p.cap_inner = softcap > 0.f ? scale / softcap : 0.f;
         p.cap_log2 = softcap * 1.4426950408889634f;
-        return gemma::launch_q4_attn(p, c, head_dim, batch, pl.ctas, pl.balanced,
+        return gemma::launch_q4_attn(p, c, head_dim, batch, pl.ctas, pl.balanced, pl.cluster,
                                      static_cast<uint8_t*>(workspace) + pl.info_off, s) ==
                        cudaSuccess
                    ? GEMMA_OK

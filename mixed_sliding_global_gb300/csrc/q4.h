@@ -37,15 +37,16 @@ struct Q4Cache {
 // Attention of a few query rows straight over the cache (q4_attn.cu) by C CTAs: with `balanced`
 // each takes an equal share of the launch's key tiles (parts of units meet in p.o_part
 // [C][2][row tile][head_dim] and p.ml_part [C][2][row tile][2], with two ints per unit in info, and
-// are merged by a second launch), else
-// C is the number of units (sequence, KV head, row tile) and each CTA takes one.
+// are merged by a second launch), else `cluster` CTAs (a cluster, which merges its parts through
+// distributed shared memory) take a unit (sequence, KV head, row tile) and C counts all of them.
 constexpr int kQ4KeyTile = 128;
 constexpr int kQ4CtasPerSm = 2;
 constexpr int kQ4MaxShares = 512;  // C of a balanced launch
+constexpr int kQ4MaxCluster = 8;
 // rows (token, query head) per CTA
 inline int q4_row_tile(int rows) { return rows > 8 ? 16 : 8; }
 cudaError_t launch_q4_attn(const RowsParams& p, const Q4Cache& c, int head_dim, int batch, int C,
-                           int balanced, void* info, cudaStream_t st);
+                           int balanced, int cluster, void* info, cudaStream_t st);
 
 cudaError_t launch_q4_append(const Q4Cache& c, const void* k_new, const void* v_new,
                              const int32_t* write_pos, int batch, int n_new, int head_dim,

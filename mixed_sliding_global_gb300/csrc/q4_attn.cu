@@ -9,7 +9,8 @@
 // numbers code * 2^-24. Scales never touch the codes: K's multiply the fp32 sums of a group of
 // 64 elements, V's multiply P (a warp's output columns all lie in one group).
 //
-// A CTA takes 8 * NQ rows and a run of keys, 128 keys at a time. Ten warps: one thread of the first
+// A CTA takes 8 * NQ rows and a run of keys, 128 keys at a time: a unit's (sequence, KV head, row
+// tile), a part of one that its cluster merges, or an equal share of the launch's. Ten warps: one thread of the first
 // extra warp streams code tiles (TMA, 128-byte swizzle for rows of at least 128 bytes) and scales
 // (bulk copies) into a ring of stages; the second extra warp describes the parts of units that the
 // CTA will meet and turns their queries into fragments, one part ahead; eight warps each take 16
@@ -63,7 +64,8 @@ struct Q4AttnParams {
     const __nv_bfloat16* k_scales;
     const __nv_bfloat16* v_scales;
     int batch;
-    int balanced;     // equal shares of the launch's key tiles per CTA (else a CTA per unit)
+    int balanced;     // equal shares of the launch's key tiles per CTA (else whole units)
+    int cluster;      // CTAs that share a unit's tiles, a cluster (1 with equal shares)
     int2* info;       // [units]: {first part row tile, last CTA} of a shared unit, or {-1, -1}
 };
 
@@ -146,6 +148,34 @@ __device__ __forceinline__ bool consumer_vote(bool flag) {
     return r != 0;
 }
 
+__device__ __forceinline__ uint32_t peer_addr(const void* local, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(r)
+                 : "r"(smem_u32(local)), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float2 ld_peer2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];"
+                 : "=f"(v.x), "=f"(v.y)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ float4 ld_peer4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+// Barrier of the cluster's threads that still run, ordering their shared memory.
+__device__ __forceinline__ void cluster_barrier() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
 template <int D>
 struct Q4Layout {
     static constexpr int NG = D / kQ4Group;                     // scale groups per row
@@ -197,6 +227,11 @@ __device__ __forceinline__ long long share_start(long long total, int C, int c) 
 }
 __device__ __forceinline__ int share_of(long long total, int C, long long x) {
     return (int)(((x + 1) * C + total - 1) / total) - 1;
+}
+
+// First of n tiles that CTA `rank` of c takes of a unit (rank c: n).
+__device__ __forceinline__ int cluster_start(int n, int c, int rank) {
+    return (int)((long long)n * rank / c);
 }
 
 // Sum over the CTA's threads of their values before this one, and the total.
@@ -260,14 +295,62 @@ struct Job {
     int lo_max, hi_min;  // keys that every row of the tile may see
 };
 
+// A unit's rows from its cluster of c CTAs (of n tiles in all; a CTA without tiles has no part), the
+// rows in `rows` and their m and l in `ml_rows` of each, through distributed shared memory:
+// M = max m_k, out = sum 2^(m_k - M) O_k / sum 2^(m_k - M) l_k, 16 bytes of O per thread at a time.
+// out: row R = row0 + r of a KV head lies (R / G * n_q + R % G) * D behind it.
+template <int D>
+__device__ __forceinline__ void cluster_merge(const uint8_t* rows, const float2* ml_rows, int c, int n,
+                                           int row0, int n_rows, int G, int n_q,
+                                           __nv_bfloat16* out) {
+    cluster_barrier();
+    for (int i = blockIdx.x % c * (kWarps * 32) + threadIdx.x; i < n_rows * (D / 4);
+         i += c * (kWarps * 32)) {
+        const int r = i / (D / 4), x = i - r * (D / 4);
+        float2 ml[kQ4MaxCluster];
+        float4 v[kQ4MaxCluster];
+        float M = kNoMax;
+#pragma unroll
+        for (int k = 0; k < kQ4MaxCluster; ++k) {
+            ml[k] = make_float2(kNoMax, 0.f);
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k < c && cluster_start(n, c, k + 1) > cluster_start(n, c, k)) {
+                ml[k] = ld_peer2(peer_addr(&ml_rows[r], k));
+                v[k] = ld_peer4(peer_addr(rows, k) + (r * D + x * 4) * 4);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kQ4MaxCluster; ++k) M = fmaxf(M, ml[k].x);
+        float l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kQ4MaxCluster; ++k) {
+            const float w = exp2f(ml[k].x - M);
+            l = fmaf(w, ml[k].y, l);
+            acc.x = fmaf(w, v[k].x, acc.x);
+            acc.y = fmaf(w, v[k].y, acc.y);
+            acc.z = fmaf(w, v[k].z, acc.z);
+            acc.w = fmaf(w, v[k].w, acc.w);
+        }
+        const float il = 1.f / l;
+        const int R = row0 + r, tok = R / G;
+        *reinterpret_cast<uint2*>(out + ((size_t)tok * n_q + R - tok * G) * D + x * 4) =
+            make_uint2(pack_bf16(acc.x * il, acc.y * il), pack_bf16(acc.z * il, acc.w * il));
+    }
+    cluster_barrier();  // no CTA leaves while another reads its shared memory
+}
+
 // PAIR: at most four rows (NQ = 1; the ring above 46.2 us against 52.3 with eight columns of rows,
 // one unit of 4 rows 9.1 against 9.3). P V then takes the pair of codes of a word's slot as two
 // operand elements of one key, weighted (P, 0) in columns 0..3 and (0, P) in columns 4..7: the
 // even and the odd output columns come out side by side and no codes are re-paired across keys.
-template <int D, int NQ, bool PAIR, int MINB>
-__global__ void __launch_bounds__(kThreads, MINB)
+// CLUSTER: several CTAs share a unit (an instantiation of its own: the tile loop's registers would
+// pay for the merge).
+template <int D, int NQ, bool PAIR, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, kQ4CtasPerSm)
     q4_attn_kernel(const __grid_constant__ CUtensorMap kmap,
-                   const __grid_constant__ CUtensorMap vmap, const Q4AttnParams pp) {
+                   const __grid_constant__ CUtensorMap vmap,
+                   const __grid_constant__ Q4AttnParams pp) {
     pdl_launch_dependents();
     using L = Q4Layout<D>;
     constexpr int RT = 8 * NQ;
@@ -288,6 +371,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
     __shared__ __align__(16) uint32_t sQ[QPRE ? 2 : 1][D / 16][32][2 * NQ];
     __shared__ float sMax[kWarps][RT], sSum[kWarps][RT];
     __shared__ __align__(8) float sInv[2][RT];
+    __shared__ __align__(8) float2 sMl[CLUSTER ? RT : 1];  // of a part for its cluster: the rows' m and l
     __shared__ int sScan[kThreads / 32], sAt[3];
     // the part being worked on and the one that the producer prepares
     __shared__ Job sJob[2];
@@ -320,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
     int left;                   // places of this CTA
     long long all = 0, x0 = 0;  // places of the launch, first one of this CTA
     int C = 0;                  // CTAs with a share (no more than places)
-    if (pp.balanced) {
+    if (!CLUSTER && pp.balanced) {
         const int per = (batch + kThreads - 1) / kThreads, b0 = min((int)threadIdx.x * per, batch);
         const int b1 = min(b0 + per, batch);
         int mine = 0, total;
@@ -346,11 +430,13 @@ __global__ void __launch_bounds__(kThreads, MINB)
         walk.enter(p, sAt[0]);
         walk.u = sAt[1];
         walk.t = sAt[2];
-    } else {  // one CTA per unit
-        walk.enter(p, blockIdx.x / upb);
-        walk.u = blockIdx.x % upb;
-        walk.t = -kHead;
-        left = walk.n + kHead;
+    } else {  // a cluster per unit
+        const int c = CLUSTER ? pp.cluster : 1;
+        const int unit = blockIdx.x / c, rank = blockIdx.x - unit * c;
+        walk.enter(p, unit / upb);
+        walk.u = unit % upb;
+        walk.t = rank ? cluster_start(walk.n, c, rank) : -kHead;
+        left = (CLUSTER ? cluster_start(walk.n, c, rank + 1) : walk.n) - walk.t;
         __syncthreads();
     }
 
@@ -490,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, MINB)
             if (n_job >= 2 && !mbar_wait(&job_empty[js], (n_job / 2 - 1) & 1, p.err)) return;
             if (lane == 0) {
                 sJob[js] = j;
-                if (pp.balanced && part.t0 == 0)  // who shares the unit, for the merge
+                if (!CLUSTER && pp.balanced && part.t0 == 0)  // who shares the unit, for the merge
                     pp.info[(part.b * p.n_kv + part.kvh) * n_rt + part.rt] =
                         j.whole ? make_int2(-1, -1)
                                 : make_int2(j.slot, share_of(all, C, first + part.n - 1));
@@ -544,9 +630,9 @@ __global__ void __launch_bounds__(kThreads, MINB)
     for (int n_job = 0;; ++n_job) {
         const int js = n_job & 1;
         // (the vote lets every warp leave together if one gave up waiting)
-        if (consumer_vote(!mbar_wait(&job_full[js], (n_job >> 1) & 1, p.err))) return;
+        if (consumer_vote(!mbar_wait(&job_full[js], (n_job >> 1) & 1, p.err))) break;
         const Job& job = sJob[js];
-        if (job.last) return;
+        if (job.last) break;
         if (bad_length(p, job.part.len)) {
             if (threadIdx.x == 0) report(p.err, GEMMA_DEVERR_SEQ_LEN);
             for (int i = threadIdx.x; i < job.n_rows * (D / 8); i += kWarps * 32)
@@ -932,6 +1018,11 @@ __global__ void __launch_bounds__(kThreads, MINB)
                         *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + row_at(job, r) + x) =
                             make_uint4(pack_bf16(y[0] * il, y[1] * il), pack_bf16(y[2] * il, y[3] * il),
                                        pack_bf16(y[4] * il, y[5] * il), pack_bf16(y[6] * il, y[7] * il));
+                    } else if (CLUSTER) {  // (the stages are done with)
+                        float4* d = reinterpret_cast<float4*>(smem) + (r * D + x) / 4;
+                        d[0] = make_float4(y[0], y[1], y[2], y[3]);
+                        d[1] = make_float4(y[4], y[5], y[6], y[7]);
+                        if (wg == 0 && g == 0) sMl[CLUSTER ? r : 0] = make_float2(m_run[n][c], l);
                     } else {
                         const size_t pr = (size_t)job.slot * RT + r;
                         float4* d = reinterpret_cast<float4*>(p.o_part + pr * D + x);
@@ -946,6 +1037,15 @@ __global__ void __launch_bounds__(kThreads, MINB)
         __syncwarp();
         if (lane == 0) mbar_arrive(&job_empty[js]);
     }
+    if (!CLUSTER) return;
+
+    const int unit = blockIdx.x / pp.cluster, b = unit / upb, u = unit - b * upb;
+    const int row0 = u % n_rt * RT, n = unit_tiles(p, p.seq_lens[b]);
+    // (one tile, or a bad length: one CTA wrote the rows)
+    cluster_merge<D>(smem, sMl, pp.cluster, n, row0, n > 1 ? min(RT, rows_total - row0) : 0, p.G,
+                     p.n_q,
+                     static_cast<__nv_bfloat16*>(p.out) +
+                         ((size_t)b * p.n_tok * p.n_q + u / n_rt * p.G) * D);
 }
 
 // Merge of the rows of units that several CTAs shared: M = max m_c,
@@ -1042,11 +1142,11 @@ bool encode_codes(CUtensorMap* map, const void* base, uint64_t row_bytes, uint64
            CUDA_SUCCESS;
 }
 
-template <int D, int NQ, bool PAIR>
+template <int D, int NQ, bool PAIR, bool CLUSTER>
 cudaError_t launch(const Q4AttnParams& pp, int C, cudaStream_t st) {
     using L = Q4Layout<D>;
     Q4AttnParams p = pp;
-    auto kernel = q4_attn_kernel<D, NQ, PAIR, kQ4CtasPerSm>;
+    auto kernel = q4_attn_kernel<D, NQ, PAIR, CLUSTER>;
     static std::atomic<bool> configured[64];  // per device; the same value every time
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
@@ -1071,7 +1171,21 @@ cudaError_t launch(const Q4AttnParams& pp, int C, cudaStream_t st) {
     if (!encode_codes(&km, p.r.k, L::ROWB, slots, rows) ||
         !encode_codes(&vm, p.r.v, L::ROWB, slots, rows))
         return cudaErrorInvalidValue;
-    cudaError_t e = launch_pdl(kernel, dim3((unsigned)C), dim3(kThreads), smem, st, km, vm, p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)C);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see pdl_wait
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CLUSTER ? 2 : 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, km, vm, p);
     if (e == cudaSuccess && p.balanced) {
         const int rows = p.r.n_tok * p.r.G;
         const int cols = (long long)rows * p.r.n_kv * p.batch >= 256 ? D : 64;
@@ -1085,17 +1199,22 @@ template <int D>
 cudaError_t launch_d(const Q4AttnParams& p, int C, cudaStream_t st) {
     const int rows = p.r.n_tok * p.r.G;
     // (8 rows of 16 x 4096 keys: 18.7, 15.8, 13.0 us at head_dim 512, 256, 64; as 16: 22.1, 18.5, 15.2)
-    if (rows > 8) return launch<D, 2, false>(p, C, st);
-    if (rows > 4) return launch<D, 1, false>(p, C, st);
-    return launch<D, 1, true>(p, C, st);
+    if (rows > 8)
+        return p.cluster > 1 ? launch<D, 2, false, true>(p, C, st)
+                             : launch<D, 2, false, false>(p, C, st);
+    if (rows > 4)
+        return p.cluster > 1 ? launch<D, 1, false, true>(p, C, st)
+                             : launch<D, 1, false, false>(p, C, st);
+    return p.cluster > 1 ? launch<D, 1, true, true>(p, C, st)
+                         : launch<D, 1, true, false>(p, C, st);
 }
 
 }  // namespace
 
 cudaError_t launch_q4_attn(const RowsParams& r, const Q4Cache& c, int head_dim, int batch, int C,
-                           int balanced, void* info, cudaStream_t st) {
+                           int balanced, int cluster, void* info, cudaStream_t st) {
     const Q4AttnParams p{r, c.k_scales, c.v_codes ? c.v_scales : c.k_scales, batch, balanced,
-                         static_cast<int2*>(info)};
+                         cluster, static_cast<int2*>(info)};
     switch (head_dim) {
         case 64: return launch_d<64>(p, C, st);
         case 128: return launch_d<128>(p, C, st);

@@ -312,6 +312,38 @@ def test_invalid_lengths_are_reported_and_zeroed():
                 1e-6).all()
 
 
+@pytest.mark.parametrize("d,n", [(64, 1), (256, 1), (256, 5), (512, 1)])
+def test_units_shared_by_clusters(d, n):
+    """Few sequences, whose key tiles are shared out within clusters: of one tile and of all, with
+    bad lengths among them, and two pages that are none."""
+    lens = [1000, n - 1, n, 1025, 129, 777]
+    c = Cache(6, 1, 1024, d)
+    fill(c, [min(max(x, 0), 1024) for x in lens], GLOBAL)
+    q = rows((6, n, 4, d), 15)
+    got = c.attend(q, lens, GLOBAL, 0, max_len=1024)
+    assert c.err.item() == g.GEMMA_DEVERR_SEQ_LEN
+    assert (got[1] == 0).all() and (got[3] == 0).all()
+    ok = [0, 2, 4, 5]
+    k, v = c.values()
+    out, mass = R.attention(q[ok], k[ok], v[ok], [lens[i] for i in ok], GLOBAL, 0, d ** -0.5)
+    assert ((got[ok].double().cpu() - out).abs() <= 2.0 ** -8 * out.abs() +
+            (2.0 ** -10 + 2.0 ** -13) * mass + 1e-6).all()
+
+    c = Cache(2, 1, 1024, d, page=128)
+    fill(c, [900, 1024], GLOBAL)
+    lost = [int(c.table[0, 3]), int(c.table[1, 7])]
+    c.table[0, 3], c.table[1, 7] = c.n_pages, -1
+    got = c.attend(q[:2], [900, 1024], GLOBAL, 0, max_len=1024)
+    assert c.err.item() == g.GEMMA_DEVERR_PAGE
+    k, v = c.values()
+    c.table[0, 3], c.table[1, 7] = lost
+    for p in lost:
+        k[p], v[p] = 0, 0
+    out, mass = R.attention(q[:2], k, v, [900, 1024], GLOBAL, 0, d ** -0.5, 0.0, c.table, 128)
+    assert ((got.double().cpu() - out).abs() <= 2.0 ** -8 * out.abs() +
+            (2.0 ** -10 + 2.0 ** -13) * mass + 1e-6).all()
+
+
 def test_bad_page_reads_as_zeros():
     for n in (1, 40):
         c = Cache(1, 1, 512, 256, False, page=128)
