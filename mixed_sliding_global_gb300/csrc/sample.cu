@@ -781,11 +781,6 @@ struct Row : Slice<F32, kThreads> {
     }
 };
 
-// floor(a b / c), a b below 2^84
-__device__ __forceinline__ u64 mul_div(u64 a, u64 b, u64 c) {
-    return (u64)((unsigned __int128)a * b / c);
-}
-
 // Draw one row (every CTA of its cluster).
 template <bool F32>
 __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C, int row) {
@@ -1159,13 +1154,15 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
                 const u64 m = s.m, n = s.n;
                 const u64 gap = need > s.start ? need - s.start : 1;
                 u64 i = 0;
-                if (n > 1 && m) {
-                    i = mul_div(gap, n, m);
-                    if (i > 0 && (unsigned __int128)i * m >= (unsigned __int128)gap * n) --i;
-                    if (i > n - 1) i = n - 1;
+                if (n > 1 && m) {  // (an estimate, off by one at most, and exact products)
+                    const unsigned __int128 gn = (unsigned __int128)gap * n;
+                    i = min((u64)((double)gap / (double)m * (double)n), n - 1);
+                    while (i > 0 && (unsigned __int128)i * m >= gn) --i;
+                    while (i < n - 1 && (unsigned __int128)(i + 1) * m < gn) ++i;
                 }
                 s.n = (uint32_t)(i + 1);
-                s.start += i + 1 == n ? m : mul_div(i + 1, m, n);
+                // floor((i + 1) m / n), the quotient's and the remainder's parts apart
+                s.start += i + 1 == n ? m : (i + 1) * (m / n) + (i + 1) * (m % n) / n;
             }
             __syncthreads();
             c.key = s.key;
@@ -1275,20 +1272,20 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
     }
     cluster_barrier();  // no CTA leaves while another reads its shared memory
     if (draw_tie < before || draw_tie >= before + mine) return;
-    // that occurrence within the slice, 16 bytes per thread at a time in the order of the indices
+    // That occurrence within the slice: every thread counts it in a run of 16-byte pieces, and the
+    // one whose run holds it looks again.
     constexpr int E = F32 ? 4 : 8;
     const long long b0 = (long long)row * p.vocab + r.i0, b1 = (long long)row * p.vocab + r.i1;
     const long long end = (long long)p.batch * p.vocab;
-    uint32_t left = draw_tie - before;
-    for (long long v0 = b0 / E; v0 * E < b1; v0 += kThreads) {
-        const long long at = (v0 + tid) * E;
+    auto hits_of = [&](long long v) {  // of piece v, as a bit per element
+        const long long at = v * E;
         uint32_t w[4] = {0u, 0u, 0u, 0u};
         if (at + E <= end) {
-            const uint4 v = reinterpret_cast<const uint4*>(p.logits)[v0 + tid];
-            w[0] = v.x;
-            w[1] = v.y;
-            w[2] = v.z;
-            w[3] = v.w;
+            const uint4 x = reinterpret_cast<const uint4*>(p.logits)[v];
+            w[0] = x.x;
+            w[1] = x.y;
+            w[2] = x.z;
+            w[3] = x.w;
         } else {  // the last elements of the array
             for (int e = 0; e < E && at + e < end; ++e) {
                 if (F32) w[e] = static_cast<const uint32_t*>(p.logits)[at + e];
@@ -1301,18 +1298,26 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
             const uint32_t bits = F32 ? w[e & 3] : w[e / 2] >> 16 * (e & 1) & 0xffffu;
             if (K::of(bits) == draw_key && at + e >= b0 && at + e < b1) hits |= 1u << e;
         }
-        const uint32_t ex = r.sum_before((uint32_t)__popc(hits));
-        if (tid == kThreads - 1) s.n = ex + __popc(hits);
-        __syncthreads();
-        const uint32_t all = s.n;
-        if (left < all) {
-            if (left >= ex && left < ex + __popc(hits)) {
-                for (uint32_t k = left - ex; k > 0; --k) hits &= hits - 1;
-                p.token[row] = (int32_t)(at + __ffs(hits) - 1 - (long long)row * p.vocab);
-            }
+        return hits;
+    };
+    const long long first = b0 / E, last = (b1 + E - 1) / E;
+    const long long run = (last - first + kThreads - 1) / kThreads;
+    const long long v0 = min(first + tid * run, last), v1 = min(v0 + run, last);
+    uint32_t count = 0;
+#pragma unroll 4
+    for (long long v = v0; v < v1; ++v) count += __popc(hits_of(v));
+    const uint32_t ex = r.sum_before(count), left = draw_tie - before;
+    if (left < ex || left >= ex + count) return;
+    uint32_t skip = left - ex;
+    for (long long v = v0; v < v1; ++v) {
+        uint32_t hits = hits_of(v);
+        const uint32_t c = __popc(hits);
+        if (skip < c) {
+            for (; skip > 0; --skip) hits &= hits - 1;
+            p.token[row] = (int32_t)(v * E + __ffs(hits) - 1 - (long long)row * p.vocab);
             return;
         }
-        left -= all;
+        skip -= c;
     }
 }
 
