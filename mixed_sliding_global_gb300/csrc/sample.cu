@@ -44,6 +44,7 @@ constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 65536, kGroups = 2048;  // 32 bins per group
 constexpr int kMaxCtas = 16;
+constexpr uint32_t kListK = 256;  // longest short list
 // what a row costs one CTA, or a cluster, besides counting its slice: in logits of the slice
 constexpr double kAloneCost = 140e3, kClusterCost = 95e3;
 constexpr uint32_t kGather = kThreads;  // fp32: numbers of one upper half that are put in order
@@ -390,6 +391,16 @@ struct Filters {
         u = p.uniform[row];
         return t >= 0.f && isfinite(t) && top_p == top_p && min_p == min_p && u >= 0.f && u < 1.f;
     }
+    // How many of the largest logits draw the row: one, or top_k; 0: it has no such number.
+    __device__ uint32_t want() const {
+        return t == 0.f ? 1u : top_k > 0 ? (uint32_t)top_k : 0u;
+    }
+    // Whether the short list below takes the row on.
+    template <bool F32>
+    __device__ bool listed(float softcap) const {
+        const uint32_t n = want();
+        return n ? n <= kListK : F32 && !(softcap > 0.f);
+    }
     __device__ F2 inverse_t() const {
         return t > 0.f ? F2{1.f, 0.f} / F2{t, 0.f} : F2{0.f, 0.f};
     }
@@ -406,7 +417,7 @@ struct Filters {
 // needed too (one evaluation per logit), and the draw may lie beyond the list; lists may also be too
 // long (many equal logits): such rows are left to the kernel below, as are all others.
 constexpr int kListThreads = 256;
-constexpr uint32_t kListK = 256, kListMax = 1024, kListSpace = 2048;
+constexpr uint32_t kListMax = 1024, kListSpace = 2048;
 
 struct ListShared {
     float2 exp2[64];
@@ -435,9 +446,9 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
     const int lead = row % C;  // (the rows' leaders on different SMs: CTAs of a rank tend to share one)
     Filters f;
     const bool good = f.load(p, row);
-    const uint32_t want = f.t == 0.f ? 1u : f.top_k > 0 ? (uint32_t)f.top_k : 0u;
+    const uint32_t want = f.want();
     // (the same in every CTA of the row)
-    if (!good || (want ? want > kListK : !F32 || p.softcap > 0.f)) {
+    if (!good || !f.listed<F32>(p.softcap)) {
         if (rank == lead && tid == 0) {
             p.open[row] = good;
             if (!good) {
@@ -1321,39 +1332,58 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
     }
 }
 
-// Every cluster draws rows i, i + clusters, ... of those that the list launch left open (all rows
-// without one): the i-th open row is found from the row flags, which nobody changes here.
+// Every cluster draws rows i, i + clusters, ... of those that are its launch's: all (kAlone), those
+// that the list launch left to it (kAfterList), or first those that the lists do not take on, without
+// waiting for them, and then those that they left open (kAhead: the list launch itself started with
+// everything before it complete, and its CTAs leave one by one; the first rows are drawn on the SMs
+// that they have left. 64 mixed rows of 262,144 68.4 -> 61.1 us, but one row with a list 13.9 ->
+// 14.2 and nine fp32 rows 32.3 -> 33.7). The i-th such row is found from the rows' filters and flags,
+// which nobody changes here.
+enum { kAlone, kAfterList, kAhead };
 template <bool F32>
 __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const SampleParams p, int C,
-                                                             int after_list) {
+                                                             int order) {
     pdl_launch_dependents();
     extern __shared__ __align__(16) uint8_t smem[];
     Shared& s = *reinterpret_cast<Shared*>(smem);
     uint32_t* hist = reinterpret_cast<uint32_t*>(smem + (sizeof(Shared) + 15) / 16 * 16);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    pdl_wait();
-    int passed = 0;  // open rows before row b0
-    int i = blockIdx.x / C;
-    for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
-        const int b = b0 + tid;
-        const bool is = b < p.batch && (!after_list || p.open[b]);
-        const unsigned word = __ballot_sync(0xffffffffu, is);
-        if (lane == 0) s.open[warp] = word;
-        __syncthreads();
-        int base = 0, all = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) base += __popc(s.open[w]);
-            all += __popc(s.open[w]);
-        }
-        for (; i < passed + all; i += gridDim.x / C) {
-            if (is && passed + base + __popc(word & ((1u << lane) - 1)) == i) s.row = b;
+    bool lists = false;  // the lists took row b on
+#pragma unroll 1
+    for (int pass = order == kAhead ? 0 : 1; pass < 2; ++pass) {
+        if (pass == 1) pdl_wait();
+        int passed = 0;  // such rows before row b0
+        int i = blockIdx.x / C;
+        for (int b0 = 0; b0 < p.batch; b0 += kThreads) {
+            const int b = b0 + tid;
+            bool is = b < p.batch;
+            if (is && order == kAhead) {
+                if (pass == 0 || p.batch > kThreads) {  // (else as in the first pass)
+                    Filters f;
+                    lists = !f.load(p, b) || f.listed<F32>(p.softcap);
+                }
+                is = pass == 0 ? !lists : lists && p.open[b];
+            } else if (is && order == kAfterList) {
+                is = p.open[b];
+            }
+            const unsigned word = __ballot_sync(0xffffffffu, is);
+            if (lane == 0) s.open[warp] = word;
             __syncthreads();
-            const int row = s.row;
-            draw_row<F32>(p, s, hist, C, row);
-            cluster_barrier();  // (shared memory is used anew)
+            int base = 0, all = 0;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) base += __popc(s.open[w]);
+                all += __popc(s.open[w]);
+            }
+            for (; i < passed + all; i += gridDim.x / C) {
+                if (is && passed + base + __popc(word & ((1u << lane) - 1)) == i) s.row = b;
+                __syncthreads();
+                const int row = s.row;
+                draw_row<F32>(p, s, hist, C, row);
+                cluster_barrier();  // (shared memory is used anew)
+            }
+            passed += all;
+            __syncthreads();
         }
-        passed += all;
-        __syncthreads();
     }
 }
 
@@ -1442,7 +1472,7 @@ cudaError_t launch(const SampleParams& p, cudaStream_t st) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= kDevices) return cudaErrorInvalidDevice;
     // the list can decide rows only if some may have a short top_k (or are fp32 without a cap)
-    const int listed = p.top_k != nullptr || (F32 && !(p.softcap > 0.f));
+    const bool listed = p.top_k != nullptr || (F32 && !(p.softcap > 0.f));
     if (listed) {
         // CTAs per row, in us with 1 / 2 / 4 / 8 / 16: bf16 with top_k 200, 262,144 logits: one row
         // - / 31.2 / 22.3 / 18.2 / 19.0, 64 - / 37.3 / 28.5 / 27.0 / 41.7 (clusters of 16 find few
@@ -1465,7 +1495,8 @@ cudaError_t launch(const SampleParams& p, cudaStream_t st) {
     e = row_ctas<F32>(p, rows[dev], &C, &clusters);
     if (e != cudaSuccess) return e;
     Launch l(clusters, C, kThreads, row_smem(C), true, st);
-    return cudaLaunchKernelEx(&l.cfg, sample_kernel<F32>, p, C, listed);
+    const int order = !listed ? kAlone : p.batch < 16 ? kAfterList : kAhead;
+    return cudaLaunchKernelEx(&l.cfg, sample_kernel<F32>, p, C, order);
 }
 
 }  // namespace
