@@ -368,7 +368,7 @@ int gemma_kv_read_q4(const void* const* k_codes, const void* const* k_scales,
  * gemma_attn_softcap (0: none). q and out are bf16 (GEMMA_FP32 gives GEMMA_ERR_UNSUPPORTED).
  * Cache rows outside every query token's keys may hold anything; a NaN group of V at a key that
  * only some tokens of a call see may reach the others' same 64 columns. V groups whose scale is
- * below 2^-20 of the largest of the sequence and KV head lose bits.
+ * below 2^-19 of the largest of the sequence and KV head lose bits.
  * Scratch: gemma_attn_workspace_size_q4(...) bytes; calls that may overlap must not share it. */
 int gemma_attn_q4(void* out, const void* q, const void* const* k_codes,
                   const void* const* k_scales, const void* const* v_codes,

@@ -18,11 +18,13 @@
 // 64-column group of O (at head_dim < 512 the warps of a group share out the tile's keys). Two CTAs
 // per SM: 96 registers a thread, which the query fragments leave free up to head_dim 256 (8 rows) or
 // 64 (16 rows); beyond they are read from shared memory for every tile.
-// The softmax reference m is common to the CTA and lazy: it moves only when a score exceeds it by
-// more than 2^8, which the tile's one barrier votes on. P and its product with V's scale are
-// rounded to fp16 (2^-11 each; the output is rounded to bf16, 2^-8); V's scales enter relative to
-// the largest one of the chunk so far, scaled into [2^5, 2^6), so that the product stays in fp16's
-// normal range down to 2^-20 of it. Everything else is fp32.
+// The softmax reference m is common to the CTA and lazy: a row's is 2^-6 of its largest weight when
+// it is set, and moves only when a score exceeds it by more than 2^14, which the tile's one barrier
+// votes on. P and its product with V's scale are rounded to fp16 (2^-11 each; the output is rounded
+// to bf16, 2^-8); V's scales enter relative to the largest one of the chunk so far, scaled into
+// [2^-1, 1), so that P and the product stay in fp16's normal range down to 2^-20 of the largest
+// (below, a weight is off by 2^-31 of it: with m at the largest itself, it was 2^-25 from 2^-14 down).
+// Everything else is fp32.
 //
 // What bounds it. Batch 64, lengths up to 16,385: the ring of 1,024 (16 / 8 heads, head_dim 256, 140
 // MB): 45.8 us, 3.1 TB/s of the 6.8 that a copy reaches; the bf16 cache's kernel takes 88.7 for four
@@ -55,7 +57,8 @@ constexpr int kT = kQ4KeyTile;      // keys per tile
 constexpr int kWarps = 8;           // consumer warps per CTA
 constexpr int kThreads = (kWarps + 2) * 32;  // and two that load and prepare for them
 constexpr int kMaxStages = 8;
-constexpr float kLazyLog2 = 8.f;
+constexpr float kTopLog2 = 6.f;    // a row's largest weight when its reference is set
+constexpr float kLazyLog2 = 14.f;  // and the largest before it is set again
 constexpr float kNoMax = -3.0e38f;  // reference before any key (finite: x - kNoMax is no NaN)
 constexpr uint32_t kPairMask = 0x80078007u;
 
@@ -823,8 +826,8 @@ __global__ void __launch_bounds__(kThreads, kQ4CtasPerSm)
                     if (edge && (key < job.lo_all || key >= job.ke)) sb[i] = 0;  // may hold anything
                     mx = max(mx, sb[i]);
                 }
-                // (a NaN scale, exponent 255, leaves NaN in its column group either way)
-                mx = min(__reduce_max_sync(0xffffffffu, mx) >> 7, 254u);
+                // (a NaN scale, exponent 255, leaves NaN in its column group either way; 252 is a scale's largest)
+                mx = min(__reduce_max_sync(0xffffffffu, mx) >> 7, 252u);
                 if ((int)mx > v_exp) {
                     const float a = v_exp - (int)mx < -126
                                         ? 0.f
@@ -837,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, kQ4CtasPerSm)
 #pragma unroll
                             for (int k = 0; k < 4; ++k) o[i][n][k] *= a;
                 }
-                const float f = __uint_as_float((uint32_t)(259 - v_exp) << 23);  // 2^(5-(v_exp-127))
+                const float f = __uint_as_float((uint32_t)(253 - v_exp) << 23);  // 2^(-1-(v_exp-127))
 #pragma unroll
                 for (int i = 0; i < (KW + 31) / 32; ++i)
                     if (i * 32 + lane < KW) {
@@ -868,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, kQ4CtasPerSm)
                         float mx = m_run[n][c];
 #pragma unroll
                         for (int w = 0; w < kWarps; ++w)
-                            mx = fmaxf(mx, sMax[w][n * 8 + 2 * tq + c]);
+                            mx = fmaxf(mx, sMax[w][n * 8 + 2 * tq + c] - kTopLog2);
                         float a = 1.f;
                         if (mx > m_run[n][c]) {
                             a = fast_exp2(m_run[n][c] - mx);  // 0 from kNoMax
@@ -962,10 +965,11 @@ __global__ void __launch_bounds__(kThreads, kQ4CtasPerSm)
                 float l = l_run[n][c];
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-                if (g == 0) sSum[warp][n * 8 + 2 * tq + c] = l;
+                if (g == 0) sSum[warp][n * 8 + 2 * tq + c] = l * 0.015625f;  // 2^-kTopLog2
             }
         // this lane's columns of rows q(n, c): x = wg * 64 + 8 g .. + 7
-        const float f2 = __uint_as_float((uint32_t)(v_exp - 5) << 23);  // 2^(v_exp - 127 - 5)
+        // (2^(v_exp - 127 + 1), and 2^-6 as for l: a largest weight of one keeps V's range)
+        const float f2 = __uint_as_float((uint32_t)(v_exp - 5) << 23);
         float v[NQ][2][8];
 #pragma unroll
         for (int n = 0; n < NQ; ++n)

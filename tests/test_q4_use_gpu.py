@@ -363,3 +363,30 @@ def test_tensors_of_other_devices_are_refused():
     for bad in (dict(uniform=u.cpu()), dict(top_p=u.cpu()), dict(workspace=ws.cpu())):
         with pytest.raises(ValueError):
             g.gemma_logit_sample(x, i32([0]), **{**dict(uniform=u, workspace=ws), **bad})
+
+
+@pytest.mark.parametrize("gap", [8.0, 12.0])
+@pytest.mark.parametrize("d,n_q", [(128, 8), (512, 16)])
+def test_small_weights_behind_a_large_one(d, n_q, gap):
+    """One key with nearly all the weight and a value of zero: what is left are weights of about
+    e^-gap. Each is off by 2^-11 of itself twice, or, below fp16's normal range, by at most 2^-31
+    of the largest weight as such and 2^-30 of it times V's largest scale as a product."""
+    L = 260
+    gen = torch.Generator().manual_seed(d)
+    q = torch.randn(1, 1, n_q, d, generator=gen)
+    q[..., :64] = 1.0                       # the first group sets the score, the others add noise
+    k = torch.randn(1, L, 1, d, generator=gen) * 0.05
+    k[..., :64] = 0.0
+    k[:, 17, :, :64] = gap * math.sqrt(d) / 64
+    v = torch.randn(1, L, 1, d, generator=gen)
+    v[:, 17] = 0.0
+    cache = [*empty_cache((1, 1, 288), d), *empty_cache((1, 1, 288), d)]
+    g.gemma_kv_append_q4(*[[t] for t in cache], [0], 0, k.bfloat16().cuda(), v.bfloat16().cuda(),
+                         i32([0]), k_eq_v=False)
+    got = attend(q.bfloat16().cuda(), cache, [L], GLOBAL, 0, L, 1, False)
+    kk, vv = (R.values(cache[i].cpu(), cache[i + 1].cpu()) for i in (0, 2))
+    out, mass = R.attention(q.bfloat16(), kk, vv, [L], GLOBAL, 0, d ** -0.5)
+    small = L * (2.0 ** -31 + 2.0 ** -30) * vv[:, :, :L].abs().max()
+    assert mass.max() < 260 * math.exp(-gap) * 3      # the large weight carries nothing
+    assert ((got.double() - out).abs() <= 2.0 ** -8 * out.abs() +
+            (2.0 ** -10 + 2.0 ** -13) * mass + small).all()
