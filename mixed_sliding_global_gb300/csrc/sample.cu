@@ -17,7 +17,8 @@
 // the bin's own largest weight, so the order of the additions does not matter). The few hundred
 // logits of a bin that a cut or the draw falls into are gathered and put in order; a bin of more
 // than 1,024 takes the histogram again, over its lower 16 bits (a row of 262,144: 88 us with
-// gathered bins, 190 with histograms of them).
+// gathered bins, 190 with histograms of them; half of it are the weights, not their atomics: sums
+// in shared memory took 97).
 //
 // Rows with a top_k of at most 256 never get there: a launch ahead (list_kernel) draws them from
 // the list of their largest logits, and leaves the others' numbers for the second launch.
@@ -719,7 +720,8 @@ struct Row : Slice<F32, kThreads> {
     // (group g belongs to CTA g % C). Needs every CTA's histogram, leaves them readable. A row's
     // values lie in a few hundred of the 2,048 groups, and a peer's shared memory gives only some
     // 16 bytes a clock: the CTAs first exchange which groups they have, and read no others.
-    __device__ void merge_counts() {
+    // fp32: the weight sums of the groups that the row has start at zero.
+    __device__ void merge_counts(u64* mass = nullptr) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int g = h * kThreads + tid;
@@ -743,6 +745,7 @@ struct Row : Slice<F32, kThreads> {
         for (int k = warp; rank + k * C < kGroups; k += kWarps) {
             const int g = rank + k * C, w = g * 16 + (lane & 15);
             if (!(s.any[g / 32] >> (g & 31) & 1u)) continue;
+            if (mass) mass[g * 32 + lane] = 0ull;
             uint32_t lo = 0, hi = 0;
             // (all loads in flight at once: a peer's memory is a few hundred ns away)
             uint32_t v[kMaxCtas / 2];
@@ -763,6 +766,7 @@ struct Row : Slice<F32, kThreads> {
             const uint32_t sum = __reduce_add_sync(0xffffffffu, lane < 16 ? lo + hi : 0u);
             if (lane < C) st_peer(peer_addr(&s.count[g], lane), sum);
         }
+        if (mass) __threadfence();
         cluster_barrier();
     }
     // count of bin 32 g + i (any CTA's)
@@ -811,11 +815,7 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
     const int want_k = f.top_k;
     r.inv_t = f.inverse_t();
     s.before[tid] = s.before[tid + kThreads] = 0;
-    // fp32: this CTA's share of the row's weight sums starts at zero
     u64* mass = F32 ? p.mass + (size_t)row * kBins : nullptr;
-    if (F32)
-        for (int i = rank * kThreads + tid; i < kBins; i += C * kThreads) mass[i] = 0ull;
-    if (F32) __threadfence();
 
     r.count_slice(0, 0);
     if (F32) {
@@ -827,7 +827,7 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
             if (lane == 0) s.own_max = m;
         }
     }
-    r.merge_counts();
+    r.merge_counts(mass);
 
     // the largest candidate and the number of them
     uint32_t total = 0;
@@ -1061,6 +1061,7 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
             if (bin > bin_max) return 0;
             if (F32) {
                 if (!cut_all && bin <= cut_bin) return bin == cut_bin ? cut_mass : 0;
+                if (!(s.live[g / 32] >> (g & 31) & 1u)) return 0;  // (never set to zero)
                 const u64 v = *reinterpret_cast<volatile u64*>(mass + bin);
                 if (!v) return 0;
                 const F2 w = r.weight(min(bin << 16 | 0xffffu, key_max));
