@@ -212,7 +212,7 @@ struct Shared {
     int top[kWarps];
     uint32_t found, key, n;
     u64 m, start;
-    uint32_t own_max, index, listed[2];  // fp32, see gather
+    uint32_t own_max, index, listed[2], queued[2];  // fp32, see gather and the weights' sums
     uint16_t rank[kGather];
 };
 
@@ -1017,8 +1017,12 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
         // fp32: weights over the lower halves of `at`, of what is kept so far
         uint32_t lower_of = 0xffffffffu;
         auto lower_masses = [&](uint32_t upper) {
-            refine(upper);
             if (lower_of == upper) return;
+            if (at == upper) {  // counted, but the sums gave way to the queue below
+                s.before2[tid] = s.before2[tid + kThreads] = 0;
+                cluster_barrier();
+            }
+            refine(upper);
             for (int q = warp; rank + q * C < kGroups; q += kWarps) {
                 const int g = rank + q * C;
                 if (s.count[g] == 0) continue;
@@ -1037,21 +1041,60 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
             cut_mass = s.before2[kGroups - 1];
         }
         if (F32) {
-            // weights of every number above the cut's bin, relative to its bin's largest
-            auto add = [&](uint32_t bits) {
-                const uint32_t key = K::of(bits);
-                if (key < K::kLow || key > K::kInf) return;
-                const uint32_t bin = key >> 16;
-                if (!cut_all && bin <= cut_bin) return;
-                const uint32_t anchor = min(bin << 16 | 0xffffu, key_max);
+            // Weights of every number above the cut's bin, relative to its bin's largest. Behind a cut
+            // they are few: 2,048 logits at a time, those that count go to a queue and then to all
+            // threads evenly. (64 rows of 32,000 with top_k 1,000: 92 us; evaluated where they were
+            // loaded, 334: every warp ran the long code for a lane or two, each at another place.)
+            const uint32_t* x = static_cast<const uint32_t*>(p.logits) + (long long)row * p.vocab;
+            const int i1 = (int)r.i1;
+            auto load = [&](int i) { return i < i1 ? x[i] : 0x7fffffffu; };  // (NaN: none)
+            auto add = [&](uint32_t key) {
+                const uint32_t anchor = min(key | 0xffffu, key_max);
                 const F2 w = key == anchor ? F2{1.f, 0.f}
                                            : r.relative(r.capped(K::value(key)),
                                                         r.capped(K::value(anchor)));
                 const u64 v = (u64)(__float2ll_rn(w.h * 0x1p40f) + __float2ll_rn(w.l * 0x1p40f));
-                if (v) atomicAdd(mass + bin, v);
+                if (v) atomicAdd(mass + (key >> 16), v);
             };
-            r.for_slice([&](uint4 v) { add(v.x); add(v.y); add(v.z); add(v.w); },
-                        [&](uint32_t bits) { add(bits); });
+            int i0 = (int)r.i0 + tid;
+            uint32_t next[2] = {load(i0), load(i0 + kThreads)};
+            if (cut_all) {
+#pragma unroll 1
+                for (; i0 < i1; i0 += kThreads) {
+                    const uint32_t key = K::of(next[0]);
+                    next[0] = next[1];
+                    next[1] = load(i0 + 2 * kThreads);
+                    if (key >= K::kLow && key <= K::kInf) add(key);
+                }
+            } else {
+                uint32_t* queue = reinterpret_cast<uint32_t*>(s.before2 + kGather);  // [2 kThreads]
+                lower_of = 0xffffffffu;  // (its sums were there)
+                if (tid == 0) s.queued[0] = 0;
+                __syncthreads();
+#pragma unroll 1
+                for (int b0 = (int)r.i0, turn = 0; b0 < i1; b0 += 2 * kThreads, turn ^= 1) {
+                    const uint32_t now[2] = {next[0], next[1]};
+                    i0 += 2 * kThreads;
+                    next[0] = load(i0);
+                    next[1] = load(i0 + kThreads);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t key = K::of(now[h]);
+                        const bool counts = key <= K::kInf && key >> 16 > cut_bin;
+                        const unsigned lanes = __ballot_sync(0xffffffffu, counts);
+                        uint32_t at0 = 0;
+                        if (lane == 0 && lanes) at0 = atomicAdd(&s.queued[turn], __popc(lanes));
+                        at0 = __shfl_sync(0xffffffffu, at0, 0);
+                        if (counts) queue[at0 + __popc(lanes & ((1u << lane) - 1))] = key;
+                    }
+                    __syncthreads();
+                    const uint32_t n = s.queued[turn];
+                    if (tid == 0) s.queued[turn ^ 1] = 0;
+#pragma unroll 1
+                    for (uint32_t k = tid; k < n; k += kThreads) add(queue[k]);
+                    __syncthreads();
+                }
+            }
             __threadfence();  // (the sums lie in global memory)
             cluster_barrier();
         }
