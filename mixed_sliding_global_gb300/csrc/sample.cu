@@ -173,7 +173,7 @@ __constant__ float2 c_exp2[64] = {
 
 // e^x for x <= 0: x = (64 k + i) ln 2 / 64 + r with |r| < 0.0055, e^x = 2^k 2^(i/64) e^r, and e^r by
 // its series, whose first terms keep their error terms (the fifth is below 2^-46). Below -60: 0.
-__device__ __forceinline__ F2 exp_f2(F2 x, const float2* exp2) {
+__device__ __forceinline__ F2 exp_f2_here(F2 x, const float2* exp2) {
     if (!(x.h > -60.f)) return F2{0.f, 0.f};
     const float n = rintf(x.h * 92.332482616893656f);  // 64 / ln 2
     // ln 2 / 64 in four parts of 11 bits and a rest (n has at most 13: the products are exact)
@@ -188,6 +188,10 @@ __device__ __forceinline__ F2 exp_f2(F2 x, const float2* exp2) {
     const float sc = __uint_as_float((uint32_t)(127 + (k >> 6)) << 23);
     return F2{w.h * sc, w.l * sc};
 }
+
+// One copy of it, for the many places that need it once: a row's steps run one after another, and
+// code that is fetched for a single use costs more than the call (9 fp32 rows 31.7 -> 29.7 us).
+__device__ __noinline__ F2 exp_f2(F2 x, const float2* exp2) { return exp_f2_here(x, exp2); }
 
 // A place in a row's order: the tokens above key `key`, and of key itself the first `ties`.
 struct Cut {
@@ -245,23 +249,25 @@ struct Slice {
     }
 
     // z of a logit: c tanh(x / c) = +-c (1 - e) / (1 + e), e = exp(-2 |x| / c)
-    __device__ F2 capped(float x) const {
+    template <bool HERE = false>  // (for loops over all logits)
+    __device__ __forceinline__ F2 capped(float x) const {
         if (!(p.softcap > 0.f)) return F2{x, 0.f};
         const F2 c{p.softcap, 0.f};
         const float a = fabsf(x);
-        const F2 e = exp_f2(F2{a, 0.f} * inner, exp2);
+        const F2 y = F2{a, 0.f} * inner, e = HERE ? exp_f2_here(y, exp2) : exp_f2(y, exp2);
         F2 t = (F2{1.f, 0.f} + F2{-e.h, -e.l}) / (F2{1.f, 0.f} + e);
         if (isinf(x)) t = F2{1.f, 0.f};
         t = t * c;
         return x < 0.f ? F2{-t.h, -t.l} : t;
     }
     // exp((z - top) / T) of a logit z <= top
-    __device__ F2 relative(F2 z, F2 top) const {
+    template <bool HERE = false>
+    __device__ __forceinline__ F2 relative(F2 z, F2 top) const {
         const F2 d = z + F2{-top.h, -top.l};
         if (isinf(top.h)) return F2{isinf(z.h) && z.h > 0.f ? 1.f : 0.f, 0.f};
         if (d.h == 0.f) return F2{1.f, 0.f};
         if (!(d.h > -1e30f)) return F2{0.f, 0.f};
-        return exp_f2(d * inv_t, exp2);
+        return HERE ? exp_f2_here(d * inv_t, exp2) : exp_f2(d * inv_t, exp2);
     }
     __device__ F2 weight(uint32_t key) const {
         return key == key_max ? F2{1.f, 0.f} : relative(capped(K::value(key)), zmax);
@@ -1051,8 +1057,9 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
             auto add = [&](uint32_t key) {
                 const uint32_t anchor = min(key | 0xffffu, key_max);
                 const F2 w = key == anchor ? F2{1.f, 0.f}
-                                           : r.relative(r.capped(K::value(key)),
-                                                        r.capped(K::value(anchor)));
+                                           : r.template relative<true>(
+                                                 r.template capped<true>(K::value(key)),
+                                                 r.template capped<true>(K::value(anchor)));
                 const u64 v = (u64)(__float2ll_rn(w.h * 0x1p40f) + __float2ll_rn(w.l * 0x1p40f));
                 if (v) atomicAdd(mass + (key >> 16), v);
             };
