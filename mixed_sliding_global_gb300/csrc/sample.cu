@@ -16,9 +16,9 @@
 // their upper 16 bits, whose bins' weights are summed into global memory as integers (40 bits below
 // the bin's own largest weight, so the order of the additions does not matter). The few hundred
 // logits of a bin that a cut or the draw falls into are gathered and put in order; a bin of more
-// than 1,024 takes the histogram again, over its lower 16 bits (a row of 262,144: 88 us with
-// gathered bins, 190 with histograms of them; half of it are the weights, not their atomics: sums
-// in shared memory took 97).
+// than 1,024 takes the histogram again, over its lower 16 bits (a row of 262,144, flat
+// and with a cap: 82 us, 190 with histograms of the bins; half of it are the weights, not their
+// atomics: with sums in shared memory it took 9 us longer).
 //
 // Rows with a top_k of at most 256 never get there: a launch ahead (list_kernel) draws them from
 // the list of their largest logits, and leaves the others' numbers for the second launch.
@@ -416,8 +416,8 @@ struct Filters {
 // The short list. A row with a top_k up to kListK, and an fp32 row without one or a cap, is drawn
 // from its n = top_k (kListK) largest logits alone. In us, the list and the histograms: bf16, one
 // row of 262,144: top_k 20 13.3, 27.8; 256 21.7, 24.7; 64 rows: 35.2, 104.8 and 55.0, 94.8; fp32, 9
-// rows of 70,001 that top_p 0.9 ends within the list: 38.9, 54.3. (With a cap the sum of all weights
-// takes longer than the histograms do: 157, 88.) The n-th largest of a CTA's threads' largest keys bounds
+// rows of 70,001 that top_p 0.9 ends within the list: 29.8, 46. (With a cap the sum of all weights
+// took longer than the histograms do: 157, 88.) The n-th largest of a CTA's threads' largest keys bounds
 // the row's n-th largest logit from below, and so does the smallest over the CTAs of each one's
 // (n / C)-th: every CTA sends its slice's keys down to the higher of these bounds to one of them,
 // which orders them and walks down their running weights. Without a top_k the sum of all weights is
@@ -1236,87 +1236,98 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
         Cut end = cut;  // what is kept in the end, and its weight
         bool end_all = cut_all;
         u64 kept = all;
-        if (top_p <= 0.f) {
-            end = Cut{key_max, 1u};
-            end_all = false;
-            kept = r.units(F2{1.f, 0.f}, 1u);
-        } else if (top_p < 1.f) {
-            const double x = (double)top_p * (double)all;
-            u64 need = (u64)ceil(x);
-            place(min(max(need, (u64)1), all), end, kept);
-            end_all = false;
-        }
-        if (min_p > 0.f) {
-            // the smallest key whose weight is at least min_p (the largest candidate's at any rate)
-            if (warp == 0) {
-                uint32_t lo = K::kLow, hi = key_max;
-                while (lo < hi) {
-                    const uint32_t step = max((hi - lo) / 32u, 1u);
-                    const uint32_t off = (uint32_t)(lane + 1) * step;
-                    bool ok = off <= hi - lo;
-                    if (ok) {
-                        const F2 w = r.weight(hi - off);
-                        ok = w.h > min_p || (w.h == min_p && w.l >= 0.f);
-                    }
-                    const unsigned bad = ~__ballot_sync(0xffffffffu, ok);
-                    const uint32_t n = bad ? (uint32_t)__ffs(bad) - 1 : 32u;
-                    const uint32_t past = (n + 1) * step;  // not ok there, or out of range
-                    if (n < 32 && past <= hi - lo) lo = hi - past + 1;
-                    hi -= n * step;
-                    if (step == 1 && n < 32) break;
-                }
-                if (lane == 0) s.key = hi;
-            }
-            __syncthreads();
-            const uint32_t floor_key = s.key;
-            __syncthreads();
-            if (end_all || floor_key > end.key) {
-                // everything from the floor up (its own tokens too, if there are any)
-                const uint32_t bin = F32 ? floor_key >> 16 : floor_key;
-                u64 from = 0;  // fp32: weight of the bin's numbers from the floor up
-                const bool few = gathers(bin);
-                if (few) {
-                    const Entry e = gather(bin);
-                    const u64 m = e.have && e.key >= floor_key && stays(e)
-                                      ? r.units(r.weight(e.key), 1u) : 0;
-                    const u64 run = r.sum_before(m) + m;
-                    if (tid == kThreads - 1) s.m = run;
-                    __syncthreads();
-                    from = s.m;
-                    __syncthreads();
-                } else if (F32) {
-                    lower_masses(bin);
-                }
-                if (warp == 0) {
-                    const int g = (int)(bin / 32), d = kGroups - 1 - g;
-                    const bool above = (uint32_t)(g * 32 + lane) > bin ||
-                                       (!F32 && (uint32_t)(g * 32 + lane) == bin);
-                    u64 m = r.warp_sums(above ? bin_mass(g, lane) : (u64)0);
-                    m = __shfl_sync(0xffffffffu, m, 31) + (d ? s.before[d - 1] : 0);
-                    if (few) {
-                        m += from;
-                    } else if (F32) {
-                        const uint32_t low = floor_key & 0xffffu;
-                        const int g2 = (int)(low / 32), d2 = kGroups - 1 - g2;
-                        const uint32_t key = bin << 16 | (uint32_t)(g2 * 32 + lane);
-                        const uint32_t c = key >= floor_key ? r.bin_count(g2, lane) : 0u;
-                        const u64 x = r.warp_sums(c ? r.units(r.weight(key), c) : (u64)0);
-                        m += __shfl_sync(0xffffffffu, x, 31) + (d2 ? s.before2[d2 - 1] : 0);
-                    }
-                    if (lane == 0) s.m = m;
-                }
-                __syncthreads();
-                kept = min(s.m, all);
-                __syncthreads();
+        // the cut by top_p with min_p's behind it, and then the draw (one copy of the search)
+#pragma unroll 1
+        for (int turn = 0; turn < 2; ++turn) {
+            u64 need = 0;
+            if (turn == 1) {
+                need = min((u64)((double)u * (double)kept) + 1, kept);  // the weight passes u kept
+            } else if (top_p <= 0.f) {
+                end = Cut{key_max, 1u};
                 end_all = false;
+                kept = r.units(F2{1.f, 0.f}, 1u);
+            } else if (top_p < 1.f) {
+                need = min(max((u64)ceil((double)top_p * (double)all), (u64)1), all);
+            }
+            Cut c{0u, 0u};
+            u64 sum = 0;
+            if (need) place(need, c, sum);
+            if (turn == 1) {
+                draw_key = c.key;
+                draw_tie = c.ties - 1;
+                break;
+            }
+            if (need) {
+                end = c;
+                end_all = false;
+                kept = sum;
+            }
+            if (min_p > 0.f) {
+                // the smallest key whose weight is at least min_p (the largest candidate's at any rate)
+                if (warp == 0) {
+                    uint32_t lo = K::kLow, hi = key_max;
+                    while (lo < hi) {
+                        const uint32_t step = max((hi - lo) / 32u, 1u);
+                        const uint32_t off = (uint32_t)(lane + 1) * step;
+                        bool ok = off <= hi - lo;
+                        if (ok) {
+                            const F2 w = r.weight(hi - off);
+                            ok = w.h > min_p || (w.h == min_p && w.l >= 0.f);
+                        }
+                        const unsigned bad = ~__ballot_sync(0xffffffffu, ok);
+                        const uint32_t n = bad ? (uint32_t)__ffs(bad) - 1 : 32u;
+                        const uint32_t past = (n + 1) * step;  // not ok there, or out of range
+                        if (n < 32 && past <= hi - lo) lo = hi - past + 1;
+                        hi -= n * step;
+                        if (step == 1 && n < 32) break;
+                    }
+                    if (lane == 0) s.key = hi;
+                }
+                __syncthreads();
+                const uint32_t floor_key = s.key;
+                __syncthreads();
+                if (end_all || floor_key > end.key) {
+                    // everything from the floor up (its own tokens too, if there are any)
+                    const uint32_t bin = F32 ? floor_key >> 16 : floor_key;
+                    u64 from = 0;  // fp32: weight of the bin's numbers from the floor up
+                    const bool few = gathers(bin);
+                    if (few) {
+                        const Entry e = gather(bin);
+                        const u64 m = e.have && e.key >= floor_key && stays(e)
+                                          ? r.units(r.weight(e.key), 1u) : 0;
+                        const u64 run = r.sum_before(m) + m;
+                        if (tid == kThreads - 1) s.m = run;
+                        __syncthreads();
+                        from = s.m;
+                        __syncthreads();
+                    } else if (F32) {
+                        lower_masses(bin);
+                    }
+                    if (warp == 0) {
+                        const int g = (int)(bin / 32), d = kGroups - 1 - g;
+                        const bool above = (uint32_t)(g * 32 + lane) > bin ||
+                                           (!F32 && (uint32_t)(g * 32 + lane) == bin);
+                        u64 m = r.warp_sums(above ? bin_mass(g, lane) : (u64)0);
+                        m = __shfl_sync(0xffffffffu, m, 31) + (d ? s.before[d - 1] : 0);
+                        if (few) {
+                            m += from;
+                        } else if (F32) {
+                            const uint32_t low = floor_key & 0xffffu;
+                            const int g2 = (int)(low / 32), d2 = kGroups - 1 - g2;
+                            const uint32_t key = bin << 16 | (uint32_t)(g2 * 32 + lane);
+                            const uint32_t c = key >= floor_key ? r.bin_count(g2, lane) : 0u;
+                            const u64 x = r.warp_sums(c ? r.units(r.weight(key), c) : (u64)0);
+                            m += __shfl_sync(0xffffffffu, x, 31) + (d2 ? s.before2[d2 - 1] : 0);
+                        }
+                        if (lane == 0) s.m = m;
+                    }
+                    __syncthreads();
+                    kept = min(s.m, all);
+                    __syncthreads();
+                    end_all = false;
+                }
             }
         }
-        Cut c;
-        u64 sum;
-        const u64 need = (u64)((double)u * (double)kept) + 1;  // the running weight passes u kept
-        place(min(need, kept), c, sum);
-        draw_key = c.key;
-        draw_tie = c.ties - 1;
     }
     if (drawn != 0xffffffffu) {
         if (rank == 0 && tid == 0) p.token[row] = (int32_t)drawn;
