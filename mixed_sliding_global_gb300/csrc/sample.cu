@@ -322,6 +322,35 @@ struct Slice {
         for (long long j = a1 + tid; j < b1; j += T) one(load1(j), j - base);
     }
 
+    // Calls take(bits, index) for the few elements whose key is wanted. bf16: where the largest of
+    // eight is; fp32: from one copy of it for four elements (instructions fetched for a rare use
+    // hold up the other warps).
+    template <class W, class F>
+    __device__ void for_wanted(W wanted, F take) {
+        for_slice_at([&](uint4 v, long long at) {
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            if (!F32) {
+                if (!wanted(K::of(vec_max(v)))) return;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const uint32_t bits = w[e / 2] >> 16 * (e & 1) & 0xffffu;
+                    if (wanted(K::of(bits))) take(bits, at + e);
+                }
+                return;
+            }
+            uint32_t hits = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) hits |= (uint32_t)wanted(K::of(w[e])) << e;
+            while (hits) {
+                const int e = __ffs(hits) - 1;
+                hits &= hits - 1;
+                take(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w, at + e);
+            }
+        }, [&](uint32_t bits, long long at) {
+            if (wanted(K::of(bits))) take(bits, at);
+        });
+    }
+
     // The largest key of this thread's part of the slice (0 if it has no candidate).
     __device__ uint32_t thread_max() {
         uint32_t best = 0;
@@ -416,7 +445,7 @@ struct Filters {
 // The short list. A row with a top_k up to kListK, and an fp32 row without one or a cap, is drawn
 // from its n = top_k (kListK) largest logits alone. In us, the list and the histograms: bf16, one
 // row of 262,144: top_k 20 13.3, 27.8; 256 21.7, 24.7; 64 rows: 35.2, 104.8 and 55.0, 94.8; fp32, 9
-// rows of 70,001 that top_p 0.9 ends within the list: 29.8, 46. (With a cap the sum of all weights
+// rows of 70,001 that top_p 0.9 ends within the list: 28.1, 46. (With a cap the sum of all weights
 // took longer than the histograms do: 157, 88.) The n-th largest of a CTA's threads' largest keys bounds
 // the row's n-th largest logit from below, and so does the smallest over the CTAs of each one's
 // (n / C)-th: every CTA sends its slice's keys down to the higher of these bounds to one of them,
@@ -509,27 +538,10 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
     // keys down to the bound: falling keys, then rising indices, in one number
     auto take = [&](uint32_t bits, long long at) {
         const uint32_t key = K::of(bits);
-        if (key < floor_key || key > K::kInf) return;
         const uint32_t i = atomicAdd(&s.n_list, 1u);
         if (i < room) st_peer(space + 8 * i, (u64)key << 32 | (0xffffffffu - (uint32_t)at));
     };
-    r.for_slice_at([&](uint4 v, long long at) {
-        if (F32) {
-            take(v.x, at);
-            take(v.y, at + 1);
-            take(v.z, at + 2);
-            take(v.w, at + 3);
-        } else {
-            const uint32_t m = K::of(r.vec_max(v));
-            if (m < floor_key || m > K::kInf) return;
-            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                take(w[k] & 0xffffu, at + 2 * k);
-                take(w[k] >> 16, at + 2 * k + 1);
-            }
-        }
-    }, take);
+    r.for_wanted([&](uint32_t key) { return key >= floor_key && key <= K::kInf; }, take);
     const bool need_sum = F32 && !want && r.key_max;
     if (need_sum || rank == lead) r.zmax = r.capped(K::value(max(r.key_max, K::kLow)));
     if (need_sum) {
@@ -538,22 +550,41 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
         // (those near the largest one, a few per thousand, are weighed together afterwards: in place
         // one lane's would hold up its warp)
         uint32_t* near = reinterpret_cast<uint32_t*>(s.pool);
-        auto add = [&](uint32_t bits) {
-            const uint32_t key = K::of(bits);
-            if (key < K::kLow || key > K::kInf || r.tiny_weight(key, tiny)) return;
-            const uint32_t i = atomicAdd(&s.n_near, 1u);
-            if (i < 2 * kListMax) near[i] = key;
-            else mine += r.units(r.weight(key), 1u);
-        };
-        r.for_slice([&](uint4 v) {
-            add(v.x);
-            add(v.y);
-            add(v.z);
-            add(v.w);
-        }, add);
+        const uint32_t* x = static_cast<const uint32_t*>(p.logits) + (long long)row * p.vocab;
+        const int i1 = (int)r.i1;
+        auto load = [&](int i) { return i < i1 ? x[i] : 0x7fffffffu; };  // (NaN: none)
+        int i0 = (int)r.i0 + tid;
+        uint32_t next[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) next[k] = load(i0 + k * T);
+#pragma unroll 1
+        for (; i0 < i1; i0 += 4 * T) {
+            uint32_t now[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                now[k] = K::of(next[k]);
+                next[k] = load(i0 + (4 + k) * T);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t key = now[k];
+                if (key < K::kLow || key > K::kInf || r.tiny_weight(key, tiny)) continue;
+                const uint32_t i = atomicAdd(&s.n_near, 1u);
+                if (i < 2 * kListMax) near[i] = key;
+            }
+        }
         __syncthreads();
-        for (uint32_t i = tid; i < min(s.n_near, 2 * kListMax); i += T)
-            mine += r.units(r.weight(near[i]), 1u);
+        const uint32_t n_near = s.n_near;
+        if (n_near <= 2 * kListMax) {
+            for (uint32_t i = tid; i < n_near; i += T) mine += r.units(r.weight(near[i]), 1u);
+        } else {  // no room: all of them where they lie
+            tiny = 0.f;
+            for (int i = (int)r.i0 + tid; i < i1; i += T) {
+                const uint32_t key = K::of(load(i));
+                if (key >= K::kLow && key <= K::kInf && !r.tiny_weight(key, tiny))
+                    mine += r.units(r.weight(key), 1u);
+            }
+        }
         mine += (u64)__float2ll_rn(tiny * 0x1p43f);
         const u64 b = r.sum_before(mine);
         if (tid == T - 1) st_peer(peer_addr(&s.sums[rank], lead), b + mine);
@@ -920,18 +951,12 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
         const uint32_t per = (uint32_t)((p.vocab + C - 1) / C);
         if (tid == 0) s.listed[buf] = 0;
         __syncthreads();
-        auto take = [&](uint32_t bits, long long at) {
-            const uint32_t key = K::of(bits);
-            if (key >> 16 != upper || key < K::kLow || key > K::kInf) return;
-            const uint32_t i = atomicAdd(&s.listed[buf], 1u);
-            if (i < kGather) list[i] = key << 16 | (0xffffu - (uint32_t)(at - r.i0));
-        };
-        r.for_slice_at([&](uint4 v, long long at) {
-            take(v.x, at);
-            take(v.y, at + 1);
-            take(v.z, at + 2);
-            take(v.w, at + 3);
-        }, take);
+        r.for_wanted(
+            [&](uint32_t key) { return key >> 16 == upper && key >= K::kLow && key <= K::kInf; },
+            [&](uint32_t bits, long long at) {
+                const uint32_t i = atomicAdd(&s.listed[buf], 1u);
+                if (i < kGather) list[i] = K::of(bits) << 16 | (0xffffu - (uint32_t)(at - r.i0));
+            });
         cluster_barrier();
         const uint32_t count = lane < C ? ld_peer(peer_addr(&s.listed[buf], lane)) : 0u;
         const uint32_t ends = r.warp_sums(count);
