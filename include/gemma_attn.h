@@ -435,8 +435,8 @@ size_t gemma_logit_workspace_size(int batch, int vocab);
  *   5. token[b] = the first one whose running sum of weights exceeds uniform[b] times the sum of
  *      what is kept.
  * temperature 0 draws the first of the order. Logits of +infinity leave only themselves (without a
- * cap), with equal weights. Weights and their sums are accurate to about 2^-40, and the result does
- * not depend on scheduling: the same call gives the same tokens.
+ * cap), with equal weights. Weights are accurate to about 2^-40 and their sums to about 2^-35, and
+ * the result does not depend on scheduling: the same call gives the same tokens.
  *   logits      DEVICE [batch][vocab] of dtype, row-major, 16-byte aligned.
  *   temperature, top_k, top_p, min_p
  *               DEVICE float / int32 / float / float [batch], each optional: NULL stands for 1, 0,

@@ -20,11 +20,11 @@
 // and with a cap: 82 us, 190 with histograms of the bins; half of it are the weights, not their
 // atomics: with sums in shared memory it took 9 us longer).
 //
-// Rows with a top_k of at most 256 never get there: a launch ahead (list_kernel) draws them from
-// the list of their largest logits, and leaves the others' numbers for the second launch.
+// Rows with a top_k of at most 256 (and fp32 rows without one or a cap) hardly get there: a launch
+// ahead (list_kernel) draws them from the list of their largest logits, and flags those that it
+// could not decide.
 //
-// What bounds it, per row of 262,144 bf16 logits (16 us for one CTA's loads, 0.08 us at the GPU's
-// rate): latencies. One row with top_k 64: 14.0 us, of it 2.5 for reading the slices and the rest
+// What bounds it, per row of 262,144 bf16 logits (0.08 us at the memory's rate): latencies. One row with top_k 64: 14.0 us, of it 2.5 for reading the slices and the rest
 // barriers of the cluster, the list's order and two launches; a row by histogram: 28 us, of it 3
 // for counting (bound by shared-memory atomics; runs of eight equal logits count as one, so that
 // a row masked with one finite value does not queue on one counter), 4.5 for merging the counts,

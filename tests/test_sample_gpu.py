@@ -1,7 +1,7 @@
 """GPU: sampling against its 64-bit definition (tests/sample_ref.py). Tokens are compared exactly: both
-sides cut and draw at real numbers, the kernel with weights good to about 2^-40, so that a row of a
-few hundred thousand tokens falls on the other side of a boundary about once in 2^20 rows; the
-seeded rows here are a few hundred."""
+sides cut and draw at real numbers, the kernel with weights good to about 2^-40 and sums to 2^-35, so
+that a row falls on the other side of a boundary about once in 2^30 rows; the seeded rows here are a
+few thousand."""
 import numpy as np
 import pytest
 import torch
