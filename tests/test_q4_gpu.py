@@ -8,8 +8,9 @@ the weights carry
   - up to 64 rows (token, query head) per KV head, straight over the cache: the roundings to fp16
     of p and of p times V's scale, 2^-10 A together, and fp32 sums: 2^-13 A covers scores up to 16
     whose exponents are off by 16 log2(e) 2^-24 per addition of eight groups, and the like;
-  - more rows, over a dequantised bf16 copy: the rounding of p to bf16 (2^-8) and that of the
-    normaliser's terms (2^-8), together 2^-7 A; and at head_dim 512 that of half of each score to
+  - more rows, over a dequantised bf16 copy (at head_dim 128 and 512 up to 128 and 192 still
+    directly, well within this): the rounding of p to bf16 (2^-8) and that of the normaliser's
+    terms (2^-8), together 2^-7 A; and at head_dim 512 that of half of each score to
     fp16: scores below 16 move exponents by at most 16 * 2^-11 = 2^-7 and weights by twice that
     with the normaliser, 2^-6 A.
 """
