@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, kQ4CtasPerSm)
                         s = 0;
                         ++round;
                     }
-                    if (bad) {  // no keys: the consumers skip the stage
+                    if (bad) {  // no keys: the stage is passed on empty
                         mbar_arrive(bar);
                         continue;
                     }
@@ -637,6 +637,9 @@ __global__ void __launch_bounds__(kThreads, kQ4CtasPerSm)
         const Job& job = sJob[js];
         if (job.last) break;
         if (bad_length(p, job.part.len)) {
+            // (its stage holds nothing, but counts: consumers that ran past stages not yet given would
+            // take a phase of the ring for another)
+            if (ok) ok = mbar_wait(&full[s], phase, p.err);
             if (threadIdx.x == 0) report(p.err, GEMMA_DEVERR_SEQ_LEN);
             for (int i = threadIdx.x; i < job.n_rows * (D / 8); i += kWarps * 32)
                 *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) +

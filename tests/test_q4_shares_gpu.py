@@ -1,0 +1,100 @@
+"""GPU: 4-bit attention dealt as equal shares of the launch's key tiles, with its merge launch.
+
+A call takes that way where the workspace query asks for scratch although its rows attend straight over
+the cache; every test here asserts that. The bound is test_q4_gpu.py's for such rows:
+2^-8 |out| + (2^-10 + 2^-13) A, A = sum p |v|."""
+import math
+
+import pytest
+import torch
+
+import mixed_sliding_global_gb300 as g
+import q4_ref as R
+
+pytestmark = pytest.mark.gpu
+
+SLIDING, GLOBAL, RING = R.SLIDING, R.GLOBAL, R.RING
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+class Case:
+    """A cache of random 4-bit rows, plain or paged, without the rows behind a sequence's end, which
+    hold NaN."""
+
+    def __init__(self, lens, n_q, n_kv, d, msl, *, k_eq_v=False, page=0, n=1, seed=0):
+        self.lens, self.msl, self.n, self.page, self.k_eq_v = lens, msl, n, page, k_eq_v
+        self.n_kv, self.d = n_kv, d
+        gen = torch.Generator().manual_seed(seed)
+        B, unit = len(lens), page or 32
+        slots = -(-msl // unit) * unit
+        self.table = None
+        shape = (B, n_kv, slots)
+        if page:
+            per = slots // page
+            self.table = torch.randperm(B * per + 2, generator=gen)[:B * per].int().reshape(B, per)
+            shape = (B * per + 2, n_kv, page)
+        self.shape = shape
+        self.t = []
+        for _ in range(1 if k_eq_v else 2):
+            codes = torch.randint(0, 256, shape + (d // 2,), generator=gen, dtype=torch.uint8)
+            # five significant bits; keys of about unit variance
+            s = (16 + torch.randint(0, 16, shape + (d // 64,), generator=gen)).float() / 64
+            self.t += [codes, s.bfloat16()]
+        for b, L in enumerate(lens):
+            at = torch.arange(max(0, L) if L <= msl else 0, slots)
+            where, slot = R.locate(at, b, GLOBAL, slots, self.table, page)
+            for s in self.t[1::2]:
+                s[where, :, slot] = math.nan
+        self.q = torch.randn(B, n, n_q, d, generator=gen).bfloat16()
+
+    def attend(self, kind=GLOBAL, window=0, softcap=0.0, table=None):
+        B, _, n_q, d = self.q.shape
+        args = [[x.cuda()] for x in self.t] + ([[None], [None]] if self.k_eq_v else [])
+        if table is None:
+            table = self.table
+        q, err = self.q.cuda(), i32([0])
+        size = g.gemma_attn_workspace_size_q4(B, kind, window, n_q, self.n_kv, d, self.msl, self.n,
+                                              k_eq_v=self.k_eq_v)
+        assert self.n * n_q // self.n_kv <= 64 and size > 0     # straight over the cache, in shares
+        ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        out = torch.full_like(q, math.nan)
+        g.gemma_attn_q4(out, q, *args, [0], 0, i32(self.lens), self.msl, kind=kind, window=window,
+                        n_kv=self.n_kv, k_eq_v=self.k_eq_v, scale=0.5 * d ** -0.5, softcap=softcap,
+                        block_table=None if table is None else table.cuda(), workspace=ws,
+                        device_error=err)
+        torch.cuda.synchronize()
+        return out.cpu(), err.item()
+
+    def check(self, out, kind=GLOBAL, window=0, softcap=0.0, lost=()):
+        """Against 64 bits; pages in `lost` read as zeros; sequences of a bad length are zero."""
+        good = [b for b, L in enumerate(self.lens) if self.n <= L <= self.msl]
+        v = [R.values(self.t[i], self.t[i + 1]) for i in range(0, len(self.t), 2)]
+        for x in v:
+            for page in lost:
+                x[page] = 0
+        pick = slice(None) if self.page else good
+        table = None if self.table is None else self.table[good]
+        ref, mass = R.attention(self.q[good], v[0][pick], v[-1][pick], [self.lens[b] for b in good],
+                                kind, window, 0.5 * self.d ** -0.5, softcap, table, self.page)
+        err = (out[good].double() - ref).abs()
+        bound = 2.0 ** -8 * ref.abs() + (2.0 ** -10 + 2.0 ** -13) * mass + 1e-6
+        assert torch.isfinite(out).all()
+        assert (err <= bound).all(), (err / bound).max().item()
+        bad = [b for b in range(len(self.lens)) if b not in good]
+        assert (out[bad] == 0).all()
+
+
+@pytest.mark.parametrize("n_q,n_kv,d,k_eq_v,n", [
+    (8, 8, 256, False, 1), (16, 8, 128, False, 3), (16, 2, 512, False, 1), (16, 4, 512, True, 2)])
+def test_runs_of_bad_lengths(n_q, n_kv, d, k_eq_v, n):
+    """Runs of sequences whose length is out of range between valid ones: more units in a row than
+    the ring has stages, none of which has a tile to wait for. The valid ones are as they are."""
+    msl = 2048
+    lens = [msl, 0, -3, msl + 1, 900, 2 ** 31 - 1] + [n - 1, 5000] * 3 + [1300, n] + [-1] * 6 + [2000]
+    c = Case(lens, n_q, n_kv, d, msl, k_eq_v=k_eq_v, n=n, seed=d + n)
+    out, err = c.attend()
+    assert err == g.GEMMA_DEVERR_SEQ_LEN
+    c.check(out)
