@@ -528,6 +528,7 @@ __global__ void __launch_bounds__(kThreads, kQ4CtasPerSm)
                             for (int k = 0; k < L::SCALES / 16; ++k)
                                 reinterpret_cast<uint4*>(st + o * L::OP + L::CODES)[k] =
                                     make_uint4(0u, 0u, 0u, 0u);
+                        fence_proxy_async_smem();  // (a later copy into the stage comes behind them)
                     }
                     mbar_arrive_expect_tx(bar, (uint32_t)nops * (L::CODES + sbytes));
                     for (int o = 0; o < nops; ++o) {

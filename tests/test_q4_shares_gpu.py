@@ -98,3 +98,20 @@ def test_runs_of_bad_lengths(n_q, n_kv, d, k_eq_v, n):
     out, err = c.attend()
     assert err == g.GEMMA_DEVERR_SEQ_LEN
     c.check(out)
+
+
+@pytest.mark.parametrize("n_q,n_kv,d,k_eq_v,n", [(8, 2, 256, False, 1), (16, 1, 512, False, 1)])
+def test_bad_pages_among_good_ones(n_q, n_kv, d, k_eq_v, n):
+    """Pages that are none read as zeros, and the tiles that reuse their stages as what they hold."""
+    lens = [8192, 2000, 8000, 100, 6500, 8192]
+    c = Case(lens, n_q, n_kv, d, 8192, k_eq_v=k_eq_v, page=128, n=n, seed=d + 1)
+    table, lost = c.table.clone(), []
+    gen = torch.Generator().manual_seed(5)
+    for b, L in enumerate(lens):
+        pages = torch.randperm(-(-L // 128), generator=gen)[:9].tolist()
+        for i, page in enumerate(pages[1:]):
+            lost.append(int(table[b, page]))
+            table[b, page] = (-1, c.shape[0], 2 ** 30, -2 ** 31)[i % 4]
+    out, err = c.attend(table=table)
+    assert err == g.GEMMA_DEVERR_PAGE
+    c.check(out, lost=lost)
