@@ -336,7 +336,8 @@ size_t gemma_attn_workspace_size_paged(int batch, gemma_layer_kind kind, int win
  *   kv_capacity is a multiple of 32 (of 128 for GEMMA_SLIDING_RING) and page_size of 128, else
  *   GEMMA_ERR_UNSUPPORTED; kv_capacity is ignored with a block table. block_table (NULL: a plain
  *   or ring cache), max_pages, page_size and n_pages are those of the paged entry points; a
- *   block table with GEMMA_SLIDING_RING gives GEMMA_ERR_INVALID_ARG.
+ *   block table with GEMMA_SLIDING_RING gives GEMMA_ERR_INVALID_ARG. So does a misaligned pointer
+ *   (16 bytes for rows and caches, 4 for positions, lengths, tables and device_error).
  */
 
 /* gemma_kv_append_q4 -- quantise this step's new rows [batch][n_new][n_kv][head_dim] (dtype bf16

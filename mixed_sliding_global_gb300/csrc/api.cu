@@ -4,6 +4,7 @@
 #include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <initializer_list>
 
 #include "../../include/gemma_attn.h"
 #include "attn_internal.h"
@@ -47,6 +48,7 @@ int sm_count() {
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256 || d == 512; }
 bool group_ok(int g) { return g == 1 || g == 2 || g == 4 || g == 8 || g == 16; }
 long long round_up(long long x, long long m) { return (x + m - 1) / m * m; }
@@ -649,7 +651,9 @@ int q4_rows(bool append, void* const* k_codes, void* const* k_scales, void* cons
     if (batch == 0 || n == 0) return GEMMA_OK;
     st = q4_pointers(k_codes, k_scales, v_codes, v_scales, o, k_eq_v, &c);
     if (st != GEMMA_OK) return st;
-    if (!k_rows || !pos || !aligned16(k_rows)) return GEMMA_ERR_INVALID_ARG;
+    if (!k_rows || !pos || !aligned16(k_rows) || !aligned4(pos) || !aligned4(block_table) ||
+        !aligned4(device_error))
+        return GEMMA_ERR_INVALID_ARG;
     if (!k_eq_v && (!v_rows || !aligned16(v_rows))) return GEMMA_ERR_INVALID_ARG;
     const int n_sm = sm_count();
     if (n_sm < 0) return GEMMA_ERR_CUDA;
@@ -842,7 +846,9 @@ int gemma_attn_q4(void* out, const void* q, const void* const* k_codes,
                      const_cast<void* const*>(v_codes), const_cast<void* const*>(v_scales), o,
                      k_eq_v, &c);
     if (st != GEMMA_OK) return st;
-    if (!out || !q || !seq_lens || !aligned16(out) || !aligned16(q)) return GEMMA_ERR_INVALID_ARG;
+    if (!out || !q || !seq_lens || !aligned16(out) || !aligned16(q) ||
+        !aligned4(seq_lens) || !aligned4(block_table) || !aligned4(device_error))
+        return GEMMA_ERR_INVALID_ARG;
     const int n_sm = sm_count();
     if (n_sm < 0) return GEMMA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -918,6 +924,11 @@ int gemma_logit_sample(const void* logits, int batch, int vocab, gemma_dtype dty
     if (batch > 65535 || vocab > gemma::kSampleMaxVocab) return GEMMA_ERR_UNSUPPORTED;
     if (batch == 0) return GEMMA_OK;
     if (!logits || !uniform || !token_out || !aligned16(logits)) return GEMMA_ERR_INVALID_ARG;
+    for (const void* x : {static_cast<const void*>(temperature), static_cast<const void*>(top_k),
+                          static_cast<const void*>(top_p), static_cast<const void*>(min_p),
+                          static_cast<const void*>(uniform), static_cast<const void*>(token_out),
+                          static_cast<const void*>(device_error)})
+        if (!aligned4(x)) return GEMMA_ERR_INVALID_ARG;
     const size_t need = gemma::sample_workspace(batch, dtype == GEMMA_FP32);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
         return GEMMA_ERR_WORKSPACE;

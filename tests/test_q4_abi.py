@@ -135,3 +135,26 @@ def test_reference_format():
     assert torch.equal(val.bfloat16().double(), val)
     assert (val - x.double()).abs().le(s.repeat_interleave(64, -1) / 2).all()
     assert torch.equal(R.values(R.pack(code, torch.signbit(x)), s.bfloat16()), val)
+
+
+def test_misaligned_words_are_refused():
+    """Positions, lengths, block tables and the error word are read and added to as 32-bit words."""
+    args = lambda **kw: {**dict(batch=1, table=None, pos=FAKE, err=FAKE), **kw}  # noqa: E731
+    paged = dict(max_pages=4, page=128, n_pages=8)
+
+    def rows(fn, batch, table, pos, err):
+        p = paged if table else dict(max_pages=0, page=0, n_pages=0)
+        return getattr(lib(), fn)(_ptrs(FAKE), _ptrs(FAKE), _ptrs(None), _ptrs(None), _i32(0), 1, 0,
+                                  FAKE, None, pos, table, *p.values(), batch, 1, 1, 1, 64, 64, 1, 0,
+                                  err, None)
+
+    def attention(batch, table, pos, err):
+        p = paged if table else dict(max_pages=0, page=0, n_pages=0)
+        return lib().gemma_attn_q4(FAKE, FAKE, _ptrs(FAKE), _ptrs(FAKE), _ptrs(None), _ptrs(None),
+                                   _i32(0), 1, 0, pos, table, *p.values(), 64, 1, batch, 1, 0, 4, 1,
+                                   64, 1, 64, 0.125, 0.0, 0, None, 0, err, None)
+
+    for bad in (dict(pos=FAKE + 2), dict(table=FAKE + 1), dict(err=FAKE + 3), dict(err=FAKE + 2)):
+        assert attention(**args(**bad)) == INVALID, bad
+        for fn in ("gemma_kv_append_q4", "gemma_kv_read_q4"):
+            assert rows(fn, **args(**bad)) == INVALID, (fn, bad)

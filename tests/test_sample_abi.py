@@ -68,3 +68,12 @@ def test_reference_definition():
     assert sample_row(x, 63.9 / 86, t=0.5) == 1 and sample_row(x, 64.1 / 86, t=0.5) == 3
     assert sample_row(np.full(3, -np.inf), 0.5) == -1
     assert sample_row(np.array([np.inf, 1, np.inf]), 0.6) == 2
+
+
+@pytest.mark.parametrize("i", range(7))
+def test_misaligned_words_are_refused(i):
+    """Parameters, tokens and the error word are 32-bit words."""
+    p = [FAKE + 2 if j == i else FAKE for j in range(7)]
+    ws = 1 << 20
+    assert lib().gemma_logit_sample(FAKE, 1, 8, 0, 30.0, p[0], p[1], p[2], p[3], p[4], p[5], FAKE, ws,
+                                    p[6], None) == INVALID
