@@ -377,9 +377,8 @@ def gemma_kv_append_q4(k_codes, k_scales, v_codes, v_scales, owner_map, layer: i
     """Quantise rows [B][n_new][n_kv][d] (bf16 or fp32) into a 4-bit cache. Per owner layer: codes
     uint8 [B][n_kv][cap][d / 2] and scales bf16 [B][n_kv][cap][d / 64] (pools
     [n_pages][n_kv][page_size][...] with a block_table int32 [B][max_pages]); write_pos int32 [B];
-    kind GEMMA_SLIDING_RING wraps the slot, the other kinds write alike."""
-    if int(owner_map[layer]) != layer:
-        return  # a shared layer writes no cache
+    kind GEMMA_SLIDING_RING wraps the slot, the other kinds write alike. A layer that shares
+    another's cache writes nothing."""
     st = (_bind or _native()).kv_append_q4(
         k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_new, v_new, write_pos, k_eq_v,
         kind, block_table, device_error, _handle(stream))

@@ -101,28 +101,29 @@ uint32_t* error_word(int dev, PyObject* o) {
     return static_cast<uint32_t*>(on(dev, t));
 }
 
+// The layer whose cache `layer` reads, or -1 for a layer or a map that the C calls refuse.
+int owner_of(PyObject* map, int layer) {
+    const Py_ssize_t n = PySequence_Size(map);
+    if (n < 0) throw Raised{};
+    auto owner = [&](Py_ssize_t i) {
+        Ref r(PySequence_GetItem(map, i));
+        return to_int(r.o);
+    };
+    const int o = layer >= 0 && layer < n ? owner(layer) : -1;
+    return o < 0 || o > layer || owner(o) != o ? -1 : o;
+}
+
 // The owner layer's 4-bit cache as a model of that one layer, and where its rows lie.
 struct Cache {
     void *kc, *ks, *vc, *vs;
     const int32_t zero = 0;
     const int32_t* table = nullptr;
     int max_pages = 0, page = 0, n_pages = 0, cap = 0, dev = 0;
-    bool owner_ok = false;
     Ref held[4];
 
-    // a: k_codes, k_scales, v_codes, v_scales, owner_map, layer
-    Cache(PyObject* const* a, bool k_eq_v, int64_t d, int64_t n_kv, int64_t batch, PyObject* table_,
+    // a: k_codes, k_scales, v_codes, v_scales; o: the owner layer
+    Cache(PyObject* const* a, int o, bool k_eq_v, int64_t d, int64_t n_kv, int64_t batch, PyObject* table_,
           const at::Tensor& of) {
-        const Py_ssize_t n = PySequence_Size(a[4]);
-        if (n < 0) throw Raised{};
-        const int layer = to_int(a[5]);
-        auto owner = [&](Py_ssize_t i) {
-            Ref r(PySequence_GetItem(a[4], i));
-            return to_int(r.o);
-        };
-        const int o = layer >= 0 && layer < n ? owner(layer) : -1;
-        if (o < 0 || o > layer || owner(o) != o) return;  // (the caller reports the status)
-        owner_ok = true;
         const at::Tensor* t[4] = {nullptr, nullptr, nullptr, nullptr};
         for (int i = 0; i < (k_eq_v ? 2 : 4); ++i) {
             if (a[i] != Py_None) {
@@ -200,6 +201,9 @@ PyObject* guarded(Py_ssize_t given, Py_ssize_t wanted, F f) {
 // k_codes, k_scales, v_codes, v_scales, owner_map, layer, k_rows, v_rows, pos, k_eq_v, kind,
 // block_table, device_error, stream
 int rows(PyObject* const* a, bool append) {
+    const int layer = to_int(a[5]), owner = owner_of(a[4], layer);
+    if (owner < 0) return GEMMA_ERR_INVALID_ARG;
+    if (append && owner != layer) return GEMMA_OK;  // a shared layer writes no cache
     const at::Tensor& k = tensor(a[6]);
     if (k.dim() != 4) raise(PyExc_ValueError, "rows must be [batch][n][n_kv][head_dim]");
     const at::Tensor& pos = tensor(a[8]);
@@ -208,8 +212,7 @@ int rows(PyObject* const* a, bool append) {
     const at::Tensor* v = k_eq_v ? nullptr : optional(a[7]);
     if (!k_eq_v && (!v || v->sizes() != k.sizes() || v->scalar_type() != k.scalar_type()))
         raise(PyExc_ValueError, "K and V rows must have one shape and type");
-    Cache c(a, k_eq_v, k.size(3), k.size(2), k.size(0), a[11], k);
-    if (!c.owner_ok) return GEMMA_ERR_INVALID_ARG;
+    Cache c(a, owner, k_eq_v, k.size(3), k.size(2), k.size(0), a[11], k);
     const int B = checked(k.size(0)), n = checked(k.size(1)), n_kv = checked(k.size(2)),
               d = checked(k.size(3)), kind = to_int(a[10]);
     const auto dt = (gemma_dtype)dtype_code(k);
@@ -241,6 +244,8 @@ PyObject* read_q4(PyObject*, PyObject* const* a, Py_ssize_t n) {
 // window, n_kv, k_eq_v, scale, softcap, block_table, workspace, device_error, stream
 PyObject* attn_q4(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     return guarded(nargs, 20, [&]() -> int {
+        const int owner = owner_of(a[4], to_int(a[5]));
+        if (owner < 0) return GEMMA_ERR_INVALID_ARG;
         const at::Tensor &out = tensor(a[6]), &q = tensor(a[7]), &lens = tensor(a[8]);
         if (q.dim() != 4 || out.sizes() != q.sizes() || out.scalar_type() != q.scalar_type())
             raise(PyExc_ValueError, "q and out must be [batch][n_new][n_q][head_dim] of one type");
@@ -249,8 +254,7 @@ PyObject* attn_q4(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                   n_kv = to_int(a[12]);
         const bool k_eq_v = to_bool(a[13]);
         const float scale = to_float(a[14]), softcap = to_float(a[15]);
-        Cache c(a, k_eq_v, q.size(3), n_kv, q.size(0), a[16], q);
-        if (!c.owner_ok) return GEMMA_ERR_INVALID_ARG;
+        Cache c(a, owner, k_eq_v, q.size(3), n_kv, q.size(0), a[16], q);
         const at::Tensor* ws = optional(a[17]);
         const int B = checked(q.size(0)), n = checked(q.size(1)), n_q = checked(q.size(2)),
                   d = checked(q.size(3));

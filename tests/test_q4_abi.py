@@ -158,3 +158,19 @@ def test_misaligned_words_are_refused():
         assert attention(**args(**bad)) == INVALID, bad
         for fn in ("gemma_kv_append_q4", "gemma_kv_read_q4"):
             assert rows(fn, **args(**bad)) == INVALID, (fn, bad)
+
+
+@pytest.mark.parametrize("owner,layer", [([1, 1], 0), ([0, 0, 1], 2), ([0], 1), ([0, 1], -1), ([-1], 0)])
+def test_binding_append_refuses_bad_owner_maps(owner, layer):
+    """A layer that shares a cache writes nothing; one that no map describes is refused, as by the C
+    entry point."""
+    codes, scales = torch.zeros(1, 1, 64, 32, dtype=torch.uint8), torch.zeros(1, 1, 64, 1).bfloat16()
+    x, pos, n = torch.zeros(1, 1, 1, 64).bfloat16(), torch.zeros(1, dtype=torch.int32), len(owner)
+    with pytest.raises(g.GemmaError) as e:
+        g.gemma_kv_append_q4([codes] * n, [scales] * n, None, None, owner, layer, x, None, pos,
+                             k_eq_v=True)
+    assert e.value.status == INVALID
+    g.gemma_kv_append_q4([codes, None], [scales, None], None, None, [0, 0], 1, x, None, pos,
+                         k_eq_v=True)
+    g.gemma_kv_append_q4([codes, None], [scales, None], None, None, [0, 0], 1, None, None, None,
+                         k_eq_v=True)
