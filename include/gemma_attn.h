@@ -381,7 +381,7 @@ int gemma_attn_q4(void* out, const void* q, const void* const* k_codes,
                   size_t workspace_bytes, uint32_t* device_error, void* stream);
 
 /* Scratch bytes of gemma_attn_q4 for these arguments on the current device ((size_t)-1 for
- * invalid ones). */
+ * arguments that it refuses). */
 size_t gemma_attn_workspace_size_q4(int batch, gemma_layer_kind kind, int window, int n_q,
                                     int n_kv, int head_dim, int max_seq_len, int n_new,
                                     int k_eq_v);
@@ -459,7 +459,7 @@ int gemma_logit_sample(const void* logits, int batch, int vocab, gemma_dtype dty
                        void* workspace, size_t workspace_bytes, uint32_t* device_error,
                        void* stream);
 
-/* Bytes of scratch gemma_logit_sample needs ((size_t)-1 for invalid arguments): 4 per row, rounded
+/* Bytes of scratch gemma_logit_sample needs ((size_t)-1 for arguments that it refuses): 4 per row, rounded
  * up to 16, and 512 KiB more per row of fp32 logits. */
 size_t gemma_logit_sample_workspace_size(int batch, int vocab, gemma_dtype dtype);
 

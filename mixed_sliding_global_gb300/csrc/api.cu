@@ -747,6 +747,12 @@ Q4Plan q4_plan(int batch, int kind, int window, int n_q, int n_kv, int head_dim,
     return pl;
 }
 
+// Positions that a step of n_new queries can reach, at most: the slots of a dequantised copy.
+int q4_expand_slots(int kind, int window, int max_seq_len, int n_new) {
+    const long long reach = kind == GEMMA_GLOBAL ? max_seq_len : (long long)window + n_new - 1;
+    return (int)(reach < max_seq_len ? reach : max_seq_len);
+}
+
 // Scratch of the attention over a dequantised copy: lengths, K rows, V rows, split partials.
 struct Q4Expand {
     int slots;
@@ -755,8 +761,7 @@ struct Q4Expand {
 Q4Expand q4_expand_plan(int batch, int kind, int window, int n_q, int n_kv, int head_dim,
                         int max_seq_len, int n_new, int k_eq_v, int n_sm) {
     Q4Expand e{};
-    const long long reach = kind == GEMMA_GLOBAL ? max_seq_len : (long long)window + n_new - 1;
-    e.slots = (int)(reach < max_seq_len ? reach : max_seq_len);
+    e.slots = q4_expand_slots(kind, window, max_seq_len, n_new);
     const size_t rows = (size_t)batch * n_kv * e.slots * head_dim * 2;
     e.k_off = (size_t)round_up(4ll * batch, 256);
     e.v_off = e.k_off + (size_t)round_up((long long)rows, 256);
@@ -801,10 +806,15 @@ size_t gemma_attn_workspace_size_q4(int batch, gemma_layer_kind kind, int window
                                     int k_eq_v) {
     if (batch < 0 || n_new < 1 || max_seq_len < n_new) return (size_t)-1;
     if (check_shape(kind, window, n_q, n_kv, head_dim, GEMMA_BF16) != GEMMA_OK) return (size_t)-1;
+    // what the call refuses has no size
+    const bool direct = (long long)n_new * (n_q / n_kv) <= q4_direct_rows(head_dim);
+    if (batch > 65535 || n_kv > 32767 || max_seq_len > (1 << 30)) return (size_t)-1;
+    if (!direct && !q4_units_ok(q4_expand_slots(kind, window, max_seq_len, n_new), n_kv, head_dim))
+        return (size_t)-1;
     if (batch == 0) return 0;
     const int n_sm = sm_count();
     if (n_sm < 0) return (size_t)-1;
-    if ((long long)n_new * (n_q / n_kv) <= q4_direct_rows(head_dim))
+    if (direct)
         return q4_plan(batch, kind, window, n_q, n_kv, head_dim, max_seq_len, n_new, n_sm).ws_bytes;
     return q4_expand_plan(batch, kind, window, n_q, n_kv, head_dim, max_seq_len, n_new, k_eq_v,
                           n_sm)
@@ -840,7 +850,10 @@ int gemma_attn_q4(void* out, const void* q, const void* const* k_codes,
     } else if (max_seq_len > c.cap) {
         return GEMMA_ERR_CAPACITY;
     }
+    const bool direct = (long long)n_new * (n_q / n_kv) <= q4_direct_rows(head_dim);
     if (batch > 65535) return GEMMA_ERR_UNSUPPORTED;
+    if (!direct && !q4_units_ok(q4_expand_slots(kind, window, max_seq_len, n_new), n_kv, head_dim))
+        return GEMMA_ERR_UNSUPPORTED;
     if (batch == 0) return GEMMA_OK;
     st = q4_pointers(const_cast<void* const*>(k_codes), const_cast<void* const*>(k_scales),
                      const_cast<void* const*>(v_codes), const_cast<void* const*>(v_scales), o,
@@ -852,7 +865,7 @@ int gemma_attn_q4(void* out, const void* q, const void* const* k_codes,
     const int n_sm = sm_count();
     if (n_sm < 0) return GEMMA_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((long long)n_new * (n_q / n_kv) <= q4_direct_rows(head_dim)) {
+    if (direct) {
         const Q4Plan pl =
             q4_plan(batch, kind, window, n_q, n_kv, head_dim, max_seq_len, n_new, n_sm);
         if (pl.ws_bytes > 0 &&
@@ -895,7 +908,6 @@ int gemma_attn_q4(void* out, const void* q, const void* const* k_codes,
     }
     const Q4Expand e = q4_expand_plan(batch, kind, window, n_q, n_kv, head_dim, max_seq_len,
                                       n_new, k_eq_v, n_sm);
-    if (!q4_units_ok(e.slots, n_kv, head_dim)) return GEMMA_ERR_UNSUPPORTED;
     if (!workspace || workspace_bytes < e.bytes || !aligned16(workspace))
         return GEMMA_ERR_WORKSPACE;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
@@ -944,7 +956,7 @@ int gemma_logit_sample(const void* logits, int batch, int vocab, gemma_dtype dty
 }
 
 size_t gemma_logit_sample_workspace_size(int batch, int vocab, gemma_dtype dtype) {
-    if (batch < 0 || vocab < 1 || vocab > gemma::kSampleMaxVocab ||
+    if (batch < 0 || batch > 65535 || vocab < 1 || vocab > gemma::kSampleMaxVocab ||
         (dtype != GEMMA_BF16 && dtype != GEMMA_FP32))
         return (size_t)-1;
     return gemma::sample_workspace(batch, dtype == GEMMA_FP32);

@@ -174,3 +174,18 @@ def test_binding_append_refuses_bad_owner_maps(owner, layer):
                          k_eq_v=True)
     g.gemma_kv_append_q4([codes, None], [scales, None], None, None, [0, 0], 1, None, None, None,
                          k_eq_v=True)
+
+
+@pytest.mark.parametrize("kw", [dict(batch=65536), dict(n_q=32768, n_kv=32768),
+                                dict(msl=(1 << 30) + 64, cap=1 << 30),
+                                dict(n=100, msl=1 << 27, cap=1 << 30),
+                                dict(n=100, kind=0, window=1 << 27, msl=1 << 28, cap=1 << 30)])
+def test_workspace_size_refuses_what_the_call_refuses(kw):
+    a = {**dict(batch=1, kind=1, window=0, n_q=4, n_kv=2, d=512, msl=64, n=1, cap=64), **kw}
+    assert attn(**a) in (UNSUPPORTED, CAPACITY, INVALID)
+    size = lib().gemma_attn_workspace_size_q4
+    shape = [a[k] for k in ("batch", "kind", "window", "n_q", "n_kv", "d", "msl", "n")]
+    assert size(*shape, 1) == ctypes.c_size_t(-1).value
+    shape[0] = 0      # (the limits of a call without sequences are the same)
+    if "batch" not in kw:
+        assert size(*shape, 1) == ctypes.c_size_t(-1).value

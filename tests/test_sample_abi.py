@@ -77,3 +77,10 @@ def test_misaligned_words_are_refused(i):
     ws = 1 << 20
     assert lib().gemma_logit_sample(FAKE, 1, 8, 0, 30.0, p[0], p[1], p[2], p[3], p[4], p[5], FAKE, ws,
                                     p[6], None) == INVALID
+
+
+def test_workspace_size_refuses_what_the_call_refuses():
+    assert call(batch=65536) == UNSUPPORTED
+    for dtype in (0, 1):
+        assert lib().gemma_logit_sample_workspace_size(65536, 8, dtype) == ctypes.c_size_t(-1).value
+        assert lib().gemma_logit_sample_workspace_size(65535, 8, dtype) >= 4 * 65535
