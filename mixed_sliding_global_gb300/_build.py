@@ -12,6 +12,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -21,6 +22,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgemma_attn.so")
 BIND_SRC = os.path.join(CSRC, "bind.cpp")
 BIND = os.path.join(PKG, "_bind.so")
+BIND_KEY = os.path.join(BUILD, "bind.key")  # the bind_key() that _bind.so was built for
 HEADER = os.path.join(ROOT, "include", "gemma_attn.h")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -44,11 +46,21 @@ def _deps():
         glob.glob(os.path.join(CSRC, "*.h")) + [HEADER, BIND_SRC, os.path.abspath(__file__)]
 
 
+def bind_key() -> str:
+    """What _bind.so depends on besides its source: the interpreter and the PyTorch that it was
+    compiled against and links."""
+    import torch
+    return "\n".join([sysconfig.get_config_var("EXT_SUFFIX") or "", sys.version, torch.__version__,
+                      str(torch._C._GLIBCXX_USE_CXX11_ABI), os.path.dirname(torch.__file__)])
+
+
 def up_to_date(lib: str = LIB) -> bool:
-    if not os.path.exists(lib) or not os.path.exists(BIND):
+    if not os.path.exists(lib) or not os.path.exists(BIND) or not os.path.exists(BIND_KEY):
         return False
     t = min(os.path.getmtime(lib), os.path.getmtime(BIND))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    with open(BIND_KEY) as f:
+        key = f.read()
+    return key == bind_key() and all(os.path.getmtime(d) <= t for d in _deps())
 
 
 def _run(cmd, what):
@@ -79,7 +91,11 @@ def _link_bind(obj: str) -> None:
     _run([shutil.which("g++") or "g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libgemma_attn.so",
           "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10",
           "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"], "link of _bind.so failed")
+    if os.path.exists(BIND_KEY):
+        os.remove(BIND_KEY)
     os.replace(tmp, BIND)
+    with open(BIND_KEY, "w") as f:
+        f.write(bind_key())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -111,5 +127,4 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose=True))

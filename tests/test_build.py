@@ -1,0 +1,27 @@
+"""When the native parts are built anew (CPU)."""
+import sys
+import sysconfig
+
+import pytest
+import torch
+
+from mixed_sliding_global_gb300 import _build
+from mixed_sliding_global_gb300.binding import library
+
+
+@pytest.mark.parametrize("what", ["torch", "path", "suffix", "python"])
+def test_another_torch_or_python_needs_another_bind(what, monkeypatch, tmp_path):
+    """_bind.so was compiled against one PyTorch and one interpreter: with others it is stale."""
+    library()
+    assert _build.up_to_date()
+    if what == "torch":
+        monkeypatch.setattr(torch, "__version__", torch.__version__ + ".post1")
+    elif what == "path":
+        monkeypatch.setattr(torch, "__file__", str(tmp_path / "torch" / "__init__.py"))
+    elif what == "suffix":
+        var = sysconfig.get_config_var
+        monkeypatch.setattr(sysconfig, "get_config_var",
+                            lambda n: ".cpython-399.so" if n == "EXT_SUFFIX" else var(n))
+    else:
+        monkeypatch.setattr(sys, "version", "3.99")
+    assert not _build.up_to_date()
