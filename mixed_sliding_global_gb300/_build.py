@@ -41,9 +41,14 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
-def _deps():
-    return sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(CSRC, "*.h")) + [HEADER, BIND_SRC, os.path.abspath(__file__)]
+def _newer_than(path, deps) -> bool:
+    return os.path.exists(path) and all(os.path.getmtime(d) <= os.path.getmtime(path)
+                                        for d in deps + [HEADER, os.path.abspath(__file__)])
+
+
+def library_up_to_date() -> bool:
+    return _newer_than(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) +
+                       glob.glob(os.path.join(CSRC, "*.h")))
 
 
 def bind_key() -> str:
@@ -54,13 +59,15 @@ def bind_key() -> str:
                       str(torch._C._GLIBCXX_USE_CXX11_ABI), os.path.dirname(torch.__file__)])
 
 
-def up_to_date(lib: str = LIB) -> bool:
-    if not os.path.exists(lib) or not os.path.exists(BIND) or not os.path.exists(BIND_KEY):
+def bind_up_to_date() -> bool:
+    if not _newer_than(BIND, [BIND_SRC]) or not os.path.exists(BIND_KEY):
         return False
-    t = min(os.path.getmtime(lib), os.path.getmtime(BIND))
     with open(BIND_KEY) as f:
-        key = f.read()
-    return key == bind_key() and all(os.path.getmtime(d) <= t for d in _deps())
+        return f.read() == bind_key()
+
+
+def up_to_date() -> bool:
+    return library_up_to_date() and bind_up_to_date()
 
 
 def _run(cmd, what):
@@ -72,6 +79,7 @@ def _run(cmd, what):
 
 def _compile_bind() -> str:
     import torch
+    os.makedirs(BUILD, exist_ok=True)
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
     obj = os.path.join(BUILD, "bind.o")
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
@@ -98,8 +106,9 @@ def _link_bind(obj: str) -> None:
         f.write(bind_key())
 
 
-def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    if not force and up_to_date():
+def build_library(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    """libgemma_attn.so alone: all that the calls marshalled by ctypes need."""
+    if not force and library_up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -115,14 +124,21 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
-        bind = ex.submit(_compile_bind)
         objs = list(ex.map(compile_one, sources()))
-        bind_obj = bind.result()
     tmp = LIB + f".tmp{os.getpid()}"
     _run([cc, "-shared", *ARCH, "-Xlinker", "-soname=libgemma_attn.so", "-o", tmp, *objs],
          "link failed")
     os.replace(tmp, LIB)
-    _link_bind(bind_obj)
+    return LIB
+
+
+def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
+    """Both parts. If _bind.so cannot be built this raises, with the library in place."""
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        bind = ex.submit(_compile_bind) if force or not bind_up_to_date() else None
+        build_library(force, verbose, extra_flags)
+        if bind:
+            _link_bind(bind.result())
     return LIB
 
 

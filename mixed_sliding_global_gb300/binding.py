@@ -108,8 +108,8 @@ def library(build_if_missing: bool = True) -> ctypes.CDLL:
     global _lib
     if _lib is None:
         path = _build.LIB
-        if build_if_missing and not _build.up_to_date():
-            _build.build()
+        if build_if_missing:
+            _build.build_library()
         if not os.path.exists(path):
             raise ImportError(f"{path} is missing: build it with mixed_sliding_global_gb300._build")
         lib = ctypes.CDLL(path)
@@ -353,10 +353,12 @@ _bind = None
 
 
 def _native():
-    """The native half of the binding (built with the library, and loaded after it)."""
+    """The native half of the binding (built when it is missing or stale, and loaded after the
+    library)."""
     global _bind
     if _bind is None:
         library()
+        _build.build()
         from . import _bind as module
         _bind = module
     return _bind
