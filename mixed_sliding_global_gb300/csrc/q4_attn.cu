@@ -473,8 +473,10 @@ __global__ void __launch_bounds__(kThreads, kQ4CtasPerSm)
         // biased exponent of the largest element -> factor 2^(13 - (exponent - 127))
         const float f =
             __uint_as_float((uint32_t)(267 - min(max((int)(mx >> 7), 13), 254)) << 23);
-        // a score is the sum of products times 2^24 (the codes') times this
-        if (lane == 0) sInv[slot][r] = (p.softcap > 0.f ? p.cap_inner : p.scale_log2) / f;
+        // a score is the sum of products times this times 2^12 (the codes' 2^24 in two halves: with
+        // all of it on one side the keys' or the queries' large numbers would leave fp32's range)
+        if (lane == 0)
+            sInv[slot][r] = (p.softcap > 0.f ? p.cap_inner : p.scale_log2) * 4096.f / f;
 #pragma unroll
         for (int c = 0; c < CH; ++c) {
             const int ch = c * 32 + lane;  // elements 8 ch .. 8 ch + 7
@@ -761,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, kQ4CtasPerSm)
                 const float2 inv = *reinterpret_cast<const float2*>(&sInv[js][n * 8 + 2 * tq]);
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    sv[n][k] = sv[n][k] * 16777216.f * (k & 1 ? inv.y : inv.x);
+                    sv[n][k] = sv[n][k] * (k & 1 ? inv.y : inv.x) * 4096.f;
             }
             if (p.softcap > 0.f) {
 #pragma unroll

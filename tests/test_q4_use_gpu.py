@@ -390,3 +390,28 @@ def test_small_weights_behind_a_large_one(d, n_q, gap):
     assert mass.max() < 260 * math.exp(-gap) * 3      # the large weight carries nothing
     assert ((got.double() - out).abs() <= 2.0 ** -8 * out.abs() +
             (2.0 ** -10 + 2.0 ** -13) * mass + small).all()
+
+
+@pytest.mark.parametrize("softcap", [0.0, 30.0])
+@pytest.mark.parametrize("n", [1, 3])
+@pytest.mark.parametrize("e", [-112, 112])
+def test_queries_and_keys_at_the_ends_of_the_range(e, n, softcap):
+    """Queries of 2^e with keys of 2^-e: scores of ordinary size from numbers whose products with the
+    codes' 2^24 leave fp32's range."""
+    d, n_q, L = 256, 8, 300
+    gen = torch.Generator().manual_seed(e + 500)
+    k = torch.randn(1, L, 2, d, generator=gen) * 2.0 ** -e
+    v = torch.randn(1, L, 2, d, generator=gen)
+    cache = [*empty_cache((1, 2, 320), d), *empty_cache((1, 2, 320), d)]
+    g.gemma_kv_append_q4(*[[t] for t in cache], [0], 0, k.bfloat16().cuda(), v.bfloat16().cuda(),
+                         i32([0]), k_eq_v=False)
+    q = (torch.randn(1, n, n_q, d, generator=gen) * 2.0 ** e).bfloat16().cuda()
+    out = torch.full_like(q, math.nan)
+    size = g.gemma_attn_workspace_size_q4(1, GLOBAL, 0, n_q, 2, d, L, n, k_eq_v=False)
+    g.gemma_attn_q4(out, q, *[[t] for t in cache], [0], 0, i32([L]), L, kind=GLOBAL, window=0,
+                    n_kv=2, k_eq_v=False, scale=d ** -0.5, softcap=softcap,
+                    workspace=torch.empty(max(size, 16), dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    kk, vv = (R.values(cache[i].cpu(), cache[i + 1].cpu()) for i in (0, 2))
+    ref, mass = R.attention(q.cpu(), kk, vv, [L], GLOBAL, 0, d ** -0.5, softcap)
+    assert ((out.cpu().double() - ref).abs() <= bound(ref, mass, n * n_q // 2, d)).all()
