@@ -21,15 +21,15 @@ def i32(x):
 
 
 class Case:
-    """A cache of random 4-bit rows, plain or paged, without the rows behind a sequence's end, which
-    hold NaN."""
+    """A cache of random 4-bit rows, plain, paged or a ring of `ring` slots; rows behind a sequence's
+    end hold NaN."""
 
-    def __init__(self, lens, n_q, n_kv, d, msl, *, k_eq_v=False, page=0, n=1, seed=0):
+    def __init__(self, lens, n_q, n_kv, d, msl, *, k_eq_v=False, page=0, n=1, seed=0, ring=0):
         self.lens, self.msl, self.n, self.page, self.k_eq_v = lens, msl, n, page, k_eq_v
         self.n_kv, self.d = n_kv, d
         gen = torch.Generator().manual_seed(seed)
         B, unit = len(lens), page or 32
-        slots = -(-msl // unit) * unit
+        slots = ring or -(-msl // unit) * unit
         self.table = None
         shape = (B, n_kv, slots)
         if page:
@@ -44,7 +44,7 @@ class Case:
             s = (16 + torch.randint(0, 16, shape + (d // 64,), generator=gen)).float() / 64
             self.t += [codes, s.bfloat16()]
         for b, L in enumerate(lens):
-            at = torch.arange(max(0, L) if L <= msl else 0, slots)
+            at = torch.arange(slots if ring else max(0, L) if L <= msl else 0, slots)
             where, slot = R.locate(at, b, GLOBAL, slots, self.table, page)
             for s in self.t[1::2]:
                 s[where, :, slot] = math.nan
@@ -115,3 +115,41 @@ def test_bad_pages_among_good_ones(n_q, n_kv, d, k_eq_v, n):
     out, err = c.attend(table=table)
     assert err == g.GEMMA_DEVERR_PAGE
     c.check(out, lost=lost)
+
+
+@pytest.mark.parametrize("lens,n_q,n_kv,d,msl,opt", [
+    # one long sequence, K as V; a window far into a long one; a ring
+    ([8192], 16, 1, 512, 8192, dict(k_eq_v=True)),
+    ([9000, 6100], 16, 1, 128, 9000, dict(kind=SLIDING, window=5000)),
+    ([4001, 7000, 20000], 4, 1, 256, 20000, dict(kind=RING, window=4000)),
+    # ragged batches at each head_dim, rows per unit of 2, 8, 16 and more
+    ([6000, 1, 333, 5888, 128, 4097, 2, 129, 700, 3000, 5999, 64], 16, 8, 64, 6000, {}),
+    ([6000, 1, 333, 5888, 128, 4097, 2, 129, 700, 3000, 5999, 64], 64, 8, 64, 6000, dict(cap=20.0)),
+    ([2900, 4000, 1300, 4096, 1, 2047, 3999, 130] + [500 + 11 * i for i in range(25)], 64, 4, 64, 4096,
+     dict(k_eq_v=True)),
+    ([5999, 2, 6000, 1025], 8, 2, 128, 6000, dict(n=2)),
+    ([5999, 2, 6000, 1025], 16, 2, 128, 6000, dict(k_eq_v=True, page=128)),
+    ([6000, 17, 4100], 16, 1, 128, 6000, dict(n=3)),
+    ([4500, 700, 3210, 4, 2222, 1, 4400, 999, 129, 4096, 3333, 2048, 1500], 8, 2, 256, 4500,
+     dict(cap=50.0, page=256)),
+    ([2000, 6000, 100], 2, 1, 256, 6000, dict(k_eq_v=True)),
+    ([2000, 6000, 100], 16, 2, 256, 6000, {}),
+    ([2000, 5990, 100], 16, 1, 256, 6000, dict(n=4, cap=30.0)),
+    ([3000, 40, 2500, 1], 4, 2, 512, 3000, {}),
+    ([3000, 40, 2500, 5], 8, 1, 512, 3000, dict(page=128)),
+    ([3000, 40, 2500, 5], 16, 1, 512, 3000, dict(n=4)),
+    ([2999, 41, 2501, 1], 32, 2, 512, 3000, dict(k_eq_v=True, cap=20.0)),
+])
+def test_against_the_definition(lens, n_q, n_kv, d, msl, opt):
+    """Whole units, parts of units and the merge, over every instantiation: rows per unit up to 4, up
+    to 8 and more, with K as V and without, windows, rings, pages and caps."""
+    o = dict(kind=GLOBAL, window=0, cap=0.0, n=1, k_eq_v=False, page=0)
+    o.update(opt)
+    if o["n"] > 1:
+        lens = [max(x, o["n"]) for x in lens]
+    ring = -(-(o["window"] + o["n"] - 1) // 128) * 128 if o["kind"] == RING else 0
+    c = Case(lens, n_q, n_kv, d, msl, k_eq_v=o["k_eq_v"], page=o["page"], n=o["n"], seed=d + n_q,
+             ring=ring)
+    out, err = c.attend(o["kind"], o["window"], o["cap"])
+    assert err == 0
+    c.check(out, o["kind"], o["window"], o["cap"])
