@@ -272,13 +272,13 @@ struct Slice {
     __device__ F2 weight(uint32_t key) const {
         return key == key_max ? F2{1.f, 0.f} : relative(capped(K::value(key)), zmax);
     }
-    // Most of a row lies below 2^-24 of the largest weight: single precision is enough there (an
-    // error of 2^-46 each; without a cap). Adds such a weight to `tiny`, else returns false.
+    // Most of a row lies below 2^-33 of the largest weight: single precision is enough there (an
+    // error of 2^-55 each; without a cap). Adds such a weight to `tiny`, else returns false.
     __device__ bool tiny_weight(uint32_t key, float& tiny) const {
         if (key == key_max || isinf(zmax.h)) return false;
         const F2 a = two_sum(K::value(key), -zmax.h);  // (zmax.l is zero without a cap)
         const float d = __fmul_rn(a.h, inv_t.h);
-        if (!(d < -17.f)) return false;
+        if (!(d < -23.f)) return false;
         const float rest = __fmaf_rn(a.h, inv_t.h, -d) + (a.l * inv_t.h + a.h * inv_t.l);
         if (d > -80.f) tiny += expf(d) * (1.f + rest);
         return true;
@@ -545,9 +545,12 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
     const bool need_sum = F32 && !want && r.key_max;
     if (need_sum || rank == lead) r.zmax = r.capped(K::value(max(r.key_max, K::kLow)));
     if (need_sum) {
-        u64 mine = 0;
-        float tiny = 0.f;
-        // (those near the largest one, a few per thousand, are weighed together afterwards: in place
+        // Equal logits round alike, and a row may have a million of them: a thread's sum is a pair of
+        // fp32 numbers and is rounded once, to units of 2^-46 (a slice has fewer than 2^17 logits),
+        // the CTA's to 2^-43.
+        F2 mine{0.f, 0.f};
+        auto add = [&](F2 w) { mine = mine + w; };
+        // (those near the largest one, a few per hundred, are weighed together afterwards: in place
         // one lane's would hold up its warp)
         uint32_t* near = reinterpret_cast<uint32_t*>(s.pool);
         const uint32_t* x = static_cast<const uint32_t*>(p.logits) + (long long)row * p.vocab;
@@ -560,6 +563,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
 #pragma unroll 1
         for (; i0 < i1; i0 += 4 * T) {
             uint32_t now[4];
+            float tiny = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 now[k] = K::of(next[k]);
@@ -572,22 +576,24 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
                 const uint32_t i = atomicAdd(&s.n_near, 1u);
                 if (i < 2 * kListMax) near[i] = key;
             }
+            const F2 sum = two_sum(mine.h, tiny);
+            mine = F2{sum.h, __fadd_rn(mine.l, sum.l)};
         }
         __syncthreads();
         const uint32_t n_near = s.n_near;
         if (n_near <= 2 * kListMax) {
-            for (uint32_t i = tid; i < n_near; i += T) mine += r.units(r.weight(near[i]), 1u);
+            for (uint32_t i = tid; i < n_near; i += T) add(r.weight(near[i]));
         } else {  // no room: all of them where they lie
-            tiny = 0.f;
             for (int i = (int)r.i0 + tid; i < i1; i += T) {
                 const uint32_t key = K::of(load(i));
+                float tiny = 0.f;  // (those are in the sum already)
                 if (key >= K::kLow && key <= K::kInf && !r.tiny_weight(key, tiny))
-                    mine += r.units(r.weight(key), 1u);
+                    add(r.weight(key));
             }
         }
-        mine += (u64)__float2ll_rn(tiny * 0x1p43f);
-        const u64 b = r.sum_before(mine);
-        if (tid == T - 1) st_peer(peer_addr(&s.sums[rank], lead), b + mine);
+        const u64 sum = (u64)(__float2ll_rn(mine.h * 0x1p46f) + __float2ll_rn(mine.l * 0x1p46f));
+        const u64 b = r.sum_before(sum);
+        if (tid == T - 1) st_peer(peer_addr(&s.sums[rank], lead), (b + sum + 4) >> 3);
     }
     __syncthreads();
     if (tid == 0) st_peer(peer_addr(&s.counts[rank], lead), s.n_list);
