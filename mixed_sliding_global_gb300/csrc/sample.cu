@@ -13,7 +13,7 @@
 // evaluated once in pairs of fp32 numbers (2^-40): cuts and draws fall between the same tokens as in
 // a 64-bit evaluation of the definition. Ties inside a value are a division, and one look at the
 // slice that holds the wanted occurrence finds its index. fp32 logits take the same histogram over
-// their upper 16 bits, whose bins' weights are summed into global memory as integers (40 bits below
+// their upper 16 bits, whose bins' weights are summed into global memory as integers (43 bits below
 // the bin's own largest weight, so the order of the additions does not matter). The few hundred
 // logits of a bin that a cut or the draw falls into are gathered and put in order; a bin of more
 // than 1,024 takes the histogram again, over its lower 16 bits (a row of 262,144, flat
@@ -1085,13 +1085,18 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
             const uint32_t* x = static_cast<const uint32_t*>(p.logits) + (long long)row * p.vocab;
             const int i1 = (int)r.i1;
             auto load = [&](int i) { return i < i1 ? x[i] : 0x7fffffffu; };  // (NaN: none)
-            auto add = [&](uint32_t key) {
+            // To units of 2^-43, rounded up where the rest exceeds a number that only the logit's index
+            // gives (multiples of the golden ratio, modulo 1): equal logits, of which a row may have a
+            // million, would all round alike to the nearest (5,000 distinct ones and 257,000 at e^-17 of
+            // the largest in one bin: the sum off by 2^-23).
+            auto add = [&](uint32_t key, uint32_t index) {
                 const uint32_t anchor = min(key | 0xffffu, key_max);
                 const F2 w = key == anchor ? F2{1.f, 0.f}
                                            : r.template relative<true>(
                                                  r.template capped<true>(K::value(key)),
                                                  r.template capped<true>(K::value(anchor)));
-                const u64 v = (u64)(__float2ll_rn(w.h * 0x1p40f) + __float2ll_rn(w.l * 0x1p40f));
+                const u64 fine = (u64)(__float2ll_rn(w.h * 0x1p62f) + __float2ll_rn(w.l * 0x1p62f));
+                const u64 v = (fine + (index * 0x9e3779b9u >> 13)) >> 19;
                 if (v) atomicAdd(mass + (key >> 16), v);
             };
             int i0 = (int)r.i0 + tid;
@@ -1102,7 +1107,7 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
                     const uint32_t key = K::of(next[0]);
                     next[0] = next[1];
                     next[1] = load(i0 + 2 * kThreads);
-                    if (key >= K::kLow && key <= K::kInf) add(key);
+                    if (key >= K::kLow && key <= K::kInf) add(key, (uint32_t)i0);
                 }
             } else {
                 uint32_t* queue = reinterpret_cast<uint32_t*>(s.before2 + kGather);  // [2 kThreads]
@@ -1123,13 +1128,15 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
                         uint32_t at0 = 0;
                         if (lane == 0 && lanes) at0 = atomicAdd(&s.queued[turn], __popc(lanes));
                         at0 = __shfl_sync(0xffffffffu, at0, 0);
-                        if (counts) queue[at0 + __popc(lanes & ((1u << lane) - 1))] = key;
+                        if (counts)
+                            queue[at0 + __popc(lanes & ((1u << lane) - 1))] =
+                                (uint32_t)(i0 + (h - 2) * kThreads);
                     }
                     __syncthreads();
                     const uint32_t n = s.queued[turn];
                     if (tid == 0) s.queued[turn ^ 1] = 0;
 #pragma unroll 1
-                    for (uint32_t k = tid; k < n; k += kThreads) add(queue[k]);
+                    for (uint32_t k = tid; k < n; k += kThreads) add(K::of(x[queue[k]]), queue[k]);
                     __syncthreads();
                 }
             }
@@ -1146,11 +1153,11 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
                 const u64 v = *reinterpret_cast<volatile u64*>(mass + bin);
                 if (!v) return 0;
                 const F2 w = r.weight(min(bin << 16 | 0xffffu, key_max));
-                // v < 2^60 as a sum of three numbers of 24 bits
+                // v <= 2^63 as a sum of three numbers of at most 24 bits
                 const float a = (float)(v >> 40), b = (float)(v >> 20 & 0xfffffu),
                             c = (float)(v & 0xfffffu);
-                return r.units(w * F2{a, 0.f}, 1u) +
-                       r.units(w * fast_sum(b * 0x1p-20f, c * 0x1p-40f), 1u);
+                return r.units(w * F2{a * 0x1p-3f, 0.f}, 1u) +
+                       r.units(w * fast_sum(b * 0x1p-23f, c * 0x1p-43f), 1u);
             }
             const uint32_t n = kept_of(bin, r.bin_count(g, i));
             return n ? r.units(r.weight(bin), n) : 0;

@@ -18,11 +18,11 @@ pytestmark = pytest.mark.gpu
 MARGIN = 2.0 ** -33
 
 
-def sums(x, t, softcap, m):
+def sums(x, t, softcap, m, k):
     """Order of a row of fp32 or bf16 logits, the running weights of its first m tokens and the sum
-    of all, in 64 bits."""
+    of all (of the first k with k), in 64 bits."""
     x = x.double().numpy()
-    order = np.argsort(-x, kind="stable")
+    order = np.argsort(-x, kind="stable")[:k or None]
     z = x[order]
     if softcap:
         z = softcap * np.tanh(z / softcap)
@@ -46,7 +46,7 @@ def near(run, total, n):
     return c, place
 
 
-def draw(x, u, t=None, p=None, softcap=0.0):
+def draw(x, u, t=None, p=None, softcap=0.0, k=0):
     B, V = x.shape
     out = torch.full((B,), -7, dtype=torch.int32, device="cuda")
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -54,26 +54,27 @@ def draw(x, u, t=None, p=None, softcap=0.0):
     ws = torch.empty(max(16, g.gemma_logit_sample_workspace_size(B, V, x.dtype)), dtype=torch.uint8,
                      device="cuda")
     g.gemma_logit_sample(x, out, f(u), temperature=f(t), top_p=f(p), softcap=softcap, workspace=ws,
+                         top_k=torch.full((B,), k, dtype=torch.int32, device="cuda") if k else None,
                          device_error=err)
     torch.cuda.synchronize()
     assert err.item() == 0
     return out.cpu().numpy()
 
 
-def check(x, B, t=1.0, softcap=0.0, m=200):
+def check(x, B, t=1.0, softcap=0.0, m=200, k=0):
     """Uniforms at the boundaries of the first m tokens, then top_p there with the last kept drawn."""
     t = float(np.float32(t))
-    order, run, total = sums(x, t, softcap, m + 1)
+    order, run, total = sums(x, t, softcap, m + 1, k)
     xs = x.cuda().expand(B, -1).contiguous()
     u, place = near(run[:m], total, B)
     assert len(u) == B
-    got = draw(xs, u, t, None, softcap)
+    got = draw(xs, u, t, None, softcap, k)
     assert (got == order[place]).all(), ((got != order[place]).sum(), B)
     # keep the shortest prefix with run >= p total; its last token weighs more than 2^-24 of it
     last = run[place] - np.where(place > 0, run[place - 1], 0)
     ok = last > 2.0 ** -22 * total
     assert ok.sum() > B // 2
-    got = draw(xs, np.full(B, 1 - 2.0 ** -24), t, u, softcap)
+    got = draw(xs, np.full(B, 1 - 2.0 ** -24), t, u, softcap, k)
     assert (got == order[place])[ok].all(), ((got != order[place])[ok].sum(), ok.sum())
 
 
@@ -99,3 +100,15 @@ def half_unit(bulk):
 def test_equal_logits_behind_distinct_ones(V, B, bulk):
     """fp32 without top_k or cap: the sum of all weights next to a short list of the largest."""
     check(row(V, half_unit(bulk), int(V - bulk)), B)
+
+
+@pytest.mark.parametrize("k", [0, 3000])
+@pytest.mark.parametrize("V,B", [(20000, 40), (262144, 8), (262144, 64), (1048560, 16)])
+@pytest.mark.parametrize("bulk", [-16.9, -12.0])
+def test_equal_logits_within_one_upper_half(V, B, bulk, k):
+    """fp32 by histogram (a top_k beyond the lists', of the whole row or of a part that ends among
+    the equal ones or before) at a temperature so small that most of the row shares its upper half:
+    the sum of one bin holds weights far apart."""
+    t = 2.0 ** -11
+    x = row(V, half_unit(bulk), int(V - bulk) + 7, heads=5000) * t + 2.0146
+    check(x, B, t=t, k=k or V)
