@@ -171,27 +171,40 @@ __constant__ float2 c_exp2[64] = {
     {0x1.ea4afa0000000p+0f, 0x1.52486c0000000p-27f}, {0x1.efa1be0000000p+0f, 0x1.cc2b440000000p-25f},
     {0x1.f507660000000p+0f, -0x1.246eb00000000p-26f}, {0x1.fa7c180000000p+0f, 0x1.9e90d80000000p-28f}};
 
-// e^x for x <= 0: x = (64 k + i) ln 2 / 64 + r with |r| < 0.0055, e^x = 2^k 2^(i/64) e^r, and e^r by
-// its series, whose first terms keep their error terms (the fifth is below 2^-46). Below -60: 0.
-__device__ __forceinline__ F2 exp_f2_here(F2 x, const float2* exp2) {
-    if (!(x.h > -60.f)) return F2{0.f, 0.f};
+// e^x = t (1 + e1) for -60 < x <= 0: x = (64 k + i) ln 2 / 64 + r with |r| < 0.0055, t = 2^k 2^(i/64)
+// and e1 = e^r - 1 by its series, whose first terms keep their error terms (the fifth is below 2^-46).
+__device__ __forceinline__ void exp_parts(F2 x, const float2* exp2, F2& t, F2& e1) {
     const float n = rintf(x.h * 92.332482616893656f);  // 64 / ln 2
     // ln 2 / 64 in four parts of 11 bits and a rest (n has at most 13: the products are exact)
     const F2 nb = two_sum(__fmul_rn(n, -0x1.2140000000000p-18f), __fmul_rn(n, -0x1.fbc0000000000p-29f));
     const F2 r = (x + F2{__fmul_rn(n, -0x1.62c0000000000p-7f), 0.f}) + fast_sum(nb.h, __fadd_rn(nb.l, __fmul_rn(n, -0x1.473de60000000p-40f)));
     const F2 r2 = r * r;
     const float c = r.h * r2.h * (0.16666667f + r.h * (0.041666668f + r.h * 0.0083333333f));
-    const F2 e = F2{1.f, 0.f} + (r + (F2{0.5f * r2.h, 0.5f * r2.l} + F2{c, 0.f}));
+    e1 = r + (F2{0.5f * r2.h, 0.5f * r2.l} + F2{c, 0.f});
     const int k = (int)n;
-    const float2 t = exp2[k & 63];
-    F2 w = e * F2{t.x, t.y};
+    const float2 f = exp2[k & 63];
     const float sc = __uint_as_float((uint32_t)(127 + (k >> 6)) << 23);
-    return F2{w.h * sc, w.l * sc};
+    t = F2{f.x * sc, f.y * sc};
+}
+// e^x for x <= 0. Below -60: 0.
+__device__ __forceinline__ F2 exp_f2_here(F2 x, const float2* exp2) {
+    if (!(x.h > -60.f)) return F2{0.f, 0.f};
+    F2 t, e1;
+    exp_parts(x, exp2, t, e1);
+    return (F2{1.f, 0.f} + e1) * t;
+}
+// e^x - 1 for x <= 0, small ones (t = 1) to full relative accuracy.
+__device__ __forceinline__ F2 expm1_f2_here(F2 x, const float2* exp2) {
+    if (!(x.h > -60.f)) return F2{-1.f, 0.f};
+    F2 t, e1;
+    exp_parts(x, exp2, t, e1);
+    return (t + F2{-1.f, 0.f}) + t * e1;
 }
 
-// One copy of it, for the many places that need it once: a row's steps run one after another, and
+// One copy of each, for the many places that need it once: a row's steps run one after another, and
 // code that is fetched for a single use costs more than the call (9 fp32 rows 31.7 -> 29.7 us).
 __device__ __noinline__ F2 exp_f2(F2 x, const float2* exp2) { return exp_f2_here(x, exp2); }
+__device__ __noinline__ F2 expm1_f2(F2 x, const float2* exp2) { return expm1_f2_here(x, exp2); }
 
 // A place in a row's order: the tokens above key `key`, and of key itself the first `ties`.
 struct Cut {
@@ -228,7 +241,8 @@ struct Slice {
     u64* part;           // shared, one per warp
     int C, rank, row;
     long long i0, i1;
-    F2 inv_t, zmax, inner;  // 1 / T, the largest z, -2 / softcap
+    F2 inv_t, zmax, inner;  // 1 / T, the largest z, -2 / (scale softcap)
+    float scale;
     uint32_t key_max;    // key of the row's largest candidate
     int tid, warp, lane;
 
@@ -244,20 +258,23 @@ struct Slice {
         const long long per = (p.vocab + C - 1) / C;
         i0 = min((long long)rank * per, (long long)p.vocab);
         i1 = min(i0 + per, (long long)p.vocab);
-        inner = p.softcap > 0.f ? F2{-2.f, 0.f} / F2{p.softcap, 0.f} : F2{0.f, 0.f};
+        scale = p.softcap > 1.f ? 0x1p-32f : 1.f;
+        inner = p.softcap > 0.f ? F2{-2.f, 0.f} / F2{p.softcap * scale, 0.f} : F2{0.f, 0.f};
         for (int i = tid; i < 64; i += T) exp2_[i] = c_exp2[i];
     }
 
-    // z of a logit: c tanh(x / c) = +-c (1 - e) / (1 + e), e = exp(-2 |x| / c)
+    // z of a logit: c tanh(x / c) = -+c m / (2 + m), m = exp(-2 |x| / c) - 1: with 1 - exp() a cap far
+    // above the logits would cancel their digits. Below |x| / c = 2^-25 it is x to 2^-50. (scale keeps
+    // 2 / c and |x| / c in range for the largest caps.)
     template <bool HERE = false>  // (for loops over all logits)
     __device__ __forceinline__ F2 capped(float x) const {
         if (!(p.softcap > 0.f)) return F2{x, 0.f};
-        const F2 c{p.softcap, 0.f};
-        const float a = fabsf(x);
-        const F2 y = F2{a, 0.f} * inner, e = HERE ? exp_f2_here(y, exp2) : exp_f2(y, exp2);
-        F2 t = (F2{1.f, 0.f} + F2{-e.h, -e.l}) / (F2{1.f, 0.f} + e);
+        const F2 y = F2{fabsf(x) * scale, 0.f} * inner;
+        if (y.h > -0x1p-24f) return F2{x, 0.f};
+        const F2 m = HERE ? expm1_f2_here(y, exp2) : expm1_f2(y, exp2);
+        F2 t = F2{-m.h, -m.l} / (F2{2.f, 0.f} + m);
         if (isinf(x)) t = F2{1.f, 0.f};
-        t = t * c;
+        t = t * F2{p.softcap, 0.f};
         return x < 0.f ? F2{-t.h, -t.l} : t;
     }
     // exp((z - top) / T) of a logit z <= top

@@ -112,3 +112,17 @@ def test_equal_logits_within_one_upper_half(V, B, bulk, k):
     t = 2.0 ** -11
     x = row(V, half_unit(bulk), int(V - bulk) + 7, heads=5000) * t + 2.0146
     check(x, B, t=t, k=k or V)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("softcap", [50.0, 1e5, 1e7, 1e12, 3e38])
+def test_large_caps(softcap, dtype):
+    """Caps far above the logits, to which z is x and a little less: with 2^-47 of the cap, or 2^-40 of
+    z if that is less, a weight is good to 2^-42 and better here."""
+    gen = torch.Generator().manual_seed(9)
+    x = (torch.randn(30000, generator=gen) * 3).to(dtype)
+    if dtype == torch.bfloat16:
+        x = torch.unique(x)[-900:]      # (boundaries between single tokens)
+    softcap = float(np.float32(softcap))
+    check(x, 64, softcap=softcap, m=300)
+    check(x, 64, softcap=softcap, m=300, k=250)
