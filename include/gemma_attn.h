@@ -436,8 +436,10 @@ size_t gemma_logit_workspace_size(int batch, int vocab);
  *   5. token[b] = the first one whose running sum of weights exceeds uniform[b] times the sum of
  *      what is kept.
  * temperature 0 draws the first of the order. Logits of +infinity leave only themselves (without a
- * cap), with equal weights. Weights are accurate to about 2^-40 and their sums to about 2^-35, and
- * the result does not depend on scheduling: the same call gives the same tokens.
+ * cap), with equal weights. A temperature below 2^-126 draws from the equal largest logits alone.
+ * Weights are accurate to about 2^-40 of the largest one, with a cap also to the error of z, 2^-47
+ * softcap or 2^-40 |z| if that is less, divided by the temperature; their sums to about 2^-34 of the
+ * sum. The result does not depend on scheduling: the same call gives the same tokens.
  *   logits      DEVICE [batch][vocab] of dtype, row-major, 16-byte aligned.
  *   temperature, top_k, top_p, min_p
  *               DEVICE float / int32 / float / float [batch], each optional: NULL stands for 1, 0,

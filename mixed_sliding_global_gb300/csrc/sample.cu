@@ -121,6 +121,10 @@ __device__ __forceinline__ F2 operator+(F2 a, F2 b) {
     const F2 s = two_sum(a.h, b.h);
     return fast_sum(s.h, __fadd_rn(s.l, __fadd_rn(a.l, b.l)));
 }
+__device__ __forceinline__ F2 operator+(float a, F2 b) {  // |a| >= |b|
+    const F2 s = fast_sum(a, b.h);
+    return fast_sum(s.h, __fadd_rn(s.l, b.l));
+}
 __device__ __forceinline__ F2 operator*(F2 a, F2 b) {
     const float m = __fmul_rn(a.h, b.h);
     float e = __fmaf_rn(a.h, b.h, -m);
@@ -191,14 +195,14 @@ __device__ __forceinline__ F2 exp_f2_here(F2 x, const float2* exp2) {
     if (!(x.h > -60.f)) return F2{0.f, 0.f};
     F2 t, e1;
     exp_parts(x, exp2, t, e1);
-    return (F2{1.f, 0.f} + e1) * t;
+    return (1.f + e1) * t;
 }
 // e^x - 1 for x <= 0, small ones (t = 1) to full relative accuracy.
 __device__ __forceinline__ F2 expm1_f2_here(F2 x, const float2* exp2) {
     if (!(x.h > -60.f)) return F2{-1.f, 0.f};
     F2 t, e1;
     exp_parts(x, exp2, t, e1);
-    return (t + F2{-1.f, 0.f}) + t * e1;
+    return (-1.f + t) + t * e1;
 }
 
 // One copy of each, for the many places that need it once: a row's steps run one after another, and
@@ -241,8 +245,9 @@ struct Slice {
     u64* part;           // shared, one per warp
     int C, rank, row;
     long long i0, i1;
-    F2 inv_t, zmax, inner;  // 1 / T, the largest z, -2 / (scale softcap)
-    float scale;
+    // 1 / (t_scale T), the largest t_scale z, -2 / (scale softcap)
+    F2 inv_t, zmax, inner;
+    float t_scale, scale;
     uint32_t key_max;    // key of the row's largest candidate
     int tid, warp, lane;
 
@@ -263,25 +268,31 @@ struct Slice {
         for (int i = tid; i < 64; i += T) exp2_[i] = c_exp2[i];
     }
 
-    // z of a logit: c tanh(x / c) = -+c m / (2 + m), m = exp(-2 |x| / c) - 1: with 1 - exp() a cap far
+    // t_scale z of a logit, z = x or c tanh(x / c) = -+c m / (2 + m), m = exp(-2 |x| / c) - 1: with 1 - exp() a cap far
     // above the logits would cancel their digits. Below |x| / c = 2^-25 it is x to 2^-50. (scale keeps
     // 2 / c and |x| / c in range for the largest caps.)
     template <bool HERE = false>  // (for loops over all logits)
     __device__ __forceinline__ F2 capped(float x) const {
-        if (!(p.softcap > 0.f)) return F2{x, 0.f};
+        if (!(p.softcap > 0.f)) return F2{x * t_scale, 0.f};
         const F2 y = F2{fabsf(x) * scale, 0.f} * inner;
-        if (y.h > -0x1p-24f) return F2{x, 0.f};
+        if (y.h > -0x1p-24f) return F2{x * t_scale, 0.f};
         const F2 m = HERE ? expm1_f2_here(y, exp2) : expm1_f2(y, exp2);
-        F2 t = F2{-m.h, -m.l} / (F2{2.f, 0.f} + m);
+        F2 t = F2{-m.h, -m.l} / (2.f + m);
         if (isinf(x)) t = F2{1.f, 0.f};
-        t = t * F2{p.softcap, 0.f};
+        t = t * F2{p.softcap * t_scale, 0.f};
         return x < 0.f ? F2{-t.h, -t.l} : t;
     }
-    // exp((z - top) / T) of a logit z <= top
+    // Above 2^64 a temperature and the z that it divides are taken 2^-64 times: 1 / T and the
+    // differences of the largest logits would leave fp32's range.
+    __device__ void set_temperature(float t) {
+        t_scale = t > 0x1p64f ? 0x1p-64f : 1.f;
+        inv_t = t > 0.f ? F2{1.f, 0.f} / F2{t * t_scale, 0.f} : F2{0.f, 0.f};
+    }
+    // exp((z - top) / T) of a logit z <= top, both times t_scale
     template <bool HERE = false>
     __device__ __forceinline__ F2 relative(F2 z, F2 top) const {
-        const F2 d = z + F2{-top.h, -top.l};
         if (isinf(top.h)) return F2{isinf(z.h) && z.h > 0.f ? 1.f : 0.f, 0.f};
+        const F2 d = z + F2{-top.h, -top.l};
         if (d.h == 0.f) return F2{1.f, 0.f};
         if (!(d.h > -1e30f)) return F2{0.f, 0.f};
         return HERE ? exp_f2_here(d * inv_t, exp2) : exp_f2(d * inv_t, exp2);
@@ -293,7 +304,8 @@ struct Slice {
     // error of 2^-55 each; without a cap). Adds such a weight to `tiny`, else returns false.
     __device__ bool tiny_weight(uint32_t key, float& tiny) const {
         if (key == key_max || isinf(zmax.h)) return false;
-        const F2 a = two_sum(K::value(key), -zmax.h);  // (zmax.l is zero without a cap)
+        // (zmax.l is zero without a cap)
+        const F2 a = two_sum(K::value(key) * t_scale, -zmax.h);
         const float d = __fmul_rn(a.h, inv_t.h);
         if (!(d < -23.f)) return false;
         const float rest = __fmaf_rn(a.h, inv_t.h, -d) + (a.l * inv_t.h + a.h * inv_t.l);
@@ -454,9 +466,6 @@ struct Filters {
         const uint32_t n = want();
         return n ? n <= kListK : F32 && !(softcap > 0.f);
     }
-    __device__ F2 inverse_t() const {
-        return t > 0.f ? F2{1.f, 0.f} / F2{t, 0.f} : F2{0.f, 0.f};
-    }
 };
 
 // The short list. A row with a top_k up to kListK, and an fp32 row without one or a cap, is drawn
@@ -512,7 +521,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
         return;
     }
     const uint32_t n = want ? want : kListK;
-    r.inv_t = f.inverse_t();
+    r.set_temperature(f.t);
     const uint32_t best = r.thread_max();
 
     // The n-th and the (n / C)-th largest of the threads' keys (0 if fewer threads have one): every
@@ -873,7 +882,7 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
     }
     const float t = f.t, top_p = f.top_p, min_p = f.min_p, u = f.u;
     const int want_k = f.top_k;
-    r.inv_t = f.inverse_t();
+    r.set_temperature(f.t);
     s.before[tid] = s.before[tid + kThreads] = 0;
     u64* mass = F32 ? p.mass + (size_t)row * kBins : nullptr;
 

@@ -126,3 +126,25 @@ def test_large_caps(softcap, dtype):
     softcap = float(np.float32(softcap))
     check(x, 64, softcap=softcap, m=300)
     check(x, 64, softcap=softcap, m=300, k=250)
+
+
+def test_logits_as_large_as_the_cap():
+    """Logits, caps and temperatures of 1e38."""
+    x = torch.tensor([3e38, 2.9e38, 1e38, 0.0, -1e38, -3.3e38])
+    for c in (3e38, 1e38):
+        c = float(np.float32(c))
+        check(x, 4, t=8e37, softcap=c, m=5)
+        check(x.bfloat16(), 4, t=8e37, softcap=c, m=5)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_large_temperatures(dtype):
+    """Temperatures of 1e20 to 3e38 with logits as large, up to the type's lowest number: their
+    differences leave fp32's range, the weights are ordinary."""
+    low = torch.finfo(dtype).min
+    for t in (1e20, 1e31, 3e38):
+        t = float(np.float32(t))
+        x = torch.tensor([0.9, 0.8, 0.1, 0.0, -0.3, -0.7]).double() * t
+        x = torch.cat([x.to(dtype), torch.tensor([low], dtype=dtype)])
+        for k in (0, 6, 7, 300):
+            check(x, 6, t=t, m=6, k=k)
