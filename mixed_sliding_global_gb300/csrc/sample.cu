@@ -300,14 +300,15 @@ struct Slice {
     __device__ F2 weight(uint32_t key) const {
         return key == key_max ? F2{1.f, 0.f} : relative(capped(K::value(key)), zmax);
     }
-    // Most of a row lies below 2^-33 of the largest weight: single precision is enough there (an
-    // error of 2^-55 each; without a cap). Adds such a weight to `tiny`, else returns false.
-    __device__ bool tiny_weight(uint32_t key, float& tiny) const {
+    // Most of a row lies below e^-9 / vocab of the largest weight: single precision is enough there
+    // (the rounding of all of them together is within 2^-34 of the largest; without a cap). Adds such a
+    // weight, exp(d) with d < below, to `tiny`, else returns false.
+    __device__ bool tiny_weight(uint32_t key, float below, float& tiny) const {
         if (key == key_max || isinf(zmax.h)) return false;
         // (zmax.l is zero without a cap)
         const F2 a = two_sum(K::value(key) * t_scale, -zmax.h);
         const float d = __fmul_rn(a.h, inv_t.h);
-        if (!(d < -23.f)) return false;
+        if (!(d < below)) return false;
         const float rest = __fmaf_rn(a.h, inv_t.h, -d) + (a.l * inv_t.h + a.h * inv_t.l);
         if (d > -80.f) tiny += expf(d) * (1.f + rest);
         return true;
@@ -576,6 +577,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
         // the CTA's to 2^-43.
         F2 mine{0.f, 0.f};
         auto add = [&](F2 w) { mine = mine + w; };
+        const float below = -9.f - logf((float)p.vocab);
         // (those near the largest one, a few per hundred, are weighed together afterwards: in place
         // one lane's would hold up its warp)
         uint32_t* near = reinterpret_cast<uint32_t*>(s.pool);
@@ -598,7 +600,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 const uint32_t key = now[k];
-                if (key < K::kLow || key > K::kInf || r.tiny_weight(key, tiny)) continue;
+                if (key < K::kLow || key > K::kInf || r.tiny_weight(key, below, tiny)) continue;
                 const uint32_t i = atomicAdd(&s.n_near, 1u);
                 if (i < 2 * kListMax) near[i] = key;
             }
@@ -613,7 +615,7 @@ __global__ void __launch_bounds__(kListThreads) list_kernel(const SampleParams p
             for (int i = (int)r.i0 + tid; i < i1; i += T) {
                 const uint32_t key = K::of(load(i));
                 float tiny = 0.f;  // (those are in the sum already)
-                if (key >= K::kLow && key <= K::kInf && !r.tiny_weight(key, tiny))
+                if (key >= K::kLow && key <= K::kInf && !r.tiny_weight(key, below, tiny))
                     add(r.weight(key));
             }
         }
