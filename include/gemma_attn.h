@@ -369,7 +369,8 @@ int gemma_kv_read_q4(const void* const* k_codes, const void* const* k_scales,
  * gemma_attn_softcap (0: none). q and out are bf16 (GEMMA_FP32 gives GEMMA_ERR_UNSUPPORTED).
  * Cache rows outside every query token's keys may hold anything; a NaN group of V at a key that
  * only some tokens of a call see may reach the others' same 64 columns. V groups whose scale is
- * below 2^-19 of the largest of the sequence and KV head lose bits.
+ * below 2^-19 of the largest of the sequence and KV head lose bits, and so do elements of a query
+ * row below 2^-30 of its largest (each is off by at most 2^-38 of that).
  * Scratch: gemma_attn_workspace_size_q4(...) bytes; calls that may overlap must not share it. */
 int gemma_attn_q4(void* out, const void* q, const void* const* k_codes,
                   const void* const* k_scales, const void* const* v_codes,
@@ -439,7 +440,7 @@ size_t gemma_logit_workspace_size(int batch, int vocab);
  * cap), with equal weights. A temperature below 2^-126 draws from the equal largest logits alone.
  * Weights are accurate to about 2^-40 of the largest one, with a cap also to the error of z, 2^-47
  * softcap or 2^-40 |z| if that is less, divided by the temperature; their sums to about 2^-34 of the
- * sum. The result does not depend on scheduling: the same call gives the same tokens.
+ * sum (for fp32 logits 2^-28 among tokens below 2^-40 of the largest). The result does not depend on scheduling: the same call gives the same tokens.
  *   logits      DEVICE [batch][vocab] of dtype, row-major, 16-byte aligned.
  *   temperature, top_k, top_p, min_p
  *               DEVICE float / int32 / float / float [batch], each optional: NULL stands for 1, 0,

@@ -227,7 +227,9 @@ GEMMA_DEVINL float fast_exp2(float x) {
 // stream be scheduled as soon as it starts, and waits for the previous kernel to complete (and
 // its memory to be visible) before its own first global memory access; so a kernel's launch
 // latency overlaps its predecessor's tail while the order of memory accesses stays the
-// stream's. Without the launch attribute both instructions have no effect.
+// stream's. Without the launch attribute both instructions have no effect. Two kernels of
+// sample.cu go together otherwise: list_kernel is launched without the attribute, and behind it
+// sample_kernel may work on rows that the lists do not touch before it waits.
 GEMMA_DEVINL void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
 GEMMA_DEVINL void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

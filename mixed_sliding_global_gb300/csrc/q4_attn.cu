@@ -16,7 +16,7 @@
 // CTA will meet and turns their queries into fragments, one part ahead; eight warps each take 16
 // keys of S over all of head_dim, exchange P through shared memory (one barrier per tile) and take a
 // 64-column group of O (at head_dim < 512 the warps of a group share out the tile's keys). Two CTAs
-// per SM: 96 registers a thread, which the query fragments leave free up to head_dim 256 (8 rows) or
+// per SM (one at head_dim 512 with a V of its own, where two stages take 139 KB): 96 registers a thread, which the query fragments leave free up to head_dim 256 (8 rows) or
 // 64 (16 rows); beyond they are read from shared memory for every tile.
 // The softmax reference m is common to the CTA and lazy: a row's is 2^-6 of its largest weight when
 // it is set, and moves only when a score exceeds it by more than 2^14, which the tile's one barrier
@@ -453,7 +453,8 @@ __global__ void __launch_bounds__(kThreads, kQ4CtasPerSm)
     // One warp turns query row r of a part into fp16 fragments: lane (g, tq) will hold, of row g of
     // each 8-row tile, elements 16 tq .. 16 tq + 15 of every group, the ones whose codes it reads.
     // The row is scaled by a power of two that brings its largest element into [2^13, 2^14)
-    // (exact unless an element is below 2^-37 of that).
+    // (exact unless an element is below 2^-30 of that, then off by at most 2^-38 of it: 2^-25, half of
+    // fp16's smallest step).
     auto prepare_row = [&](const Job& j, int slot, int r) {
         constexpr int CH = (D / 8 + 31) / 32;
         uint4 raw[CH];

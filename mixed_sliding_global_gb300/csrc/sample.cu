@@ -17,18 +17,19 @@
 // the bin's own largest weight, so the order of the additions does not matter). The few hundred
 // logits of a bin that a cut or the draw falls into are gathered and put in order; a bin of more
 // than 1,024 takes the histogram again, over its lower 16 bits (a row of 262,144, flat
-// and with a cap: 82 us, 190 with histograms of the bins; half of it are the weights, not their
+// and with a cap: 81 us, 190 with histograms of the bins; half of it are the weights, not their
 // atomics: with sums in shared memory it took 9 us longer).
 //
 // Rows with a top_k of at most 256 (and fp32 rows without one or a cap) hardly get there: a launch
 // ahead (list_kernel) draws them from the list of their largest logits, and flags those that it
 // could not decide.
 //
-// What bounds it, per row of 262,144 bf16 logits (0.08 us at the memory's rate): latencies. One row with top_k 64: 14.0 us, of it 2.5 for reading the slices and the rest
-// barriers of the cluster, the list's order and two launches; a row by histogram: 28 us, of it 3
+// What bounds it, per row of 262,144 bf16 logits (0.08 us at the memory's rate): latencies. One row with
+// top_k 64: 14.5 us, of it 2.5 for reading the slices and the rest barriers of the cluster, the
+// list's order and two launches; a row by histogram: 29 us, of it 3
 // for counting (bound by shared-memory atomics; runs of eight equal logits count as one, so that
 // a row masked with one finite value does not queue on one counter), 4.5 for merging the counts,
-// 12 for cuts and draw. 64 rows by histogram: 103 us (three rounds of clusters), of which 5 us
+// 12 for cuts and draw. 64 rows by histogram: 106 us (three rounds of clusters), of which 5 us
 // would do at the memory's rate.
 #include <atomic>
 
@@ -471,8 +472,8 @@ struct Filters {
 
 // The short list. A row with a top_k up to kListK, and an fp32 row without one or a cap, is drawn
 // from its n = top_k (kListK) largest logits alone. In us, the list and the histograms: bf16, one
-// row of 262,144: top_k 20 13.3, 27.8; 256 21.7, 24.7; 64 rows: 35.2, 104.8 and 55.0, 94.8; fp32, 9
-// rows of 70,001 that top_p 0.9 ends within the list: 28.1, 46. (With a cap the sum of all weights
+// row of 262,144: top_k 20 12.9, 27.8; 256 21.6, 24.7; 64 rows: 35.2, 104.8 and 55.0, 94.8; fp32, 9
+// rows of 70,001 that top_p 0.9 ends within the list: 29.2, 46. (With a cap the sum of all weights
 // took longer than the histograms do: 157, 88.) The n-th largest of a CTA's threads' largest keys bounds
 // the row's n-th largest logit from below, and so does the smallest over the CTAs of each one's
 // (n / C)-th: every CTA sends its slice's keys down to the higher of these bounds to one of them,
@@ -1108,8 +1109,8 @@ __device__ void draw_row(const SampleParams& p, Shared& s, uint32_t* hist, int C
         if (F32) {
             // Weights of every number above the cut's bin, relative to its bin's largest. Behind a cut
             // they are few: 2,048 logits at a time, those that count go to a queue and then to all
-            // threads evenly. (64 rows of 32,000 with top_k 1,000: 92 us; evaluated where they were
-            // loaded, 334: every warp ran the long code for a lane or two, each at another place.)
+            // threads evenly. (64 rows of 32,000 of deviation 8 with top_k 1,000 and top_p 0.9: 78 us. When
+            // this was done 334 became 91, the weights evaluated where they were loaded: every warp ran the long code for a lane or two, each at another place.)
             const uint32_t* x = static_cast<const uint32_t*>(p.logits) + (long long)row * p.vocab;
             const int i1 = (int)r.i1;
             auto load = [&](int i) { return i < i1 ? x[i] : 0x7fffffffu; };  // (NaN: none)
@@ -1611,8 +1612,11 @@ cudaError_t launch(const SampleParams& p, cudaStream_t st) {
         const int c = (p.vocab + slice - 1) / slice, C = c > most ? most : c;
         cudaError_t e = configure(list_kernel<F32>, lists[dev], 64 * 1024);
         if (e != cudaSuccess) return e;
-        // (not ahead of the launch before it: that one's CTAs may fill most SMs, and the lists
-        // would crowd on the others: 22.8 us for 8 rows of 262,144 logits against 16.1)
+        // Not ahead of the launch before it. sample_kernel's first pass (kAhead) relies on that: it reads
+        // logits and filters and writes tokens and sums before it waits for the lists, so everything
+        // before these has to be complete when they start. It is faster too: the CTAs of the launch
+        // before may fill most SMs, and the lists would crowd on the others (22.8 us for 8 rows of
+        // 262,144 logits against 16.1).
         Launch l(p.batch, C, kListThreads, sizeof(ListShared), false, st);
         e = cudaLaunchKernelEx(&l.cfg, list_kernel<F32>, p, C);
         if (e != cudaSuccess) return e;
