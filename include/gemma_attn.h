@@ -370,7 +370,8 @@ int gemma_kv_read_q4(const void* const* k_codes, const void* const* k_scales,
  * Cache rows outside every query token's keys may hold anything; a NaN group of V at a key that
  * only some tokens of a call see may reach the others' same 64 columns. V groups whose scale is
  * below 2^-19 of the largest of the sequence and KV head lose bits, and so do elements of a query
- * row below 2^-30 of its largest (each is off by at most 2^-38 of that).
+ * row below 2^-30 of its largest (each is off by at most 2^-38 of that). Weighted values are summed
+ * before they are divided by the weights' sum: values beyond about 2^100 may overflow there.
  * Scratch: gemma_attn_workspace_size_q4(...) bytes; calls that may overlap must not share it. */
 int gemma_attn_q4(void* out, const void* q, const void* const* k_codes,
                   const void* const* k_scales, const void* const* v_codes,
