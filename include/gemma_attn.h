@@ -75,6 +75,9 @@ typedef enum {
 #define GEMMA_DEVERR_PAGE 16u      /* a block-table entry outside [0, n_pages) (paged entry points) */
 
 #define GEMMA_DEVERR_SAMPLE 32u    /* gemma_logit_sample: bad parameters, or a row without candidates */
+#define GEMMA_DEVERR_TREE 64u      /* parents[b][i] outside [-1, i), or a path that is none */
+#define GEMMA_DEVERR_FORK 128u     /* gemma_pages_fork: a bad sequence, or a destination in use */
+#define GEMMA_DEVERR_POOL_FULL 256u /* gemma_pages_reserve: no free page left */
 
 /*
  * gemma_kv_append -- write this step's new K (and V) rows of an owner layer into its cache.
@@ -387,6 +390,170 @@ int gemma_attn_q4(void* out, const void* q, const void* const* k_codes,
 size_t gemma_attn_workspace_size_q4(int batch, gemma_layer_kind kind, int window, int n_q,
                                     int n_kv, int head_dim, int max_seq_len, int n_new,
                                     int k_eq_v);
+
+/*
+ * Drafted trees -- one decode step that checks several drafted continuations of a sequence at once.
+ * The pages decode one token per step (first page, section 5.1); here a step brings a tree of up to
+ * GEMMA_TREE_MAX_NODES drafted tokens per sequence: node 0 is the last token that the sequence has
+ * for certain, every other node a guess of what follows its parent.
+ *   n_nodes     nodes of the bucket, at most GEMMA_TREE_MAX_NODES (else GEMMA_ERR_UNSUPPORTED).
+ *   n_real      DEVICE int32 [batch], or NULL: a sequence's own nodes are the first n_real[b] of the
+ *               bucket's, 0 <= n_real[b] <= n_nodes (else GEMMA_DEVERR_N_REAL).
+ *   parents     DEVICE int32 [batch][n_nodes]: parents[b][i] is an earlier node (< i), or -1: a
+ *               root. Anything else in a sequence's own nodes sets GEMMA_DEVERR_TREE, and the
+ *               sequence is skipped. Entries behind them are not read as nodes.
+ * A step: gemma_kv_append (_bucket, _ring, _paged) writes the nodes' rows at positions base + i;
+ * gemma_attn_tree attends, layer by layer; the next token behind each node is drawn from the final
+ * logits (gemma_logit_softcap_argmax, gemma_logit_sample); gemma_tree_accept follows those tokens
+ * through the tree; gemma_kv_keep moves the accepted nodes' rows together, in every cache.
+ */
+#define GEMMA_TREE_MAX_NODES 128
+
+/*
+ * gemma_attn_tree -- attention of a tree's nodes over the cache. Per sequence b, with n its nodes:
+ *   base   = seq_lens[b] - n            node i's rows lie at cache position base + i
+ *   depth  = its number of ancestors    node i stands at position base + depth(i) of the text
+ *   keys(i) = { j < base, on a sliding layer with base + depth(i) - j < window }, and
+ *             { base + m : m is node i or an ancestor, on a sliding layer with
+ *                          depth(i) - depth(m) < window }
+ *   out    = sum_j softmax_j(scale * q . K[j]) * V[j]   over those keys, the scores soft-capped as
+ *            in gemma_attn_softcap where softcap > 0.
+ * A chain (parents[i] = i - 1) is gemma_attn_prefill. Source of layers, heads and windows: as for
+ * gemma_attn_decode; rotary positions are the caller's (base + depth(i)).
+ *   out, q            DEVICE [batch][n_nodes][n_q][head_dim]; rows behind a sequence's own nodes, and
+ *                     those of skipped sequences, are written as zeros.
+ *   seq_lens          DEVICE int32 [batch], n <= seq_lens[b] <= max_seq_len, counting the nodes.
+ *   block_table       NULL: a plain or ring cache of kv_capacity slots; else a paged pool as for
+ *                     gemma_attn_paged (kv_capacity is ignored; GEMMA_SLIDING_RING gives
+ *                     GEMMA_ERR_INVALID_ARG). Pages are read from the first window's start rounded
+ *                     down to a multiple of 64 keys.
+ *   A ring needs kv_capacity >= window + n_nodes - 1.
+ * bf16 and fp32 (the debug path). Cache rows that no node of the sequence attends may hold anything;
+ * a NaN or infinite V row of one branch may reach the other branches' outputs. P is rounded to bf16
+ * before it weighs V, as in the other bf16 entry points.
+ * Scratch: gemma_attn_workspace_size_tree(...) bytes (fp32 needs none); calls that may overlap must
+ * not share it. Other arguments and errors as for gemma_attn_decode.
+ */
+int gemma_attn_tree(void* out, const void* q, const void* const* k_cache,
+                    const void* const* v_cache, const int32_t* owner_map, int n_layers, int layer,
+                    const int32_t* seq_lens, const int32_t* parents, const int32_t* n_real,
+                    const int32_t* block_table, int max_pages, int page_size, int n_pages,
+                    int max_seq_len, int n_nodes, int batch, gemma_layer_kind kind, int window,
+                    int n_q, int n_kv, int head_dim, int k_eq_v, int kv_capacity, float scale,
+                    float softcap, gemma_dtype dtype, void* workspace, size_t workspace_bytes,
+                    uint32_t* device_error, void* stream);
+
+/* Scratch bytes of gemma_attn_tree for these arguments on the current device ((size_t)-1 for
+ * arguments that it refuses). */
+size_t gemma_attn_workspace_size_tree(int batch, gemma_layer_kind kind, int window, int n_q,
+                                      int n_kv, int head_dim, int max_seq_len, int n_nodes);
+
+/*
+ * gemma_tree_accept -- the drafted tokens that hold. From node 0, as long as a child of the current
+ * node has the token drawn behind that node, go on to the lowest such child:
+ *   path[0] = 0;  path[k + 1] = min { c : parents[b][c] == path[k], tokens[b][c] == next[b][path[k]] }
+ *   tokens, parents, next   DEVICE int32 [batch][n_nodes]: the nodes' tokens, the tree, and the
+ *               token drawn behind each node. A negative next token ends the path.
+ *   path_out    DEVICE int32 [batch][n_nodes]: the path's nodes, then -1.
+ *   n_keep_out  DEVICE int32 [batch]: its length, at least 1 for a tree with nodes.
+ *   token_out   DEVICE int32 [batch]: next[b][last node of the path], the token that follows it.
+ *   seq_lens    DEVICE int32 [batch] counting the nodes, or NULL.
+ *   lens_out    DEVICE int32 [batch], or NULL: seq_lens[b] - n + n_keep; may be seq_lens itself.
+ * A sequence without nodes, or with a bad tree, gets n_keep 0 and token -1 (lens_out then counts
+ * none of its nodes); one with a bad n_real or length also keeps its length.
+ */
+int gemma_tree_accept(const int32_t* tokens, const int32_t* parents, const int32_t* next,
+                      const int32_t* n_real, const int32_t* seq_lens, int batch, int n_nodes,
+                      int32_t* path_out, int32_t* n_keep_out, int32_t* token_out,
+                      int32_t* lens_out, uint32_t* device_error, void* stream);
+
+/*
+ * gemma_kv_keep -- move the accepted nodes' rows to where the sequence goes on:
+ *   cache[b][h][write_pos[b] + i][:] = its row at write_pos[b] + path[b][i]   for i < n_keep[b],
+ * in the order of i, in every cache of the call; all other rows stay as they are.
+ *   caches      HOST array [n_caches] of DEVICE caches [batch][n_kv][kv_capacity] of rows of
+ *               row_bytes bytes (even; bf16, fp32 and 4-bit caches' codes and scales alike), or of
+ *               pools [n_pages][n_kv][page_size] with a block table. A ring wraps (kind
+ *               GEMMA_SLIDING_RING, kv_capacity >= n_nodes); the other kinds move alike.
+ *   write_pos   DEVICE int32 [batch]: position of node 0's row (the append's write_pos).
+ *   path        DEVICE int32 [batch][n_nodes], rising strictly within [0, n_nodes) up to n_keep[b].
+ *   n_keep      DEVICE int32 [batch], 0 <= n_keep[b] <= n_nodes.
+ * A bad path or n_keep sets GEMMA_DEVERR_TREE, a position outside the cache GEMMA_DEVERR_WRITE_POS,
+ * and nothing of the sequence moves; rows from or to a bad page stay (GEMMA_DEVERR_PAGE). With a
+ * block table the positions' pages must not be shared with another sequence
+ * (gemma_pages_reserve).
+ */
+int gemma_kv_keep(void* const* caches, int n_caches, const int32_t* write_pos, const int32_t* path,
+                  const int32_t* n_keep, const int32_t* block_table, int max_pages, int page_size,
+                  int n_pages, int batch, int n_nodes, gemma_layer_kind kind, int n_kv,
+                  int kv_capacity, int row_bytes, uint32_t* device_error, void* stream);
+
+/*
+ * Pages of a pool -- the block table of the paged entry points kept on the device, so that a step
+ * that takes, shares and gives back pages can be captured in a graph.
+ *   block_table DEVICE int32 [batch][max_pages], here also written; a negative entry: no page.
+ *   page_refs   DEVICE int32 [n_pages]: how many entries hold the page. A page is free while this is
+ *               0. The caller starts with all 0 and all entries -1, and keeps the two in step where
+ *               it edits them itself.
+ * page_size is a multiple of 128, n_pages at most 2^29, batch * max_pages below 2^31, batch at most
+ * 65535 (else GEMMA_ERR_UNSUPPORTED). An entry outside [.., n_pages), or one whose page nobody
+ * holds, sets GEMMA_DEVERR_PAGE and is left alone. Results do not depend on scheduling. Calls on one
+ * table must not overlap each other, nor a call that reads or writes its pages.
+ */
+
+/* gemma_pages_free -- give back the pages that hold no position in [keep_from[b], keep_to[b]): all of
+ * a finished sequence (keep_to 0), what lies before a sliding window (keep_from), rejected or
+ * reserved positions at the end (keep_to).
+ *   keep_from, keep_to   DEVICE int32 [batch]; one of them may be NULL (no bound). */
+int gemma_pages_free(int32_t* block_table, int max_pages, int page_size, int n_pages,
+                     int32_t* page_refs, const int32_t* keep_from, const int32_t* keep_to,
+                     int batch, uint32_t* device_error, void* stream);
+
+/* gemma_pages_fork -- sequence dst[i] goes on from what sequence src[i] holds: it shares the pages
+ * of the source's first seq_lens[src[i]] positions, and seq_lens[dst[i]] becomes that length.
+ *   seq_lens    DEVICE int32 [batch], read and written.
+ *   src, dst    DEVICE int32 [n], n <= batch.
+ * A destination must hold no page and be no source of the call; of equal destinations the first
+ * counts. Other forks set GEMMA_DEVERR_FORK (a source of a length outside its table
+ * GEMMA_DEVERR_SEQ_LEN) and change nothing. */
+int gemma_pages_fork(int32_t* block_table, int max_pages, int page_size, int n_pages,
+                     int32_t* page_refs, int32_t* seq_lens, const int32_t* src, const int32_t* dst,
+                     int n, int batch, uint32_t* device_error, void* stream);
+
+/* gemma_pages_reserve -- pages of their own for the positions [seq_lens[b], seq_lens[b] + n_add[b])
+ * of every sequence, before they are written. A position without a page gets a free one, the lowest
+ * first, in the order of sequences and positions. Of a shared page every holder that is about to
+ * write to it gets a copy of its rows below seq_lens[b], in every pool, but for the first holder (in
+ * the order of sequences) where all holders are in the call: it keeps the page.
+ *   pools           HOST array [n_pools] of DEVICE pools [n_pages][pool_n_kv[j]][page_size] of rows
+ *                   of pool_row_bytes[j] bytes (even): all pools that the table stands for, K and V of
+ *                   every owner layer (codes and scales of 4-bit ones).
+ *   n_add           DEVICE int32 [batch], >= 0; positions beyond max_pages * page_size, or a negative
+ *                   length, skip the sequence (GEMMA_DEVERR_WRITE_POS).
+ *   workspace       DEVICE scratch of gemma_pages_workspace_size(n_pages) bytes, 16-byte aligned;
+ *                   contents on entry are ignored; calls that may overlap must not share it.
+ * Where the free pages run out (GEMMA_DEVERR_POOL_FULL) the positions that are left stay without a
+ * page, or on their shared one, and must not be written; the same call goes on once pages are free. */
+int gemma_pages_reserve(void* const* pools, const int32_t* pool_n_kv,
+                        const int32_t* pool_row_bytes, int n_pools, int32_t* block_table,
+                        int max_pages, int page_size, int n_pages, int32_t* page_refs,
+                        const int32_t* seq_lens, const int32_t* n_add, int batch, void* workspace,
+                        size_t workspace_bytes, uint32_t* device_error, void* stream);
+
+/* gemma_pages_compact -- move the pages in use to the front of the pools, so that what lies behind
+ * them can be taken away: with n_used the number of pages in use, the i-th of them at or behind
+ * n_used (by index) moves to the i-th free page before n_used, in every pool, table entry and count.
+ *   n_used_out      DEVICE int32 [1], or NULL.
+ *   Other arguments as for gemma_pages_reserve. */
+int gemma_pages_compact(void* const* pools, const int32_t* pool_n_kv,
+                        const int32_t* pool_row_bytes, int n_pools, int32_t* block_table,
+                        int max_pages, int page_size, int n_pages, int32_t* page_refs,
+                        int32_t* n_used_out, int batch, void* workspace, size_t workspace_bytes,
+                        uint32_t* device_error, void* stream);
+
+/* Scratch bytes of gemma_pages_reserve and gemma_pages_compact ((size_t)-1 for n_pages outside
+ * [1, 2^29]). */
+size_t gemma_pages_workspace_size(int n_pages);
 
 /*
  * gemma_logit_softcap_argmax -- final-logit soft-cap and greedy argmax of each row.

@@ -9,7 +9,8 @@ loading fails loudly when the library has not been built.
 from .binding import (  # noqa: F401
     GEMMA_SLIDING, GEMMA_GLOBAL, GEMMA_SLIDING_RING, GEMMA_BF16, GEMMA_FP32, GEMMA_OK,
     GEMMA_DEVERR_SEQ_LEN, GEMMA_DEVERR_WRITE_POS, GEMMA_DEVERR_TIMEOUT, GEMMA_DEVERR_N_REAL,
-    GEMMA_DEVERR_PAGE, GEMMA_DEVERR_SAMPLE,
+    GEMMA_DEVERR_PAGE, GEMMA_DEVERR_SAMPLE, GEMMA_DEVERR_TREE, GEMMA_DEVERR_FORK,
+    GEMMA_DEVERR_POOL_FULL, GEMMA_TREE_MAX_NODES,
     GemmaError, library, library_path, exported_symbols,
     gemma_kv_append, gemma_attn_decode, gemma_attn_decode_static, gemma_attn_prefill, gemma_attn_softcap,
     gemma_kv_append_bucket, gemma_attn_prefill_bucket, gemma_attn_decode_append,
@@ -17,5 +18,8 @@ from .binding import (  # noqa: F401
     gemma_kv_append_q4, gemma_kv_read_q4, gemma_attn_q4, gemma_attn_workspace_size_q4,
     gemma_attn_workspace_size, gemma_logit_softcap_argmax, gemma_logit_workspace_size,
     gemma_logit_sample, gemma_logit_sample_workspace_size,
+    gemma_attn_tree, gemma_attn_workspace_size_tree, gemma_tree_accept, gemma_kv_keep,
+    gemma_pages_free, gemma_pages_fork, gemma_pages_reserve, gemma_pages_compact,
+    gemma_pages_workspace_size,
     gemma_status_string, gemma_abi_version,
 )

@@ -17,6 +17,8 @@ GEMMA_DEVERR_SEQ_LEN, GEMMA_DEVERR_WRITE_POS, GEMMA_DEVERR_TIMEOUT = 1, 2, 4
 GEMMA_DEVERR_N_REAL = 8
 GEMMA_DEVERR_PAGE = 16
 GEMMA_DEVERR_SAMPLE = 32
+GEMMA_DEVERR_TREE, GEMMA_DEVERR_FORK, GEMMA_DEVERR_POOL_FULL = 64, 128, 256
+GEMMA_TREE_MAX_NODES = 128
 
 _c_int, _c_void_p, _c_size_t, _c_float = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_float
 _PVOID = ctypes.POINTER(ctypes.c_void_p)
@@ -85,6 +87,23 @@ _SIGNATURES = {
                            [_c_void_p] * 7 + [_c_size_t, _c_void_p, _c_void_p]),
     "gemma_logit_sample_workspace_size": (_c_size_t, [_c_int, _c_int, _c_int]),
     "gemma_logit_workspace_size": (_c_size_t, [_c_int, _c_int]),
+    "gemma_attn_tree": (_c_int, [_c_void_p, _c_void_p, _PVOID, _PVOID, _PI32, _c_int, _c_int] +
+                        [_c_void_p] * 4 + [_c_int] * 13 + [_c_float, _c_float, _c_int, _c_void_p,
+                                                           _c_size_t, _c_void_p, _c_void_p]),
+    "gemma_attn_workspace_size_tree": (_c_size_t, [_c_int] * 8),
+    "gemma_tree_accept": (_c_int, [_c_void_p] * 5 + [_c_int, _c_int] + [_c_void_p] * 6),
+    "gemma_kv_keep": (_c_int, [_PVOID, _c_int] + [_c_void_p] * 4 + [_c_int] * 9 + [_c_void_p] * 2),
+    "gemma_pages_free": (_c_int, [_c_void_p, _c_int, _c_int, _c_int] + [_c_void_p] * 3 +
+                         [_c_int, _c_void_p, _c_void_p]),
+    "gemma_pages_fork": (_c_int, [_c_void_p, _c_int, _c_int, _c_int] + [_c_void_p] * 4 +
+                         [_c_int, _c_int, _c_void_p, _c_void_p]),
+    "gemma_pages_reserve": (_c_int, [_PVOID, _PI32, _PI32, _c_int, _c_void_p, _c_int, _c_int,
+                                     _c_int] + [_c_void_p] * 3 + [_c_int, _c_void_p, _c_size_t,
+                                                                  _c_void_p, _c_void_p]),
+    "gemma_pages_compact": (_c_int, [_PVOID, _PI32, _PI32, _c_int, _c_void_p, _c_int, _c_int,
+                                     _c_int] + [_c_void_p] * 2 + [_c_int, _c_void_p, _c_size_t,
+                                                                  _c_void_p, _c_void_p]),
+    "gemma_pages_workspace_size": (_c_size_t, [_c_int]),
     "gemma_status_string": (ctypes.c_char_p, [_c_int]),
     "gemma_abi_version": (_c_int, []),
 }
@@ -424,6 +443,114 @@ def gemma_attn_workspace_size_q4(batch: int, kind: int, window: int, n_q: int, n
                                                max_seq_len, n_new, int(bool(k_eq_v)))
     if n == ctypes.c_size_t(-1).value:
         raise ValueError("invalid arguments for gemma_attn_workspace_size_q4")
+    return int(n)
+
+
+def gemma_attn_tree(out: torch.Tensor, q: torch.Tensor, k_cache, v_cache, owner_map, layer: int,
+                    seq_lens: torch.Tensor, parents: torch.Tensor, max_seq_len: int, *, kind: int,
+                    window: int, n_kv: int, k_eq_v: bool, scale: float, softcap: float = 0.0,
+                    n_real: Optional[torch.Tensor] = None,
+                    block_table: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None,
+                    device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Attention of a drafted tree's nodes: q, out [B][n_nodes][n_q][d] (bf16 or fp32), parents int32
+    [B][n_nodes] (-1: a root), n_real int32 [B] (each sequence's own nodes; None: all), seq_lens
+    counting them. Caches per layer [B][n_kv][cap][d], or pools [n_pages][n_kv][page_size][d] with a
+    block_table int32 [B][max_pages]."""
+    st = (_bind or _native()).attn_tree(
+        k_cache, v_cache, owner_map, layer, out, q, seq_lens, parents, max_seq_len, kind, window,
+        n_kv, k_eq_v, scale, softcap, n_real, block_table, workspace, device_error, _handle(stream))
+    if st:
+        _check("gemma_attn_tree", st)
+
+
+def gemma_attn_workspace_size_tree(batch: int, kind: int, window: int, n_q: int, n_kv: int,
+                                   head_dim: int, max_seq_len: int, n_nodes: int) -> int:
+    n = library().gemma_attn_workspace_size_tree(batch, kind, window, n_q, n_kv, head_dim,
+                                                 max_seq_len, n_nodes)
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("invalid arguments for gemma_attn_workspace_size_tree")
+    return int(n)
+
+
+def gemma_tree_accept(tokens: torch.Tensor, parents: torch.Tensor, next_tokens: torch.Tensor,
+                      path_out: torch.Tensor, n_keep_out: torch.Tensor, token_out: torch.Tensor, *,
+                      n_real: Optional[torch.Tensor] = None,
+                      seq_lens: Optional[torch.Tensor] = None,
+                      lens_out: Optional[torch.Tensor] = None,
+                      device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The drafted path that the tokens drawn behind its nodes confirm: tokens, parents,
+    next_tokens, path_out int32 [B][n_nodes]; n_keep_out, token_out (and n_real, seq_lens,
+    lens_out) int32 [B]. lens_out may be seq_lens."""
+    st = (_bind or _native()).tree_accept(tokens, parents, next_tokens, path_out, n_keep_out,
+                                          token_out, n_real, seq_lens, lens_out, device_error,
+                                          _handle(stream))
+    if st:
+        _check("gemma_tree_accept", st)
+
+
+def gemma_kv_keep(caches, write_pos: torch.Tensor, path: torch.Tensor, n_keep: torch.Tensor, *,
+                  kind: int = GEMMA_GLOBAL, block_table: Optional[torch.Tensor] = None,
+                  device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Move rows write_pos[b] + path[b][i] to write_pos[b] + i, i < n_keep[b], in every cache of the
+    list: tensors [B][n_kv][cap][...] of one shape and any type (pools [n_pages][n_kv][page_size]
+    [...] with a block_table). kind GEMMA_SLIDING_RING wraps, the other kinds move alike."""
+    st = (_bind or _native()).kv_keep(caches, write_pos, path, n_keep, kind, block_table,
+                                      device_error, _handle(stream))
+    if st:
+        _check("gemma_kv_keep", st)
+
+
+def gemma_pages_free(block_table: torch.Tensor, page_refs: torch.Tensor, *, page_size: int,
+                     keep_from: Optional[torch.Tensor] = None,
+                     keep_to: Optional[torch.Tensor] = None,
+                     device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Give back the pages without a position in [keep_from[b], keep_to[b]) (int32 [B], one may be
+    None). block_table int32 [B][max_pages], page_refs int32 [n_pages]."""
+    st = (_bind or _native()).pages_free(block_table, page_refs, page_size, keep_from, keep_to,
+                                         device_error, _handle(stream))
+    if st:
+        _check("gemma_pages_free", st)
+
+
+def gemma_pages_fork(block_table: torch.Tensor, page_refs: torch.Tensor, seq_lens: torch.Tensor,
+                     src: torch.Tensor, dst: torch.Tensor, *, page_size: int,
+                     device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Sequence dst[i] shares the pages of sequence src[i] and gets its length (int32 [n])."""
+    st = (_bind or _native()).pages_fork(block_table, page_refs, seq_lens, src, dst, page_size,
+                                         device_error, _handle(stream))
+    if st:
+        _check("gemma_pages_fork", st)
+
+
+def gemma_pages_reserve(pools, block_table: torch.Tensor, page_refs: torch.Tensor,
+                        seq_lens: torch.Tensor, n_add: torch.Tensor, *,
+                        workspace: Optional[torch.Tensor] = None,
+                        device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Pages of their own for positions [seq_lens[b], seq_lens[b] + n_add[b]): free ones for those
+    without, copies of shared ones. pools: every tensor [n_pages][n_kv][page_size][...] that the
+    table stands for."""
+    st = (_bind or _native()).pages_reserve(pools, block_table, page_refs, seq_lens, n_add,
+                                            workspace, device_error, _handle(stream))
+    if st:
+        _check("gemma_pages_reserve", st)
+
+
+def gemma_pages_compact(pools, block_table: torch.Tensor, page_refs: torch.Tensor, *,
+                        n_used: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None,
+                        device_error: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Move the pages in use to the front of every pool; n_used int32 [1] gets their number."""
+    st = (_bind or _native()).pages_compact(pools, block_table, page_refs, n_used, workspace,
+                                            device_error, _handle(stream))
+    if st:
+        _check("gemma_pages_compact", st)
+
+
+def gemma_pages_workspace_size(n_pages: int) -> int:
+    n = library().gemma_pages_workspace_size(int(n_pages))
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError("invalid arguments for gemma_pages_workspace_size")
     return int(n)
 
 

@@ -11,6 +11,7 @@
 #include "logits.h"
 #include "q4.h"
 #include "sample.h"
+#include "tree.h"
 
 using gemma::RowsParams;
 
@@ -960,6 +961,352 @@ size_t gemma_logit_sample_workspace_size(int batch, int vocab, gemma_dtype dtype
         (dtype != GEMMA_BF16 && dtype != GEMMA_FP32))
         return (size_t)-1;
     return gemma::sample_workspace(batch, dtype == GEMMA_FP32);
+}
+
+// ---------------------------------------------------------------------------------------------
+// drafted trees
+// ---------------------------------------------------------------------------------------------
+namespace {
+
+// Chunks of keys per row tile: as many as keep one wave of CTAs, each of at least a tile of keys.
+struct TreePlan {
+    int n_split, chunk;
+    size_t o_bytes, ws_bytes;
+};
+TreePlan tree_plan(int batch, int kind, int window, int n_q, int n_kv, int head_dim,
+                   int max_seq_len, int n_nodes, int n_sm) {
+    const long long T = gemma::kTreeKeyTile;
+    const int rows = n_nodes * (n_q / n_kv), tile = 16 * gemma::tree_row_groups(rows);
+    const long long units = (long long)batch * n_kv * ((rows + tile - 1) / tile);
+    long long reach = kind == GEMMA_GLOBAL ? max_seq_len : (long long)window - 1 + n_nodes;
+    if (reach > max_seq_len) reach = max_seq_len;
+    reach += T - 1;  // (rings and pages start at whole tiles)
+    long long n = (long long)n_sm * gemma::tree_ctas_per_sm(head_dim, rows) / units;
+    if (n > kMaxSplit) n = kMaxSplit;
+    if (n < 1) n = 1;
+    TreePlan pl{1, 1 << 30, 0, 0};
+    const long long chunk = round_up((reach + n - 1) / n, T);
+    n = (reach + chunk - 1) / chunk;
+    if (n <= 1) return pl;
+    pl.n_split = (int)n;
+    pl.chunk = (int)chunk;
+    const size_t parts = (size_t)batch * n_q * n_nodes * n;
+    pl.o_bytes = parts * head_dim * sizeof(float);
+    pl.ws_bytes = pl.o_bytes + (size_t)round_up((long long)(parts * 2 * sizeof(float)), 256);
+    return pl;
+}
+
+// Sizes that gemma_attn_tree refuses whatever the pointers.
+int tree_sizes(int batch, int kind, int window, int n_q, int n_kv, int head_dim, int max_seq_len,
+               int n_nodes, int dtype) {
+    if (batch < 0 || n_nodes < 1 || max_seq_len < 1) return GEMMA_ERR_INVALID_ARG;
+    const int st = check_shape(kind, window, n_q, n_kv, head_dim, dtype);
+    if (st != GEMMA_OK) return st;
+    if (n_nodes > gemma::kTreeMaxNodes || batch > 65535 || n_kv > 65535 || max_seq_len > (1 << 30))
+        return GEMMA_ERR_UNSUPPORTED;
+    // (one warp per row and slice of a merge, one CTA per row of the fp32 path)
+    if ((long long)batch * n_q * n_nodes > (1ll << 30)) return GEMMA_ERR_UNSUPPORTED;
+    return GEMMA_OK;
+}
+
+}  // namespace
+
+size_t gemma_attn_workspace_size_tree(int batch, gemma_layer_kind kind, int window, int n_q,
+                                      int n_kv, int head_dim, int max_seq_len, int n_nodes) {
+    if (tree_sizes(batch, kind, window, n_q, n_kv, head_dim, max_seq_len, n_nodes, GEMMA_BF16) !=
+        GEMMA_OK)
+        return (size_t)-1;
+    if (batch == 0) return 0;
+    const int n_sm = sm_count();
+    if (n_sm < 0) return (size_t)-1;
+    return tree_plan(batch, kind, window, n_q, n_kv, head_dim, max_seq_len, n_nodes, n_sm).ws_bytes;
+}
+
+int gemma_attn_tree(void* out, const void* q, const void* const* k_cache,
+                    const void* const* v_cache, const int32_t* owner_map, int n_layers, int layer,
+                    const int32_t* seq_lens, const int32_t* parents, const int32_t* n_real,
+                    const int32_t* block_table, int max_pages, int page_size, int n_pages,
+                    int max_seq_len, int n_nodes, int batch, gemma_layer_kind kind, int window,
+                    int n_q, int n_kv, int head_dim, int k_eq_v, int kv_capacity, float scale,
+                    float softcap, gemma_dtype dtype, void* workspace, size_t workspace_bytes,
+                    uint32_t* device_error, void* stream) {
+    if (n_nodes == 0 && batch >= 0) return GEMMA_OK;
+    if (!std::isfinite(softcap) || softcap < 0.f) return GEMMA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || !(scale > 0.f)) return GEMMA_ERR_INVALID_ARG;
+    int st = tree_sizes(batch, kind, window, n_q, n_kv, head_dim, max_seq_len, n_nodes, dtype);
+    if (st != GEMMA_OK) return st;
+    const bool ring = kind == GEMMA_SLIDING_RING;
+    if (block_table) {
+        if (ring) return GEMMA_ERR_INVALID_ARG;
+        st = check_paged(max_pages, page_size, n_pages);
+        if (st != GEMMA_OK) return st;
+        if ((long long)n_pages * n_kv > (1ll << 31) - 1) return GEMMA_ERR_UNSUPPORTED;
+        kv_capacity = max_pages * page_size;
+    }
+    if (kv_capacity < 1) return GEMMA_ERR_INVALID_ARG;
+    if (kv_capacity > (1 << 30)) return GEMMA_ERR_UNSUPPORTED;
+    if (ring) {
+        if (kv_capacity % 128 != 0) return GEMMA_ERR_UNSUPPORTED;
+        if ((long long)kv_capacity < (long long)window + n_nodes - 1) return GEMMA_ERR_CAPACITY;
+    } else if (max_seq_len > kv_capacity) {
+        return GEMMA_ERR_CAPACITY;
+    }
+    int o = 0;
+    st = resolve_owner(owner_map, n_layers, layer, &o);
+    if (st != GEMMA_OK) return st;
+    if (batch == 0) return GEMMA_OK;
+    if (!out || !q || !seq_lens || !parents || !k_cache || !k_cache[o]) return GEMMA_ERR_INVALID_ARG;
+    if (!k_eq_v && (!v_cache || !v_cache[o])) return GEMMA_ERR_INVALID_ARG;
+    const void* kc = k_cache[o];
+    const void* vc = k_eq_v ? kc : v_cache[o];
+    if (!aligned16(out) || !aligned16(q) || !aligned16(kc) || !aligned16(vc))
+        return GEMMA_ERR_INVALID_ARG;
+    for (const void* x : {static_cast<const void*>(seq_lens), static_cast<const void*>(parents),
+                          static_cast<const void*>(n_real), static_cast<const void*>(block_table),
+                          static_cast<const void*>(device_error)})
+        if (!aligned4(x)) return GEMMA_ERR_INVALID_ARG;
+    const int n_sm = sm_count();
+    if (n_sm < 0) return GEMMA_ERR_CUDA;
+    const TreePlan pl =
+        tree_plan(batch, kind, window, n_q, n_kv, head_dim, max_seq_len, n_nodes, n_sm);
+    const bool bf16 = dtype == GEMMA_BF16;
+    if (bf16 && pl.ws_bytes > 0 &&
+        (!workspace || workspace_bytes < pl.ws_bytes || !aligned16(workspace)))
+        return GEMMA_ERR_WORKSPACE;
+    gemma::TreeParams tp{};
+    RowsParams& p = tp.p;
+    tp.parents = parents;
+    p.q = q;
+    p.k = kc;
+    p.v = vc;
+    p.seq_lens = seq_lens;
+    p.n_real = n_real;
+    p.out = out;
+    p.o_part = static_cast<float*>(workspace);
+    p.ml_part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + pl.o_bytes);
+    p.err = device_error;
+    p.n_tok = n_nodes;
+    p.n_q = n_q;
+    p.n_kv = n_kv;
+    p.G = n_q / n_kv;
+    p.cap = kv_capacity;
+    p.window = window;
+    p.is_sliding = kind != GEMMA_GLOBAL;
+    p.ring = ring ? kv_capacity : 0;
+    p.block_table = block_table;
+    p.page_size = block_table ? page_size : 0;
+    p.max_pages = max_pages;
+    p.n_pages = n_pages;
+    p.k_eq_v = k_eq_v ? 1 : 0;
+    p.max_seq_len = max_seq_len;
+    p.n_split = pl.n_split;
+    p.chunk = pl.chunk;
+    p.scale = scale;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    p.softcap = softcap;
+    p.cap_inner = softcap > 0.f ? scale / softcap : 0.f;
+    p.cap_log2 = softcap * 1.4426950408889634f;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (!bf16) {
+        e = gemma::launch_tree_f32(tp, head_dim, batch, s);
+    } else {
+        e = gemma::launch_tree_rows(tp, head_dim, batch, s);
+        if (e == cudaSuccess && pl.n_split > 1) e = gemma::launch_tree_combine(tp, head_dim, batch, s);
+    }
+    return e == cudaSuccess ? GEMMA_OK : GEMMA_ERR_CUDA;
+}
+
+int gemma_tree_accept(const int32_t* tokens, const int32_t* parents, const int32_t* next,
+                      const int32_t* n_real, const int32_t* seq_lens, int batch, int n_nodes,
+                      int32_t* path_out, int32_t* n_keep_out, int32_t* token_out,
+                      int32_t* lens_out, uint32_t* device_error, void* stream) {
+    if (batch < 0 || n_nodes < 1) return GEMMA_ERR_INVALID_ARG;
+    if (n_nodes > gemma::kTreeMaxNodes || batch > (1 << 24)) return GEMMA_ERR_UNSUPPORTED;
+    if (batch == 0) return GEMMA_OK;
+    if (!tokens || !parents || !next || !path_out || !n_keep_out || !token_out ||
+        (lens_out && !seq_lens))
+        return GEMMA_ERR_INVALID_ARG;
+    for (const void* x :
+         {static_cast<const void*>(tokens), static_cast<const void*>(parents),
+          static_cast<const void*>(next), static_cast<const void*>(n_real),
+          static_cast<const void*>(seq_lens), static_cast<const void*>(path_out),
+          static_cast<const void*>(n_keep_out), static_cast<const void*>(token_out),
+          static_cast<const void*>(lens_out), static_cast<const void*>(device_error)})
+        if (!aligned4(x)) return GEMMA_ERR_INVALID_ARG;
+    return gemma::launch_tree_accept(tokens, parents, next, n_real, seq_lens, batch, n_nodes,
+                                     path_out, n_keep_out, token_out, lens_out, device_error,
+                                     static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GEMMA_OK
+               : GEMMA_ERR_CUDA;
+}
+
+int gemma_kv_keep(void* const* caches, int n_caches, const int32_t* write_pos, const int32_t* path,
+                  const int32_t* n_keep, const int32_t* block_table, int max_pages, int page_size,
+                  int n_pages, int batch, int n_nodes, gemma_layer_kind kind, int n_kv,
+                  int kv_capacity, int row_bytes, uint32_t* device_error, void* stream) {
+    if (batch < 0 || n_nodes < 1 || n_caches < 0 || n_kv < 1 || row_bytes < 2 || row_bytes % 2 != 0)
+        return GEMMA_ERR_INVALID_ARG;
+    if (kind != GEMMA_SLIDING && kind != GEMMA_GLOBAL && kind != GEMMA_SLIDING_RING)
+        return GEMMA_ERR_INVALID_ARG;
+    const bool ring = kind == GEMMA_SLIDING_RING;
+    if (block_table) {
+        if (ring) return GEMMA_ERR_INVALID_ARG;
+        const int st = check_paged(max_pages, page_size, n_pages);
+        if (st != GEMMA_OK) return st;
+        kv_capacity = max_pages * page_size;
+    }
+    if (kv_capacity < 1) return GEMMA_ERR_INVALID_ARG;
+    if (kv_capacity > (1 << 30) || n_nodes > gemma::kTreeMaxNodes || batch > 65535 ||
+        (long long)n_kv * row_bytes > (1ll << 30))
+        return GEMMA_ERR_UNSUPPORTED;
+    if (ring && kv_capacity < n_nodes) return GEMMA_ERR_CAPACITY;
+    if (batch == 0 || n_caches == 0) return GEMMA_OK;
+    if (!caches || !write_pos || !path || !n_keep) return GEMMA_ERR_INVALID_ARG;
+    for (int i = 0; i < n_caches; ++i)
+        if (!caches[i] || !aligned16(caches[i])) return GEMMA_ERR_INVALID_ARG;
+    for (const void* x : {static_cast<const void*>(write_pos), static_cast<const void*>(path),
+                          static_cast<const void*>(n_keep), static_cast<const void*>(block_table),
+                          static_cast<const void*>(device_error)})
+        if (!aligned4(x)) return GEMMA_ERR_INVALID_ARG;
+    gemma::KeepLayout k{};
+    k.write_pos = write_pos;
+    k.path = path;
+    k.n_keep = n_keep;
+    k.pg = gemma::PagedLayout{block_table, max_pages, page_size, n_pages};
+    k.n = n_nodes;
+    k.n_kv = n_kv;
+    k.cap = kv_capacity;
+    k.ring = ring ? kv_capacity : 0;
+    k.row_bytes = row_bytes;
+    return gemma::launch_kv_keep(caches, n_caches, k, batch, device_error,
+                                 static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GEMMA_OK
+               : GEMMA_ERR_CUDA;
+}
+
+// ---------------------------------------------------------------------------------------------
+// pages of a pool
+// ---------------------------------------------------------------------------------------------
+namespace {
+
+int page_table(int32_t* block_table, int max_pages, int page_size, int n_pages, int32_t* page_refs,
+               int batch, const uint32_t* device_error, gemma::PageTable* t) {
+    if (batch < 0) return GEMMA_ERR_INVALID_ARG;
+    const int st = check_paged(max_pages, page_size, n_pages);
+    if (st != GEMMA_OK) return st;
+    if (n_pages > gemma::kMaxPages || batch > 65535 ||
+        (long long)batch * max_pages > (1ll << 31) - 1)
+        return GEMMA_ERR_UNSUPPORTED;
+    if (batch == 0) return GEMMA_OK;
+    if (!block_table || !page_refs || !aligned4(block_table) || !aligned4(page_refs) ||
+        !aligned4(device_error))
+        return GEMMA_ERR_INVALID_ARG;
+    *t = gemma::PageTable{block_table, page_refs, max_pages, page_size, n_pages, batch};
+    return GEMMA_OK;
+}
+
+int page_pools(void* const* pools, const int32_t* pool_n_kv, const int32_t* pool_row_bytes,
+               int n_pools, int page_size, int n_pages, const void* workspace,
+               size_t workspace_bytes) {
+    if (n_pools < 1 || !pools || !pool_n_kv || !pool_row_bytes) return GEMMA_ERR_INVALID_ARG;
+    for (int i = 0; i < n_pools; ++i) {
+        if (!pools[i] || !aligned16(pools[i]) || pool_n_kv[i] < 1 || pool_row_bytes[i] < 2 ||
+            pool_row_bytes[i] % 2 != 0)
+            return GEMMA_ERR_INVALID_ARG;
+        // a page of up to 1 GB: the copies' units are counted in 32 bits
+        if ((long long)pool_n_kv[i] * pool_row_bytes[i] > (1ll << 30) / page_size)
+            return GEMMA_ERR_UNSUPPORTED;
+    }
+    if (!workspace || workspace_bytes < gemma::pages_workspace(n_pages) || !aligned16(workspace))
+        return GEMMA_ERR_WORKSPACE;
+    return GEMMA_OK;
+}
+
+}  // namespace
+
+size_t gemma_pages_workspace_size(int n_pages) {
+    if (n_pages < 1 || n_pages > gemma::kMaxPages) return (size_t)-1;
+    return gemma::pages_workspace(n_pages);
+}
+
+int gemma_pages_free(int32_t* block_table, int max_pages, int page_size, int n_pages,
+                     int32_t* page_refs, const int32_t* keep_from, const int32_t* keep_to,
+                     int batch, uint32_t* device_error, void* stream) {
+    gemma::PageTable t;
+    const int st = page_table(block_table, max_pages, page_size, n_pages, page_refs, batch,
+                              device_error, &t);
+    if (st != GEMMA_OK || batch == 0) return st;
+    if ((!keep_from && !keep_to) || !aligned4(keep_from) || !aligned4(keep_to))
+        return GEMMA_ERR_INVALID_ARG;
+    const int n_sm = sm_count();
+    if (n_sm < 0) return GEMMA_ERR_CUDA;
+    return gemma::launch_pages_free(t, keep_from, keep_to, device_error, n_sm,
+                                    static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GEMMA_OK
+               : GEMMA_ERR_CUDA;
+}
+
+int gemma_pages_fork(int32_t* block_table, int max_pages, int page_size, int n_pages,
+                     int32_t* page_refs, int32_t* seq_lens, const int32_t* src, const int32_t* dst,
+                     int n, int batch, uint32_t* device_error, void* stream) {
+    if (n < 0) return GEMMA_ERR_INVALID_ARG;
+    gemma::PageTable t;
+    const int st = page_table(block_table, max_pages, page_size, n_pages, page_refs, batch,
+                              device_error, &t);
+    if (st != GEMMA_OK || batch == 0 || n == 0) return st;
+    if (n > batch) return GEMMA_ERR_INVALID_ARG;  // each fork needs a sequence of its own
+    if (!seq_lens || !src || !dst || !aligned4(seq_lens) || !aligned4(src) || !aligned4(dst))
+        return GEMMA_ERR_INVALID_ARG;
+    return gemma::launch_pages_fork(t, seq_lens, src, dst, n, device_error,
+                                    static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GEMMA_OK
+               : GEMMA_ERR_CUDA;
+}
+
+int gemma_pages_reserve(void* const* pools, const int32_t* pool_n_kv,
+                        const int32_t* pool_row_bytes, int n_pools, int32_t* block_table,
+                        int max_pages, int page_size, int n_pages, int32_t* page_refs,
+                        const int32_t* seq_lens, const int32_t* n_add, int batch, void* workspace,
+                        size_t workspace_bytes, uint32_t* device_error, void* stream) {
+    gemma::PageTable t;
+    int st = page_table(block_table, max_pages, page_size, n_pages, page_refs, batch, device_error,
+                        &t);
+    if (st != GEMMA_OK || batch == 0) return st;
+    if (!seq_lens || !n_add || !aligned4(seq_lens) || !aligned4(n_add))
+        return GEMMA_ERR_INVALID_ARG;
+    st = page_pools(pools, pool_n_kv, pool_row_bytes, n_pools, page_size, n_pages, workspace,
+                    workspace_bytes);
+    if (st != GEMMA_OK) return st;
+    const int n_sm = sm_count();
+    if (n_sm < 0) return GEMMA_ERR_CUDA;
+    return gemma::launch_pages_reserve(
+               gemma::PagePools{pools, pool_n_kv, pool_row_bytes, n_pools}, t, seq_lens, n_add,
+               workspace, device_error, n_sm, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GEMMA_OK
+               : GEMMA_ERR_CUDA;
+}
+
+int gemma_pages_compact(void* const* pools, const int32_t* pool_n_kv,
+                        const int32_t* pool_row_bytes, int n_pools, int32_t* block_table,
+                        int max_pages, int page_size, int n_pages, int32_t* page_refs,
+                        int32_t* n_used_out, int batch, void* workspace, size_t workspace_bytes,
+                        uint32_t* device_error, void* stream) {
+    gemma::PageTable t;
+    int st = page_table(block_table, max_pages, page_size, n_pages, page_refs, batch, device_error,
+                        &t);
+    if (st != GEMMA_OK || batch == 0) return st;
+    if (!aligned4(n_used_out)) return GEMMA_ERR_INVALID_ARG;
+    st = page_pools(pools, pool_n_kv, pool_row_bytes, n_pools, page_size, n_pages, workspace,
+                    workspace_bytes);
+    if (st != GEMMA_OK) return st;
+    const int n_sm = sm_count();
+    if (n_sm < 0) return GEMMA_ERR_CUDA;
+    return gemma::launch_pages_compact(
+               gemma::PagePools{pools, pool_n_kv, pool_row_bytes, n_pools}, t, n_used_out,
+               workspace, device_error, n_sm, static_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? GEMMA_OK
+               : GEMMA_ERR_CUDA;
 }
 
 }  // extern "C"

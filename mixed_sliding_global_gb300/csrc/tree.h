@@ -1,0 +1,71 @@
+// tree.h -- launch interfaces of the drafted-tree step and of the page bookkeeping (api.cu).
+#pragma once
+
+#include "attn_internal.h"
+
+namespace gemma {
+
+constexpr int kTreeMaxNodes = 128;  // nodes of a tree: an ancestor set is four words
+constexpr int kTreeKeyTile = 64;    // keys per tile; chunks of keys are multiples of it
+
+// One attention launch over trees. p: n_tok = nodes of the bucket, n_real the sequences' own
+// (nullptr: all); o_part [batch][n_kv][rows][n_split][D] and ml_part [..][n_split][2] hold the
+// partial results of n_split > 1 chunks of p.chunk keys (rows = nodes x G).
+struct TreeParams {
+    RowsParams p;
+    const int32_t* parents;  // [batch][n_tok], -1 or an earlier node
+};
+
+// Row groups (16 rows each) of a CTA's tile for this many rows per KV head.
+constexpr int tree_row_groups(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+
+// CTAs of the bf16 launch that fit an SM.
+int tree_ctas_per_sm(int head_dim, int rows);
+
+cudaError_t launch_tree_rows(const TreeParams& tp, int head_dim, int batch, cudaStream_t st);
+cudaError_t launch_tree_f32(const TreeParams& tp, int head_dim, int batch, cudaStream_t st);
+cudaError_t launch_tree_combine(const TreeParams& tp, int head_dim, int batch, cudaStream_t st);
+
+cudaError_t launch_tree_accept(const int32_t* tokens, const int32_t* parents, const int32_t* next,
+                               const int32_t* n_real, const int32_t* seq_lens, int batch, int n,
+                               int32_t* path, int32_t* n_keep, int32_t* token, int32_t* lens_out,
+                               uint32_t* err, cudaStream_t st);
+
+// Rows of row_bytes bytes in caches [batch][n_kv][cap] or pools [n_pages][n_kv][page_size].
+struct KeepLayout {
+    const int32_t* write_pos;
+    const int32_t* path;
+    const int32_t* n_keep;
+    PagedLayout pg;
+    int n, n_kv, cap, ring;
+    int row_bytes;
+};
+cudaError_t launch_kv_keep(void* const* caches, int n_caches, const KeepLayout& k, int batch,
+                           uint32_t* err, cudaStream_t st);
+
+// Pools that share a block table and page numbers.
+struct PagePools {
+    void* const* pools;
+    const int32_t* n_kv;
+    const int32_t* row_bytes;
+    int n_pools;
+};
+// A block table and the reference counts of its pages.
+struct PageTable {
+    int32_t* table;  // [batch][max_pages]
+    int32_t* refs;   // [n_pages]
+    int max_pages, page_size, n_pages, batch;
+};
+constexpr int kMaxPages = 1 << 29;  // of a pool whose pages are moved or given out
+constexpr size_t pages_workspace(int n_pages) { return 256 + 28 * ((size_t)n_pages + 4); }
+cudaError_t launch_pages_free(const PageTable& t, const int32_t* keep_from, const int32_t* keep_to,
+                              uint32_t* err, int n_sm, cudaStream_t st);
+cudaError_t launch_pages_fork(const PageTable& t, int32_t* seq_lens, const int32_t* src,
+                              const int32_t* dst, int n, uint32_t* err, cudaStream_t st);
+cudaError_t launch_pages_reserve(const PagePools& pools, const PageTable& t,
+                                 const int32_t* seq_lens, const int32_t* n_add, void* workspace,
+                                 uint32_t* err, int n_sm, cudaStream_t st);
+cudaError_t launch_pages_compact(const PagePools& pools, const PageTable& t, int32_t* n_used,
+                                 void* workspace, uint32_t* err, int n_sm, cudaStream_t st);
+
+}  // namespace gemma

@@ -1,0 +1,748 @@
+// tree_attn.cu -- attention of a tree of drafted tokens over a device-resident KV cache.
+//
+// A sequence's tree has n nodes whose K/V rows were appended at base .. base + n - 1 (base = len -
+// n). Node i stands at text position base + depth(i) and attends
+//   the prefix keys j < base (on a sliding layer those with base + depth(i) - j < window), and
+//   its ancestors and itself (on a sliding layer those with depth(i) - depth(m) < window);
+// out = softmax(scale * q k^T) v over them. Definition and layers as in rows_attn.cu ("Porting
+// Gemma-4 (2B / 4B / 12B) to AWS Inferentia2", sections 2.1-2.3 and 4.3).
+//
+// All nodes share the prefix, so a KV head's rows (nodes x G query heads) go through its keys
+// together: with R rows a key costs 4 R d operations for 4 d bytes, and tiles of up to 64 rows read
+// the cache once for all of them. bf16 kernel, per CTA: one KV head of one sequence, a tile of 16,
+// 32 or 64 rows, one chunk of keys:
+//  - a producer warp streams K and V tiles of 64 keys through a ring of slots (tiled TMA, 128-byte
+//    swizzle);
+//  - eight consumer warps stand in groups of 16 rows; the CW warps of a group share out the keys of
+//    S = Q K^T (mma.sync m16n8k16, Q fragments from shared memory) and, after one exchange of row
+//    maxima and one of P (bf16) through shared memory, the columns of O += P V;
+//  - the reference of a row's exponentials moves only when the maximum grows by more than 2^8;
+//  - ancestor sets are four words per token, walked up from the parents while the first tiles
+//    load; only tiles that reach the tree or a window's edge look at masks.
+// Sums, maxima and O are fp32; P is rounded to bf16 for the matrix instruction and summed as
+// rounded. Chunks leave partial (m, l, O) for tree_combine_kernel, an unsplit launch writes `out`.
+#include <atomic>
+#include <climits>
+
+#include "common.cuh"
+#include "tc.cuh"
+#include "tmap.h"
+#include "tree.h"
+
+namespace gemma {
+
+namespace {
+
+constexpr int kTrWarps = 8;                       // consumers
+constexpr int kTrThreads = (kTrWarps + 1) * 32;
+constexpr int T = kTreeKeyTile;
+constexpr int kTrMaxSlots = 8;
+constexpr int kTrWords = kTreeMaxNodes / 32;
+constexpr float kTrLazyLog2 = 8.f;
+
+// Shared memory: ring of key or value tiles, Q rows, P rows, row maxima, the tree.
+template <int D, int MW>
+struct TrLay {
+    static constexpr int M = 16 * MW;             // rows of the tile
+    static constexpr int CW = kTrWarps / MW;      // warps of a row group
+    static constexpr int SLOT = T * D * 2;
+    static constexpr int BOX = T * 128;           // one TMA box: 64 keys x 64 columns
+    static constexpr int Q_ROW = 2 * D + 16;      // padded bytes per Q row
+    static constexpr int P_ROW = 2 * T + 16;
+    static constexpr int FIXED = M * Q_ROW + M * P_ROW + CW * M * 4 + 64 * kTrWords * 4 + 64 * 4 +
+                                 kTreeMaxNodes * 4 + 2 * kTrMaxSlots * 8 + 1024;
+    // two CTAs per SM where their rings then hold four tiles each, else one
+    static constexpr bool TWO = FIXED + 4 * SLOT <= 113 * 1024;
+    static constexpr int BUDGET = TWO ? 113 * 1024 : 227 * 1024;
+    static constexpr int FIT = (BUDGET - FIXED) / SLOT;
+    static constexpr int SLOTS = FIT > kTrMaxSlots ? kTrMaxSlots : FIT;
+    static constexpr int Q_OFF = SLOTS * SLOT;
+    static constexpr int P_OFF = Q_OFF + M * Q_ROW;
+    static constexpr int MAX_OFF = P_OFF + M * P_ROW;
+    static constexpr int ANC_OFF = MAX_OFF + CW * M * 4;
+    static constexpr int DEPTH_OFF = ANC_OFF + 64 * kTrWords * 4;
+    static constexpr int PAR_OFF = DEPTH_OFF + 64 * 4;
+    static constexpr int BAR_OFF = PAR_OFF + kTreeMaxNodes * 4;
+    static constexpr int SMEM = BAR_OFF + 2 * kTrMaxSlots * 8 + 1024;  // + alignment slack
+    static_assert(SLOTS >= 2 && SMEM <= 232448 && BAR_OFF % 8 == 0, "shared memory budget");
+};
+
+// Byte offset of element (key, d) in a tile written by TMA with 128-byte swizzle.
+GEMMA_DEVINL uint32_t tr_off(int key, int d) {
+    return (uint32_t)((d >> 6) * (T * 128) + key * 128 + ((((d >> 3) & 7) ^ (key & 7)) << 4) +
+                      (d & 7) * 2);
+}
+
+// Barrier of n threads that tells each whether v is true for any.
+GEMMA_DEVINL bool named_bar_or(int id, int n, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)v), "r"(id), "r"(n)
+        : "memory");
+    return r != 0;
+}
+
+// A sequence's lengths. bad: an error bit, the sequence has no rows.
+struct TrSeq {
+    int len, n, base;
+    uint32_t bad;
+};
+GEMMA_DEVINL TrSeq tr_seq(const RowsParams& p, int b) {
+    TrSeq s;
+    s.len = __ldg(p.seq_lens + b);
+    s.n = p.n_real ? __ldg(p.n_real + b) : p.n_tok;
+    s.bad = 0;
+    if (s.n < 0 || s.n > p.n_tok) s.bad = GEMMA_DEVERR_N_REAL;
+    else if (s.len < s.n || (!p.ring && s.len > p.cap) || s.len > p.max_seq_len)
+        s.bad = GEMMA_DEVERR_SEQ_LEN;
+    s.base = s.len - s.n;
+    return s;
+}
+// First key that any node may attend, and where the chunks start (rings and pages: whole tiles).
+GEMMA_DEVINL int tr_first(const RowsParams& p, const TrSeq& s) {
+    return p.is_sliding ? max(0, s.base - p.window + 1) : 0;
+}
+GEMMA_DEVINL int tr_start(const RowsParams& p, const TrSeq& s) {
+    const int first = tr_first(p, s);
+    return p.ring || p.page_size ? first & ~(T - 1) : first;
+}
+// Chunks of a sequence that hold keys.
+GEMMA_DEVINL int tr_chunks(const RowsParams& p, const TrSeq& s) {
+    return min(p.n_split, (s.len - tr_start(p, s) + p.chunk - 1) / p.chunk);
+}
+
+// Walks from node i to the root: the set of the nodes it attends, and its depth. par: validated.
+GEMMA_DEVINL int tr_walk(const int* par, int i, int window, uint32_t (&set)[kTrWords]) {
+#pragma unroll
+    for (int w = 0; w < kTrWords; ++w) set[w] = 0;
+    int depth = 0;
+    for (int m = i; m >= 0; m = par[m], ++depth)
+        if (depth < window) {
+#pragma unroll
+            for (int w = 0; w < kTrWords; ++w)
+                if (w == m >> 5) set[w] |= 1u << (m & 31);
+        }
+    return depth - 1;
+}
+
+// scale * dot, soft-capped where a cap is set, in log2 units. tanh through one exponential and one
+// reciprocal: its absolute error (2^-22) times the cap is what the score is off by.
+GEMMA_DEVINL float tr_score(const RowsParams& p, float dot) {
+    if (p.softcap > 0.f) {
+        const float e = fast_exp2(dot * p.cap_inner * 2.885390081777927f);  // exp(2 x)
+        float r;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+        return fmaf(-2.f * p.cap_log2, r, p.cap_log2);
+    }
+    return dot * p.scale_log2;
+}
+
+}  // namespace
+
+template <int D, int MW>
+__global__ void __launch_bounds__(kTrThreads, TrLay<D, MW>::TWO ? 2 : 1)
+    tree_rows_kernel(const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap, const TreeParams tp) {
+    pdl_launch_dependents();
+    using Lay = TrLay<D, MW>;
+    constexpr int M = Lay::M, CW = Lay::CW, S = Lay::SLOTS;
+    constexpr int NT = T / CW / 8;   // 8-key n-tiles of a warp's share of S
+    constexpr int OC = D / CW;       // a warp's columns of O
+    constexpr int ON = OC / 8;
+    const RowsParams& p = tp.p;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* ring = smem;
+    uint8_t* sQ = smem + Lay::Q_OFF;
+    uint8_t* sP = smem + Lay::P_OFF;
+    float* sMax = reinterpret_cast<float*>(smem + Lay::MAX_OFF);               // [CW][M]
+    uint32_t* sAnc = reinterpret_cast<uint32_t*>(smem + Lay::ANC_OFF);         // [64][kTrWords]
+    int* sDepth = reinterpret_cast<int*>(smem + Lay::DEPTH_OFF);               // [64]
+    int* sPar = reinterpret_cast<int*>(smem + Lay::PAR_OFF);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + Lay::BAR_OFF);
+    uint64_t* empty = full + kTrMaxSlots;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = blockIdx.x % p.n_split, rt = blockIdx.x / p.n_split;
+    const int kvh = blockIdx.y, b = blockIdx.z;
+    const int rows_total = p.n_tok * p.G;
+    const int row0 = rt * M, n_rows = min(M, rows_total - row0);
+    const bool direct = p.n_split == 1;
+
+    pdl_wait();  // the previous kernel on the stream has completed
+    const TrSeq sq = tr_seq(p, b);
+    const int live = sq.bad ? 0 : max(0, min(n_rows, sq.n * p.G - row0));  // rows of real nodes
+    if (live == 0) {
+        if (sq.bad && split == 0 && rt == 0 && kvh == 0 && threadIdx.x == 0) report(p.err, sq.bad);
+        for (int i = threadIdx.x; direct && i < n_rows * (D / 8); i += kTrThreads) {
+            const int r = i / (D / 8), R = row0 + r, tk = R / p.G;
+            __nv_bfloat16* dst =
+                reinterpret_cast<__nv_bfloat16*>(p.out) +
+                (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) * (size_t)D;
+            reinterpret_cast<uint4*>(dst)[i - r * (D / 8)] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        return;
+    }
+    const int first = tr_first(p, sq);
+    const int kb = tr_start(p, sq) + split * p.chunk;
+    if (kb >= sq.len) return;
+    const int ke = min(sq.len, kb + p.chunk);
+    const int n_tiles = (ke - kb + T - 1) / T;
+    const int nops = p.k_eq_v ? 1 : 2;
+
+    if (warp == kTrWarps) {
+        // ------------------------- producer: tiles in the order of their use -------------------
+        if (lane == 0) {
+            for (int s = 0; s < S; ++s) {
+                mbar_init(&full[s], 1);
+                mbar_init(&empty[s], kTrWarps);
+            }
+            fence_barrier_init();
+        }
+        __syncwarp();
+        named_bar_arrive(1, kTrThreads);
+        if (lane == 0) {
+            const int n_loads = n_tiles * nops;
+            int row3 = 0, slot0 = 0;
+            bool ok = true;
+            for (int L = 0; L < n_loads && ok; ++L) {
+                const int s = L % S, use = L / S;
+                if (use > 0 && !(ok = mbar_wait(&empty[s], (use - 1) & 1, p.err))) break;
+                const bool is_v = nops == 2 && (L & 1);
+                if (!is_v) {
+                    const int t = nops == 2 ? L >> 1 : L;
+                    if (!kv_place(p, b, kvh, kb + t * T, row3, slot0)) {
+                        report(p.err, GEMMA_DEVERR_PAGE);  // reads zeros
+                        row3 = p.n_pages * p.n_kv;
+                    }
+                }
+                mbar_arrive_expect_tx(&full[s], Lay::SLOT);
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_3d(ring + s * Lay::SLOT + c * Lay::BOX, is_v ? &vmap : &kmap, c * 64,
+                                slot0, row3, &full[s]);
+            }
+        }
+        return;
+    }
+
+    // -------------------------------------- consumers ------------------------------------------
+    // Q rows (zeros behind the tile's), and the tree
+    {
+        const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(p.q);
+        constexpr int CH = D / 8;
+        for (int i = threadIdx.x; i < M * CH; i += kTrWarps * 32) {
+            const int r = i / CH, ch = i - r * CH;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (r < live) {
+                const int R = row0 + r, tk = R / p.G;
+                v = __ldg(reinterpret_cast<const uint4*>(
+                              q + (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) *
+                                      (size_t)D) + ch);
+            }
+            *reinterpret_cast<uint4*>(sQ + r * Lay::Q_ROW + ch * 16) = v;
+        }
+    }
+    bool bad = false;
+    if ((int)threadIdx.x < sq.n) {
+        const int m = __ldg(tp.parents + (size_t)b * p.n_tok + threadIdx.x);
+        bad = m < -1 || m >= (int)threadIdx.x;
+        sPar[threadIdx.x] = bad ? -1 : m;
+    }
+    bad = named_bar_or(2, kTrWarps * 32, bad);  // a bad tree: every row masked, zeros
+    if (bad && split == 0 && rt == 0 && kvh == 0 && threadIdx.x == 0)
+        report(p.err, GEMMA_DEVERR_TREE);
+    const int tk0 = row0 / p.G;  // the tile's first token
+    if ((int)threadIdx.x < (row0 + live - 1) / p.G - tk0 + 1) {
+        const int i = threadIdx.x;  // at most 64 tokens
+        uint32_t set[kTrWords];
+        sDepth[i] = tr_walk(sPar, tk0 + i, p.is_sliding ? p.window : INT_MAX, set);
+#pragma unroll
+        for (int w = 0; w < kTrWords; ++w) sAnc[i * kTrWords + w] = set[w];
+    }
+    named_bar_sync(1, kTrThreads);  // with the producer: its barriers exist
+
+    const int mw = warp / CW, cw = warp - mw * CW;  // row group, share of keys and columns
+    const int g = lane >> 2, tq = lane & 3;
+    // this thread's rows 16 mw + g and + 8: the first prefix key they attend, and their token
+    int lo[2], tok[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = 16 * mw + g + 8 * i;
+        tok[i] = r < live && !bad ? (row0 + r) / p.G - tk0 : -1;
+        lo[i] = tok[i] < 0        ? INT_MAX
+                : p.is_sliding ? max(0, sq.base + sDepth[tok[i]] - p.window + 1)
+                                  : 0;
+    }
+    const int lo_max = max(lo[0], lo[1]);
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    float o[ON][4];
+#pragma unroll
+    for (int j = 0; j < ON; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+
+    // A wait that gives up makes this warp stop waiting but keep walking the tiles, so that every
+    // consumer warp still reaches every barrier.
+    bool ok = true;
+    int L = 0;
+    for (int t = 0; t < n_tiles; ++t) {
+        const int kt0 = kb + t * T;
+        const int sk = L % S;
+        if (ok) ok = mbar_wait(&full[sk], (L / S) & 1, p.err);
+        ++L;
+        const uint8_t* tK = ring + sk * Lay::SLOT;
+
+        // (1) S: 16 rows x this warp's keys
+        float s[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+        const uint32_t qa0 =
+            smem_u32(sQ + (16 * mw + (lane & 15)) * Lay::Q_ROW + (lane >> 4) * 16);
+        if constexpr (NT == 1) {
+#pragma unroll
+            for (int ks = 0; ks < D / 32; ++ks) {
+                uint32_t a[8], b0, b1, b2, b3;
+                ldsm_x4(qa0 + ks * 64, a[0], a[1], a[2], a[3]);
+                ldsm_x4(qa0 + ks * 64 + 32, a[4], a[5], a[6], a[7]);
+                ldsm_x4(smem_u32(tK + tr_off(cw * 8 + (lane & 7), ks * 32 + (lane >> 3) * 8)), b0,
+                        b1, b2, b3);
+                mma_bf16(s[0], a[0], a[1], a[2], a[3], b0, b1);
+                mma_bf16(s[0], a[4], a[5], a[6], a[7], b2, b3);
+            }
+        } else {
+#pragma unroll
+            for (int ks = 0; ks < D / 16; ++ks) {
+                uint32_t a0, a1, a2, a3;
+                ldsm_x4(qa0 + ks * 32, a0, a1, a2, a3);
+#pragma unroll
+                for (int j = 0; j < NT; j += 2) {
+                    uint32_t b0, b1, b2, b3;
+                    const int key = cw * (8 * NT) + j * 8 + (lane & 7) + ((lane >> 4) << 3);
+                    ldsm_x4(smem_u32(tK + tr_off(key, ks * 16 + ((lane >> 3) & 1) * 8)), b0, b1, b2,
+                            b3);
+                    mma_bf16(s[j], a0, a1, a2, a3, b0, b1);
+                    mma_bf16(s[j + 1], a0, a1, a2, a3, b2, b3);
+                }
+            }
+        }
+        if (nops == 2) {  // K has been read
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[sk]);
+        }
+
+        // (2) scores, masks, the rows' maxima over all warps of the group
+        const int kw = kt0 + cw * (8 * NT);  // this warp's first key
+        float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[j][e] = tr_score(p, s[j][e]);
+        if (!(kw >= lo_max && kw + 8 * NT <= sq.base)) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = kw + j * 8 + 2 * tq + (e & 1), i = e >> 1, m = key - sq.base;
+                    bool in = m < 0 && key >= lo[i];
+                    if (m >= 0 && key < ke && tok[i] >= 0)
+                        in = (sAnc[tok[i] * kTrWords + (m >> 5)] >> (m & 31)) & 1u;
+                    if (!in) s[j][e] = -INFINITY;
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            mx[0] = fmax3f(mx[0], s[j][0], s[j][1]);
+            mx[1] = fmax3f(mx[1], s[j][2], s[j][3]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+            if (tq == 0) sMax[cw * M + 16 * mw + g + 8 * i] = mx[i];
+        }
+        named_bar_sync(3 + mw, CW * 32);
+        float alpha[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = 16 * mw + g + 8 * i;
+#pragma unroll
+            for (int c = 0; c < CW; ++c) mx[i] = fmaxf(mx[i], sMax[c * M + r]);
+            alpha[i] = 1.f;
+            if (mx[i] > m_run[i] + kTrLazyLog2) {
+                alpha[i] = fast_exp2(m_run[i] - mx[i]);  // 0 while the reference is -inf
+                m_run[i] = mx[i];
+            }
+            const float neg = m_run[i] == -INFINITY ? 0.f : -m_run[i];
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const uint32_t pb = pack_bf16(fast_exp2(s[j][2 * i] + neg),
+                                              fast_exp2(s[j][2 * i + 1] + neg));
+                *reinterpret_cast<uint32_t*>(sP + r * Lay::P_ROW +
+                                             (cw * (8 * NT) + j * 8 + 2 * tq) * 2) = pb;
+                sum += __uint_as_float(pb << 16) + __uint_as_float(pb & 0xffff0000u);
+            }
+            l_run[i] = fmaf(l_run[i], alpha[i], sum);
+        }
+        named_bar_sync(3 + mw, CW * 32);
+
+        // (3) O = diag(alpha) O + P V over this warp's columns
+        if (alpha[0] != 1.f || alpha[1] != 1.f) {
+#pragma unroll
+            for (int j = 0; j < ON; ++j) {
+                o[j][0] *= alpha[0];
+                o[j][1] *= alpha[0];
+                o[j][2] *= alpha[1];
+                o[j][3] *= alpha[1];
+            }
+        }
+        int sv = sk;
+        if (nops == 2) {
+            sv = L % S;
+            if (ok) ok = mbar_wait(&full[sv], (L / S) & 1, p.err);
+            ++L;
+        }
+        const uint8_t* tV = ring + sv * Lay::SLOT;
+        const bool edge = kt0 < first || kt0 + T > ke;
+#pragma unroll
+        for (int kk = 0; kk < T / 16; ++kk) {
+            uint32_t a0, a1, a2, a3;
+            ldsm_x4(smem_u32(sP + (16 * mw + (lane & 15)) * Lay::P_ROW + kk * 32 + (lane >> 4) * 16),
+                    a0, a1, a2, a3);
+            uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;
+            if (edge) {  // rows outside of the tree's keys may hold anything: zeros
+                auto in = [&](int k) { return kt0 + k >= first && kt0 + k < ke; };
+                const int k0 = kk * 16 + 2 * tq;
+                mlo = (in(k0) ? 0x0000ffffu : 0u) | (in(k0 + 1) ? 0xffff0000u : 0u);
+                mhi = (in(k0 + 8) ? 0x0000ffffu : 0u) | (in(k0 + 9) ? 0xffff0000u : 0u);
+            }
+            const int vkey = kk * 16 + (lane & 15);
+#pragma unroll
+            for (int j = 0; j < ON; j += 2) {
+                if constexpr (ON == 1) {
+                    uint32_t v0, v1;
+                    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
+                                 : "=r"(v0), "=r"(v1)
+                                 : "r"(smem_u32(tV + tr_off(vkey, cw * OC))));
+                    mma_bf16(o[j], a0, a1, a2, a3, v0 & mlo, v1 & mhi);
+                } else {
+                    uint32_t v0, v1, v2, v3;
+                    ldsm_x4_t(smem_u32(tV + tr_off(vkey, cw * OC + j * 8 + (lane >> 4) * 8)), v0, v1,
+                              v2, v3);
+                    mma_bf16(o[j], a0, a1, a2, a3, v0 & mlo, v1 & mhi);
+                    mma_bf16(o[j + 1], a0, a1, a2, a3, v2 & mlo, v3 & mhi);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[sv]);
+    }
+
+    // ---- the rows' sums over the group's keys, and the results ----
+    named_bar_sync(3 + mw, CW * 32);  // the last maxima have been read
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], 1);
+        l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], 2);
+        if (tq == 0) sMax[cw * M + 16 * mw + g + 8 * i] = l_run[i];
+    }
+    named_bar_sync(3 + mw, CW * 32);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = 16 * mw + g + 8 * i;
+        if (r >= n_rows) continue;
+        float l = 0.f;
+#pragma unroll
+        for (int c = 0; c < CW; ++c) l += sMax[c * M + r];
+        const int R = row0 + r;
+        if (direct) {
+            const int tk = R / p.G;
+            __nv_bfloat16* dst =
+                reinterpret_cast<__nv_bfloat16*>(p.out) +
+                (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) * (size_t)D +
+                cw * OC + 2 * tq;
+            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // (a row of NaN stays one)
+#pragma unroll
+            for (int j = 0; j < ON; ++j)
+                *reinterpret_cast<uint32_t*>(dst + j * 8) =
+                    pack_bf16(o[j][2 * i] * inv, o[j][2 * i + 1] * inv);
+        } else {
+            const size_t pr =
+                (((size_t)b * p.n_kv + kvh) * rows_total + R) * p.n_split + split;
+            float* dst = p.o_part + pr * D + cw * OC + 2 * tq;
+#pragma unroll
+            for (int j = 0; j < ON; ++j)
+                *reinterpret_cast<float2*>(dst + j * 8) = make_float2(o[j][2 * i], o[j][2 * i + 1]);
+            if (cw == 0 && tq == 0)
+                *reinterpret_cast<float2*>(p.ml_part + pr * 2) = make_float2(m_run[i], l);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// merge of the chunks: M = max_c m_c, out = sum_c 2^(m_c - M) O_c / sum_c 2^(m_c - M) l_c
+// ---------------------------------------------------------------------------------------------
+// One warp per row and slice of 128 columns (64 at head_dim 64).
+template <int D>
+__global__ void __launch_bounds__(256) tree_combine_kernel(const TreeParams tp, long long n_warps) {
+    pdl_launch_dependents();
+    pdl_wait();  // the previous kernel on the stream has completed
+    constexpr int V = D >= 128 ? 4 : 2, SL = D / (32 * V);
+    const RowsParams& p = tp.p;
+    const int lane = threadIdx.x & 31;
+    const long long wi = blockIdx.x * 8ll + (threadIdx.x >> 5);
+    if (wi >= n_warps) return;
+    const long long row = wi / SL;
+    const int col = (int)(wi - row * SL) * (32 * V) + lane * V;
+    const int rows_total = p.n_tok * p.G;
+    const int R = (int)(row % rows_total);
+    const int kvh = (int)(row / rows_total % p.n_kv), b = (int)(row / rows_total / p.n_kv);
+    const int tk = R / p.G;
+    const TrSeq sq = tr_seq(p, b);
+    const int nc = sq.bad || tk >= sq.n ? 0 : tr_chunks(p, sq);
+    float acc[V], top = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.f;
+    const float2* ml = reinterpret_cast<const float2*>(p.ml_part) + row * p.n_split;
+    for (int c = lane; c < nc; c += 32) top = fmaxf(top, ml[c].x);
+    top = warp_max(top);
+    const float* src = p.o_part + row * p.n_split * D + col;
+#pragma unroll 4
+    for (int c = 0; c < nc; ++c) {
+        const float2 mlc = ml[c];
+        const float w = mlc.x == -INFINITY ? 0.f : fast_exp2(mlc.x - top);
+        l = fmaf(w, mlc.y, l);
+        if constexpr (V == 4) {
+            const float4 v = __ldcs(reinterpret_cast<const float4*>(src + (size_t)c * D));
+            acc[0] = fmaf(w, v.x, acc[0]);
+            acc[1] = fmaf(w, v.y, acc[1]);
+            acc[2] = fmaf(w, v.z, acc[2]);
+            acc[3] = fmaf(w, v.w, acc[3]);
+        } else {
+            const float2 v = __ldcs(reinterpret_cast<const float2*>(src + (size_t)c * D));
+            acc[0] = fmaf(w, v.x, acc[0]);
+            acc[1] = fmaf(w, v.y, acc[1]);
+        }
+    }
+    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(
+        reinterpret_cast<__nv_bfloat16*>(p.out) +
+        (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) * (size_t)D + col);
+#pragma unroll
+    for (int e = 0; e < V; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+}
+
+// ---------------------------------------------------------------------------------------------
+// fp32 (debug path): one CTA per row, its warps share out the keys four at a time, FFMA and expf
+// ---------------------------------------------------------------------------------------------
+constexpr int kTrF32Warps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kTrF32Warps * 32) tree_f32_kernel(const TreeParams tp) {
+    pdl_launch_dependents();
+    pdl_wait();  // the previous kernel on the stream has completed
+    constexpr int E = D / 32, U = 4;
+    const RowsParams& p = tp.p;
+    __shared__ int s_par[kTreeMaxNodes];
+    __shared__ uint32_t s_set[kTrWords];
+    __shared__ int s_depth;
+    __shared__ float s_m[kTrF32Warps], s_l[kTrF32Warps], s_o[kTrF32Warps][D];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int head = blockIdx.x % p.n_q, node = blockIdx.x / p.n_q, b = blockIdx.y;
+    const int kvh = head / p.G;
+    const TrSeq sq = tr_seq(p, b);
+    float* out = reinterpret_cast<float*>(p.out) +
+                 (((size_t)b * p.n_tok + node) * p.n_q + head) * (size_t)D;
+    bool bad = false;
+    if (!sq.bad && (int)threadIdx.x < sq.n) {
+        const int m = __ldg(tp.parents + (size_t)b * p.n_tok + threadIdx.x);
+        bad = m < -1 || m >= (int)threadIdx.x;
+        s_par[threadIdx.x] = bad ? -1 : m;
+    }
+    bad = __syncthreads_or(bad);
+    if (sq.bad || bad || node >= sq.n) {
+        if (blockIdx.x == 0 && threadIdx.x == 0 && (sq.bad || bad))
+            report(p.err, sq.bad ? sq.bad : GEMMA_DEVERR_TREE);
+        for (int c = threadIdx.x; c < D; c += kTrF32Warps * 32) out[c] = 0.f;
+        return;
+    }
+    if (threadIdx.x == 0) {
+        uint32_t set[kTrWords];
+        s_depth = tr_walk(s_par, node, p.is_sliding ? p.window : INT_MAX, set);
+#pragma unroll
+        for (int w = 0; w < kTrWords; ++w) s_set[w] = set[w];
+    }
+    __syncthreads();
+    const int lo = p.is_sliding ? max(0, sq.base + s_depth - p.window + 1) : 0;
+    const float* q = reinterpret_cast<const float*>(p.q) +
+                     (((size_t)b * p.n_tok + node) * p.n_q + head) * (size_t)D;
+    const float* K = reinterpret_cast<const float*>(p.k);
+    const float* V = reinterpret_cast<const float*>(p.v);
+    const size_t rs = (size_t)kv_row_slots(p);
+    float qr[E], acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        qr[e] = q[lane + 32 * e];
+        acc[e] = 0.f;
+    }
+    float m = -INFINITY, l = 0.f;
+    for (int j0 = lo + warp * U; j0 < sq.len; j0 += kTrF32Warps * U) {
+        float s[U];
+        size_t row[U];
+        bool in[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int j = j0 + u, n = j - sq.base;
+            in[u] = j < sq.len && (n < 0 || ((s_set[n >> 5] >> (n & 31)) & 1u));
+            int krow = 0, kslot = 0;
+            if (in[u] && !kv_place(p, b, kvh, j, krow, kslot)) {  // a bad page: zeros
+                if (lane == 0) report(p.err, GEMMA_DEVERR_PAGE);
+                krow = -1;
+            }
+            row[u] = krow < 0 ? (size_t)-1 : (size_t)krow * rs + (size_t)kslot;
+            float dot = 0.f;
+            if (in[u] && row[u] != (size_t)-1) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) dot = fmaf(qr[e], K[row[u] * D + lane + 32 * e], dot);
+            }
+            s[u] = dot;
+        }
+        float top = m;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            s[u] = warp_sum(s[u]) * p.scale;
+            if (p.softcap > 0.f) s[u] = p.softcap * tanhf(s[u] / p.softcap);
+            if (in[u]) top = fmaxf(top, s[u]);
+        }
+        if (top == -INFINITY) continue;  // nothing attended so far
+        const float alpha = expf(m - top);
+        l *= alpha;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= alpha;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (!in[u]) continue;
+            const float w = expf(s[u] - top);
+            l += w;
+            if (row[u] == (size_t)-1) continue;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(w, V[row[u] * D + lane + 32 * e], acc[e]);
+        }
+        m = top;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[warp][lane + 32 * e] = acc[e];
+    if (lane == 0) {
+        s_m[warp] = m;
+        s_l[warp] = l;
+    }
+    __syncthreads();
+    float top = -INFINITY, sum = 0.f;
+    for (int w = 0; w < kTrF32Warps; ++w) top = fmaxf(top, s_m[w]);
+    for (int w = 0; w < kTrF32Warps; ++w) sum += s_m[w] == -INFINITY ? 0.f : s_l[w] * expf(s_m[w] - top);
+    for (int c = threadIdx.x; c < D; c += kTrF32Warps * 32) {
+        float x = 0.f;
+        for (int w = 0; w < kTrF32Warps; ++w)
+            if (s_m[w] != -INFINITY) x = fmaf(s_o[w][c], expf(s_m[w] - top), x);
+        out[c] = x / sum;
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// launchers
+// ---------------------------------------------------------------------------------------------
+template <int D>
+static int ctas_per_sm(int groups) {
+    return (groups == 1 ? TrLay<D, 1>::TWO : groups == 2 ? TrLay<D, 2>::TWO : TrLay<D, 4>::TWO) ? 2
+                                                                                              : 1;
+}
+
+int tree_ctas_per_sm(int head_dim, int rows) {
+    const int groups = tree_row_groups(rows);
+    switch (head_dim) {
+        case 64: return ctas_per_sm<64>(groups);
+        case 128: return ctas_per_sm<128>(groups);
+        case 256: return ctas_per_sm<256>(groups);
+    }
+    return ctas_per_sm<512>(groups);
+}
+
+template <int D, int MW>
+static cudaError_t launch_rows_dm(const TreeParams& tp, int batch, cudaStream_t st) {
+    using Lay = TrLay<D, MW>;
+    const RowsParams& p = tp.p;
+    auto kernel = tree_rows_kernel<D, MW>;
+    static std::atomic<bool> configured[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+    if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_relaxed)) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_relaxed);
+    }
+    CUtensorMap km, vm;
+    // [rows][slots][D]: rows = sequences x KV heads (pages x KV heads for a paged pool)
+    const uint64_t slots = (uint64_t)(p.page_size ? p.page_size : p.cap);
+    const uint64_t rows = (uint64_t)(p.page_size ? p.n_pages : batch) * p.n_kv;
+    const uint64_t dims[3] = {(uint64_t)D, slots, rows};
+    const uint64_t strides[2] = {(uint64_t)D * 2, slots * D * 2};
+    const uint32_t box[3] = {64, (uint32_t)T, 1};
+    if (!encode_bf16_sw128(&km, p.k, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    if (!encode_bf16_sw128(&vm, p.v, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    const unsigned tiles = (unsigned)((p.n_tok * p.G + Lay::M - 1) / Lay::M);
+    return launch_pdl(kernel, dim3(tiles * p.n_split, p.n_kv, batch), dim3(kTrThreads), Lay::SMEM,
+                      st, km, vm, tp);
+}
+
+template <int D>
+static cudaError_t launch_rows_d(const TreeParams& tp, int batch, cudaStream_t st) {
+    switch (tree_row_groups(tp.p.n_tok * tp.p.G)) {
+        case 1: return launch_rows_dm<D, 1>(tp, batch, st);
+        case 2: return launch_rows_dm<D, 2>(tp, batch, st);
+    }
+    return launch_rows_dm<D, 4>(tp, batch, st);
+}
+
+cudaError_t launch_tree_rows(const TreeParams& tp, int head_dim, int batch, cudaStream_t st) {
+    switch (head_dim) {
+        case 64: return launch_rows_d<64>(tp, batch, st);
+        case 128: return launch_rows_d<128>(tp, batch, st);
+        case 256: return launch_rows_d<256>(tp, batch, st);
+        case 512: return launch_rows_d<512>(tp, batch, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_tree_f32(const TreeParams& tp, int head_dim, int batch, cudaStream_t st) {
+    const dim3 grid((unsigned)(tp.p.n_tok * tp.p.n_q), batch), block(kTrF32Warps * 32);
+    switch (head_dim) {
+        case 64: return launch_pdl(tree_f32_kernel<64>, grid, block, 0, st, tp);
+        case 128: return launch_pdl(tree_f32_kernel<128>, grid, block, 0, st, tp);
+        case 256: return launch_pdl(tree_f32_kernel<256>, grid, block, 0, st, tp);
+        case 512: return launch_pdl(tree_f32_kernel<512>, grid, block, 0, st, tp);
+    }
+    return cudaErrorInvalidValue;
+}
+
+template <int D>
+static cudaError_t launch_combine_d(const TreeParams& tp, int batch, cudaStream_t st) {
+    constexpr int SL = D >= 128 ? D / 128 : 1;
+    const long long warps = (long long)batch * tp.p.n_q * tp.p.n_tok * SL;
+    return launch_pdl(tree_combine_kernel<D>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st,
+                      tp, warps);
+}
+
+cudaError_t launch_tree_combine(const TreeParams& tp, int head_dim, int batch, cudaStream_t st) {
+    switch (head_dim) {
+        case 64: return launch_combine_d<64>(tp, batch, st);
+        case 128: return launch_combine_d<128>(tp, batch, st);
+        case 256: return launch_combine_d<256>(tp, batch, st);
+        case 512: return launch_combine_d<512>(tp, batch, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace gemma
