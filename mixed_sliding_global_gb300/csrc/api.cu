@@ -972,7 +972,9 @@ namespace {
 struct TreePlan {
     int n_split, chunk;
     size_t o_bytes, ws_bytes;
+    bool pair;  // on CTA pairs, in equal shares of the key tiles
 };
+constexpr int kTreePairRows = 0;
 TreePlan tree_plan(int batch, int kind, int window, int n_q, int n_kv, int head_dim,
                    int max_seq_len, int n_nodes, int n_sm) {
     const long long T = gemma::kTreeKeyTile;
@@ -981,10 +983,18 @@ TreePlan tree_plan(int batch, int kind, int window, int n_q, int n_kv, int head_
     long long reach = kind == GEMMA_GLOBAL ? max_seq_len : (long long)window - 1 + n_nodes;
     if (reach > max_seq_len) reach = max_seq_len;
     reach += T - 1;  // (rings and pages start at whole tiles)
+    // (a pair's launch counts its tiles of 128 keys and 256 rows in 32 bits)
+    const long long pair_tiles =
+        (long long)batch * n_kv * ((rows + 255) / 256) * ((reach + 127) / 128);
+    if (head_dim >= 256 && batch <= gemma::kTreePairMaxBatch && pair_tiles <= (1ll << 30) &&
+        rows > kTreePairRows) {
+        const size_t ws = gemma::tree_pair_workspace(head_dim, batch, n_sm);
+        return TreePlan{1, 1 << 30, 0, ws, true};
+    }
     long long n = (long long)n_sm * gemma::tree_ctas_per_sm(head_dim, rows) / units;
     if (n > kMaxSplit) n = kMaxSplit;
     if (n < 1) n = 1;
-    TreePlan pl{1, 1 << 30, 0, 0};
+    TreePlan pl{1, 1 << 30, 0, 0, false};
     const long long chunk = round_up((reach + n - 1) / n, T);
     n = (reach + chunk - 1) / chunk;
     if (n <= 1) return pl;
@@ -1110,6 +1120,8 @@ int gemma_attn_tree(void* out, const void* q, const void* const* k_cache,
     cudaError_t e;
     if (!bf16) {
         e = gemma::launch_tree_f32(tp, head_dim, batch, s);
+    } else if (pl.pair) {
+        e = gemma::launch_tree_pair(tp, head_dim, batch, workspace, s);
     } else {
         e = gemma::launch_tree_rows(tp, head_dim, batch, s);
         if (e == cudaSuccess && pl.n_split > 1) e = gemma::launch_tree_combine(tp, head_dim, batch, s);

@@ -22,6 +22,13 @@ constexpr int tree_row_groups(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2
 // CTAs of the bf16 launch that fit an SM.
 int tree_ctas_per_sm(int head_dim, int rows);
 
+// On CTA pairs (prefill_pair.cu), head_dim 256 and 512, any number of rows, at most
+// kTreePairMaxBatch sequences; the merge included.
+constexpr int kTreePairMaxBatch = 1024;
+size_t tree_pair_workspace(int head_dim, int batch, int n_sm);
+cudaError_t launch_tree_pair(const TreeParams& tp, int head_dim, int batch, void* workspace,
+                             cudaStream_t st);
+
 cudaError_t launch_tree_rows(const TreeParams& tp, int head_dim, int batch, cudaStream_t st);
 cudaError_t launch_tree_f32(const TreeParams& tp, int head_dim, int batch, cudaStream_t st);
 cudaError_t launch_tree_combine(const TreeParams& tp, int head_dim, int batch, cudaStream_t st);

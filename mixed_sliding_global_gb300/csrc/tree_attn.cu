@@ -463,11 +463,11 @@ __global__ void __launch_bounds__(kTrThreads, TrLay<D, MW>::TWO ? 2 : 1)
                 reinterpret_cast<__nv_bfloat16*>(p.out) +
                 (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) * (size_t)D +
                 cw * OC + 2 * tq;
-            const float inv = l > 0.f || l != l ? 1.f / l : 0.f;  // (a row of NaN stays one)
+            const float inv = 1.f / l;
 #pragma unroll
-            for (int j = 0; j < ON; ++j)
+            for (int j = 0; j < ON; ++j)  // (no keys: zeros, whatever the other rows' V holds)
                 *reinterpret_cast<uint32_t*>(dst + j * 8) =
-                    pack_bf16(o[j][2 * i] * inv, o[j][2 * i + 1] * inv);
+                    l == 0.f ? 0u : pack_bf16(o[j][2 * i] * inv, o[j][2 * i + 1] * inv);
         } else {
             const size_t pr =
                 (((size_t)b * p.n_kv + kvh) * rows_total + R) * p.n_split + split;
@@ -526,12 +526,12 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeParams tp, 
             acc[1] = fmaf(w, v.y, acc[1]);
         }
     }
-    const float inv = l > 0.f || l != l ? 1.f / l : 0.f;
+    const float inv = 1.f / l;
     uint32_t* dst = reinterpret_cast<uint32_t*>(
         reinterpret_cast<__nv_bfloat16*>(p.out) +
         (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) * (size_t)D + col);
 #pragma unroll
-    for (int e = 0; e < V; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+    for (int e = 0; e < V; e += 2) dst[e / 2] = l == 0.f ? 0u : pack_bf16(acc[e] * inv, acc[e + 1] * inv);
 }
 
 // ---------------------------------------------------------------------------------------------
