@@ -17,6 +17,12 @@ using gemma::RowsParams;
 
 namespace {
 
+#ifndef GEMMA_TREE_PAIR_ROWS
+#define GEMMA_TREE_PAIR_ROWS 128
+#endif
+#ifndef GEMMA_TREE_TC_ROWS
+#define GEMMA_TREE_TC_ROWS 0
+#endif
 constexpr int kMaxSplit = 128;
 #ifndef GEMMA_MIN_CHUNK_KEYS
 #define GEMMA_MIN_CHUNK_KEYS 256
@@ -972,9 +978,11 @@ namespace {
 struct TreePlan {
     int n_split, chunk;
     size_t o_bytes, ws_bytes;
-    bool pair;  // on CTA pairs, in equal shares of the key tiles
+    int path;  // kTreeRows, or in equal shares of the key tiles on single SMs or on CTA pairs
+    int workers;
 };
-constexpr int kTreePairRows = 0;
+enum { kTreeRows, kTreeTc, kTreePair };
+constexpr int kTreePairRows = GEMMA_TREE_PAIR_ROWS, kTreePairRows512 = 64, kTreeTcRows = GEMMA_TREE_TC_ROWS;
 TreePlan tree_plan(int batch, int kind, int window, int n_q, int n_kv, int head_dim,
                    int max_seq_len, int n_nodes, int n_sm) {
     const long long T = gemma::kTreeKeyTile;
@@ -983,18 +991,28 @@ TreePlan tree_plan(int batch, int kind, int window, int n_q, int n_kv, int head_
     long long reach = kind == GEMMA_GLOBAL ? max_seq_len : (long long)window - 1 + n_nodes;
     if (reach > max_seq_len) reach = max_seq_len;
     reach += T - 1;  // (rings and pages start at whole tiles)
-    // (a pair's launch counts its tiles of 128 keys and 256 rows in 32 bits)
-    const long long pair_tiles =
-        (long long)batch * n_kv * ((rows + 255) / 256) * ((reach + 127) / 128);
-    if (head_dim >= 256 && batch <= gemma::kTreePairMaxBatch && pair_tiles <= (1ll << 30) &&
-        rows > kTreePairRows) {
-        const size_t ws = gemma::tree_pair_workspace(head_dim, batch, n_sm);
-        return TreePlan{1, 1 << 30, 0, ws, true};
+    // equal shares: no more workers than tiles (which are counted in 32 bits)
+    auto shares = [&](int path, long long row_tile, long long keys, long long most) {
+        const long long tiles = (long long)batch * n_kv * ((rows + row_tile - 1) / row_tile) *
+                                ((reach + keys - 1) / keys);
+        TreePlan pl{1, 1 << 30, 0, 0, path, (int)(tiles < most ? tiles : most)};
+        pl.ws_bytes = path == kTreePair ? gemma::tree_pair_workspace(head_dim, batch, pl.workers)
+                                        : gemma::tree_tc_workspace(head_dim, batch, pl.workers);
+        if (tiles > (1ll << 30)) pl.workers = 0;
+        return pl;
+    };
+    if (batch <= gemma::kTreePairMaxBatch) {
+        TreePlan pl{};
+        if (head_dim >= 256 && rows > (head_dim == 512 ? kTreePairRows512 : kTreePairRows))
+            pl = shares(kTreePair, 256, 128, n_sm / (head_dim / 128));
+        else if (head_dim <= 256 && rows > kTreeTcRows)
+            pl = shares(kTreeTc, 128, 64, n_sm);
+        if (pl.workers > 0) return pl;
     }
     long long n = (long long)n_sm * gemma::tree_ctas_per_sm(head_dim, rows) / units;
     if (n > kMaxSplit) n = kMaxSplit;
     if (n < 1) n = 1;
-    TreePlan pl{1, 1 << 30, 0, 0, false};
+    TreePlan pl{1, 1 << 30, 0, 0, kTreeRows, 0};
     const long long chunk = round_up((reach + n - 1) / n, T);
     n = (reach + chunk - 1) / chunk;
     if (n <= 1) return pl;
@@ -1120,8 +1138,10 @@ int gemma_attn_tree(void* out, const void* q, const void* const* k_cache,
     cudaError_t e;
     if (!bf16) {
         e = gemma::launch_tree_f32(tp, head_dim, batch, s);
-    } else if (pl.pair) {
-        e = gemma::launch_tree_pair(tp, head_dim, batch, workspace, s);
+    } else if (pl.path == kTreeTc) {
+        e = gemma::launch_tree_tc(tp, head_dim, batch, workspace, pl.workers, s);
+    } else if (pl.path == kTreePair) {
+        e = gemma::launch_tree_pair(tp, head_dim, batch, workspace, pl.workers, s);
     } else {
         e = gemma::launch_tree_rows(tp, head_dim, batch, s);
         if (e == cudaSuccess && pl.n_split > 1) e = gemma::launch_tree_combine(tp, head_dim, batch, s);

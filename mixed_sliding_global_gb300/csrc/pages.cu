@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         for (int b0 = 0; b0 < t.batch; b0 += stride)
             each(b0, [&](int at, int) {
                 const int page = -2 - t.table[at];
-                if (page < 0) return;
+                if (page < 0 || page >= t.n_pages) return;
                 atomicSub(t.refs + page, 1);
                 atomicMin(w.first + page, at);
             });
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         for (int b0 = 0; b0 < t.batch; b0 += stride)
             each(b0, [&](int at, int) {
                 const int page = -2 - t.table[at];
-                if (page < 0) return;
+                if (page < 0 || page >= t.n_pages) return;
                 const int others = __ldcg(t.refs + page);
                 if (others < 0) report(err, GEMMA_DEVERR_PAGE);
                 if (others <= 0 && __ldcg(w.first + page) == at) t.table[at] = -2 - page - kKeeper;
@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kPlanThreads)
             if (e < -1 - kKeeper) {
                 const int page = -2 - kKeeper - e;
                 t.table[at] = page;
-                t.refs[page] = 1;
+                if (page < t.n_pages) t.refs[page] = 1;
             } else if (e < 0) {
                 ++need;
             }
@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         each(b0, [&](int at, int rows) {
             const int e = t.table[at];
             if (e >= 0) return;
-            const int old = -2 - e;
+            const int old = -2 - e < t.n_pages ? -2 - e : -1;
             if (k < n_free) {
                 const int page = w.list[k];
                 t.table[at] = page;
@@ -450,21 +450,26 @@ __global__ void __launch_bounds__(kPlanThreads)
     // thread tid looks at the pages [p0, p1)
     const int per = (t.n_pages + kPlanThreads - 1) / kPlanThreads;
     const int p0 = min((long long)t.n_pages, (long long)tid * per), p1 = min(t.n_pages, p0 + per);
+    // (the counts are read once, so that what follows agrees with itself whatever they hold)
     int mine = 0, n_used = 0;
 #pragma unroll 4
-    for (int p = p0; p < p1; ++p) mine += t.refs[p] > 0;
+    for (int p = p0; p < p1; ++p) {
+        const int used = t.refs[p] > 0;
+        w.list[p] = used;
+        mine += used;
+    }
     const int before = block_scan(mine, s_warp, &n_used);
     // used pages among the first n_used
     if (n_used >= p0 && (n_used < p1 || (tid == kPlanThreads - 1 && n_used == t.n_pages))) {
         int k = before;
-        for (int p = p0; p < n_used; ++p) k += t.refs[p] > 0;
+        for (int p = p0; p < n_used; ++p) k += w.list[p];
         s_below = k;
     }
     __syncthreads();
     const int below = s_below, moves = n_used - below;
     int k = before;
     for (int p = p0; p < p1; ++p) {
-        const bool used = t.refs[p] > 0;
+        const int used = w.list[p];
         if (p < n_used) {
             if (!used) w.first[p - k] = p;  // a hole
             w.list[p] = used ? p : -1;

@@ -74,6 +74,7 @@
 #include "tc.cuh"
 #include "tmap.h"
 #include "tree.h"
+#include "tree_dev.cuh"
 
 namespace gemma {
 
@@ -127,8 +128,8 @@ struct PrParams {
     int n_pairs;   // clusters walking the units (each of H pairs)
     // trees
     const int32_t* parents;  // [batch][n_tok]
-    float* part_o;           // [2 n_pairs slots][kPrRows][D]
-    float2* part_ml;         // [2 n_pairs slots][H][kPrRows]
+    float* part_o;           // [2 n_pairs slots][2][H][64][128 rows] x 4 columns
+    float2* part_ml;         // [2 n_pairs slots][2][H][128 rows]
     int32_t* before;         // [batch + 1] key tiles of earlier sequences, for the merge
 };
 
@@ -370,16 +371,18 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     // tiles first (in order), then the others
     int* ulist = reinterpret_cast<int*>(smem + Lay::ULIST_OFF);
     if constexpr (TREE) {
-        if (warp == 1) {  // tiles before each sequence: 32 sequences at a time
+        // tiles before each sequence: every sequence's own first, then sums, 32 at a time
+        for (int b = threadIdx.x; b < fp.batch; b += blockDim.x) {
+            PrUnit U;
+            int live_rt;
+            pr_tree_seq(p, b, U, live_rt);
+            ulist[b] = U.n_tiles * live_rt * p.n_kv;
+        }
+        __syncthreads();
+        if (warp == 1) {
             int sum = 0;
             for (int b0 = 0; b0 < fp.batch; b0 += 32) {
-                int n = 0;
-                if (b0 + lane < fp.batch) {
-                    PrUnit U;
-                    int live_rt;
-                    pr_tree_seq(p, b0 + lane, U, live_rt);
-                    n = U.n_tiles * live_rt * p.n_kv;
-                }
+                const int n = b0 + lane < fp.batch ? ulist[b0 + lane] : 0;
                 int incl = n;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -391,7 +394,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             }
             if (lane == 0) ulist[fp.batch] = sum;
             __syncwarp();
-            if (blockIdx.x == 0 && fp.before)
+            if (blockIdx.x == 0)
                 for (int i = lane; i <= fp.batch; i += 32) fp.before[i] = ulist[i];
         }
     }
@@ -709,18 +712,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         PrShare share;
         if constexpr (TREE) {
             share.init(fp, worker, ulist);
-            // zeros for row tiles without nodes
-            for (int x = worker; x < fp.n_units; x += fp.n_pairs) {
-                PrUnit U;
-                int live_rt;
-                const int per = fp.n_rt * p.n_kv, rem = x % per;
-                pr_tree_seq(p, x / per, U, live_rt);
-                U.kvh = rem / fp.n_rt;
-                U.rt = rem - U.kvh * fp.n_rt;
-                U.row0 = U.rt * kPrRows;
-                U.n_rows = min(kPrRows, p.n_tok * p.G - U.row0);
-                if (U.rt >= live_rt) zero_unit(U);
-            }
         }
         // finds the next unit with tiles (writing zeros for units without), or returns false
         auto next_tiled = [&](PrUnit& U) -> bool {
@@ -737,45 +728,52 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             }
         };
 
+        // Trees: the nodes that this thread's row of a unit attends (into anc), and the first prefix
+        // key that it does (tree_lo).
+        uint32_t* anc =
+            reinterpret_cast<uint32_t*>(smem + Lay::ANC_OFF) + (w * 128 + r) * kPrWords;
+        int tree_lo = INT_MAX;
+        auto tree_row = [&](const PrUnit& U) {
+            uint32_t set[kPrWords];
+            const int32_t* par = fp.parents + (size_t)U.b * p.n_tok;
+            bool bad = false;
+#pragma unroll
+            for (int k = 0; k < kPrWords; ++k) {
+                const int i = lane + 32 * k;
+                set[k] = 0;
+                if (i < U.n_real) {
+                    const int m = __ldg(par + i);
+                    bad |= m < -1 || m >= i;
+                }
+            }
+            bad = __any_sync(0xffffffffu, bad);  // the same in every warp: no row attends
+            if (bad && w == 0 && r == 0 && rank == 0) report(p.err, GEMMA_DEVERR_TREE);
+            tree_lo = INT_MAX;
+            if (r < real_here(U) && !bad) {
+                const int window = p.is_sliding ? p.window : INT_MAX;
+                int depth = 0;
+                for (int m = (U.row0 + 128 * (int)c + r) / p.G; m >= 0; m = __ldg(par + m), ++depth)
+                    if (depth < window) {
+#pragma unroll
+                        for (int k = 0; k < kPrWords; ++k)
+                            if (k == m >> 5) set[k] |= 1u << (m & 31);
+                    }
+                tree_lo = p.is_sliding ? max(0, U.len - U.n_real + depth - p.window) : 0;
+            }
+#pragma unroll
+            for (int k = 0; k < kPrWords; ++k) anc[k] = set[k];
+        };
+
         PrUnit cur;
         if (next_tiled(cur)) {
+            if constexpr (TREE) tree_row(cur);
             int T_base = 0, ord = 0;
             for (;;) {
                 const int lo_pos = cur.len - cur.n_real;  // position of the unit's token 0
                 int lo = 1, hi = 0;
-                uint32_t* anc = reinterpret_cast<uint32_t*>(smem + Lay::ANC_OFF) +
-                                (w * 128 + r) * kPrWords;  // (this thread's alone)
                 if constexpr (TREE) {
-                    lo = INT_MAX;
+                    lo = tree_lo;
                     hi = lo_pos;  // the prefix
-                    uint32_t set[kPrWords];
-                    const int32_t* par = fp.parents + (size_t)cur.b * p.n_tok;
-                    bool bad = false;
-#pragma unroll
-                    for (int k = 0; k < kPrWords; ++k) {
-                        const int i = lane + 32 * k;
-                        set[k] = 0;
-                        if (i < cur.n_real) {
-                            const int m = __ldg(par + i);
-                            bad |= m < -1 || m >= i;
-                        }
-                    }
-                    bad = __any_sync(0xffffffffu, bad);  // the same in every warp: no row attends
-                    if (bad && w == 0 && r == 0 && rank == 0) report(p.err, GEMMA_DEVERR_TREE);
-                    if (r < real_here(cur) && !bad) {
-                        const int window = p.is_sliding ? p.window : INT_MAX;
-                        int depth = 0;
-                        for (int m = (cur.row0 + 128 * (int)c + r) / p.G; m >= 0;
-                             m = __ldg(par + m), ++depth)
-                            if (depth < window) {
-#pragma unroll
-                                for (int k = 0; k < kPrWords; ++k)
-                                    if (k == m >> 5) set[k] |= 1u << (m & 31);
-                            }
-                        lo = p.is_sliding ? max(0, lo_pos + depth - p.window) : 0;
-                    }
-#pragma unroll
-                    for (int k = 0; k < kPrWords; ++k) anc[k] = set[k];
                 } else if (r < real_here(cur)) {
                     const int pos = lo_pos + (cur.row0 + 128 * (int)c + r) / p.G;
                     lo = p.is_sliding ? max(0, pos - p.window + 1) : 0;
@@ -884,25 +882,10 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                     const int kt0 = cur.k_begin + t * kPrKeys + 64 * w;
                     if (!(kt0 >= lo && kt0 + 64 <= hi)) {
                         if constexpr (TREE) {
-                            // bit e: key kt0 + e is a prefix key from lo on, or an ancestor
-                            const int m0 = kt0 - hi;  // the node in column 0
-                            unsigned long long see = 0;
-                            if (m0 >= 0) {
+                            uint32_t set[kPrWords];
 #pragma unroll
-                                for (int k = 0; k < kPrWords; ++k) {
-                                    const int sh = m0 - 32 * k;  // right by sh, or left
-                                    const unsigned long long x = anc[k];
-                                    if (sh > -64 && sh < 32) see |= sh >= 0 ? x >> sh : x << -sh;
-                                }
-                            } else if (m0 > -64) {
-                                see = ((unsigned long long)anc[1] << 32 | anc[0]) << -m0;
-                            }
-                            const int p0 = lo - kt0, p1 = min(64, -m0);  // prefix columns [p0, p1)
-                            if (p1 > 0 && p0 < p1) {
-                                const unsigned long long upto =
-                                    p1 == 64 ? ~0ull : (1ull << p1) - 1;
-                                see |= p0 > 0 ? upto & ~((1ull << p0) - 1) : upto;
-                            }
+                            for (int k = 0; k < kPrWords; ++k) set[k] = anc[k];
+                            const unsigned long long see = tr_window(set, kt0 - hi, lo - kt0);
                             const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
 #pragma unroll
                             for (int e = 0; e < 32; ++e) {
@@ -991,6 +974,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 
                 PrUnit nxt;
                 const bool more = next_tiled(nxt);
+                // (while the last P V runs)
+                if (TREE && more && (nxt.b != cur.b || nxt.row0 != cur.row0)) tree_row(nxt);
 
                 // ---- epilogue: O / l -> bf16 for this group's 128 columns ----
                 const int T_last = T_base + cur.n_tiles - 1;
@@ -1011,12 +996,11 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                 const bool issuer_t = r == 0;
                 const int tk0 = (cur.row0 + 128 * (int)c) / p.G;
                 if (TREE && cur.slot >= 0) {
-                    // a part: this thread's row of O as it is, 128 bytes at a time, and (m, l)
-                    const size_t row = (size_t)cur.slot * kPrRows + 128 * (int)c + r;
-                    float4* dst = reinterpret_cast<float4*>(fp.part_o + row * D + 256 * h + 128 * w);
-                    if (w == 0)
-                        fp.part_ml[((size_t)cur.slot * H + h) * kPrRows + 128 * (int)c + r] =
-                            make_float2(m, lt);
+                    // a part: O as it is, and (m, l). Four columns of all rows after another, so
+                    // that a warp's store is 512 consecutive bytes
+                    const size_t part = ((size_t)cur.slot * 2 + c) * H + h;  // of 128 rows
+                    float4* dst = reinterpret_cast<float4*>(fp.part_o) + (part * 64 + 32 * w) * 128 + r;
+                    if (w == 0) fp.part_ml[part * 128 + r] = make_float2(m, lt);
 #pragma unroll 1
                     for (int sl = 0; sl < 4; ++sl) {
                         uint32_t v[32];
@@ -1029,7 +1013,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                         }
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
-                            dst[sl * 8 + q] = make_float4(
+                            dst[(sl * 8 + q) * 128] = make_float4(
                                 __uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
                                 __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
                     }
@@ -1078,6 +1062,20 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                 ++ord;
             }
         }
+        if constexpr (TREE) {
+            // zeros for row tiles without nodes
+            for (int x = worker; x < fp.n_units; x += fp.n_pairs) {
+                PrUnit U;
+                int live_rt;
+                const int per = fp.n_rt * p.n_kv, rem = x % per;
+                pr_tree_seq(p, x / per, U, live_rt);
+                U.kvh = rem / fp.n_rt;
+                U.rt = rem - U.kvh * fp.n_rt;
+                U.row0 = U.rt * kPrRows;
+                U.n_rows = min(kPrRows, p.n_tok * p.G - U.row0);
+                if (U.rt >= live_rt) zero_unit(U);
+            }
+        }
     }
     if (warp < 8 && (threadIdx.x & 127) == 0) bulk_wait_all();  // the epilogues' TMA stores
     tc_fence_before();
@@ -1092,62 +1090,92 @@ __global__ void __launch_bounds__(kPrThreads, 1)
 // ---------------------------------------------------------------------------------------------
 // Trees: merge of the parts of every unit that more than one worker took a share of,
 //   M = max_w m_w, out = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w
-// (at head_dim 512 each half of the columns with its own (m, l)). One warp per row and 128 columns.
+// (at head_dim 512 each half of the columns with its own (m, l)). A lane per row and 16 columns: reads
+// of 512 consecutive bytes, writes of whole sectors. WAYS warps share out the parts of 32 rows and 16
+// columns (few units are cut into many parts) and meet in shared memory.
 // ---------------------------------------------------------------------------------------------
-template <int H>
-__global__ void __launch_bounds__(256) pair_merge_kernel(const PrParams fp, long long n_warps) {
+template <int H, int WAYS>
+__global__ void __launch_bounds__(256) pair_merge_kernel(const PrParams fp) {
     pdl_launch_dependents();
     pdl_wait();  // the parts
-    constexpr int D = 256 * H, SL = D / 128;
+    constexpr int D = 256 * H;
     const RowsParams& p = fp.p;
     const int lane = threadIdx.x & 31;
-    const long long wi = blockIdx.x * 8ll + (threadIdx.x >> 5);
-    if (wi >= n_warps) return;
-    const long long row = wi / SL;
-    const int sl = (int)(wi - row * SL), h = sl / 2, col = sl * 128 + lane * 4;
-    const int rows_total = p.n_tok * p.G;
-    const int R = (int)(row % rows_total), kvh = (int)(row / rows_total % p.n_kv),
-              b = (int)(row / rows_total / p.n_kv);
+    // a CTA's warps: the same rows, neighbouring slices of 16 columns, WAYS warps each
+    constexpr int SLICES = 8 / WAYS;
+    const int warp = threadIdx.x >> 5, way = warp % WAYS;
+    const int slice = (blockIdx.x % (D / (16 * SLICES))) * SLICES + warp / WAYS;
+    const int x = blockIdx.x / (D / (16 * SLICES)), group = x & 7, unit = x >> 3;
+    const int per = fp.n_rt * p.n_kv, b = unit / per, kvh = unit % per / fp.n_rt,
+              rt = unit % fp.n_rt;
     PrUnit U;
     int live_rt;
     pr_tree_seq(p, b, U, live_rt);
-    const int tk = R / p.G, rt = R / kPrRows;
     if (U.bad || rt >= live_rt) return;  // zeros already
     const int total = fp.before[fp.batch], share = (total + fp.n_pairs - 1) / fp.n_pairs;
     const int f0 = fp.before[b] + (kvh * live_rt + rt) * U.n_tiles, f1 = f0 + U.n_tiles;
     const int w0 = f0 / share, w1 = (f1 - 1) / share;
     if (w0 == w1) return;  // a whole unit: written by its worker
-    // worker w's part is the first of its share but for one that began before the unit
-    auto slot = [&](int w) { return 2 * w + (w * share < f0); };
-    const int rr = R - rt * kPrRows;
-    auto ml = [&](int w) { return fp.part_ml[((size_t)slot(w) * H + h) * kPrRows + rr]; };
+    const int rr = group * 32 + lane, R = rt * kPrRows + rr;
+    const bool there = R < p.n_tok * p.G;
+    // worker w's part is the first of its share but for one that began before the unit; the
+    // 128-row, 256-column piece with this row and slice
+    const int c = rr >> 7, h = slice >> 4, r = rr & 127;
+    auto part = [&](int w) { return ((size_t)(2 * w + (w * share < f0)) * 2 + c) * H + h; };
     float top = -INFINITY;
-    for (int w = w0 + lane; w <= w1; w += 32) top = fmaxf(top, ml(w).x);
-    top = warp_max(top);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float l = 0.f;
 #pragma unroll 4
-    for (int w = w0; w <= w1; ++w) {
-        const float2 x = ml(w);
-        const float4 o = __ldcs(reinterpret_cast<const float4*>(
-            fp.part_o + ((size_t)slot(w) * kPrRows + rr) * D + col));
-        const float e = x.x == -INFINITY ? 0.f : fast_exp2(x.x - top);
-        l = fmaf(e, x.y, l);
-        acc.x = fmaf(e, o.x, acc.x);
-        acc.y = fmaf(e, o.y, acc.y);
-        acc.z = fmaf(e, o.z, acc.z);
-        acc.w = fmaf(e, o.w, acc.w);
+    for (int w = w0; w <= w1; ++w) top = fmaxf(top, fp.part_ml[part(w) * 128 + r].x);
+    float acc[16], l = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+#pragma unroll 2
+    for (int w = w0 + way; w <= w1; w += WAYS) {
+        const size_t pt = part(w);
+        const float2 ml = fp.part_ml[pt * 128 + r];
+        const float4* src =
+            reinterpret_cast<const float4*>(fp.part_o) + (pt * 64 + 4 * (slice & 15)) * 128 + r;
+        const float e = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - top);
+        l = fmaf(e, ml.y, l);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const float4 o = __ldcs(src + q * 128);
+            if (e == 0.f) continue;  // (O without keys may be NaN where V is)
+            acc[4 * q] = fmaf(e, o.x, acc[4 * q]);
+            acc[4 * q + 1] = fmaf(e, o.y, acc[4 * q + 1]);
+            acc[4 * q + 2] = fmaf(e, o.z, acc[4 * q + 2]);
+            acc[4 * q + 3] = fmaf(e, o.w, acc[4 * q + 3]);
+        }
     }
+    if constexpr (WAYS > 1) {
+        __shared__ float s_acc[8][17][32];
+        if (way) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s_acc[warp][e][lane] = acc[e];
+            s_acc[warp][16][lane] = l;
+        }
+        __syncthreads();
+        if (way) return;
+#pragma unroll
+        for (int k = 1; k < WAYS; ++k) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[e] += s_acc[warp + k][e][lane];
+            l += s_acc[warp + k][16][lane];
+        }
+    }
+    if (!there) return;
     const float inv = 1.f / l;
-    uint2* dst = reinterpret_cast<uint2*>(
+    uint32_t out[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)  // (no keys: zeros, whatever the other rows' V holds)
+        out[e] = l == 0.f ? 0u : pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    const int tk = R / p.G;
+    uint4* dst = reinterpret_cast<uint4*>(
         reinterpret_cast<__nv_bfloat16*>(p.out) +
-        (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) * (size_t)D + col);
-    *dst = l != 0.f ? make_uint2(pack_bf16(acc.x * inv, acc.y * inv),
-                                 pack_bf16(acc.z * inv, acc.w * inv))
-                    : make_uint2(0u, 0u);
+        (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) * (size_t)D + slice * 16);
+    dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+    dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
 }
 
-// ---------------------------------------------------------------------------------------------
 // Scratch of a tree launch on n clusters: parts, their (m, l), tiles before each sequence.
 struct PrTreeScratch {
     size_t ml_off, before_off, bytes;
@@ -1163,7 +1191,8 @@ static PrTreeScratch pr_tree_scratch(int H, int n_clusters, int batch) {
 
 template <int H>
 static cudaError_t launch_pair(const RowsParams& p, int batch, cudaStream_t st,
-                               const TreeParams* tree = nullptr, void* workspace = nullptr) {
+                               const TreeParams* tree = nullptr, void* workspace = nullptr,
+                               int workers = 0) {
     using Lay = PrLay<H>;
     constexpr int D = Lay::D;
     CUtensorMap km, vm;
@@ -1245,13 +1274,13 @@ static cudaError_t launch_pair(const RowsParams& p, int batch, cudaStream_t st,
     fp.n_pairs = fp.n_units < n_clusters ? fp.n_units : n_clusters;
     if (tree) {
         fp.parents = tree->parents;
-        fp.n_pairs = n_clusters;
-        const PrTreeScratch ws = pr_tree_scratch(H, n_clusters, batch);
+        fp.n_pairs = workers < n_clusters ? workers : n_clusters;
+        const PrTreeScratch ws = pr_tree_scratch(H, fp.n_pairs, batch);
         uint8_t* base = static_cast<uint8_t*>(workspace);
         fp.part_o = reinterpret_cast<float*>(base);
         fp.part_ml = reinterpret_cast<float2*>(base + ws.ml_off);
         fp.before = reinterpret_cast<int32_t*>(base + ws.before_off);
-        cfg.gridDim = dim3(2 * H * n_clusters);
+        cfg.gridDim = dim3(2 * H * fp.n_pairs);
         cfg.dynamicSmemBytes = Lay::TREE_SMEM;
         const cudaError_t e =
             p.softcap > 0.f
@@ -1259,9 +1288,12 @@ static cudaError_t launch_pair(const RowsParams& p, int batch, cudaStream_t st,
                 : cudaLaunchKernelEx(&cfg, prefill_pair_kernel<H, false, kPrTree>, km, vm, qm, om,
                                      fp);
         if (e != cudaSuccess) return e;
-        const long long warps = (long long)batch * p.n_q * p.n_tok * (D / 128);
-        return launch_pdl(pair_merge_kernel<H>, dim3((unsigned)((warps + 7) / 8)), dim3(256), 0, st,
-                          fp, warps);
+        // (parts per unit: about the workers over the units)
+        if (fp.n_units * 4 < fp.n_pairs)
+            return launch_pdl(pair_merge_kernel<H, 8>, dim3((unsigned)(fp.n_units * 8 * (D / 16))),
+                              dim3(256), 0, st, fp);
+        return launch_pdl(pair_merge_kernel<H, 1>, dim3((unsigned)(fp.n_units * 8 * (D / 128))),
+                          dim3(256), 0, st, fp);
     }
     cfg.gridDim = dim3(2 * H * fp.n_pairs);
     if (p.softcap > 0.f)
@@ -1274,15 +1306,14 @@ static cudaError_t launch_pair(const RowsParams& p, int batch, cudaStream_t st,
     return cudaLaunchKernelEx(&cfg, prefill_pair_kernel<H, false, kPrPlain>, km, vm, qm, om, fp);
 }
 
-size_t tree_pair_workspace(int head_dim, int batch, int n_sm) {
-    const int H = head_dim / 256;
-    return pr_tree_scratch(H, n_sm / (2 * H), batch).bytes;
+size_t tree_pair_workspace(int head_dim, int batch, int workers) {
+    return pr_tree_scratch(head_dim / 256, workers, batch).bytes;
 }
 
 cudaError_t launch_tree_pair(const TreeParams& tp, int head_dim, int batch, void* workspace,
-                             cudaStream_t st) {
-    if (head_dim == 256) return launch_pair<1>(tp.p, batch, st, &tp, workspace);
-    if (head_dim == 512) return launch_pair<2>(tp.p, batch, st, &tp, workspace);
+                             int workers, cudaStream_t st) {
+    if (head_dim == 256) return launch_pair<1>(tp.p, batch, st, &tp, workspace, workers);
+    if (head_dim == 512) return launch_pair<2>(tp.p, batch, st, &tp, workspace, workers);
     return cudaErrorInvalidValue;
 }
 

@@ -19,15 +19,21 @@ struct TreeParams {
 // Row groups (16 rows each) of a CTA's tile for this many rows per KV head.
 constexpr int tree_row_groups(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
 
+// On single SMs with tcgen05 (tree_tc.cu), head_dim 64 to 256, at most kTreePairMaxBatch sequences;
+// the merge included. workers: CTAs, one per SM at most.
+size_t tree_tc_workspace(int head_dim, int batch, int workers);
+cudaError_t launch_tree_tc(const TreeParams& tp, int head_dim, int batch, void* workspace,
+                           int workers, cudaStream_t st);
+
 // CTAs of the bf16 launch that fit an SM.
 int tree_ctas_per_sm(int head_dim, int rows);
 
 // On CTA pairs (prefill_pair.cu), head_dim 256 and 512, any number of rows, at most
-// kTreePairMaxBatch sequences; the merge included.
+// kTreePairMaxBatch sequences; the merge included. workers: clusters, as many as fit at most.
 constexpr int kTreePairMaxBatch = 1024;
-size_t tree_pair_workspace(int head_dim, int batch, int n_sm);
+size_t tree_pair_workspace(int head_dim, int batch, int workers);
 cudaError_t launch_tree_pair(const TreeParams& tp, int head_dim, int batch, void* workspace,
-                             cudaStream_t st);
+                             int workers, cudaStream_t st);
 
 cudaError_t launch_tree_rows(const TreeParams& tp, int head_dim, int batch, cudaStream_t st);
 cudaError_t launch_tree_f32(const TreeParams& tp, int head_dim, int batch, cudaStream_t st);

@@ -28,6 +28,7 @@
 #include "tc.cuh"
 #include "tmap.h"
 #include "tree.h"
+#include "tree_dev.cuh"
 
 namespace gemma {
 
@@ -37,8 +38,6 @@ constexpr int kTrWarps = 8;                       // consumers
 constexpr int kTrThreads = (kTrWarps + 1) * 32;
 constexpr int T = kTreeKeyTile;
 constexpr int kTrMaxSlots = 8;
-constexpr int kTrWords = kTreeMaxNodes / 32;
-constexpr float kTrLazyLog2 = 8.f;
 
 // Shared memory: ring of key or value tiles, Q rows, P rows, row maxima, the tree.
 template <int D, int MW>
@@ -67,81 +66,364 @@ struct TrLay {
     static_assert(SLOTS >= 2 && SMEM <= 232448 && BAR_OFF % 8 == 0, "shared memory budget");
 };
 
+// The same for head_dim up to 256, where a warp holds O of its 16 rows whole: KG warps share out a
+// tile's keys.
+template <int D, int MW>
+struct TrKeys {
+    static constexpr int M = 16 * MW;             // rows of the tile
+    static constexpr int KG = MW == 1 ? 4 : kTrWarps / MW;
+    static constexpr int WARPS = MW * KG;         // consumers
+    static constexpr int SLOT = T * D * 2;
+    static constexpr int Q_ROW = 2 * D + 16;
+    static constexpr int O_ROW = D + 8;           // floats per row of the merge buffer
+    static constexpr int MERGE = KG * M * O_ROW * 4;  // in the ring, once its tiles are used up
+    static constexpr int FIXED = M * Q_ROW + 2 * KG * M * 4 + 64 * kTrWords * 4 + 64 * 4 +
+                                 kTreeMaxNodes * 4 + 2 * kTrMaxSlots * 8 + 1024;
+    static constexpr int PAIR_FIT = (113 * 1024 - FIXED) / SLOT;  // slots of each of two CTAs per SM
+    static constexpr bool TWO = PAIR_FIT >= 4 && PAIR_FIT * SLOT >= MERGE;
+    static constexpr int FIT = TWO ? PAIR_FIT : (227 * 1024 - FIXED) / SLOT;
+    static constexpr int SLOTS = FIT > kTrMaxSlots ? kTrMaxSlots : FIT;
+    static constexpr int RING = SLOTS * SLOT;
+    static constexpr int Q_OFF = RING;
+    static constexpr int ML_OFF = Q_OFF + M * Q_ROW;                 // m [KG][M], l [KG][M]
+    static constexpr int ANC_OFF = ML_OFF + 2 * KG * M * 4;
+    static constexpr int DEPTH_OFF = ANC_OFF + 64 * kTrWords * 4;
+    static constexpr int PAR_OFF = DEPTH_OFF + 64 * 4;
+    static constexpr int BAR_OFF = PAR_OFF + kTreeMaxNodes * 4;
+    static constexpr int SMEM = BAR_OFF + 2 * kTrMaxSlots * 8 + 1024;  // + alignment slack
+    static_assert(SLOTS >= 4 && RING >= MERGE && SMEM <= 232448 && BAR_OFF % 8 == 0,
+                  "shared memory budget");
+};
+
 // Byte offset of element (key, d) in a tile written by TMA with 128-byte swizzle.
 GEMMA_DEVINL uint32_t tr_off(int key, int d) {
     return (uint32_t)((d >> 6) * (T * 128) + key * 128 + ((((d >> 3) & 7) ^ (key & 7)) << 4) +
                       (d & 7) * 2);
 }
 
-// Barrier of n threads that tells each whether v is true for any.
-GEMMA_DEVINL bool named_bar_or(int id, int n, bool v) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
-        "bar.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)v), "r"(id), "r"(n)
-        : "memory");
-    return r != 0;
-}
-
-// A sequence's lengths. bad: an error bit, the sequence has no rows.
-struct TrSeq {
-    int len, n, base;
-    uint32_t bad;
-};
-GEMMA_DEVINL TrSeq tr_seq(const RowsParams& p, int b) {
-    TrSeq s;
-    s.len = __ldg(p.seq_lens + b);
-    s.n = p.n_real ? __ldg(p.n_real + b) : p.n_tok;
-    s.bad = 0;
-    if (s.n < 0 || s.n > p.n_tok) s.bad = GEMMA_DEVERR_N_REAL;
-    else if (s.len < s.n || (!p.ring && s.len > p.cap) || s.len > p.max_seq_len)
-        s.bad = GEMMA_DEVERR_SEQ_LEN;
-    s.base = s.len - s.n;
-    return s;
-}
-// First key that any node may attend, and where the chunks start (rings and pages: whole tiles).
-GEMMA_DEVINL int tr_first(const RowsParams& p, const TrSeq& s) {
-    return p.is_sliding ? max(0, s.base - p.window + 1) : 0;
-}
-GEMMA_DEVINL int tr_start(const RowsParams& p, const TrSeq& s) {
-    const int first = tr_first(p, s);
-    return p.ring || p.page_size ? first & ~(T - 1) : first;
-}
-// Chunks of a sequence that hold keys.
-GEMMA_DEVINL int tr_chunks(const RowsParams& p, const TrSeq& s) {
-    return min(p.n_split, (s.len - tr_start(p, s) + p.chunk - 1) / p.chunk);
-}
-
-// Walks from node i to the root: the set of the nodes it attends, and its depth. par: validated.
-GEMMA_DEVINL int tr_walk(const int* par, int i, int window, uint32_t (&set)[kTrWords]) {
-#pragma unroll
-    for (int w = 0; w < kTrWords; ++w) set[w] = 0;
-    int depth = 0;
-    for (int m = i; m >= 0; m = par[m], ++depth)
-        if (depth < window) {
-#pragma unroll
-            for (int w = 0; w < kTrWords; ++w)
-                if (w == m >> 5) set[w] |= 1u << (m & 31);
-        }
-    return depth - 1;
-}
-
-// scale * dot, soft-capped where a cap is set, in log2 units. tanh through one exponential and one
-// reciprocal: its absolute error (2^-22) times the cap is what the score is off by.
-GEMMA_DEVINL float tr_score(const RowsParams& p, float dot) {
-    if (p.softcap > 0.f) {
-        const float e = fast_exp2(dot * p.cap_inner * 2.885390081777927f);  // exp(2 x)
-        float r;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-        return fmaf(-2.f * p.cap_log2, r, p.cap_log2);
-    }
-    return dot * p.scale_log2;
-}
-
 }  // namespace
 
+// head_dim up to 256: a warp has 16 rows and a share of every tile's keys, and keeps O whole
+template <int D, int MW>
+__global__ void __launch_bounds__((TrKeys<D, MW>::WARPS + 1) * 32, TrKeys<D, MW>::TWO ? 2 : 1)
+    tree_keys_kernel(const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap, const TreeParams tp) {
+    pdl_launch_dependents();
+    using Lay = TrKeys<D, MW>;
+    constexpr int M = Lay::M, KG = Lay::KG, S = Lay::SLOTS, WARPS = Lay::WARPS;
+    constexpr int KN = T / KG;       // a warp's keys of a tile
+    constexpr int NT = KN / 8;
+    constexpr int ON = D / 8;
+    const RowsParams& p = tp.p;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* ring = smem;
+    uint8_t* sQ = smem + Lay::Q_OFF;
+    float* sM = reinterpret_cast<float*>(smem + Lay::ML_OFF);                  // [KG][M]
+    float* sL = sM + KG * M;                                                   // [KG][M]
+    uint32_t* sAnc = reinterpret_cast<uint32_t*>(smem + Lay::ANC_OFF);         // [64][kTrWords]
+    int* sDepth = reinterpret_cast<int*>(smem + Lay::DEPTH_OFF);               // [64]
+    int* sPar = reinterpret_cast<int*>(smem + Lay::PAR_OFF);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + Lay::BAR_OFF);
+    uint64_t* empty = full + kTrMaxSlots;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = blockIdx.x % p.n_split, rt = blockIdx.x / p.n_split;
+    const int kvh = blockIdx.y, b = blockIdx.z;
+    const int rows_total = p.n_tok * p.G;
+    const int row0 = rt * M, n_rows = min(M, rows_total - row0);
+    const bool direct = p.n_split == 1;
+
+    pdl_wait();  // the previous kernel on the stream has completed
+    const TrSeq sq = tr_seq(p, b);
+    const int live = sq.bad ? 0 : max(0, min(n_rows, sq.n * p.G - row0));  // rows of real nodes
+    if (live == 0) {
+        if (sq.bad && split == 0 && rt == 0 && kvh == 0 && threadIdx.x == 0) report(p.err, sq.bad);
+        for (int i = threadIdx.x; direct && i < n_rows * (D / 8); i += (WARPS + 1) * 32) {
+            const int r = i / (D / 8), R = row0 + r, tk = R / p.G;
+            __nv_bfloat16* dst =
+                reinterpret_cast<__nv_bfloat16*>(p.out) +
+                (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) * (size_t)D;
+            reinterpret_cast<uint4*>(dst)[i - r * (D / 8)] = make_uint4(0u, 0u, 0u, 0u);
+        }
+        return;
+    }
+    const int first = tr_first(p, sq);
+    const int kb = tr_start(p, sq) + split * p.chunk;
+    if (kb >= sq.len) return;
+    const int ke = min(sq.len, kb + p.chunk);
+    const int n_tiles = (ke - kb + T - 1) / T;
+    const int nops = p.k_eq_v ? 1 : 2;
+
+    if (warp == WARPS) {
+        // ------------------------- producer: tiles in the order of their use -------------------
+        if (lane == 0) {
+            for (int s = 0; s < S; ++s) {
+                mbar_init(&full[s], 1);
+                mbar_init(&empty[s], WARPS);
+            }
+            fence_barrier_init();
+        }
+        __syncwarp();
+        named_bar_arrive(1, (WARPS + 1) * 32);
+        if (lane == 0) {
+            const int n_loads = n_tiles * nops;
+            int row3 = 0, slot0 = 0;
+            bool ok = true;
+            for (int L = 0; L < n_loads && ok; ++L) {
+                const int s = L % S, use = L / S;
+                if (use > 0 && !(ok = mbar_wait(&empty[s], (use - 1) & 1, p.err))) break;
+                const bool is_v = nops == 2 && (L & 1);
+                if (!is_v) {
+                    const int t = nops == 2 ? L >> 1 : L;
+                    if (!kv_place(p, b, kvh, kb + t * T, row3, slot0)) {
+                        report(p.err, GEMMA_DEVERR_PAGE);  // reads zeros
+                        row3 = p.n_pages * p.n_kv;
+                    }
+                }
+                mbar_arrive_expect_tx(&full[s], Lay::SLOT);
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c)
+                    tma_load_3d(ring + s * Lay::SLOT + c * (T * 128), is_v ? &vmap : &kmap, c * 64,
+                                slot0, row3, &full[s]);
+            }
+        }
+        return;
+    }
+
+    // -------------------------------------- consumers ------------------------------------------
+    // Q rows (zeros behind the tile's), and the tree
+    {
+        const __nv_bfloat16* q = reinterpret_cast<const __nv_bfloat16*>(p.q);
+        constexpr int CH = D / 8;
+        for (int i = threadIdx.x; i < M * CH; i += WARPS * 32) {
+            const int r = i / CH, ch = i - r * CH;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (r < live) {
+                const int R = row0 + r, tk = R / p.G;
+                v = __ldg(reinterpret_cast<const uint4*>(
+                              q + (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) *
+                                      (size_t)D) + ch);
+            }
+            *reinterpret_cast<uint4*>(sQ + r * Lay::Q_ROW + ch * 16) = v;
+        }
+    }
+    bool bad = false;
+    if ((int)threadIdx.x < sq.n) {
+        const int m = __ldg(tp.parents + (size_t)b * p.n_tok + threadIdx.x);
+        bad = m < -1 || m >= (int)threadIdx.x;
+        sPar[threadIdx.x] = bad ? -1 : m;
+    }
+    bad = named_bar_or(2, WARPS * 32, bad);  // a bad tree: every row masked, zeros
+    if (bad && split == 0 && rt == 0 && kvh == 0 && threadIdx.x == 0)
+        report(p.err, GEMMA_DEVERR_TREE);
+    const int tk0 = row0 / p.G;  // the tile's first token
+    if ((int)threadIdx.x < (row0 + live - 1) / p.G - tk0 + 1) {
+        const int i = threadIdx.x;  // at most 64 tokens
+        uint32_t set[kTrWords];
+        sDepth[i] = tr_walk(sPar, tk0 + i, p.is_sliding ? p.window : INT_MAX, set);
+#pragma unroll
+        for (int w = 0; w < kTrWords; ++w) sAnc[i * kTrWords + w] = set[w];
+    }
+    named_bar_sync(1, (WARPS + 1) * 32);  // with the producer: its barriers exist
+
+    const int mw = warp / KG, kg = warp - mw * KG;  // row group, share of the keys
+    const int g = lane >> 2, tq = lane & 3;
+    // this thread's rows 16 mw + g and + 8: the first prefix key they attend, and their token
+    int lo[2], tok[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = 16 * mw + g + 8 * i;
+        tok[i] = r < live && !bad ? (row0 + r) / p.G - tk0 : -1;
+        lo[i] = tok[i] < 0        ? INT_MAX
+                : p.is_sliding ? max(0, sq.base + sDepth[tok[i]] - p.window + 1)
+                                  : 0;
+    }
+    const int lo_max = max(lo[0], lo[1]);
+    float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
+    float o[ON][4];
+#pragma unroll
+    for (int j = 0; j < ON; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    const uint32_t qa0 = smem_u32(sQ + (16 * mw + (lane & 15)) * Lay::Q_ROW + (lane >> 4) * 16);
+
+    // No warp waits for another before the end: each has its own keys, and its rows' reference.
+    bool ok = true;
+    int L = 0;
+    for (int t = 0; t < n_tiles; ++t) {
+        const int kt0 = kb + t * T;
+        const int sk = L % S;
+        if (ok) ok = mbar_wait(&full[sk], (L / S) & 1, p.err);
+        ++L;
+        const uint8_t* tK = ring + sk * Lay::SLOT;
+
+        // (1) S: 16 rows x this warp's keys
+        float s[NT][4];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+            uint32_t a0, a1, a2, a3;
+            ldsm_x4(qa0 + ks * 32, a0, a1, a2, a3);
+#pragma unroll
+            for (int j = 0; j < NT; j += 2) {
+                uint32_t b0, b1, b2, b3;
+                const int key = kg * KN + j * 8 + (lane & 7) + ((lane >> 4) << 3);
+                ldsm_x4(smem_u32(tK + tr_off(key, ks * 16 + ((lane >> 3) & 1) * 8)), b0, b1, b2, b3);
+                mma_bf16(s[j], a0, a1, a2, a3, b0, b1);
+                mma_bf16(s[j + 1], a0, a1, a2, a3, b2, b3);
+            }
+        }
+        if (nops == 2) {  // K has been read
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[sk]);
+        }
+
+        // (2) scores, masks, the rows' maxima, P as the A operand of P V
+        const int kw = kt0 + kg * KN;  // this warp's first key
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[j][e] = tr_score(p, s[j][e]);
+        if (!(kw >= lo_max && kw + KN <= sq.base)) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int key = kw + j * 8 + 2 * tq + (e & 1), i = e >> 1, m = key - sq.base;
+                    bool in = m < 0 && key >= lo[i];
+                    if (m >= 0 && key < ke && tok[i] >= 0)
+                        in = (sAnc[tok[i] * kTrWords + (m >> 5)] >> (m & 31)) & 1u;
+                    if (!in) s[j][e] = -INFINITY;
+                }
+        }
+        float alpha[2];
+        uint32_t pa[NT][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) mx = fmax3f(mx, s[j][2 * i], s[j][2 * i + 1]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            alpha[i] = 1.f;
+            if (mx > m_run[i] + kTrLazyLog2) {
+                alpha[i] = fast_exp2(m_run[i] - mx);  // 0 while the reference is -inf
+                m_run[i] = mx;
+            }
+            const float neg = m_run[i] == -INFINITY ? 0.f : -m_run[i];
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                pa[j][i] = pack_bf16(fast_exp2(s[j][2 * i] + neg), fast_exp2(s[j][2 * i + 1] + neg));
+                sum += __uint_as_float(pa[j][i] << 16) + __uint_as_float(pa[j][i] & 0xffff0000u);
+            }
+            l_run[i] = fmaf(l_run[i], alpha[i], sum);
+        }
+        if (alpha[0] != 1.f || alpha[1] != 1.f) {
+#pragma unroll
+            for (int j = 0; j < ON; ++j) {
+                o[j][0] *= alpha[0];
+                o[j][1] *= alpha[0];
+                o[j][2] *= alpha[1];
+                o[j][3] *= alpha[1];
+            }
+        }
+
+        // (3) O += P V over this warp's keys, all columns
+        int sv = sk;
+        if (nops == 2) {
+            sv = L % S;
+            if (ok) ok = mbar_wait(&full[sv], (L / S) & 1, p.err);
+            ++L;
+        }
+        const uint8_t* tV = ring + sv * Lay::SLOT;
+        const bool edge = kt0 < first || kt0 + T > ke;
+#pragma unroll
+        for (int kk = 0; kk < KN / 16; ++kk) {
+            uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;
+            if (edge) {  // rows outside of the tree's keys may hold anything: zeros
+                auto in = [&](int k) { return kw + k >= first && kw + k < ke; };
+                const int k0 = kk * 16 + 2 * tq;
+                mlo = (in(k0) ? 0x0000ffffu : 0u) | (in(k0 + 1) ? 0xffff0000u : 0u);
+                mhi = (in(k0 + 8) ? 0x0000ffffu : 0u) | (in(k0 + 9) ? 0xffff0000u : 0u);
+            }
+            const int vkey = kg * KN + kk * 16 + (lane & 15);
+#pragma unroll
+            for (int j = 0; j < ON; j += 2) {
+                uint32_t v0, v1, v2, v3;
+                ldsm_x4_t(smem_u32(tV + tr_off(vkey, j * 8 + (lane >> 4) * 8)), v0, v1, v2, v3);
+                mma_bf16(o[j], pa[2 * kk][0], pa[2 * kk][1], pa[2 * kk + 1][0], pa[2 * kk + 1][1],
+                         v0 & mlo, v1 & mhi);
+                mma_bf16(o[j + 1], pa[2 * kk][0], pa[2 * kk][1], pa[2 * kk + 1][0],
+                         pa[2 * kk + 1][1], v2 & mlo, v3 & mhi);
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[sv]);
+    }
+
+    // ---- merge of the key groups through the ring (its last tile has been read) ----
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], 1);
+        l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], 2);
+        if (tq == 0) {
+            sM[kg * M + 16 * mw + g + 8 * i] = m_run[i];
+            sL[kg * M + 16 * mw + g + 8 * i] = l_run[i];
+        }
+    }
+    named_bar_sync(2, WARPS * 32);
+    float* sO = reinterpret_cast<float*>(ring);  // [KG][M][O_ROW]
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int r = 16 * mw + g + 8 * i;
+        float top = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < KG; ++k) top = fmaxf(top, sM[k * M + r]);
+        const float w = m_run[i] == -INFINITY ? 0.f : fast_exp2(m_run[i] - top);
+        float* dst = sO + (kg * M + r) * Lay::O_ROW + 2 * tq;
+#pragma unroll
+        for (int j = 0; j < ON; ++j)
+            *reinterpret_cast<float2*>(dst + j * 8) =
+                w == 0.f ? make_float2(0.f, 0.f) : make_float2(o[j][2 * i] * w, o[j][2 * i + 1] * w);
+    }
+    named_bar_sync(2, WARPS * 32);
+    constexpr int CH = D / 4;  // four columns of a row per thread and step
+    for (int x = threadIdx.x; x < n_rows * CH; x += WARPS * 32) {
+        const int r = x / CH, ch = x - r * CH, R = row0 + r;
+        float top = -INFINITY, l = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < KG; ++k) top = fmaxf(top, sM[k * M + r]);
+#pragma unroll
+        for (int k = 0; k < KG; ++k) {
+            const float4 v = *reinterpret_cast<const float4*>(sO + (k * M + r) * Lay::O_ROW + 4 * ch);
+            const float mk = sM[k * M + r];
+            l += mk == -INFINITY ? 0.f : fast_exp2(mk - top) * sL[k * M + r];
+            a.x += v.x;
+            a.y += v.y;
+            a.z += v.z;
+            a.w += v.w;
+        }
+        if (direct) {
+            const int tk = R / p.G;
+            uint2* dst = reinterpret_cast<uint2*>(
+                reinterpret_cast<__nv_bfloat16*>(p.out) +
+                (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) * (size_t)D + 4 * ch);
+            const float inv = 1.f / l;  // (no keys: zeros, whatever the other rows' V holds)
+            *dst = l == 0.f ? make_uint2(0u, 0u)
+                            : make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+        } else {
+            const size_t pr =
+                (((size_t)b * p.n_kv + kvh) * rows_total + R) * p.n_split + split;
+            *reinterpret_cast<float4*>(p.o_part + pr * D + 4 * ch) = a;
+            if (ch == 0) *reinterpret_cast<float2*>(p.ml_part + pr * 2) = make_float2(top, l);
+        }
+    }
+}
+
+// head_dim 512 (O of 16 rows is two warps' registers): the warps of a row group share out the keys of
+// S and the columns of O
 template <int D, int MW>
 __global__ void __launch_bounds__(kTrThreads, TrLay<D, MW>::TWO ? 2 : 1)
     tree_rows_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -543,7 +825,7 @@ template <int D>
 __global__ void __launch_bounds__(kTrF32Warps * 32) tree_f32_kernel(const TreeParams tp) {
     pdl_launch_dependents();
     pdl_wait();  // the previous kernel on the stream has completed
-    constexpr int E = D / 32, U = 4;
+    constexpr int E = D / 32, U = D >= 512 ? 2 : 4;  // keys of a step
     const RowsParams& p = tp.p;
     __shared__ int s_par[kTreeMaxNodes];
     __shared__ uint32_t s_set[kTrWords];
@@ -587,34 +869,51 @@ __global__ void __launch_bounds__(kTrF32Warps * 32) tree_f32_kernel(const TreePa
         qr[e] = q[lane + 32 * e];
         acc[e] = 0.f;
     }
-    float m = -INFINITY, l = 0.f;
-    for (int j0 = lo + warp * U; j0 < sq.len; j0 += kTrF32Warps * U) {
-        float s[U];
-        size_t row[U];
-        bool in[U];
+    // a step's K and V rows are in flight while the step before is computed
+    float kn[U][E], vn[U][E];
+    bool in[U];
+    auto load = [&](int j0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int j = j0 + u, n = j - sq.base;
             in[u] = j < sq.len && (n < 0 || ((s_set[n >> 5] >> (n & 31)) & 1u));
             int krow = 0, kslot = 0;
-            if (in[u] && !kv_place(p, b, kvh, j, krow, kslot)) {  // a bad page: zeros
+            bool there = in[u];
+            if (there && !kv_place(p, b, kvh, j, krow, kslot)) {  // a bad page: zeros
                 if (lane == 0) report(p.err, GEMMA_DEVERR_PAGE);
-                krow = -1;
+                there = false;
             }
-            row[u] = krow < 0 ? (size_t)-1 : (size_t)krow * rs + (size_t)kslot;
-            float dot = 0.f;
-            if (in[u] && row[u] != (size_t)-1) {
+            const size_t at = ((size_t)krow * rs + (size_t)kslot) * D + lane;
 #pragma unroll
-                for (int e = 0; e < E; ++e) dot = fmaf(qr[e], K[row[u] * D + lane + 32 * e], dot);
+            for (int e = 0; e < E; ++e) {
+                kn[u][e] = there ? __ldg(K + at + 32 * e) : 0.f;
+                vn[u][e] = there ? __ldg(V + at + 32 * e) : 0.f;
             }
-            s[u] = dot;
         }
+    };
+    float m = -INFINITY, l = 0.f;
+    constexpr int STEP = kTrF32Warps * U;
+    if (lo + warp * U < sq.len) load(lo + warp * U);
+    for (int j0 = lo + warp * U; j0 < sq.len; j0 += STEP) {
+        float s[U], v[U][E];
+        bool now[U];
         float top = m;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            s[u] = 0.f;
+            now[u] = in[u];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                s[u] = fmaf(qr[e], kn[u][e], s[u]);
+                v[u][e] = vn[u][e];
+            }
+        }
+        if (j0 + STEP < sq.len) load(j0 + STEP);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             s[u] = warp_sum(s[u]) * p.scale;
             if (p.softcap > 0.f) s[u] = p.softcap * tanhf(s[u] / p.softcap);
-            if (in[u]) top = fmaxf(top, s[u]);
+            if (now[u]) top = fmaxf(top, s[u]);
         }
         if (top == -INFINITY) continue;  // nothing attended so far
         const float alpha = expf(m - top);
@@ -623,12 +922,11 @@ __global__ void __launch_bounds__(kTrF32Warps * 32) tree_f32_kernel(const TreePa
         for (int e = 0; e < E; ++e) acc[e] *= alpha;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            if (!in[u]) continue;
+            if (!now[u]) continue;
             const float w = expf(s[u] - top);
             l += w;
-            if (row[u] == (size_t)-1) continue;
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(w, V[row[u] * D + lane + 32 * e], acc[e]);
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[u][e], acc[e]);
         }
         m = top;
     }
@@ -653,10 +951,27 @@ __global__ void __launch_bounds__(kTrF32Warps * 32) tree_f32_kernel(const TreePa
 // ---------------------------------------------------------------------------------------------
 // launchers
 // ---------------------------------------------------------------------------------------------
+// The kernel of a shape: its layout, threads and entry.
+template <int D, int MW>
+struct TrKernel {
+    using Lay = TrKeys<D, MW>;
+    static constexpr int THREADS = (Lay::WARPS + 1) * 32;
+    static auto entry() { return tree_keys_kernel<D, MW>; }
+};
+template <int MW>
+struct TrKernel<512, MW> {
+    using Lay = TrLay<512, MW>;
+    static constexpr int THREADS = kTrThreads;
+    static auto entry() { return tree_rows_kernel<512, MW>; }
+};
+
 template <int D>
 static int ctas_per_sm(int groups) {
-    return (groups == 1 ? TrLay<D, 1>::TWO : groups == 2 ? TrLay<D, 2>::TWO : TrLay<D, 4>::TWO) ? 2
-                                                                                              : 1;
+    return (groups == 1   ? TrKernel<D, 1>::Lay::TWO
+            : groups == 2 ? TrKernel<D, 2>::Lay::TWO
+                          : TrKernel<D, 4>::Lay::TWO)
+               ? 2
+               : 1;
 }
 
 int tree_ctas_per_sm(int head_dim, int rows) {
@@ -671,9 +986,9 @@ int tree_ctas_per_sm(int head_dim, int rows) {
 
 template <int D, int MW>
 static cudaError_t launch_rows_dm(const TreeParams& tp, int batch, cudaStream_t st) {
-    using Lay = TrLay<D, MW>;
+    using Lay = typename TrKernel<D, MW>::Lay;
     const RowsParams& p = tp.p;
-    auto kernel = tree_rows_kernel<D, MW>;
+    auto kernel = TrKernel<D, MW>::entry();
     static std::atomic<bool> configured[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
@@ -693,7 +1008,7 @@ static cudaError_t launch_rows_dm(const TreeParams& tp, int batch, cudaStream_t 
     if (!encode_bf16_sw128(&km, p.k, 3, dims, strides, box)) return cudaErrorInvalidValue;
     if (!encode_bf16_sw128(&vm, p.v, 3, dims, strides, box)) return cudaErrorInvalidValue;
     const unsigned tiles = (unsigned)((p.n_tok * p.G + Lay::M - 1) / Lay::M);
-    return launch_pdl(kernel, dim3(tiles * p.n_split, p.n_kv, batch), dim3(kTrThreads), Lay::SMEM,
+    return launch_pdl(kernel, dim3(tiles * p.n_split, p.n_kv, batch), dim3(TrKernel<D, MW>::THREADS), Lay::SMEM,
                       st, km, vm, tp);
 }
 

@@ -1,0 +1,750 @@
+// tree_tc.cu -- attention of a drafted tree with up to 128 rows per KV head and tile, on the
+// 5th-generation tensor cores (tcgen05, one SM per tile). Definition in tree_attn.cu.
+//
+// A unit is one KV head of one sequence and 128 of its rows (nodes x G query heads). Per tile of 64
+// keys: S = Q K^T (M 128, N 64) into tensor memory, softmax by four warps (a thread per row), P as
+// bf16 back into tensor memory, O += P V (N = head_dim). With 64 rows of head_dim 256 a tile's
+// 64 KB take longer to arrive (1.45 us when all SMs load) than the tensor core (0.8 us) or the
+// softmax (0.6 us) needs, so the tile rate is that of memory, and what is left to lose is the start,
+// the end and the change from one unit to the next:
+//  - the key tiles of all units form one sequence (lengths are known on the device alone), of which
+//    every CTA takes an equal share; every warp works out the share by itself, from a scan of the
+//    lengths, before the first barrier wait;
+//  - barriers, tensor memory and tensor maps are set up before the wait for the previous kernel;
+//  - S and P have two buffers each, so that S(t + 1) and P V(t - 1) run beside the softmax of t, and
+//    loads run ahead through the ring, into the next unit too;
+//  - a unit cut between CTAs leaves parts (O fp32 as it stands in tensor memory, four columns of all
+//    rows after another, so that stores are of 512 consecutive bytes) for tc_merge_kernel.
+// Warps: 0-3 softmax and epilogue, 4 TMA producer, 5 MMA issuer.
+#include <atomic>
+#include <climits>
+
+#include "common.cuh"
+#include "tc.cuh"
+#include "tmap.h"
+#include "tree.h"
+#include "tree_dev.cuh"
+
+namespace gemma {
+
+namespace {
+
+constexpr int kTcThreads = 192;
+constexpr int kTcRows = 128;
+constexpr int kTcKeys = kTreeKeyTile;
+constexpr int kTcMaxSlots = 12;
+constexpr int kTcBox = kTcKeys * 128;  // 64 keys x 64 columns
+constexpr int kTcQBox = kTcRows * 128;
+// TMEM columns: O, S (two buffers), P (two buffers of packed bf16)
+constexpr int kTcO = 0, kTcS = 256, kTcP = 384;
+
+template <int D>
+struct TcLay {
+    static constexpr int SLOT = kTcKeys * D * 2;
+    static constexpr int Q = kTcRows * D * 2;
+    static constexpr int FIT = (232448 - Q - 1024 - 512) / SLOT;
+    static constexpr int SLOTS = FIT > kTcMaxSlots ? kTcMaxSlots : FIT;
+    static constexpr int Q_OFF = SLOTS * SLOT;
+    static constexpr int BAR_OFF = Q_OFF + Q;
+    static constexpr int SMEM = BAR_OFF + 512 + 1024;  // + alignment slack
+    static_assert(SMEM <= 232448 && (2 * kTcMaxSlots + 13) * 8 + 4 <= 512, "shared memory budget");
+};
+
+struct TcParams {
+    TreeParams tp;
+    int batch, n_rt, workers;
+    float* part_o;    // [2 workers slots][D / 4][128 rows] x 4 columns
+    float2* part_ml;  // [2 workers slots][128 rows]
+    int32_t* before;  // [batch + 1] key tiles of earlier sequences, for the merge
+};
+
+// A unit, or a part of one.
+struct TcUnit {
+    int b, kvh, rt;
+    TrSeq sq;
+    int first;             // first key that a node may attend
+    int k_begin, n_tiles;  // the part's
+    int slot;              // workspace slot, -1: the whole unit
+};
+
+// A sequence's tiles per unit, and its row tiles that have rows.
+GEMMA_DEVINL int tc_tiles(const RowsParams& p, const TrSeq& s, int& live_rt) {
+    live_rt = s.bad ? 0 : (s.n * p.G + kTcRows - 1) / kTcRows;
+    return live_rt ? (s.len - tr_start(p, s) + kTcKeys - 1) / kTcKeys : 0;
+}
+
+// A CTA's parts, in the order of (sequence, KV head, row tile, keys). Whole warps run it alike.
+struct TcShare {
+    int pos, end, begin, b, seq0, worker;  // seq0: tiles of the sequences before b
+    GEMMA_DEVINL void init(const TcParams& tp, bool write_before) {
+        const int lane = threadIdx.x & 31;
+        worker = blockIdx.x;
+        int total = 0, excl = 0;
+        for (int b0 = 0; b0 < tp.batch; b0 += 32) {
+            const int incl = scan(tp, b0, excl);
+            if (write_before && b0 + lane < tp.batch) tp.before[b0 + lane] = total + excl;
+            total += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (write_before && lane == 0) tp.before[tp.batch] = total;
+        const int share = (total + tp.workers - 1) / tp.workers;
+        begin = pos = min(total, worker * share);
+        end = min(total, pos + share);
+        b = 0;
+        seq0 = 0;
+        int sum = 0;
+        for (int b0 = 0; b0 < tp.batch && pos < end; b0 += 32) {
+            const int incl = tp.batch > 32 || b0 ? scan(tp, b0, excl) : scan(tp, 0, excl);
+            // the last sequence whose tiles start at or before pos (and that has any behind it)
+            const unsigned in = __ballot_sync(0xffffffffu, sum + incl > pos);
+            if (in) {
+                const int l = __ffs(in) - 1;
+                b = b0 + l;
+                seq0 = sum + __shfl_sync(0xffffffffu, excl, l);
+                return;
+            }
+            sum += __shfl_sync(0xffffffffu, incl, 31);
+        }
+    }
+    // inclusive (and exclusive) prefix sums of 32 sequences' tiles
+    static GEMMA_DEVINL int scan(const TcParams& tp, int b0, int& excl) {
+        const int lane = threadIdx.x & 31;
+        int n = 0;
+        if (b0 + lane < tp.batch) {
+            int live_rt;
+            n = tc_tiles(tp.tp.p, tr_seq(tp.tp.p, b0 + lane), live_rt);
+            n *= live_rt * tp.tp.p.n_kv;
+        }
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        excl = incl - n;
+        return incl;
+    }
+    GEMMA_DEVINL bool next(const TcParams& tp, TcUnit& U) {
+        if (pos >= end) return false;
+        const RowsParams& p = tp.tp.p;
+        for (;; ++b) {  // (sequences without tiles are passed over)
+            U.sq = tr_seq(p, b);
+            int live_rt;
+            const int nt = tc_tiles(p, U.sq, live_rt), all = nt * live_rt * p.n_kv;
+            if (pos < seq0 + all) {
+                const int rel = pos - seq0, idx = rel / nt, t0 = rel - idx * nt;
+                const int t1 = min(nt, t0 + end - pos);
+                U.b = b;
+                U.kvh = idx / live_rt;
+                U.rt = idx - U.kvh * live_rt;
+                U.first = tr_first(p, U.sq);
+                U.k_begin = tr_start(p, U.sq) + t0 * kTcKeys;
+                U.n_tiles = t1 - t0;
+                U.slot = t0 == 0 && t1 == nt ? -1 : 2 * worker + (pos != begin);
+                pos += t1 - t0;
+                return true;
+            }
+            seq0 += all;
+        }
+    }
+};
+
+GEMMA_DEVINL void prefetch_map(const CUtensorMap* m) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
+}
+
+}  // namespace
+
+template <int D, bool SOFTCAP>
+__global__ void __launch_bounds__(kTcThreads, 1)
+    tree_tc_kernel(const __grid_constant__ CUtensorMap kmap,
+                   const __grid_constant__ CUtensorMap vmap,
+                   const __grid_constant__ CUtensorMap qmap, const TcParams tp) {
+    using Lay = TcLay<D>;
+    constexpr int S = Lay::SLOTS;
+    pdl_launch_dependents();
+    const RowsParams& p = tp.tp.p;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* ring = smem;
+    uint8_t* sQ = smem + Lay::Q_OFF;  // [D / 64][128][64] bf16
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + Lay::BAR_OFF);
+    uint64_t* empty = full + kTcMaxSlots;   // the MMAs that read the slot have completed
+    uint64_t* q_full = empty + kTcMaxSlots;
+    uint64_t* q_free = q_full + 1;          // a part's last S has completed
+    uint64_t* s_full = q_full + 2;          // [2] S is in TMEM
+    uint64_t* s_free = q_full + 4;          // [2] the softmax warps have read it
+    uint64_t* p_full = q_full + 6;          // [2] P is in TMEM
+    uint64_t* pv_done = q_full + 8;         // [2] P V has completed
+    uint64_t* o_full = q_full + 10;         // a part's last P V has completed
+    uint64_t* o_free = q_full + 11;         // O has been read
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(q_full + 12);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int nops = p.k_eq_v ? 1 : 2;
+
+    if (warp == 4) {
+        if (lane == 0) {
+            prefetch_map(&kmap);
+            prefetch_map(&qmap);
+            if (nops == 2) prefetch_map(&vmap);
+            for (int s = 0; s < S; ++s) {
+                mbar_init(&full[s], 1);
+                mbar_init(&empty[s], 1);
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&s_full[i], 1);
+                mbar_init(&s_free[i], 4);
+                mbar_init(&p_full[i], 4);
+                mbar_init(&pv_done[i], 1);
+            }
+            mbar_init(q_full, 1);
+            mbar_init(q_free, 1);
+            mbar_init(o_full, 1);
+            mbar_init(o_free, 4);
+            fence_barrier_init();
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        tmem_alloc(tslot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    pdl_wait();  // the previous kernel on the stream has completed
+    TcShare share;
+    share.init(tp, blockIdx.x == 0 && warp == 0);
+
+    if (warp == 4) {
+        // ------------------------------------ TMA producer --------------------------------------
+        // K(0), V(0), K(1), ... into a ring of slots; each part's Q rows first, once the last S of
+        // the part before has read the buffer.
+        TcUnit U;
+        bool ok = true;
+        int L = 0, ord = 0;
+        while (share.next(tp, U)) {
+            if (lane == 0) {
+                if (ord > 0 && ok) ok = mbar_wait(q_free, (ord - 1) & 1, p.err);
+                if (ok) {
+                    mbar_arrive_expect_tx(q_full, Lay::Q);
+#pragma unroll
+                    for (int j = 0; j < D / 64; ++j)  // (tokens past the bucket read 0)
+                        tma_load_4d(sQ + j * kTcQBox, &qmap, 64 * j, U.kvh * p.G,
+                                    U.rt * kTcRows / p.G, U.b, q_full);
+                }
+                for (int t = 0; t < U.n_tiles && ok; ++t) {
+                    int row3 = 0, slot0 = 0;
+                    if (!kv_place(p, U.b, U.kvh, U.k_begin + t * kTcKeys, row3, slot0)) {
+                        report(p.err, GEMMA_DEVERR_PAGE);  // reads zeros
+                        row3 = p.n_pages * p.n_kv;
+                    }
+                    for (int v = 0; v < nops && ok; ++v, ++L) {
+                        const int s = L % S, use = L / S;
+                        if (use > 0) ok = mbar_wait(&empty[s], (use - 1) & 1, p.err);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(&full[s], Lay::SLOT);
+#pragma unroll
+                        for (int j = 0; j < D / 64; ++j)
+                            tma_load_3d(ring + s * Lay::SLOT + j * kTcBox, v ? &vmap : &kmap, 64 * j,
+                                        slot0, row3, &full[s]);
+                    }
+                }
+            }
+            ++ord;
+            __syncwarp();
+        }
+        if (lane == 0) {
+            // what was loaded has been read before the CTA may exit
+            for (int k = 1; k <= S && k <= L && ok; ++k)
+                ok = mbar_wait(&empty[(L - k) % S], ((L - k) / S) & 1, p.err);
+        }
+        __syncwarp();
+    } else if (warp == 5) {
+        // ------------------------------------- MMA issuer ---------------------------------------
+        // S(0), S(1), P V(0), S(2), P V(1), ...
+        const uint32_t id_s = idesc_bf16(128, kTcKeys, 0, 0), id_pv = idesc_bf16(128, D, 0, 1);
+        const uint64_t qd = smem_desc_sw128(smem_u32(sQ), 0, 1024);
+        bool ok = true;
+        struct Tile {
+            int key0, n_valid, n_head;
+            bool valid, first, last;
+        };
+        TcUnit U;
+        U.n_tiles = 0;
+        int t = 0, ord = -1;
+        auto next = [&](Tile& x) {
+            if (t >= U.n_tiles) {
+                x.valid = share.next(tp, U);
+                if (!x.valid) return;
+                t = 0;
+                ++ord;
+            }
+            x.valid = true;
+            x.key0 = U.k_begin + t * kTcKeys;
+            x.n_valid = min(kTcKeys, U.sq.len - x.key0);
+            x.n_head = max(0, U.first - x.key0);
+            x.first = t == 0;
+            x.last = t == U.n_tiles - 1;
+            ++t;
+        };
+        Tile cur, prev;
+        prev.valid = false;
+        int T = 0, prev_ord = -1;
+        for (;; ++T) {
+            next(cur);
+            const int cur_ord = ord;
+            if (!cur.valid && !prev.valid) break;
+            if (cur.valid) {
+                const int L = T * nops, s = L % S, buf = T & 1;
+                if (ok) ok = mbar_wait(&full[s], (L / S) & 1, p.err);
+                if (cur.first && ok) ok = mbar_wait(q_full, cur_ord & 1, p.err);
+                if (T >= 2 && ok) ok = mbar_wait(&s_free[buf], ((T >> 1) - 1) & 1, p.err);
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t kd = smem_desc_sw128(smem_u32(ring + s * Lay::SLOT), 0, 1024);
+#pragma unroll
+                    for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            umma_ss(tmem + kTcS + 64 * buf,
+                                    qd + (uint64_t)((j * kTcQBox + ks * 32) >> 4),
+                                    kd + (uint64_t)((j * kTcBox + ks * 32) >> 4), id_s,
+                                    (j | ks) ? 1u : 0u);
+                    umma_commit(&s_full[buf]);
+                    if (nops == 2) umma_commit(&empty[s]);
+                    if (cur.last) umma_commit(q_free);
+                }
+                __syncwarp();
+            }
+            if (prev.valid) {
+                const int Tp = T - 1, L = Tp * nops + nops - 1, s = L % S, buf = Tp & 1;
+                if (ok) ok = mbar_wait(&full[s], (L / S) & 1, p.err);
+                uint8_t* tile = ring + s * Lay::SLOT;
+                if (prev.n_valid < kTcKeys || prev.n_head > 0) {
+                    // rows outside of the sequence's keys may hold anything: zeros
+                    for (int i = lane; i < kTcKeys * (D / 8); i += 32) {
+                        const int key = i / (D / 8), ch = i - key * (D / 8);
+                        if (key >= prev.n_valid || key < prev.n_head)
+                            *reinterpret_cast<uint4*>(tile + (ch >> 3) * kTcBox + key * 128 +
+                                                      (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (ok) ok = mbar_wait(&p_full[buf], (Tp >> 1) & 1, p.err);
+                if (prev.first && prev_ord > 0 && ok)
+                    ok = mbar_wait(o_free, (prev_ord - 1) & 1, p.err);
+                tc_fence_after();
+                if (lane == 0) {
+                    const uint64_t vd = smem_desc_sw128(smem_u32(tile), kTcBox, 1024);
+#pragma unroll
+                    for (int kk = 0; kk < kTcKeys / 16; ++kk)
+                        umma_ts(tmem + kTcO, tmem + kTcP + 32 * buf + 8 * kk,
+                                vd + (uint64_t)((kk * 2048) >> 4), id_pv,
+                                (prev.first && kk == 0) ? 0u : 1u);
+                    umma_commit(&pv_done[buf]);
+                    umma_commit(&empty[s]);
+                    if (prev.last) umma_commit(o_full);
+                }
+                __syncwarp();
+            }
+            prev = cur;
+            prev_ord = cur_ord;
+        }
+    } else {
+        // -------------------------------- softmax and epilogue ----------------------------------
+        const int r = threadIdx.x;  // row of the tile = TMEM lane
+        const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+        const uint32_t tO = tmem + kTcO + lanes;
+        bool ok = true;
+        TcUnit U;
+        int T = 0, ord = 0, in_b = -1, in_rt = -1;
+        uint32_t anc[kTrWords];
+        int lo = INT_MAX;
+        for (; share.next(tp, U); ++ord) {
+            const int base = U.sq.base, R = U.rt * kTcRows + r;
+            if (U.b != in_b || U.rt != in_rt) {
+                // the nodes that this row attends, and its first prefix key (the same for the next
+                // KV head of the sequence)
+                in_b = U.b;
+                in_rt = U.rt;
+                const int32_t* par = tp.tp.parents + (size_t)U.b * p.n_tok;
+                bool bad = false;
+#pragma unroll
+                for (int k = 0; k < kTrWords; ++k) {
+                    const int i = lane + 32 * k;
+                    anc[k] = 0;
+                    if (i < U.sq.n) {
+                        const int m = __ldg(par + i);
+                        bad |= m < -1 || m >= i;
+                    }
+                }
+                bad = __any_sync(0xffffffffu, bad);  // the same in every warp: no row attends
+                if (bad && threadIdx.x == 0) report(p.err, GEMMA_DEVERR_TREE);
+                lo = INT_MAX;
+                if (R < U.sq.n * p.G && !bad) {
+                    const int window = p.is_sliding ? p.window : INT_MAX;
+                    int depth = 0;
+                    for (int m = R / p.G; m >= 0; m = __ldg(par + m), ++depth)
+                        if (depth < window) {
+#pragma unroll
+                            for (int k = 0; k < kTrWords; ++k)
+                                if (k == m >> 5) anc[k] |= 1u << (m & 31);
+                        }
+                    lo = p.is_sliding ? max(0, base + depth - p.window) : 0;
+                }
+            }
+            const bool idle = __all_sync(0xffffffffu, lo == INT_MAX);  // no row of the warp attends
+            float m = -INFINITY, l = 0.f;
+            for (int t = 0; t < U.n_tiles; ++t, ++T) {
+                const int buf = T & 1;
+                if (ok) ok = mbar_wait(&s_full[buf], (T >> 1) & 1, p.err);
+                tc_fence_after();
+                if (idle) {  // P = 0 (both buffers keep it for the rest of the part)
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_free[buf]);
+                    if (t < 2) {
+                        if (T >= 2 && ok) ok = mbar_wait(&pv_done[buf], ((T >> 1) - 1) & 1, p.err);
+                        tc_fence_after();
+                        uint32_t z[32];
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) z[e] = 0u;
+                        tmem_st32(tmem + kTcP + 32 * buf + lanes, z);
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                    }
+                    if (lane == 0) mbar_arrive(&p_full[buf]);
+                    continue;
+                }
+                float s[64];
+                {
+                    uint32_t v0[32], v1[32];
+                    tmem_ld32(tmem + kTcS + 64 * buf + lanes, v0);
+                    tmem_ld32(tmem + kTcS + 64 * buf + 32 + lanes, v1);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        s[e] = __uint_as_float(v0[e]);
+                        s[32 + e] = __uint_as_float(v1[e]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_free[buf]);  // S(T + 2) may overwrite it
+                float sl2 = p.scale_log2;  // scale > 0: the raw maximum scales to the maximum
+                if constexpr (SOFTCAP) {
+#pragma unroll
+                    for (int e = 0; e < 64; ++e) s[e] = tr_score(p, s[e]);
+                    sl2 = 1.f;
+                }
+                const int kt0 = U.k_begin + t * kTcKeys;
+                if (!(kt0 >= lo && kt0 + kTcKeys <= base)) {
+                    const unsigned long long see = tr_window(anc, kt0 - base, lo - kt0);
+                    const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        if (!((s0 >> e) & 1u)) s[e] = -INFINITY;
+                        if (!((s1 >> e) & 1u)) s[32 + e] = -INFINITY;
+                    }
+                }
+                float mx8[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mx8[i] = fmax3f(s[i], s[8 + i], s[16 + i]);
+#pragma unroll
+                for (int e = 24; e < 56; e += 16)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) mx8[i] = fmax3f(mx8[i], s[e + i], s[e + 8 + i]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) mx8[i] = fmaxf(mx8[i], s[56 + i]);
+                const float mx = fmax3f(fmax3f(mx8[0], mx8[1], mx8[2]), fmax3f(mx8[3], mx8[4], mx8[5]),
+                                        fmaxf(mx8[6], mx8[7])) * sl2;
+                const float m_prev = m;
+                if (mx > m + kTrLazyLog2) {
+                    l = m == -INFINITY ? 0.f : l * fast_exp2(m - mx);
+                    m = mx;
+                }
+                // O rows whose reference moved: rescaled once P V(T - 1) has completed (a row
+                // without keys so far has O = 0)
+                const bool moved = t > 0 && m != m_prev && m_prev != -INFINITY;
+                if (__any_sync(0xffffffffu, moved)) {
+                    if (ok) ok = mbar_wait(&pv_done[buf ^ 1], ((T - 1) >> 1) & 1, p.err);
+                    tc_fence_after();
+                    const float alpha = moved ? fast_exp2(m_prev - m) : 1.f;
+#pragma unroll 1
+                    for (int j = 0; j < D / 32; ++j) {
+                        uint32_t v[32];
+                        tmem_ld32(tO + j * 32, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            v[e] = __float_as_uint(__uint_as_float(v[e]) * alpha);
+                        tmem_st32(tO + j * 32, v);
+                    }
+                    tmem_st_wait();
+                }
+                const float neg = m == -INFINITY ? 0.f : -m;
+                const unsigned long long sl2x2 = f32x2(sl2, sl2), neg2 = f32x2(neg, neg);
+                unsigned long long sum2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
+                uint32_t pw[32];
+#pragma unroll
+                for (int k = 0; k < 32; ++k) {
+                    const float2 x =
+                        f32x2_split(fma_f32x2(f32x2(s[2 * k], s[2 * k + 1]), sl2x2, neg2));
+                    pw[k] = pack_bf16(fast_exp2(x.x), fast_exp2(x.y));
+                    // (summed as rounded)
+                    sum2[k & 1] = add_f32x2(sum2[k & 1], f32x2(__uint_as_float(pw[k] << 16),
+                                                               __uint_as_float(pw[k] & 0xffff0000u)));
+                }
+                const float2 sa = f32x2_split(sum2[0]), sb = f32x2_split(sum2[1]);
+                l += (sa.x + sa.y) + (sb.x + sb.y);
+                // the buffer is free once P V(T - 2) has completed
+                if (T >= 2 && ok) ok = mbar_wait(&pv_done[buf], ((T >> 1) - 1) & 1, p.err);
+                tc_fence_after();
+                tmem_st32(tmem + kTcP + 32 * buf + lanes, pw);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[buf]);
+            }
+            // ---- the part's results ----
+            if (ok) ok = mbar_wait(o_full, ord & 1, p.err);
+            tc_fence_after();
+            const int n_rows = min(kTcRows, p.n_tok * p.G - U.rt * kTcRows);
+            const int tk = R / p.G;
+            __nv_bfloat16* out =
+                reinterpret_cast<__nv_bfloat16*>(p.out) +
+                (((size_t)U.b * p.n_tok + tk) * p.n_q + U.kvh * p.G + (R - tk * p.G)) * (size_t)D;
+            float4* part = reinterpret_cast<float4*>(tp.part_o) + (size_t)max(U.slot, 0) * (D / 4) * kTcRows + r;
+            if (U.slot >= 0) tp.part_ml[(size_t)U.slot * kTcRows + r] = make_float2(m, l);
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+            for (int j = 0; j < D / 32; ++j) {
+                uint32_t v[32];
+                tmem_ld32(tO + j * 32, v);
+                tmem_ld_wait();
+                if (j == D / 32 - 1) {  // O has been read
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(o_free);
+                }
+                if (U.slot >= 0) {
+                    if (idle) continue;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        part[(size_t)(j * 8 + q) * kTcRows] = make_float4(
+                            __uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
+                            __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
+                } else if (r < n_rows) {
+                    uint4* dst = reinterpret_cast<uint4*>(out + j * 32);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t w4[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)  // (no keys: zeros, whatever the other rows' V holds)
+                            w4[e] = l == 0.f ? 0u
+                                             : pack_bf16(__uint_as_float(v[8 * q + 2 * e]) * inv,
+                                                         __uint_as_float(v[8 * q + 2 * e + 1]) * inv);
+                        dst[q] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                    }
+                }
+            }
+        }
+        // zeros for row tiles without nodes
+        for (int x = blockIdx.x; x < tp.n_rt * tp.batch * p.n_kv; x += tp.workers) {
+            const int per = tp.n_rt * p.n_kv, b = x / per, kvh = x % per / tp.n_rt, rt = x % tp.n_rt;
+            const TrSeq sq = tr_seq(p, b);
+            if (!sq.bad && rt * kTcRows < sq.n * p.G) continue;
+            if (sq.bad && kvh == 0 && rt == 0 && threadIdx.x == 0) report(p.err, sq.bad);
+            const int n_rows = min(kTcRows, p.n_tok * p.G - rt * kTcRows);
+            for (int i = threadIdx.x; i < n_rows * (D / 8); i += 128) {
+                const int R = rt * kTcRows + i / (D / 8), tk = R / p.G;
+                reinterpret_cast<uint4*>(
+                    reinterpret_cast<__nv_bfloat16*>(p.out) +
+                    (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) *
+                        (size_t)D)[i % (D / 8)] = make_uint4(0u, 0u, 0u, 0u);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 5) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// merge of the parts of every unit that more than one CTA took a share of,
+//   M = max_w m_w, out = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w
+// A lane per row and 16 columns: reads of 512 consecutive bytes, writes of whole sectors. WAYS warps
+// share out the parts (few units are cut into many) and meet in shared memory.
+// ---------------------------------------------------------------------------------------------
+template <int D, int WAYS>
+__global__ void __launch_bounds__(256) tc_merge_kernel(const TcParams tp) {
+    pdl_launch_dependents();
+    pdl_wait();  // the parts
+    constexpr int SLICES = 8 / WAYS, PER = D / (16 * SLICES) > 0 ? D / (16 * SLICES) : 1;
+    const RowsParams& p = tp.tp.p;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, way = warp % WAYS;
+    const int slice = (blockIdx.x % PER) * SLICES + warp / WAYS;
+    const int x = blockIdx.x / PER, group = x & 3, unit = x >> 2;
+    const int per = tp.n_rt * p.n_kv, b = unit / per, kvh = unit % per / tp.n_rt,
+              rt = unit % tp.n_rt;
+    const int rr = group * 32 + lane, R = rt * kTcRows + rr;
+    if (rt * kTcRows + group * 32 >= p.n_tok * p.G) return;
+    const TrSeq sq = tr_seq(p, b);
+    int live_rt;
+    const int nt = tc_tiles(p, sq, live_rt);
+    if (rt >= live_rt) return;  // zeros already
+    const int total = tp.before[tp.batch], share = (total + tp.workers - 1) / tp.workers;
+    const int f0 = tp.before[b] + (kvh * live_rt + rt) * nt, f1 = f0 + nt;
+    const int w0 = f0 / share, w1 = (f1 - 1) / share;
+    if (w0 == w1) return;  // a whole unit: written by its CTA
+    // CTA w's part is the first of its share but for one that began before the unit
+    auto part = [&](int w) { return (size_t)(2 * w + (w * share < f0)); };
+    float top = -INFINITY;
+#pragma unroll 4
+    for (int w = w0; w <= w1; ++w) top = fmaxf(top, tp.part_ml[part(w) * kTcRows + rr].x);
+    float acc[16], l = 0.f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+    const bool some = slice < D / 16 && __any_sync(0xffffffffu, top != -INFINITY);
+    if (some) {
+#pragma unroll 2
+        for (int w = w0 + way; w <= w1; w += WAYS) {
+            const float2 ml = tp.part_ml[part(w) * kTcRows + rr];
+            const float4* src = reinterpret_cast<const float4*>(tp.part_o) +
+                                (part(w) * (D / 4) + 4 * slice) * kTcRows + rr;
+            const float e = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - top);
+            l = fmaf(e, ml.y, l);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float4 o = __ldcs(src + q * kTcRows);
+                if (e == 0.f) continue;  // (O without keys may be NaN where V is)
+                acc[4 * q] = fmaf(e, o.x, acc[4 * q]);
+                acc[4 * q + 1] = fmaf(e, o.y, acc[4 * q + 1]);
+                acc[4 * q + 2] = fmaf(e, o.z, acc[4 * q + 2]);
+                acc[4 * q + 3] = fmaf(e, o.w, acc[4 * q + 3]);
+            }
+        }
+    }
+    if constexpr (WAYS > 1) {
+        __shared__ float s_acc[8][17][32];
+        if (way) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s_acc[warp][e][lane] = acc[e];
+            s_acc[warp][16][lane] = l;
+        }
+        __syncthreads();
+        if (way) return;
+#pragma unroll
+        for (int k = 1; k < WAYS; ++k) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[e] += s_acc[warp + k][e][lane];
+            l += s_acc[warp + k][16][lane];
+        }
+    }
+    if (R >= p.n_tok * p.G || slice >= D / 16) return;
+    const float inv = 1.f / l;
+    uint32_t out[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)  // (no keys: zeros, whatever the other rows' V holds)
+        out[e] = l == 0.f ? 0u : pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    const int tk = R / p.G;
+    uint4* dst = reinterpret_cast<uint4*>(
+        reinterpret_cast<__nv_bfloat16*>(p.out) +
+        (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) * (size_t)D + slice * 16);
+    dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+    dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+// ---------------------------------------------------------------------------------------------
+// launch
+// ---------------------------------------------------------------------------------------------
+namespace {
+
+struct TcScratch {
+    size_t ml_off, before_off, bytes;
+};
+TcScratch tc_scratch(int head_dim, int batch, int workers) {
+    TcScratch s;
+    const size_t rows = (size_t)2 * workers * kTcRows;
+    s.ml_off = rows * head_dim * sizeof(float);
+    s.before_off = s.ml_off + rows * sizeof(float2);
+    s.bytes = s.before_off + ((size_t)batch + 4) / 4 * 16;
+    return s;
+}
+
+template <int D>
+cudaError_t launch_tc(const TreeParams& tree, int batch, void* workspace, int workers,
+                      cudaStream_t st) {
+    using Lay = TcLay<D>;
+    const RowsParams& p = tree.p;
+    static std::atomic<bool> configured[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+    if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_relaxed)) {
+        cudaError_t e = cudaFuncSetAttribute(
+            tree_tc_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(tree_tc_kernel<D, true>,
+                                     cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_relaxed);
+    }
+    CUtensorMap km, vm, qm;
+    // [rows][slots][D]: rows = sequences x KV heads (pages x KV heads for a paged pool)
+    const uint64_t slots = (uint64_t)(p.page_size ? p.page_size : p.cap);
+    const uint64_t rows = (uint64_t)(p.page_size ? p.n_pages : batch) * p.n_kv;
+    const uint64_t dims[3] = {(uint64_t)D, slots, rows};
+    const uint64_t strides[2] = {(uint64_t)D * 2, slots * D * 2};
+    const uint32_t box[3] = {64, (uint32_t)kTcKeys, 1};
+    if (!encode_bf16_sw128(&km, p.k, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    if (!encode_bf16_sw128(&vm, p.v, 3, dims, strides, box)) return cudaErrorInvalidValue;
+    // Q [B][n_tok][n_q][D]: G heads of one KV head's group x 128 / G tokens are a row tile
+    const uint64_t qdims[4] = {(uint64_t)D, (uint64_t)p.n_q, (uint64_t)p.n_tok, (uint64_t)batch};
+    const uint64_t qstrides[3] = {(uint64_t)D * 2, (uint64_t)p.n_q * D * 2,
+                                  (uint64_t)p.n_tok * p.n_q * D * 2};
+    const uint32_t qbox[4] = {64, (uint32_t)p.G, (uint32_t)(kTcRows / p.G), 1};
+    if (!encode_bf16_sw128(&qm, p.q, 4, qdims, qstrides, qbox)) return cudaErrorInvalidValue;
+    TcParams tp{};
+    tp.tp = tree;
+    tp.batch = batch;
+    tp.n_rt = (p.n_tok * p.G + kTcRows - 1) / kTcRows;
+    tp.workers = workers;
+    const TcScratch ws = tc_scratch(D, batch, workers);
+    uint8_t* base = static_cast<uint8_t*>(workspace);
+    tp.part_o = reinterpret_cast<float*>(base);
+    tp.part_ml = reinterpret_cast<float2*>(base + ws.ml_off);
+    tp.before = reinterpret_cast<int32_t*>(base + ws.before_off);
+    auto kernel = p.softcap > 0.f ? tree_tc_kernel<D, true> : tree_tc_kernel<D, false>;
+    const cudaError_t e = launch_pdl(kernel, dim3(workers), dim3(kTcThreads), Lay::SMEM, st, km, vm, qm, tp);
+    if (e != cudaSuccess) return e;
+    const int units = tp.n_rt * batch * p.n_kv;
+    // (parts per unit: about the CTAs over the units)
+    if (units * 4 < workers)
+        return launch_pdl(tc_merge_kernel<D, 8>, dim3((unsigned)(units * 4 * (D / 16))), dim3(256), 0,
+                          st, tp);
+    constexpr int PER = D / 128 > 0 ? D / 128 : 1;
+    return launch_pdl(tc_merge_kernel<D, 1>, dim3((unsigned)(units * 4 * PER)), dim3(256), 0, st, tp);
+}
+
+}  // namespace
+
+size_t tree_tc_workspace(int head_dim, int batch, int workers) {
+    return tc_scratch(head_dim, batch, workers).bytes;
+}
+
+cudaError_t launch_tree_tc(const TreeParams& tp, int head_dim, int batch, void* workspace,
+                           int workers, cudaStream_t st) {
+    switch (head_dim) {
+        case 64: return launch_tc<64>(tp, batch, workspace, workers, st);
+        case 128: return launch_tc<128>(tp, batch, workspace, workers, st);
+        case 256: return launch_tc<256>(tp, batch, workspace, workers, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace gemma

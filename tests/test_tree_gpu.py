@@ -197,7 +197,8 @@ def test_chain_is_the_prefill_step():
 def test_shared_layers_read_their_owners_cache():
     p = Problem([100], [6], 6, n_q=4, n_kv=2, d=64)
     out = torch.empty_like(p.q)
-    ws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    ws = torch.empty(max(16, g.gemma_attn_workspace_size_tree(1, GLOBAL, 0, 4, 2, 64, 100, 6)),
+                     dtype=torch.uint8, device="cuda")
     g.gemma_attn_tree(out, p.q, [p.k, None, None], [p.v, None, None], [0, 0, 0], 2, i32([100]),
                       i32(p.parents), 100, kind=GLOBAL, window=0, n_kv=2, k_eq_v=False,
                       scale=p.scale, workspace=ws)
