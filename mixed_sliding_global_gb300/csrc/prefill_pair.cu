@@ -37,7 +37,7 @@
 //               so the softmax of tile t+1 does not wait for the P V of tile t).
 //   warp 8      TMA producer: each unit's Q rows (once the previous unit's last S has read the
 //               Q buffer) and this CTA's halves of the K and V tiles (128-byte swizzle, boxes of
-//               64 keys x 64 columns) into a FIFO ring of 32 KB slots, in the MMA order.
+//               64 keys x 64 columns) into 32 KB slots (two of K, two of V; one of V at head_dim 512), in the MMA order.
 //   warp 9      even CTA: issues S(t) = Q K(t)^T once both CTAs' softmax warps have read S(t-1),
 //               so the softmax of tile t overlaps the P V of tile t-1 and the S of tile t+1.
 //               Odd CTA: forwards each of its ring slots' arrivals to the even CTA's barriers
@@ -63,7 +63,7 @@
 //  - the units are cut by keys: the key tiles of all units form one sequence, of which every worker
 //    takes an equal share (lengths are known on the device alone). A worker's first and last unit
 //    may be parts, whose O (fp32) and (m, l) go to the worker's two slots of the workspace for
-//    pair_merge_kernel; whole units are written as in the other modes;
+//    tree_merge_kernel; whole units are written as in the other modes;
 //  - the mask: prefix keys from the row's window start on, and behind them a 64-bit window of the
 //    row's ancestor set, walked up from its node at the start of a part;
 //  - a soft-cap goes through one exponential and one reciprocal (absolute error 2^-21 of the cap).
@@ -85,6 +85,7 @@ constexpr int kPrThreads = kPrWarps * 32;
 constexpr int kPrProducerWarp = 8;
 constexpr int kPrSWarp = 9;     // S issuer (even CTA) / slot forwarder (odd CTA)
 constexpr int kPrPvWarp = 10;   // P V issuer (even CTA)
+constexpr int kPrQWarp = 11;    // trees: Q loads
 constexpr int kPrKeys = 128;                  // keys per tile (N of S)
 constexpr int kPrRows = 256;                  // rows per unit (M of the pair's MMAs)
 constexpr int kPrBox = 64 * 128;              // TMA box: 64 keys x 64 columns of bf16
@@ -104,7 +105,10 @@ constexpr int kPrSCol = 0, kPrPCol = 128, kPrOCol = 256;  // TMEM columns
 template <int H>
 struct PrLay {
     static constexpr int D = 256 * H;                  // head_dim
-    static constexpr int SLOTS = H == 1 ? 4 : 3;       // ring slots
+    // Ring slots: K and V have slots of their own, so that each issuer sees every phase of the
+    // barriers it waits on (a parity wait two phases behind passes at once: with three slots in
+    // turn, V(t)'s slot held K(t) before, and its wait could pass while K(t) was on its way).
+    static constexpr int K_SLOTS = 2, V_SLOTS = H == 1 ? 2 : 1, SLOTS = K_SLOTS + V_SLOTS;
     static constexpr int Q_OFF = SLOTS * kPrSlot;
     static constexpr int STAGE_OFF = Q_OFF + kPrQBytes;
     static constexpr int X_OFF = STAGE_OFF + kPrStage;
@@ -296,7 +300,7 @@ struct PrTileIter {
 // SOFTCAP: the soft-capped variant; MODE: a padded bucket's, dealing out its units from the work
 // list, or a tree's (separate instantiations, so that the plain kernel carries no code for either)
 template <int H, bool SOFTCAP, int MODE>
-__global__ void __launch_bounds__(kPrThreads, 1)
+__global__ void __launch_bounds__(kPrThreads + (MODE == kPrTree ? 32 : 0), 1)
     prefill_pair_kernel(const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap,
                         const __grid_constant__ CUtensorMap qmap,
@@ -395,7 +399,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             if (lane == 0) ulist[fp.batch] = sum;
             __syncwarp();
             if (blockIdx.x == 0)
-                for (int i = lane; i <= fp.batch; i += 32) fp.before[i] = ulist[i];
+                for (int i = lane; i <= fp.batch + 1; i += 32)
+                    fp.before[i] = i <= fp.batch ? ulist[i] : 0;  // (units are cut)
         }
     }
     if constexpr (LIST) {
@@ -476,7 +481,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         // the previous unit's last S (the last reader of the Q buffer) has completed.
         if (lane == 0) {
             bool ok = true;
-            int L = 0;
+            int n_loads[2] = {0, 0};  // of K and of V
             auto place = [&](const PrTile& T, int key, int& row3, int& slot0) {
                 if (p.page_size && key - T.key0 >= T.n_valid) {
                     // a group behind the last key: its page may be none of the sequence's
@@ -489,8 +494,8 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                 }
             };
             auto load = [&](const PrTile& T, bool is_v) {
-                const int s = L % kPrSlots, use = L / kPrSlots;
-                ++L;
+                const int n = n_loads[is_v]++, N = is_v ? Lay::V_SLOTS : Lay::K_SLOTS;
+                const int s = (is_v ? Lay::K_SLOTS : 0) + n % N, use = n / N;
                 if (use > 0 && ok) ok = mbar_wait(&empty[s], (use - 1) & 1, p.err);
                 mbar_arrive_expect_tx(&full[s], kPrSlot);
                 if (!ok) return;
@@ -525,7 +530,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             for (;;) {
                 const PrTile cur = it.next(fp);
                 if (!cur.valid && !prev.valid) break;
-                if (cur.valid && cur.first) {
+                if (!TREE && cur.valid && cur.first) {
                     // (a barrier of its own: this thread runs tiles ahead of the S MMAs, and a
                     // parity wait must not be more than one phase ahead of the barrier)
                     if (cur.ord > 0 && ok) ok = mbar_wait(q_free, (cur.ord - 1) & 1, p.err);
@@ -545,29 +550,52 @@ __global__ void __launch_bounds__(kPrThreads, 1)
             }
             // the last releases of the slots and of the Q buffer (arrivals of the MMA commits
             // on this CTA's barriers) have landed before the CTA may exit
-            for (int k = 1; k <= kPrSlots && k <= L; ++k) {
-                const int LL = L - k;
-                if (ok) ok = mbar_wait(&empty[LL % kPrSlots], (LL / kPrSlots) & 1, p.err);
+            for (int v = 0; v < 2; ++v) {
+                const int N = v ? Lay::V_SLOTS : Lay::K_SLOTS;
+                for (int n = max(0, n_loads[v] - N); n < n_loads[v]; ++n)
+                    if (ok) ok = mbar_wait(&empty[(v ? Lay::K_SLOTS : 0) + n % N], (n / N) & 1, p.err);
             }
-            if (Tn > 0 && ok) ok = mbar_wait(q_free, it.ord & 1, p.err);
+            if (!TREE && Tn > 0 && ok) ok = mbar_wait(q_free, it.ord & 1, p.err);
+        }
+    } else if (TREE && warp == kPrQWarp) {
+        // ----------------------------- trees: Q rows ---------------------------------------
+        // of a warp of their own: parts are short, and the wait for the last S of the part before
+        // must not hold back the next part's keys
+        if (lane == 0) {
+            PrShare share;
+            PrUnit U;
+            bool ok = true;
+            int ord = 0;
+            share.init(fp, worker, ulist);
+            for (; share.next(fp, worker, ulist, U); ++ord) {
+                if (ord > 0 && ok) ok = mbar_wait(q_free, (ord - 1) & 1, p.err);
+                mbar_arrive_expect_tx(q_full, kPrQBytes);
+                if (!ok) continue;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    tma_load_4d(sQ + j * kPrQBox, &qmap, 256 * (int)h + 64 * j, U.kvh * p.G,
+                                (U.row0 + 128 * (int)c) / p.G, U.b, q_full);
+            }
+            if (ord > 0 && ok) mbar_wait(q_free, (ord - 1) & 1, p.err);
         }
     } else if (c == 0 && (warp == kPrSWarp || warp == kPrPvWarp)) {
         // ------------------ MMA issuers: S (warp 9) and P V (warp 10) -----------------------
         // An MMA is accepted only when the one before it is nearly done, so an issuing thread
         // is busy for about the tensor time of what it issues. With S and P V from separate
         // threads, one issuer's waits (for P, or for the softmax to have read S) leave the
-        // tensor core to the other's MMAs. Both walk the producer's slot order.
+        // tensor core to the other's MMAs. Each walks its own slots.
         const bool is_s = warp == kPrSWarp;
         const uint32_t id_s = idesc_bf16(256, kPrKeys, 0, 0);
         const uint32_t id_pv = idesc_bf16(256, 256, 0, 1);
         const uint32_t tS = tmem + kPrSCol, tP = tmem + kPrPCol, tO = tmem + kPrOCol;
         bool ok = true;
-        int L = 0;
-        // the next slot with both CTAs' halves landed (V: its edge rows zeroed here)
+        int n_taken = 0;
+        // the next slot of K or of V with both CTAs' halves landed (V: its edge rows zeroed here)
         auto take = [&](const PrTile& T, bool is_v) -> int {
-            const int s = L % kPrSlots;
-            const uint32_t ph = (L / kPrSlots) & 1;
-            ++L;
+            const int N = is_v ? Lay::V_SLOTS : Lay::K_SLOTS;
+            const int s = (is_v ? Lay::K_SLOTS : 0) + n_taken % N;
+            const uint32_t ph = (n_taken / N) & 1;
+            ++n_taken;
             if (ok) ok = mbar_wait(&full[s], ph, p.err);
             if (is_v) zero_v(slots + s * kPrSlot, T);
             if (ok) ok = mbar_wait(&pfull[s], ph, p.err);
@@ -581,9 +609,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
         for (;;) {
             const PrTile cur = it.next(fp);
             if (!cur.valid && !prev.valid) break;
-            if (cur.valid && !is_s) {
-                ++L;  // K(Tn): the S issuer's
-            } else if (cur.valid) {
+            if (cur.valid && is_s) {
                 // S(Tn) = Q K(Tn)^T, once both CTAs' softmax warps have read S(Tn - 1)
                 const int sk = take(cur, false);
                 if (cur.first && ok) {
@@ -608,9 +634,7 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                 }
                 __syncwarp();
             }
-            if (prev.valid && is_s) {
-                ++L;  // V(Tn - 1): the P V issuer's
-            } else if (prev.valid) {
+            if (prev.valid && !is_s) {
                 // O (+)= P(Tn - 1) V(Tn - 1)
                 const int Tp = Tn - 1;
                 const int sv = take(prev, true);
@@ -639,12 +663,12 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     } else if (c == 1 && warp == kPrSWarp) {
         // ------------------- odd CTA: forwards its slots' arrivals ---------------------------
         bool ok = true;
-        int L = 0;
+        int n_seen[2] = {0, 0};  // of K and of V
         const uint32_t pfull0 = map_to_peer(&pfull[0], lead);
         auto fwd = [&](const PrTile& T, bool is_v) {
-            const int s = L % kPrSlots;
-            const uint32_t ph = (L / kPrSlots) & 1;
-            ++L;
+            const int n = n_seen[is_v]++, N = is_v ? Lay::V_SLOTS : Lay::K_SLOTS;
+            const int s = (is_v ? Lay::K_SLOTS : 0) + n % N;
+            const uint32_t ph = (n / N) & 1;
             if (ok) ok = mbar_wait(&full[s], ph, p.err);
             if (is_v) zero_v(slots + s * kPrSlot, T);
             if (lane == 0) mbar_arrive_remote(pfull0 + 8u * (uint32_t)s);
@@ -1062,20 +1086,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
                 ++ord;
             }
         }
-        if constexpr (TREE) {
-            // zeros for row tiles without nodes
-            for (int x = worker; x < fp.n_units; x += fp.n_pairs) {
-                PrUnit U;
-                int live_rt;
-                const int per = fp.n_rt * p.n_kv, rem = x % per;
-                pr_tree_seq(p, x / per, U, live_rt);
-                U.kvh = rem / fp.n_rt;
-                U.rt = rem - U.kvh * fp.n_rt;
-                U.row0 = U.rt * kPrRows;
-                U.n_rows = min(kPrRows, p.n_tok * p.G - U.row0);
-                if (U.rt >= live_rt) zero_unit(U);
-            }
-        }
     }
     if (warp < 8 && (threadIdx.x & 127) == 0) bulk_wait_all();  // the epilogues' TMA stores
     tc_fence_before();
@@ -1087,95 +1097,6 @@ __global__ void __launch_bounds__(kPrThreads, 1)
     }
 }
 
-// ---------------------------------------------------------------------------------------------
-// Trees: merge of the parts of every unit that more than one worker took a share of,
-//   M = max_w m_w, out = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w
-// (at head_dim 512 each half of the columns with its own (m, l)). A lane per row and 16 columns: reads
-// of 512 consecutive bytes, writes of whole sectors. WAYS warps share out the parts of 32 rows and 16
-// columns (few units are cut into many parts) and meet in shared memory.
-// ---------------------------------------------------------------------------------------------
-template <int H, int WAYS>
-__global__ void __launch_bounds__(256) pair_merge_kernel(const PrParams fp) {
-    pdl_launch_dependents();
-    pdl_wait();  // the parts
-    constexpr int D = 256 * H;
-    const RowsParams& p = fp.p;
-    const int lane = threadIdx.x & 31;
-    // a CTA's warps: the same rows, neighbouring slices of 16 columns, WAYS warps each
-    constexpr int SLICES = 8 / WAYS;
-    const int warp = threadIdx.x >> 5, way = warp % WAYS;
-    const int slice = (blockIdx.x % (D / (16 * SLICES))) * SLICES + warp / WAYS;
-    const int x = blockIdx.x / (D / (16 * SLICES)), group = x & 7, unit = x >> 3;
-    const int per = fp.n_rt * p.n_kv, b = unit / per, kvh = unit % per / fp.n_rt,
-              rt = unit % fp.n_rt;
-    PrUnit U;
-    int live_rt;
-    pr_tree_seq(p, b, U, live_rt);
-    if (U.bad || rt >= live_rt) return;  // zeros already
-    const int total = fp.before[fp.batch], share = (total + fp.n_pairs - 1) / fp.n_pairs;
-    const int f0 = fp.before[b] + (kvh * live_rt + rt) * U.n_tiles, f1 = f0 + U.n_tiles;
-    const int w0 = f0 / share, w1 = (f1 - 1) / share;
-    if (w0 == w1) return;  // a whole unit: written by its worker
-    const int rr = group * 32 + lane, R = rt * kPrRows + rr;
-    const bool there = R < p.n_tok * p.G;
-    // worker w's part is the first of its share but for one that began before the unit; the
-    // 128-row, 256-column piece with this row and slice
-    const int c = rr >> 7, h = slice >> 4, r = rr & 127;
-    auto part = [&](int w) { return ((size_t)(2 * w + (w * share < f0)) * 2 + c) * H + h; };
-    float top = -INFINITY;
-#pragma unroll 4
-    for (int w = w0; w <= w1; ++w) top = fmaxf(top, fp.part_ml[part(w) * 128 + r].x);
-    float acc[16], l = 0.f;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-#pragma unroll 2
-    for (int w = w0 + way; w <= w1; w += WAYS) {
-        const size_t pt = part(w);
-        const float2 ml = fp.part_ml[pt * 128 + r];
-        const float4* src =
-            reinterpret_cast<const float4*>(fp.part_o) + (pt * 64 + 4 * (slice & 15)) * 128 + r;
-        const float e = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - top);
-        l = fmaf(e, ml.y, l);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            const float4 o = __ldcs(src + q * 128);
-            if (e == 0.f) continue;  // (O without keys may be NaN where V is)
-            acc[4 * q] = fmaf(e, o.x, acc[4 * q]);
-            acc[4 * q + 1] = fmaf(e, o.y, acc[4 * q + 1]);
-            acc[4 * q + 2] = fmaf(e, o.z, acc[4 * q + 2]);
-            acc[4 * q + 3] = fmaf(e, o.w, acc[4 * q + 3]);
-        }
-    }
-    if constexpr (WAYS > 1) {
-        __shared__ float s_acc[8][17][32];
-        if (way) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s_acc[warp][e][lane] = acc[e];
-            s_acc[warp][16][lane] = l;
-        }
-        __syncthreads();
-        if (way) return;
-#pragma unroll
-        for (int k = 1; k < WAYS; ++k) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[e] += s_acc[warp + k][e][lane];
-            l += s_acc[warp + k][16][lane];
-        }
-    }
-    if (!there) return;
-    const float inv = 1.f / l;
-    uint32_t out[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)  // (no keys: zeros, whatever the other rows' V holds)
-        out[e] = l == 0.f ? 0u : pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    const int tk = R / p.G;
-    uint4* dst = reinterpret_cast<uint4*>(
-        reinterpret_cast<__nv_bfloat16*>(p.out) +
-        (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) * (size_t)D + slice * 16);
-    dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-    dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
-}
-
 // Scratch of a tree launch on n clusters: parts, their (m, l), tiles before each sequence.
 struct PrTreeScratch {
     size_t ml_off, before_off, bytes;
@@ -1185,7 +1106,7 @@ static PrTreeScratch pr_tree_scratch(int H, int n_clusters, int batch) {
     PrTreeScratch s;
     s.ml_off = rows * (256 * H) * sizeof(float);
     s.before_off = s.ml_off + rows * H * sizeof(float2);
-    s.bytes = s.before_off + ((size_t)batch + 4) / 4 * 16;
+    s.bytes = s.before_off + ((size_t)batch + 8) / 4 * 16;
     return s;
 }
 
@@ -1273,27 +1194,27 @@ static cudaError_t launch_pair(const RowsParams& p, int batch, cudaStream_t st,
     fp.n_units = fp.n_rt * batch * p.n_kv;
     fp.n_pairs = fp.n_units < n_clusters ? fp.n_units : n_clusters;
     if (tree) {
-        fp.parents = tree->parents;
-        fp.n_pairs = workers < n_clusters ? workers : n_clusters;
+        MergeParams mp{};
+        mp.tp = *tree;
+        mp.batch = batch;
+        mp.n_rt = fp.n_rt;
+        mp.workers = fp.n_pairs = workers < n_clusters ? workers : n_clusters;
+        mp.keys = kPrKeys;
         const PrTreeScratch ws = pr_tree_scratch(H, fp.n_pairs, batch);
         uint8_t* base = static_cast<uint8_t*>(workspace);
-        fp.part_o = reinterpret_cast<float*>(base);
-        fp.part_ml = reinterpret_cast<float2*>(base + ws.ml_off);
-        fp.before = reinterpret_cast<int32_t*>(base + ws.before_off);
+        fp.parents = tree->parents;
+        mp.part_o = fp.part_o = reinterpret_cast<float*>(base);
+        mp.part_ml = fp.part_ml = reinterpret_cast<float2*>(base + ws.ml_off);
+        mp.before = fp.before = reinterpret_cast<int32_t*>(base + ws.before_off);
         cfg.gridDim = dim3(2 * H * fp.n_pairs);
+        cfg.blockDim = dim3(kPrThreads + 32);
         cfg.dynamicSmemBytes = Lay::TREE_SMEM;
         const cudaError_t e =
             p.softcap > 0.f
                 ? cudaLaunchKernelEx(&cfg, prefill_pair_kernel<H, true, kPrTree>, km, vm, qm, om, fp)
                 : cudaLaunchKernelEx(&cfg, prefill_pair_kernel<H, false, kPrTree>, km, vm, qm, om,
                                      fp);
-        if (e != cudaSuccess) return e;
-        // (parts per unit: about the workers over the units)
-        if (fp.n_units * 4 < fp.n_pairs)
-            return launch_pdl(pair_merge_kernel<H, 8>, dim3((unsigned)(fp.n_units * 8 * (D / 16))),
-                              dim3(256), 0, st, fp);
-        return launch_pdl(pair_merge_kernel<H, 1>, dim3((unsigned)(fp.n_units * 8 * (D / 128))),
-                          dim3(256), 0, st, fp);
+        return e == cudaSuccess ? launch_tree_merge(mp, D, kPrRows, st) : e;
     }
     cfg.gridDim = dim3(2 * H * fp.n_pairs);
     if (p.softcap > 0.f)

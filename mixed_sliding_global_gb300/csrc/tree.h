@@ -25,6 +25,19 @@ size_t tree_tc_workspace(int head_dim, int batch, int workers);
 cudaError_t launch_tree_tc(const TreeParams& tp, int head_dim, int batch, void* workspace,
                            int workers, cudaStream_t st);
 
+// Parts of units cut into equal shares of the key tiles, and where they lie in the workspace. A worker
+// has two slots: for the part that its share begins with, and for the one that it ends with.
+struct MergeParams {
+    TreeParams tp;
+    int batch, n_rt;  // row tiles per (sequence, KV head)
+    int workers;
+    int keys;         // of a key tile
+    float* part_o;    // [2 workers][pieces of 128 rows and up to 256 columns][columns / 4][128][4]
+    float2* part_ml;  // [2 workers][pieces][128]
+    int32_t* before;  // [batch + 1] key tiles of earlier sequences; then whether no unit was cut
+};
+cudaError_t launch_tree_merge(const MergeParams& mp, int head_dim, int rows, cudaStream_t st);
+
 // CTAs of the bf16 launch that fit an SM.
 int tree_ctas_per_sm(int head_dim, int rows);
 

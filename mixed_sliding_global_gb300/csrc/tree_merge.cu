@@ -1,0 +1,135 @@
+// tree_merge.cu -- merge of the parts that the equal shares of tree_tc.cu and prefill_pair.cu leave of a
+// unit (one KV head of one sequence, a tile of rows):
+//   M = max_w m_w, out = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w
+// and zeros for row tiles without nodes. A lane has one row and 16 columns: parts lie with four columns
+// of 128 rows after another, so reads are of 512 consecutive bytes, and writes are whole sectors. WAYS
+// warps share out the parts (few units are cut into many) and meet in shared memory. Latency bound: one
+// pass, so that a warp waits for memory twice (lengths, parts). It takes 2.5 us of a step of 9 on nine
+// parts of 32 rows.
+#include "common.cuh"
+#include "tree.h"
+#include "tree_dev.cuh"
+
+namespace gemma {
+
+template <int D, int ROWS, int WAYS>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const MergeParams mp) {
+    pdl_launch_dependents();
+    constexpr int COLS = D < 256 ? D : 256;            // of a piece: 128 rows x COLS
+    constexpr int C = ROWS / 128, H = D / COLS;        // pieces of a part
+    constexpr int SLICES = 8 / WAYS;                   // of 16 columns, per CTA
+    constexpr int PER = (D / 16 + SLICES - 1) / SLICES, GROUPS = ROWS / 32;
+    const RowsParams& p = mp.tp.p;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, way = warp % WAYS;
+    const int slice = (blockIdx.x % PER) * SLICES + warp / WAYS;
+    const int x = blockIdx.x / PER, group = x % GROUPS, unit = x / GROUPS;
+    const int per = mp.n_rt * p.n_kv, b = unit / per, kvh = unit % per / mp.n_rt,
+              rt = unit % mp.n_rt;
+    const int rr = group * 32 + lane, R = rt * ROWS + rr, rows_total = p.n_tok * p.G;
+    if (rt * ROWS + group * 32 >= rows_total) return;
+    const int tk = R / p.G;
+    uint4* dst = reinterpret_cast<uint4*>(
+        reinterpret_cast<__nv_bfloat16*>(p.out) +
+        (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) * (size_t)D + slice * 16);
+    const bool mine = R < rows_total && slice < D / 16;
+    pdl_wait();  // the parts
+    const int total = mp.before[mp.batch], whole = mp.before[mp.batch + 1], first = mp.before[b];
+    const TrSeq sq = tr_seq(p, b);
+    const int live_rt = sq.bad ? 0 : (sq.n * p.G + ROWS - 1) / ROWS;
+    if (rt >= live_rt) {
+        if (sq.bad && rt == 0 && kvh == 0 && group == 0 && slice == 0 && way == 0 && lane == 0)
+            report(p.err, sq.bad);
+        if (mine && way == 0) dst[0] = dst[1] = make_uint4(0u, 0u, 0u, 0u);
+        return;
+    }
+    if (whole) return;  // units were not cut
+    const int nt = (sq.len - tr_start(p, sq) + mp.keys - 1) / mp.keys;
+    const int share = (total + mp.workers - 1) / mp.workers;
+    const int f0 = first + (kvh * live_rt + rt) * nt, f1 = f0 + nt;
+    const int w0 = f0 / share, w1 = (f1 - 1) / share;
+    if (w0 == w1) return;  // a whole unit: written by its worker
+    const int c = rr >> 7, h = slice * 16 / COLS, r = rr & 127;
+    float m = -INFINITY, l = 0.f, acc[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+    if (slice < D / 16) {
+#pragma unroll 2
+        for (int w = w0 + way; w <= w1; w += WAYS) {
+            // worker w's part is the first of its share but for one that began before the unit
+            const size_t piece = ((size_t)(2 * w + (w * share < f0)) * C + c) * H + h;
+            const float2 ml = mp.part_ml[piece * 128 + r];
+            const float4* src = reinterpret_cast<const float4*>(mp.part_o) +
+                                (piece * (COLS / 4) + 4 * (slice % (COLS / 16))) * 128 + r;
+            float4 o[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) o[q] = __ldcs(src + q * 128);
+            if (ml.x == -INFINITY) continue;  // (no keys: O is nothing, or NaN where V is)
+            const float top = fmaxf(m, ml.x), a = fast_exp2(m - top), e = fast_exp2(ml.x - top);
+            m = top;
+            l = fmaf(l, a, e * ml.y);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                acc[4 * q] = fmaf(acc[4 * q], a, e * o[q].x);
+                acc[4 * q + 1] = fmaf(acc[4 * q + 1], a, e * o[q].y);
+                acc[4 * q + 2] = fmaf(acc[4 * q + 2], a, e * o[q].z);
+                acc[4 * q + 3] = fmaf(acc[4 * q + 3], a, e * o[q].w);
+            }
+        }
+    }
+    if constexpr (WAYS > 1) {
+        __shared__ float s_acc[8][18][32];
+        if (way) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s_acc[warp][e][lane] = acc[e];
+            s_acc[warp][16][lane] = l;
+            s_acc[warp][17][lane] = m;
+        }
+        __syncthreads();
+        if (way) return;
+        float top = m;
+#pragma unroll
+        for (int k = 1; k < WAYS; ++k) top = fmaxf(top, s_acc[warp + k][17][lane]);
+        const float a = m == -INFINITY ? 0.f : fast_exp2(m - top);
+        l *= a;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[e] *= a;
+#pragma unroll
+        for (int k = 1; k < WAYS; ++k) {
+            const float mk = s_acc[warp + k][17][lane], ak = mk == -INFINITY ? 0.f : fast_exp2(mk - top);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[e] = fmaf(ak, s_acc[warp + k][e][lane], acc[e]);
+            l = fmaf(ak, s_acc[warp + k][16][lane], l);
+        }
+    }
+    if (!mine) return;
+    const float inv = 1.f / l;
+    uint32_t out[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e)  // (no keys: zeros)
+        out[e] = l == 0.f ? 0u : pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+    dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+}
+
+template <int D, int ROWS>
+static cudaError_t launch_merge(const MergeParams& mp, cudaStream_t st) {
+    const long long groups = (long long)mp.n_rt * mp.batch * mp.tp.p.n_kv * (ROWS / 32);
+    // (parts per unit: about the workers over the units)
+    if ((long long)mp.n_rt * mp.batch * mp.tp.p.n_kv * 4 < mp.workers)
+        return launch_pdl(tree_merge_kernel<D, ROWS, 8>, dim3((unsigned)(groups * (D / 16))),
+                          dim3(256), 0, st, mp);
+    return launch_pdl(tree_merge_kernel<D, ROWS, 1>, dim3((unsigned)(groups * ((D / 16 + 7) / 8))),
+                      dim3(256), 0, st, mp);
+}
+
+cudaError_t launch_tree_merge(const MergeParams& mp, int head_dim, int rows, cudaStream_t st) {
+    if (rows == 256) return head_dim == 256 ? launch_merge<256, 256>(mp, st) : launch_merge<512, 256>(mp, st);
+    switch (head_dim) {
+        case 64: return launch_merge<64, 128>(mp, st);
+        case 128: return launch_merge<128, 128>(mp, st);
+        case 256: return launch_merge<256, 128>(mp, st);
+    }
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace gemma

@@ -12,10 +12,12 @@
 //    lengths, before the first barrier wait;
 //  - barriers, tensor memory and tensor maps are set up before the wait for the previous kernel;
 //  - S and P have two buffers each, so that S(t + 1) and P V(t - 1) run beside the softmax of t, and
-//    loads run ahead through the ring, into the next unit too;
+//    loads run ahead, into the next unit too;
 //  - a unit cut between CTAs leaves parts (O fp32 as it stands in tensor memory, four columns of all
-//    rows after another, so that stores are of 512 consecutive bytes) for tc_merge_kernel.
-// Warps: 0-3 softmax and epilogue, 4 TMA producer, 5 MMA issuer.
+//    rows after another, so that stores are of 512 consecutive bytes) for tree_merge_kernel.
+// Warps: 0-3 softmax and epilogue, 4 loads K and V, 6 loads Q (the wait for the last S of the part
+// before must not hold back the next part's keys), 5 issues S and 7 P V (one thread issuing both lost
+// 1000 of 2960 cycles per tile in its waits).
 #include <atomic>
 #include <climits>
 
@@ -29,7 +31,7 @@ namespace gemma {
 
 namespace {
 
-constexpr int kTcThreads = 192;
+constexpr int kTcThreads = 256;
 constexpr int kTcRows = 128;
 constexpr int kTcKeys = kTreeKeyTile;
 constexpr int kTcMaxSlots = 12;
@@ -50,14 +52,6 @@ struct TcLay {
     static_assert(SMEM <= 232448 && (2 * kTcMaxSlots + 13) * 8 + 4 <= 512, "shared memory budget");
 };
 
-struct TcParams {
-    TreeParams tp;
-    int batch, n_rt, workers;
-    float* part_o;    // [2 workers slots][D / 4][128 rows] x 4 columns
-    float2* part_ml;  // [2 workers slots][128 rows]
-    int32_t* before;  // [batch + 1] key tiles of earlier sequences, for the merge
-};
-
 // A unit, or a part of one.
 struct TcUnit {
     int b, kvh, rt;
@@ -73,66 +67,89 @@ GEMMA_DEVINL int tc_tiles(const RowsParams& p, const TrSeq& s, int& live_rt) {
     return live_rt ? (s.len - tr_start(p, s) + kTcKeys - 1) / kTcKeys : 0;
 }
 
-// A CTA's parts, in the order of (sequence, KV head, row tile, keys). Whole warps run it alike.
-struct TcShare {
-    int pos, end, begin, b, seq0, worker;  // seq0: tiles of the sequences before b
-    GEMMA_DEVINL void init(const TcParams& tp, bool write_before) {
-        const int lane = threadIdx.x & 31;
-        worker = blockIdx.x;
-        int total = 0, excl = 0;
-        for (int b0 = 0; b0 < tp.batch; b0 += 32) {
-            const int incl = scan(tp, b0, excl);
-            if (write_before && b0 + lane < tp.batch) tp.before[b0 + lane] = total + excl;
-            total += __shfl_sync(0xffffffffu, incl, 31);
-        }
-        if (write_before && lane == 0) tp.before[tp.batch] = total;
-        const int share = (total + tp.workers - 1) / tp.workers;
-        begin = pos = min(total, worker * share);
-        end = min(total, pos + share);
-        b = 0;
-        seq0 = 0;
-        int sum = 0;
-        for (int b0 = 0; b0 < tp.batch && pos < end; b0 += 32) {
-            const int incl = tp.batch > 32 || b0 ? scan(tp, b0, excl) : scan(tp, 0, excl);
-            // the last sequence whose tiles start at or before pos (and that has any behind it)
-            const unsigned in = __ballot_sync(0xffffffffu, sum + incl > pos);
-            if (in) {
-                const int l = __ffs(in) - 1;
-                b = b0 + l;
-                seq0 = sum + __shfl_sync(0xffffffffu, excl, l);
-                return;
-            }
-            sum += __shfl_sync(0xffffffffu, incl, 31);
+// Place in a ring: its slot, and how often the ring has been gone round.
+struct TcRing {
+    int slot = 0, use = 0;
+    GEMMA_DEVINL void step(int n) {
+        if (++slot == n) {
+            slot = 0;
+            ++use;
         }
     }
-    // inclusive (and exclusive) prefix sums of 32 sequences' tiles
-    static GEMMA_DEVINL int scan(const TcParams& tp, int b0, int& excl) {
-        const int lane = threadIdx.x & 31;
-        int n = 0;
-        if (b0 + lane < tp.batch) {
+};
+
+// A CTA's parts, in the order of (sequence, KV head, row tile, keys). Whole warps run it alike.
+// Units are not cut where they are at most as many as the CTAs and the longest alone takes no longer
+// than an equal share and the merge of its parts: kTcTileNs of a tile where memory does not hold it
+// up against kTcShareNs of one when all SMs load, and kTcMergeNs.
+constexpr int kTcTileNs = 900, kTcShareNs = 1630, kTcMergeNs = 6000;
+struct TcShare {
+    int pos, end, begin, b, seq0, worker;  // seq0: tiles (whole units) of the sequences before b
+    bool whole;
+    GEMMA_DEVINL void init(const MergeParams& tp, bool write_before) {
+        // lane l has the sequences l * per .. + per - 1: one round of loads for many of them
+        const RowsParams& p = tp.tp.p;
+        const int lane = threadIdx.x & 31, per = (tp.batch + 31) / 32;
+        const int b_lo = min(tp.batch, lane * per), b_hi = min(tp.batch, b_lo + per);
+        int n = 0, u = 0, longest = 0;
+#pragma unroll 4
+        for (int x = b_lo; x < b_hi; ++x) {
             int live_rt;
-            n = tc_tiles(tp.tp.p, tr_seq(tp.tp.p, b0 + lane), live_rt);
-            n *= live_rt * tp.tp.p.n_kv;
+            const int nt = tc_tiles(p, tr_seq(p, x), live_rt);
+            n += nt * live_rt * p.n_kv;
+            u += live_rt * p.n_kv;
+            longest = max(longest, nt);
         }
-        int incl = n;
+        int n_incl = n, u_incl = u;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += y;
+            const int y = __shfl_up_sync(0xffffffffu, n_incl, o),
+                      z = __shfl_up_sync(0xffffffffu, u_incl, o);
+            if (lane >= o) {
+                n_incl += y;
+                u_incl += z;
+            }
         }
-        excl = incl - n;
-        return incl;
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        const int total = __shfl_sync(0xffffffffu, n_incl, 31),
+                  units = __shfl_sync(0xffffffffu, u_incl, 31);
+        const int share = (total + tp.workers - 1) / tp.workers;
+        whole = units <= tp.workers &&
+                (long long)longest * kTcTileNs <= (long long)share * kTcShareNs + kTcMergeNs;
+        if (write_before) {
+            int sum = n_incl - n;
+            for (int x = b_lo; x < b_hi; ++x) {
+                tp.before[x] = sum;
+                int live_rt;
+                sum += tc_tiles(p, tr_seq(p, x), live_rt) * live_rt * p.n_kv;
+            }
+            if (lane == 0) {
+                tp.before[tp.batch] = total;
+                tp.before[tp.batch + 1] = whole;
+            }
+        }
+        worker = blockIdx.x;
+        const int all = whole ? units : total, step = whole ? 1 : share;
+        begin = pos = min(all, worker * step);
+        end = min(all, pos + step);
+        // next() goes on from the first sequence of the lane that holds pos
+        const int incl = whole ? u_incl : n_incl;
+        const unsigned in = __ballot_sync(0xffffffffu, incl > pos);
+        const int l = in ? __ffs(in) - 1 : 0;
+        b = l * per;
+        seq0 = __shfl_sync(0xffffffffu, whole ? u_incl - u : n_incl - n, l);
     }
-    GEMMA_DEVINL bool next(const TcParams& tp, TcUnit& U) {
+    GEMMA_DEVINL bool next(const MergeParams& tp, TcUnit& U) {
         if (pos >= end) return false;
         const RowsParams& p = tp.tp.p;
         for (;; ++b) {  // (sequences without tiles are passed over)
             U.sq = tr_seq(p, b);
             int live_rt;
-            const int nt = tc_tiles(p, U.sq, live_rt), all = nt * live_rt * p.n_kv;
+            const int nt = tc_tiles(p, U.sq, live_rt), unit = whole ? 1 : nt,
+                      all = unit * live_rt * p.n_kv;
             if (pos < seq0 + all) {
-                const int rel = pos - seq0, idx = rel / nt, t0 = rel - idx * nt;
-                const int t1 = min(nt, t0 + end - pos);
+                const int rel = pos - seq0, idx = whole ? rel : rel / nt, t0 = rel - idx * unit;
+                const int t1 = whole ? nt : min(nt, t0 + end - pos);
                 U.b = b;
                 U.kvh = idx / live_rt;
                 U.rt = idx - U.kvh * live_rt;
@@ -140,7 +157,7 @@ struct TcShare {
                 U.k_begin = tr_start(p, U.sq) + t0 * kTcKeys;
                 U.n_tiles = t1 - t0;
                 U.slot = t0 == 0 && t1 == nt ? -1 : 2 * worker + (pos != begin);
-                pos += t1 - t0;
+                pos += whole ? 1 : t1 - t0;
                 return true;
             }
             seq0 += all;
@@ -148,6 +165,12 @@ struct TcShare {
     }
 };
 
+// 32 bytes (a whole sector) from one thread; 32-byte aligned
+GEMMA_DEVINL void st_global_v8(void* dst, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
 GEMMA_DEVINL void prefetch_map(const CUtensorMap* m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
@@ -158,7 +181,7 @@ template <int D, bool SOFTCAP>
 __global__ void __launch_bounds__(kTcThreads, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap,
-                   const __grid_constant__ CUtensorMap qmap, const TcParams tp) {
+                   const __grid_constant__ CUtensorMap qmap, const MergeParams tp) {
     using Lay = TcLay<D>;
     constexpr int S = Lay::SLOTS;
     pdl_launch_dependents();
@@ -181,6 +204,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     uint32_t* tslot = reinterpret_cast<uint32_t*>(q_full + 12);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int nops = p.k_eq_v ? 1 : 2;
+    // Slots of K and of V of their own (K read as V: of both), so that an issuer sees every phase of the
+    // barriers it waits on: a parity wait two phases behind passes at once.
+    const int nk = nops == 2 ? (S + 1) / 2 : S, nv = S - nk;
 
     if (warp == 4) {
         if (lane == 0) {
@@ -218,139 +244,128 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
     if (warp == 4) {
         // ------------------------------------ TMA producer --------------------------------------
-        // K(0), V(0), K(1), ... into a ring of slots; each part's Q rows first, once the last S of
-        // the part before has read the buffer.
+        // K(0), V(0), K(1), ...
         TcUnit U;
         bool ok = true;
-        int L = 0, ord = 0;
+        TcRing rk, rv;
         while (share.next(tp, U)) {
             if (lane == 0) {
-                if (ord > 0 && ok) ok = mbar_wait(q_free, (ord - 1) & 1, p.err);
-                if (ok) {
-                    mbar_arrive_expect_tx(q_full, Lay::Q);
-#pragma unroll
-                    for (int j = 0; j < D / 64; ++j)  // (tokens past the bucket read 0)
-                        tma_load_4d(sQ + j * kTcQBox, &qmap, 64 * j, U.kvh * p.G,
-                                    U.rt * kTcRows / p.G, U.b, q_full);
-                }
                 for (int t = 0; t < U.n_tiles && ok; ++t) {
                     int row3 = 0, slot0 = 0;
                     if (!kv_place(p, U.b, U.kvh, U.k_begin + t * kTcKeys, row3, slot0)) {
                         report(p.err, GEMMA_DEVERR_PAGE);  // reads zeros
                         row3 = p.n_pages * p.n_kv;
                     }
-                    for (int v = 0; v < nops && ok; ++v, ++L) {
-                        const int s = L % S, use = L / S;
-                        if (use > 0) ok = mbar_wait(&empty[s], (use - 1) & 1, p.err);
+                    for (int v = 0; v < nops && ok; ++v) {
+                        TcRing& ring_v = v ? rv : rk;
+                        const int s = (v ? nk : 0) + ring_v.slot;
+                        if (ring_v.use > 0) ok = mbar_wait(&empty[s], (ring_v.use - 1) & 1, p.err);
                         if (!ok) break;
                         mbar_arrive_expect_tx(&full[s], Lay::SLOT);
 #pragma unroll
                         for (int j = 0; j < D / 64; ++j)
                             tma_load_3d(ring + s * Lay::SLOT + j * kTcBox, v ? &vmap : &kmap, 64 * j,
                                         slot0, row3, &full[s]);
+                        ring_v.step(v ? nv : nk);
                     }
                 }
             }
-            ++ord;
             __syncwarp();
         }
         if (lane == 0) {
             // what was loaded has been read before the CTA may exit
-            for (int k = 1; k <= S && k <= L && ok; ++k)
-                ok = mbar_wait(&empty[(L - k) % S], ((L - k) / S) & 1, p.err);
+            for (int s = 0; s < nk + nv && ok; ++s) {
+                const int uses = s < nk ? rk.use + (s < rk.slot) : rv.use + (s - nk < rv.slot);
+                if (uses > 0) ok = mbar_wait(&empty[s], (uses - 1) & 1, p.err);
+            }
         }
         __syncwarp();
-    } else if (warp == 5) {
-        // ------------------------------------- MMA issuer ---------------------------------------
-        // S(0), S(1), P V(0), S(2), P V(1), ...
+    } else if (warp == 6) {
+        // ------------------------------------- Q rows -------------------------------------------
+        // a part's, once the last S of the part before has read the buffer
+        TcUnit U;
+        bool ok = true;
+        int ord = 0;
+        for (; share.next(tp, U); ++ord) {
+            if (ord > 0 && ok) ok = mbar_wait(q_free, (ord - 1) & 1, p.err);
+            if (lane == 0 && ok) {
+                mbar_arrive_expect_tx(q_full, Lay::Q);
+#pragma unroll
+                for (int j = 0; j < D / 64; ++j)  // (tokens past the bucket read 0)
+                    tma_load_4d(sQ + j * kTcQBox, &qmap, 64 * j, U.kvh * p.G, U.rt * kTcRows / p.G,
+                                U.b, q_full);
+            }
+            __syncwarp();
+        }
+        if (ord > 0 && ok) mbar_wait(q_free, (ord - 1) & 1, p.err);  // (landed before the CTA exits)
+    } else if (warp == 5 || warp == 7) {
+        // ---------------------------- MMA issuers: S (5) and P V (7) ----------------------------
+        // An MMA is accepted only when the one before it is nearly done, so what an issuer spends
+        // in waits is lost to the tensor core unless another one issues meanwhile.
+        const bool is_s = warp == 5;
         const uint32_t id_s = idesc_bf16(128, kTcKeys, 0, 0), id_pv = idesc_bf16(128, D, 0, 1);
         const uint64_t qd = smem_desc_sw128(smem_u32(sQ), 0, 1024);
         bool ok = true;
-        struct Tile {
-            int key0, n_valid, n_head;
-            bool valid, first, last;
-        };
         TcUnit U;
-        U.n_tiles = 0;
-        int t = 0, ord = -1;
-        auto next = [&](Tile& x) {
-            if (t >= U.n_tiles) {
-                x.valid = share.next(tp, U);
-                if (!x.valid) return;
-                t = 0;
-                ++ord;
-            }
-            x.valid = true;
-            x.key0 = U.k_begin + t * kTcKeys;
-            x.n_valid = min(kTcKeys, U.sq.len - x.key0);
-            x.n_head = max(0, U.first - x.key0);
-            x.first = t == 0;
-            x.last = t == U.n_tiles - 1;
-            ++t;
-        };
-        Tile cur, prev;
-        prev.valid = false;
-        int T = 0, prev_ord = -1;
-        for (;; ++T) {
-            next(cur);
-            const int cur_ord = ord;
-            if (!cur.valid && !prev.valid) break;
-            if (cur.valid) {
-                const int L = T * nops, s = L % S, buf = T & 1;
-                if (ok) ok = mbar_wait(&full[s], (L / S) & 1, p.err);
-                if (cur.first && ok) ok = mbar_wait(q_full, cur_ord & 1, p.err);
-                if (T >= 2 && ok) ok = mbar_wait(&s_free[buf], ((T >> 1) - 1) & 1, p.err);
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint64_t kd = smem_desc_sw128(smem_u32(ring + s * Lay::SLOT), 0, 1024);
-#pragma unroll
-                    for (int j = 0; j < D / 64; ++j)
-#pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
-                            umma_ss(tmem + kTcS + 64 * buf,
-                                    qd + (uint64_t)((j * kTcQBox + ks * 32) >> 4),
-                                    kd + (uint64_t)((j * kTcBox + ks * 32) >> 4), id_s,
-                                    (j | ks) ? 1u : 0u);
-                    umma_commit(&s_full[buf]);
-                    if (nops == 2) umma_commit(&empty[s]);
-                    if (cur.last) umma_commit(q_free);
-                }
-                __syncwarp();
-            }
-            if (prev.valid) {
-                const int Tp = T - 1, L = Tp * nops + nops - 1, s = L % S, buf = Tp & 1;
-                if (ok) ok = mbar_wait(&full[s], (L / S) & 1, p.err);
+        int T = 0;  // tile of the share
+        TcRing rg;  // of K or of V
+        const int n_slots = is_s || nops == 1 ? nk : nv, slot0 = is_s || nops == 1 ? 0 : nk;
+        for (int ord = 0; share.next(tp, U); ++ord) {
+            for (int t = 0; t < U.n_tiles; ++t, ++T, rg.step(n_slots)) {
+                const bool last = t == U.n_tiles - 1;
+                const int s = slot0 + rg.slot, buf = T & 1;
                 uint8_t* tile = ring + s * Lay::SLOT;
-                if (prev.n_valid < kTcKeys || prev.n_head > 0) {
-                    // rows outside of the sequence's keys may hold anything: zeros
-                    for (int i = lane; i < kTcKeys * (D / 8); i += 32) {
-                        const int key = i / (D / 8), ch = i - key * (D / 8);
-                        if (key >= prev.n_valid || key < prev.n_head)
-                            *reinterpret_cast<uint4*>(tile + (ch >> 3) * kTcBox + key * 128 +
-                                                      (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
-                if (ok) ok = mbar_wait(&p_full[buf], (Tp >> 1) & 1, p.err);
-                if (prev.first && prev_ord > 0 && ok)
-                    ok = mbar_wait(o_free, (prev_ord - 1) & 1, p.err);
-                tc_fence_after();
-                if (lane == 0) {
-                    const uint64_t vd = smem_desc_sw128(smem_u32(tile), kTcBox, 1024);
+                if (is_s) {
+                    if (t == 0 && ok) ok = mbar_wait(q_full, ord & 1, p.err);
+                    if (T >= 2 && ok) ok = mbar_wait(&s_free[buf], ((T >> 1) - 1) & 1, p.err);
+                    if (ok) ok = mbar_wait(&full[s], rg.use & 1, p.err);
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint64_t kd = smem_desc_sw128(smem_u32(tile), 0, 1024);
 #pragma unroll
-                    for (int kk = 0; kk < kTcKeys / 16; ++kk)
-                        umma_ts(tmem + kTcO, tmem + kTcP + 32 * buf + 8 * kk,
-                                vd + (uint64_t)((kk * 2048) >> 4), id_pv,
-                                (prev.first && kk == 0) ? 0u : 1u);
-                    umma_commit(&pv_done[buf]);
-                    umma_commit(&empty[s]);
-                    if (prev.last) umma_commit(o_full);
+                        for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks)
+                                umma_ss(tmem + kTcS + 64 * buf,
+                                        qd + (uint64_t)((j * kTcQBox + ks * 32) >> 4),
+                                        kd + (uint64_t)((j * kTcBox + ks * 32) >> 4), id_s,
+                                        (j | ks) ? 1u : 0u);
+                        umma_commit(&s_full[buf]);
+                        if (nops == 2) umma_commit(&empty[s]);
+                        if (last) umma_commit(q_free);
+                    }
+                } else {
+                    const int key0 = U.k_begin + t * kTcKeys, n_valid = U.sq.len - key0,
+                              n_head = U.first - key0;
+                    if (ok) ok = mbar_wait(&full[s], rg.use & 1, p.err);
+                    if (n_valid < kTcKeys || n_head > 0) {
+                        // rows outside of the sequence's keys may hold anything: zeros
+                        for (int i = lane; i < kTcKeys * (D / 8); i += 32) {
+                            const int key = i / (D / 8), ch = i - key * (D / 8);
+                            if (key >= n_valid || key < n_head)
+                                *reinterpret_cast<uint4*>(tile + (ch >> 3) * kTcBox + key * 128 +
+                                                          (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (t == 0 && ord > 0 && ok) ok = mbar_wait(o_free, (ord - 1) & 1, p.err);
+                    if (ok) ok = mbar_wait(&p_full[buf], (T >> 1) & 1, p.err);
+                    tc_fence_after();
+                    if (lane == 0) {
+                        const uint64_t vd = smem_desc_sw128(smem_u32(tile), kTcBox, 1024);
+#pragma unroll
+                        for (int kk = 0; kk < kTcKeys / 16; ++kk)
+                            umma_ts(tmem + kTcO, tmem + kTcP + 32 * buf + 8 * kk,
+                                    vd + (uint64_t)((kk * 2048) >> 4), id_pv,
+                                    (t == 0 && kk == 0) ? 0u : 1u);
+                        umma_commit(&pv_done[buf]);
+                        umma_commit(&empty[s]);
+                        if (last) umma_commit(o_full);
+                    }
                 }
                 __syncwarp();
             }
-            prev = cur;
-            prev_ord = cur_ord;
         }
     } else {
         // -------------------------------- softmax and epilogue ----------------------------------
@@ -359,7 +374,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t tO = tmem + kTcO + lanes;
         bool ok = true;
         TcUnit U;
-        int T = 0, ord = 0, in_b = -1, in_rt = -1;
+        int T = 0, ord = 0, in_b = -1, in_rt = -1;  // T: tile of the share
         uint32_t anc[kTrWords];
         int lo = INT_MAX;
         for (; share.next(tp, U); ++ord) {
@@ -404,8 +419,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (idle) {  // P = 0 (both buffers keep it for the rest of the part)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s_free[buf]);
+                    // (not before the other warps have arrived for P(T - 2))
+                    if (T >= 2 && ok) ok = mbar_wait(&pv_done[buf], ((T >> 1) - 1) & 1, p.err);
                     if (t < 2) {
-                        if (T >= 2 && ok) ok = mbar_wait(&pv_done[buf], ((T >> 1) - 1) & 1, p.err);
                         tc_fence_after();
                         uint32_t z[32];
 #pragma unroll
@@ -519,6 +535,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             float4* part = reinterpret_cast<float4*>(tp.part_o) + (size_t)max(U.slot, 0) * (D / 4) * kTcRows + r;
             if (U.slot >= 0) tp.part_ml[(size_t)U.slot * kTcRows + r] = make_float2(m, l);
             const float inv = l == 0.f ? 0.f : 1.f / l;
+            const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
 #pragma unroll 1
             for (int j = 0; j < D / 32; ++j) {
                 uint32_t v[32];
@@ -537,35 +554,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             __uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
                             __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
                 } else if (r < n_rows) {
-                    uint4* dst = reinterpret_cast<uint4*>(out + j * 32);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t w4[4];
+                    for (int q = 0; q < 2; ++q) {
+                        uint32_t w8[8];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)  // (no keys: zeros, whatever the other rows' V holds)
-                            w4[e] = l == 0.f ? 0u
-                                             : pack_bf16(__uint_as_float(v[8 * q + 2 * e]) * inv,
-                                                         __uint_as_float(v[8 * q + 2 * e + 1]) * inv);
-                        dst[q] = make_uint4(w4[0], w4[1], w4[2], w4[3]);
+                        for (int e = 0; e < 8; ++e)  // (no keys: zeros, whatever the other rows' V holds)
+                            w8[e] = l == 0.f ? 0u
+                                             : pack_bf16(__uint_as_float(v[16 * q + 2 * e]) * inv,
+                                                         __uint_as_float(v[16 * q + 2 * e + 1]) * inv);
+                        if (wide) {
+                            st_global_v8(out + j * 32 + q * 16, w8);
+                        } else {
+                            uint4* dst = reinterpret_cast<uint4*>(out + j * 32 + q * 16);
+                            dst[0] = make_uint4(w8[0], w8[1], w8[2], w8[3]);
+                            dst[1] = make_uint4(w8[4], w8[5], w8[6], w8[7]);
+                        }
                     }
                 }
             }
         }
-        // zeros for row tiles without nodes
-        for (int x = blockIdx.x; x < tp.n_rt * tp.batch * p.n_kv; x += tp.workers) {
-            const int per = tp.n_rt * p.n_kv, b = x / per, kvh = x % per / tp.n_rt, rt = x % tp.n_rt;
-            const TrSeq sq = tr_seq(p, b);
-            if (!sq.bad && rt * kTcRows < sq.n * p.G) continue;
-            if (sq.bad && kvh == 0 && rt == 0 && threadIdx.x == 0) report(p.err, sq.bad);
-            const int n_rows = min(kTcRows, p.n_tok * p.G - rt * kTcRows);
-            for (int i = threadIdx.x; i < n_rows * (D / 8); i += 128) {
-                const int R = rt * kTcRows + i / (D / 8), tk = R / p.G;
-                reinterpret_cast<uint4*>(
-                    reinterpret_cast<__nv_bfloat16*>(p.out) +
-                    (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) *
-                        (size_t)D)[i % (D / 8)] = make_uint4(0u, 0u, 0u, 0u);
-            }
-        }
+        // the last commits have arrived before the CTA may exit
+        for (int x = max(0, T - 2); x < T && ok; ++x) ok = mbar_wait(&pv_done[x & 1], (x >> 1) & 1, p.err);
     }
     tc_fence_before();
     __syncthreads();
@@ -573,91 +582,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
-}
-
-// ---------------------------------------------------------------------------------------------
-// merge of the parts of every unit that more than one CTA took a share of,
-//   M = max_w m_w, out = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w
-// A lane per row and 16 columns: reads of 512 consecutive bytes, writes of whole sectors. WAYS warps
-// share out the parts (few units are cut into many) and meet in shared memory.
-// ---------------------------------------------------------------------------------------------
-template <int D, int WAYS>
-__global__ void __launch_bounds__(256) tc_merge_kernel(const TcParams tp) {
-    pdl_launch_dependents();
-    pdl_wait();  // the parts
-    constexpr int SLICES = 8 / WAYS, PER = D / (16 * SLICES) > 0 ? D / (16 * SLICES) : 1;
-    const RowsParams& p = tp.tp.p;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, way = warp % WAYS;
-    const int slice = (blockIdx.x % PER) * SLICES + warp / WAYS;
-    const int x = blockIdx.x / PER, group = x & 3, unit = x >> 2;
-    const int per = tp.n_rt * p.n_kv, b = unit / per, kvh = unit % per / tp.n_rt,
-              rt = unit % tp.n_rt;
-    const int rr = group * 32 + lane, R = rt * kTcRows + rr;
-    if (rt * kTcRows + group * 32 >= p.n_tok * p.G) return;
-    const TrSeq sq = tr_seq(p, b);
-    int live_rt;
-    const int nt = tc_tiles(p, sq, live_rt);
-    if (rt >= live_rt) return;  // zeros already
-    const int total = tp.before[tp.batch], share = (total + tp.workers - 1) / tp.workers;
-    const int f0 = tp.before[b] + (kvh * live_rt + rt) * nt, f1 = f0 + nt;
-    const int w0 = f0 / share, w1 = (f1 - 1) / share;
-    if (w0 == w1) return;  // a whole unit: written by its CTA
-    // CTA w's part is the first of its share but for one that began before the unit
-    auto part = [&](int w) { return (size_t)(2 * w + (w * share < f0)); };
-    float top = -INFINITY;
-#pragma unroll 4
-    for (int w = w0; w <= w1; ++w) top = fmaxf(top, tp.part_ml[part(w) * kTcRows + rr].x);
-    float acc[16], l = 0.f;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-    const bool some = slice < D / 16 && __any_sync(0xffffffffu, top != -INFINITY);
-    if (some) {
-#pragma unroll 2
-        for (int w = w0 + way; w <= w1; w += WAYS) {
-            const float2 ml = tp.part_ml[part(w) * kTcRows + rr];
-            const float4* src = reinterpret_cast<const float4*>(tp.part_o) +
-                                (part(w) * (D / 4) + 4 * slice) * kTcRows + rr;
-            const float e = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - top);
-            l = fmaf(e, ml.y, l);
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float4 o = __ldcs(src + q * kTcRows);
-                if (e == 0.f) continue;  // (O without keys may be NaN where V is)
-                acc[4 * q] = fmaf(e, o.x, acc[4 * q]);
-                acc[4 * q + 1] = fmaf(e, o.y, acc[4 * q + 1]);
-                acc[4 * q + 2] = fmaf(e, o.z, acc[4 * q + 2]);
-                acc[4 * q + 3] = fmaf(e, o.w, acc[4 * q + 3]);
-            }
-        }
-    }
-    if constexpr (WAYS > 1) {
-        __shared__ float s_acc[8][17][32];
-        if (way) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) s_acc[warp][e][lane] = acc[e];
-            s_acc[warp][16][lane] = l;
-        }
-        __syncthreads();
-        if (way) return;
-#pragma unroll
-        for (int k = 1; k < WAYS; ++k) {
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[e] += s_acc[warp + k][e][lane];
-            l += s_acc[warp + k][16][lane];
-        }
-    }
-    if (R >= p.n_tok * p.G || slice >= D / 16) return;
-    const float inv = 1.f / l;
-    uint32_t out[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e)  // (no keys: zeros, whatever the other rows' V holds)
-        out[e] = l == 0.f ? 0u : pack_bf16(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-    const int tk = R / p.G;
-    uint4* dst = reinterpret_cast<uint4*>(
-        reinterpret_cast<__nv_bfloat16*>(p.out) +
-        (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) * (size_t)D + slice * 16);
-    dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-    dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
 }
 
 // ---------------------------------------------------------------------------------------------
@@ -673,7 +597,7 @@ TcScratch tc_scratch(int head_dim, int batch, int workers) {
     const size_t rows = (size_t)2 * workers * kTcRows;
     s.ml_off = rows * head_dim * sizeof(float);
     s.before_off = s.ml_off + rows * sizeof(float2);
-    s.bytes = s.before_off + ((size_t)batch + 4) / 4 * 16;
+    s.bytes = s.before_off + ((size_t)batch + 8) / 4 * 16;
     return s;
 }
 
@@ -709,26 +633,21 @@ cudaError_t launch_tc(const TreeParams& tree, int batch, void* workspace, int wo
                                   (uint64_t)p.n_tok * p.n_q * D * 2};
     const uint32_t qbox[4] = {64, (uint32_t)p.G, (uint32_t)(kTcRows / p.G), 1};
     if (!encode_bf16_sw128(&qm, p.q, 4, qdims, qstrides, qbox)) return cudaErrorInvalidValue;
-    TcParams tp{};
+    MergeParams tp{};
     tp.tp = tree;
     tp.batch = batch;
     tp.n_rt = (p.n_tok * p.G + kTcRows - 1) / kTcRows;
     tp.workers = workers;
+    tp.keys = kTcKeys;
     const TcScratch ws = tc_scratch(D, batch, workers);
     uint8_t* base = static_cast<uint8_t*>(workspace);
     tp.part_o = reinterpret_cast<float*>(base);
     tp.part_ml = reinterpret_cast<float2*>(base + ws.ml_off);
     tp.before = reinterpret_cast<int32_t*>(base + ws.before_off);
     auto kernel = p.softcap > 0.f ? tree_tc_kernel<D, true> : tree_tc_kernel<D, false>;
-    const cudaError_t e = launch_pdl(kernel, dim3(workers), dim3(kTcThreads), Lay::SMEM, st, km, vm, qm, tp);
-    if (e != cudaSuccess) return e;
-    const int units = tp.n_rt * batch * p.n_kv;
-    // (parts per unit: about the CTAs over the units)
-    if (units * 4 < workers)
-        return launch_pdl(tc_merge_kernel<D, 8>, dim3((unsigned)(units * 4 * (D / 16))), dim3(256), 0,
-                          st, tp);
-    constexpr int PER = D / 128 > 0 ? D / 128 : 1;
-    return launch_pdl(tc_merge_kernel<D, 1>, dim3((unsigned)(units * 4 * PER)), dim3(256), 0, st, tp);
+    const cudaError_t e =
+        launch_pdl(kernel, dim3(workers), dim3(kTcThreads), Lay::SMEM, st, km, vm, qm, tp);
+    return e == cudaSuccess ? launch_tree_merge(tp, D, kTcRows, st) : e;
 }
 
 }  // namespace
