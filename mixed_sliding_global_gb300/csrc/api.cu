@@ -993,10 +993,11 @@ TreePlan tree_plan(int batch, int kind, int window, int n_q, int n_kv, int head_
     reach += T - 1;  // (rings and pages start at whole tiles)
     // equal shares: no more workers than tiles (which are counted in 32 bits)
     auto shares = [&](int path, long long row_tile, long long keys, long long most) {
+        const long long halves = path == kTreePair ? head_dim / 256 : 1;
         const long long tiles = (long long)batch * n_kv * ((rows + row_tile - 1) / row_tile) *
-                                ((reach + keys - 1) / keys);
+                                halves * ((reach + keys - 1) / keys);
         TreePlan pl{1, 1 << 30, 0, 0, path, (int)(tiles < most ? tiles : most)};
-        pl.ws_bytes = path == kTreePair ? gemma::tree_pair_workspace(head_dim, batch, pl.workers)
+        pl.ws_bytes = path == kTreePair ? gemma::tree_pair_workspace(batch, pl.workers)
                                         : gemma::tree_tc_workspace(head_dim, batch, pl.workers);
         if (tiles > (1ll << 30)) pl.workers = 0;
         return pl;
@@ -1004,7 +1005,7 @@ TreePlan tree_plan(int batch, int kind, int window, int n_q, int n_kv, int head_
     if (batch <= gemma::kTreePairMaxBatch) {
         TreePlan pl{};
         if (head_dim >= 256 && rows > (head_dim == 512 ? kTreePairRows512 : kTreePairRows))
-            pl = shares(kTreePair, 256, 128, n_sm / (head_dim / 128));
+            pl = shares(kTreePair, 256, 128, n_sm / 2);
         else if (head_dim <= 256 && rows > kTreeTcRows)
             pl = shares(kTreeTc, 128, 64, n_sm);
         if (pl.workers > 0) return pl;

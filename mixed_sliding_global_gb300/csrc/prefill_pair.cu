@@ -57,24 +57,11 @@
 // The key range of a unit is clamped to [first row's window start, last row's position] before
 // any load; rows of a V tile outside the range are zeroed in shared memory before they enter
 // P V (they may hold anything, NaN included).
-//
-// Drafted trees (mode kPrTree; definition in tree_attn.cu) run on the same warps: a unit's rows are
-// the nodes' query heads, its keys all keys of the sequence, and what differs is
-//  - the units are cut by keys: the key tiles of all units form one sequence, of which every worker
-//    takes an equal share (lengths are known on the device alone). A worker's first and last unit
-//    may be parts, whose O (fp32) and (m, l) go to the worker's two slots of the workspace for
-//    tree_merge_kernel; whole units are written as in the other modes;
-//  - the mask: prefix keys from the row's window start on, and behind them a 64-bit window of the
-//    row's ancestor set, walked up from its node at the start of a part;
-//  - a soft-cap goes through one exponential and one reciprocal (absolute error 2^-21 of the cap).
 #include <atomic>
-#include <climits>
 
 #include "attn_internal.h"
 #include "tc.cuh"
 #include "tmap.h"
-#include "tree.h"
-#include "tree_dev.cuh"
 
 namespace gemma {
 
@@ -85,7 +72,6 @@ constexpr int kPrThreads = kPrWarps * 32;
 constexpr int kPrProducerWarp = 8;
 constexpr int kPrSWarp = 9;     // S issuer (even CTA) / slot forwarder (odd CTA)
 constexpr int kPrPvWarp = 10;   // P V issuer (even CTA)
-constexpr int kPrQWarp = 11;    // trees: Q loads
 constexpr int kPrKeys = 128;                  // keys per tile (N of S)
 constexpr int kPrRows = 256;                  // rows per unit (M of the pair's MMAs)
 constexpr int kPrBox = 64 * 128;              // TMA box: 64 keys x 64 columns of bf16
@@ -96,8 +82,6 @@ constexpr int kPrStage = 2 * 128 * 64;        // epilogue: 2 groups x 128 rows x
 constexpr int kPrSmemLimit = 232448;          // max dynamic shared memory per block
 constexpr int kPrListMax = 512;               // units a padded bucket's work list holds
 constexpr float kPrLazyLog2 = 8.f;
-constexpr int kPrWords = kTreeMaxNodes / 32;
-enum { kPrPlain, kPrList, kPrTree };          // how units are dealt out
 constexpr int kPrSCol = 0, kPrPCol = 128, kPrOCol = 256;  // TMEM columns
 // H parts of head_dim (256 columns each): a cluster of H pairs. Shared memory: ring, Q,
 // staging, the partner pair's partial scores (H = 2: [2 groups][8 chunks][128 rows] x 16
@@ -117,10 +101,6 @@ struct PrLay {
     static constexpr int BAR_OFF = MX_OFF + (2 * 2 * 128 + 2 * 128) * 4;
     static constexpr int ULIST_OFF = BAR_OFF + 256;    // a padded bucket's work list
     static constexpr int SMEM = ULIST_OFF + (kPrListMax + 1) * 4 + 1024;  // + alignment slack
-    // trees: tiles before each sequence, ancestor sets [2 groups][128 rows] in the list's place
-    static constexpr int ANC_OFF = ULIST_OFF + (kTreePairMaxBatch + 4) * 4;
-    static constexpr int TREE_SMEM = ANC_OFF + 2 * 128 * kPrWords * 4 + 1024;
-    static_assert(ANC_OFF % 16 == 0 && TREE_SMEM <= kPrSmemLimit, "shared memory budget");
     static_assert(SMEM <= kPrSmemLimit, "shared memory budget");
 };
 
@@ -130,11 +110,6 @@ struct PrParams {
     int n_rt;      // 256-row tiles per (sequence, KV head)
     int n_units;   // n_rt * batch * n_kv
     int n_pairs;   // clusters walking the units (each of H pairs)
-    // trees
-    const int32_t* parents;  // [batch][n_tok]
-    float* part_o;           // [2 n_pairs slots][2][H][64][128 rows] x 4 columns
-    float2* part_ml;         // [2 n_pairs slots][2][H][128 rows]
-    int32_t* before;         // [batch + 1] key tiles of earlier sequences, for the merge
 };
 
 struct PrUnit {
@@ -145,7 +120,6 @@ struct PrUnit {
     bool bad, bad_real;
     int k_begin, k_end, n_tiles;
     int n_head;       // leading keys of the first tile before every row's window (aligned start)
-    int slot;         // trees: workspace slot of a part, -1: a whole unit
 };
 
 // Unit u: row tiles from the last (longest key ranges) to the first, then sequences, then KV
@@ -182,60 +156,6 @@ __device__ __forceinline__ PrUnit pr_unit(const PrParams& fp, int u) {
     return U;
 }
 
-// Trees: sequence b's tiles per unit and its units per KV head that have rows.
-__device__ __forceinline__ void pr_tree_seq(const RowsParams& p, int b, PrUnit& U, int& live_rt) {
-    U.b = b;
-    U.len = __ldg(p.seq_lens + b);
-    U.n_real = p.n_real ? __ldg(p.n_real + b) : p.n_tok;
-    U.bad_real = U.n_real < 0 || U.n_real > p.n_tok;
-    U.bad = U.bad_real || U.len < U.n_real || (!p.ring && U.len > p.cap) || U.len > p.max_seq_len;
-    live_rt = U.bad ? 0 : (U.n_real * p.G + kPrRows - 1) / kPrRows;
-    const int first = p.is_sliding ? max(0, U.len - U.n_real - p.window + 1) : 0;
-    U.k_begin = (p.ring || p.page_size) ? (first & ~63) : first;
-    U.k_end = U.len;
-    U.n_head = first - U.k_begin;
-    U.n_tiles = live_rt ? (U.k_end - U.k_begin + kPrKeys - 1) / kPrKeys : 0;
-}
-
-// Trees: a worker's parts, in the order of (sequence, KV head, row tile, keys).
-struct PrShare {
-    int pos, end, b, begin;
-    __device__ __forceinline__ void init(const PrParams& fp, int worker, const int* before) {
-        const int total = before[fp.batch];
-        const int share = (total + fp.n_pairs - 1) / fp.n_pairs;
-        begin = pos = min(total, worker * share);
-        end = min(total, pos + share);
-        int lo = 0, hi = fp.batch - 1;  // the last sequence whose tiles start at or before pos
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) / 2;
-            if (before[mid] <= pos) lo = mid;
-            else hi = mid - 1;
-        }
-        b = lo;
-    }
-    __device__ __forceinline__ bool next(const PrParams& fp, int worker, const int* before,
-                                         PrUnit& U) {
-        if (pos >= end) return false;
-        while (before[b + 1] <= pos) ++b;
-        const RowsParams& p = fp.p;
-        int live_rt;
-        pr_tree_seq(p, b, U, live_rt);
-        const int rel = pos - before[b], nt = U.n_tiles, idx = rel / nt, t0 = rel - idx * nt;
-        const int t1 = min(nt, t0 + end - pos);
-        U.kvh = idx / live_rt;
-        U.rt = idx - U.kvh * live_rt;
-        U.row0 = U.rt * kPrRows;
-        U.n_rows = min(kPrRows, p.n_tok * p.G - U.row0);
-        U.n_rows_real = min(kPrRows, U.n_real * p.G - U.row0);
-        U.slot = t0 == 0 && t1 == nt ? -1 : 2 * worker + (pos != begin);
-        if (t0) U.n_head = 0;
-        U.k_begin += t0 * kPrKeys;
-        U.n_tiles = t1 - t0;
-        pos += t1 - t0;
-        return true;
-    }
-};
-
 // One tile of the flat per-pair sequence, as the producer and the issuers see it.
 struct PrTile {
     bool valid, first, last;
@@ -247,36 +167,29 @@ struct PrTile {
     int row0;      // the unit's first row
 };
 
-// kPrList (a padded bucket): the units come from the work list in shared memory, entry j to
+// LIST (a padded bucket): the units come from the work list in shared memory, entry j to
 // worker j mod W, the units with key tiles first (so that pad rows' empty units take no
-// worker's turn); kPrPlain: worker w takes units w, w + W, w + 2W, ...; kPrTree: its share's parts
-// (list: the tiles before each sequence).
-template <int MODE>
+// worker's turn); otherwise worker w takes units w, w + W, w + 2W, ...
+template <bool LIST>
 struct PrTileIter {
     int u, stride, t, ord;
     const int* list;
-    PrShare share;
     PrUnit U;
     __device__ __forceinline__ void init(const PrParams& fp, int worker, const int* ulist) {
-        u = MODE == kPrTree ? worker : worker - fp.n_pairs;  // next() advances to the first unit
+        u = worker - fp.n_pairs;  // next() advances to the first unit
         stride = fp.n_pairs;
         list = ulist;
         t = 0;
         ord = -1;
         U.n_tiles = 0;
-        if constexpr (MODE == kPrTree) share.init(fp, worker, ulist);
     }
     __device__ __forceinline__ PrTile next(const PrParams& fp) {
         PrTile T;
         T.valid = false;
         while (t >= U.n_tiles) {
-            if constexpr (MODE == kPrTree) {
-                if (!share.next(fp, u, list, U)) return T;
-            } else {
-                u += stride;
-                if (u >= fp.n_units) return T;
-                U = pr_unit(fp, MODE == kPrList ? list[u] : u);
-            }
+            u += stride;
+            if (u >= fp.n_units) return T;
+            U = pr_unit(fp, LIST ? list[u] : u);
             t = 0;
             if (U.n_tiles > 0) ++ord;
         }
@@ -297,10 +210,10 @@ struct PrTileIter {
 
 }  // namespace
 
-// SOFTCAP: the soft-capped variant; MODE: a padded bucket's, dealing out its units from the work
-// list, or a tree's (separate instantiations, so that the plain kernel carries no code for either)
-template <int H, bool SOFTCAP, int MODE>
-__global__ void __launch_bounds__(kPrThreads + (MODE == kPrTree ? 32 : 0), 1)
+// SOFTCAP: the soft-capped variant; LIST: a padded bucket's, dealing out its units from the work
+// list (separate instantiations, so that the plain kernel carries no code for either)
+template <int H, bool SOFTCAP, bool LIST>
+__global__ void __launch_bounds__(kPrThreads, 1)
     prefill_pair_kernel(const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap,
                         const __grid_constant__ CUtensorMap qmap,
@@ -310,7 +223,6 @@ __global__ void __launch_bounds__(kPrThreads + (MODE == kPrTree ? 32 : 0), 1)
     using Lay = PrLay<H>;
     constexpr int D = Lay::D;
     constexpr int kPrSlots = Lay::SLOTS;
-    constexpr bool LIST = MODE == kPrList, TREE = MODE == kPrTree;
     const RowsParams& p = fp.p;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -374,35 +286,6 @@ __global__ void __launch_bounds__(kPrThreads + (MODE == kPrTree ? 32 : 0), 1)
     // a padded bucket's work list: every thread evaluates units, warp 0 lists those with key
     // tiles first (in order), then the others
     int* ulist = reinterpret_cast<int*>(smem + Lay::ULIST_OFF);
-    if constexpr (TREE) {
-        // tiles before each sequence: every sequence's own first, then sums, 32 at a time
-        for (int b = threadIdx.x; b < fp.batch; b += blockDim.x) {
-            PrUnit U;
-            int live_rt;
-            pr_tree_seq(p, b, U, live_rt);
-            ulist[b] = U.n_tiles * live_rt * p.n_kv;
-        }
-        __syncthreads();
-        if (warp == 1) {
-            int sum = 0;
-            for (int b0 = 0; b0 < fp.batch; b0 += 32) {
-                const int n = b0 + lane < fp.batch ? ulist[b0 + lane] : 0;
-                int incl = n;
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += y;
-                }
-                if (b0 + lane < fp.batch) ulist[b0 + lane] = sum + incl - n;
-                sum += __shfl_sync(0xffffffffu, incl, 31);
-            }
-            if (lane == 0) ulist[fp.batch] = sum;
-            __syncwarp();
-            if (blockIdx.x == 0)
-                for (int i = lane; i <= fp.batch + 1; i += 32)
-                    fp.before[i] = i <= fp.batch ? ulist[i] : 0;  // (units are cut)
-        }
-    }
     if constexpr (LIST) {
         for (int u = threadIdx.x; u < fp.n_units; u += blockDim.x)
             ulist[u] = pr_unit(fp, u).n_tiles > 0 ? 1 : 0;  // a flag first, then the entry
@@ -522,7 +405,7 @@ __global__ void __launch_bounds__(kPrThreads + (MODE == kPrTree ? 32 : 0), 1)
                     }
                 }
             };
-            PrTileIter<MODE> it;
+            PrTileIter<LIST> it;
             it.init(fp, worker, ulist);
             PrTile prev;
             prev.valid = false;
@@ -530,7 +413,7 @@ __global__ void __launch_bounds__(kPrThreads + (MODE == kPrTree ? 32 : 0), 1)
             for (;;) {
                 const PrTile cur = it.next(fp);
                 if (!cur.valid && !prev.valid) break;
-                if (!TREE && cur.valid && cur.first) {
+                if (cur.valid && cur.first) {
                     // (a barrier of its own: this thread runs tiles ahead of the S MMAs, and a
                     // parity wait must not be more than one phase ahead of the barrier)
                     if (cur.ord > 0 && ok) ok = mbar_wait(q_free, (cur.ord - 1) & 1, p.err);
@@ -555,28 +438,7 @@ __global__ void __launch_bounds__(kPrThreads + (MODE == kPrTree ? 32 : 0), 1)
                 for (int n = max(0, n_loads[v] - N); n < n_loads[v]; ++n)
                     if (ok) ok = mbar_wait(&empty[(v ? Lay::K_SLOTS : 0) + n % N], (n / N) & 1, p.err);
             }
-            if (!TREE && Tn > 0 && ok) ok = mbar_wait(q_free, it.ord & 1, p.err);
-        }
-    } else if (TREE && warp == kPrQWarp) {
-        // ----------------------------- trees: Q rows ---------------------------------------
-        // of a warp of their own: parts are short, and the wait for the last S of the part before
-        // must not hold back the next part's keys
-        if (lane == 0) {
-            PrShare share;
-            PrUnit U;
-            bool ok = true;
-            int ord = 0;
-            share.init(fp, worker, ulist);
-            for (; share.next(fp, worker, ulist, U); ++ord) {
-                if (ord > 0 && ok) ok = mbar_wait(q_free, (ord - 1) & 1, p.err);
-                mbar_arrive_expect_tx(q_full, kPrQBytes);
-                if (!ok) continue;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    tma_load_4d(sQ + j * kPrQBox, &qmap, 256 * (int)h + 64 * j, U.kvh * p.G,
-                                (U.row0 + 128 * (int)c) / p.G, U.b, q_full);
-            }
-            if (ord > 0 && ok) mbar_wait(q_free, (ord - 1) & 1, p.err);
+            if (Tn > 0 && ok) ok = mbar_wait(q_free, it.ord & 1, p.err);
         }
     } else if (c == 0 && (warp == kPrSWarp || warp == kPrPvWarp)) {
         // ------------------ MMA issuers: S (warp 9) and P V (warp 10) -----------------------
@@ -601,7 +463,7 @@ __global__ void __launch_bounds__(kPrThreads + (MODE == kPrTree ? 32 : 0), 1)
             if (ok) ok = mbar_wait(&pfull[s], ph, p.err);
             return s;
         };
-        PrTileIter<MODE> it;
+        PrTileIter<LIST> it;
         it.init(fp, worker, ulist);
         PrTile prev;
         prev.valid = false;
@@ -675,7 +537,7 @@ __global__ void __launch_bounds__(kPrThreads + (MODE == kPrTree ? 32 : 0), 1)
             __syncwarp();
         };
         const uint32_t q_pfull0 = map_to_peer(q_pfull, lead);
-        PrTileIter<MODE> it;
+        PrTileIter<LIST> it;
         it.init(fp, worker, ulist);
         PrTile prev;
         prev.valid = false;
@@ -733,78 +595,30 @@ __global__ void __launch_bounds__(kPrThreads + (MODE == kPrTree ? 32 : 0), 1)
                 report(p.err, U.bad_real ? GEMMA_DEVERR_N_REAL : GEMMA_DEVERR_SEQ_LEN);
         };
         int u = worker - fp.n_pairs;
-        PrShare share;
-        if constexpr (TREE) {
-            share.init(fp, worker, ulist);
-        }
         // finds the next unit with tiles (writing zeros for units without), or returns false
         auto next_tiled = [&](PrUnit& U) -> bool {
-            if constexpr (TREE) {
-                return share.next(fp, worker, ulist, U);
-            } else {
-                for (;;) {
-                    u += fp.n_pairs;
-                    if (u >= fp.n_units) return false;
-                    U = pr_unit(fp, LIST ? ulist[u] : u);
-                    if (U.n_tiles > 0) return true;
-                    zero_unit(U);
-                }
+            for (;;) {
+                u += fp.n_pairs;
+                if (u >= fp.n_units) return false;
+                U = pr_unit(fp, LIST ? ulist[u] : u);
+                if (U.n_tiles > 0) return true;
+                zero_unit(U);
             }
-        };
-
-        // Trees: the nodes that this thread's row of a unit attends (into anc), and the first prefix
-        // key that it does (tree_lo).
-        uint32_t* anc =
-            reinterpret_cast<uint32_t*>(smem + Lay::ANC_OFF) + (w * 128 + r) * kPrWords;
-        int tree_lo = INT_MAX;
-        auto tree_row = [&](const PrUnit& U) {
-            uint32_t set[kPrWords];
-            const int32_t* par = fp.parents + (size_t)U.b * p.n_tok;
-            bool bad = false;
-#pragma unroll
-            for (int k = 0; k < kPrWords; ++k) {
-                const int i = lane + 32 * k;
-                set[k] = 0;
-                if (i < U.n_real) {
-                    const int m = __ldg(par + i);
-                    bad |= m < -1 || m >= i;
-                }
-            }
-            bad = __any_sync(0xffffffffu, bad);  // the same in every warp: no row attends
-            if (bad && w == 0 && r == 0 && rank == 0) report(p.err, GEMMA_DEVERR_TREE);
-            tree_lo = INT_MAX;
-            if (r < real_here(U) && !bad) {
-                const int window = p.is_sliding ? p.window : INT_MAX;
-                int depth = 0;
-                for (int m = (U.row0 + 128 * (int)c + r) / p.G; m >= 0; m = __ldg(par + m), ++depth)
-                    if (depth < window) {
-#pragma unroll
-                        for (int k = 0; k < kPrWords; ++k)
-                            if (k == m >> 5) set[k] |= 1u << (m & 31);
-                    }
-                tree_lo = p.is_sliding ? max(0, U.len - U.n_real + depth - p.window) : 0;
-            }
-#pragma unroll
-            for (int k = 0; k < kPrWords; ++k) anc[k] = set[k];
         };
 
         PrUnit cur;
         if (next_tiled(cur)) {
-            if constexpr (TREE) tree_row(cur);
             int T_base = 0, ord = 0;
             for (;;) {
                 const int lo_pos = cur.len - cur.n_real;  // position of the unit's token 0
                 int lo = 1, hi = 0;
-                if constexpr (TREE) {
-                    lo = tree_lo;
-                    hi = lo_pos;  // the prefix
-                } else if (r < real_here(cur)) {
+                if (r < real_here(cur)) {
                     const int pos = lo_pos + (cur.row0 + 128 * (int)c + r) / p.G;
                     lo = p.is_sliding ? max(0, pos - p.window + 1) : 0;
                     hi = pos + 1;
                 }
                 // the next unit's Q rows towards L2 while this unit runs
-                if (MODE == kPrPlain && cur.n_tiles > 2) {
+                if (!LIST && cur.n_tiles > 2) {
                     const int u2 = u + fp.n_pairs;
                     if (u2 < fp.n_units) {
                         const PrUnit U2 = pr_unit(fp, u2);
@@ -889,13 +703,6 @@ __global__ void __launch_bounds__(kPrThreads + (MODE == kPrTree ? 32 : 0), 1)
 #pragma unroll
                         for (int e = 0; e < 64; e += 2) {
                             const float2 a = f32x2_split(mul_f32x2(f32x2(s[e], s[e + 1]), ci2));
-                            if constexpr (TREE) {  // 1 - 2 / (1 + exp(2 x))
-                                const float ex = fast_exp2(a.x * 2.885390081777927f),
-                                            ey = fast_exp2(a.y * 2.885390081777927f);
-                                s[e] = fmaf(-2.f * p.cap_log2, fast_rcp(1.f + ex), p.cap_log2);
-                                s[e + 1] = fmaf(-2.f * p.cap_log2, fast_rcp(1.f + ey), p.cap_log2);
-                                continue;
-                            }
                             const float2 o = f32x2_split(
                                 mul_f32x2(f32x2(fast_tanh(a.x), fast_tanh(a.y)), cl2));
                             s[e] = o.x;
@@ -905,23 +712,10 @@ __global__ void __launch_bounds__(kPrThreads + (MODE == kPrTree ? 32 : 0), 1)
                     }
                     const int kt0 = cur.k_begin + t * kPrKeys + 64 * w;
                     if (!(kt0 >= lo && kt0 + 64 <= hi)) {
-                        if constexpr (TREE) {
-                            uint32_t set[kPrWords];
 #pragma unroll
-                            for (int k = 0; k < kPrWords; ++k) set[k] = anc[k];
-                            const unsigned long long see = tr_window(set, kt0 - hi, lo - kt0);
-                            const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) {
-                                if (!((s0 >> e) & 1u)) s[e] = -INFINITY;
-                                if (!((s1 >> e) & 1u)) s[32 + e] = -INFINITY;
-                            }
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 64; ++e) {
-                                const int key = kt0 + e;
-                                if (key < lo || key >= hi) s[e] = -INFINITY;
-                            }
+                        for (int e = 0; e < 64; ++e) {
+                            const int key = kt0 + e;
+                            if (key < lo || key >= hi) s[e] = -INFINITY;
                         }
                     }
                     float mx8[8];
@@ -998,8 +792,6 @@ __global__ void __launch_bounds__(kPrThreads + (MODE == kPrTree ? 32 : 0), 1)
 
                 PrUnit nxt;
                 const bool more = next_tiled(nxt);
-                // (while the last P V runs)
-                if (TREE && more && (nxt.b != cur.b || nxt.row0 != cur.row0)) tree_row(nxt);
 
                 // ---- epilogue: O / l -> bf16 for this group's 128 columns ----
                 const int T_last = T_base + cur.n_tiles - 1;
@@ -1010,7 +802,6 @@ __global__ void __launch_bounds__(kPrThreads + (MODE == kPrTree ? 32 : 0), 1)
                 named_bar_sync(2, 256);
                 const float lt = l_w + lxs[(w ^ 1) * 128 + r];
                 const float inv = (cur.bad || !(lt > 0.f)) ? 0.f : 1.f / lt;
-                const bool none = TREE && lt == 0.f;  // zeros, whatever the other rows' V holds
                 const unsigned long long inv2 = f32x2(inv, inv);
                 // in slices of 32 columns: each thread converts its row's slice to bf16 into this
                 // group's staging rows (64 bytes each, 16-byte chunks placed as the 64-byte TMA
@@ -1019,34 +810,6 @@ __global__ void __launch_bounds__(kPrThreads + (MODE == kPrTree ? 32 : 0), 1)
                 // are not written), so no thread waits for global stores
                 const bool issuer_t = r == 0;
                 const int tk0 = (cur.row0 + 128 * (int)c) / p.G;
-                if (TREE && cur.slot >= 0) {
-                    // a part: O as it is, and (m, l). Four columns of all rows after another, so
-                    // that a warp's store is 512 consecutive bytes
-                    const size_t part = ((size_t)cur.slot * 2 + c) * H + h;  // of 128 rows
-                    float4* dst = reinterpret_cast<float4*>(fp.part_o) + (part * 64 + 32 * w) * 128 + r;
-                    if (w == 0) fp.part_ml[part * 128 + r] = make_float2(m, lt);
-#pragma unroll 1
-                    for (int sl = 0; sl < 4; ++sl) {
-                        uint32_t v[32];
-                        tmem_ld32(tOw + sl * 32, v);
-                        tmem_ld_wait();
-                        if (sl == 3) {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive_remote(o_free0);
-                        }
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            dst[(sl * 8 + q) * 128] = make_float4(
-                                __uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
-                                __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
-                    }
-                    if (!more) break;
-                    T_base += cur.n_tiles;
-                    cur = nxt;
-                    ++ord;
-                    continue;
-                }
 #pragma unroll 1
                 for (int sl = 0; sl < 4; ++sl) {
                     if (issuer_t) bulk_wait_read_all();  // the last slice's store has read `stage`
@@ -1067,7 +830,7 @@ __global__ void __launch_bounds__(kPrThreads + (MODE == kPrTree ? 32 : 0), 1)
                             const float2 o = f32x2_split(mul_f32x2(
                                 f32x2(__uint_as_float(v[8 * cc + 2 * q]), __uint_as_float(v[8 * cc + 2 * q + 1])),
                                 inv2));
-                            w4[q] = none ? 0u : pack_bf16(o.x, o.y);
+                            w4[q] = pack_bf16(o.x, o.y);
                         }
                         *reinterpret_cast<uint4*>(stage + r * 64 + ((cc ^ ((r >> 1) & 3)) * 16)) =
                             make_uint4(w4[0], w4[1], w4[2], w4[3]);
@@ -1097,23 +860,9 @@ __global__ void __launch_bounds__(kPrThreads + (MODE == kPrTree ? 32 : 0), 1)
     }
 }
 
-// Scratch of a tree launch on n clusters: parts, their (m, l), tiles before each sequence.
-struct PrTreeScratch {
-    size_t ml_off, before_off, bytes;
-};
-static PrTreeScratch pr_tree_scratch(int H, int n_clusters, int batch) {
-    const size_t rows = (size_t)2 * n_clusters * kPrRows;
-    PrTreeScratch s;
-    s.ml_off = rows * (256 * H) * sizeof(float);
-    s.before_off = s.ml_off + rows * H * sizeof(float2);
-    s.bytes = s.before_off + ((size_t)batch + 8) / 4 * 16;
-    return s;
-}
-
+// ---------------------------------------------------------------------------------------------
 template <int H>
-static cudaError_t launch_pair(const RowsParams& p, int batch, cudaStream_t st,
-                               const TreeParams* tree = nullptr, void* workspace = nullptr,
-                               int workers = 0) {
+static cudaError_t launch_pair(const RowsParams& p, int batch, cudaStream_t st) {
     using Lay = PrLay<H>;
     constexpr int D = Lay::D;
     CUtensorMap km, vm;
@@ -1159,20 +908,14 @@ static cudaError_t launch_pair(const RowsParams& p, int batch, cudaStream_t st,
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     if (n_clusters <= 0) {
-        cudaError_t e = cudaFuncSetAttribute(prefill_pair_kernel<H, false, kPrPlain>,
+        cudaError_t e = cudaFuncSetAttribute(prefill_pair_kernel<H, false, false>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(prefill_pair_kernel<H, true, kPrPlain>,
+            e = cudaFuncSetAttribute(prefill_pair_kernel<H, true, false>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
         if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(prefill_pair_kernel<H, false, kPrList>,
+            e = cudaFuncSetAttribute(prefill_pair_kernel<H, false, true>,
                                      cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(prefill_pair_kernel<H, false, kPrTree>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::TREE_SMEM);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(prefill_pair_kernel<H, true, kPrTree>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::TREE_SMEM);
         if (e != cudaSuccess) return e;
         int n_sm = 0;
         e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
@@ -1181,61 +924,27 @@ static cudaError_t launch_pair(const RowsParams& p, int batch, cudaStream_t st,
         cudaLaunchConfig_t occ = cfg;
         occ.gridDim = dim3(2 * H * n_clusters);
         int fit = 0;
-        e = cudaOccupancyMaxActiveClusters(&fit, prefill_pair_kernel<H, false, kPrPlain>, &occ);
+        e = cudaOccupancyMaxActiveClusters(&fit, prefill_pair_kernel<H, false, false>, &occ);
         if (e != cudaSuccess) return e;
         if (fit < 1) return cudaErrorInvalidConfiguration;
         if (fit < n_clusters) n_clusters = fit;
         if (dev >= 0 && dev < 64) clusters_fit[dev].store(n_clusters, std::memory_order_relaxed);
     }
-    PrParams fp{};
+    PrParams fp;
     fp.p = p;
     fp.batch = batch;
     fp.n_rt = (p.n_tok * p.G + kPrRows - 1) / kPrRows;
     fp.n_units = fp.n_rt * batch * p.n_kv;
     fp.n_pairs = fp.n_units < n_clusters ? fp.n_units : n_clusters;
-    if (tree) {
-        MergeParams mp{};
-        mp.tp = *tree;
-        mp.batch = batch;
-        mp.n_rt = fp.n_rt;
-        mp.workers = fp.n_pairs = workers < n_clusters ? workers : n_clusters;
-        mp.keys = kPrKeys;
-        const PrTreeScratch ws = pr_tree_scratch(H, fp.n_pairs, batch);
-        uint8_t* base = static_cast<uint8_t*>(workspace);
-        fp.parents = tree->parents;
-        mp.part_o = fp.part_o = reinterpret_cast<float*>(base);
-        mp.part_ml = fp.part_ml = reinterpret_cast<float2*>(base + ws.ml_off);
-        mp.before = fp.before = reinterpret_cast<int32_t*>(base + ws.before_off);
-        cfg.gridDim = dim3(2 * H * fp.n_pairs);
-        cfg.blockDim = dim3(kPrThreads + 32);
-        cfg.dynamicSmemBytes = Lay::TREE_SMEM;
-        const cudaError_t e =
-            p.softcap > 0.f
-                ? cudaLaunchKernelEx(&cfg, prefill_pair_kernel<H, true, kPrTree>, km, vm, qm, om, fp)
-                : cudaLaunchKernelEx(&cfg, prefill_pair_kernel<H, false, kPrTree>, km, vm, qm, om,
-                                     fp);
-        return e == cudaSuccess ? launch_tree_merge(mp, D, kPrRows, st) : e;
-    }
     cfg.gridDim = dim3(2 * H * fp.n_pairs);
     if (p.softcap > 0.f)
-        return cudaLaunchKernelEx(&cfg, prefill_pair_kernel<H, true, kPrPlain>, km, vm, qm, om, fp);
+        return cudaLaunchKernelEx(&cfg, prefill_pair_kernel<H, true, false>, km, vm, qm, om, fp);
     // a padded bucket deals out its units with key tiles first (the work list) where the units
     // of a row tile divide the workers evenly, so that the plain order would give a worker the
     // same sequences in every wave (elsewhere building the list costs more than it saves)
     if (p.n_real && fp.n_units <= kPrListMax && fp.n_pairs % (batch * p.n_kv) == 0)
-        return cudaLaunchKernelEx(&cfg, prefill_pair_kernel<H, false, kPrList>, km, vm, qm, om, fp);
-    return cudaLaunchKernelEx(&cfg, prefill_pair_kernel<H, false, kPrPlain>, km, vm, qm, om, fp);
-}
-
-size_t tree_pair_workspace(int head_dim, int batch, int workers) {
-    return pr_tree_scratch(head_dim / 256, workers, batch).bytes;
-}
-
-cudaError_t launch_tree_pair(const TreeParams& tp, int head_dim, int batch, void* workspace,
-                             int workers, cudaStream_t st) {
-    if (head_dim == 256) return launch_pair<1>(tp.p, batch, st, &tp, workspace, workers);
-    if (head_dim == 512) return launch_pair<2>(tp.p, batch, st, &tp, workspace, workers);
-    return cudaErrorInvalidValue;
+        return cudaLaunchKernelEx(&cfg, prefill_pair_kernel<H, false, true>, km, vm, qm, om, fp);
+    return cudaLaunchKernelEx(&cfg, prefill_pair_kernel<H, false, false>, km, vm, qm, om, fp);
 }
 
 cudaError_t launch_prefill_pair(const RowsParams& p, int head_dim, int batch, cudaStream_t st) {

@@ -41,10 +41,10 @@ cudaError_t launch_tree_merge(const MergeParams& mp, int head_dim, int rows, cud
 // CTAs of the bf16 launch that fit an SM.
 int tree_ctas_per_sm(int head_dim, int rows);
 
-// On CTA pairs (prefill_pair.cu), head_dim 256 and 512, any number of rows, at most
-// kTreePairMaxBatch sequences; the merge included. workers: clusters, as many as fit at most.
+// On CTA pairs (tree_pair.cu), head_dim 256 and 512, any number of rows, at most
+// kTreePairMaxBatch sequences; the merge included. workers: pairs, one per two SMs at most.
 constexpr int kTreePairMaxBatch = 1024;
-size_t tree_pair_workspace(int head_dim, int batch, int workers);
+size_t tree_pair_workspace(int batch, int workers);
 cudaError_t launch_tree_pair(const TreeParams& tp, int head_dim, int batch, void* workspace,
                              int workers, cudaStream_t st);
 

@@ -2,6 +2,10 @@
 // lengths and key range, a node's ancestors, and its scores.
 #pragma once
 
+#include <cuda.h>
+
+#include <climits>
+
 #include "common.cuh"
 #include "tree.h"
 
@@ -97,6 +101,228 @@ GEMMA_DEVINL float tr_score(const RowsParams& p, float dot) {
         return fmaf(-2.f * p.cap_log2, r, p.cap_log2);
     }
     return dot * p.scale_log2;
+}
+
+// A unit (one KV head of one sequence, a tile of ROWS rows, one of HALVES parts of head_dim), or a part
+// of its keys.
+struct TreeUnit {
+    int b, kvh, rt, half;
+    TrSeq sq;
+    int first;             // first key that a node may attend
+    int k_begin, n_tiles;  // the part's
+    int slot;              // workspace slot, -1: the whole unit
+};
+
+// A sequence's tiles of KEYS keys per unit, and its row tiles that have rows.
+template <int KEYS, int ROWS>
+GEMMA_DEVINL int tree_tiles(const RowsParams& p, const TrSeq& s, int& live_rt) {
+    live_rt = s.bad ? 0 : (s.n * p.G + ROWS - 1) / ROWS;
+    return live_rt ? (s.len - tr_start(p, s) + KEYS - 1) / KEYS : 0;
+}
+
+// Place in a ring of slots: the slot, and how often the ring has been gone round.
+struct TreeRing {
+    int slot = 0, use = 0;
+    GEMMA_DEVINL void step(int n) {
+        if (++slot == n) {
+            slot = 0;
+            ++use;
+        }
+    }
+};
+
+// A worker's parts: the key tiles of all units, in the order of (sequence, KV head, row tile, half,
+// keys), in equal shares. Whole warps run it alike, each by itself: lengths are known on the device
+// alone, and this way no warp waits for another. Units are not cut where they are at most as many as
+// the workers and the longest alone (tile_ns a tile) takes no longer than an equal share (share_ns a
+// tile, when every SM works) and the merge of its parts (merge_ns).
+template <int KEYS, int ROWS, int HALVES>
+struct TreeShare {
+    int pos, end, begin, b, seq0, worker;  // seq0: tiles (whole units) of the sequences before b
+    bool whole;
+    GEMMA_DEVINL void init(const MergeParams& mp, int worker_, bool write_before, int tile_ns,
+                           int share_ns, int merge_ns) {
+        // lane l has the sequences l * per .. + per - 1: one round of loads for many of them
+        const RowsParams& p = mp.tp.p;
+        const int lane = threadIdx.x & 31, per = (mp.batch + 31) / 32;
+        const int b_lo = min(mp.batch, lane * per), b_hi = min(mp.batch, b_lo + per);
+        int n = 0, u = 0, longest = 0;
+#pragma unroll 4
+        for (int x = b_lo; x < b_hi; ++x) {
+            int live_rt;
+            const int nt = tree_tiles<KEYS, ROWS>(p, tr_seq(p, x), live_rt);
+            n += nt * live_rt * p.n_kv * HALVES;
+            u += live_rt * p.n_kv * HALVES;
+            longest = max(longest, nt);
+        }
+        int n_incl = n, u_incl = u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, n_incl, o),
+                      z = __shfl_up_sync(0xffffffffu, u_incl, o);
+            if (lane >= o) {
+                n_incl += y;
+                u_incl += z;
+            }
+        }
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        const int total = __shfl_sync(0xffffffffu, n_incl, 31),
+                  units = __shfl_sync(0xffffffffu, u_incl, 31);
+        const int share = (total + mp.workers - 1) / mp.workers;
+        whole = units <= mp.workers &&
+                (long long)longest * tile_ns <= (long long)share * share_ns + merge_ns;
+        if (write_before) {
+            int sum = n_incl - n;
+            for (int x = b_lo; x < b_hi; ++x) {
+                mp.before[x] = sum;
+                int live_rt;
+                sum += tree_tiles<KEYS, ROWS>(p, tr_seq(p, x), live_rt) * live_rt * p.n_kv * HALVES;
+            }
+            if (lane == 0) {
+                mp.before[mp.batch] = total;
+                mp.before[mp.batch + 1] = whole;
+            }
+        }
+        worker = worker_;
+        const int all = whole ? units : total, step = whole ? 1 : share;
+        begin = pos = min(all, worker * step);
+        end = min(all, pos + step);
+        // next() goes on from the first sequence of the lane that holds pos
+        const int incl = whole ? u_incl : n_incl;
+        const unsigned in = __ballot_sync(0xffffffffu, incl > pos);
+        const int l = in ? __ffs(in) - 1 : 0;
+        b = l * per;
+        seq0 = __shfl_sync(0xffffffffu, whole ? u_incl - u : n_incl - n, l);
+    }
+    GEMMA_DEVINL bool next(const MergeParams& mp, TreeUnit& U) {
+        if (pos >= end) return false;
+        const RowsParams& p = mp.tp.p;
+        for (;; ++b) {  // (sequences without tiles are passed over)
+            U.sq = tr_seq(p, b);
+            int live_rt;
+            const int nt = tree_tiles<KEYS, ROWS>(p, U.sq, live_rt), unit = whole ? 1 : nt,
+                      all = unit * live_rt * p.n_kv * HALVES;
+            if (pos < seq0 + all) {
+                const int rel = pos - seq0, idx = whole ? rel : rel / nt, t0 = rel - idx * unit;
+                const int t1 = whole ? nt : min(nt, t0 + end - pos);
+                U.b = b;
+                U.half = idx % HALVES;
+                U.kvh = idx / HALVES / live_rt;
+                U.rt = idx / HALVES - U.kvh * live_rt;
+                U.first = tr_first(p, U.sq);
+                U.k_begin = tr_start(p, U.sq) + t0 * KEYS;
+                U.n_tiles = t1 - t0;
+                U.slot = t0 == 0 && t1 == nt ? -1 : 2 * worker + (pos != begin);
+                pos += whole ? 1 : t1 - t0;
+                return true;
+            }
+            seq0 += all;
+        }
+    }
+};
+
+// What a row attends: its ancestors, and the first prefix key. Whole warps; every warp of a sequence
+// finds a bad tree by itself.
+struct TreeRow {
+    uint32_t anc[kTrWords];
+    int lo;  // INT_MAX: the row attends nothing
+    GEMMA_DEVINL void find(const TreeParams& tp, const TreeUnit& U, int R, bool reports) {
+        const RowsParams& p = tp.p;
+        const int lane = threadIdx.x & 31;
+        const int32_t* par = tp.parents + (size_t)U.b * p.n_tok;
+        bool bad = false;
+#pragma unroll
+        for (int k = 0; k < kTrWords; ++k) {
+            const int i = lane + 32 * k;
+            anc[k] = 0;
+            if (i < U.sq.n) {
+                const int m = __ldg(par + i);
+                bad |= m < -1 || m >= i;
+            }
+        }
+        bad = __any_sync(0xffffffffu, bad);
+        if (bad && reports) report(p.err, GEMMA_DEVERR_TREE);
+        lo = INT_MAX;
+        if (R >= U.sq.n * p.G || bad) return;
+        const int window = p.is_sliding ? p.window : INT_MAX;
+        int depth = 0;
+        for (int m = R / p.G; m >= 0; m = __ldg(par + m), ++depth)
+            if (depth < window) {
+#pragma unroll
+                for (int k = 0; k < kTrWords; ++k)
+                    if (k == m >> 5) anc[k] |= 1u << (m & 31);
+            }
+        lo = p.is_sliding ? max(0, U.sq.base + depth - p.window) : 0;
+    }
+};
+
+// 32 bytes (a whole sector) from one thread; 32-byte aligned
+GEMMA_DEVINL void st_global_v8(void* dst, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+// 32 consecutive columns of a row of the output, O / l (zeros without keys, whatever the other rows' V
+// holds); wide: `out` is 32-byte aligned
+GEMMA_DEVINL void tree_store32(__nv_bfloat16* out, const uint32_t (&v)[32], float l, bool wide) {
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            w[e] = l == 0.f ? 0u
+                            : pack_bf16(__uint_as_float(v[16 * q + 2 * e]) * inv,
+                                        __uint_as_float(v[16 * q + 2 * e + 1]) * inv);
+        if (wide) {
+            st_global_v8(out + q * 16, w);
+        } else {
+            uint4* dst = reinterpret_cast<uint4*>(out + q * 16);
+            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+    }
+}
+// Maximum of 64 scores.
+GEMMA_DEVINL float tree_max64(const float (&s)[64]) {
+    float m[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = fmax3f(s[i], s[8 + i], s[16 + i]);
+#pragma unroll
+    for (int e = 24; e < 56; e += 16)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m[i] = fmax3f(m[i], s[e + i], s[e + 8 + i]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m[i] = fmaxf(m[i], s[56 + i]);
+    return fmax3f(fmax3f(m[0], m[1], m[2]), fmax3f(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
+}
+// P = 2^(s * scale + neg) of 64 scores as packed bf16; returns their sum, as rounded.
+GEMMA_DEVINL float tree_exp64(const float (&s)[64], float scale, float neg, uint32_t (&pw)[32]) {
+    const unsigned long long scale2 = f32x2(scale, scale), neg2 = f32x2(neg, neg);
+    unsigned long long sum[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+        const float2 x = f32x2_split(fma_f32x2(f32x2(s[2 * k], s[2 * k + 1]), scale2, neg2));
+        pw[k] = pack_bf16(fast_exp2(x.x), fast_exp2(x.y));
+        sum[k & 1] = add_f32x2(sum[k & 1], f32x2(__uint_as_float(pw[k] << 16),
+                                                 __uint_as_float(pw[k] & 0xffff0000u)));
+    }
+    const float2 a = f32x2_split(sum[0]), b = f32x2_split(sum[1]);
+    return (a.x + a.y) + (b.x + b.y);
+}
+// Keys that a row does not attend leave 64 scores: key 0 of them is kt0.
+GEMMA_DEVINL void tree_mask64(float (&s)[64], const TreeRow& row, int kt0, int base) {
+    if (kt0 >= row.lo && kt0 + 64 <= base) return;
+    const unsigned long long see = tr_window(row.anc, kt0 - base, row.lo - kt0);
+    const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+        if (!((s0 >> e) & 1u)) s[e] = -INFINITY;
+        if (!((s1 >> e) & 1u)) s[32 + e] = -INFINITY;
+    }
+}
+GEMMA_DEVINL void prefetch_map(const CUtensorMap* m) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }
 
 }  // namespace gemma

@@ -1,11 +1,10 @@
-// tree_merge.cu -- merge of the parts that the equal shares of tree_tc.cu and prefill_pair.cu leave of a
-// unit (one KV head of one sequence, a tile of rows):
+// tree_merge.cu -- merge of the parts that the equal shares of tree_tc.cu and tree_pair.cu leave of a
+// unit (one KV head of one sequence, a tile of rows, 256 columns at most):
 //   M = max_w m_w, out = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w
 // and zeros for row tiles without nodes. A lane has one row and 16 columns: parts lie with four columns
 // of 128 rows after another, so reads are of 512 consecutive bytes, and writes are whole sectors. WAYS
 // warps share out the parts (few units are cut into many) and meet in shared memory. Latency bound: one
-// pass, so that a warp waits for memory twice (lengths, parts). It takes 2.5 us of a step of 9 on nine
-// parts of 32 rows.
+// pass, so that a warp waits for memory twice (lengths, parts).
 #include "common.cuh"
 #include "tree.h"
 #include "tree_dev.cuh"
@@ -16,7 +15,7 @@ template <int D, int ROWS, int WAYS>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeParams mp) {
     pdl_launch_dependents();
     constexpr int COLS = D < 256 ? D : 256;            // of a piece: 128 rows x COLS
-    constexpr int C = ROWS / 128, H = D / COLS;        // pieces of a part
+    constexpr int C = ROWS / 128, HALVES = D / COLS;   // pieces of a part; parts of head_dim
     constexpr int SLICES = 8 / WAYS;                   // of 16 columns, per CTA
     constexpr int PER = (D / 16 + SLICES - 1) / SLICES, GROUPS = ROWS / 32;
     const RowsParams& p = mp.tp.p;
@@ -45,10 +44,11 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeParams mp) {
     if (whole) return;  // units were not cut
     const int nt = (sq.len - tr_start(p, sq) + mp.keys - 1) / mp.keys;
     const int share = (total + mp.workers - 1) / mp.workers;
-    const int f0 = first + (kvh * live_rt + rt) * nt, f1 = f0 + nt;
+    const int half = slice * 16 / COLS;
+    const int f0 = first + ((kvh * live_rt + rt) * HALVES + half) * nt, f1 = f0 + nt;
     const int w0 = f0 / share, w1 = (f1 - 1) / share;
     if (w0 == w1) return;  // a whole unit: written by its worker
-    const int c = rr >> 7, h = slice * 16 / COLS, r = rr & 127;
+    const int c = rr >> 7, r = rr & 127;
     float m = -INFINITY, l = 0.f, acc[16];
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e] = 0.f;
@@ -56,7 +56,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeParams mp) {
 #pragma unroll 2
         for (int w = w0 + way; w <= w1; w += WAYS) {
             // worker w's part is the first of its share but for one that began before the unit
-            const size_t piece = ((size_t)(2 * w + (w * share < f0)) * C + c) * H + h;
+            const size_t piece = (size_t)(2 * w + (w * share < f0)) * C + c;
             const float2 ml = mp.part_ml[piece * 128 + r];
             const float4* src = reinterpret_cast<const float4*>(mp.part_o) +
                                 (piece * (COLS / 4) + 4 * (slice % (COLS / 16))) * 128 + r;

@@ -19,7 +19,6 @@
 // before must not hold back the next part's keys), 5 issues S and 7 P V (one thread issuing both lost
 // 1000 of 2960 cycles per tile in its waits).
 #include <atomic>
-#include <climits>
 
 #include "common.cuh"
 #include "tc.cuh"
@@ -52,128 +51,10 @@ struct TcLay {
     static_assert(SMEM <= 232448 && (2 * kTcMaxSlots + 13) * 8 + 4 <= 512, "shared memory budget");
 };
 
-// A unit, or a part of one.
-struct TcUnit {
-    int b, kvh, rt;
-    TrSeq sq;
-    int first;             // first key that a node may attend
-    int k_begin, n_tiles;  // the part's
-    int slot;              // workspace slot, -1: the whole unit
-};
-
-// A sequence's tiles per unit, and its row tiles that have rows.
-GEMMA_DEVINL int tc_tiles(const RowsParams& p, const TrSeq& s, int& live_rt) {
-    live_rt = s.bad ? 0 : (s.n * p.G + kTcRows - 1) / kTcRows;
-    return live_rt ? (s.len - tr_start(p, s) + kTcKeys - 1) / kTcKeys : 0;
-}
-
-// Place in a ring: its slot, and how often the ring has been gone round.
-struct TcRing {
-    int slot = 0, use = 0;
-    GEMMA_DEVINL void step(int n) {
-        if (++slot == n) {
-            slot = 0;
-            ++use;
-        }
-    }
-};
-
-// A CTA's parts, in the order of (sequence, KV head, row tile, keys). Whole warps run it alike.
-// Units are not cut where they are at most as many as the CTAs and the longest alone takes no longer
-// than an equal share and the merge of its parts: kTcTileNs of a tile where memory does not hold it
-// up against kTcShareNs of one when all SMs load, and kTcMergeNs.
-constexpr int kTcTileNs = 900, kTcShareNs = 1630, kTcMergeNs = 6000;
-struct TcShare {
-    int pos, end, begin, b, seq0, worker;  // seq0: tiles (whole units) of the sequences before b
-    bool whole;
-    GEMMA_DEVINL void init(const MergeParams& tp, bool write_before) {
-        // lane l has the sequences l * per .. + per - 1: one round of loads for many of them
-        const RowsParams& p = tp.tp.p;
-        const int lane = threadIdx.x & 31, per = (tp.batch + 31) / 32;
-        const int b_lo = min(tp.batch, lane * per), b_hi = min(tp.batch, b_lo + per);
-        int n = 0, u = 0, longest = 0;
-#pragma unroll 4
-        for (int x = b_lo; x < b_hi; ++x) {
-            int live_rt;
-            const int nt = tc_tiles(p, tr_seq(p, x), live_rt);
-            n += nt * live_rt * p.n_kv;
-            u += live_rt * p.n_kv;
-            longest = max(longest, nt);
-        }
-        int n_incl = n, u_incl = u;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, n_incl, o),
-                      z = __shfl_up_sync(0xffffffffu, u_incl, o);
-            if (lane >= o) {
-                n_incl += y;
-                u_incl += z;
-            }
-        }
-        longest = __reduce_max_sync(0xffffffffu, longest);
-        const int total = __shfl_sync(0xffffffffu, n_incl, 31),
-                  units = __shfl_sync(0xffffffffu, u_incl, 31);
-        const int share = (total + tp.workers - 1) / tp.workers;
-        whole = units <= tp.workers &&
-                (long long)longest * kTcTileNs <= (long long)share * kTcShareNs + kTcMergeNs;
-        if (write_before) {
-            int sum = n_incl - n;
-            for (int x = b_lo; x < b_hi; ++x) {
-                tp.before[x] = sum;
-                int live_rt;
-                sum += tc_tiles(p, tr_seq(p, x), live_rt) * live_rt * p.n_kv;
-            }
-            if (lane == 0) {
-                tp.before[tp.batch] = total;
-                tp.before[tp.batch + 1] = whole;
-            }
-        }
-        worker = blockIdx.x;
-        const int all = whole ? units : total, step = whole ? 1 : share;
-        begin = pos = min(all, worker * step);
-        end = min(all, pos + step);
-        // next() goes on from the first sequence of the lane that holds pos
-        const int incl = whole ? u_incl : n_incl;
-        const unsigned in = __ballot_sync(0xffffffffu, incl > pos);
-        const int l = in ? __ffs(in) - 1 : 0;
-        b = l * per;
-        seq0 = __shfl_sync(0xffffffffu, whole ? u_incl - u : n_incl - n, l);
-    }
-    GEMMA_DEVINL bool next(const MergeParams& tp, TcUnit& U) {
-        if (pos >= end) return false;
-        const RowsParams& p = tp.tp.p;
-        for (;; ++b) {  // (sequences without tiles are passed over)
-            U.sq = tr_seq(p, b);
-            int live_rt;
-            const int nt = tc_tiles(p, U.sq, live_rt), unit = whole ? 1 : nt,
-                      all = unit * live_rt * p.n_kv;
-            if (pos < seq0 + all) {
-                const int rel = pos - seq0, idx = whole ? rel : rel / nt, t0 = rel - idx * unit;
-                const int t1 = whole ? nt : min(nt, t0 + end - pos);
-                U.b = b;
-                U.kvh = idx / live_rt;
-                U.rt = idx - U.kvh * live_rt;
-                U.first = tr_first(p, U.sq);
-                U.k_begin = tr_start(p, U.sq) + t0 * kTcKeys;
-                U.n_tiles = t1 - t0;
-                U.slot = t0 == 0 && t1 == nt ? -1 : 2 * worker + (pos != begin);
-                pos += whole ? 1 : t1 - t0;
-                return true;
-            }
-            seq0 += all;
-        }
-    }
-};
-
-// 32 bytes (a whole sector) from one thread; 32-byte aligned
-GEMMA_DEVINL void st_global_v8(void* dst, const uint32_t (&v)[8]) {
-    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(v[0]),
-                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
-GEMMA_DEVINL void prefetch_map(const CUtensorMap* m) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
-}
+using Share = TreeShare<kTcKeys, kTcRows, 1>;
+// Of a tile where memory does not hold it up, of one when all SMs load, and of the merge of parts:
+// what TreeShare weighs against each other.
+constexpr int kTcTileNs = 1150, kTcShareNs = 1630, kTcMergeNs = 6000;
 
 }  // namespace
 
@@ -239,15 +120,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tslot;
     pdl_wait();  // the previous kernel on the stream has completed
-    TcShare share;
-    share.init(tp, blockIdx.x == 0 && warp == 0);
+    Share share;
+    share.init(tp, blockIdx.x, blockIdx.x == 0 && warp == 0, kTcTileNs, kTcShareNs, kTcMergeNs);
 
     if (warp == 4) {
         // ------------------------------------ TMA producer --------------------------------------
         // K(0), V(0), K(1), ...
-        TcUnit U;
+        TreeUnit U;
         bool ok = true;
-        TcRing rk, rv;
+        TreeRing rk, rv;
         while (share.next(tp, U)) {
             if (lane == 0) {
                 for (int t = 0; t < U.n_tiles && ok; ++t) {
@@ -257,7 +138,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         row3 = p.n_pages * p.n_kv;
                     }
                     for (int v = 0; v < nops && ok; ++v) {
-                        TcRing& ring_v = v ? rv : rk;
+                        TreeRing& ring_v = v ? rv : rk;
                         const int s = (v ? nk : 0) + ring_v.slot;
                         if (ring_v.use > 0) ok = mbar_wait(&empty[s], (ring_v.use - 1) & 1, p.err);
                         if (!ok) break;
@@ -283,7 +164,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     } else if (warp == 6) {
         // ------------------------------------- Q rows -------------------------------------------
         // a part's, once the last S of the part before has read the buffer
-        TcUnit U;
+        TreeUnit U;
         bool ok = true;
         int ord = 0;
         for (; share.next(tp, U); ++ord) {
@@ -306,9 +187,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t id_s = idesc_bf16(128, kTcKeys, 0, 0), id_pv = idesc_bf16(128, D, 0, 1);
         const uint64_t qd = smem_desc_sw128(smem_u32(sQ), 0, 1024);
         bool ok = true;
-        TcUnit U;
+        TreeUnit U;
         int T = 0;  // tile of the share
-        TcRing rg;  // of K or of V
+        TreeRing rg;  // of K or of V
         const int n_slots = is_s || nops == 1 ? nk : nv, slot0 = is_s || nops == 1 ? 0 : nk;
         for (int ord = 0; share.next(tp, U); ++ord) {
             for (int t = 0; t < U.n_tiles; ++t, ++T, rg.step(n_slots)) {
@@ -373,44 +254,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const uint32_t lanes = (uint32_t)(32 * warp) << 16;
         const uint32_t tO = tmem + kTcO + lanes;
         bool ok = true;
-        TcUnit U;
+        TreeUnit U;
         int T = 0, ord = 0, in_b = -1, in_rt = -1;  // T: tile of the share
-        uint32_t anc[kTrWords];
-        int lo = INT_MAX;
+        TreeRow row;
         for (; share.next(tp, U); ++ord) {
             const int base = U.sq.base, R = U.rt * kTcRows + r;
-            if (U.b != in_b || U.rt != in_rt) {
-                // the nodes that this row attends, and its first prefix key (the same for the next
-                // KV head of the sequence)
+            if (U.b != in_b || U.rt != in_rt) {  // (the same for the next KV head of the sequence)
                 in_b = U.b;
                 in_rt = U.rt;
-                const int32_t* par = tp.tp.parents + (size_t)U.b * p.n_tok;
-                bool bad = false;
-#pragma unroll
-                for (int k = 0; k < kTrWords; ++k) {
-                    const int i = lane + 32 * k;
-                    anc[k] = 0;
-                    if (i < U.sq.n) {
-                        const int m = __ldg(par + i);
-                        bad |= m < -1 || m >= i;
-                    }
-                }
-                bad = __any_sync(0xffffffffu, bad);  // the same in every warp: no row attends
-                if (bad && threadIdx.x == 0) report(p.err, GEMMA_DEVERR_TREE);
-                lo = INT_MAX;
-                if (R < U.sq.n * p.G && !bad) {
-                    const int window = p.is_sliding ? p.window : INT_MAX;
-                    int depth = 0;
-                    for (int m = R / p.G; m >= 0; m = __ldg(par + m), ++depth)
-                        if (depth < window) {
-#pragma unroll
-                            for (int k = 0; k < kTrWords; ++k)
-                                if (k == m >> 5) anc[k] |= 1u << (m & 31);
-                        }
-                    lo = p.is_sliding ? max(0, base + depth - p.window) : 0;
-                }
+                row.find(tp.tp, U, R, threadIdx.x == 0);
             }
-            const bool idle = __all_sync(0xffffffffu, lo == INT_MAX);  // no row of the warp attends
+            const bool idle = __all_sync(0xffffffffu, row.lo == INT_MAX);  // no row of the warp attends
             float m = -INFINITY, l = 0.f;
             for (int t = 0; t < U.n_tiles; ++t, ++T) {
                 const int buf = T & 1;
@@ -455,27 +309,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     for (int e = 0; e < 64; ++e) s[e] = tr_score(p, s[e]);
                     sl2 = 1.f;
                 }
-                const int kt0 = U.k_begin + t * kTcKeys;
-                if (!(kt0 >= lo && kt0 + kTcKeys <= base)) {
-                    const unsigned long long see = tr_window(anc, kt0 - base, lo - kt0);
-                    const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        if (!((s0 >> e) & 1u)) s[e] = -INFINITY;
-                        if (!((s1 >> e) & 1u)) s[32 + e] = -INFINITY;
-                    }
-                }
-                float mx8[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) mx8[i] = fmax3f(s[i], s[8 + i], s[16 + i]);
-#pragma unroll
-                for (int e = 24; e < 56; e += 16)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) mx8[i] = fmax3f(mx8[i], s[e + i], s[e + 8 + i]);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) mx8[i] = fmaxf(mx8[i], s[56 + i]);
-                const float mx = fmax3f(fmax3f(mx8[0], mx8[1], mx8[2]), fmax3f(mx8[3], mx8[4], mx8[5]),
-                                        fmaxf(mx8[6], mx8[7])) * sl2;
+                tree_mask64(s, row, U.k_begin + t * kTcKeys, base);
+                const float mx = tree_max64(s) * sl2;
                 const float m_prev = m;
                 if (mx > m + kTrLazyLog2) {
                     l = m == -INFINITY ? 0.f : l * fast_exp2(m - mx);
@@ -500,21 +335,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     tmem_st_wait();
                 }
-                const float neg = m == -INFINITY ? 0.f : -m;
-                const unsigned long long sl2x2 = f32x2(sl2, sl2), neg2 = f32x2(neg, neg);
-                unsigned long long sum2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
                 uint32_t pw[32];
-#pragma unroll
-                for (int k = 0; k < 32; ++k) {
-                    const float2 x =
-                        f32x2_split(fma_f32x2(f32x2(s[2 * k], s[2 * k + 1]), sl2x2, neg2));
-                    pw[k] = pack_bf16(fast_exp2(x.x), fast_exp2(x.y));
-                    // (summed as rounded)
-                    sum2[k & 1] = add_f32x2(sum2[k & 1], f32x2(__uint_as_float(pw[k] << 16),
-                                                               __uint_as_float(pw[k] & 0xffff0000u)));
-                }
-                const float2 sa = f32x2_split(sum2[0]), sb = f32x2_split(sum2[1]);
-                l += (sa.x + sa.y) + (sb.x + sb.y);
+                l += tree_exp64(s, sl2, m == -INFINITY ? 0.f : -m, pw);
                 // the buffer is free once P V(T - 2) has completed
                 if (T >= 2 && ok) ok = mbar_wait(&pv_done[buf], ((T >> 1) - 1) & 1, p.err);
                 tc_fence_after();
@@ -534,7 +356,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 (((size_t)U.b * p.n_tok + tk) * p.n_q + U.kvh * p.G + (R - tk * p.G)) * (size_t)D;
             float4* part = reinterpret_cast<float4*>(tp.part_o) + (size_t)max(U.slot, 0) * (D / 4) * kTcRows + r;
             if (U.slot >= 0) tp.part_ml[(size_t)U.slot * kTcRows + r] = make_float2(m, l);
-            const float inv = l == 0.f ? 0.f : 1.f / l;
             const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
 #pragma unroll 1
             for (int j = 0; j < D / 32; ++j) {
@@ -554,22 +375,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             __uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1]),
                             __uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3]));
                 } else if (r < n_rows) {
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        uint32_t w8[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)  // (no keys: zeros, whatever the other rows' V holds)
-                            w8[e] = l == 0.f ? 0u
-                                             : pack_bf16(__uint_as_float(v[16 * q + 2 * e]) * inv,
-                                                         __uint_as_float(v[16 * q + 2 * e + 1]) * inv);
-                        if (wide) {
-                            st_global_v8(out + j * 32 + q * 16, w8);
-                        } else {
-                            uint4* dst = reinterpret_cast<uint4*>(out + j * 32 + q * 16);
-                            dst[0] = make_uint4(w8[0], w8[1], w8[2], w8[3]);
-                            dst[1] = make_uint4(w8[4], w8[5], w8[6], w8[7]);
-                        }
-                    }
+                    tree_store32(out + j * 32, v, l, wide);
                 }
             }
         }
