@@ -979,10 +979,14 @@ struct TreePlan {
     int n_split, chunk;
     size_t o_bytes, ws_bytes;
     int path;  // kTreeRows, or in equal shares of the key tiles on single SMs or on CTA pairs
-    int workers;
+    int workers, cluster;
 };
 enum { kTreeRows, kTreeTc, kTreePair };
-constexpr int kTreePairRows = GEMMA_TREE_PAIR_ROWS, kTreePairRows512 = 64, kTreeTcRows = GEMMA_TREE_TC_ROWS;
+constexpr int kTreePairRows = GEMMA_TREE_PAIR_ROWS, kTreePairRows512 = 32, kTreeTcRows = GEMMA_TREE_TC_ROWS;
+#ifndef GEMMA_TREE_MERGE_NS
+#define GEMMA_TREE_MERGE_NS 4500
+#endif
+constexpr long long kTreeMergeNs = GEMMA_TREE_MERGE_NS;
 TreePlan tree_plan(int batch, int kind, int window, int n_q, int n_kv, int head_dim,
                    int max_seq_len, int n_nodes, int n_sm) {
     const long long T = gemma::kTreeKeyTile;
@@ -996,7 +1000,7 @@ TreePlan tree_plan(int batch, int kind, int window, int n_q, int n_kv, int head_
         const long long halves = path == kTreePair ? head_dim / 256 : 1;
         const long long tiles = (long long)batch * n_kv * ((rows + row_tile - 1) / row_tile) *
                                 halves * ((reach + keys - 1) / keys);
-        TreePlan pl{1, 1 << 30, 0, 0, path, (int)(tiles < most ? tiles : most)};
+        TreePlan pl{1, 1 << 30, 0, 0, path, (int)(tiles < most ? tiles : most), 0};
         pl.ws_bytes = path == kTreePair ? gemma::tree_pair_workspace(batch, pl.workers)
                                         : gemma::tree_tc_workspace(head_dim, batch, pl.workers);
         if (tiles > (1ll << 30)) pl.workers = 0;
@@ -1006,14 +1010,28 @@ TreePlan tree_plan(int batch, int kind, int window, int n_q, int n_kv, int head_
         TreePlan pl{};
         if (head_dim >= 256 && rows > (head_dim == 512 ? kTreePairRows512 : kTreePairRows))
             pl = shares(kTreePair, 256, 128, n_sm / 2);
-        else if (head_dim <= 256 && rows > kTreeTcRows)
+        else if (head_dim <= 256 && rows > kTreeTcRows) {
             pl = shares(kTreeTc, 128, 64, n_sm);
+            // a cluster for each unit, where that ends no later (times in ns)
+            const long long u = (long long)batch * n_kv * ((rows + 127) / 128), nt = (reach + 63) / 64;
+            const long long tile_ns = 500 + 2 * head_dim;
+            const long long cluster_ns = 700 + (rows < 128 ? rows : 128) * head_dim * 16ll / 100;
+            long long best = (u * nt + n_sm - 1) / n_sm * tile_ns + kTreeMergeNs;
+            for (int c = 1; c <= kMaxClusterSplit && u * c <= n_sm; c *= 2) {
+                const long long t = (nt + c - 1) / c * tile_ns + (c > 1 ? cluster_ns : 0);
+                if (t <= best && (c == 1 || u <= gemma::tree_tc_clusters(head_dim, c))) {
+                    best = t;
+                    pl.cluster = c;
+                    pl.ws_bytes = 0;
+                }
+            }
+        }
         if (pl.workers > 0) return pl;
     }
     long long n = (long long)n_sm * gemma::tree_ctas_per_sm(head_dim, rows) / units;
     if (n > kMaxSplit) n = kMaxSplit;
     if (n < 1) n = 1;
-    TreePlan pl{1, 1 << 30, 0, 0, kTreeRows, 0};
+    TreePlan pl{1, 1 << 30, 0, 0, kTreeRows, 0, 0};
     const long long chunk = round_up((reach + n - 1) / n, T);
     n = (reach + chunk - 1) / chunk;
     if (n <= 1) return pl;
@@ -1140,7 +1158,7 @@ int gemma_attn_tree(void* out, const void* q, const void* const* k_cache,
     if (!bf16) {
         e = gemma::launch_tree_f32(tp, head_dim, batch, s);
     } else if (pl.path == kTreeTc) {
-        e = gemma::launch_tree_tc(tp, head_dim, batch, workspace, pl.workers, s);
+        e = gemma::launch_tree_tc(tp, head_dim, batch, workspace, pl.workers, pl.cluster, s);
     } else if (pl.path == kTreePair) {
         e = gemma::launch_tree_pair(tp, head_dim, batch, workspace, pl.workers, s);
     } else {

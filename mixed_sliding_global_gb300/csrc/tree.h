@@ -20,10 +20,12 @@ struct TreeParams {
 constexpr int tree_row_groups(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
 
 // On single SMs with tcgen05 (tree_tc.cu), head_dim 64 to 256, at most kTreePairMaxBatch sequences;
-// the merge included. workers: CTAs, one per SM at most.
+// the merge included. workers: CTAs, one per SM at most; or a cluster of 1 to 8 CTAs for each unit
+// (cluster > 0; no workspace).
+int tree_tc_clusters(int head_dim, int cluster);  // clusters of 2, 4 or 8 that run at once
 size_t tree_tc_workspace(int head_dim, int batch, int workers);
 cudaError_t launch_tree_tc(const TreeParams& tp, int head_dim, int batch, void* workspace,
-                           int workers, cudaStream_t st);
+                           int workers, int cluster, cudaStream_t st);
 
 // Parts of units cut into equal shares of the key tiles, and where they lie in the workspace. A worker
 // has two slots: for the part that its share begins with, and for the one that it ends with.

@@ -221,6 +221,38 @@ struct TreeShare {
     }
 };
 
+// One unit, or the part of its keys that CTA k of n takes: what a worker does where units are dealt out by
+// the host.
+template <int KEYS, int ROWS>
+struct TreeAlone {
+    TreeUnit U;
+    bool more;
+    GEMMA_DEVINL void init(const MergeParams& mp, int unit, int k, int n) {
+        const RowsParams& p = mp.tp.p;
+        const int per = mp.n_rt * p.n_kv;
+        U.b = unit / per;
+        U.kvh = unit % per / mp.n_rt;
+        U.rt = unit % mp.n_rt;
+        U.half = 0;
+        U.slot = -1;
+        U.sq = tr_seq(p, U.b);
+        int live_rt;
+        int nt = tree_tiles<KEYS, ROWS>(p, U.sq, live_rt);
+        if (U.rt >= live_rt) nt = 0;
+        const int t0 = nt * k / n;
+        U.first = tr_first(p, U.sq);
+        U.k_begin = tr_start(p, U.sq) + t0 * KEYS;
+        U.n_tiles = nt * (k + 1) / n - t0;
+        more = U.n_tiles > 0;
+    }
+    GEMMA_DEVINL bool next(const MergeParams&, TreeUnit& X) {
+        X = U;
+        const bool now = more;
+        more = false;
+        return now;
+    }
+};
+
 // What a row attends: its ancestors, and the first prefix key. Whole warps; every warp of a sequence
 // finds a bad tree by itself.
 struct TreeRow {

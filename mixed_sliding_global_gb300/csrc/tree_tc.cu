@@ -19,6 +19,7 @@
 // before must not hold back the next part's keys), 5 issues S and 7 P V (one thread issuing both lost
 // 1000 of 2960 cycles per tile in its waits).
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "tc.cuh"
@@ -34,6 +35,7 @@ constexpr int kTcThreads = 256;
 constexpr int kTcRows = 128;
 constexpr int kTcKeys = kTreeKeyTile;
 constexpr int kTcMaxSlots = 12;
+constexpr int kTcMaxCluster = 8;
 constexpr int kTcBox = kTcKeys * 128;  // 64 keys x 64 columns
 constexpr int kTcQBox = kTcRows * 128;
 // TMEM columns: O, S (two buffers), P (two buffers of packed bf16)
@@ -51,6 +53,17 @@ struct TcLay {
     static_assert(SMEM <= 232448 && (2 * kTcMaxSlots + 13) * 8 + 4 <= 512, "shared memory budget");
 };
 
+GEMMA_DEVINL float2 ld_cluster_f32x2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+GEMMA_DEVINL void st_cluster_f32x4(uint32_t addr, float a, float b, float c, float d) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c),
+                 "f"(d)
+                 : "memory");
+}
+
 using Share = TreeShare<kTcKeys, kTcRows, 1>;
 // Of a tile where memory does not hold it up, of one when all SMs load, and of the merge of parts:
 // what TreeShare weighs against each other.
@@ -58,7 +71,9 @@ constexpr int kTcTileNs = 1150, kTcShareNs = 1630, kTcMergeNs = 6000;
 
 }  // namespace
 
-template <int D, bool SOFTCAP>
+// CLUSTER: a unit to each cluster of tp.workers CTAs, which share out its key tiles and merge their
+// O through distributed shared memory (or, one CTA, write it): no second launch, no workspace
+template <int D, bool SOFTCAP, bool CLUSTER>
 __global__ void __launch_bounds__(kTcThreads, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap,
@@ -120,8 +135,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tslot;
     pdl_wait();  // the previous kernel on the stream has completed
-    Share share;
-    share.init(tp, blockIdx.x, blockIdx.x == 0 && warp == 0, kTcTileNs, kTcShareNs, kTcMergeNs);
+    const int n_cta = CLUSTER ? tp.workers : 1, cta = CLUSTER ? (int)cluster_rank() : 0;
+    std::conditional_t<CLUSTER, TreeAlone<kTcKeys, kTcRows>, Share> share;
+    if constexpr (CLUSTER)
+        share.init(tp, blockIdx.x / n_cta, cta, n_cta);
+    else
+        share.init(tp, blockIdx.x, blockIdx.x == 0 && warp == 0, kTcTileNs, kTcShareNs, kTcMergeNs);
+    // softmax warps: the row's reference and sum (of the last part)
+    float m = -INFINITY, l = 0.f;
 
     if (warp == 4) {
         // ------------------------------------ TMA producer --------------------------------------
@@ -265,7 +286,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 row.find(tp.tp, U, R, threadIdx.x == 0);
             }
             const bool idle = __all_sync(0xffffffffu, row.lo == INT_MAX);  // no row of the warp attends
-            float m = -INFINITY, l = 0.f;
+            m = -INFINITY;
+            l = 0.f;
             for (int t = 0; t < U.n_tiles; ++t, ++T) {
                 const int buf = T & 1;
                 if (ok) ok = mbar_wait(&s_full[buf], (T >> 1) & 1, p.err);
@@ -349,6 +371,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             // ---- the part's results ----
             if (ok) ok = mbar_wait(o_full, ord & 1, p.err);
             tc_fence_after();
+            if (CLUSTER && n_cta > 1) continue;
             const int n_rows = min(kTcRows, p.n_tok * p.G - U.rt * kTcRows);
             const int tk = R / p.G;
             __nv_bfloat16* out =
@@ -382,6 +405,92 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // the last commits have arrived before the CTA may exit
         for (int x = max(0, T - 2); x < T && ok; ++x) ok = mbar_wait(&pv_done[x & 1], (x >> 1) & 1, p.err);
     }
+    if constexpr (CLUSTER) {
+        // The CTAs of the cluster tell each other their rows' (m, l); then each scales its O by 2^(m - M)
+        // and sends every CTA its slice of the columns; then each adds up its slice. The buffers are the
+        // ring and the Q rows, which nobody reads any more behind the first barrier.
+        const TreeUnit& U = share.U;
+        const int r = threadIdx.x, R = U.rt * kTcRows + r;
+        const int n_rows = min(kTcRows, p.n_tok * p.G - U.rt * kTcRows), tk = R / p.G;
+        __nv_bfloat16* out =
+            reinterpret_cast<__nv_bfloat16*>(p.out) +
+            (((size_t)U.b * p.n_tok + tk) * p.n_q + U.kvh * p.G + (R - tk * p.G)) * (size_t)D;
+        if (U.sq.bad && U.kvh == 0 && U.rt == 0 && cta == 0 && r == 0) report(p.err, U.sq.bad);
+        if (n_cta == 1) {
+            if (U.n_tiles == 0 && r < n_rows)  // no nodes
+                for (int j = 0; j < D / 8; ++j)
+                    reinterpret_cast<uint4*>(out)[j] = make_uint4(0u, 0u, 0u, 0u);
+        } else {
+            const int lg = 31 - __clz(D / n_cta), slice = 1 << lg;  // columns (powers of two)
+            if (warp < 4) reinterpret_cast<float2*>(sQ)[r] = make_float2(m, l);
+            tc_fence_before();
+            cluster_sync();
+            tc_fence_after();
+            float L = 0.f;
+            uint32_t have = 0;  // CTAs that had keys of this row
+            if (warp < 4) {
+                float M = -INFINITY;
+                float2 ml[kTcMaxCluster];
+#pragma unroll
+                for (int k = 0; k < kTcMaxCluster; ++k)
+                    ml[k] = k < n_cta ? ld_cluster_f32x2(map_to_peer(sQ + 8 * r, k))
+                                      : make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int k = 0; k < kTcMaxCluster; ++k) M = fmaxf(M, ml[k].x);
+#pragma unroll
+                for (int k = 0; k < kTcMaxCluster; ++k) {
+                    if (ml[k].x == -INFINITY) continue;
+                    have |= 1u << k;
+                    L = fmaf(fast_exp2(ml[k].x - M), ml[k].y, L);
+                }
+                if (__any_sync(0xffffffffu, have >> cta & 1)) {
+                    const float w = m == -INFINITY ? 0.f : fast_exp2(m - M);
+                    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+#pragma unroll 1
+                    for (int j = 0; j < D / 32; ++j) {
+                        uint32_t v[32];
+                        tmem_ld32(tmem + kTcO + lanes + j * 32, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) {  // four columns: [source][slice / 4][row]
+                            const int col = j * 32 + 4 * q, to = col >> lg, c4 = (col & (slice - 1)) >> 2;
+                            st_cluster_f32x4(
+                                map_to_peer(ring + ((size_t)(cta * (slice / 4) + c4) * kTcRows + r) * 16, to),
+                                __uint_as_float(v[4 * q]) * w, __uint_as_float(v[4 * q + 1]) * w,
+                                __uint_as_float(v[4 * q + 2]) * w, __uint_as_float(v[4 * q + 3]) * w);
+                        }
+                    }
+                }
+            }
+            cluster_sync();
+            if (warp < 4 && r < n_rows) {
+                const float inv = 1.f / L;
+                for (int c8 = 0; c8 < slice / 8; ++c8) {
+                    float a[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) a[e] = 0.f;
+#pragma unroll
+                    for (int k = 0; k < kTcMaxCluster; ++k) {
+                        if (!(have >> k & 1)) continue;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float4 x = *reinterpret_cast<const float4*>(
+                                ring + ((size_t)(k * (slice / 4) + 2 * c8 + h) * kTcRows + r) * 16);
+                            a[4 * h] += x.x;
+                            a[4 * h + 1] += x.y;
+                            a[4 * h + 2] += x.z;
+                            a[4 * h + 3] += x.w;
+                        }
+                    }
+                    // (no keys: zeros)
+                    reinterpret_cast<uint4*>(out + cta * slice)[c8] =
+                        L == 0.f ? make_uint4(0u, 0u, 0u, 0u)
+                                 : make_uint4(pack_bf16(a[0] * inv, a[1] * inv), pack_bf16(a[2] * inv, a[3] * inv),
+                                              pack_bf16(a[4] * inv, a[5] * inv), pack_bf16(a[6] * inv, a[7] * inv));
+                }
+            }
+        }
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == 5) {
@@ -408,20 +517,23 @@ TcScratch tc_scratch(int head_dim, int batch, int workers) {
 }
 
 template <int D>
-cudaError_t launch_tc(const TreeParams& tree, int batch, void* workspace, int workers,
+cudaError_t launch_tc(const TreeParams& tree, int batch, void* workspace, int workers, int cluster,
                       cudaStream_t st) {
     using Lay = TcLay<D>;
     const RowsParams& p = tree.p;
+    using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, MergeParams);
+    const Kernel kernels[2][2] = {{tree_tc_kernel<D, false, false>, tree_tc_kernel<D, true, false>},
+                                  {tree_tc_kernel<D, false, true>, tree_tc_kernel<D, true, true>}};
     static std::atomic<bool> configured[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
     if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_relaxed)) {
-        cudaError_t e = cudaFuncSetAttribute(
-            tree_tc_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(tree_tc_kernel<D, true>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
-        if (e != cudaSuccess) return e;
+        for (const auto& row : kernels)
+            for (Kernel k : row) {
+                const cudaError_t e = cudaFuncSetAttribute(
+                    k, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
+                if (e != cudaSuccess) return e;
+            }
         if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_relaxed);
     }
     CUtensorMap km, vm, qm;
@@ -443,14 +555,31 @@ cudaError_t launch_tc(const TreeParams& tree, int batch, void* workspace, int wo
     tp.tp = tree;
     tp.batch = batch;
     tp.n_rt = (p.n_tok * p.G + kTcRows - 1) / kTcRows;
-    tp.workers = workers;
+    tp.workers = cluster ? cluster : workers;
     tp.keys = kTcKeys;
+    const Kernel kernel = kernels[cluster > 0][p.softcap > 0.f];
+    if (cluster) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(tp.n_rt * batch * p.n_kv * cluster));
+        cfg.blockDim = dim3(kTcThreads);
+        cfg.dynamicSmemBytes = Lay::SMEM;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)cluster;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see pdl_wait
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, kernel, km, vm, qm, tp);
+    }
     const TcScratch ws = tc_scratch(D, batch, workers);
     uint8_t* base = static_cast<uint8_t*>(workspace);
     tp.part_o = reinterpret_cast<float*>(base);
     tp.part_ml = reinterpret_cast<float2*>(base + ws.ml_off);
     tp.before = reinterpret_cast<int32_t*>(base + ws.before_off);
-    auto kernel = p.softcap > 0.f ? tree_tc_kernel<D, true> : tree_tc_kernel<D, false>;
     const cudaError_t e =
         launch_pdl(kernel, dim3(workers), dim3(kTcThreads), Lay::SMEM, st, km, vm, qm, tp);
     return e == cudaSuccess ? launch_tree_merge(tp, D, kTcRows, st) : e;
@@ -458,16 +587,55 @@ cudaError_t launch_tc(const TreeParams& tree, int batch, void* workspace, int wo
 
 }  // namespace
 
+template <int D>
+static int clusters_fit(int cluster) {
+    static std::atomic<int> cache[64][4];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    const int i = cluster == 2 ? 1 : cluster == 4 ? 2 : 3;
+    if (dev >= 0 && dev < 64) {
+        const int n = cache[dev][i].load(std::memory_order_relaxed);
+        if (n > 0) return n;
+    }
+    if (cudaFuncSetAttribute(tree_tc_kernel<D, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             TcLay<D>::SMEM) != cudaSuccess)
+        return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cluster * 64);
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = TcLay<D>::SMEM;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)cluster;
+    attr.val.clusterDim.y = 1;
+    attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, tree_tc_kernel<D, false, true>, &cfg) != cudaSuccess) return 0;
+    if (dev >= 0 && dev < 64) cache[dev][i].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+int tree_tc_clusters(int head_dim, int cluster) {
+    switch (head_dim) {
+        case 64: return clusters_fit<64>(cluster);
+        case 128: return clusters_fit<128>(cluster);
+        case 256: return clusters_fit<256>(cluster);
+    }
+    return 0;
+}
+
 size_t tree_tc_workspace(int head_dim, int batch, int workers) {
     return tc_scratch(head_dim, batch, workers).bytes;
 }
 
 cudaError_t launch_tree_tc(const TreeParams& tp, int head_dim, int batch, void* workspace,
-                           int workers, cudaStream_t st) {
+                           int workers, int cluster, cudaStream_t st) {
     switch (head_dim) {
-        case 64: return launch_tc<64>(tp, batch, workspace, workers, st);
-        case 128: return launch_tc<128>(tp, batch, workspace, workers, st);
-        case 256: return launch_tc<256>(tp, batch, workspace, workers, st);
+        case 64: return launch_tc<64>(tp, batch, workspace, workers, cluster, st);
+        case 128: return launch_tc<128>(tp, batch, workspace, workers, cluster, st);
+        case 256: return launch_tc<256>(tp, batch, workspace, workers, cluster, st);
     }
     return cudaErrorInvalidValue;
 }
