@@ -15,6 +15,7 @@ template <int D, int ROWS, int WAYS>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeParams mp) {
     pdl_launch_dependents();
     constexpr int COLS = D < 256 ? D : 256;            // of a piece: 128 rows x COLS
+    constexpr int BATCH = WAYS > 4 ? 4 : 2;            // parts in flight per warp
     constexpr int C = ROWS / 128, HALVES = D / COLS;   // pieces of a part; parts of head_dim
     constexpr int SLICES = 8 / WAYS;                   // of 16 columns, per CTA
     constexpr int PER = (D / 16 + SLICES - 1) / SLICES, GROUPS = ROWS / 32;
@@ -53,26 +54,42 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeParams mp) {
 #pragma unroll
     for (int e = 0; e < 16; ++e) acc[e] = 0.f;
     if (slice < D / 16) {
-#pragma unroll 2
-        for (int w = w0 + way; w <= w1; w += WAYS) {
-            // worker w's part is the first of its share but for one that began before the unit
-            const size_t piece = (size_t)(2 * w + (w * share < f0)) * C + c;
-            const float2 ml = mp.part_ml[piece * 128 + r];
-            const float4* src = reinterpret_cast<const float4*>(mp.part_o) +
-                                (piece * (COLS / 4) + 4 * (slice % (COLS / 16))) * 128 + r;
-            float4 o[4];
+        for (int wb = w0 + way; wb <= w1; wb += BATCH * WAYS) {
+            float2 ml[BATCH];
+            float4 o[BATCH][4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) o[q] = __ldcs(src + q * 128);
-            if (ml.x == -INFINITY) continue;  // (no keys: O is nothing, or NaN where V is)
-            const float top = fmaxf(m, ml.x), a = fast_exp2(m - top), e = fast_exp2(ml.x - top);
+            for (int i = 0; i < BATCH; ++i) {
+                const int w = wb + i * WAYS;
+                // worker w's part is the first of its share but for one that began before the unit
+                const size_t piece = (size_t)(2 * w + (w * share < f0)) * C + c;
+                const float4* src = reinterpret_cast<const float4*>(mp.part_o) +
+                                    (piece * (COLS / 4) + 4 * (slice % (COLS / 16))) * 128 + r;
+                ml[i] = w <= w1 ? mp.part_ml[piece * 128 + r] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    o[i][q] = w <= w1 ? __ldcs(src + q * 128) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            float top = m;
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) top = fmaxf(top, ml[i].x);
+            if (top == -INFINITY) continue;
+            const float a = fast_exp2(m - top);  // 0 while there was nothing
             m = top;
-            l = fmaf(l, a, e * ml.y);
+            l *= a;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                acc[4 * q] = fmaf(acc[4 * q], a, e * o[q].x);
-                acc[4 * q + 1] = fmaf(acc[4 * q + 1], a, e * o[q].y);
-                acc[4 * q + 2] = fmaf(acc[4 * q + 2], a, e * o[q].z);
-                acc[4 * q + 3] = fmaf(acc[4 * q + 3], a, e * o[q].w);
+            for (int e = 0; e < 16; ++e) acc[e] *= a;
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                if (ml[i].x == -INFINITY) continue;  // (no keys: O is nothing, or NaN where V is)
+                const float e = fast_exp2(ml[i].x - top);
+                l = fmaf(e, ml[i].y, l);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    acc[4 * q] = fmaf(e, o[i][q].x, acc[4 * q]);
+                    acc[4 * q + 1] = fmaf(e, o[i][q].y, acc[4 * q + 1]);
+                    acc[4 * q + 2] = fmaf(e, o[i][q].z, acc[4 * q + 2]);
+                    acc[4 * q + 3] = fmaf(e, o[i][q].w, acc[4 * q + 3]);
+                }
             }
         }
     }
@@ -114,12 +131,17 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeParams mp) {
 template <int D, int ROWS>
 static cudaError_t launch_merge(const MergeParams& mp, cudaStream_t st) {
     const long long groups = (long long)mp.n_rt * mp.batch * mp.tp.p.n_kv * (ROWS / 32);
-    // (parts per unit: about the workers over the units)
-    if ((long long)mp.n_rt * mp.batch * mp.tp.p.n_kv * 4 < mp.workers)
-        return launch_pdl(tree_merge_kernel<D, ROWS, 8>, dim3((unsigned)(groups * (D / 16))),
-                          dim3(256), 0, st, mp);
-    return launch_pdl(tree_merge_kernel<D, ROWS, 1>, dim3((unsigned)(groups * ((D / 16 + 7) / 8))),
-                      dim3(256), 0, st, mp);
+    // Parts per unit, about. In us of the whole step with 1 / 4 / 8 warps to a row and slice: 6 parts
+    // (14 units of 244 rows, head_dim 256) 43.2 / 42.7 / 50.7, 19 parts (one tree of 512 rows, head_dim 512) 23.3 / 23.0 / 24.3, 64 parts (one
+    // unit of 32 rows, head_dim 64) 13.5 / - / 9.4.
+    const long long parts = mp.workers / ((long long)mp.n_rt * mp.batch * mp.tp.p.n_kv * (D > 256 ? 2 : 1));
+    auto launch = [&](auto kernel, int slices) {
+        return launch_pdl(kernel, dim3((unsigned)(groups * ((D / 16 + slices - 1) / slices))), dim3(256),
+                          0, st, mp);
+    };
+    if (parts < 4) return launch(tree_merge_kernel<D, ROWS, 1>, 8);
+    if (parts < 24) return launch(tree_merge_kernel<D, ROWS, 4>, 2);
+    return launch(tree_merge_kernel<D, ROWS, 8>, 1);
 }
 
 cudaError_t launch_tree_merge(const MergeParams& mp, int head_dim, int rows, cudaStream_t st) {
