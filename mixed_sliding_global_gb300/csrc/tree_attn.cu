@@ -817,21 +817,26 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeParams tp, 
 }
 
 // ---------------------------------------------------------------------------------------------
-// fp32 (debug path): one CTA per row, its warps share out the keys four at a time, FFMA and expf
+// fp32 (debug path): FFMA and expf
 // ---------------------------------------------------------------------------------------------
+// One CTA per row. A key belongs to D / 16 lanes, 16 columns each, so that its dot product takes two to
+// five shuffles; the lanes of a key are one of the CTA's streams, each with its own softmax over every
+// n-th key, and the streams meet in shared memory. Latency bound on a few hundred keys: the rows of a
+// stream's next key are on their way while it works on one (17 nodes x 4 heads, 700 keys, head_dim 128:
+// 28 us with a warp per key and five shuffles for each).
 constexpr int kTrF32Warps = 8;
 
 template <int D>
 __global__ void __launch_bounds__(kTrF32Warps * 32) tree_f32_kernel(const TreeParams tp) {
     pdl_launch_dependents();
     pdl_wait();  // the previous kernel on the stream has completed
-    constexpr int E = D / 32, U = D >= 512 ? 2 : 4;  // keys of a step
+    constexpr int LPK = D / 16, STREAMS = kTrF32Warps * 32 / LPK;
     const RowsParams& p = tp.p;
     __shared__ int s_par[kTreeMaxNodes];
     __shared__ uint32_t s_set[kTrWords];
     __shared__ int s_depth;
-    __shared__ float s_m[kTrF32Warps], s_l[kTrF32Warps], s_o[kTrF32Warps][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ __align__(16) float s_o[STREAMS][D];
+    __shared__ float s_m[STREAMS], s_l[STREAMS];
     const int head = blockIdx.x % p.n_q, node = blockIdx.x / p.n_q, b = blockIdx.y;
     const int kvh = head / p.G;
     const TrSeq sq = tr_seq(p, b);
@@ -858,92 +863,101 @@ __global__ void __launch_bounds__(kTrF32Warps * 32) tree_f32_kernel(const TreePa
     }
     __syncthreads();
     const int lo = p.is_sliding ? max(0, sq.base + s_depth - p.window + 1) : 0;
-    const float* q = reinterpret_cast<const float*>(p.q) +
-                     (((size_t)b * p.n_tok + node) * p.n_q + head) * (size_t)D;
-    const float* K = reinterpret_cast<const float*>(p.k);
-    const float* V = reinterpret_cast<const float*>(p.v);
+    const int stream = threadIdx.x / LPK, part = threadIdx.x % LPK;  // columns 4 part + 4 LPK i ..
+    const float4* q = reinterpret_cast<const float4*>(
+        reinterpret_cast<const float*>(p.q) + (((size_t)b * p.n_tok + node) * p.n_q + head) * (size_t)D);
+    const float4* K = reinterpret_cast<const float4*>(p.k);
+    const float4* V = reinterpret_cast<const float4*>(p.v);
     const size_t rs = (size_t)kv_row_slots(p);
-    float qr[E], acc[E];
+    float4 qr[4], acc[4], kn[4], vn[4];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        qr[e] = q[lane + 32 * e];
-        acc[e] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+        qr[i] = __ldg(q + part + LPK * i);
+        acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    // a step's K and V rows are in flight while the step before is computed
-    float kn[U][E], vn[U][E];
-    bool in[U];
-    auto load = [&](int j0) {
+    auto attended = [&](int j) {
+        const int n = j - sq.base;
+        return n < 0 || ((s_set[n >> 5] >> (n & 31)) & 1u);
+    };
+    // the stream's first attended key from j on
+    auto seek = [&](int j) {
+        while (j < sq.len && !attended(j)) j += STREAMS;
+        return j;
+    };
+    auto load = [&](int j) {
+        int krow = 0, kslot = 0;
+        const bool there = kv_place(p, b, kvh, j, krow, kslot);  // a bad page: zeros
+        if (!there && part == 0) report(p.err, GEMMA_DEVERR_PAGE);
+        const size_t at = ((size_t)krow * rs + (size_t)kslot) * (D / 4) + part;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int j = j0 + u, n = j - sq.base;
-            in[u] = j < sq.len && (n < 0 || ((s_set[n >> 5] >> (n & 31)) & 1u));
-            int krow = 0, kslot = 0;
-            bool there = in[u];
-            if (there && !kv_place(p, b, kvh, j, krow, kslot)) {  // a bad page: zeros
-                if (lane == 0) report(p.err, GEMMA_DEVERR_PAGE);
-                there = false;
-            }
-            const size_t at = ((size_t)krow * rs + (size_t)kslot) * D + lane;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                kn[u][e] = there ? __ldg(K + at + 32 * e) : 0.f;
-                vn[u][e] = there ? __ldg(V + at + 32 * e) : 0.f;
-            }
+        for (int i = 0; i < 4; ++i) {
+            kn[i] = there ? __ldg(K + at + LPK * i) : make_float4(0.f, 0.f, 0.f, 0.f);
+            vn[i] = there ? __ldg(V + at + LPK * i) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
     };
     float m = -INFINITY, l = 0.f;
-    constexpr int STEP = kTrF32Warps * U;
-    if (lo + warp * U < sq.len) load(lo + warp * U);
-    for (int j0 = lo + warp * U; j0 < sq.len; j0 += STEP) {
-        float s[U], v[U][E];
-        bool now[U];
-        float top = m;
+    int j = seek(lo + stream);
+    if (j < sq.len) load(j);
+    // (streams of a warp leave at different times: their shuffles name their own lanes)
+    const unsigned mask = LPK == 32 ? 0xffffffffu
+                                    : ((1u << (LPK & 31)) - 1) << (threadIdx.x % 32 / LPK * LPK);
+    while (j < sq.len) {
+        float s = 0.f;
+        float4 v[4];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            s[u] = 0.f;
-            now[u] = in[u];
+        for (int i = 0; i < 4; ++i) {
+            s = fmaf(qr[i].x, kn[i].x, s);
+            s = fmaf(qr[i].y, kn[i].y, s);
+            s = fmaf(qr[i].z, kn[i].z, s);
+            s = fmaf(qr[i].w, kn[i].w, s);
+            v[i] = vn[i];
+        }
+        j = seek(j + STREAMS);
+        if (j < sq.len) load(j);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                s[u] = fmaf(qr[e], kn[u][e], s[u]);
-                v[u][e] = vn[u][e];
+        for (int o = LPK / 2; o > 0; o >>= 1) s += __shfl_xor_sync(mask, s, o);
+        s *= p.scale;
+        if (p.softcap > 0.f) s = p.softcap * tanhf(s / p.softcap);
+        if (s > m) {
+            const float alpha = expf(m - s);
+            m = s;
+            l *= alpha;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[i].x *= alpha;
+                acc[i].y *= alpha;
+                acc[i].z *= alpha;
+                acc[i].w *= alpha;
             }
         }
-        if (j0 + STEP < sq.len) load(j0 + STEP);
+        const float w = expf(s - m);
+        l += w;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            s[u] = warp_sum(s[u]) * p.scale;
-            if (p.softcap > 0.f) s[u] = p.softcap * tanhf(s[u] / p.softcap);
-            if (now[u]) top = fmaxf(top, s[u]);
+        for (int i = 0; i < 4; ++i) {
+            acc[i].x = fmaf(w, v[i].x, acc[i].x);
+            acc[i].y = fmaf(w, v[i].y, acc[i].y);
+            acc[i].z = fmaf(w, v[i].z, acc[i].z);
+            acc[i].w = fmaf(w, v[i].w, acc[i].w);
         }
-        if (top == -INFINITY) continue;  // nothing attended so far
-        const float alpha = expf(m - top);
-        l *= alpha;
-#pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] *= alpha;
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if (!now[u]) continue;
-            const float w = expf(s[u] - top);
-            l += w;
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(w, v[u][e], acc[e]);
-        }
-        m = top;
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) s_o[warp][lane + 32 * e] = acc[e];
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
+    for (int i = 0; i < 4; ++i) reinterpret_cast<float4*>(s_o[stream])[part + LPK * i] = acc[i];
+    if (part == 0) {
+        s_m[stream] = m;
+        s_l[stream] = l;
     }
     __syncthreads();
     float top = -INFINITY, sum = 0.f;
-    for (int w = 0; w < kTrF32Warps; ++w) top = fmaxf(top, s_m[w]);
-    for (int w = 0; w < kTrF32Warps; ++w) sum += s_m[w] == -INFINITY ? 0.f : s_l[w] * expf(s_m[w] - top);
+    for (int w = 0; w < STREAMS; ++w) top = fmaxf(top, s_m[w]);
+    __syncthreads();
+    if (threadIdx.x < STREAMS)  // the streams' weights in the place of their maxima
+        s_m[threadIdx.x] = s_m[threadIdx.x] == -INFINITY ? 0.f : expf(s_m[threadIdx.x] - top);
+    __syncthreads();
+    for (int w = 0; w < STREAMS; ++w) sum = fmaf(s_m[w], s_l[w], sum);
     for (int c = threadIdx.x; c < D; c += kTrF32Warps * 32) {
         float x = 0.f;
-        for (int w = 0; w < kTrF32Warps; ++w)
-            if (s_m[w] != -INFINITY) x = fmaf(s_o[w][c], expf(s_m[w] - top), x);
+        for (int w = 0; w < STREAMS; ++w)
+            if (s_m[w] != 0.f) x = fmaf(s_o[w][c], s_m[w], x);
         out[c] = x / sum;
     }
 }

@@ -362,8 +362,7 @@ __global__ void __launch_bounds__(kTpThreads, 1)
                 tc_fence_before();  // (P takes the place of S behind the groups' barrier)
                 float sl2 = p.scale_log2;  // scale > 0: the raw maximum scales to the maximum
                 if constexpr (SOFTCAP) {
-#pragma unroll
-                    for (int e = 0; e < 64; ++e) s[e] = tr_score(p, s[e]);
+                    tree_cap64(s, p);
                     sl2 = 1.f;
                 }
                 tree_mask64(s, row, U.k_begin + t * kTpKeys + 64 * w, U.sq.base);

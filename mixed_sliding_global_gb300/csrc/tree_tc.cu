@@ -327,8 +327,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 if (lane == 0) mbar_arrive(&s_free[buf]);  // S(T + 2) may overwrite it
                 float sl2 = p.scale_log2;  // scale > 0: the raw maximum scales to the maximum
                 if constexpr (SOFTCAP) {
-#pragma unroll
-                    for (int e = 0; e < 64; ++e) s[e] = tr_score(p, s[e]);
+                    tree_cap64(s, p);
                     sl2 = 1.f;
                 }
                 tree_mask64(s, row, U.k_begin + t * kTcKeys, base);
