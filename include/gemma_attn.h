@@ -431,6 +431,8 @@ size_t gemma_attn_workspace_size_q4(int batch, gemma_layer_kind kind, int window
  * bf16 and fp32 (the debug path). Cache rows that no node of the sequence attends may hold anything;
  * a NaN or infinite V row of one branch may reach the other branches' outputs. P is rounded to bf16
  * before it weighs V, as in the other bf16 entry points.
+ * Limits (else GEMMA_ERR_UNSUPPORTED): batch and n_kv at most 65535, max_seq_len at most 2^30, and 2^30
+ * key tiles in all (of 64 keys, for every KV head and 128 rows of every sequence).
  * Scratch: gemma_attn_workspace_size_tree(...) bytes (fp32 needs none); calls that may overlap must
  * not share it. Other arguments and errors as for gemma_attn_decode.
  */

@@ -17,12 +17,6 @@ using gemma::RowsParams;
 
 namespace {
 
-#ifndef GEMMA_TREE_PAIR_ROWS
-#define GEMMA_TREE_PAIR_ROWS 128
-#endif
-#ifndef GEMMA_TREE_TC_ROWS
-#define GEMMA_TREE_TC_ROWS 0
-#endif
 constexpr int kMaxSplit = 128;
 #ifndef GEMMA_MIN_CHUNK_KEYS
 #define GEMMA_MIN_CHUNK_KEYS 256
@@ -974,64 +968,77 @@ size_t gemma_logit_sample_workspace_size(int batch, int vocab, gemma_dtype dtype
 // ---------------------------------------------------------------------------------------------
 namespace {
 
-// Chunks of keys per row tile: as many as keep one wave of CTAs, each of at least a tile of keys.
-struct TreePlan {
-    int n_split, chunk;
-    size_t o_bytes, ws_bytes;
-    int path;  // kTreeRows, or in equal shares of the key tiles on single SMs or on CTA pairs
-    int workers, cluster;
-};
+// How a bf16 step runs, by sizes alone.
 enum { kTreeRows, kTreeTc, kTreePair };
-constexpr int kTreePairRows = GEMMA_TREE_PAIR_ROWS, kTreePairRows512 = 32, kTreeTcRows = GEMMA_TREE_TC_ROWS;
-#ifndef GEMMA_TREE_MERGE_NS
-#define GEMMA_TREE_MERGE_NS 4500
-#endif
-constexpr long long kTreeMergeNs = GEMMA_TREE_MERGE_NS;
+struct TreePlan {
+    int path;
+    int n_split, chunk;    // kTreeRows: chunks of keys
+    int workers, cluster;  // kTreeTc, kTreePair: equal shares, or kTreeTc: a cluster for each unit
+    size_t o_bytes, ws_bytes;
+};
+
+// Key tiles of a step, at most; the unit that 32 bits have to count.
+long long tree_tiles(int batch, int n_kv, long long rows, long long row_tile, long long reach,
+                     long long keys) {
+    return (long long)batch * n_kv * ((rows + row_tile - 1) / row_tile) * ((reach + keys - 1) / keys);
+}
+// Positions that a sequence's nodes can attend (rings and pages start at whole tiles).
+long long tree_reach(int kind, int window, int max_seq_len, int n_nodes) {
+    const long long reach = kind == GEMMA_GLOBAL ? max_seq_len : (long long)window - 1 + n_nodes;
+    return (reach < max_seq_len ? reach : max_seq_len) + gemma::kTreeKeyTile - 1;
+}
+
 TreePlan tree_plan(int batch, int kind, int window, int n_q, int n_kv, int head_dim,
                    int max_seq_len, int n_nodes, int n_sm) {
     const long long T = gemma::kTreeKeyTile;
-    const int rows = n_nodes * (n_q / n_kv), tile = 16 * gemma::tree_row_groups(rows);
-    const long long units = (long long)batch * n_kv * ((rows + tile - 1) / tile);
-    long long reach = kind == GEMMA_GLOBAL ? max_seq_len : (long long)window - 1 + n_nodes;
-    if (reach > max_seq_len) reach = max_seq_len;
-    reach += T - 1;  // (rings and pages start at whole tiles)
-    // equal shares: no more workers than tiles (which are counted in 32 bits)
-    auto shares = [&](int path, long long row_tile, long long keys, long long most) {
-        const long long halves = path == kTreePair ? head_dim / 256 : 1;
-        const long long tiles = (long long)batch * n_kv * ((rows + row_tile - 1) / row_tile) *
-                                halves * ((reach + keys - 1) / keys);
-        TreePlan pl{1, 1 << 30, 0, 0, path, (int)(tiles < most ? tiles : most), 0};
-        pl.ws_bytes = path == kTreePair ? gemma::tree_pair_workspace(batch, pl.workers)
-                                        : gemma::tree_tc_workspace(head_dim, batch, pl.workers);
-        if (tiles > (1ll << 30)) pl.workers = 0;
+    const long long rows = (long long)n_nodes * (n_q / n_kv), units = (long long)batch * n_kv;
+    const long long reach = tree_reach(kind, window, max_seq_len, n_nodes);
+    TreePlan pl{kTreeRows, 1, 1 << 30, 0, 0, 0, 0};
+    // Two SMs and 256 rows per tile, or one and 128. Head_dim 256 in us, pairs / single SMs: 61 nodes x 4
+    // heads, 2 KV heads, 1 sequence of 8192 keys 20 / 20, 7 of 4800 35 / 37, 16 of 4096 46 / 60, 64 of 2048
+    // (64 nodes) 75 / 112; with 128 rows or fewer a pair's second SM would have none.
+    // Head_dim 512: pairs from 33 rows on, mma.sync before. 32 rows, 4 KV heads, 1024 keys, 1 sequence 14.1
+    // on mma.sync, 13.8 on pairs, 32 sequences 53 and 88; 48 rows 21 and 14.3, 137 and 91.
+    if (head_dim == 512 ? rows > gemma::kTreeRowsMax : head_dim == 256 && rows > 128) {
+        const long long tiles = tree_tiles(batch, n_kv, rows, 256, reach, 128) * (head_dim / 256);
+        pl.path = kTreePair;
+        pl.workers = (int)(tiles < n_sm / 2 ? tiles : n_sm / 2);
+        pl.ws_bytes = gemma::tree_pair_workspace(batch, pl.workers);
         return pl;
-    };
-    if (batch <= gemma::kTreePairMaxBatch) {
-        TreePlan pl{};
-        if (head_dim >= 256 && rows > (head_dim == 512 ? kTreePairRows512 : kTreePairRows))
-            pl = shares(kTreePair, 256, 128, n_sm / 2);
-        else if (head_dim <= 256 && rows > kTreeTcRows) {
-            pl = shares(kTreeTc, 128, 64, n_sm);
-            // a cluster for each unit, where that ends no later (times in ns)
-            const long long u = (long long)batch * n_kv * ((rows + 127) / 128), nt = (reach + 63) / 64;
-            const long long tile_ns = 500 + 2 * head_dim;
-            const long long cluster_ns = 700 + (rows < 128 ? rows : 128) * head_dim * 16ll / 100;
-            long long best = (u * nt + n_sm - 1) / n_sm * tile_ns + kTreeMergeNs;
-            for (int c = 1; c <= kMaxClusterSplit && u * c <= n_sm; c *= 2) {
-                const long long t = (nt + c - 1) / c * tile_ns + (c > 1 ? cluster_ns : 0);
-                if (t <= best && (c == 1 || u <= gemma::tree_tc_clusters(head_dim, c))) {
-                    best = t;
-                    pl.cluster = c;
-                    pl.ws_bytes = 0;
-                }
+    }
+    // Up to 16 rows of head_dim 64 or 128 over many keys: mma.sync takes a 64-key tile in less than the 0.6
+    // us that one takes on tcgen05. Head_dim 64, 8 rows, tcgen05 / mma.sync: 64 x 2 heads x 4096 keys 60 /
+    // 30 us, 8 x 4 x 4096 18.6 / 13.4, 32 x 4 x 512 10.8 / 11.5, 1 x 4 x 8192 12.2 / 20.3; head_dim 128:
+    // 62 / 49, 19.7 / 15.8, 11.1 / 12.7, 13.6 / 17.8.
+    if (head_dim <= 256 && !(head_dim <= 128 && rows <= 16 && units * reach >= 100000)) {
+        pl.path = kTreeTc;
+        const long long tiles = tree_tiles(batch, n_kv, rows, 128, reach, T);
+        pl.workers = (int)(tiles < n_sm ? tiles : n_sm);
+        pl.ws_bytes = gemma::tree_tc_workspace(head_dim, batch, pl.workers);
+        // A cluster for each unit (no merge launch), where that ends no later than equal shares. In ns: a
+        // tile takes 560 at head_dim 64 and 1000 at 256; the merge launch of equal shares 4500; a cluster's
+        // exchange 1.0, 2.0 and 5.9 thousand with 32 rows of 256, 128 of 64, 128 of 256. One unit of 32 rows
+        // and head_dim 256, clusters of 8 / shares: 1100 keys 9.6 / 10.2 us; 128 rows: 14.6 / 11.7; 128
+        // units of 17 tiles, alone / shares: 30.6 / 34.4.
+        const long long u = units * ((rows + 127) / 128);
+        const long long nt = kind == GEMMA_SLIDING_RING ? (reach + T - 1) / T : reach / T;
+        const long long tile_ns = 500 + 2 * head_dim, merge_ns = 4500;
+        const long long cluster_ns = 700 + (rows < 128 ? rows : 128) * head_dim * 16 / 100;
+        long long best = (u * nt + n_sm - 1) / n_sm * tile_ns + merge_ns;
+        for (int c = 1; c <= 8 && u * c <= n_sm; c *= 2) {
+            const long long t = (nt + c - 1) / c * tile_ns + (c > 1 ? cluster_ns : 0);
+            if (t <= best && (c == 1 || u <= gemma::tree_tc_clusters(head_dim, c))) {
+                best = t;
+                pl.cluster = c;
+                pl.ws_bytes = 0;
             }
         }
-        if (pl.workers > 0) return pl;
+        return pl;
     }
-    long long n = (long long)n_sm * gemma::tree_ctas_per_sm(head_dim, rows) / units;
+    // chunks of keys: as many as keep one wave of CTAs, each of at least a tile
+    long long n = (long long)n_sm * gemma::tree_ctas_per_sm(head_dim) / units;
     if (n > kMaxSplit) n = kMaxSplit;
     if (n < 1) n = 1;
-    TreePlan pl{1, 1 << 30, 0, 0, kTreeRows, 0, 0};
     const long long chunk = round_up((reach + n - 1) / n, T);
     n = (reach + chunk - 1) / chunk;
     if (n <= 1) return pl;
@@ -1053,6 +1060,10 @@ int tree_sizes(int batch, int kind, int window, int n_q, int n_kv, int head_dim,
         return GEMMA_ERR_UNSUPPORTED;
     // (one warp per row and slice of a merge, one CTA per row of the fp32 path)
     if ((long long)batch * n_q * n_nodes > (1ll << 30)) return GEMMA_ERR_UNSUPPORTED;
+    // (key tiles are counted in 32 bits)
+    if (tree_tiles(batch, n_kv, (long long)n_nodes * (n_q / n_kv), 128,
+                   tree_reach(kind, window, max_seq_len, n_nodes), gemma::kTreeKeyTile) > (1ll << 30))
+        return GEMMA_ERR_UNSUPPORTED;
     return GEMMA_OK;
 }
 

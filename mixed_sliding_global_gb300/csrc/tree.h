@@ -16,12 +16,15 @@ struct TreeParams {
     const int32_t* parents;  // [batch][n_tok], -1 or an earlier node
 };
 
-// Row groups (16 rows each) of a CTA's tile for this many rows per KV head.
-constexpr int tree_row_groups(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+constexpr int kTreeRowsMax = 32;  // rows per KV head of launch_tree_rows
 
-// On single SMs with tcgen05 (tree_tc.cu), head_dim 64 to 256, at most kTreePairMaxBatch sequences;
-// the merge included. workers: CTAs, one per SM at most; or a cluster of 1 to 8 CTAs for each unit
-// (cluster > 0; no workspace).
+// On CTA pairs (tree_pair.cu), head_dim 256 and 512, any number of rows; the merge included. workers:
+// pairs, one per two SMs at most.
+size_t tree_pair_workspace(int batch, int workers);
+cudaError_t launch_tree_pair(const TreeParams& tp, int head_dim, int batch, void* workspace,
+                             int workers, cudaStream_t st);
+// On single SMs with tcgen05 (tree_tc.cu), head_dim 64 to 256, any number of rows; the merge included.
+// workers: CTAs, one per SM at most; or a cluster of 1 to 8 CTAs for each unit (cluster > 0; no workspace).
 int tree_tc_clusters(int head_dim, int cluster);  // clusters of 2, 4 or 8 that run at once
 size_t tree_tc_workspace(int head_dim, int batch, int workers);
 cudaError_t launch_tree_tc(const TreeParams& tp, int head_dim, int batch, void* workspace,
@@ -32,7 +35,7 @@ cudaError_t launch_tree_tc(const TreeParams& tp, int head_dim, int batch, void* 
 struct MergeParams {
     TreeParams tp;
     int batch, n_rt;  // row tiles per (sequence, KV head)
-    int workers;
+    int workers;      // (CTAs of a unit's cluster where units are dealt out by the host)
     int keys;         // of a key tile
     float* part_o;    // [2 workers][pieces of 128 rows and up to 256 columns][columns / 4][128][4]
     float2* part_ml;  // [2 workers][pieces][128]
@@ -40,16 +43,9 @@ struct MergeParams {
 };
 cudaError_t launch_tree_merge(const MergeParams& mp, int head_dim, int rows, cudaStream_t st);
 
-// CTAs of the bf16 launch that fit an SM.
-int tree_ctas_per_sm(int head_dim, int rows);
-
-// On CTA pairs (tree_pair.cu), head_dim 256 and 512, any number of rows, at most
-// kTreePairMaxBatch sequences; the merge included. workers: pairs, one per two SMs at most.
-constexpr int kTreePairMaxBatch = 1024;
-size_t tree_pair_workspace(int batch, int workers);
-cudaError_t launch_tree_pair(const TreeParams& tp, int head_dim, int batch, void* workspace,
-                             int workers, cudaStream_t st);
-
+// On mma.sync (tree_attn.cu): head_dim 64 and 128 with up to 16 rows, 512 with up to 32; the CTAs that fit
+// an SM.
+int tree_ctas_per_sm(int head_dim);
 cudaError_t launch_tree_rows(const TreeParams& tp, int head_dim, int batch, cudaStream_t st);
 cudaError_t launch_tree_f32(const TreeParams& tp, int head_dim, int batch, cudaStream_t st);
 cudaError_t launch_tree_combine(const TreeParams& tp, int head_dim, int batch, cudaStream_t st);

@@ -8,19 +8,21 @@
 // Gemma-4 (2B / 4B / 12B) to AWS Inferentia2", sections 2.1-2.3 and 4.3).
 //
 // All nodes share the prefix, so a KV head's rows (nodes x G query heads) go through its keys
-// together: with R rows a key costs 4 R d operations for 4 d bytes, and tiles of up to 64 rows read
-// the cache once for all of them. bf16 kernel, per CTA: one KV head of one sequence, a tile of 16,
-// 32 or 64 rows, one chunk of keys:
-//  - a producer warp streams K and V tiles of 64 keys through a ring of slots (tiled TMA, 128-byte
-//    swizzle);
-//  - eight consumer warps stand in groups of 16 rows; the CW warps of a group share out the keys of
-//    S = Q K^T (mma.sync m16n8k16, Q fragments from shared memory) and, after one exchange of row
-//    maxima and one of P (bf16) through shared memory, the columns of O += P V;
-//  - the reference of a row's exponentials moves only when the maximum grows by more than 2^8;
-//  - ancestor sets are four words per token, walked up from the parents while the first tiles
-//    load; only tiles that reach the tree or a window's edge look at masks.
-// Sums, maxima and O are fp32; P is rounded to bf16 for the matrix instruction and summed as
-// rounded. Chunks leave partial (m, l, O) for tree_combine_kernel, an unsplit launch writes `out`.
+// together: with R rows a key costs 4 R d operations for 4 d bytes. Many rows run on the 5th-generation
+// tensor cores (tree_tc.cu, tree_pair.cu). Here:
+//  - tree_keys_kernel, head_dim 64 and 128, up to 16 rows, many keys: bound by memory. A warp has the 16
+//    rows and a share of every tile's keys, and keeps O whole, so that no warp waits for another;
+//  - tree_rows_kernel, head_dim 512, up to 32 rows: O of 16 rows is two warps' registers at least, so the
+//    warps of a row group share out the keys of S and the columns of O += P V, with an exchange of row
+//    maxima and one of P through shared memory per tile;
+//  - tree_f32_kernel, the fp32 debug path.
+// The first two, per CTA: one KV head of one sequence and one chunk of keys. A producer warp streams K and
+// V tiles of 64 keys through a ring of slots (tiled TMA, 128-byte swizzle); mma.sync m16n8k16; the
+// reference of a row's exponentials moves only when the maximum grows by more than 2^8; ancestor sets are
+// four words per token, walked up from the parents while the first tiles load; only tiles that reach the
+// tree or a window's edge look at masks. Sums, maxima and O are fp32; P is rounded to bf16 for the matrix
+// instruction and summed as rounded. Chunks leave partial (m, l, O) for tree_combine_kernel, an unsplit
+// launch writes `out`.
 #include <atomic>
 #include <climits>
 
@@ -66,8 +68,8 @@ struct TrLay {
     static_assert(SLOTS >= 2 && SMEM <= 232448 && BAR_OFF % 8 == 0, "shared memory budget");
 };
 
-// The same for head_dim up to 256, where a warp holds O of its 16 rows whole: KG warps share out a
-// tile's keys.
+// The same for head_dim up to 128, where a warp holds O of its 16 rows whole: KG warps share out a tile's
+// keys.
 template <int D, int MW>
 struct TrKeys {
     static constexpr int M = 16 * MW;             // rows of the tile
@@ -103,7 +105,7 @@ GEMMA_DEVINL uint32_t tr_off(int key, int d) {
 
 }  // namespace
 
-// head_dim up to 256: a warp has 16 rows and a share of every tile's keys, and keeps O whole
+// head_dim up to 128: a warp has the rows and a share of every tile's keys, and keeps O whole
 template <int D, int MW>
 __global__ void __launch_bounds__((TrKeys<D, MW>::WARPS + 1) * 32, TrKeys<D, MW>::TWO ? 2 : 1)
     tree_keys_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -128,17 +130,17 @@ __global__ void __launch_bounds__((TrKeys<D, MW>::WARPS + 1) * 32, TrKeys<D, MW>
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + Lay::BAR_OFF);
     uint64_t* empty = full + kTrMaxSlots;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int split = blockIdx.x % p.n_split, rt = blockIdx.x / p.n_split;
+    const int split = blockIdx.x;
     const int kvh = blockIdx.y, b = blockIdx.z;
     const int rows_total = p.n_tok * p.G;
-    const int row0 = rt * M, n_rows = min(M, rows_total - row0);
+    const int row0 = 0, n_rows = rows_total;
     const bool direct = p.n_split == 1;
 
     pdl_wait();  // the previous kernel on the stream has completed
     const TrSeq sq = tr_seq(p, b);
     const int live = sq.bad ? 0 : max(0, min(n_rows, sq.n * p.G - row0));  // rows of real nodes
     if (live == 0) {
-        if (sq.bad && split == 0 && rt == 0 && kvh == 0 && threadIdx.x == 0) report(p.err, sq.bad);
+        if (sq.bad && split == 0 && kvh == 0 && threadIdx.x == 0) report(p.err, sq.bad);
         for (int i = threadIdx.x; direct && i < n_rows * (D / 8); i += (WARPS + 1) * 32) {
             const int r = i / (D / 8), R = row0 + r, tk = R / p.G;
             __nv_bfloat16* dst =
@@ -215,7 +217,7 @@ __global__ void __launch_bounds__((TrKeys<D, MW>::WARPS + 1) * 32, TrKeys<D, MW>
         sPar[threadIdx.x] = bad ? -1 : m;
     }
     bad = named_bar_or(2, WARPS * 32, bad);  // a bad tree: every row masked, zeros
-    if (bad && split == 0 && rt == 0 && kvh == 0 && threadIdx.x == 0)
+    if (bad && split == 0 && kvh == 0 && threadIdx.x == 0)
         report(p.err, GEMMA_DEVERR_TREE);
     const int tk0 = row0 / p.G;  // the tile's first token
     if ((int)threadIdx.x < (row0 + live - 1) / p.G - tk0 + 1) {
@@ -448,17 +450,17 @@ __global__ void __launch_bounds__(kTrThreads, TrLay<D, MW>::TWO ? 2 : 1)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + Lay::BAR_OFF);
     uint64_t* empty = full + kTrMaxSlots;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int split = blockIdx.x % p.n_split, rt = blockIdx.x / p.n_split;
+    const int split = blockIdx.x;
     const int kvh = blockIdx.y, b = blockIdx.z;
     const int rows_total = p.n_tok * p.G;
-    const int row0 = rt * M, n_rows = min(M, rows_total - row0);
+    const int row0 = 0, n_rows = rows_total;
     const bool direct = p.n_split == 1;
 
     pdl_wait();  // the previous kernel on the stream has completed
     const TrSeq sq = tr_seq(p, b);
     const int live = sq.bad ? 0 : max(0, min(n_rows, sq.n * p.G - row0));  // rows of real nodes
     if (live == 0) {
-        if (sq.bad && split == 0 && rt == 0 && kvh == 0 && threadIdx.x == 0) report(p.err, sq.bad);
+        if (sq.bad && split == 0 && kvh == 0 && threadIdx.x == 0) report(p.err, sq.bad);
         for (int i = threadIdx.x; direct && i < n_rows * (D / 8); i += kTrThreads) {
             const int r = i / (D / 8), R = row0 + r, tk = R / p.G;
             __nv_bfloat16* dst =
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(kTrThreads, TrLay<D, MW>::TWO ? 2 : 1)
         sPar[threadIdx.x] = bad ? -1 : m;
     }
     bad = named_bar_or(2, kTrWarps * 32, bad);  // a bad tree: every row masked, zeros
-    if (bad && split == 0 && rt == 0 && kvh == 0 && threadIdx.x == 0)
+    if (bad && split == 0 && kvh == 0 && threadIdx.x == 0)
         report(p.err, GEMMA_DEVERR_TREE);
     const int tk0 = row0 / p.G;  // the tile's first token
     if ((int)threadIdx.x < (row0 + live - 1) / p.G - tk0 + 1) {
@@ -703,19 +705,11 @@ __global__ void __launch_bounds__(kTrThreads, TrLay<D, MW>::TWO ? 2 : 1)
             const int vkey = kk * 16 + (lane & 15);
 #pragma unroll
             for (int j = 0; j < ON; j += 2) {
-                if constexpr (ON == 1) {
-                    uint32_t v0, v1;
-                    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0,%1}, [%2];"
-                                 : "=r"(v0), "=r"(v1)
-                                 : "r"(smem_u32(tV + tr_off(vkey, cw * OC))));
-                    mma_bf16(o[j], a0, a1, a2, a3, v0 & mlo, v1 & mhi);
-                } else {
-                    uint32_t v0, v1, v2, v3;
-                    ldsm_x4_t(smem_u32(tV + tr_off(vkey, cw * OC + j * 8 + (lane >> 4) * 8)), v0, v1,
-                              v2, v3);
-                    mma_bf16(o[j], a0, a1, a2, a3, v0 & mlo, v1 & mhi);
-                    mma_bf16(o[j + 1], a0, a1, a2, a3, v2 & mlo, v3 & mhi);
-                }
+                uint32_t v0, v1, v2, v3;
+                ldsm_x4_t(smem_u32(tV + tr_off(vkey, cw * OC + j * 8 + (lane >> 4) * 8)), v0, v1,
+                          v2, v3);
+                mma_bf16(o[j], a0, a1, a2, a3, v0 & mlo, v1 & mhi);
+                mma_bf16(o[j + 1], a0, a1, a2, a3, v2 & mlo, v3 & mhi);
             }
         }
         __syncwarp();
@@ -979,23 +973,10 @@ struct TrKernel<512, MW> {
     static auto entry() { return tree_rows_kernel<512, MW>; }
 };
 
-template <int D>
-static int ctas_per_sm(int groups) {
-    return (groups == 1   ? TrKernel<D, 1>::Lay::TWO
-            : groups == 2 ? TrKernel<D, 2>::Lay::TWO
-                          : TrKernel<D, 4>::Lay::TWO)
-               ? 2
-               : 1;
-}
-
-int tree_ctas_per_sm(int head_dim, int rows) {
-    const int groups = tree_row_groups(rows);
-    switch (head_dim) {
-        case 64: return ctas_per_sm<64>(groups);
-        case 128: return ctas_per_sm<128>(groups);
-        case 256: return ctas_per_sm<256>(groups);
-    }
-    return ctas_per_sm<512>(groups);
+int tree_ctas_per_sm(int head_dim) {
+    return head_dim == 64    ? TrKernel<64, 1>::Lay::TWO + 1
+           : head_dim == 128 ? TrKernel<128, 1>::Lay::TWO + 1
+                             : 1;
 }
 
 template <int D, int MW>
@@ -1021,26 +1002,18 @@ static cudaError_t launch_rows_dm(const TreeParams& tp, int batch, cudaStream_t 
     const uint32_t box[3] = {64, (uint32_t)T, 1};
     if (!encode_bf16_sw128(&km, p.k, 3, dims, strides, box)) return cudaErrorInvalidValue;
     if (!encode_bf16_sw128(&vm, p.v, 3, dims, strides, box)) return cudaErrorInvalidValue;
-    const unsigned tiles = (unsigned)((p.n_tok * p.G + Lay::M - 1) / Lay::M);
-    return launch_pdl(kernel, dim3(tiles * p.n_split, p.n_kv, batch), dim3(TrKernel<D, MW>::THREADS), Lay::SMEM,
-                      st, km, vm, tp);
-}
-
-template <int D>
-static cudaError_t launch_rows_d(const TreeParams& tp, int batch, cudaStream_t st) {
-    switch (tree_row_groups(tp.p.n_tok * tp.p.G)) {
-        case 1: return launch_rows_dm<D, 1>(tp, batch, st);
-        case 2: return launch_rows_dm<D, 2>(tp, batch, st);
-    }
-    return launch_rows_dm<D, 4>(tp, batch, st);
+    return launch_pdl(kernel, dim3(p.n_split, p.n_kv, batch), dim3(TrKernel<D, MW>::THREADS),
+                      Lay::SMEM, st, km, vm, tp);
 }
 
 cudaError_t launch_tree_rows(const TreeParams& tp, int head_dim, int batch, cudaStream_t st) {
+    const int rows = tp.p.n_tok * tp.p.G;
+    if (rows > kTreeRowsMax || (head_dim != 512 && rows > 16)) return cudaErrorInvalidValue;
     switch (head_dim) {
-        case 64: return launch_rows_d<64>(tp, batch, st);
-        case 128: return launch_rows_d<128>(tp, batch, st);
-        case 256: return launch_rows_d<256>(tp, batch, st);
-        case 512: return launch_rows_d<512>(tp, batch, st);
+        case 64: return launch_rows_dm<64, 1>(tp, batch, st);
+        case 128: return launch_rows_dm<128, 1>(tp, batch, st);
+        case 512:
+            return rows <= 16 ? launch_rows_dm<512, 1>(tp, batch, st) : launch_rows_dm<512, 2>(tp, batch, st);
     }
     return cudaErrorInvalidValue;
 }
@@ -1068,7 +1041,6 @@ cudaError_t launch_tree_combine(const TreeParams& tp, int head_dim, int batch, c
     switch (head_dim) {
         case 64: return launch_combine_d<64>(tp, batch, st);
         case 128: return launch_combine_d<128>(tp, batch, st);
-        case 256: return launch_combine_d<256>(tp, batch, st);
         case 512: return launch_combine_d<512>(tp, batch, st);
     }
     return cudaErrorInvalidValue;

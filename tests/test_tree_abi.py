@@ -47,6 +47,7 @@ def attn(out=FAKE, q=FAKE, kc=(FAKE,), vc=(FAKE,), owner=(0,), layer=0, lens=FAK
     (dict(msl=0), INVALID),
     (dict(msl=65), CAPACITY),
     (dict(msl=(1 << 30) + 1, cap=(1 << 30) + 1), UNSUPPORTED),
+    (dict(batch=64, n_kv=4, msl=1 << 28, cap=1 << 28), UNSUPPORTED),  # 2^30 key tiles and a few
     (dict(cap=0), INVALID),
     (dict(kind=3), INVALID),
     (dict(kind=0, window=0), INVALID),
