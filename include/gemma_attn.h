@@ -498,9 +498,11 @@ int gemma_kv_keep(void* const* caches, int n_caches, const int32_t* write_pos, c
  *               0. The caller starts with all 0 and all entries -1, and keeps the two in step where
  *               it edits them itself.
  * page_size is a multiple of 128, n_pages at most 2^29, batch * max_pages below 2^31, batch at most
- * 65535 (else GEMMA_ERR_UNSUPPORTED). An entry outside [.., n_pages), or one whose page nobody
- * holds, sets GEMMA_DEVERR_PAGE and is left alone. Results do not depend on scheduling. Calls on one
- * table must not overlap each other, nor a call that reads or writes its pages.
+ * 65535 (else GEMMA_ERR_UNSUPPORTED); a batch of 0 does nothing. An entry of n_pages or more sets
+ * GEMMA_DEVERR_PAGE and is left alone (a fork does not pass it on). So does, where gemma_pages_reserve or
+ * gemma_pages_compact meets it, one whose page nobody holds; gemma_pages_free takes it out of the table.
+ * Results do not depend on scheduling. Calls on one table must not overlap each other, nor a call that
+ * reads or writes its pages.
  */
 
 /* gemma_pages_free -- give back the pages that hold no position in [keep_from[b], keep_to[b]): all of

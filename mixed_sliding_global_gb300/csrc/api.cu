@@ -1,7 +1,9 @@
 // api.cu -- the C ABI declared in include/gemma_attn.h: host-side validation, owner-layer
 // resolution, the split plan of the decode bucket, and kernel launches. Nothing here
 // allocates memory or synchronises; every launch goes to the caller's stream.
+#include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <initializer_list>
@@ -1162,7 +1164,7 @@ int gemma_attn_tree(void* out, const void* q, const void* const* k_cache,
     p.scale = scale;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.softcap = softcap;
-    p.cap_inner = softcap > 0.f ? scale / softcap : 0.f;
+    p.cap_inner = softcap > 0.f ? std::min(scale / softcap, FLT_MAX) : 0.f;
     p.cap_log2 = softcap * 1.4426950408889634f;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;

@@ -50,7 +50,7 @@ struct TrLay {
     static constexpr int BOX = T * 128;           // one TMA box: 64 keys x 64 columns
     static constexpr int Q_ROW = 2 * D + 16;      // padded bytes per Q row
     static constexpr int P_ROW = 2 * T + 16;
-    static constexpr int FIXED = M * Q_ROW + M * P_ROW + CW * M * 4 + 64 * kTrWords * 4 + 64 * 4 +
+    static constexpr int FIXED = M * Q_ROW + M * P_ROW + CW * M * 4 + 32 * kTrWords * 4 + 32 * 4 +
                                  kTreeMaxNodes * 4 + 2 * kTrMaxSlots * 8 + 1024;
     // two CTAs per SM where their rings then hold four tiles each, else one
     static constexpr bool TWO = FIXED + 4 * SLOT <= 113 * 1024;
@@ -61,8 +61,8 @@ struct TrLay {
     static constexpr int P_OFF = Q_OFF + M * Q_ROW;
     static constexpr int MAX_OFF = P_OFF + M * P_ROW;
     static constexpr int ANC_OFF = MAX_OFF + CW * M * 4;
-    static constexpr int DEPTH_OFF = ANC_OFF + 64 * kTrWords * 4;
-    static constexpr int PAR_OFF = DEPTH_OFF + 64 * 4;
+    static constexpr int DEPTH_OFF = ANC_OFF + 32 * kTrWords * 4;
+    static constexpr int PAR_OFF = DEPTH_OFF + 32 * 4;
     static constexpr int BAR_OFF = PAR_OFF + kTreeMaxNodes * 4;
     static constexpr int SMEM = BAR_OFF + 2 * kTrMaxSlots * 8 + 1024;  // + alignment slack
     static_assert(SLOTS >= 2 && SMEM <= 232448 && BAR_OFF % 8 == 0, "shared memory budget");
@@ -70,16 +70,16 @@ struct TrLay {
 
 // The same for head_dim up to 128, where a warp holds O of its 16 rows whole: KG warps share out a tile's
 // keys.
-template <int D, int MW>
+template <int D>
 struct TrKeys {
-    static constexpr int M = 16 * MW;             // rows of the tile
-    static constexpr int KG = MW == 1 ? 4 : kTrWarps / MW;
-    static constexpr int WARPS = MW * KG;         // consumers
+    static constexpr int M = 16;                  // rows of the tile
+    static constexpr int KG = 4;
+    static constexpr int WARPS = KG;              // consumers
     static constexpr int SLOT = T * D * 2;
     static constexpr int Q_ROW = 2 * D + 16;
     static constexpr int O_ROW = D + 8;           // floats per row of the merge buffer
     static constexpr int MERGE = KG * M * O_ROW * 4;  // in the ring, once its tiles are used up
-    static constexpr int FIXED = M * Q_ROW + 2 * KG * M * 4 + 64 * kTrWords * 4 + 64 * 4 +
+    static constexpr int FIXED = M * Q_ROW + 2 * KG * M * 4 + 32 * kTrWords * 4 + 32 * 4 +
                                  kTreeMaxNodes * 4 + 2 * kTrMaxSlots * 8 + 1024;
     static constexpr int PAIR_FIT = (113 * 1024 - FIXED) / SLOT;  // slots of each of two CTAs per SM
     static constexpr bool TWO = PAIR_FIT >= 4 && PAIR_FIT * SLOT >= MERGE;
@@ -89,8 +89,8 @@ struct TrKeys {
     static constexpr int Q_OFF = RING;
     static constexpr int ML_OFF = Q_OFF + M * Q_ROW;                 // m [KG][M], l [KG][M]
     static constexpr int ANC_OFF = ML_OFF + 2 * KG * M * 4;
-    static constexpr int DEPTH_OFF = ANC_OFF + 64 * kTrWords * 4;
-    static constexpr int PAR_OFF = DEPTH_OFF + 64 * 4;
+    static constexpr int DEPTH_OFF = ANC_OFF + 32 * kTrWords * 4;
+    static constexpr int PAR_OFF = DEPTH_OFF + 32 * 4;
     static constexpr int BAR_OFF = PAR_OFF + kTreeMaxNodes * 4;
     static constexpr int SMEM = BAR_OFF + 2 * kTrMaxSlots * 8 + 1024;  // + alignment slack
     static_assert(SLOTS >= 4 && RING >= MERGE && SMEM <= 232448 && BAR_OFF % 8 == 0,
@@ -106,12 +106,12 @@ GEMMA_DEVINL uint32_t tr_off(int key, int d) {
 }  // namespace
 
 // head_dim up to 128: a warp has the rows and a share of every tile's keys, and keeps O whole
-template <int D, int MW>
-__global__ void __launch_bounds__((TrKeys<D, MW>::WARPS + 1) * 32, TrKeys<D, MW>::TWO ? 2 : 1)
+template <int D>
+__global__ void __launch_bounds__((TrKeys<D>::WARPS + 1) * 32, TrKeys<D>::TWO ? 2 : 1)
     tree_keys_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const TreeParams tp) {
     pdl_launch_dependents();
-    using Lay = TrKeys<D, MW>;
+    using Lay = TrKeys<D>;
     constexpr int M = Lay::M, KG = Lay::KG, S = Lay::SLOTS, WARPS = Lay::WARPS;
     constexpr int KN = T / KG;       // a warp's keys of a tile
     constexpr int NT = KN / 8;
@@ -124,28 +124,27 @@ __global__ void __launch_bounds__((TrKeys<D, MW>::WARPS + 1) * 32, TrKeys<D, MW>
     uint8_t* sQ = smem + Lay::Q_OFF;
     float* sM = reinterpret_cast<float*>(smem + Lay::ML_OFF);                  // [KG][M]
     float* sL = sM + KG * M;                                                   // [KG][M]
-    uint32_t* sAnc = reinterpret_cast<uint32_t*>(smem + Lay::ANC_OFF);         // [64][kTrWords]
-    int* sDepth = reinterpret_cast<int*>(smem + Lay::DEPTH_OFF);               // [64]
+    uint32_t* sAnc = reinterpret_cast<uint32_t*>(smem + Lay::ANC_OFF);         // [32][kTrWords]
+    int* sDepth = reinterpret_cast<int*>(smem + Lay::DEPTH_OFF);               // [32]
     int* sPar = reinterpret_cast<int*>(smem + Lay::PAR_OFF);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + Lay::BAR_OFF);
     uint64_t* empty = full + kTrMaxSlots;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.x;
     const int kvh = blockIdx.y, b = blockIdx.z;
-    const int rows_total = p.n_tok * p.G;
-    const int row0 = 0, n_rows = rows_total;
+    const int n_rows = p.n_tok * p.G;
     const bool direct = p.n_split == 1;
 
     pdl_wait();  // the previous kernel on the stream has completed
     const TrSeq sq = tr_seq(p, b);
-    const int live = sq.bad ? 0 : max(0, min(n_rows, sq.n * p.G - row0));  // rows of real nodes
+    const int live = sq.bad ? 0 : max(0, min(n_rows, sq.n * p.G));  // rows of real nodes
     if (live == 0) {
         if (sq.bad && split == 0 && kvh == 0 && threadIdx.x == 0) report(p.err, sq.bad);
         for (int i = threadIdx.x; direct && i < n_rows * (D / 8); i += (WARPS + 1) * 32) {
-            const int r = i / (D / 8), R = row0 + r, tk = R / p.G;
+            const int r = i / (D / 8), tk = r / p.G;
             __nv_bfloat16* dst =
                 reinterpret_cast<__nv_bfloat16*>(p.out) +
-                (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) * (size_t)D;
+                (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (r - tk * p.G)) * (size_t)D;
             reinterpret_cast<uint4*>(dst)[i - r * (D / 8)] = make_uint4(0u, 0u, 0u, 0u);
         }
         return;
@@ -202,9 +201,9 @@ __global__ void __launch_bounds__((TrKeys<D, MW>::WARPS + 1) * 32, TrKeys<D, MW>
             const int r = i / CH, ch = i - r * CH;
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
             if (r < live) {
-                const int R = row0 + r, tk = R / p.G;
+                const int tk = r / p.G;
                 v = __ldg(reinterpret_cast<const uint4*>(
-                              q + (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) *
+                              q + (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (r - tk * p.G)) *
                                       (size_t)D) + ch);
             }
             *reinterpret_cast<uint4*>(sQ + r * Lay::Q_ROW + ch * 16) = v;
@@ -219,24 +218,23 @@ __global__ void __launch_bounds__((TrKeys<D, MW>::WARPS + 1) * 32, TrKeys<D, MW>
     bad = named_bar_or(2, WARPS * 32, bad);  // a bad tree: every row masked, zeros
     if (bad && split == 0 && kvh == 0 && threadIdx.x == 0)
         report(p.err, GEMMA_DEVERR_TREE);
-    const int tk0 = row0 / p.G;  // the tile's first token
-    if ((int)threadIdx.x < (row0 + live - 1) / p.G - tk0 + 1) {
-        const int i = threadIdx.x;  // at most 64 tokens
+    if ((int)threadIdx.x < (live - 1) / p.G + 1) {
+        const int i = threadIdx.x;  // at most 32 tokens
         uint32_t set[kTrWords];
-        sDepth[i] = tr_walk(sPar, tk0 + i, p.is_sliding ? p.window : INT_MAX, set);
+        sDepth[i] = tr_walk(sPar, i, p.is_sliding ? p.window : INT_MAX, set);
 #pragma unroll
         for (int w = 0; w < kTrWords; ++w) sAnc[i * kTrWords + w] = set[w];
     }
     named_bar_sync(1, (WARPS + 1) * 32);  // with the producer: its barriers exist
 
-    const int mw = warp / KG, kg = warp - mw * KG;  // row group, share of the keys
+    const int kg = warp;  // share of the keys
     const int g = lane >> 2, tq = lane & 3;
-    // this thread's rows 16 mw + g and + 8: the first prefix key they attend, and their token
+    // this thread's rows g and g + 8: the first prefix key they attend, and their token
     int lo[2], tok[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int r = 16 * mw + g + 8 * i;
-        tok[i] = r < live && !bad ? (row0 + r) / p.G - tk0 : -1;
+        const int r = g + 8 * i;
+        tok[i] = r < live && !bad ? r / p.G : -1;
         lo[i] = tok[i] < 0        ? INT_MAX
                 : p.is_sliding ? max(0, sq.base + sDepth[tok[i]] - p.window + 1)
                                   : 0;
@@ -246,7 +244,7 @@ __global__ void __launch_bounds__((TrKeys<D, MW>::WARPS + 1) * 32, TrKeys<D, MW>
     float o[ON][4];
 #pragma unroll
     for (int j = 0; j < ON; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
-    const uint32_t qa0 = smem_u32(sQ + (16 * mw + (lane & 15)) * Lay::Q_ROW + (lane >> 4) * 16);
+    const uint32_t qa0 = smem_u32(sQ + ((lane & 15)) * Lay::Q_ROW + (lane >> 4) * 16);
 
     // No warp waits for another before the end: each has its own keys, and its rows' reference.
     bool ok = true;
@@ -370,15 +368,15 @@ __global__ void __launch_bounds__((TrKeys<D, MW>::WARPS + 1) * 32, TrKeys<D, MW>
         l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], 1);
         l_run[i] += __shfl_xor_sync(0xffffffffu, l_run[i], 2);
         if (tq == 0) {
-            sM[kg * M + 16 * mw + g + 8 * i] = m_run[i];
-            sL[kg * M + 16 * mw + g + 8 * i] = l_run[i];
+            sM[kg * M + g + 8 * i] = m_run[i];
+            sL[kg * M + g + 8 * i] = l_run[i];
         }
     }
     named_bar_sync(2, WARPS * 32);
     float* sO = reinterpret_cast<float*>(ring);  // [KG][M][O_ROW]
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int r = 16 * mw + g + 8 * i;
+        const int r = g + 8 * i;
         float top = -INFINITY;
 #pragma unroll
         for (int k = 0; k < KG; ++k) top = fmaxf(top, sM[k * M + r]);
@@ -392,7 +390,7 @@ __global__ void __launch_bounds__((TrKeys<D, MW>::WARPS + 1) * 32, TrKeys<D, MW>
     named_bar_sync(2, WARPS * 32);
     constexpr int CH = D / 4;  // four columns of a row per thread and step
     for (int x = threadIdx.x; x < n_rows * CH; x += WARPS * 32) {
-        const int r = x / CH, ch = x - r * CH, R = row0 + r;
+        const int r = x / CH, ch = x - r * CH;
         float top = -INFINITY, l = 0.f;
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -401,23 +399,23 @@ __global__ void __launch_bounds__((TrKeys<D, MW>::WARPS + 1) * 32, TrKeys<D, MW>
         for (int k = 0; k < KG; ++k) {
             const float4 v = *reinterpret_cast<const float4*>(sO + (k * M + r) * Lay::O_ROW + 4 * ch);
             const float mk = sM[k * M + r];
-            l += mk == -INFINITY ? 0.f : fast_exp2(mk - top) * sL[k * M + r];
+            l += mk == -INFINITY ? sL[k * M + r] : fast_exp2(mk - top) * sL[k * M + r];  // (0, or NaN)
             a.x += v.x;
             a.y += v.y;
             a.z += v.z;
             a.w += v.w;
         }
         if (direct) {
-            const int tk = R / p.G;
+            const int tk = r / p.G;
             uint2* dst = reinterpret_cast<uint2*>(
                 reinterpret_cast<__nv_bfloat16*>(p.out) +
-                (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) * (size_t)D + 4 * ch);
+                (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (r - tk * p.G)) * (size_t)D + 4 * ch);
             const float inv = 1.f / l;  // (no keys: zeros, whatever the other rows' V holds)
             *dst = l == 0.f ? make_uint2(0u, 0u)
                             : make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
         } else {
             const size_t pr =
-                (((size_t)b * p.n_kv + kvh) * rows_total + R) * p.n_split + split;
+                (((size_t)b * p.n_kv + kvh) * n_rows + r) * p.n_split + split;
             *reinterpret_cast<float4*>(p.o_part + pr * D + 4 * ch) = a;
             if (ch == 0) *reinterpret_cast<float2*>(p.ml_part + pr * 2) = make_float2(top, l);
         }
@@ -444,28 +442,27 @@ __global__ void __launch_bounds__(kTrThreads, TrLay<D, MW>::TWO ? 2 : 1)
     uint8_t* sQ = smem + Lay::Q_OFF;
     uint8_t* sP = smem + Lay::P_OFF;
     float* sMax = reinterpret_cast<float*>(smem + Lay::MAX_OFF);               // [CW][M]
-    uint32_t* sAnc = reinterpret_cast<uint32_t*>(smem + Lay::ANC_OFF);         // [64][kTrWords]
-    int* sDepth = reinterpret_cast<int*>(smem + Lay::DEPTH_OFF);               // [64]
+    uint32_t* sAnc = reinterpret_cast<uint32_t*>(smem + Lay::ANC_OFF);         // [32][kTrWords]
+    int* sDepth = reinterpret_cast<int*>(smem + Lay::DEPTH_OFF);               // [32]
     int* sPar = reinterpret_cast<int*>(smem + Lay::PAR_OFF);
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + Lay::BAR_OFF);
     uint64_t* empty = full + kTrMaxSlots;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.x;
     const int kvh = blockIdx.y, b = blockIdx.z;
-    const int rows_total = p.n_tok * p.G;
-    const int row0 = 0, n_rows = rows_total;
+    const int n_rows = p.n_tok * p.G;
     const bool direct = p.n_split == 1;
 
     pdl_wait();  // the previous kernel on the stream has completed
     const TrSeq sq = tr_seq(p, b);
-    const int live = sq.bad ? 0 : max(0, min(n_rows, sq.n * p.G - row0));  // rows of real nodes
+    const int live = sq.bad ? 0 : max(0, min(n_rows, sq.n * p.G));  // rows of real nodes
     if (live == 0) {
         if (sq.bad && split == 0 && kvh == 0 && threadIdx.x == 0) report(p.err, sq.bad);
         for (int i = threadIdx.x; direct && i < n_rows * (D / 8); i += kTrThreads) {
-            const int r = i / (D / 8), R = row0 + r, tk = R / p.G;
+            const int r = i / (D / 8), tk = r / p.G;
             __nv_bfloat16* dst =
                 reinterpret_cast<__nv_bfloat16*>(p.out) +
-                (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) * (size_t)D;
+                (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (r - tk * p.G)) * (size_t)D;
             reinterpret_cast<uint4*>(dst)[i - r * (D / 8)] = make_uint4(0u, 0u, 0u, 0u);
         }
         return;
@@ -522,9 +519,9 @@ __global__ void __launch_bounds__(kTrThreads, TrLay<D, MW>::TWO ? 2 : 1)
             const int r = i / CH, ch = i - r * CH;
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
             if (r < live) {
-                const int R = row0 + r, tk = R / p.G;
+                const int tk = r / p.G;
                 v = __ldg(reinterpret_cast<const uint4*>(
-                              q + (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) *
+                              q + (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (r - tk * p.G)) *
                                       (size_t)D) + ch);
             }
             *reinterpret_cast<uint4*>(sQ + r * Lay::Q_ROW + ch * 16) = v;
@@ -539,11 +536,10 @@ __global__ void __launch_bounds__(kTrThreads, TrLay<D, MW>::TWO ? 2 : 1)
     bad = named_bar_or(2, kTrWarps * 32, bad);  // a bad tree: every row masked, zeros
     if (bad && split == 0 && kvh == 0 && threadIdx.x == 0)
         report(p.err, GEMMA_DEVERR_TREE);
-    const int tk0 = row0 / p.G;  // the tile's first token
-    if ((int)threadIdx.x < (row0 + live - 1) / p.G - tk0 + 1) {
-        const int i = threadIdx.x;  // at most 64 tokens
+    if ((int)threadIdx.x < (live - 1) / p.G + 1) {
+        const int i = threadIdx.x;  // at most 32 tokens
         uint32_t set[kTrWords];
-        sDepth[i] = tr_walk(sPar, tk0 + i, p.is_sliding ? p.window : INT_MAX, set);
+        sDepth[i] = tr_walk(sPar, i, p.is_sliding ? p.window : INT_MAX, set);
 #pragma unroll
         for (int w = 0; w < kTrWords; ++w) sAnc[i * kTrWords + w] = set[w];
     }
@@ -556,7 +552,7 @@ __global__ void __launch_bounds__(kTrThreads, TrLay<D, MW>::TWO ? 2 : 1)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int r = 16 * mw + g + 8 * i;
-        tok[i] = r < live && !bad ? (row0 + r) / p.G - tk0 : -1;
+        tok[i] = r < live && !bad ? r / p.G : -1;
         lo[i] = tok[i] < 0        ? INT_MAX
                 : p.is_sliding ? max(0, sq.base + sDepth[tok[i]] - p.window + 1)
                                   : 0;
@@ -732,12 +728,11 @@ __global__ void __launch_bounds__(kTrThreads, TrLay<D, MW>::TWO ? 2 : 1)
         float l = 0.f;
 #pragma unroll
         for (int c = 0; c < CW; ++c) l += sMax[c * M + r];
-        const int R = row0 + r;
         if (direct) {
-            const int tk = R / p.G;
+            const int tk = r / p.G;
             __nv_bfloat16* dst =
                 reinterpret_cast<__nv_bfloat16*>(p.out) +
-                (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (R - tk * p.G)) * (size_t)D +
+                (((size_t)b * p.n_tok + tk) * p.n_q + kvh * p.G + (r - tk * p.G)) * (size_t)D +
                 cw * OC + 2 * tq;
             const float inv = 1.f / l;
 #pragma unroll
@@ -746,7 +741,7 @@ __global__ void __launch_bounds__(kTrThreads, TrLay<D, MW>::TWO ? 2 : 1)
                     l == 0.f ? 0u : pack_bf16(o[j][2 * i] * inv, o[j][2 * i + 1] * inv);
         } else {
             const size_t pr =
-                (((size_t)b * p.n_kv + kvh) * rows_total + R) * p.n_split + split;
+                (((size_t)b * p.n_kv + kvh) * n_rows + r) * p.n_split + split;
             float* dst = p.o_part + pr * D + cw * OC + 2 * tq;
 #pragma unroll
             for (int j = 0; j < ON; ++j)
@@ -912,7 +907,7 @@ __global__ void __launch_bounds__(kTrF32Warps * 32) tree_f32_kernel(const TreePa
         for (int o = LPK / 2; o > 0; o >>= 1) s += __shfl_xor_sync(mask, s, o);
         s *= p.scale;
         if (p.softcap > 0.f) s = p.softcap * tanhf(s / p.softcap);
-        if (s > m) {
+        if (!(s <= m)) {  // (a NaN too: it reaches the output)
             const float alpha = expf(m - s);
             m = s;
             l *= alpha;
@@ -924,7 +919,7 @@ __global__ void __launch_bounds__(kTrF32Warps * 32) tree_f32_kernel(const TreePa
                 acc[i].w *= alpha;
             }
         }
-        const float w = expf(s - m);
+        const float w = s == -INFINITY ? 0.f : expf(s - m);
         l += w;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -962,9 +957,9 @@ __global__ void __launch_bounds__(kTrF32Warps * 32) tree_f32_kernel(const TreePa
 // The kernel of a shape: its layout, threads and entry.
 template <int D, int MW>
 struct TrKernel {
-    using Lay = TrKeys<D, MW>;
+    using Lay = TrKeys<D>;
     static constexpr int THREADS = (Lay::WARPS + 1) * 32;
-    static auto entry() { return tree_keys_kernel<D, MW>; }
+    static auto entry() { return tree_keys_kernel<D>; }
 };
 template <int MW>
 struct TrKernel<512, MW> {

@@ -91,16 +91,25 @@ GEMMA_DEVINL unsigned long long tr_window(const uint32_t (&anc)[kTrWords], int m
     return see;
 }
 
-// scale * dot, soft-capped where a cap is set, in log2 units. tanh through one exponential and one
-// reciprocal: its absolute error (2^-22) times the cap is what the score is off by.
+// tanh(x) / x by its Taylor series to x^11, of u = x^2: the first term left out is 0.0036 x^12, below
+// 2^-20 for |x| <= 1/2.
+constexpr float kTanh3 = -1.f / 3.f, kTanh5 = 2.f / 15.f, kTanh7 = -17.f / 315.f, kTanh9 = 62.f / 2835.f,
+                kTanh11 = -1382.f / 155925.f;
+GEMMA_DEVINL float tr_tanh_over_x(float u) {
+    return fmaf(fmaf(fmaf(fmaf(fmaf(kTanh11, u, kTanh9), u, kTanh7), u, kTanh5), u, kTanh3), u, 1.f);
+}
+// scale * dot, soft-capped where a cap is set, in log2 units: cap * tanh(x), x = scale * dot / cap. Above
+// |x| = 1/2 tanh goes through one exponential and one reciprocal; below, its absolute error there (2^-22,
+// times the cap) would be large against the score, and the series takes its place.
 GEMMA_DEVINL float tr_score(const RowsParams& p, float dot) {
+    const float s = dot * p.scale_log2;
     if (p.softcap > 0.f) {
-        const float e = fast_exp2(dot * p.cap_inner * 2.885390081777927f);  // exp(2 x)
+        const float x = dot * p.cap_inner, e = fast_exp2(x * 2.885390081777927f);  // exp(2 x)
         float r;
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-        return fmaf(-2.f * p.cap_log2, r, p.cap_log2);
+        return fabsf(x) <= 0.5f ? s * tr_tanh_over_x(x * x) : fmaf(-2.f * p.cap_log2, r, p.cap_log2);
     }
-    return dot * p.scale_log2;
+    return s;
 }
 
 // A unit (one KV head of one sequence, a tile of ROWS rows, one of HALVES parts of head_dim), or a part
@@ -315,30 +324,27 @@ GEMMA_DEVINL void tree_store32(__nv_bfloat16* out, const uint32_t (&v)[32], floa
         }
     }
 }
-// 64 scores soft-capped, in log2 units: cap_log2 * tanh(x), x = dot * cap_inner. Where no |x| of the warp is
-// above 1/2, tanh is its Taylor series to x^11 (the first term left out is 0.0036 x^13, below 2^-21 there):
-// the exponential and the reciprocal of tr_score, 2 of 3 special-function instructions per score, made the
+// 64 scores soft-capped, in log2 units (tr_score). Where no |x| of the warp is above 1/2, by the series
+// alone: the exponential and the reciprocal, 2 of 3 special-function instructions per score, made the
 // capped tile of 128 x 128 scores special-function bound (2.5 us against 1.4 without a cap, 1.6 with this).
 GEMMA_DEVINL void tree_cap64(float (&s)[64], const RowsParams& p) {
     float top = 0.f;
 #pragma unroll
     for (int e = 0; e < 64; e += 2) top = fmax3f(top, fabsf(s[e]), fabsf(s[e + 1]));
     if (__all_sync(0xffffffffu, top * p.cap_inner <= 0.5f)) {
-        const unsigned long long in = f32x2(p.cap_inner, p.cap_inner), out = f32x2(p.cap_log2, p.cap_log2);
-        const unsigned long long c11 = f32x2(-1382.f / 155925.f, -1382.f / 155925.f),
-                                 c9 = f32x2(62.f / 2835.f, 62.f / 2835.f),
-                                 c7 = f32x2(-17.f / 315.f, -17.f / 315.f),
-                                 c5 = f32x2(2.f / 15.f, 2.f / 15.f), c3 = f32x2(-1.f / 3.f, -1.f / 3.f),
-                                 one = f32x2(1.f, 1.f);
+        const unsigned long long in = f32x2(p.cap_inner, p.cap_inner), out = f32x2(p.scale_log2, p.scale_log2);
+        const unsigned long long c11 = f32x2(kTanh11, kTanh11), c9 = f32x2(kTanh9, kTanh9),
+                                 c7 = f32x2(kTanh7, kTanh7), c5 = f32x2(kTanh5, kTanh5),
+                                 c3 = f32x2(kTanh3, kTanh3), one = f32x2(1.f, 1.f);
 #pragma unroll
         for (int e = 0; e < 64; e += 2) {
-            const unsigned long long x = mul_f32x2(f32x2(s[e], s[e + 1]), in), u = mul_f32x2(x, x);
+            const unsigned long long v = f32x2(s[e], s[e + 1]), x = mul_f32x2(v, in), u = mul_f32x2(x, x);
             unsigned long long t = fma_f32x2(c11, u, c9);
             t = fma_f32x2(t, u, c7);
             t = fma_f32x2(t, u, c5);
             t = fma_f32x2(t, u, c3);
             t = fma_f32x2(t, u, one);
-            const float2 y = f32x2_split(mul_f32x2(mul_f32x2(x, out), t));
+            const float2 y = f32x2_split(mul_f32x2(mul_f32x2(v, out), t));
             s[e] = y.x;
             s[e + 1] = y.y;
         }

@@ -71,7 +71,10 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeParams mp) {
             }
             float top = m;
 #pragma unroll
-            for (int i = 0; i < BATCH; ++i) top = fmaxf(top, ml[i].x);
+            for (int i = 0; i < BATCH; ++i) {
+                top = fmaxf(top, ml[i].x);
+                if (ml[i].x == -INFINITY) l += ml[i].y;  // (0; NaN where every score was)
+            }
             if (top == -INFINITY) continue;
             const float a = fast_exp2(m - top);  // 0 while there was nothing
             m = top;
@@ -132,8 +135,8 @@ template <int D, int ROWS>
 static cudaError_t launch_merge(const MergeParams& mp, cudaStream_t st) {
     const long long groups = (long long)mp.n_rt * mp.batch * mp.tp.p.n_kv * (ROWS / 32);
     // Parts per unit, about. In us of the whole step with 1 / 4 / 8 warps to a row and slice: 6 parts
-    // (14 units of 244 rows, head_dim 256) 43.2 / 42.7 / 50.7, 19 parts (one tree of 512 rows, head_dim 512) 23.3 / 23.0 / 24.3, 64 parts (one
-    // unit of 32 rows, head_dim 64) 13.5 / - / 9.4.
+    // (14 units of 244 rows, head_dim 256) 43.2 / 42.7 / 50.7, 19 parts (one tree of 512 rows, head_dim
+    // 512) 23.3 / 23.0 / 24.3, 64 parts (one unit of 32 rows, head_dim 64) 13.5 / - / 9.4.
     const long long parts = mp.workers / ((long long)mp.n_rt * mp.batch * mp.tp.p.n_kv * (D > 256 ? 2 : 1));
     auto launch = [&](auto kernel, int slices) {
         return launch_pdl(kernel, dim3((unsigned)(groups * ((D / 16 + slices - 1) / slices))), dim3(256),

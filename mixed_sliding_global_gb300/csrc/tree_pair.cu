@@ -122,8 +122,9 @@ __global__ void __launch_bounds__(kTpThreads, 1)
     const uint32_t tmem = *tslot;
     pdl_wait();  // the previous kernel on the stream has completed
     PairShare share;
-    // (compute bound: a tile takes as long alone as when every SM works; the constants in TreeShare's
-    // terms, measured at both head_dims)
+    // (compute bound: a tile takes as long alone as when every SM works, and the parts and their merge as
+    // long as six of them, three at head_dim 512. Whole / cut: 30 units of 10 tiles, head_dim 256, 23.6 /
+    // 25.6 us; 50 of 10, head_dim 512, 32.9 / 36.6; 20 of 5 19.2 / 21.1)
     share.init(mp, worker, blockIdx.x == 0 && warp == 0, 1000 * KB, 1000 * KB, 6000);
     TreeUnit U{};
     bool ok = true;

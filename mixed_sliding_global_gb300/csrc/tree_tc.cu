@@ -51,6 +51,8 @@ struct TcLay {
     static constexpr int BAR_OFF = Q_OFF + Q;
     static constexpr int SMEM = BAR_OFF + 512 + 1024;  // + alignment slack
     static_assert(SMEM <= 232448 && (2 * kTcMaxSlots + 13) * 8 + 4 <= 512, "shared memory budget");
+    // CTAs of two clusters that waited for each other's tensor memory would wait for ever
+    static_assert(2 * (SMEM + 1024) > 228 * 1024, "one CTA per SM");
 };
 
 GEMMA_DEVINL float2 ld_cluster_f32x2(uint32_t addr) {
@@ -438,7 +440,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 for (int k = 0; k < kTcMaxCluster; ++k) M = fmaxf(M, ml[k].x);
 #pragma unroll
                 for (int k = 0; k < kTcMaxCluster; ++k) {
-                    if (ml[k].x == -INFINITY) continue;
+                    if (ml[k].x == -INFINITY) {
+                        L += ml[k].y;  // (0; NaN where every score was)
+                        continue;
+                    }
                     have |= 1u << k;
                     L = fmaf(fast_exp2(ml[k].x - M), ml[k].y, L);
                 }
