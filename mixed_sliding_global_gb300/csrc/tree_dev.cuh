@@ -7,6 +7,7 @@
 #include <climits>
 
 #include "common.cuh"
+#include "tc.cuh"
 #include "tree.h"
 
 namespace gemma {
@@ -324,54 +325,83 @@ GEMMA_DEVINL void tree_store32(__nv_bfloat16* out, const uint32_t (&v)[32], floa
         }
     }
 }
-// 64 scores soft-capped, in log2 units (tr_score). Where no |x| of the warp is above 1/2, by the series
-// alone: the exponential and the reciprocal, 2 of 3 special-function instructions per score, made the
-// capped tile of 128 x 128 scores special-function bound (2.5 us against 1.4 without a cap, 1.6 with this).
-GEMMA_DEVINL void tree_cap64(float (&s)[64], const RowsParams& p) {
+// N scores of a row soft-capped, in log2 units (tr_score); a NaN may spread to the score beside it. Three
+// forms of tanh, by the largest |x| of the thread's scores:
+//  - up to 1/8 (in the whole warp) the series' first three terms, the next being 0.054 x^6 < 2^-22;
+//  - up to 1/2 the series;
+//  - above, 1 - 2 / (1 + e^2x), two scores to a reciprocal: off by at most 2^-20 of 1 where the row's
+//    largest score is 0.46 at least. With the softmax's own exponential 5 special-function instructions for
+//    two scores, which bound such a tile.
+template <int N>
+GEMMA_DEVINL void tree_cap(float (&s)[N], const RowsParams& p) {
     float top = 0.f;
 #pragma unroll
-    for (int e = 0; e < 64; e += 2) top = fmax3f(top, fabsf(s[e]), fabsf(s[e + 1]));
-    if (__all_sync(0xffffffffu, top * p.cap_inner <= 0.5f)) {
-        const unsigned long long in = f32x2(p.cap_inner, p.cap_inner), out = f32x2(p.scale_log2, p.scale_log2);
-        const unsigned long long c11 = f32x2(kTanh11, kTanh11), c9 = f32x2(kTanh9, kTanh9),
-                                 c7 = f32x2(kTanh7, kTanh7), c5 = f32x2(kTanh5, kTanh5),
-                                 c3 = f32x2(kTanh3, kTanh3), one = f32x2(1.f, 1.f);
+    for (int e = 0; e < N; e += 2) top = fmax3f(top, fabsf(s[e]), fabsf(s[e + 1]));
+    top *= p.cap_inner;
+    const float k = p.scale_log2;
+    const unsigned long long in = f32x2(p.cap_inner, p.cap_inner), c5 = f32x2(k * kTanh5, k * kTanh5),
+                             c3 = f32x2(k * kTanh3, k * kTanh3), c1 = f32x2(k, k);
+    if (__all_sync(0xffffffffu, top <= 0.125f)) {
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) {
+        for (int e = 0; e < N; e += 2) {
+            const unsigned long long v = f32x2(s[e], s[e + 1]), x = mul_f32x2(v, in), u = mul_f32x2(x, x);
+            const float2 y = f32x2_split(mul_f32x2(v, fma_f32x2(fma_f32x2(c5, u, c3), u, c1)));
+            s[e] = y.x;
+            s[e + 1] = y.y;
+        }
+    } else if (top <= 0.5f) {
+        const unsigned long long c11 = f32x2(k * kTanh11, k * kTanh11), c9 = f32x2(k * kTanh9, k * kTanh9),
+                                 c7 = f32x2(k * kTanh7, k * kTanh7);
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
             const unsigned long long v = f32x2(s[e], s[e + 1]), x = mul_f32x2(v, in), u = mul_f32x2(x, x);
             unsigned long long t = fma_f32x2(c11, u, c9);
             t = fma_f32x2(t, u, c7);
             t = fma_f32x2(t, u, c5);
             t = fma_f32x2(t, u, c3);
-            t = fma_f32x2(t, u, one);
-            const float2 y = f32x2_split(mul_f32x2(mul_f32x2(v, out), t));
+            const float2 y = f32x2_split(mul_f32x2(v, fma_f32x2(t, u, c1)));
             s[e] = y.x;
             s[e + 1] = y.y;
         }
     } else {
+        const float in2 = 2.885390081777927f * p.cap_inner;  // exp(2 x) = 2^(in2 s)
 #pragma unroll
-        for (int e = 0; e < 64; ++e) s[e] = tr_score(p, s[e]);
+        for (int e = 0; e < N; e += 2) {
+            // (2^58 at most, so that the product of two stays in range; a NaN stays one)
+            float x = s[e] * in2, y = s[e + 1] * in2;
+            x = x > 58.f ? 58.f : x;
+            y = y > 58.f ? 58.f : y;
+            const float a = 1.f + fast_exp2(x), b = 1.f + fast_exp2(y);
+            float q;
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(a * b));
+            q *= -2.f * p.cap_log2;
+            s[e] = fmaf(q, b, p.cap_log2);
+            s[e + 1] = fmaf(q, a, p.cap_log2);
+        }
     }
+    __syncwarp();
 }
-// Maximum of 64 scores.
-GEMMA_DEVINL float tree_max64(const float (&s)[64]) {
+// Maximum of N scores (32 or 64).
+template <int N>
+GEMMA_DEVINL float tree_max(const float (&s)[N]) {
     float m[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) m[i] = fmax3f(s[i], s[8 + i], s[16 + i]);
 #pragma unroll
-    for (int e = 24; e < 56; e += 16)
+    for (int e = 24; e + 8 < N; e += 16)
 #pragma unroll
         for (int i = 0; i < 8; ++i) m[i] = fmax3f(m[i], s[e + i], s[e + 8 + i]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m[i] = fmaxf(m[i], s[56 + i]);
+    for (int i = 0; i < 8; ++i) m[i] = fmaxf(m[i], s[N - 8 + i]);
     return fmax3f(fmax3f(m[0], m[1], m[2]), fmax3f(m[3], m[4], m[5]), fmaxf(m[6], m[7]));
 }
-// P = 2^(s * scale + neg) of 64 scores as packed bf16; returns their sum, as rounded.
-GEMMA_DEVINL float tree_exp64(const float (&s)[64], float scale, float neg, uint32_t (&pw)[32]) {
+// P = 2^(s * scale + neg) of N scores as packed bf16; returns their sum, as rounded.
+template <int N>
+GEMMA_DEVINL float tree_exp(const float (&s)[N], float scale, float neg, uint32_t (&pw)[N / 2]) {
     const unsigned long long scale2 = f32x2(scale, scale), neg2 = f32x2(neg, neg);
     unsigned long long sum[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
+    for (int k = 0; k < N / 2; ++k) {
         const float2 x = f32x2_split(fma_f32x2(f32x2(s[2 * k], s[2 * k + 1]), scale2, neg2));
         pw[k] = pack_bf16(fast_exp2(x.x), fast_exp2(x.y));
         sum[k & 1] = add_f32x2(sum[k & 1], f32x2(__uint_as_float(pw[k] << 16),
@@ -380,17 +410,22 @@ GEMMA_DEVINL float tree_exp64(const float (&s)[64], float scale, float neg, uint
     const float2 a = f32x2_split(sum[0]), b = f32x2_split(sum[1]);
     return (a.x + a.y) + (b.x + b.y);
 }
-// Keys that a row does not attend leave 64 scores: key 0 of them is kt0.
-GEMMA_DEVINL void tree_mask64(float (&s)[64], const TreeRow& row, int kt0, int base) {
-    if (kt0 >= row.lo && kt0 + 64 <= base) return;
+// Scores of keys that a row does not attend become x: N of them (32 or 64), key 0 is kt0.
+template <int N>
+GEMMA_DEVINL void tree_mask(float (&s)[N], const TreeRow& row, int kt0, int base, float x) {
+    if (kt0 >= row.lo && kt0 + N <= base) return;
     const unsigned long long see = tr_window(row.anc, kt0 - base, row.lo - kt0);
     const uint32_t s0 = (uint32_t)see, s1 = (uint32_t)(see >> 32);
 #pragma unroll
     for (int e = 0; e < 32; ++e) {
-        if (!((s0 >> e) & 1u)) s[e] = -INFINITY;
-        if (!((s1 >> e) & 1u)) s[32 + e] = -INFINITY;
+        if (!((s0 >> e) & 1u)) s[e] = x;
+        if constexpr (N == 64)
+            if (!((s1 >> e) & 1u)) s[32 + e] = x;
     }
 }
+// Packed P of 32 or 64 keys into tensor memory.
+GEMMA_DEVINL void tmem_store(uint32_t addr, const uint32_t (&v)[32]) { tmem_st32(addr, v); }
+GEMMA_DEVINL void tmem_store(uint32_t addr, const uint32_t (&v)[16]) { tmem_st16(addr, v); }
 GEMMA_DEVINL void prefetch_map(const CUtensorMap* m) {
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(m)) : "memory");
 }

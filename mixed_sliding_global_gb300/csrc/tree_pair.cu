@@ -17,12 +17,13 @@
 //  - parts leave O as it stands in tensor memory, four columns of all rows after another, so that
 //    stores are of 512 consecutive bytes;
 //  - barriers, tensor memory and tensor maps are set up before the wait for the previous kernel.
-// Warps of each CTA: 0-7 softmax (two groups of four: group w has columns 64 w .. of S and 128 w .. of O,
-// the groups swap row maxima through shared memory), 8 loads K and V, 9 issues S and 10 P V (even CTA)
-// or they forward their slots' arrivals to the even CTA, whose MMAs read both halves (odd CTA), 11 loads
-// Q. Barriers that the issuers wait on live in the even CTA and count arrivals from both; their
+// Warps of each CTA: softmax (two groups of four, with a soft-cap four: group w has columns 64 w .. (32 w
+// ..) of S and 128 w .. (64 w ..) of O, the groups swap row maxima through shared memory); then one that
+// loads K and V, two that issue S and P V (even CTA) or forward their slots' arrivals to the even CTA, whose
+// MMAs read both halves (odd CTA), and one that loads Q. Barriers that the issuers wait on live in the even CTA and count arrivals from both; their
 // commits arrive in both CTAs.
 #include <atomic>
+#include <climits>
 
 #include "common.cuh"
 #include "tc.cuh"
@@ -34,42 +35,54 @@ namespace gemma {
 
 namespace {
 
-constexpr int kTpThreads = 384;
 constexpr int kTpRows = 256, kTpKeys = 128;
 constexpr int kTpBox = 64 * 128;      // TMA box: 64 keys x 64 columns
 constexpr int kTpSlot = 4 * kTpBox;   // K: 64 keys x 256 columns; V: 128 keys x 128 columns
 constexpr int kTpQBox = 128 * 128;
 constexpr int kTpO = 0, kTpS = 256;   // TMEM columns: O; S / P, two buffers of 128
 
-template <int D>
+template <int D, bool SOFTCAP>
 struct TpLay {
+    // Groups of four softmax warps. A tile with a soft-cap is bound by the softmax, and four have more of
+    // it in flight; without, two end earlier. Two / four, 76 units of 4096 keys, head_dim 256: no cap 64 /
+    // 68 us, a cap of 10 times the scores 77 / 75, of twice 191 / 125 (with a reciprocal per score; now
+    // 99); 76 units of 256 keys 15.6 / 16.8.
+    static constexpr int GROUPS = SOFTCAP ? 4 : 2;
+    static constexpr int SOFT = 4 * GROUPS;                  // softmax warps
+    static constexpr int THREADS = 32 * (SOFT + 4);
+    static constexpr int COLS = 128 / GROUPS, O_COLS = 256 / GROUPS;  // a group's columns of S and O
     static constexpr int KB = D / 256;                       // K slots of a tile
     static constexpr int K_SLOTS = D == 512 ? 2 : 3, V_SLOTS = D == 512 ? 1 : 2;
     static constexpr int SLOTS = K_SLOTS + V_SLOTS;
     static constexpr int Q = 128 * D * 2;
     static constexpr int Q_OFF = SLOTS * kTpSlot;
-    static constexpr int MX_OFF = Q_OFF + Q;                 // row maxima [2][2 groups][128]
-    static constexpr int BAR_OFF = MX_OFF + 2 * 2 * 128 * 4;
+    static constexpr int MX_OFF = Q_OFF + Q;                 // row maxima [3][128], sums [2][128]
+    static constexpr int BAR_OFF = MX_OFF + 5 * 128 * 4;
     static constexpr int SMEM = BAR_OFF + 256;
     static_assert(SMEM <= 232448, "shared memory budget");
 };
 
 }  // namespace
 
+// A float's bits as an integer of the same order, and back.
+GEMMA_DEVINL int tp_ordered(int x) { return x ^ ((x >> 31) & 0x7fffffff); }
+
 template <int D, bool SOFTCAP>
-__global__ void __launch_bounds__(kTpThreads, 1)
+__global__ void __launch_bounds__(TpLay<D, SOFTCAP>::THREADS, 1)
     tree_pair_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap,
                      const __grid_constant__ CUtensorMap qmap, const MergeParams mp) {
-    using Lay = TpLay<D>;
+    using Lay = TpLay<D, SOFTCAP>;
     using PairShare = TreeShare<kTpKeys, kTpRows, Lay::KB>;
     constexpr int KB = Lay::KB, NK = Lay::K_SLOTS, NV = Lay::V_SLOTS;
+    constexpr int GROUPS = Lay::GROUPS, SOFT = Lay::SOFT, COLS = Lay::COLS, O_COLS = Lay::O_COLS;
     pdl_launch_dependents();
     const RowsParams& p = mp.tp.p;
     extern __shared__ __align__(1024) uint8_t tp_smem[];
     uint8_t* smem = tp_smem;
     uint8_t* sQ = smem + Lay::Q_OFF;                                 // [D / 64][128][64] bf16
-    float* mxs = reinterpret_cast<float*>(smem + Lay::MX_OFF);       // [2][2][128]
+    int* mxs = reinterpret_cast<int*>(smem + Lay::MX_OFF);           // [3][128], ordered as the floats
+    float* lxs = reinterpret_cast<float*>(mxs + 3 * 128);            // [2][128]
     // full: this CTA's half has landed; pfull (even CTA): the odd CTA's has (forwarded); empty: the
     // MMAs that read the slot have completed (in both CTAs)
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + Lay::BAR_OFF);
@@ -88,7 +101,8 @@ __global__ void __launch_bounds__(kTpThreads, 1)
     const uint32_t c = cluster_rank();
     const int worker = blockIdx.x / 2;
 
-    if (threadIdx.x == 256) {
+    for (int i = threadIdx.x; i < 3 * 128; i += Lay::THREADS) mxs[i] = INT_MIN;
+    if (threadIdx.x == 32 * SOFT) {
         prefetch_map(&kmap);
         prefetch_map(&qmap);
         prefetch_map(&vmap);
@@ -102,17 +116,17 @@ __global__ void __launch_bounds__(kTpThreads, 1)
         mbar_init(q_free, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], 16);  // 8 softmax warps per CTA
+            mbar_init(&p_full[i], 2 * SOFT);  // both CTAs' softmax warps
             mbar_init(&pv_done[i], 1);
         }
         mbar_init(o_full, 1);
-        mbar_init(o_free, 16);
+        mbar_init(o_free, 2 * SOFT);
         fence_barrier_init();
     }
     __syncthreads();
     // both CTAs run and their barriers exist before the pair's allocation and any remote arrival
     cluster_sync();
-    if (warp == 9) {
+    if (warp == SOFT + 1) {
         tmem_alloc_pair(tslot, 512);
         tmem_relinquish_pair();
     }
@@ -143,7 +157,7 @@ __global__ void __launch_bounds__(kTpThreads, 1)
         __syncwarp();
     };
 
-    if (warp == 8) {
+    if (warp == SOFT) {
         // -------------------------------------- K and V -----------------------------------------
         // in the order of their use: K(0), K(1), V(0), K(2), V(1), ..., into the next part too
         TreeRing rk, rv;
@@ -211,7 +225,7 @@ __global__ void __launch_bounds__(kTpThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 11) {
+    } else if (warp == SOFT + 3) {
         // ---------------------------------------- Q ---------------------------------------------
         // a part's rows, once the last S of the part before has read the buffer
         int ord = 0;
@@ -227,7 +241,7 @@ __global__ void __launch_bounds__(kTpThreads, 1)
             __syncwarp();
         }
         if (ord > 0 && ok) mbar_wait(q_free, (ord - 1) & 1, p.err);  // (landed before the CTA exits)
-    } else if (c == 0 && warp == 9) {
+    } else if (c == 0 && warp == SOFT + 1) {
         // ------------------------------------- S issuer -----------------------------------------
         const uint32_t id_s = idesc_bf16(256, kTpKeys, 0, 0);
         const uint64_t qd = smem_desc_sw128(smem_u32(sQ), 0, 1024);
@@ -269,7 +283,7 @@ __global__ void __launch_bounds__(kTpThreads, 1)
                 }
             }
         }
-    } else if (c == 0 && warp == 10) {
+    } else if (c == 0 && warp == SOFT + 2) {
         // ------------------------------------ P V issuer ----------------------------------------
         const uint32_t id_pv = idesc_bf16(256, 256, 0, 1);
         TreeRing rv;
@@ -299,7 +313,7 @@ __global__ void __launch_bounds__(kTpThreads, 1)
                 __syncwarp();
             }
         }
-    } else if (c == 1 && warp == 9) {
+    } else if (c == 1 && warp == SOFT + 1) {
         // --------------------- odd CTA: arrivals of Q and K, to the even CTA --------------------
         const uint32_t pfull0 = map_to_peer(&pfull[0], 0), q_pfull0 = map_to_peer(q_pfull, 0);
         TreeRing rk;
@@ -313,7 +327,7 @@ __global__ void __launch_bounds__(kTpThreads, 1)
                 __syncwarp();
             }
         }
-    } else if (c == 1 && warp == 10) {
+    } else if (c == 1 && warp == SOFT + 2) {
         // ------------------------- odd CTA: arrivals of V, edges zeroed -------------------------
         const uint32_t pfull0 = map_to_peer(&pfull[0], 0);
         TreeRing rv;
@@ -326,13 +340,13 @@ __global__ void __launch_bounds__(kTpThreads, 1)
                 __syncwarp();
             }
         }
-    } else if (warp < 8) {
+    } else if (warp < SOFT) {
         // -------------------------------- softmax and epilogue ----------------------------------
         const int w = warp >> 2, r = threadIdx.x & 127;  // group; row of this CTA = TMEM lane
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-        const uint32_t tO = tmem + kTpO + 128 * w + lanes;
+        const uint32_t tO = tmem + kTpO + O_COLS * w + lanes;
         const uint32_t p_full0 = map_to_peer(p_full, 0), o_free0 = map_to_peer(o_free, 0);
-        int T = 0, ord = 0, in_b = -1, in_rt = -1;  // T: tile of the share
+        int T = 0, ord = 0, in_b = -1, in_rt = -1, mx_at = 0;  // T: tile of the share
         TreeRow row;
         bool more = share.next(mp, U);
         for (; more; ++ord) {
@@ -348,30 +362,41 @@ __global__ void __launch_bounds__(kTpThreads, 1)
                 const uint32_t tSP = tmem + kTpS + 128 * buf + lanes;
                 if (ok) ok = mbar_wait(&s_full[buf], (T >> 1) & 1, p.err);
                 tc_fence_after();
-                float s[64];
+                float s[COLS];
                 {
-                    uint32_t v0[32], v1[32];
-                    tmem_ld32(tSP + 64 * w, v0);
-                    tmem_ld32(tSP + 64 * w + 32, v1);
+                    uint32_t v[COLS / 32][32];
+#pragma unroll
+                    for (int i = 0; i < COLS / 32; ++i) tmem_ld32(tSP + COLS * w + 32 * i, v[i]);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        s[e] = __uint_as_float(v0[e]);
-                        s[32 + e] = __uint_as_float(v1[e]);
-                    }
+                    for (int e = 0; e < COLS; ++e) s[e] = __uint_as_float(v[e / 32][e % 32]);
                 }
                 tc_fence_before();  // (P takes the place of S behind the groups' barrier)
                 float sl2 = p.scale_log2;  // scale > 0: the raw maximum scales to the maximum
+                const int kt0 = U.k_begin + t * kTpKeys + COLS * w;
                 if constexpr (SOFTCAP) {
-                    tree_cap64(s, p);
+                    tree_mask(s, row, kt0, U.sq.base, 0.f);  // (they may be NaN)
+                    tree_cap(s, p);
                     sl2 = 1.f;
                 }
-                tree_mask64(s, row, U.k_begin + t * kTpKeys + 64 * w, U.sq.base);
-                float mx = tree_max64(s) * sl2;
-                float* mxb = mxs + buf * 256;
-                mxb[w * 128 + r] = mx;
-                named_bar_sync(1, 256);
-                mx = fmaxf(mx, mxb[(w ^ 1) * 128 + r]);
+                tree_mask(s, row, kt0, U.sq.base, -INFINITY);
+                float mx = tree_max(s) * sl2;
+                // the row's maximum over the groups (of two, an exchange: 2 us less of 178 for 16 trees of 512
+                // rows over 16k keys than the atomics; of four, it would take 4 KB more than there are)
+                if constexpr (GROUPS == 2) {
+                    float* mxb = reinterpret_cast<float*>(mxs) + buf * 256;
+                    mxb[w * 128 + r] = mx;
+                    named_bar_sync(1, 32 * SOFT);
+                    mx = fmaxf(mx, mxb[(w ^ 1) * 128 + r]);
+                } else {
+                    // three places in turn: the one that the tile after the next takes was read by all
+                    // before this barrier
+                    atomicMax(mxs + mx_at * 128 + r, tp_ordered(__float_as_int(mx)));
+                    named_bar_sync(1, 32 * SOFT);
+                    mx = __int_as_float(tp_ordered(mxs[mx_at * 128 + r]));
+                    mx_at = mx_at == 2 ? 0 : mx_at + 1;
+                    if (w == 0) mxs[(mx_at == 2 ? 0 : mx_at + 1) * 128 + r] = INT_MIN;
+                }
                 tc_fence_after();
                 const float m_prev = m;
                 if (mx > m + kTrLazyLog2) {
@@ -386,7 +411,7 @@ __global__ void __launch_bounds__(kTpThreads, 1)
                     tc_fence_after();
                     const float alpha = moved ? fast_exp2(m_prev - m) : 1.f;
 #pragma unroll 1
-                    for (int j = 0; j < 4; ++j) {
+                    for (int j = 0; j < O_COLS / 32; ++j) {
                         uint32_t v[32];
                         tmem_ld32(tO + j * 32, v);
                         tmem_ld_wait();
@@ -397,9 +422,9 @@ __global__ void __launch_bounds__(kTpThreads, 1)
                     }
                     tmem_st_wait();
                 }
-                uint32_t pw[32];
-                l += tree_exp64(s, sl2, m == -INFINITY ? 0.f : -m, pw);
-                tmem_st32(tSP + 32 * w, pw);
+                uint32_t pw[COLS / 2];
+                l += tree_exp(s, sl2, m == -INFINITY ? 0.f : -m, pw);
+                tmem_store(tSP + COLS / 2 * w, pw);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -412,29 +437,41 @@ __global__ void __launch_bounds__(kTpThreads, 1)
             more = share.next(mp, U);
             if (ok) ok = mbar_wait(o_full, ord & 1, p.err);
             tc_fence_after();
-            // the row's sum over both groups; the other parity's maxima have been read by all
-            float* lx = mxs + (T & 1) * 256;
-            lx[w * 128 + r] = l;
-            named_bar_sync(2, 256);
-            l += lx[(w ^ 1) * 128 + r];
-            named_bar_sync(2, 256);  // (before the next tile's maxima)
+            // the row's sum over the groups
+            if constexpr (GROUPS == 2) {
+                // (in the place of the other parity's maxima, which have been read by all)
+                float* lx = reinterpret_cast<float*>(mxs) + (T & 1) * 256;
+                lx[w * 128 + r] = l;
+                named_bar_sync(2, 32 * SOFT);
+                l += lx[(w ^ 1) * 128 + r];
+                named_bar_sync(2, 32 * SOFT);  // (before the next tile's maxima)
+            } else {
+                if (w >= 2) lxs[(w - 2) * 128 + r] = l;
+                named_bar_sync(2, 32 * SOFT);
+                if (w < 2) l += lxs[w * 128 + r];
+                if (w == 1) lxs[128 + r] = l;
+                named_bar_sync(2, 32 * SOFT);
+                if (w == 0) lxs[r] = l += lxs[128 + r];
+                named_bar_sync(2, 32 * SOFT);
+                l = lxs[r];
+            }
             const int n_rows = p.n_tok * p.G - (D0.rt * kTpRows + 128 * (int)c);  // of this CTA
             const bool idle = __all_sync(0xffffffffu, row0.lo == INT_MAX);
             const int tk = R / p.G;
             __nv_bfloat16* out =
                 reinterpret_cast<__nv_bfloat16*>(p.out) +
                 (((size_t)D0.b * p.n_tok + tk) * p.n_q + D0.kvh * p.G + (R - tk * p.G)) * (size_t)D +
-                256 * D0.half + 128 * w;
+                256 * D0.half + O_COLS * w;
             const size_t piece = (size_t)max(D0.slot, 0) * 2 + c;
-            float4* part = reinterpret_cast<float4*>(mp.part_o) + (piece * 64 + 32 * w) * 128 + r;
+            float4* part = reinterpret_cast<float4*>(mp.part_o) + (piece * 64 + O_COLS / 4 * w) * 128 + r;
             if (D0.slot >= 0 && w == 0) mp.part_ml[piece * 128 + r] = make_float2(m, l);
             const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
 #pragma unroll 1
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < O_COLS / 32; ++j) {
                 uint32_t v[32];
                 tmem_ld32(tO + j * 32, v);
                 tmem_ld_wait();
-                if (j == 3) {  // O has been read
+                if (j == O_COLS / 32 - 1) {  // O has been read
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_remote(o_free0);
@@ -458,7 +495,7 @@ __global__ void __launch_bounds__(kTpThreads, 1)
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // no CTA arrives on another's barriers any more
-    if (warp == 9) {
+    if (warp == SOFT + 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem, 512);
     }
@@ -481,11 +518,12 @@ TpScratch tp_scratch(int batch, int workers) {
     return s;
 }
 
-template <int D>
+template <int D, bool SOFTCAP>
 cudaError_t launch_tp(const TreeParams& tree, int batch, void* workspace, int workers,
                       cudaStream_t st) {
-    using Lay = TpLay<D>;
+    using Lay = TpLay<D, SOFTCAP>;
     const RowsParams& p = tree.p;
+    auto kernel = tree_pair_kernel<D, SOFTCAP>;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -495,7 +533,7 @@ cudaError_t launch_tp(const TreeParams& tree, int batch, void* workspace, int wo
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see pdl_wait
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.gridDim = dim3(2 * workers);
-    cfg.blockDim = dim3(kTpThreads);
+    cfg.blockDim = dim3(Lay::THREADS);
     cfg.dynamicSmemBytes = Lay::SMEM;
     cfg.stream = st;
     cfg.attrs = attr;
@@ -507,12 +545,9 @@ cudaError_t launch_tp(const TreeParams& tree, int batch, void* workspace, int wo
     int fit = dev >= 0 && dev < 64 ? clusters_fit[dev].load(std::memory_order_relaxed) : 0;
     if (fit <= 0) {
         cudaError_t e = cudaFuncSetAttribute(
-            tree_pair_kernel<D, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
-        if (e == cudaSuccess)
-            e = cudaFuncSetAttribute(tree_pair_kernel<D, true>,
-                                     cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
+            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
         if (e != cudaSuccess) return e;
-        e = cudaOccupancyMaxActiveClusters(&fit, tree_pair_kernel<D, false>, &cfg);
+        e = cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg);
         if (e != cudaSuccess) return e;
         if (fit < 1) return cudaErrorInvalidConfiguration;
         if (dev >= 0 && dev < 64) clusters_fit[dev].store(fit, std::memory_order_relaxed);
@@ -545,7 +580,6 @@ cudaError_t launch_tp(const TreeParams& tree, int batch, void* workspace, int wo
     mp.part_o = reinterpret_cast<float*>(base);
     mp.part_ml = reinterpret_cast<float2*>(base + ws.ml_off);
     mp.before = reinterpret_cast<int32_t*>(base + ws.before_off);
-    auto kernel = p.softcap > 0.f ? tree_pair_kernel<D, true> : tree_pair_kernel<D, false>;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, km, vm, qm, mp);
     return e == cudaSuccess ? launch_tree_merge(mp, D, kTpRows, st) : e;
 }
@@ -556,8 +590,13 @@ size_t tree_pair_workspace(int batch, int workers) { return tp_scratch(batch, wo
 
 cudaError_t launch_tree_pair(const TreeParams& tp, int head_dim, int batch, void* workspace,
                              int workers, cudaStream_t st) {
-    if (head_dim == 256) return launch_tp<256>(tp, batch, workspace, workers, st);
-    if (head_dim == 512) return launch_tp<512>(tp, batch, workspace, workers, st);
+    const bool cap = tp.p.softcap > 0.f;
+    if (head_dim == 256)
+        return cap ? launch_tp<256, true>(tp, batch, workspace, workers, st)
+                   : launch_tp<256, false>(tp, batch, workspace, workers, st);
+    if (head_dim == 512)
+        return cap ? launch_tp<512, true>(tp, batch, workspace, workers, st)
+                   : launch_tp<512, false>(tp, batch, workspace, workers, st);
     return cudaErrorInvalidValue;
 }
 

@@ -2,11 +2,10 @@
 // 5th-generation tensor cores (tcgen05, one SM per tile). Definition in tree_attn.cu.
 //
 // A unit is one KV head of one sequence and 128 of its rows (nodes x G query heads). Per tile of 64
-// keys: S = Q K^T (M 128, N 64) into tensor memory, softmax by four warps (a thread per row), P as
-// bf16 back into tensor memory, O += P V (N = head_dim). With 64 rows of head_dim 256 a tile's
-// 64 KB take longer to arrive (1.45 us when all SMs load) than the tensor core (0.8 us) or the
-// softmax (0.6 us) needs, so the tile rate is that of memory, and what is left to lose is the start,
-// the end and the change from one unit to the next:
+// keys: S = Q K^T (M 128, N 64) into tensor memory, softmax by four warps (a thread per row; eight with a
+// soft-cap), P as bf16 back into tensor memory, O += P V (N = head_dim). A tile takes 1.1 us at head_dim
+// 256 where its 64 KB are there in time; when all SMs load, memory gives 6.1 TB/s or a tile in 1.6 us, so
+// what is left to lose is the start, the end and the change from one unit to the next:
 //  - the key tiles of all units form one sequence (lengths are known on the device alone), of which
 //    every CTA takes an equal share; every warp works out the share by itself, from a scan of the
 //    lengths, before the first barrier wait;
@@ -14,10 +13,13 @@
 //  - S and P have two buffers each, so that S(t + 1) and P V(t - 1) run beside the softmax of t, and
 //    loads run ahead, into the next unit too;
 //  - a unit cut between CTAs leaves parts (O fp32 as it stands in tensor memory, four columns of all
-//    rows after another, so that stores are of 512 consecutive bytes) for tree_merge_kernel.
-// Warps: 0-3 softmax and epilogue, 4 loads K and V, 6 loads Q (the wait for the last S of the part
-// before must not hold back the next part's keys), 5 issues S and 7 P V (one thread issuing both lost
-// 1000 of 2960 cycles per tile in its waits).
+//    rows after another, so that stores are of 512 consecutive bytes) for tree_merge_kernel; or, where
+//    there are few units, a cluster shares a unit out and merges through distributed shared memory.
+// Measured: 16 trees of 32 over a ring of 1024 (128 units of 64 rows, head_dim 256) 30 us, 4.8 TB/s; one
+// tree of 8 over a window of 512, 9 us.
+// Warps: softmax and epilogue, then one that loads K and V, one that issues S, one that loads Q (the wait
+// for the last S of the part before must not hold back the next part's keys) and one that issues P V (one
+// thread issuing both lost 1000 of 2960 cycles per tile in its waits).
 #include <atomic>
 #include <type_traits>
 
@@ -31,7 +33,6 @@ namespace gemma {
 
 namespace {
 
-constexpr int kTcThreads = 256;
 constexpr int kTcRows = 128;
 constexpr int kTcKeys = kTreeKeyTile;
 constexpr int kTcMaxSlots = 12;
@@ -41,15 +42,23 @@ constexpr int kTcQBox = kTcRows * 128;
 // TMEM columns: O, S (two buffers), P (two buffers of packed bf16)
 constexpr int kTcO = 0, kTcS = 256, kTcP = 384;
 
-template <int D>
+template <int D, bool SOFTCAP>
 struct TcLay {
+    // Groups of four softmax warps: a tile with a soft-cap is bound by the softmax. One / two, 152 units of
+    // 4096 keys, head_dim 256, no cap 97 us, a cap of 10 times the scores 102 / 98, of twice 153 / 105.
+    static constexpr int GROUPS = SOFTCAP ? 2 : 1;
+    static constexpr int SOFT = 4 * GROUPS;                          // softmax warps
+    static constexpr int THREADS = 32 * (SOFT + 4);
+    static constexpr int COLS = kTcKeys / GROUPS, O_COLS = D / GROUPS;  // a group's columns of S and O
     static constexpr int SLOT = kTcKeys * D * 2;
+    static constexpr int EXTRA = 2 * 2 * 128 * 4 + 512;              // row maxima, barriers
     static constexpr int Q = kTcRows * D * 2;
-    static constexpr int FIT = (232448 - Q - 1024 - 512) / SLOT;
+    static constexpr int FIT = (232448 - Q - EXTRA) / SLOT;
     static constexpr int SLOTS = FIT > kTcMaxSlots ? kTcMaxSlots : FIT;
     static constexpr int Q_OFF = SLOTS * SLOT;
-    static constexpr int BAR_OFF = Q_OFF + Q;
-    static constexpr int SMEM = BAR_OFF + 512 + 1024;  // + alignment slack
+    static constexpr int MX_OFF = Q_OFF + Q;                         // row maxima [2][2 groups][128]
+    static constexpr int BAR_OFF = MX_OFF + EXTRA - 512;
+    static constexpr int SMEM = BAR_OFF + 512;
     static_assert(SMEM <= 232448 && (2 * kTcMaxSlots + 13) * 8 + 4 <= 512, "shared memory budget");
     // CTAs of two clusters that waited for each other's tensor memory would wait for ever
     static_assert(2 * (SMEM + 1024) > 228 * 1024, "one CTA per SM");
@@ -76,19 +85,19 @@ constexpr int kTcTileNs = 1150, kTcShareNs = 1630, kTcMergeNs = 6000;
 // CLUSTER: a unit to each cluster of tp.workers CTAs, which share out its key tiles and merge their
 // O through distributed shared memory (or, one CTA, write it): no second launch, no workspace
 template <int D, bool SOFTCAP, bool CLUSTER>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ CUtensorMap qmap, const MergeParams tp) {
-    using Lay = TcLay<D>;
-    constexpr int S = Lay::SLOTS;
+    using Lay = TcLay<D, SOFTCAP>;
+    constexpr int S = Lay::SLOTS, GROUPS = Lay::GROUPS, SOFT = Lay::SOFT, COLS = Lay::COLS, O_COLS = Lay::O_COLS;
     pdl_launch_dependents();
     const RowsParams& p = tp.tp.p;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t tc_smem[];
+    uint8_t* smem = tc_smem;
     uint8_t* ring = smem;
     uint8_t* sQ = smem + Lay::Q_OFF;  // [D / 64][128][64] bf16
+    float* mxs = reinterpret_cast<float*>(smem + Lay::MX_OFF);  // [2][2][128]
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + Lay::BAR_OFF);
     uint64_t* empty = full + kTcMaxSlots;   // the MMAs that read the slot have completed
     uint64_t* q_full = empty + kTcMaxSlots;
@@ -106,7 +115,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // barriers it waits on: a parity wait two phases behind passes at once.
     const int nk = nops == 2 ? (S + 1) / 2 : S, nv = S - nk;
 
-    if (warp == 4) {
+    if (warp == SOFT) {
         if (lane == 0) {
             prefetch_map(&kmap);
             prefetch_map(&qmap);
@@ -117,18 +126,18 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&s_full[i], 1);
-                mbar_init(&s_free[i], 4);
-                mbar_init(&p_full[i], 4);
+                mbar_init(&s_free[i], SOFT);
+                mbar_init(&p_full[i], SOFT);
                 mbar_init(&pv_done[i], 1);
             }
             mbar_init(q_full, 1);
             mbar_init(q_free, 1);
             mbar_init(o_full, 1);
-            mbar_init(o_free, 4);
+            mbar_init(o_free, SOFT);
             fence_barrier_init();
         }
         __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp == SOFT + 1) {
         tmem_alloc(tslot, 512);
         tmem_relinquish();
     }
@@ -146,7 +155,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // softmax warps: the row's reference and sum (of the last part)
     float m = -INFINITY, l = 0.f;
 
-    if (warp == 4) {
+    if (warp == SOFT) {
         // ------------------------------------ TMA producer --------------------------------------
         // K(0), V(0), K(1), ...
         TreeUnit U;
@@ -184,7 +193,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 6) {
+    } else if (warp == SOFT + 2) {
         // ------------------------------------- Q rows -------------------------------------------
         // a part's, once the last S of the part before has read the buffer
         TreeUnit U;
@@ -202,11 +211,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
         }
         if (ord > 0 && ok) mbar_wait(q_free, (ord - 1) & 1, p.err);  // (landed before the CTA exits)
-    } else if (warp == 5 || warp == 7) {
-        // ---------------------------- MMA issuers: S (5) and P V (7) ----------------------------
+    } else if (warp == SOFT + 1 || warp == SOFT + 3) {
+        // ------------------------------ MMA issuers: S and P V ----------------------------------
         // An MMA is accepted only when the one before it is nearly done, so what an issuer spends
         // in waits is lost to the tensor core unless another one issues meanwhile.
-        const bool is_s = warp == 5;
+        const bool is_s = warp == SOFT + 1;
         const uint32_t id_s = idesc_bf16(128, kTcKeys, 0, 0), id_pv = idesc_bf16(128, D, 0, 1);
         const uint64_t qd = smem_desc_sw128(smem_u32(sQ), 0, 1024);
         bool ok = true;
@@ -273,9 +282,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
     } else {
         // -------------------------------- softmax and epilogue ----------------------------------
-        const int r = threadIdx.x;  // row of the tile = TMEM lane
-        const uint32_t lanes = (uint32_t)(32 * warp) << 16;
-        const uint32_t tO = tmem + kTcO + lanes;
+        const int w = GROUPS == 1 ? 0 : warp >> 2, r = threadIdx.x & 127;  // group; row of the tile = TMEM lane
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t tO = tmem + kTcO + O_COLS * w + lanes;
         bool ok = true;
         TreeUnit U;
         int T = 0, ord = 0, in_b = -1, in_rt = -1;  // T: tile of the share
@@ -301,10 +310,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (T >= 2 && ok) ok = mbar_wait(&pv_done[buf], ((T >> 1) - 1) & 1, p.err);
                     if (t < 2) {
                         tc_fence_after();
-                        uint32_t z[32];
+                        uint32_t z[COLS / 2];
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) z[e] = 0u;
-                        tmem_st32(tmem + kTcP + 32 * buf + lanes, z);
+                        for (int e = 0; e < COLS / 2; ++e) z[e] = 0u;
+                        tmem_store(tmem + kTcP + 32 * buf + COLS / 2 * w + lanes, z);
                         tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
@@ -312,28 +321,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     if (lane == 0) mbar_arrive(&p_full[buf]);
                     continue;
                 }
-                float s[64];
+                float s[COLS];
                 {
-                    uint32_t v0[32], v1[32];
-                    tmem_ld32(tmem + kTcS + 64 * buf + lanes, v0);
-                    tmem_ld32(tmem + kTcS + 64 * buf + 32 + lanes, v1);
+                    uint32_t v[COLS / 32][32];
+#pragma unroll
+                    for (int i = 0; i < COLS / 32; ++i)
+                        tmem_ld32(tmem + kTcS + 64 * buf + COLS * w + 32 * i + lanes, v[i]);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        s[e] = __uint_as_float(v0[e]);
-                        s[32 + e] = __uint_as_float(v1[e]);
-                    }
+                    for (int e = 0; e < COLS; ++e) s[e] = __uint_as_float(v[e / 32][e % 32]);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_free[buf]);  // S(T + 2) may overwrite it
                 float sl2 = p.scale_log2;  // scale > 0: the raw maximum scales to the maximum
+                const int kt0 = U.k_begin + t * kTcKeys + COLS * w;
                 if constexpr (SOFTCAP) {
-                    tree_cap64(s, p);
+                    tree_mask(s, row, kt0, base, 0.f);  // (they may be NaN)
+                    tree_cap(s, p);
                     sl2 = 1.f;
                 }
-                tree_mask64(s, row, U.k_begin + t * kTcKeys, base);
-                const float mx = tree_max64(s) * sl2;
+                tree_mask(s, row, kt0, base, -INFINITY);
+                float mx = tree_max(s) * sl2;
+                if constexpr (GROUPS == 2) {  // the row's maximum over both groups
+                    float* mxb = mxs + buf * 256;
+                    mxb[w * 128 + r] = mx;
+                    named_bar_sync(1 + (warp & 3), 64);
+                    mx = fmaxf(mx, mxb[(w ^ 1) * 128 + r]);
+                }
                 const float m_prev = m;
                 if (mx > m + kTrLazyLog2) {
                     l = m == -INFINITY ? 0.f : l * fast_exp2(m - mx);
@@ -347,7 +362,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     tc_fence_after();
                     const float alpha = moved ? fast_exp2(m_prev - m) : 1.f;
 #pragma unroll 1
-                    for (int j = 0; j < D / 32; ++j) {
+                    for (int j = 0; j < O_COLS / 32; ++j) {
                         uint32_t v[32];
                         tmem_ld32(tO + j * 32, v);
                         tmem_ld_wait();
@@ -358,18 +373,27 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     }
                     tmem_st_wait();
                 }
-                uint32_t pw[32];
-                l += tree_exp64(s, sl2, m == -INFINITY ? 0.f : -m, pw);
+                uint32_t pw[COLS / 2];
+                l += tree_exp(s, sl2, m == -INFINITY ? 0.f : -m, pw);
                 // the buffer is free once P V(T - 2) has completed
                 if (T >= 2 && ok) ok = mbar_wait(&pv_done[buf], ((T >> 1) - 1) & 1, p.err);
                 tc_fence_after();
-                tmem_st32(tmem + kTcP + 32 * buf + lanes, pw);
+                tmem_store(tmem + kTcP + 32 * buf + COLS / 2 * w + lanes, pw);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[buf]);
             }
             // ---- the part's results ----
+            if constexpr (GROUPS == 2) {
+                // the row's sum over both groups, in the place of the other parity's maxima, which have
+                // been read by both
+                float* lx = mxs + (T & 1) * 256;
+                lx[w * 128 + r] = l;
+                named_bar_sync(1 + (warp & 3), 64);
+                l += lx[(w ^ 1) * 128 + r];
+                named_bar_sync(1 + (warp & 3), 64);  // (before the next tile's maxima)
+            }
             if (ok) ok = mbar_wait(o_full, ord & 1, p.err);
             tc_fence_after();
             if (CLUSTER && n_cta > 1) continue;
@@ -377,16 +401,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             const int tk = R / p.G;
             __nv_bfloat16* out =
                 reinterpret_cast<__nv_bfloat16*>(p.out) +
-                (((size_t)U.b * p.n_tok + tk) * p.n_q + U.kvh * p.G + (R - tk * p.G)) * (size_t)D;
-            float4* part = reinterpret_cast<float4*>(tp.part_o) + (size_t)max(U.slot, 0) * (D / 4) * kTcRows + r;
-            if (U.slot >= 0) tp.part_ml[(size_t)U.slot * kTcRows + r] = make_float2(m, l);
+                (((size_t)U.b * p.n_tok + tk) * p.n_q + U.kvh * p.G + (R - tk * p.G)) * (size_t)D + O_COLS * w;
+            float4* part = reinterpret_cast<float4*>(tp.part_o) + ((size_t)max(U.slot, 0) * (D / 4) + O_COLS / 4 * w) * kTcRows + r;
+            if (U.slot >= 0 && w == 0) tp.part_ml[(size_t)U.slot * kTcRows + r] = make_float2(m, l);
             const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
 #pragma unroll 1
-            for (int j = 0; j < D / 32; ++j) {
+            for (int j = 0; j < O_COLS / 32; ++j) {
                 uint32_t v[32];
                 tmem_ld32(tO + j * 32, v);
                 tmem_ld_wait();
-                if (j == D / 32 - 1) {  // O has been read
+                if (j == O_COLS / 32 - 1) {  // O has been read
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(o_free);
@@ -411,14 +435,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // and sends every CTA its slice of the columns; then each adds up its slice. The buffers are the
         // ring and the Q rows, which nobody reads any more behind the first barrier.
         const TreeUnit& U = share.U;
-        const int r = threadIdx.x, R = U.rt * kTcRows + r;
+        const int w = GROUPS == 1 ? 0 : warp >> 2, r = threadIdx.x & 127, R = U.rt * kTcRows + r;
         const int n_rows = min(kTcRows, p.n_tok * p.G - U.rt * kTcRows), tk = R / p.G;
         __nv_bfloat16* out =
             reinterpret_cast<__nv_bfloat16*>(p.out) +
             (((size_t)U.b * p.n_tok + tk) * p.n_q + U.kvh * p.G + (R - tk * p.G)) * (size_t)D;
-        if (U.sq.bad && U.kvh == 0 && U.rt == 0 && cta == 0 && r == 0) report(p.err, U.sq.bad);
+        if (U.sq.bad && U.kvh == 0 && U.rt == 0 && cta == 0 && threadIdx.x == 0) report(p.err, U.sq.bad);
         if (n_cta == 1) {
-            if (U.n_tiles == 0 && r < n_rows)  // no nodes
+            if (U.n_tiles == 0 && warp < 4 && r < n_rows)  // no nodes
                 for (int j = 0; j < D / 8; ++j)
                     reinterpret_cast<uint4*>(out)[j] = make_uint4(0u, 0u, 0u, 0u);
         } else {
@@ -429,7 +453,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             tc_fence_after();
             float L = 0.f;
             uint32_t have = 0;  // CTAs that had keys of this row
-            if (warp < 4) {
+            if (warp < SOFT) {
                 float M = -INFINITY;
                 float2 ml[kTcMaxCluster];
 #pragma unroll
@@ -448,10 +472,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                     L = fmaf(fast_exp2(ml[k].x - M), ml[k].y, L);
                 }
                 if (__any_sync(0xffffffffu, have >> cta & 1)) {
-                    const float w = m == -INFINITY ? 0.f : fast_exp2(m - M);
-                    const uint32_t lanes = (uint32_t)(32 * warp) << 16;
+                    const float a = m == -INFINITY ? 0.f : fast_exp2(m - M);
+                    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
 #pragma unroll 1
-                    for (int j = 0; j < D / 32; ++j) {
+                    for (int j = w * (O_COLS / 32); j < (w + 1) * (O_COLS / 32); ++j) {
                         uint32_t v[32];
                         tmem_ld32(tmem + kTcO + lanes + j * 32, v);
                         tmem_ld_wait();
@@ -460,16 +484,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                             const int col = j * 32 + 4 * q, to = col >> lg, c4 = (col & (slice - 1)) >> 2;
                             st_cluster_f32x4(
                                 map_to_peer(ring + ((size_t)(cta * (slice / 4) + c4) * kTcRows + r) * 16, to),
-                                __uint_as_float(v[4 * q]) * w, __uint_as_float(v[4 * q + 1]) * w,
-                                __uint_as_float(v[4 * q + 2]) * w, __uint_as_float(v[4 * q + 3]) * w);
+                                __uint_as_float(v[4 * q]) * a, __uint_as_float(v[4 * q + 1]) * a,
+                                __uint_as_float(v[4 * q + 2]) * a, __uint_as_float(v[4 * q + 3]) * a);
                         }
                     }
                 }
             }
             cluster_sync();
-            if (warp < 4 && r < n_rows) {
+            if (warp < SOFT && r < n_rows) {
                 const float inv = 1.f / L;
-                for (int c8 = 0; c8 < slice / 8; ++c8) {
+                for (int c8 = w; c8 < slice / 8; c8 += GROUPS) {
                     float a[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) a[e] = 0.f;
@@ -497,7 +521,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 5) {
+    if (warp == SOFT + 1) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -520,24 +544,22 @@ TcScratch tc_scratch(int head_dim, int batch, int workers) {
     return s;
 }
 
-template <int D>
+template <int D, bool SOFTCAP>
 cudaError_t launch_tc(const TreeParams& tree, int batch, void* workspace, int workers, int cluster,
                       cudaStream_t st) {
-    using Lay = TcLay<D>;
+    using Lay = TcLay<D, SOFTCAP>;
     const RowsParams& p = tree.p;
     using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, MergeParams);
-    const Kernel kernels[2][2] = {{tree_tc_kernel<D, false, false>, tree_tc_kernel<D, true, false>},
-                                  {tree_tc_kernel<D, false, true>, tree_tc_kernel<D, true, true>}};
+    const Kernel kernels[2] = {tree_tc_kernel<D, SOFTCAP, false>, tree_tc_kernel<D, SOFTCAP, true>};
     static std::atomic<bool> configured[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
     if (dev < 0 || dev >= 64 || !configured[dev].load(std::memory_order_relaxed)) {
-        for (const auto& row : kernels)
-            for (Kernel k : row) {
-                const cudaError_t e = cudaFuncSetAttribute(
-                    k, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
-                if (e != cudaSuccess) return e;
-            }
+        for (Kernel k : kernels) {
+            const cudaError_t e =
+                cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::SMEM);
+            if (e != cudaSuccess) return e;
+        }
         if (dev >= 0 && dev < 64) configured[dev].store(true, std::memory_order_relaxed);
     }
     CUtensorMap km, vm, qm;
@@ -561,11 +583,11 @@ cudaError_t launch_tc(const TreeParams& tree, int batch, void* workspace, int wo
     tp.n_rt = (p.n_tok * p.G + kTcRows - 1) / kTcRows;
     tp.workers = cluster ? cluster : workers;
     tp.keys = kTcKeys;
-    const Kernel kernel = kernels[cluster > 0][p.softcap > 0.f];
+    const Kernel kernel = kernels[cluster > 0];
     if (cluster) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(tp.n_rt * batch * p.n_kv * cluster));
-        cfg.blockDim = dim3(kTcThreads);
+        cfg.blockDim = dim3(Lay::THREADS);
         cfg.dynamicSmemBytes = Lay::SMEM;
         cfg.stream = st;
         cudaLaunchAttribute attr[2];
@@ -585,7 +607,7 @@ cudaError_t launch_tc(const TreeParams& tree, int batch, void* workspace, int wo
     tp.part_ml = reinterpret_cast<float2*>(base + ws.ml_off);
     tp.before = reinterpret_cast<int32_t*>(base + ws.before_off);
     const cudaError_t e =
-        launch_pdl(kernel, dim3(workers), dim3(kTcThreads), Lay::SMEM, st, km, vm, qm, tp);
+        launch_pdl(kernel, dim3(workers), dim3(Lay::THREADS), Lay::SMEM, st, km, vm, qm, tp);
     return e == cudaSuccess ? launch_tree_merge(tp, D, kTcRows, st) : e;
 }
 
@@ -602,12 +624,12 @@ static int clusters_fit(int cluster) {
         if (n > 0) return n;
     }
     if (cudaFuncSetAttribute(tree_tc_kernel<D, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             TcLay<D>::SMEM) != cudaSuccess)
+                             TcLay<D, false>::SMEM) != cudaSuccess)
         return 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(cluster * 64);
-    cfg.blockDim = dim3(kTcThreads);
-    cfg.dynamicSmemBytes = TcLay<D>::SMEM;
+    cfg.blockDim = dim3(TcLay<D, false>::THREADS);
+    cfg.dynamicSmemBytes = TcLay<D, false>::SMEM;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
     attr.val.clusterDim.x = (unsigned)cluster;
@@ -636,10 +658,13 @@ size_t tree_tc_workspace(int head_dim, int batch, int workers) {
 
 cudaError_t launch_tree_tc(const TreeParams& tp, int head_dim, int batch, void* workspace,
                            int workers, int cluster, cudaStream_t st) {
+    auto launch = [&](auto plain, auto capped) {
+        return (tp.p.softcap > 0.f ? capped : plain)(tp, batch, workspace, workers, cluster, st);
+    };
     switch (head_dim) {
-        case 64: return launch_tc<64>(tp, batch, workspace, workers, cluster, st);
-        case 128: return launch_tc<128>(tp, batch, workspace, workers, cluster, st);
-        case 256: return launch_tc<256>(tp, batch, workspace, workers, cluster, st);
+        case 64: return launch(launch_tc<64, false>, launch_tc<64, true>);
+        case 128: return launch(launch_tc<128, false>, launch_tc<128, true>);
+        case 256: return launch(launch_tc<256, false>, launch_tc<256, true>);
     }
     return cudaErrorInvalidValue;
 }

@@ -20,9 +20,11 @@ WAYS = [(8, 8, 64, 16, [2600] * 5, torch.bfloat16),       # a warp's matrix inst
 
 class Capped(Problem):
     def tolerance(self, ref, mass, size, d, n_keys):
-        """The bound without a cap, and for the cap a score's relative error: tanh's series is off by
-        0.0036 x^12 < 2^-20 of itself up to |x| = 1/2, and above that 1 - 2 / (1 + e^2x) by at most 2^-22
-        of 1, against a tanh of 0.46; with their own roundings 2^-19 covers both (twice: the normaliser)."""
+        """The bound without a cap, and what the cap adds to a score: tanh's series is off by 0.0036 x^12
+        < 2^-20 of itself up to |x| = 1/2; rows with larger scores take 1 - 2 / (1 + e^2x), off by r (an
+        exponential of 2^-22.5, a reciprocal of 2^-23 and three roundings of 2^-24) = 2^-21.2 twice, or
+        2^-20.2 of the cap at most, where the row's largest |x| is above 1/2 and so size above cap / 2:
+        2^-19.2 of size. 2^-19 of size covers both (twice: the normaliser)."""
         cap, self.softcap = self.softcap, 0.0
         bound = super().tolerance(ref, mass, size, d, n_keys)
         self.softcap = cap
