@@ -1,7 +1,7 @@
 // bind.cpp -- the Python calls of the 4-bit cache, of sampling, of drafted trees and of pages:
-// arguments checked and marshalled natively. A decode step makes several of these calls per layer, and marshalled in the interpreter
-// each took longer than its kernels: an attention call 12.1 us of host time, an append 10.4 (the
-// Grace cores); here 3.3 and 3.0, most of it the launch.
+// arguments checked and marshalled natively. A decode step makes several of these calls per layer, and
+// marshalled in the interpreter each took longer than its kernels: an attention call 12.1 us of host
+// time, an append 10.4 (the Grace cores); here 3.3 and 3.0, most of it the launch.
 //
 // binding.py holds the functions' signatures and documentation and passes every argument by
 // position. Nothing is kept from one call to the next. Returns the C call's status; a check that

@@ -37,7 +37,8 @@
 //               so the softmax of tile t+1 does not wait for the P V of tile t).
 //   warp 8      TMA producer: each unit's Q rows (once the previous unit's last S has read the
 //               Q buffer) and this CTA's halves of the K and V tiles (128-byte swizzle, boxes of
-//               64 keys x 64 columns) into 32 KB slots (two of K, two of V; one of V at head_dim 512), in the MMA order.
+//               64 keys x 64 columns) into 32 KB slots (two of K, two of V; one of V at head_dim
+//               512), in the MMA order.
 //   warp 9      even CTA: issues S(t) = Q K(t)^T once both CTAs' softmax warps have read S(t-1),
 //               so the softmax of tile t overlaps the P V of tile t-1 and the S of tile t+1.
 //               Odd CTA: forwards each of its ring slots' arrivals to the even CTA's barriers

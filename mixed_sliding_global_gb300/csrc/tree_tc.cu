@@ -15,7 +15,7 @@
 //  - a unit cut between CTAs leaves parts (O fp32 as it stands in tensor memory, four columns of all
 //    rows after another, so that stores are of 512 consecutive bytes) for tree_merge_kernel; or, where
 //    there are few units, a cluster shares a unit out and merges through distributed shared memory.
-// Measured: 16 trees of 32 over a ring of 1024 (128 units of 64 rows, head_dim 256) 30 us, 4.8 TB/s; one
+// Measured: 16 trees of 32 over a ring of 1024 (128 units of 64 rows, head_dim 256) 30 us, 4.9 TB/s; one
 // tree of 8 over a window of 512, 9 us.
 // Warps: softmax and epilogue, then one that loads K and V, one that issues S, one that loads Q (the wait
 // for the last S of the part before must not hold back the next part's keys) and one that issues P V (one
