@@ -3,7 +3,7 @@
 //   M = max_w m_w, out = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w
 // and zeros for row tiles without nodes. A lane has one row and 16 columns: parts lie with four columns
 // of 128 rows after another, so reads are of 512 consecutive bytes, and writes are whole sectors. WAYS
-// warps share out the parts (few units are cut into many) and meet in shared memory. Latency bound: one
+// warps share out the parts (few units are cut into many), BATCH at a time, and meet in shared memory. Latency bound: one
 // pass, so that a warp waits for memory twice (lengths, parts).
 #include "common.cuh"
 #include "tree.h"
@@ -11,11 +11,10 @@
 
 namespace gemma {
 
-template <int D, int ROWS, int WAYS>
+template <int D, int ROWS, int WAYS, int BATCH>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeParams mp) {
     pdl_launch_dependents();
     constexpr int COLS = D < 256 ? D : 256;            // of a piece: 128 rows x COLS
-    constexpr int BATCH = WAYS > 4 ? 4 : 2;            // parts in flight per warp
     constexpr int C = ROWS / 128, HALVES = D / COLS;   // pieces of a part; parts of head_dim
     constexpr int SLICES = 8 / WAYS;                   // of 16 columns, per CTA
     constexpr int PER = (D / 16 + SLICES - 1) / SLICES, GROUPS = ROWS / 32;
@@ -134,17 +133,27 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const MergeParams mp) {
 template <int D, int ROWS>
 static cudaError_t launch_merge(const MergeParams& mp, cudaStream_t st) {
     const long long groups = (long long)mp.n_rt * mp.batch * mp.tp.p.n_kv * (ROWS / 32);
-    // Parts per unit, about. In us of the whole step with 1 / 4 / 8 warps to a row and slice: 6 parts
-    // (14 units of 244 rows, head_dim 256) 43.2 / 42.7 / 50.7, 19 parts (one tree of 512 rows, head_dim
-    // 512) 23.3 / 23.0 / 24.3, 64 parts (one unit of 32 rows, head_dim 64) 13.5 / - / 9.4.
+    // Parts per unit, about, decide how many warps share them out and how many of them a warp has in flight;
+    // while the CTAs are fewer than the SMs, twice the warps. In us of the whole step with 1 x 2, 2 x 2, 2 x
+    // 4, 4 x 2, 4 x 4 and 8 x 4: 5 parts (14 units of 244 rows, head_dim 256) 24.7, 23.0, 24.7, 24.9, 26.8, -;
+    // 9 (8 units of 256 rows, head_dim 512) 21.2, 18.6, 18.0, 19.2, 19.7, -; 9 (16 of 64, head_dim 128) 21.2,
+    // 18.3, 17.4, 16.8, 16.4, -; 19 (4 of 256, head_dim 512) 28.6, 25.4, 24.0, 23.1, 22.4, -; 64 (one of 64,
+    // head_dim 64) 20.6, 14.7, 13.3, 11.3, 10.7, 9.3.
     const long long parts = mp.workers / ((long long)mp.n_rt * mp.batch * mp.tp.p.n_kv * (D > 256 ? 2 : 1));
+    const long long warps = groups * (D / 16);
+    int ways = parts < 5 ? 1 : parts < 10 ? 2 : parts < 24 ? 4 : 8;
+    if (ways > 1 && ways < 8 && warps * ways < 8 * 152) ways *= 2;
     auto launch = [&](auto kernel, int slices) {
         return launch_pdl(kernel, dim3((unsigned)(groups * ((D / 16 + slices - 1) / slices))), dim3(256),
                           0, st, mp);
     };
-    if (parts < 4) return launch(tree_merge_kernel<D, ROWS, 1>, 8);
-    if (parts < 24) return launch(tree_merge_kernel<D, ROWS, 4>, 2);
-    return launch(tree_merge_kernel<D, ROWS, 8>, 1);
+    const bool four = parts >= 4 * ways;
+    switch (ways) {
+        case 1: return launch(tree_merge_kernel<D, ROWS, 1, 2>, 8);
+        case 2: return launch(four ? tree_merge_kernel<D, ROWS, 2, 4> : tree_merge_kernel<D, ROWS, 2, 2>, 4);
+        case 4: return launch(four ? tree_merge_kernel<D, ROWS, 4, 4> : tree_merge_kernel<D, ROWS, 4, 2>, 2);
+    }
+    return launch(tree_merge_kernel<D, ROWS, 8, 4>, 1);
 }
 
 cudaError_t launch_tree_merge(const MergeParams& mp, int head_dim, int rows, cudaStream_t st) {
