@@ -975,7 +975,7 @@ enum { kTreeRows, kTreeTc, kTreePair };
 struct TreePlan {
     int path;
     int n_split, chunk;    // kTreeRows: chunks of keys
-    int workers, cluster;  // kTreeTc, kTreePair: equal shares, or kTreeTc: a cluster for each unit
+    int workers, cluster;  // kTreeTc, kTreePair: equal shares, or (cluster > 0) a cluster or pair for each unit
     size_t o_bytes, ws_bytes;
 };
 
@@ -1002,8 +1002,20 @@ TreePlan tree_plan(int batch, int kind, int window, int n_q, int n_kv, int head_
     // Head_dim 512: pairs from 33 rows on, mma.sync before. 32 rows, 4 KV heads, 1024 keys, 1 sequence 14.1
     // on mma.sync, 13.8 on pairs, 32 sequences 53 and 88; 48 rows 21 and 14.3, 137 and 91.
     if (head_dim == 512 ? rows > gemma::kTreeRowsMax : head_dim == 256 && rows > 128) {
-        const long long tiles = tree_tiles(batch, n_kv, rows, 256, reach, 128) * (head_dim / 256);
+        const int halves = head_dim / 256;
+        const long long u = units * ((rows + 255) / 256) * halves, nt = (reach + 127) / 128;
+        const long long tiles = u * nt;
         pl.path = kTreePair;
+        // A pair for each unit, without parts and their merge, where no unit has more than 8 (4) tiles above
+        // an equal share (of one tile, or with all windows full): 8 x 1.4 us, 4 x 2.2. Equal shares / alone,
+        // 14 units of 244 rows, head_dim 256: 2 tiles 11.2 / 9.1 us, 4 15.7 / 11.9, 8 21.2 / 17.7; 16 of 256,
+        // head_dim 512, 4 tiles 17.3 / 13.9.
+        const long long share = kind == GEMMA_GLOBAL ? 1 : (tiles + n_sm / 2 - 1) / (n_sm / 2);
+        if (u <= n_sm / 2 && nt - share <= 8 / halves) {
+            pl.workers = (int)u;
+            pl.cluster = 1;
+            return pl;
+        }
         pl.workers = (int)(tiles < n_sm / 2 ? tiles : n_sm / 2);
         pl.ws_bytes = gemma::tree_pair_workspace(batch, pl.workers);
         return pl;
@@ -1173,7 +1185,7 @@ int gemma_attn_tree(void* out, const void* q, const void* const* k_cache,
     } else if (pl.path == kTreeTc) {
         e = gemma::launch_tree_tc(tp, head_dim, batch, workspace, pl.workers, pl.cluster, s);
     } else if (pl.path == kTreePair) {
-        e = gemma::launch_tree_pair(tp, head_dim, batch, workspace, pl.workers, s);
+        e = gemma::launch_tree_pair(tp, head_dim, batch, workspace, pl.workers, pl.cluster > 0, s);
     } else {
         e = gemma::launch_tree_rows(tp, head_dim, batch, s);
         if (e == cudaSuccess && pl.n_split > 1) e = gemma::launch_tree_combine(tp, head_dim, batch, s);

@@ -19,10 +19,10 @@ struct TreeParams {
 constexpr int kTreeRowsMax = 32;  // rows per KV head of launch_tree_rows
 
 // On CTA pairs (tree_pair.cu), head_dim 256 and 512, any number of rows; the merge included. workers:
-// pairs, one per two SMs at most.
+// pairs, one per two SMs at most; alone: one per unit (no merge, no workspace).
 size_t tree_pair_workspace(int batch, int workers);
 cudaError_t launch_tree_pair(const TreeParams& tp, int head_dim, int batch, void* workspace,
-                             int workers, cudaStream_t st);
+                             int workers, bool alone, cudaStream_t st);
 // On single SMs with tcgen05 (tree_tc.cu), head_dim 64 to 256, any number of rows; the merge included.
 // workers: CTAs, one per SM at most; or a cluster of 1 to 8 CTAs for each unit (cluster > 0; no workspace).
 int tree_tc_clusters(int head_dim, int cluster);  // clusters of 2, 4 or 8 that run at once

@@ -233,17 +233,18 @@ struct TreeShare {
 
 // One unit, or the part of its keys that CTA k of n takes: what a worker does where units are dealt out by
 // the host.
-template <int KEYS, int ROWS>
+template <int KEYS, int ROWS, int HALVES>
 struct TreeAlone {
     TreeUnit U;
     bool more;
     GEMMA_DEVINL void init(const MergeParams& mp, int unit, int k, int n) {
         const RowsParams& p = mp.tp.p;
+        U.half = unit % HALVES;
+        unit /= HALVES;
         const int per = mp.n_rt * p.n_kv;
         U.b = unit / per;
         U.kvh = unit % per / mp.n_rt;
         U.rt = unit % mp.n_rt;
-        U.half = 0;
         U.slot = -1;
         U.sq = tr_seq(p, U.b);
         int live_rt;

@@ -13,7 +13,8 @@
 //  - S has two buffers, and P(t) takes the place of S(t) in its buffer, so that S(t + 1) runs beside
 //    the softmax of t and S(t + 2) waits for P V(t) alone: the tensor core always has an MMA group
 //    that it may start;
-//  - units are cut into equal shares of the key tiles, parts merged by tree_merge_kernel (TreeShare);
+//  - units are cut into equal shares of the key tiles, parts merged by tree_merge_kernel (TreeShare); or,
+//    short ones, a pair has one whole (TreeAlone);
 //  - parts leave O as it stands in tensor memory, four columns of all rows after another, so that
 //    stores are of 512 consecutive bytes;
 //  - barriers, tensor memory and tensor maps are set up before the wait for the previous kernel.
@@ -24,6 +25,7 @@
 // commits arrive in both CTAs.
 #include <atomic>
 #include <climits>
+#include <type_traits>
 
 #include "common.cuh"
 #include "tc.cuh"
@@ -67,13 +69,15 @@ struct TpLay {
 // A float's bits as an integer of the same order, and back.
 GEMMA_DEVINL int tp_ordered(int x) { return x ^ ((x >> 31) & 0x7fffffff); }
 
-template <int D, bool SOFTCAP>
+// ALONE: a unit to each pair, which writes zeros itself where there is nothing: no merge, no workspace
+template <int D, bool SOFTCAP, bool ALONE>
 __global__ void __launch_bounds__(TpLay<D, SOFTCAP>::THREADS, 1)
     tree_pair_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap,
                      const __grid_constant__ CUtensorMap qmap, const MergeParams mp) {
     using Lay = TpLay<D, SOFTCAP>;
-    using PairShare = TreeShare<kTpKeys, kTpRows, Lay::KB>;
+    using PairShare = std::conditional_t<ALONE, TreeAlone<kTpKeys, kTpRows, Lay::KB>,
+                                         TreeShare<kTpKeys, kTpRows, Lay::KB>>;
     constexpr int KB = Lay::KB, NK = Lay::K_SLOTS, NV = Lay::V_SLOTS;
     constexpr int GROUPS = Lay::GROUPS, SOFT = Lay::SOFT, COLS = Lay::COLS, O_COLS = Lay::O_COLS;
     pdl_launch_dependents();
@@ -136,10 +140,14 @@ __global__ void __launch_bounds__(TpLay<D, SOFTCAP>::THREADS, 1)
     const uint32_t tmem = *tslot;
     pdl_wait();  // the previous kernel on the stream has completed
     PairShare share;
-    // (compute bound: a tile takes as long alone as when every SM works, and the parts and their merge as
-    // long as six of them, three at head_dim 512. Whole / cut: 30 units of 10 tiles, head_dim 256, 23.6 /
-    // 25.6 us; 50 of 10, head_dim 512, 32.9 / 36.6; 20 of 5 19.2 / 21.1)
-    share.init(mp, worker, blockIdx.x == 0 && warp == 0, 1000 * KB, 1000 * KB, 6000);
+    if constexpr (ALONE) {
+        share.init(mp, worker, 0, 1);
+    } else {
+        // (compute bound: a tile takes as long alone as when every SM works, and the parts and their merge as
+        // long as six of them, three at head_dim 512. Whole / cut: 30 units of 10 tiles, head_dim 256, 23.6 /
+        // 25.6 us; 50 of 10, head_dim 512, 32.9 / 36.6; 20 of 5 19.2 / 21.1)
+        share.init(mp, worker, blockIdx.x == 0 && warp == 0, 1000 * KB, 1000 * KB, 6000);
+    }
     TreeUnit U{};
     bool ok = true;
 
@@ -492,6 +500,19 @@ __global__ void __launch_bounds__(TpLay<D, SOFTCAP>::THREADS, 1)
         for (int x = max(0, T - 2); x < T && ok; ++x)
             ok = mbar_wait(&pv_done[x & 1], (x >> 1) & 1, p.err);
     }
+    if constexpr (ALONE) {
+        const TreeUnit& X = share.U;
+        const int r = threadIdx.x, n_rows = p.n_tok * p.G - (X.rt * kTpRows + 128 * (int)c);
+        if (X.sq.bad && X.kvh == 0 && X.rt == 0 && X.half == 0 && c == 0 && r == 0) report(p.err, X.sq.bad);
+        if (X.n_tiles == 0 && r < min(128, n_rows)) {  // no nodes
+            const int R = X.rt * kTpRows + 128 * (int)c + r, tk = R / p.G;
+            uint4* out = reinterpret_cast<uint4*>(
+                reinterpret_cast<__nv_bfloat16*>(p.out) +
+                (((size_t)X.b * p.n_tok + tk) * p.n_q + X.kvh * p.G + (R - tk * p.G)) * (size_t)D +
+                256 * X.half);
+            for (int j = 0; j < 32; ++j) out[j] = make_uint4(0u, 0u, 0u, 0u);
+        }
+    }
     tc_fence_before();
     __syncthreads();
     cluster_sync();  // no CTA arrives on another's barriers any more
@@ -518,12 +539,12 @@ TpScratch tp_scratch(int batch, int workers) {
     return s;
 }
 
-template <int D, bool SOFTCAP>
+template <int D, bool SOFTCAP, bool ALONE>
 cudaError_t launch_tp(const TreeParams& tree, int batch, void* workspace, int workers,
                       cudaStream_t st) {
     using Lay = TpLay<D, SOFTCAP>;
     const RowsParams& p = tree.p;
-    auto kernel = tree_pair_kernel<D, SOFTCAP>;
+    auto kernel = tree_pair_kernel<D, SOFTCAP, ALONE>;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -552,7 +573,7 @@ cudaError_t launch_tp(const TreeParams& tree, int batch, void* workspace, int wo
         if (fit < 1) return cudaErrorInvalidConfiguration;
         if (dev >= 0 && dev < 64) clusters_fit[dev].store(fit, std::memory_order_relaxed);
     }
-    if (workers > fit) workers = fit;
+    if (!ALONE && workers > fit) workers = fit;
     cfg.gridDim = dim3(2 * workers);
     CUtensorMap km, vm, qm;
     // [rows][slots][D]: rows = sequences x KV heads (pages x KV heads for a paged pool)
@@ -575,13 +596,15 @@ cudaError_t launch_tp(const TreeParams& tree, int batch, void* workspace, int wo
     mp.n_rt = (p.n_tok * p.G + kTpRows - 1) / kTpRows;
     mp.workers = workers;
     mp.keys = kTpKeys;
-    const TpScratch ws = tp_scratch(batch, workers);
-    uint8_t* base = static_cast<uint8_t*>(workspace);
-    mp.part_o = reinterpret_cast<float*>(base);
-    mp.part_ml = reinterpret_cast<float2*>(base + ws.ml_off);
-    mp.before = reinterpret_cast<int32_t*>(base + ws.before_off);
+    if (!ALONE) {
+        const TpScratch ws = tp_scratch(batch, workers);
+        uint8_t* base = static_cast<uint8_t*>(workspace);
+        mp.part_o = reinterpret_cast<float*>(base);
+        mp.part_ml = reinterpret_cast<float2*>(base + ws.ml_off);
+        mp.before = reinterpret_cast<int32_t*>(base + ws.before_off);
+    }
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, km, vm, qm, mp);
-    return e == cudaSuccess ? launch_tree_merge(mp, D, kTpRows, st) : e;
+    return e == cudaSuccess && !ALONE ? launch_tree_merge(mp, D, kTpRows, st) : e;
 }
 
 }  // namespace
@@ -589,14 +612,18 @@ cudaError_t launch_tp(const TreeParams& tree, int batch, void* workspace, int wo
 size_t tree_pair_workspace(int batch, int workers) { return tp_scratch(batch, workers).bytes; }
 
 cudaError_t launch_tree_pair(const TreeParams& tp, int head_dim, int batch, void* workspace,
-                             int workers, cudaStream_t st) {
+                             int workers, bool alone, cudaStream_t st) {
     const bool cap = tp.p.softcap > 0.f;
+    auto launch = [&](auto plain, auto capped, auto plain_alone, auto capped_alone) {
+        return (alone ? cap ? capped_alone : plain_alone : cap ? capped : plain)(tp, batch, workspace,
+                                                                                workers, st);
+    };
     if (head_dim == 256)
-        return cap ? launch_tp<256, true>(tp, batch, workspace, workers, st)
-                   : launch_tp<256, false>(tp, batch, workspace, workers, st);
+        return launch(launch_tp<256, false, false>, launch_tp<256, true, false>, launch_tp<256, false, true>,
+                      launch_tp<256, true, true>);
     if (head_dim == 512)
-        return cap ? launch_tp<512, true>(tp, batch, workspace, workers, st)
-                   : launch_tp<512, false>(tp, batch, workspace, workers, st);
+        return launch(launch_tp<512, false, false>, launch_tp<512, true, false>, launch_tp<512, false, true>,
+                      launch_tp<512, true, true>);
     return cudaErrorInvalidValue;
 }
 

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
     const uint32_t tmem = *tslot;
     pdl_wait();  // the previous kernel on the stream has completed
     const int n_cta = CLUSTER ? tp.workers : 1, cta = CLUSTER ? (int)cluster_rank() : 0;
-    std::conditional_t<CLUSTER, TreeAlone<kTcKeys, kTcRows>, Share> share;
+    std::conditional_t<CLUSTER, TreeAlone<kTcKeys, kTcRows, 1>, Share> share;
     if constexpr (CLUSTER)
         share.init(tp, blockIdx.x / n_cta, cta, n_cta);
     else
