@@ -24,22 +24,27 @@ __global__ void __launch_bounds__(kAcceptWarps * 32)
     const int lane = threadIdx.x & 31;
     const int b = blockIdx.x * kAcceptWarps + (threadIdx.x >> 5);
     if (b >= batch) return;
+    const size_t row = (size_t)b * n;
+    // (the whole bucket, so that nothing waits for n_real)
+    int tok[kNodeRegs], par[kNodeRegs], nxt[kNodeRegs], out[kNodeRegs];
+#pragma unroll
+    for (int k = 0; k < kNodeRegs; ++k) {
+        const int i = lane + 32 * k;
+        tok[k] = i < n ? __ldg(tokens + row + i) : -1;
+        par[k] = i < n ? __ldg(parents + row + i) : -1;
+        nxt[k] = i < n ? __ldg(next + row + i) : -1;
+        out[k] = -1;
+    }
     const int nr = n_real ? __ldg(n_real + b) : n;
     const int len = seq_lens ? seq_lens[b] : 0;
     const bool bad_real = nr < 0 || nr > n;
     const bool bad_len = !bad_real && seq_lens && len < nr;
-    const size_t row = (size_t)b * n;
-
-    int tok[kNodeRegs], par[kNodeRegs], nxt[kNodeRegs], out[kNodeRegs];
     bool bad_node = false;
 #pragma unroll
     for (int k = 0; k < kNodeRegs; ++k) {
         const int i = lane + 32 * k;
         const bool live = !bad_real && i < nr;
-        tok[k] = live ? __ldg(tokens + row + i) : -1;
-        par[k] = live ? __ldg(parents + row + i) : -1;
-        nxt[k] = live ? __ldg(next + row + i) : -1;
-        out[k] = -1;
+        if (!live) tok[k] = par[k] = nxt[k] = -1;
         bad_node |= live && (par[k] < -1 || par[k] >= i);
     }
     const bool bad_tree = __any_sync(0xffffffffu, bad_node);
@@ -116,6 +121,9 @@ __global__ void __launch_bounds__(kKeepThreads)
     const int b = blockIdx.z, tid = threadIdx.x;
     const int nk = __ldg(k.n_keep + b);
     const int pos = __ldg(k.write_pos + b);
+    // (of the whole bucket, so that it does not wait for n_keep)
+    const int m = tid < k.n ? __ldg(k.path + (size_t)b * k.n + tid) : 0;
+    const int before = tid && tid < k.n ? __ldg(k.path + (size_t)b * k.n + tid - 1) : -1;
     const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0;
     if (nk < 0 || nk > k.n) {
         if (first_cta && tid == 0) report(err, GEMMA_DEVERR_TREE);
@@ -124,8 +132,6 @@ __global__ void __launch_bounds__(kKeepThreads)
     if (nk == 0) return;
     bool bad = false, move = false;
     if (tid < nk) {
-        const int m = __ldg(k.path + (size_t)b * k.n + tid);
-        const int before = tid ? __ldg(k.path + (size_t)b * k.n + tid - 1) : -1;
         bad = m <= before || m >= k.n;
         move = m != tid;
         s_path[tid] = m;
