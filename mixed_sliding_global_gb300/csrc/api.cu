@@ -975,7 +975,8 @@ enum { kTreeRows, kTreeTc, kTreePair };
 struct TreePlan {
     int path;
     int n_split, chunk;    // kTreeRows: chunks of keys
-    int workers, cluster;  // kTreeTc, kTreePair: equal shares, or (cluster > 0) a cluster or pair for each unit
+    int deal;              // kTreeTc, kTreePair: how units are dealt out
+    int workers, cluster;  // to CTAs or pairs; CTAs of a unit's cluster
     size_t o_bytes, ws_bytes;
 };
 
@@ -995,7 +996,9 @@ TreePlan tree_plan(int batch, int kind, int window, int n_q, int n_kv, int head_
     const long long T = gemma::kTreeKeyTile;
     const long long rows = (long long)n_nodes * (n_q / n_kv), units = (long long)batch * n_kv;
     const long long reach = tree_reach(kind, window, max_seq_len, n_nodes);
-    TreePlan pl{kTreeRows, 1, 1 << 30, 0, 0, 0, 0};
+    TreePlan pl{};
+    pl.n_split = 1;
+    pl.chunk = 1 << 30;
     // Two SMs and 256 rows per tile, or one and 128. Head_dim 256 in us, pairs / single SMs: 61 nodes x 4
     // heads, 2 KV heads, 1 sequence of 8192 keys 20 / 20, 7 of 4800 35 / 37, 16 of 4096 46 / 60, 64 of 2048
     // (64 nodes) 75 / 112; with 128 rows or fewer a pair's second SM would have none.
@@ -1013,11 +1016,14 @@ TreePlan tree_plan(int batch, int kind, int window, int n_q, int n_kv, int head_
         const long long share = kind == GEMMA_GLOBAL ? 1 : (tiles + n_sm / 2 - 1) / (n_sm / 2);
         if (u <= n_sm / 2 && nt - share <= 8 / halves) {
             pl.workers = (int)u;
-            pl.cluster = 1;
+            pl.deal = gemma::kTreeAlone;
             return pl;
         }
         pl.workers = (int)(tiles < n_sm / 2 ? tiles : n_sm / 2);
-        pl.ws_bytes = gemma::tree_pair_workspace(batch, pl.workers);
+        // Of more units than pairs whole ones to each, where they are that short: 184 units of 5 tiles, head_dim
+        // 256, 56.6 / 45.1 us, 408 (of two halves) of 2, head_dim 512, 138 / 112.
+        if (u > n_sm / 2 && nt <= 8 / halves) pl.deal = gemma::kTreeWhole;
+        else pl.ws_bytes = gemma::tree_pair_workspace(batch, pl.workers);
         return pl;
     }
     // Up to 16 rows of head_dim 64 or 128 over many keys: mma.sync takes a 64-key tile in less than the 0.6
@@ -1044,9 +1050,13 @@ TreePlan tree_plan(int batch, int kind, int window, int n_q, int n_kv, int head_
             if (t <= best && (c == 1 || u <= gemma::tree_tc_clusters(head_dim, c))) {
                 best = t;
                 pl.cluster = c;
-                pl.ws_bytes = 0;
+                pl.deal = gemma::kTreeAlone;
             }
         }
+        // more units than SMs, all short: whole ones to each (152 x 3 of 9 tiles, head_dim 64, capped 49.9 / 46.8
+        // us)
+        if (u > n_sm && nt * tile_ns <= 7500) pl.deal = gemma::kTreeWhole;
+        if (pl.deal != gemma::kTreeShares) pl.ws_bytes = 0;
         return pl;
     }
     // chunks of keys: as many as keep one wave of CTAs, each of at least a tile
@@ -1183,9 +1193,9 @@ int gemma_attn_tree(void* out, const void* q, const void* const* k_cache,
     if (!bf16) {
         e = gemma::launch_tree_f32(tp, head_dim, batch, s);
     } else if (pl.path == kTreeTc) {
-        e = gemma::launch_tree_tc(tp, head_dim, batch, workspace, pl.workers, pl.cluster, s);
+        e = gemma::launch_tree_tc(tp, head_dim, batch, workspace, pl.workers, pl.cluster, pl.deal, s);
     } else if (pl.path == kTreePair) {
-        e = gemma::launch_tree_pair(tp, head_dim, batch, workspace, pl.workers, pl.cluster > 0, s);
+        e = gemma::launch_tree_pair(tp, head_dim, batch, workspace, pl.workers, pl.deal, s);
     } else {
         e = gemma::launch_tree_rows(tp, head_dim, batch, s);
         if (e == cudaSuccess && pl.n_split > 1) e = gemma::launch_tree_combine(tp, head_dim, batch, s);

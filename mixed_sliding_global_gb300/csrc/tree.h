@@ -18,17 +18,22 @@ struct TreeParams {
 
 constexpr int kTreeRowsMax = 32;  // rows per KV head of launch_tree_rows
 
+// How units (a KV head of a sequence and a tile of rows) are dealt out to workers: in equal shares of their
+// key tiles, parts merged; each to a pair or cluster of its own; or whole ones in about equal shares. Only
+// the first needs a workspace.
+enum { kTreeShares, kTreeAlone, kTreeWhole };
+
 // On CTA pairs (tree_pair.cu), head_dim 256 and 512, any number of rows; the merge included. workers:
-// pairs, one per two SMs at most; alone: one per unit (no merge, no workspace).
+// pairs, one per two SMs at most, or, alone, one per unit.
 size_t tree_pair_workspace(int batch, int workers);
 cudaError_t launch_tree_pair(const TreeParams& tp, int head_dim, int batch, void* workspace,
-                             int workers, bool alone, cudaStream_t st);
+                             int workers, int deal, cudaStream_t st);
 // On single SMs with tcgen05 (tree_tc.cu), head_dim 64 to 256, any number of rows; the merge included.
 // workers: CTAs, one per SM at most; or a cluster of 1 to 8 CTAs for each unit (cluster > 0; no workspace).
 int tree_tc_clusters(int head_dim, int cluster);  // clusters of 2, 4 or 8 that run at once
 size_t tree_tc_workspace(int head_dim, int batch, int workers);
 cudaError_t launch_tree_tc(const TreeParams& tp, int head_dim, int batch, void* workspace,
-                           int workers, int cluster, cudaStream_t st);
+                           int workers, int cluster, int deal, cudaStream_t st);
 
 // Parts of units cut into equal shares of the key tiles, and where they lie in the workspace. A worker
 // has two slots: for the part that its share begins with, and for the one that it ends with.

@@ -145,11 +145,12 @@ struct TreeRing {
 // keys), in equal shares. Whole warps run it alike, each by itself: lengths are known on the device
 // alone, and this way no warp waits for another. Units are not cut where they are at most as many as
 // the workers and the longest alone (tile_ns a tile) takes no longer than an equal share (share_ns a
-// tile, when every SM works) and the merge of its parts (merge_ns).
-template <int KEYS, int ROWS, int HALVES>
+// tile, when every SM works) and the merge of its parts (merge_ns). WHOLE: they never are, and of more
+// units than workers a worker takes those that begin in its share.
+template <int KEYS, int ROWS, int HALVES, bool WHOLE>
 struct TreeShare {
     int pos, end, begin, b, seq0, worker;  // seq0: tiles (whole units) of the sequences before b
-    bool whole;
+    bool whole;  // a worker has one unit
     GEMMA_DEVINL void init(const MergeParams& mp, int worker_, bool write_before, int tile_ns,
                            int share_ns, int merge_ns) {
         // lane l has the sequences l * per .. + per - 1: one round of loads for many of them
@@ -180,7 +181,7 @@ struct TreeShare {
                   units = __shfl_sync(0xffffffffu, u_incl, 31);
         const int share = (total + mp.workers - 1) / mp.workers;
         whole = units <= mp.workers &&
-                (long long)longest * tile_ns <= (long long)share * share_ns + merge_ns;
+                (WHOLE || (long long)longest * tile_ns <= (long long)share * share_ns + merge_ns);
         if (write_before) {
             int sum = n_incl - n;
             for (int x = b_lo; x < b_hi; ++x) {
@@ -212,9 +213,13 @@ struct TreeShare {
             int live_rt;
             const int nt = tree_tiles<KEYS, ROWS>(p, U.sq, live_rt), unit = whole ? 1 : nt,
                       all = unit * live_rt * p.n_kv * HALVES;
+            if (WHOLE && !whole && nt > 0 && pos < seq0 + all) {  // on to where a unit begins
+                pos = seq0 + (pos - seq0 + nt - 1) / nt * nt;
+                if (pos >= end) return false;
+            }
             if (pos < seq0 + all) {
                 const int rel = pos - seq0, idx = whole ? rel : rel / nt, t0 = rel - idx * unit;
-                const int t1 = whole ? nt : min(nt, t0 + end - pos);
+                const int t1 = whole || WHOLE ? nt : min(nt, t0 + end - pos);
                 U.b = b;
                 U.half = idx % HALVES;
                 U.kvh = idx / HALVES / live_rt;
@@ -263,6 +268,27 @@ struct TreeAlone {
         return now;
     }
 };
+
+// Row tiles without nodes: zeros, an eighth of a tile at a time, and bad lengths are reported. One warp of
+// each of `workers` CTAs, in turn.
+template <int D, int ROWS>
+GEMMA_DEVINL void tree_dead_rows(const MergeParams& mp, int worker, int workers) {
+    const RowsParams& p = mp.tp.p;
+    const int lane = threadIdx.x & 31;
+    for (long long i = worker; i < 8ll * mp.n_rt * mp.batch; i += workers) {
+        const int b = (int)(i / (8 * mp.n_rt)), rt = (int)(i / 8 % mp.n_rt), eighth = (int)(i % 8);
+        const TrSeq sq = tr_seq(p, b);
+        if (rt < (sq.bad ? 0 : (sq.n * p.G + ROWS - 1) / ROWS)) continue;
+        if (sq.bad && rt == 0 && eighth == 0 && lane == 0) report(p.err, sq.bad);
+        // (tokens with all their heads: 8 G divides ROWS)
+        const int toks = ROWS / p.G / 8, tok0 = rt * (ROWS / p.G) + eighth * toks,
+                  n_tok = min(toks, p.n_tok - tok0);
+        uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(p.out) +
+                                              ((size_t)b * p.n_tok + tok0) * p.n_q * (size_t)D);
+        const long long n = (long long)n_tok * p.n_q * (D / 8);
+        for (long long k = lane; k < n; k += 32) dst[k] = make_uint4(0u, 0u, 0u, 0u);
+    }
+}
 
 // What a row attends: its ancestors, and the first prefix key. Whole warps; every warp of a sequence
 // finds a bad tree by itself.

@@ -69,15 +69,16 @@ struct TpLay {
 // A float's bits as an integer of the same order, and back.
 GEMMA_DEVINL int tp_ordered(int x) { return x ^ ((x >> 31) & 0x7fffffff); }
 
-// ALONE: a unit to each pair, which writes zeros itself where there is nothing: no merge, no workspace
-template <int D, bool SOFTCAP, bool ALONE>
+// Alone: a unit to each pair, which writes zeros itself where there is nothing: no merge, no workspace
+template <int D, bool SOFTCAP, int DEAL>
 __global__ void __launch_bounds__(TpLay<D, SOFTCAP>::THREADS, 1)
     tree_pair_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap,
                      const __grid_constant__ CUtensorMap qmap, const MergeParams mp) {
     using Lay = TpLay<D, SOFTCAP>;
+    constexpr bool ALONE = DEAL == kTreeAlone;
     using PairShare = std::conditional_t<ALONE, TreeAlone<kTpKeys, kTpRows, Lay::KB>,
-                                         TreeShare<kTpKeys, kTpRows, Lay::KB>>;
+                                         TreeShare<kTpKeys, kTpRows, Lay::KB, DEAL == kTreeWhole>>;
     constexpr int KB = Lay::KB, NK = Lay::K_SLOTS, NV = Lay::V_SLOTS;
     constexpr int GROUPS = Lay::GROUPS, SOFT = Lay::SOFT, COLS = Lay::COLS, O_COLS = Lay::O_COLS;
     pdl_launch_dependents();
@@ -146,7 +147,7 @@ __global__ void __launch_bounds__(TpLay<D, SOFTCAP>::THREADS, 1)
         // (compute bound: a tile takes as long alone as when every SM works, and the parts and their merge as
         // long as six of them, three at head_dim 512. Whole / cut: 30 units of 10 tiles, head_dim 256, 23.6 /
         // 25.6 us; 50 of 10, head_dim 512, 32.9 / 36.6; 20 of 5 19.2 / 21.1)
-        share.init(mp, worker, blockIdx.x == 0 && warp == 0, 1000 * KB, 1000 * KB, 6000);
+        share.init(mp, worker, blockIdx.x == 0 && warp == 0 && DEAL == kTreeShares, 1000 * KB, 1000 * KB, 6000);
     }
     TreeUnit U{};
     bool ok = true;
@@ -248,6 +249,7 @@ __global__ void __launch_bounds__(TpLay<D, SOFTCAP>::THREADS, 1)
             }
             __syncwarp();
         }
+        if constexpr (DEAL == kTreeWhole) tree_dead_rows<D, kTpRows>(mp, blockIdx.x, gridDim.x);
         if (ord > 0 && ok) mbar_wait(q_free, (ord - 1) & 1, p.err);  // (landed before the CTA exits)
     } else if (c == 0 && warp == SOFT + 1) {
         // ------------------------------------- S issuer -----------------------------------------
@@ -539,12 +541,11 @@ TpScratch tp_scratch(int batch, int workers) {
     return s;
 }
 
-template <int D, bool SOFTCAP, bool ALONE>
-cudaError_t launch_tp(const TreeParams& tree, int batch, void* workspace, int workers,
-                      cudaStream_t st) {
+template <int D, bool SOFTCAP, int DEAL>
+cudaError_t launch_tp(const TreeParams& tree, int batch, void* workspace, int workers, cudaStream_t st) {
     using Lay = TpLay<D, SOFTCAP>;
     const RowsParams& p = tree.p;
-    auto kernel = tree_pair_kernel<D, SOFTCAP, ALONE>;
+    auto kernel = tree_pair_kernel<D, SOFTCAP, DEAL>;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -573,7 +574,7 @@ cudaError_t launch_tp(const TreeParams& tree, int batch, void* workspace, int wo
         if (fit < 1) return cudaErrorInvalidConfiguration;
         if (dev >= 0 && dev < 64) clusters_fit[dev].store(fit, std::memory_order_relaxed);
     }
-    if (!ALONE && workers > fit) workers = fit;
+    if (DEAL != kTreeAlone && workers > fit) workers = fit;
     cfg.gridDim = dim3(2 * workers);
     CUtensorMap km, vm, qm;
     // [rows][slots][D]: rows = sequences x KV heads (pages x KV heads for a paged pool)
@@ -596,7 +597,7 @@ cudaError_t launch_tp(const TreeParams& tree, int batch, void* workspace, int wo
     mp.n_rt = (p.n_tok * p.G + kTpRows - 1) / kTpRows;
     mp.workers = workers;
     mp.keys = kTpKeys;
-    if (!ALONE) {
+    if (DEAL == kTreeShares) {
         const TpScratch ws = tp_scratch(batch, workers);
         uint8_t* base = static_cast<uint8_t*>(workspace);
         mp.part_o = reinterpret_cast<float*>(base);
@@ -604,26 +605,33 @@ cudaError_t launch_tp(const TreeParams& tree, int batch, void* workspace, int wo
         mp.before = reinterpret_cast<int32_t*>(base + ws.before_off);
     }
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, km, vm, qm, mp);
-    return e == cudaSuccess && !ALONE ? launch_tree_merge(mp, D, kTpRows, st) : e;
+    return e == cudaSuccess && DEAL == kTreeShares ? launch_tree_merge(mp, D, kTpRows, st) : e;
 }
 
 }  // namespace
 
 size_t tree_pair_workspace(int batch, int workers) { return tp_scratch(batch, workers).bytes; }
 
-cudaError_t launch_tree_pair(const TreeParams& tp, int head_dim, int batch, void* workspace,
-                             int workers, bool alone, cudaStream_t st) {
+template <int D>
+static cudaError_t launch_tp_deal(const TreeParams& tp, int batch, void* workspace, int workers, int deal,
+                                  cudaStream_t st) {
     const bool cap = tp.p.softcap > 0.f;
-    auto launch = [&](auto plain, auto capped, auto plain_alone, auto capped_alone) {
-        return (alone ? cap ? capped_alone : plain_alone : cap ? capped : plain)(tp, batch, workspace,
-                                                                                workers, st);
-    };
-    if (head_dim == 256)
-        return launch(launch_tp<256, false, false>, launch_tp<256, true, false>, launch_tp<256, false, true>,
-                      launch_tp<256, true, true>);
-    if (head_dim == 512)
-        return launch(launch_tp<512, false, false>, launch_tp<512, true, false>, launch_tp<512, false, true>,
-                      launch_tp<512, true, true>);
+    switch (deal) {
+        case kTreeShares:
+            return cap ? launch_tp<D, true, kTreeShares>(tp, batch, workspace, workers, st)
+                       : launch_tp<D, false, kTreeShares>(tp, batch, workspace, workers, st);
+        case kTreeAlone:
+            return cap ? launch_tp<D, true, kTreeAlone>(tp, batch, workspace, workers, st)
+                       : launch_tp<D, false, kTreeAlone>(tp, batch, workspace, workers, st);
+    }
+    return cap ? launch_tp<D, true, kTreeWhole>(tp, batch, workspace, workers, st)
+               : launch_tp<D, false, kTreeWhole>(tp, batch, workspace, workers, st);
+}
+
+cudaError_t launch_tree_pair(const TreeParams& tp, int head_dim, int batch, void* workspace,
+                             int workers, int deal, cudaStream_t st) {
+    if (head_dim == 256) return launch_tp_deal<256>(tp, batch, workspace, workers, deal, st);
+    if (head_dim == 512) return launch_tp_deal<512>(tp, batch, workspace, workers, deal, st);
     return cudaErrorInvalidValue;
 }
 

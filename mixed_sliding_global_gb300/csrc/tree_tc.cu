@@ -75,21 +75,23 @@ GEMMA_DEVINL void st_cluster_f32x4(uint32_t addr, float a, float b, float c, flo
                  : "memory");
 }
 
-using Share = TreeShare<kTcKeys, kTcRows, 1>;
-// Of a tile where memory does not hold it up, of one when all SMs load, and of the merge of parts:
-// what TreeShare weighs against each other.
-constexpr int kTcTileNs = 1150, kTcShareNs = 1630, kTcMergeNs = 6000;
+// Of a tile where memory does not hold it up, of one when all SMs load, and of parts and their merge: what
+// TreeShare weighs against each other.
+constexpr int tc_tile_ns(int d) { return 300 + 3 * d; }
+constexpr int tc_share_ns(int d) { return d == 256 ? 1630 : tc_tile_ns(d); }
+constexpr int kTcMergeNs = 7500;
 
 }  // namespace
 
-// CLUSTER: a unit to each cluster of tp.workers CTAs, which share out its key tiles and merge their
+// Alone: a unit to each cluster of tp.workers CTAs, which share out its key tiles and merge their
 // O through distributed shared memory (or, one CTA, write it): no second launch, no workspace
-template <int D, bool SOFTCAP, bool CLUSTER>
+template <int D, bool SOFTCAP, int DEAL>
 __global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
     tree_tc_kernel(const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap,
                    const __grid_constant__ CUtensorMap qmap, const MergeParams tp) {
     using Lay = TcLay<D, SOFTCAP>;
+    constexpr bool CLUSTER = DEAL == kTreeAlone;
     constexpr int S = Lay::SLOTS, GROUPS = Lay::GROUPS, SOFT = Lay::SOFT, COLS = Lay::COLS, O_COLS = Lay::O_COLS;
     pdl_launch_dependents();
     const RowsParams& p = tp.tp.p;
@@ -147,11 +149,13 @@ __global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
     const uint32_t tmem = *tslot;
     pdl_wait();  // the previous kernel on the stream has completed
     const int n_cta = CLUSTER ? tp.workers : 1, cta = CLUSTER ? (int)cluster_rank() : 0;
-    std::conditional_t<CLUSTER, TreeAlone<kTcKeys, kTcRows, 1>, Share> share;
+    std::conditional_t<CLUSTER, TreeAlone<kTcKeys, kTcRows, 1>,
+                       TreeShare<kTcKeys, kTcRows, 1, DEAL == kTreeWhole>> share;
     if constexpr (CLUSTER)
         share.init(tp, blockIdx.x / n_cta, cta, n_cta);
     else
-        share.init(tp, blockIdx.x, blockIdx.x == 0 && warp == 0, kTcTileNs, kTcShareNs, kTcMergeNs);
+        share.init(tp, blockIdx.x, blockIdx.x == 0 && warp == 0 && DEAL == kTreeShares, tc_tile_ns(D),
+                   tc_share_ns(D), kTcMergeNs);
     // softmax warps: the row's reference and sum (of the last part)
     float m = -INFINITY, l = 0.f;
 
@@ -210,6 +214,7 @@ __global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
             }
             __syncwarp();
         }
+        if constexpr (DEAL == kTreeWhole) tree_dead_rows<D, kTcRows>(tp, blockIdx.x, gridDim.x);
         if (ord > 0 && ok) mbar_wait(q_free, (ord - 1) & 1, p.err);  // (landed before the CTA exits)
     } else if (warp == SOFT + 1 || warp == SOFT + 3) {
         // ------------------------------ MMA issuers: S and P V ----------------------------------
@@ -546,11 +551,12 @@ TcScratch tc_scratch(int head_dim, int batch, int workers) {
 
 template <int D, bool SOFTCAP>
 cudaError_t launch_tc(const TreeParams& tree, int batch, void* workspace, int workers, int cluster,
-                      cudaStream_t st) {
+                      int deal, cudaStream_t st) {
     using Lay = TcLay<D, SOFTCAP>;
     const RowsParams& p = tree.p;
     using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, MergeParams);
-    const Kernel kernels[2] = {tree_tc_kernel<D, SOFTCAP, false>, tree_tc_kernel<D, SOFTCAP, true>};
+    const Kernel kernels[3] = {tree_tc_kernel<D, SOFTCAP, kTreeShares>, tree_tc_kernel<D, SOFTCAP, kTreeAlone>,
+                               tree_tc_kernel<D, SOFTCAP, kTreeWhole>};
     static std::atomic<bool> configured[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
@@ -581,10 +587,10 @@ cudaError_t launch_tc(const TreeParams& tree, int batch, void* workspace, int wo
     tp.tp = tree;
     tp.batch = batch;
     tp.n_rt = (p.n_tok * p.G + kTcRows - 1) / kTcRows;
-    tp.workers = cluster ? cluster : workers;
+    tp.workers = deal == kTreeAlone ? cluster : workers;
     tp.keys = kTcKeys;
-    const Kernel kernel = kernels[cluster > 0];
-    if (cluster) {
+    const Kernel kernel = kernels[deal];
+    if (deal == kTreeAlone) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3((unsigned)(tp.n_rt * batch * p.n_kv * cluster));
         cfg.blockDim = dim3(Lay::THREADS);
@@ -603,12 +609,14 @@ cudaError_t launch_tc(const TreeParams& tree, int batch, void* workspace, int wo
     }
     const TcScratch ws = tc_scratch(D, batch, workers);
     uint8_t* base = static_cast<uint8_t*>(workspace);
-    tp.part_o = reinterpret_cast<float*>(base);
-    tp.part_ml = reinterpret_cast<float2*>(base + ws.ml_off);
-    tp.before = reinterpret_cast<int32_t*>(base + ws.before_off);
+    if (deal == kTreeShares) {
+        tp.part_o = reinterpret_cast<float*>(base);
+        tp.part_ml = reinterpret_cast<float2*>(base + ws.ml_off);
+        tp.before = reinterpret_cast<int32_t*>(base + ws.before_off);
+    }
     const cudaError_t e =
         launch_pdl(kernel, dim3(workers), dim3(Lay::THREADS), Lay::SMEM, st, km, vm, qm, tp);
-    return e == cudaSuccess ? launch_tree_merge(tp, D, kTcRows, st) : e;
+    return e == cudaSuccess && deal == kTreeShares ? launch_tree_merge(tp, D, kTcRows, st) : e;
 }
 
 }  // namespace
@@ -623,7 +631,7 @@ static int clusters_fit(int cluster) {
         const int n = cache[dev][i].load(std::memory_order_relaxed);
         if (n > 0) return n;
     }
-    if (cudaFuncSetAttribute(tree_tc_kernel<D, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(tree_tc_kernel<D, false, kTreeAlone>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              TcLay<D, false>::SMEM) != cudaSuccess)
         return 0;
     cudaLaunchConfig_t cfg = {};
@@ -638,7 +646,7 @@ static int clusters_fit(int cluster) {
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
     int n = 0;
-    if (cudaOccupancyMaxActiveClusters(&n, tree_tc_kernel<D, false, true>, &cfg) != cudaSuccess) return 0;
+    if (cudaOccupancyMaxActiveClusters(&n, tree_tc_kernel<D, false, kTreeAlone>, &cfg) != cudaSuccess) return 0;
     if (dev >= 0 && dev < 64) cache[dev][i].store(n, std::memory_order_relaxed);
     return n;
 }
@@ -657,9 +665,9 @@ size_t tree_tc_workspace(int head_dim, int batch, int workers) {
 }
 
 cudaError_t launch_tree_tc(const TreeParams& tp, int head_dim, int batch, void* workspace,
-                           int workers, int cluster, cudaStream_t st) {
+                           int workers, int cluster, int deal, cudaStream_t st) {
     auto launch = [&](auto plain, auto capped) {
-        return (tp.p.softcap > 0.f ? capped : plain)(tp, batch, workspace, workers, cluster, st);
+        return (tp.p.softcap > 0.f ? capped : plain)(tp, batch, workspace, workers, cluster, deal, st);
     };
     switch (head_dim) {
         case 64: return launch(launch_tc<64, false>, launch_tc<64, true>);
