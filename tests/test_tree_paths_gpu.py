@@ -40,6 +40,12 @@ LAYOUTS = [dict(), dict(page=128), dict(kind=SLIDING, window=77), dict(kind=SLID
     (16, 1, 256, True, 2, 2000, 16),      # pairs: few units, many parts
     (16, 1, 512, True, 34, 350, 6),       # pairs at head_dim 512, in two halves
     (8, 2, 512, False, 5, 900, 100),
+    (16, 1, 512, True, 45, 300, 6),       # more units than pairs, short ones: whole ones to each
+    (4, 2, 64, False, 90, 300, 11),       # the same of SMs
+    (16, 2, 256, False, 35, 1500, 40),    # many more units than pairs, cut
+    (16, 1, 512, True, 60, 900, 6),
+    (8, 4, 256, False, 60, 900, 10),      # the same of SMs
+    (4, 2, 64, False, 120, 900, 9),
     (4, 2, 512, False, 20, 600, 15),      # head_dim 512, 30 rows
     (2, 2, 512, True, 20, 600, 16),
 ])
@@ -66,7 +72,8 @@ def test_few_rows_over_many_keys(d, layout, group, nodes):
 
 @pytest.mark.parametrize("n_q,n_kv,d,nodes,batch,top", [
     (4, 2, 64, 9, 40, 300), (4, 2, 64, 3, 2, 100), (16, 1, 256, 9, 36, 300), (16, 1, 512, 9, 9, 300),
-    (2, 2, 512, 9, 9, 300), (8, 8, 128, 8, 9, 2100)])
+    (2, 2, 512, 9, 9, 300), (8, 8, 128, 8, 9, 2100), (16, 2, 256, 9, 50, 300), (16, 1, 512, 9, 50, 300),
+    (4, 2, 64, 9, 100, 300), (16, 2, 256, 9, 60, 1300), (4, 2, 64, 9, 120, 900), (16, 1, 512, 9, 3, 900)])
 def test_bad_sequences_among_others(n_q, n_kv, d, nodes, batch, top):
     """Bad lengths, counts and trees are skipped and reported; every other sequence is what it is alone."""
     gen = torch.Generator().manual_seed(7)
@@ -134,3 +141,18 @@ def test_many_sequences_of_one_key():
         p = Problem(lens, [2, 1] * (B // 2), 2, n_q=n_q, n_kv=n_kv, d=d, k_eq_v=True, parents=parents)
         p.check(p.run())
         assert p.err == 0
+
+
+@pytest.mark.parametrize("n_q,n_kv,d,nodes,top", [
+    (16, 2, 256, 12, 4000), (16, 1, 512, 12, 3000), (4, 2, 64, 12, 4000), (8, 4, 128, 12, 2000),
+    (16, 2, 256, 12, 300), (16, 1, 512, 12, 300), (4, 2, 64, 12, 300), (8, 4, 256, 12, 300)])
+@pytest.mark.parametrize("live", [[0], [63], [7, 40], []])
+def test_a_batch_with_few_live_sequences(n_q, n_kv, d, nodes, top, live):
+    """A bucket of 64 sequences of which few have nodes: theirs is cut into many parts, and the rows of all
+    others are zeros."""
+    reals = [nodes if b in live else 0 for b in range(64)]
+    lens = [top if b in live else 0 for b in range(64)]
+    p = Problem(lens, reals, nodes, n_q=n_q, n_kv=n_kv, d=d, k_eq_v=True, seed=d, cap=top)
+    p.msl = top
+    p.check(p.run())
+    assert p.err == 0
