@@ -1026,23 +1026,26 @@ TreePlan tree_plan(int batch, int kind, int window, int n_q, int n_kv, int head_
         else pl.ws_bytes = gemma::tree_pair_workspace(batch, pl.workers);
         return pl;
     }
-    // Up to 16 rows of head_dim 64 or 128 over many keys: mma.sync takes a 64-key tile in less than the 0.6
-    // us that one takes on tcgen05. Head_dim 64, 8 rows, tcgen05 / mma.sync: 64 x 2 heads x 4096 keys 60 /
-    // 30 us, 8 x 4 x 4096 18.6 / 13.4, 32 x 4 x 512 10.8 / 11.5, 1 x 4 x 8192 12.2 / 20.3; head_dim 128:
-    // 62 / 49, 19.7 / 15.8, 11.1 / 12.7, 13.6 / 17.8.
-    if (head_dim <= 256 && !(head_dim <= 128 && rows <= 16 && units * reach >= 100000)) {
+    // Up to 16 rows of head_dim 64 or 128 over many keys of not too few units: mma.sync takes a tile in less
+    // time than one takes on tcgen05. 16 rows, tcgen05 / mma.sync, head_dim 64: 64 x 2 heads x 4096 keys 43 /
+    // 30 us, 8 x 2 x 8192 20.9 / 15.5, 32 x 4 x 512 9.3 / 11.5, 1 x 4 x 32768 20.5 / 25.5; head_dim 128: 45.6 /
+    // 50.1, 21.5 / 17.3, 10.2 / 12.7, 21.4 / 22.8.
+    const bool few = head_dim <= 128 && rows <= 16 && units * reach >= 100000 && units >= 8 &&
+                     (head_dim == 64 || units < 64);
+    if (head_dim <= 256 && !few) {
         pl.path = kTreeTc;
-        const long long tiles = tree_tiles(batch, n_kv, rows, 128, reach, T);
+        const long long keys = head_dim <= 128 ? 128 : 64;  // of a tile
+        const long long tiles = tree_tiles(batch, n_kv, rows, 128, reach, keys);
         pl.workers = (int)(tiles < n_sm ? tiles : n_sm);
         pl.ws_bytes = gemma::tree_tc_workspace(head_dim, batch, pl.workers);
         // A cluster for each unit (no merge launch), where that ends no later than equal shares. In ns: a
-        // tile takes 560 at head_dim 64 and 1000 at 256; the merge launch of equal shares 4500; a cluster's
+        // tile takes 850 at head_dim 64 and 128 (of 128 keys) and 1000 at 256; the merge launch of equal shares 4500; a cluster's
         // exchange 1.0, 2.0 and 5.9 thousand with 32 rows of 256, 128 of 64, 128 of 256. One unit of 32 rows
         // and head_dim 256, clusters of 8 / shares: 1100 keys 9.6 / 10.2 us; 128 rows: 14.6 / 11.7; 128
         // units of 17 tiles, alone / shares: 30.6 / 34.4.
         const long long u = units * ((rows + 127) / 128);
-        const long long nt = kind == GEMMA_SLIDING_RING ? (reach + T - 1) / T : reach / T;
-        const long long tile_ns = 500 + 2 * head_dim, merge_ns = 4500;
+        const long long nt = kind == GEMMA_SLIDING_RING ? (reach + keys - 1) / keys : (reach - T + keys) / keys;
+        const long long tile_ns = head_dim == 256 ? 1012 : 850, merge_ns = 4500;
         const long long cluster_ns = 700 + (rows < 128 ? rows : 128) * head_dim * 16 / 100;
         long long best = (u * nt + n_sm - 1) / n_sm * tile_ns + merge_ns;
         for (int c = 1; c <= 8 && u * c <= n_sm; c *= 2) {
@@ -1053,8 +1056,8 @@ TreePlan tree_plan(int batch, int kind, int window, int n_q, int n_kv, int head_
                 pl.deal = gemma::kTreeAlone;
             }
         }
-        // more units than SMs, all short: whole ones to each (152 x 3 of 9 tiles, head_dim 64, capped 49.9 / 46.8
-        // us)
+        // more units than SMs, all short: whole ones to each (equal shares / whole: 456 units of 6 tiles,
+        // head_dim 64, 40 / 31 us)
         if (u > n_sm && nt * tile_ns <= 7500) pl.deal = gemma::kTreeWhole;
         if (pl.deal != gemma::kTreeShares) pl.ws_bytes = 0;
         return pl;

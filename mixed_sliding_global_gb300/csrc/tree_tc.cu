@@ -1,11 +1,12 @@
 // tree_tc.cu -- attention of a drafted tree with up to 128 rows per KV head and tile, on the
 // 5th-generation tensor cores (tcgen05, one SM per tile). Definition in tree_attn.cu.
 //
-// A unit is one KV head of one sequence and 128 of its rows (nodes x G query heads). Per tile of 64
-// keys: S = Q K^T (M 128, N 64) into tensor memory, softmax by four warps (a thread per row; eight with a
-// soft-cap), P as bf16 back into tensor memory, O += P V (N = head_dim). A tile takes 1.1 us at head_dim
-// 256 where its 64 KB are there in time; when all SMs load, memory gives 6.1 TB/s or a tile in 1.6 us, so
-// what is left to lose is the start, the end and the change from one unit to the next:
+// A unit is one KV head of one sequence and 128 of its rows (nodes x G query heads). Per tile of 64 keys
+// (128 at head_dim 64 and 128): S = Q K^T (M 128, N keys) into tensor memory, softmax by groups of four
+// warps (a thread per row and 32 or 64 keys), P as bf16 back into tensor memory, O += P V (N = head_dim). A
+// tile takes 1.05 us at head_dim 256 where its 64 KB are there in time; when all SMs load, memory gives 6.1
+// TB/s or a tile in 1.6 us, so what is left to lose is the start, the end and the change from one unit to the
+// next:
 //  - the key tiles of all units form one sequence (lengths are known on the device alone), of which
 //    every CTA takes an equal share; every warp works out the share by itself, from a scan of the
 //    lengths, before the first barrier wait;
@@ -34,29 +35,39 @@ namespace gemma {
 namespace {
 
 constexpr int kTcRows = 128;
-constexpr int kTcKeys = kTreeKeyTile;
 constexpr int kTcMaxSlots = 12;
 constexpr int kTcMaxCluster = 8;
-constexpr int kTcBox = kTcKeys * 128;  // 64 keys x 64 columns
+constexpr int kTcBox = 64 * 128;  // 64 keys x 64 columns
 constexpr int kTcQBox = kTcRows * 128;
-// TMEM columns: O, S (two buffers), P (two buffers of packed bf16)
-constexpr int kTcO = 0, kTcS = 256, kTcP = 384;
 
 template <int D, bool SOFTCAP>
 struct TcLay {
-    // Groups of four softmax warps: a tile with a soft-cap is bound by the softmax. One / two, 152 units of
-    // 4096 keys, head_dim 256, no cap 97 us, a cap of 10 times the scores 102 / 98, of twice 153 / 105.
-    static constexpr int GROUPS = SOFTCAP ? 2 : 1;
+    // Keys per tile: with 64 a tile takes 0.6 us whatever it holds, in the waits of its steps one after another
+    // (152 units of 128 rows over 4096 keys, K as V, head_dim 64: 64 keys 46 us, 128 33; head_dim 128: 48 /
+    // 36; one of 64 rows over 300 keys 6.5 / 7.2). At 256 O, S and P of 128 would not fit tensor memory.
+    static constexpr int KEYS = D <= 128 ? 128 : 64, BOXES = KEYS / 64;
+    // Groups of four softmax warps, 64 columns each or, where a soft-cap makes the softmax the bound, 32. One /
+    // two at head_dim 256, 152 units of 4096 keys, no cap 97 us, a cap of 10 times the scores 102 / 98, of
+    // twice 153 / 105.
+    static constexpr int GROUPS = (D <= 128 ? 2 : 1) * (SOFTCAP ? 2 : 1);
     static constexpr int SOFT = 4 * GROUPS;                          // softmax warps
     static constexpr int THREADS = 32 * (SOFT + 4);
-    static constexpr int COLS = kTcKeys / GROUPS, O_COLS = D / GROUPS;  // a group's columns of S and O
-    static constexpr int SLOT = kTcKeys * D * 2;
-    static constexpr int EXTRA = 2 * 2 * 128 * 4 + 512;              // row maxima, barriers
+    static constexpr int COLS = KEYS / GROUPS;                       // a group's columns of S
+    static constexpr int O_COLS = D / GROUPS < 32 ? 32 : D / GROUPS;    // and of O, where it has some
+    static constexpr int O_GROUPS = D / O_COLS;
+    static constexpr int SLOT = KEYS * D * 2, BLOCK = BOXES * kTcBox;  // a tile; 64 columns of it
+    // Of a tile where memory does not hold it up, of one when all SMs load, and of parts and their merge: what
+    // TreeShare weighs against each other.
+    static constexpr int TILE_NS = D == 256 ? 1070 : 900, SHARE_NS = D == 256 ? 1630 : 900, MERGE_NS = 7500;
+    // TMEM columns: O, S (two buffers), P (two buffers of packed bf16)
+    static constexpr int O_COL = 0, S_COL = D, P_COL = S_COL + 2 * KEYS;
+    static_assert(P_COL + KEYS <= 512, "tensor memory budget");
+    static constexpr int EXTRA = 2 * (GROUPS > 1 ? GROUPS : 2) * 128 * 4 + 512;  // row maxima, barriers
     static constexpr int Q = kTcRows * D * 2;
     static constexpr int FIT = (232448 - Q - EXTRA) / SLOT;
     static constexpr int SLOTS = FIT > kTcMaxSlots ? kTcMaxSlots : FIT;
     static constexpr int Q_OFF = SLOTS * SLOT;
-    static constexpr int MX_OFF = Q_OFF + Q;                         // row maxima [2][2 groups][128]
+    static constexpr int MX_OFF = Q_OFF + Q;                         // row maxima [2][groups][128]
     static constexpr int BAR_OFF = MX_OFF + EXTRA - 512;
     static constexpr int SMEM = BAR_OFF + 512;
     static_assert(SMEM <= 232448 && (2 * kTcMaxSlots + 13) * 8 + 4 <= 512, "shared memory budget");
@@ -75,11 +86,6 @@ GEMMA_DEVINL void st_cluster_f32x4(uint32_t addr, float a, float b, float c, flo
                  : "memory");
 }
 
-// Of a tile where memory does not hold it up, of one when all SMs load, and of parts and their merge: what
-// TreeShare weighs against each other.
-constexpr int tc_tile_ns(int d) { return 300 + 3 * d; }
-constexpr int tc_share_ns(int d) { return d == 256 ? 1630 : tc_tile_ns(d); }
-constexpr int kTcMergeNs = 7500;
 
 }  // namespace
 
@@ -92,14 +98,16 @@ __global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
                    const __grid_constant__ CUtensorMap qmap, const MergeParams tp) {
     using Lay = TcLay<D, SOFTCAP>;
     constexpr bool CLUSTER = DEAL == kTreeAlone;
-    constexpr int S = Lay::SLOTS, GROUPS = Lay::GROUPS, SOFT = Lay::SOFT, COLS = Lay::COLS, O_COLS = Lay::O_COLS;
+    constexpr int KEYS = Lay::KEYS, BOXES = Lay::BOXES, kTcO = Lay::O_COL, kTcS = Lay::S_COL, kTcP = Lay::P_COL;
+    constexpr int S = Lay::SLOTS, GROUPS = Lay::GROUPS, SOFT = Lay::SOFT, COLS = Lay::COLS;
+    constexpr int O_COLS = Lay::O_COLS, O_GROUPS = Lay::O_GROUPS;
     pdl_launch_dependents();
     const RowsParams& p = tp.tp.p;
     extern __shared__ __align__(1024) uint8_t tc_smem[];
     uint8_t* smem = tc_smem;
     uint8_t* ring = smem;
     uint8_t* sQ = smem + Lay::Q_OFF;  // [D / 64][128][64] bf16
-    float* mxs = reinterpret_cast<float*>(smem + Lay::MX_OFF);  // [2][2][128]
+    float* mxs = reinterpret_cast<float*>(smem + Lay::MX_OFF);  // [2][groups][128]
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + Lay::BAR_OFF);
     uint64_t* empty = full + kTcMaxSlots;   // the MMAs that read the slot have completed
     uint64_t* q_full = empty + kTcMaxSlots;
@@ -149,13 +157,13 @@ __global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
     const uint32_t tmem = *tslot;
     pdl_wait();  // the previous kernel on the stream has completed
     const int n_cta = CLUSTER ? tp.workers : 1, cta = CLUSTER ? (int)cluster_rank() : 0;
-    std::conditional_t<CLUSTER, TreeAlone<kTcKeys, kTcRows, 1>,
-                       TreeShare<kTcKeys, kTcRows, 1, DEAL == kTreeWhole>> share;
+    std::conditional_t<CLUSTER, TreeAlone<Lay::KEYS, kTcRows, 1>,
+                       TreeShare<Lay::KEYS, kTcRows, 1, DEAL == kTreeWhole>> share;
     if constexpr (CLUSTER)
         share.init(tp, blockIdx.x / n_cta, cta, n_cta);
     else
-        share.init(tp, blockIdx.x, blockIdx.x == 0 && warp == 0 && DEAL == kTreeShares, tc_tile_ns(D),
-                   tc_share_ns(D), kTcMergeNs);
+        share.init(tp, blockIdx.x, blockIdx.x == 0 && warp == 0 && DEAL == kTreeShares, Lay::TILE_NS,
+                   Lay::SHARE_NS, Lay::MERGE_NS);
     // softmax warps: the row's reference and sum (of the last part)
     float m = -INFINITY, l = 0.f;
 
@@ -168,10 +176,17 @@ __global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
         while (share.next(tp, U)) {
             if (lane == 0) {
                 for (int t = 0; t < U.n_tiles && ok; ++t) {
-                    int row3 = 0, slot0 = 0;
-                    if (!kv_place(p, U.b, U.kvh, U.k_begin + t * kTcKeys, row3, slot0)) {
-                        report(p.err, GEMMA_DEVERR_PAGE);  // reads zeros
-                        row3 = p.n_pages * p.n_kv;
+                    int row3[BOXES], slot0[BOXES];
+#pragma unroll
+                    for (int g = 0; g < BOXES; ++g) {
+                        const int key = U.k_begin + t * KEYS + 64 * g;
+                        if (g && p.page_size && key >= U.sq.len) {  // behind the last key: no page
+                            row3[g] = p.n_pages * p.n_kv;
+                            slot0[g] = 0;
+                        } else if (!kv_place(p, U.b, U.kvh, key, row3[g], slot0[g])) {
+                            report(p.err, GEMMA_DEVERR_PAGE);  // reads zeros
+                            row3[g] = p.n_pages * p.n_kv;
+                        }
                     }
                     for (int v = 0; v < nops && ok; ++v) {
                         TreeRing& ring_v = v ? rv : rk;
@@ -180,9 +195,11 @@ __global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
                         if (!ok) break;
                         mbar_arrive_expect_tx(&full[s], Lay::SLOT);
 #pragma unroll
-                        for (int j = 0; j < D / 64; ++j)
-                            tma_load_3d(ring + s * Lay::SLOT + j * kTcBox, v ? &vmap : &kmap, 64 * j,
-                                        slot0, row3, &full[s]);
+                        for (int g = 0; g < BOXES; ++g)
+#pragma unroll
+                            for (int j = 0; j < D / 64; ++j)
+                                tma_load_3d(ring + s * Lay::SLOT + j * Lay::BLOCK + g * kTcBox,
+                                            v ? &vmap : &kmap, 64 * j, slot0[g], row3[g], &full[s]);
                         ring_v.step(v ? nv : nk);
                     }
                 }
@@ -221,7 +238,7 @@ __global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
         // An MMA is accepted only when the one before it is nearly done, so what an issuer spends
         // in waits is lost to the tensor core unless another one issues meanwhile.
         const bool is_s = warp == SOFT + 1;
-        const uint32_t id_s = idesc_bf16(128, kTcKeys, 0, 0), id_pv = idesc_bf16(128, D, 0, 1);
+        const uint32_t id_s = idesc_bf16(128, KEYS, 0, 0), id_pv = idesc_bf16(128, D, 0, 1);
         const uint64_t qd = smem_desc_sw128(smem_u32(sQ), 0, 1024);
         bool ok = true;
         TreeUnit U;
@@ -244,24 +261,24 @@ __global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
                         for (int j = 0; j < D / 64; ++j)
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
-                                umma_ss(tmem + kTcS + 64 * buf,
+                                umma_ss(tmem + kTcS + KEYS * buf,
                                         qd + (uint64_t)((j * kTcQBox + ks * 32) >> 4),
-                                        kd + (uint64_t)((j * kTcBox + ks * 32) >> 4), id_s,
+                                        kd + (uint64_t)((j * Lay::BLOCK + ks * 32) >> 4), id_s,
                                         (j | ks) ? 1u : 0u);
                         umma_commit(&s_full[buf]);
                         if (nops == 2) umma_commit(&empty[s]);
                         if (last) umma_commit(q_free);
                     }
                 } else {
-                    const int key0 = U.k_begin + t * kTcKeys, n_valid = U.sq.len - key0,
+                    const int key0 = U.k_begin + t * KEYS, n_valid = U.sq.len - key0,
                               n_head = U.first - key0;
                     if (ok) ok = mbar_wait(&full[s], rg.use & 1, p.err);
-                    if (n_valid < kTcKeys || n_head > 0) {
+                    if (n_valid < KEYS || n_head > 0) {
                         // rows outside of the sequence's keys may hold anything: zeros
-                        for (int i = lane; i < kTcKeys * (D / 8); i += 32) {
+                        for (int i = lane; i < KEYS * (D / 8); i += 32) {
                             const int key = i / (D / 8), ch = i - key * (D / 8);
                             if (key >= n_valid || key < n_head)
-                                *reinterpret_cast<uint4*>(tile + (ch >> 3) * kTcBox + key * 128 +
+                                *reinterpret_cast<uint4*>(tile + (ch >> 3) * Lay::BLOCK + key * 128 +
                                                           (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                         }
                         fence_proxy_async_smem();
@@ -271,10 +288,10 @@ __global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
                     if (ok) ok = mbar_wait(&p_full[buf], (T >> 1) & 1, p.err);
                     tc_fence_after();
                     if (lane == 0) {
-                        const uint64_t vd = smem_desc_sw128(smem_u32(tile), kTcBox, 1024);
+                        const uint64_t vd = smem_desc_sw128(smem_u32(tile), Lay::BLOCK, 1024);
 #pragma unroll
-                        for (int kk = 0; kk < kTcKeys / 16; ++kk)
-                            umma_ts(tmem + kTcO, tmem + kTcP + 32 * buf + 8 * kk,
+                        for (int kk = 0; kk < KEYS / 16; ++kk)
+                            umma_ts(tmem + kTcO, tmem + kTcP + KEYS / 2 * buf + 8 * kk,
                                     vd + (uint64_t)((kk * 2048) >> 4), id_pv,
                                     (t == 0 && kk == 0) ? 0u : 1u);
                         umma_commit(&pv_done[buf]);
@@ -318,7 +335,7 @@ __global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
                         uint32_t z[COLS / 2];
 #pragma unroll
                         for (int e = 0; e < COLS / 2; ++e) z[e] = 0u;
-                        tmem_store(tmem + kTcP + 32 * buf + COLS / 2 * w + lanes, z);
+                        tmem_store(tmem + kTcP + KEYS / 2 * buf + COLS / 2 * w + lanes, z);
                         tmem_st_wait();
                         tc_fence_before();
                         __syncwarp();
@@ -331,7 +348,7 @@ __global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
                     uint32_t v[COLS / 32][32];
 #pragma unroll
                     for (int i = 0; i < COLS / 32; ++i)
-                        tmem_ld32(tmem + kTcS + 64 * buf + COLS * w + 32 * i + lanes, v[i]);
+                        tmem_ld32(tmem + kTcS + KEYS * buf + COLS * w + 32 * i + lanes, v[i]);
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < COLS; ++e) s[e] = __uint_as_float(v[e / 32][e % 32]);
@@ -340,7 +357,7 @@ __global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_free[buf]);  // S(T + 2) may overwrite it
                 float sl2 = p.scale_log2;  // scale > 0: the raw maximum scales to the maximum
-                const int kt0 = U.k_begin + t * kTcKeys + COLS * w;
+                const int kt0 = U.k_begin + t * KEYS + COLS * w;
                 if constexpr (SOFTCAP) {
                     tree_mask(s, row, kt0, base, 0.f);  // (they may be NaN)
                     tree_cap(s, p);
@@ -348,11 +365,12 @@ __global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
                 }
                 tree_mask(s, row, kt0, base, -INFINITY);
                 float mx = tree_max(s) * sl2;
-                if constexpr (GROUPS == 2) {  // the row's maximum over both groups
-                    float* mxb = mxs + buf * 256;
+                if constexpr (GROUPS > 1) {  // the row's maximum over the groups
+                    float* mxb = mxs + buf * (128 * GROUPS);
                     mxb[w * 128 + r] = mx;
-                    named_bar_sync(1 + (warp & 3), 64);
-                    mx = fmaxf(mx, mxb[(w ^ 1) * 128 + r]);
+                    named_bar_sync(1 + (warp & 3), 32 * GROUPS);
+#pragma unroll
+                    for (int i = 0; i < GROUPS; ++i) mx = fmaxf(mx, mxb[i * 128 + r]);
                 }
                 const float m_prev = m;
                 if (mx > m + kTrLazyLog2) {
@@ -367,7 +385,7 @@ __global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
                     tc_fence_after();
                     const float alpha = moved ? fast_exp2(m_prev - m) : 1.f;
 #pragma unroll 1
-                    for (int j = 0; j < O_COLS / 32; ++j) {
+                    for (int j = 0; j < (w < O_GROUPS ? O_COLS / 32 : 0); ++j) {
                         uint32_t v[32];
                         tmem_ld32(tO + j * 32, v);
                         tmem_ld_wait();
@@ -383,21 +401,23 @@ __global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
                 // the buffer is free once P V(T - 2) has completed
                 if (T >= 2 && ok) ok = mbar_wait(&pv_done[buf], ((T >> 1) - 1) & 1, p.err);
                 tc_fence_after();
-                tmem_store(tmem + kTcP + 32 * buf + COLS / 2 * w + lanes, pw);
+                tmem_store(tmem + kTcP + KEYS / 2 * buf + COLS / 2 * w + lanes, pw);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[buf]);
             }
             // ---- the part's results ----
-            if constexpr (GROUPS == 2) {
-                // the row's sum over both groups, in the place of the other parity's maxima, which have
-                // been read by both
-                float* lx = mxs + (T & 1) * 256;
+            if constexpr (GROUPS > 1) {
+                // the row's sum over the groups, in the place of the other parity's maxima, which have been
+                // read by all
+                float* lx = mxs + (T & 1) * (128 * GROUPS);
                 lx[w * 128 + r] = l;
-                named_bar_sync(1 + (warp & 3), 64);
-                l += lx[(w ^ 1) * 128 + r];
-                named_bar_sync(1 + (warp & 3), 64);  // (before the next tile's maxima)
+                named_bar_sync(1 + (warp & 3), 32 * GROUPS);
+                l = 0.f;
+#pragma unroll
+                for (int i = 0; i < GROUPS; ++i) l += lx[i * 128 + r];
+                named_bar_sync(1 + (warp & 3), 32 * GROUPS);  // (before the next tile's maxima)
             }
             if (ok) ok = mbar_wait(o_full, ord & 1, p.err);
             tc_fence_after();
@@ -410,8 +430,9 @@ __global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
             float4* part = reinterpret_cast<float4*>(tp.part_o) + ((size_t)max(U.slot, 0) * (D / 4) + O_COLS / 4 * w) * kTcRows + r;
             if (U.slot >= 0 && w == 0) tp.part_ml[(size_t)U.slot * kTcRows + r] = make_float2(m, l);
             const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+            if (w >= O_GROUPS && lane == 0) mbar_arrive(o_free);  // (has no columns)
 #pragma unroll 1
-            for (int j = 0; j < O_COLS / 32; ++j) {
+            for (int j = 0; j < (w < O_GROUPS ? O_COLS / 32 : 0); ++j) {
                 uint32_t v[32];
                 tmem_ld32(tO + j * 32, v);
                 tmem_ld_wait();
@@ -480,7 +501,7 @@ __global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
                     const float a = m == -INFINITY ? 0.f : fast_exp2(m - M);
                     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
 #pragma unroll 1
-                    for (int j = w * (O_COLS / 32); j < (w + 1) * (O_COLS / 32); ++j) {
+                    for (int j = w * (O_COLS / 32); j < min(D / 32, (w + 1) * (O_COLS / 32)); ++j) {
                         uint32_t v[32];
                         tmem_ld32(tmem + kTcO + lanes + j * 32, v);
                         tmem_ld_wait();
@@ -574,7 +595,7 @@ cudaError_t launch_tc(const TreeParams& tree, int batch, void* workspace, int wo
     const uint64_t rows = (uint64_t)(p.page_size ? p.n_pages : batch) * p.n_kv;
     const uint64_t dims[3] = {(uint64_t)D, slots, rows};
     const uint64_t strides[2] = {(uint64_t)D * 2, slots * D * 2};
-    const uint32_t box[3] = {64, (uint32_t)kTcKeys, 1};
+    const uint32_t box[3] = {64, 64, 1};
     if (!encode_bf16_sw128(&km, p.k, 3, dims, strides, box)) return cudaErrorInvalidValue;
     if (!encode_bf16_sw128(&vm, p.v, 3, dims, strides, box)) return cudaErrorInvalidValue;
     // Q [B][n_tok][n_q][D]: G heads of one KV head's group x 128 / G tokens are a row tile
@@ -588,7 +609,7 @@ cudaError_t launch_tc(const TreeParams& tree, int batch, void* workspace, int wo
     tp.batch = batch;
     tp.n_rt = (p.n_tok * p.G + kTcRows - 1) / kTcRows;
     tp.workers = deal == kTreeAlone ? cluster : workers;
-    tp.keys = kTcKeys;
+    tp.keys = Lay::KEYS;
     const Kernel kernel = kernels[deal];
     if (deal == kTreeAlone) {
         cudaLaunchConfig_t cfg = {};
