@@ -1,10 +1,10 @@
 // tree_merge.cu -- merge of the parts that the equal shares of tree_tc.cu and tree_pair.cu leave of a
 // unit (one KV head of one sequence, a tile of rows, 256 columns at most):
 //   M = max_w m_w, out = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w
-// and zeros for row tiles without nodes. A lane has one row and 16 columns: parts lie with four columns of 128 rows after another, so reads are of
-// 512 consecutive bytes, and writes are whole sectors. WAYS warps share out the parts (few units are cut
-// into many), BATCH at a time, and meet in shared memory. Latency bound: a warp waits for memory twice
-// (lengths, parts) where BATCH covers its parts.
+// and zeros for row tiles without nodes. A lane has one row and 16 columns: parts lie with four columns of
+// 128 rows after another, so reads are of 512 consecutive bytes, and writes are whole sectors. WAYS warps
+// share out the parts (few units are cut into many), BATCH at a time, and meet in shared memory. Latency
+// bound: a warp waits for memory twice (lengths, parts) where BATCH covers its parts.
 #include "common.cuh"
 #include "tree.h"
 #include "tree_dev.cuh"

@@ -21,8 +21,8 @@
 // Warps of each CTA: softmax (two groups of four, with a soft-cap four: group w has columns 64 w .. (32 w
 // ..) of S and 128 w .. (64 w ..) of O, the groups swap row maxima through shared memory); then one that
 // loads K and V, two that issue S and P V (even CTA) or forward their slots' arrivals to the even CTA, whose
-// MMAs read both halves (odd CTA), and one that loads Q. Barriers that the issuers wait on live in the even CTA and count arrivals from both; their
-// commits arrive in both CTAs.
+// MMAs read both halves (odd CTA), and one that loads Q. Barriers that the issuers wait on live in the even
+// CTA and count arrivals from both; their commits arrive in both CTAs.
 #include <atomic>
 #include <climits>
 #include <type_traits>

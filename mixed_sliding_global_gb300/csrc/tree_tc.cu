@@ -71,6 +71,8 @@ struct TcLay {
     static constexpr int BAR_OFF = MX_OFF + EXTRA - 512;
     static constexpr int SMEM = BAR_OFF + 512;
     static_assert(SMEM <= 232448 && (2 * kTcMaxSlots + 13) * 8 + 4 <= 512, "shared memory budget");
+    // (a cluster's exchange lies in the ring)
+    static_assert(SLOTS * SLOT >= kTcRows * D * 4, "shared memory budget");
     // CTAs of two clusters that waited for each other's tensor memory would wait for ever
     static_assert(2 * (SMEM + 1024) > 228 * 1024, "one CTA per SM");
 };
@@ -85,7 +87,6 @@ GEMMA_DEVINL void st_cluster_f32x4(uint32_t addr, float a, float b, float c, flo
                  "f"(d)
                  : "memory");
 }
-
 
 }  // namespace
 
@@ -427,7 +428,8 @@ __global__ void __launch_bounds__(TcLay<D, SOFTCAP>::THREADS, 1)
             __nv_bfloat16* out =
                 reinterpret_cast<__nv_bfloat16*>(p.out) +
                 (((size_t)U.b * p.n_tok + tk) * p.n_q + U.kvh * p.G + (R - tk * p.G)) * (size_t)D + O_COLS * w;
-            float4* part = reinterpret_cast<float4*>(tp.part_o) + ((size_t)max(U.slot, 0) * (D / 4) + O_COLS / 4 * w) * kTcRows + r;
+            float4* part = reinterpret_cast<float4*>(tp.part_o) +
+                           ((size_t)max(U.slot, 0) * (D / 4) + O_COLS / 4 * w) * kTcRows + r;
             if (U.slot >= 0 && w == 0) tp.part_ml[(size_t)U.slot * kTcRows + r] = make_float2(m, l);
             const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
             if (w >= O_GROUPS && lane == 0) mbar_arrive(o_free);  // (has no columns)

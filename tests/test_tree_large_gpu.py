@@ -79,7 +79,8 @@ def test_pages_behind_32_bits():
     last = n_pages - 1
     pool[last - 1:] = torch.randn(2, n_kv, page, d, device="cuda").bfloat16()
     data = pool[last - 1:].clone()
-    table, refs, lens = torch.full((3, 4), -1, dtype=torch.int32, device="cuda"), i32([0] * n_pages), i32([200, 0, 0])
+    table = torch.full((3, 4), -1, dtype=torch.int32, device="cuda")
+    refs, lens = i32([0] * n_pages), i32([200, 0, 0])
     refs[:] = 1                                     # all taken but three pages far behind
     refs[last - 5:last - 2] = 0
     table[0, :2] = i32([last - 1, last])
