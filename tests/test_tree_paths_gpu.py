@@ -156,3 +156,23 @@ def test_a_batch_with_few_live_sequences(n_q, n_kv, d, nodes, top, live):
     p.msl = top
     p.check(p.run())
     assert p.err == 0
+
+
+@pytest.mark.parametrize("kind,window", [(SLIDING, 100), (SLIDING, 640), (GLOBAL, 0)])
+@pytest.mark.parametrize("n_q,n_kv,d,nodes,dtype", [
+    (4, 2, 64, 9, torch.bfloat16), (8, 8, 64, 8, torch.bfloat16), (4, 2, 128, 40, torch.bfloat16),
+    (8, 2, 256, 8, torch.bfloat16), (16, 2, 256, 30, torch.bfloat16), (16, 1, 512, 9, torch.bfloat16),
+    (2, 2, 512, 9, torch.bfloat16), (4, 2, 64, 5, torch.float32)])
+def test_tables_of_the_pages_in_use(n_q, n_kv, d, nodes, dtype, kind, window):
+    """Entries of pages that lie wholly below the window or behind the last key are -1, as the page
+    bookkeeping leaves them: they are not read."""
+    lens = [nodes, 128, 129, 256, 300, 320, 700, 1300, 2049, 2560]
+    p = Problem(lens, [min(nodes, n) for n in lens], nodes, kind=kind, window=window, n_q=n_q, n_kv=n_kv,
+                d=d, page=128, dtype=dtype, seed=d)
+    for b, n in enumerate(lens):
+        base = n - min(nodes, n)
+        first = max(0, base - window + 1) if kind == SLIDING else 0
+        p.table[b, :first // 128] = -1
+        p.table[b, (n - 1) // 128 + 1:] = -1
+    p.check(p.run())
+    assert p.err == 0
