@@ -52,7 +52,7 @@ cudaError_t launch_tree_merge(const MergeParams& mp, int head_dim, int rows, cud
 // an SM.
 int tree_ctas_per_sm(int head_dim);
 cudaError_t launch_tree_rows(const TreeParams& tp, int head_dim, int batch, cudaStream_t st);
-cudaError_t launch_tree_f32(const TreeParams& tp, int head_dim, int batch, cudaStream_t st);
+cudaError_t launch_tree_f32(const TreeParams& tp, int head_dim, int batch, int n_sm, cudaStream_t st);
 cudaError_t launch_tree_combine(const TreeParams& tp, int head_dim, int batch, cudaStream_t st);
 
 cudaError_t launch_tree_accept(const int32_t* tokens, const int32_t* parents, const int32_t* next,

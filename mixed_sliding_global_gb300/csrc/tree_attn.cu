@@ -813,13 +813,11 @@ __global__ void __launch_bounds__(256) tree_combine_kernel(const TreeParams tp, 
 // n-th key, and the streams meet in shared memory. Latency bound on a few hundred keys: the rows of a
 // stream's next key are on their way while it works on one (17 nodes x 4 heads, 700 keys, head_dim 128:
 // 28 us with a warp per key and five shuffles for each).
-constexpr int kTrF32Warps = 8;
-
-template <int D>
-__global__ void __launch_bounds__(kTrF32Warps * 32) tree_f32_kernel(const TreeParams tp) {
+template <int D, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32) tree_f32_kernel(const TreeParams tp) {
     pdl_launch_dependents();
     pdl_wait();  // the previous kernel on the stream has completed
-    constexpr int LPK = D / 16, STREAMS = kTrF32Warps * 32 / LPK;
+    constexpr int LPK = D / 16, STREAMS = WARPS * 32 / LPK;
     const RowsParams& p = tp.p;
     __shared__ int s_par[kTreeMaxNodes];
     __shared__ uint32_t s_set[kTrWords];
@@ -841,7 +839,7 @@ __global__ void __launch_bounds__(kTrF32Warps * 32) tree_f32_kernel(const TreePa
     if (sq.bad || bad || node >= sq.n) {
         if (blockIdx.x == 0 && threadIdx.x == 0 && (sq.bad || bad))
             report(p.err, sq.bad ? sq.bad : GEMMA_DEVERR_TREE);
-        for (int c = threadIdx.x; c < D; c += kTrF32Warps * 32) out[c] = 0.f;
+        for (int c = threadIdx.x; c < D; c += WARPS * 32) out[c] = 0.f;
         return;
     }
     if (threadIdx.x == 0) {
@@ -937,14 +935,17 @@ __global__ void __launch_bounds__(kTrF32Warps * 32) tree_f32_kernel(const TreePa
     }
     __syncthreads();
     float top = -INFINITY, sum = 0.f;
+#pragma unroll 8
     for (int w = 0; w < STREAMS; ++w) top = fmaxf(top, s_m[w]);
     __syncthreads();
     if (threadIdx.x < STREAMS)  // the streams' weights in the place of their maxima
         s_m[threadIdx.x] = s_m[threadIdx.x] == -INFINITY ? 0.f : expf(s_m[threadIdx.x] - top);
     __syncthreads();
+#pragma unroll 8
     for (int w = 0; w < STREAMS; ++w) sum = fmaf(s_m[w], s_l[w], sum);
-    for (int c = threadIdx.x; c < D; c += kTrF32Warps * 32) {
+    for (int c = threadIdx.x; c < D; c += WARPS * 32) {
         float x = 0.f;
+#pragma unroll 8
         for (int w = 0; w < STREAMS; ++w)
             if (s_m[w] != 0.f) x = fmaf(s_o[w][c], s_m[w], x);
         out[c] = x / sum;
@@ -1013,13 +1014,22 @@ cudaError_t launch_tree_rows(const TreeParams& tp, int head_dim, int batch, cuda
     return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_tree_f32(const TreeParams& tp, int head_dim, int batch, cudaStream_t st) {
-    const dim3 grid((unsigned)(tp.p.n_tok * tp.p.n_q), batch), block(kTrF32Warps * 32);
+template <int D>
+static cudaError_t launch_f32_d(const TreeParams& tp, int batch, int n_sm, cudaStream_t st) {
+    const dim3 grid((unsigned)(tp.p.n_tok * tp.p.n_q), batch);
+    // a CTA per SM: twice the streams for it. 8 / 16 warps: 136 rows over 700 keys of head_dim 128 16.0 / 11.0
+    // us, 48 over 1600 of 256 38 / 26; 272 over 700 of 128 16.8 / 20.0
+    if ((long long)grid.x * batch <= n_sm)
+        return launch_pdl(tree_f32_kernel<D, 16>, grid, dim3(512), 0, st, tp);
+    return launch_pdl(tree_f32_kernel<D, 8>, grid, dim3(256), 0, st, tp);
+}
+
+cudaError_t launch_tree_f32(const TreeParams& tp, int head_dim, int batch, int n_sm, cudaStream_t st) {
     switch (head_dim) {
-        case 64: return launch_pdl(tree_f32_kernel<64>, grid, block, 0, st, tp);
-        case 128: return launch_pdl(tree_f32_kernel<128>, grid, block, 0, st, tp);
-        case 256: return launch_pdl(tree_f32_kernel<256>, grid, block, 0, st, tp);
-        case 512: return launch_pdl(tree_f32_kernel<512>, grid, block, 0, st, tp);
+        case 64: return launch_f32_d<64>(tp, batch, n_sm, st);
+        case 128: return launch_f32_d<128>(tp, batch, n_sm, st);
+        case 256: return launch_f32_d<256>(tp, batch, n_sm, st);
+        case 512: return launch_f32_d<512>(tp, batch, n_sm, st);
     }
     return cudaErrorInvalidValue;
 }
