@@ -13,8 +13,8 @@
 //  - S has two buffers, and P(t) takes the place of S(t) in its buffer, so that S(t + 1) runs beside
 //    the softmax of t and S(t + 2) waits for P V(t) alone: the tensor core always has an MMA group
 //    that it may start;
-//  - units are cut into equal shares of the key tiles, parts merged by tree_merge_kernel (TreeShare); or,
-//    short ones, a pair has one whole (TreeAlone);
+//  - units are cut into equal shares of the key tiles, parts merged by tree_merge_kernel (TreeShare); short
+//    ones are not: a pair has one (TreeAlone) or several;
 //  - parts leave O as it stands in tensor memory, four columns of all rows after another, so that
 //    stores are of 512 consecutive bytes;
 //  - barriers, tensor memory and tensor maps are set up before the wait for the previous kernel.

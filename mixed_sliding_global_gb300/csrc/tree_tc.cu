@@ -14,8 +14,9 @@
 //  - S and P have two buffers each, so that S(t + 1) and P V(t - 1) run beside the softmax of t, and
 //    loads run ahead, into the next unit too;
 //  - a unit cut between CTAs leaves parts (O fp32 as it stands in tensor memory, four columns of all
-//    rows after another, so that stores are of 512 consecutive bytes) for tree_merge_kernel; or, where
-//    there are few units, a cluster shares a unit out and merges through distributed shared memory.
+//    rows after another, so that stores are of 512 consecutive bytes) for tree_merge_kernel; where there
+//    are few units, a cluster shares a unit out and merges through distributed shared memory, and many
+//    short ones are not cut.
 // Measured: 16 trees of 32 over a ring of 1024 (128 units of 64 rows, head_dim 256) 30 us, 4.9 TB/s; one
 // tree of 8 over a window of 512, 9 us.
 // Warps: softmax and epilogue, then one that loads K and V, one that issues S, one that loads Q (the wait
