@@ -508,7 +508,8 @@ int gemma_kv_keep(void* const* caches, int n_caches, const int32_t* write_pos, c
 /* gemma_pages_free -- give back the pages that hold no position in [keep_from[b], keep_to[b]): all of
  * a finished sequence (keep_to 0), what lies before a sliding window (keep_from), rejected or
  * reserved positions at the end (keep_to).
- *   keep_from, keep_to   DEVICE int32 [batch]; one of them may be NULL (no bound). */
+ *   keep_from, keep_to   DEVICE int32 [batch]; one of them may be NULL (no bound). With keep_to at or
+ *                        below keep_from nothing is kept. */
 int gemma_pages_free(int32_t* block_table, int max_pages, int page_size, int n_pages,
                      int32_t* page_refs, const int32_t* keep_from, const int32_t* keep_to,
                      int batch, uint32_t* device_error, void* stream);

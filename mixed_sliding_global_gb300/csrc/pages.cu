@@ -85,10 +85,11 @@ __global__ void __launch_bounds__(256)
     const int total = t.batch * t.max_pages;
     for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
         const int b = (int)(i / t.max_pages), blk = (int)(i - (long long)b * t.max_pages);
-        const long long begin = (long long)blk * t.page_size, end = begin + t.page_size;
-        const bool keep = (!keep_from || end > __ldg(keep_from + b)) &&
-                          (!keep_to || begin < __ldg(keep_to + b));
-        if (keep) continue;
+        // the page's positions within the bounds
+        long long begin = (long long)blk * t.page_size, end = begin + t.page_size;
+        if (keep_from) begin = max(begin, (long long)__ldg(keep_from + b));
+        if (keep_to) end = min(end, (long long)__ldg(keep_to + b));
+        if (begin < end) continue;
         const int page = t.table[i];
         if (page < 0) continue;
         if (page >= t.n_pages) {
