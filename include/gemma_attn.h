@@ -548,6 +548,7 @@ int gemma_pages_reserve(void* const* pools, const int32_t* pool_n_kv,
 /* gemma_pages_compact -- move the pages in use to the front of the pools, so that what lies behind
  * them can be taken away: with n_used the number of pages in use, the i-th of them at or behind
  * n_used (by index) moves to the i-th free page before n_used, in every pool, table entry and count.
+ * Every table entry is looked at, also where no page moves.
  *   n_used_out      DEVICE int32 [1], or NULL.
  *   Other arguments as for gemma_pages_reserve. */
 int gemma_pages_compact(void* const* pools, const int32_t* pool_n_kv,

@@ -192,7 +192,8 @@ __device__ __forceinline__ void copy_span(uint8_t* dst, const uint8_t* src, int 
 }
 
 // Copies of whole pages (compact: one unit is kCopyBytes of a page) or of the first rows of every
-// head (reserve: of a head's rows). Compact also gives the tables the pages' new places.
+// head (reserve: of a head's rows). Compact also gives the table the pages' new places; it looks at every
+// entry, moves or not, since an entry of no page in use is reported.
 template <bool WHOLE>
 __global__ void __launch_bounds__(kCopyThreads)
     pages_copy_kernel(const __grid_constant__ CopyPools pools, const PageTable t, void* workspace,
@@ -201,7 +202,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     pdl_wait();  // the plan
     const Workspace w = carve(workspace, t.n_pages);
     const int n_copies = *w.n_copies;
-    if (WHOLE && remap && n_copies > 0) {
+    if (WHOLE && remap) {
         const int total = t.batch * t.max_pages;
         for (long long i = blockIdx.x * (long long)kCopyThreads + threadIdx.x; i < total;
              i += gridDim.x * (long long)kCopyThreads) {
