@@ -475,7 +475,9 @@ int gemma_tree_accept(const int32_t* tokens, const int32_t* parents, const int32
  * in the order of i, in every cache of the call; all other rows stay as they are.
  *   caches      HOST array [n_caches] of DEVICE caches [batch][n_kv][kv_capacity] of rows of
  *               row_bytes bytes (even; bf16, fp32 and 4-bit caches' codes and scales alike), or of
- *               pools [n_pages][n_kv][page_size] with a block table. A ring wraps (kind
+ *               pools [n_pages][n_kv][page_size] with a block table. No two may have bytes in common: a
+ *               cache that several layers read, or that holds K and V, is named once (else
+ *               GEMMA_ERR_INVALID_ARG). A ring wraps (kind
  *               GEMMA_SLIDING_RING, kv_capacity >= n_nodes); the other kinds move alike.
  *   write_pos   DEVICE int32 [batch]: position of node 0's row (the append's write_pos).
  *   path        DEVICE int32 [batch][n_nodes], rising strictly within [0, n_nodes) up to n_keep[b].

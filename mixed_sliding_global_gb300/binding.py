@@ -494,7 +494,8 @@ def gemma_kv_keep(caches, write_pos: torch.Tensor, path: torch.Tensor, n_keep: t
                   device_error: Optional[torch.Tensor] = None, stream=None) -> None:
     """Move rows write_pos[b] + path[b][i] to write_pos[b] + i, i < n_keep[b], in every cache of the
     list: tensors [B][n_kv][cap][...] of one shape and any type (pools [n_pages][n_kv][page_size]
-    [...] with a block_table). kind GEMMA_SLIDING_RING wraps, the other kinds move alike."""
+    [...] with a block_table), no two sharing memory: a cache of several layers, or of K and V, is
+    named once. kind GEMMA_SLIDING_RING wraps, the other kinds move alike."""
     st = (_bind or _native()).kv_keep(caches, write_pos, path, n_keep, kind, block_table,
                                       device_error, _handle(stream))
     if st:

@@ -1254,6 +1254,17 @@ int gemma_kv_keep(void* const* caches, int n_caches, const int32_t* write_pos, c
     if (!caches || !write_pos || !path || !n_keep) return GEMMA_ERR_INVALID_ARG;
     for (int i = 0; i < n_caches; ++i)
         if (!caches[i] || !aligned16(caches[i])) return GEMMA_ERR_INVALID_ARG;
+    // Rows move in place, each cache by threads of its own: none may share bytes with another.
+    const uint64_t rows = block_table ? (uint64_t)n_pages * page_size : (uint64_t)batch * kv_capacity,
+                   row = (uint64_t)n_kv * row_bytes;  // (below 2^61 and at most 2^30)
+    const uint64_t size = rows > UINT64_MAX / row ? UINT64_MAX : rows * row;
+    bool overlap = false;
+    for (int i = 1; i < n_caches; ++i)
+        for (int j = 0; j < i; ++j) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(caches[i]), b = reinterpret_cast<uintptr_t>(caches[j]);
+            overlap |= (a > b ? a - b : b - a) < size;
+        }
+    if (overlap) return GEMMA_ERR_INVALID_ARG;
     for (const void* x : {static_cast<const void*>(write_pos), static_cast<const void*>(path),
                           static_cast<const void*>(n_keep), static_cast<const void*>(block_table),
                           static_cast<const void*>(device_error)})
