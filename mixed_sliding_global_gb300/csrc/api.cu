@@ -1189,7 +1189,8 @@ int gemma_attn_tree(void* out, const void* q, const void* const* k_cache,
     p.scale = scale;
     p.scale_log2 = scale * 1.4426950408889634f;
     p.softcap = softcap;
-    p.cap_inner = softcap > 0.f ? std::min(scale / softcap, FLT_MAX) : 0.f;
+    // (finite, and so is 2 log2(e) times it: a score of zero stays one under the smallest cap)
+    p.cap_inner = softcap > 0.f ? std::min(scale / softcap, FLT_MAX / 4) : 0.f;
     p.cap_log2 = softcap * 1.4426950408889634f;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
