@@ -14,6 +14,7 @@ namespace gemma {
 
 constexpr int kTrWords = kTreeMaxNodes / 32;  // words of an ancestor set
 constexpr float kTrLazyLog2 = 8.f;            // a row's reference moves past this growth only
+constexpr float kTrPlainCap = 64.f;           // caps with one form of tanh per thread (tree_cap)
 
 // Barrier of n threads that tells each whether v is true for any.
 GEMMA_DEVINL bool named_bar_or(int id, int n, bool v) {
@@ -373,12 +374,17 @@ GEMMA_DEVINL void tree_store32(__nv_bfloat16* out, const uint32_t (&v)[32], floa
     }
 }
 // N scores of a row soft-capped, in log2 units (tr_score); a NaN may spread to the score beside it. Three
-// forms of tanh, by the largest |x| of the thread's scores:
-//  - up to 1/8 (in the whole warp) the series' first three terms, the next being 0.054 x^6 < 2^-22;
+// forms of tanh, by the thread's scores, so that a score's error is small against the row's largest score or
+// against itself:
+//  - up to |x| = 1/8 (in the whole warp) the series' first three terms, the next being 0.054 x^6 < 2^-22;
 //  - up to 1/2 the series;
-//  - above, 1 - 2 / (1 + e^2x), two scores to a reciprocal: off by at most 2^-20 of 1 where the row's
-//    largest score is 0.46 at least. With the softmax's own exponential 5 special-function instructions for
-//    two scores, which bound such a tile.
+//  - above, 1 - 2 / (1 + e^2x), two scores to a reciprocal: off by at most 2^-20 of the cap. With the
+//    softmax's own exponential 5 special-function instructions for two scores, which bound such a tile.
+//    Up to a cap of 64 that is 2^-14 of a weight, 1/64 of what P's rounding may move it by; above, it is
+//    small against the row's largest score where one of the thread's is above 0.46 of the cap before the
+//    tanh, and where none is (keys far below the others) scores up to 1/2 take the series one by one. 76
+//    units of 4096 keys, head_dim 256, so / with that choice for every cap, in us: a cap of 8 times the
+//    scores 89 / 125, of twice 86 / 130.
 template <int N>
 GEMMA_DEVINL void tree_cap(float (&s)[N], const RowsParams& p) {
     float top = 0.f;
@@ -412,18 +418,36 @@ GEMMA_DEVINL void tree_cap(float (&s)[N], const RowsParams& p) {
         }
     } else {
         const float in2 = 2.885390081777927f * p.cap_inner;  // exp(2 x) = 2^(in2 s)
-#pragma unroll
-        for (int e = 0; e < N; e += 2) {
+        auto two = [&](float& s0, float& s1) {
             // (2^58 at most, so that the product of two stays in range; a NaN stays one)
-            float x = s[e] * in2, y = s[e + 1] * in2;
+            float x = s0 * in2, y = s1 * in2;
             x = x > 58.f ? 58.f : x;
             y = y > 58.f ? 58.f : y;
             const float a = 1.f + fast_exp2(x), b = 1.f + fast_exp2(y);
             float q;
             asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q) : "f"(a * b));
             q *= -2.f * p.cap_log2;
-            s[e] = fmaf(q, b, p.cap_log2);
-            s[e + 1] = fmaf(q, a, p.cap_log2);
+            s0 = fmaf(q, b, p.cap_log2);
+            s1 = fmaf(q, a, p.cap_log2);
+        };
+        bool apart = false;
+        if (p.softcap > kTrPlainCap) {
+            float hi = s[0];
+#pragma unroll
+            for (int e = 0; e < N; e += 2) hi = fmax3f(hi, s[e], s[e + 1]);
+            apart = !(hi * p.cap_inner >= 0.46f);
+        }
+        if (!apart) {
+#pragma unroll
+            for (int e = 0; e < N; e += 2) two(s[e], s[e + 1]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; e += 2) {
+                const float s0 = s[e], s1 = s[e + 1], x = s0 * p.cap_inner, y = s1 * p.cap_inner;
+                two(s[e], s[e + 1]);
+                if (fabsf(x) <= 0.5f) s[e] = s0 * k * tr_tanh_over_x(x * x);
+                if (fabsf(y) <= 0.5f) s[e + 1] = s1 * k * tr_tanh_over_x(y * y);
+            }
         }
     }
     __syncwarp();

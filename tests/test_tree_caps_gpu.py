@@ -1,4 +1,5 @@
-"""Soft-capped tree attention with caps and scores far from each other."""
+"""Soft-capped tree attention where a row's scores lie far apart: a key far below the cap's zero beside
+scores that are small against the cap, and rows of which every score is far below zero."""
 import math
 
 import pytest
@@ -38,15 +39,51 @@ def run(q, k, v, lens, parents, softcap):
     return out
 
 
-def bound(ref, mass, size, d, n_keys, dtype):
+def bound(ref, mass, size, d, n_keys, dtype, softcap=1e9):
     """As in test_tree_gpu.Problem, `size` the largest scale * sum_i |q_i k_i| of the keys that carry
     weight, and for the cap 2^-19 of it (test_tree_values_gpu.Capped), twice: the normaliser. A cap's
-    error is one of the score it is taken of."""
+    error is one of the score it is taken of, or, up to a cap of 64, 2^-20 of the cap."""
+    if softcap <= 64:
+        size = size + softcap / 2
     if dtype == torch.float32:
         rel = 2 * (d / 32 + 8) * 2.0 ** -24 * size + 2.0 ** -20 + n_keys * 2.0 ** -23
         return (rel + 2 * 2.0 ** -19 * size) * (mass + ref.abs()) + 1e-12
     rel = 2 * (d / 16 + 16) * 2.0 ** -23 * size + 2.0 ** -20 + (n_keys / 16 + 64) * 2.0 ** -23
     return 2.0 ** -8 * ref.abs() + (2.0 ** -8 + rel + 2 * 2.0 ** -19 * size) * (mass + ref.abs()) + 1e-12
+
+
+@pytest.mark.parametrize("n_q,n_kv,d,nodes,lens,dtype", WAYS)
+@pytest.mark.parametrize("softcap", [64.0, 1e4, 1e6, 1e20])
+def test_keys_far_below_the_others(n_q, n_kv, d, nodes, lens, dtype, softcap):
+    """Every 16th key lies 0.5 of the cap below the rest: hardly any weight (some e^-30 of the
+    other keys' at most), and no effect on the scores of the rest, which are some 2^-6 to 2^-66 of the cap."""
+    low = lambda j: j % 16 == 5  # noqa: E731
+    q, k, v, parents = problem(n_q, n_kv, d, nodes, lens, dtype, softcap, low, d)
+    out = run(q, k, v, lens, parents, softcap)
+    for b, n in enumerate(lens):
+        see = tree_ref.keys_of(parents[b], nodes, n - nodes, tree_ref.GLOBAL, 0)
+        kb, vb = k[b, :, :n].transpose(0, 1), v[b, :, :n].transpose(0, 1)
+        ref, mass, _ = tree_ref.attention(q[b], kb, vb, see, d ** -0.5, softcap)
+        carry = see & ~low(torch.arange(n))
+        assert carry.any(1).all()
+        size = tree_ref.attention(q[b], torch.where(low(torch.arange(n, device="cuda"))[:, None, None], 0, kb),
+                                  vb, see, d ** -0.5)[2]
+        e = (out[b].double() - ref).abs()
+        assert (e <= bound(ref, mass, size, d, n, dtype, softcap)).all()
+
+
+@pytest.mark.parametrize("n_q,n_kv,d,nodes,lens,dtype", WAYS)
+@pytest.mark.parametrize("softcap", [20.0, 400.0])
+def test_all_keys_far_below_zero(n_q, n_kv, d, nodes, lens, dtype, softcap):
+    """Every score is about -0.6 of the cap: the error is one of the scores' size."""
+    q, k, v, parents = problem(n_q, n_kv, d, nodes, lens, dtype, softcap, lambda j: j >= 0, d)
+    out = run(q, k, v, lens, parents, softcap)
+    for b, n in enumerate(lens):
+        see = tree_ref.keys_of(parents[b], nodes, n - nodes, tree_ref.GLOBAL, 0)
+        kb, vb = k[b, :, :n].transpose(0, 1), v[b, :, :n].transpose(0, 1)
+        ref, mass, size = tree_ref.attention(q[b], kb, vb, see, d ** -0.5, softcap)
+        e = (out[b].double() - ref).abs()
+        assert (e <= bound(ref, mass, size, d, n, dtype)).all()
 
 
 @pytest.mark.parametrize("n_q,n_kv,d,nodes,lens,dtype", WAYS)
