@@ -540,7 +540,12 @@ int gemma_pages_fork(int32_t* block_table, int max_pages, int page_size, int n_p
  *   workspace       DEVICE scratch of gemma_pages_workspace_size(n_pages) bytes, 16-byte aligned;
  *                   contents on entry are ignored; calls that may overlap must not share it.
  * Where the free pages run out (GEMMA_DEVERR_POOL_FULL) the positions that are left stay without a
- * page, or on their shared one, and must not be written; the same call goes on once pages are free. */
+ * page, or on their shared one; the same call goes on once pages are free. A position has a page of its own,
+ * and may be written, exactly where its entry is a page with page_refs 1: where a holder of a shared page
+ * had to stay on it, not even the first holder's may (its rows might be the other's). A captured step makes
+ * its write positions and node counts from that, on the device: a sequence with a position that is not its
+ * own gets write_pos -1 (appends skip it, GEMMA_DEVERR_WRITE_POS) and n_real 0 (its tree has no nodes,
+ * nothing is kept, its length stays). */
 int gemma_pages_reserve(void* const* pools, const int32_t* pool_n_kv,
                         const int32_t* pool_row_bytes, int n_pools, int32_t* block_table,
                         int max_pages, int page_size, int n_pages, int32_t* page_refs,

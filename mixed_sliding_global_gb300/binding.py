@@ -530,7 +530,8 @@ def gemma_pages_reserve(pools, block_table: torch.Tensor, page_refs: torch.Tenso
                         device_error: Optional[torch.Tensor] = None, stream=None) -> None:
     """Pages of their own for positions [seq_lens[b], seq_lens[b] + n_add[b]): free ones for those
     without, copies of shared ones. pools: every tensor [n_pages][n_kv][page_size][...] that the
-    table stands for."""
+    table stands for. With a full pool some stay without: a position may be written where its entry is
+    a page with page_refs 1."""
     st = (_bind or _native()).pages_reserve(pools, block_table, page_refs, seq_lens, n_add,
                                             workspace, device_error, _handle(stream))
     if st:
