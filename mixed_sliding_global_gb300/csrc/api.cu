@@ -1161,6 +1161,7 @@ int gemma_attn_tree(void* out, const void* q, const void* const* k_cache,
     gemma::TreeParams tp{};
     RowsParams& p = tp.p;
     tp.parents = parents;
+    tp.n_sm = n_sm;
     p.q = q;
     p.k = kc;
     p.v = vc;
@@ -1195,7 +1196,7 @@ int gemma_attn_tree(void* out, const void* q, const void* const* k_cache,
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (!bf16) {
-        e = gemma::launch_tree_f32(tp, head_dim, batch, n_sm, s);
+        e = gemma::launch_tree_f32(tp, head_dim, batch, s);
     } else if (pl.path == kTreeTc) {
         e = gemma::launch_tree_tc(tp, head_dim, batch, workspace, pl.workers, pl.cluster, pl.deal, s);
     } else if (pl.path == kTreePair) {

@@ -14,6 +14,7 @@ constexpr int kTreeKeyTile = 64;    // keys per tile; chunks of keys are multipl
 struct TreeParams {
     RowsParams p;
     const int32_t* parents;  // [batch][n_tok], -1 or an earlier node
+    int n_sm;                // of the device
 };
 
 constexpr int kTreeRowsMax = 32;  // rows per KV head of launch_tree_rows
@@ -52,7 +53,7 @@ cudaError_t launch_tree_merge(const MergeParams& mp, int head_dim, int rows, cud
 // an SM.
 int tree_ctas_per_sm(int head_dim);
 cudaError_t launch_tree_rows(const TreeParams& tp, int head_dim, int batch, cudaStream_t st);
-cudaError_t launch_tree_f32(const TreeParams& tp, int head_dim, int batch, int n_sm, cudaStream_t st);
+cudaError_t launch_tree_f32(const TreeParams& tp, int head_dim, int batch, cudaStream_t st);
 cudaError_t launch_tree_combine(const TreeParams& tp, int head_dim, int batch, cudaStream_t st);
 
 cudaError_t launch_tree_accept(const int32_t* tokens, const int32_t* parents, const int32_t* next,

@@ -1015,21 +1015,21 @@ cudaError_t launch_tree_rows(const TreeParams& tp, int head_dim, int batch, cuda
 }
 
 template <int D>
-static cudaError_t launch_f32_d(const TreeParams& tp, int batch, int n_sm, cudaStream_t st) {
+static cudaError_t launch_f32_d(const TreeParams& tp, int batch, cudaStream_t st) {
     const dim3 grid((unsigned)(tp.p.n_tok * tp.p.n_q), batch);
     // a CTA per SM: twice the streams for it. 8 / 16 warps: 136 rows over 700 keys of head_dim 128 16.0 / 11.0
     // us, 48 over 1600 of 256 38 / 26; 272 over 700 of 128 16.8 / 20.0
-    if ((long long)grid.x * batch <= n_sm)
+    if ((long long)grid.x * batch <= tp.n_sm)
         return launch_pdl(tree_f32_kernel<D, 16>, grid, dim3(512), 0, st, tp);
     return launch_pdl(tree_f32_kernel<D, 8>, grid, dim3(256), 0, st, tp);
 }
 
-cudaError_t launch_tree_f32(const TreeParams& tp, int head_dim, int batch, int n_sm, cudaStream_t st) {
+cudaError_t launch_tree_f32(const TreeParams& tp, int head_dim, int batch, cudaStream_t st) {
     switch (head_dim) {
-        case 64: return launch_f32_d<64>(tp, batch, n_sm, st);
-        case 128: return launch_f32_d<128>(tp, batch, n_sm, st);
-        case 256: return launch_f32_d<256>(tp, batch, n_sm, st);
-        case 512: return launch_f32_d<512>(tp, batch, n_sm, st);
+        case 64: return launch_f32_d<64>(tp, batch, st);
+        case 128: return launch_f32_d<128>(tp, batch, st);
+        case 256: return launch_f32_d<256>(tp, batch, st);
+        case 512: return launch_f32_d<512>(tp, batch, st);
     }
     return cudaErrorInvalidValue;
 }

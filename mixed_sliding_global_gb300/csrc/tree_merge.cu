@@ -240,7 +240,7 @@ static cudaError_t launch_merge(const MergeParams& mp, cudaStream_t st) {
     const long long parts = mp.workers / (units * (D > 256 ? 2 : 1));
     const long long warps = groups * (D / 16);
     int ways = parts < 5 ? 1 : parts < 10 ? 2 : parts < 24 ? 4 : 8;
-    if (ways > 1 && ways < 8 && warps * ways < 8 * 152) ways *= 2;
+    if (ways > 1 && ways < 8 && warps * ways < 8 * mp.tp.n_sm) ways *= 2;
     auto launch = [&](auto kernel, int slices) {
         return launch_pdl(kernel, dim3((unsigned)(groups * ((D / 16 + slices - 1) / slices))), dim3(256),
                           0, st, mp);
