@@ -52,10 +52,7 @@ struct TrLay {
     static constexpr int P_ROW = 2 * T + 16;
     static constexpr int FIXED = M * Q_ROW + M * P_ROW + CW * M * 4 + 32 * kTrWords * 4 + 32 * 4 +
                                  kTreeMaxNodes * 4 + 2 * kTrMaxSlots * 8 + 1024;
-    // two CTAs per SM where their rings then hold four tiles each, else one
-    static constexpr bool TWO = FIXED + 4 * SLOT <= 113 * 1024;
-    static constexpr int BUDGET = TWO ? 113 * 1024 : 227 * 1024;
-    static constexpr int FIT = (BUDGET - FIXED) / SLOT;
+    static constexpr int FIT = (227 * 1024 - FIXED) / SLOT;  // one CTA per SM
     static constexpr int SLOTS = FIT > kTrMaxSlots ? kTrMaxSlots : FIT;
     static constexpr int Q_OFF = SLOTS * SLOT;
     static constexpr int P_OFF = Q_OFF + M * Q_ROW;
@@ -81,9 +78,7 @@ struct TrKeys {
     static constexpr int MERGE = KG * M * O_ROW * 4;  // in the ring, once its tiles are used up
     static constexpr int FIXED = M * Q_ROW + 2 * KG * M * 4 + 32 * kTrWords * 4 + 32 * 4 +
                                  kTreeMaxNodes * 4 + 2 * kTrMaxSlots * 8 + 1024;
-    static constexpr int PAIR_FIT = (113 * 1024 - FIXED) / SLOT;  // slots of each of two CTAs per SM
-    static constexpr bool TWO = PAIR_FIT >= 4 && PAIR_FIT * SLOT >= MERGE;
-    static constexpr int FIT = TWO ? PAIR_FIT : (227 * 1024 - FIXED) / SLOT;
+    static constexpr int FIT = (113 * 1024 - FIXED) / SLOT;  // two CTAs per SM
     static constexpr int SLOTS = FIT > kTrMaxSlots ? kTrMaxSlots : FIT;
     static constexpr int RING = SLOTS * SLOT;
     static constexpr int Q_OFF = RING;
@@ -93,7 +88,7 @@ struct TrKeys {
     static constexpr int PAR_OFF = DEPTH_OFF + 32 * 4;
     static constexpr int BAR_OFF = PAR_OFF + kTreeMaxNodes * 4;
     static constexpr int SMEM = BAR_OFF + 2 * kTrMaxSlots * 8 + 1024;  // + alignment slack
-    static_assert(SLOTS >= 4 && RING >= MERGE && SMEM <= 232448 && BAR_OFF % 8 == 0,
+    static_assert(SLOTS >= 4 && RING >= MERGE && SMEM <= 113 * 1024 && BAR_OFF % 8 == 0,
                   "shared memory budget");
 };
 
@@ -107,7 +102,7 @@ GEMMA_DEVINL uint32_t tr_off(int key, int d) {
 
 // head_dim up to 128: a warp has the rows and a share of every tile's keys, and keeps O whole
 template <int D>
-__global__ void __launch_bounds__((TrKeys<D>::WARPS + 1) * 32, TrKeys<D>::TWO ? 2 : 1)
+__global__ void __launch_bounds__((TrKeys<D>::WARPS + 1) * 32, 2)
     tree_keys_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const TreeParams tp) {
     pdl_launch_dependents();
@@ -425,7 +420,7 @@ __global__ void __launch_bounds__((TrKeys<D>::WARPS + 1) * 32, TrKeys<D>::TWO ? 
 // head_dim 512 (O of 16 rows is two warps' registers): the warps of a row group share out the keys of
 // S and the columns of O
 template <int D, int MW>
-__global__ void __launch_bounds__(kTrThreads, TrLay<D, MW>::TWO ? 2 : 1)
+__global__ void __launch_bounds__(kTrThreads, 1)
     tree_rows_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const TreeParams tp) {
     pdl_launch_dependents();
@@ -970,9 +965,7 @@ struct TrKernel<512, MW> {
 };
 
 int tree_ctas_per_sm(int head_dim) {
-    return head_dim == 64    ? TrKernel<64, 1>::Lay::TWO + 1
-           : head_dim == 128 ? TrKernel<128, 1>::Lay::TWO + 1
-                             : 1;
+    return head_dim <= 128 ? 2 : 1;
 }
 
 template <int D, int MW>
