@@ -1039,10 +1039,11 @@ TreePlan tree_plan(int batch, int kind, int window, int n_q, int n_kv, int head_
         pl.workers = (int)(tiles < n_sm ? tiles : n_sm);
         pl.ws_bytes = gemma::tree_tc_workspace(head_dim, batch, pl.workers);
         // A cluster for each unit (no merge launch), where that ends no later than equal shares. In ns: a tile
-        // takes 850 at head_dim 64 and 128 (of 128 keys) and 1000 at 256; the merge launch of equal shares
-        // 4500; a cluster's exchange 1.0, 2.0 and 5.9 thousand with 32 rows of 256, 128 of 64, 128 of 256. One
-        // unit of 32 rows and head_dim 256, clusters of 8 / shares: 1100 keys 9.6 / 10.2 us; 128 rows: 14.6 /
-        // 11.7; 128 units of 17 tiles, alone / shares: 30.6 / 34.4.
+        // takes 850 at head_dim 64 and 128 (of 128 keys) and 1012 at 256; the merge launch of equal shares
+        // 4500 (TreeShare, which knows the lengths, counts what its parts take to write as well); a cluster's
+        // exchange 1.0, 2.0 and 5.9 thousand with 32 rows of 256, 128 of 64, 128 of 256. One unit of 32 rows and
+        // head_dim 256, clusters of 8 / shares: 1100 keys 9.6 / 10.2 us; 128 rows: 14.6 / 11.7; 128 units of 17
+        // tiles, alone / shares: 30.6 / 34.4.
         const long long u = units * ((rows + 127) / 128);
         const long long nt = kind == GEMMA_SLIDING_RING ? (reach + keys - 1) / keys : (reach - T + keys) / keys;
         const long long tile_ns = head_dim == 256 ? 1012 : 850, merge_ns = 4500;
