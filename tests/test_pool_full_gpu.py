@@ -19,7 +19,7 @@ def i32(x):
 
 
 def documented_step():
-    """README's block that reserves pages, as code."""
+    """The code block for users that reserves pages, compiled as it stands."""
     path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")
     with open(path) as f:
         blocks = re.findall(r"```python\n(.*?)```", f.read(), re.S)
